@@ -21,6 +21,9 @@
  *     kvc_window_prefill_step  a windowed multi-token step that stages only
  *                          the rows whose eviction its chunk would see
  *     kvc_tensor_scatter   the ONNX TensorScatter cache update (linear/circular)
+ *     kvc_quant_append, kvc_dequant_rows, kvc_gqa_decode_quant  a cache whose
+ *                          rows are quantised as they are written, read back
+ *                          in 16 bits or attended over as codes
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -88,6 +91,8 @@ typedef enum {
 } kvc_status;
 
 typedef enum { KVC_F32 = 0, KVC_BF16 = 1, KVC_F16 = 2 } kvc_dtype;
+/* 8-bit codes of a quantised row (code * scale is the value) */
+typedef enum { KVC_INT8 = 0, KVC_E4M3 = 1 } kvc_quant_format;
 typedef enum { KVC_LINEAR = 0, KVC_CIRCULAR = 1 } kvc_mode;
 typedef enum { KVC_APPEND = 0, KVC_COPY_BACK = 1 } kvc_phase;
 /* How the resident rows of a cache follow the absolute length T (the
@@ -655,6 +660,81 @@ kvc_status kvc_window_prefill_step(void *out, const void *q, void *k_cache, void
 size_t kvc_gqa_prefill_workspace_size(int batch, int q_heads, int kv_heads, int new_tokens,
                                       int64_t rows_per_head, int head_dim, int dtype,
                                       int local_window_size);
+
+/*
+ * A cache quantised as it is written ("Persistent KV Cache and Decode
+ * Performance Roadmap", "Phase 3: cache quantization and fusion").  A row x of
+ * head_dim values is held as head_dim 8-bit codes and one float32 scale:
+ *     KVC_INT8:  scale = max|x| / 127, code = clamp(rint(x / scale), -127, 127)
+ *     KVC_E4M3:  scale = max|x| / 448, code = x / scale to e4m3 (nearest even,
+ *                saturated)
+ * with both divisions in float32; code * scale is the value read back.  A row
+ * of zeros (or one so small that its scale is 0) has scale 0 and codes 0; a
+ * row with a NaN or an infinity has scale NaN and codes 0, so it reads back
+ * as NaN.  The cache of B x kv_heads x capacity rows is four arrays:
+ *   kq_cache, vq_cache  device [batch, kv_heads, capacity, head_dim] bytes
+ *   k_scale, v_scale    device float32 [batch, kv_heads, capacity]
+ * (16-byte aligned, not overlapping).  `windowed` is KVC_CONTIGUOUS or KVC_RING
+ * in all three calls (other policies move rows and are KVC_ERR_UNSUPPORTED);
+ * `format` is a kvc_quant_format (KVC_ERR_DTYPE otherwise).
+ *
+ * kvc_quant_append -- write the S new rows of each (batch, kv head): K rotated
+ * at P + i in float32 and quantised without a rounding in between, V as given.
+ * Row P + i of a contiguous cache, slot (P + i) mod C of a ring (of S > C rows
+ * only the last C).  A row past rope_max_pos sets KVC_DEV_ROPE_RANGE, lengths
+ * that do not fit the capacity KVC_DEV_CAPACITY; that batch row writes nothing.
+ * new_k, new_v  device [batch, kv_heads, new_tokens, head_dim], any kvc_dtype.
+ * len           outputs of kvc_seq_lengths for the same S, C and policy.
+ * head_dim      a multiple of 16, at most 256 (KVC_ERR_UNSUPPORTED).
+ */
+kvc_status kvc_quant_append(void *kq_cache, void *vq_cache, float *k_scale, float *v_scale,
+                            const void *new_k, const void *new_v, kvc_lengths len, int batch,
+                            int kv_heads, int new_tokens, int64_t capacity, int head_dim, int dtype,
+                            int format, int windowed, const float *rope_cos,
+                            const float *rope_sin, int64_t rope_max_pos, int32_t *dev_status,
+                            void *stream);
+
+/*
+ * kvc_dequant_rows -- rows [0, L) of k_out, v_out <- the L resident rows
+ * (L = len.cache_total), oldest first, as code * scale rounded to `dtype`: for
+ * a ring, row r is position T - L + r.  Rows past L are left as they were, so
+ * kvc_gqa_prefill_chunk can run a chunk over the rows of a contiguous cache
+ * right after kvc_quant_append (rows_per_head = rows_out).
+ * k_out, v_out  device [batch, kv_heads, rows_out, head_dim]; a batch row with
+ *               L > rows_out sets KVC_DEV_CAPACITY and is left as it was.
+ * head_dim as kvc_quant_append; batch * kv_heads <= 65535 (KVC_ERR_SHAPE).
+ */
+kvc_status kvc_dequant_rows(void *k_out, void *v_out, const void *kq_cache, const void *vq_cache,
+                            const float *k_scale, const float *v_scale, kvc_lengths len, int batch,
+                            int kv_heads, int64_t capacity, int64_t rows_out, int head_dim,
+                            int dtype, int format, int windowed, int32_t *dev_status, void *stream);
+
+/*
+ * kvc_gqa_decode_quant -- kvc_gqa_decode (contiguous) or kvc_gqa_decode_ring
+ * (ring) over a quantised cache, without a 16-bit copy of it: the codes go to
+ * the tensor cores as halves (exactly) and the rows' scales enter in float32.
+ * Masks, lengths, rope and errors as those calls; a NaN scale of a visible row
+ * makes the output NaN.  Rejected batch rows keep their output.
+ * out, q     device [batch, q_heads, 1, head_dim], KVC_BF16 or KVC_F16.
+ * head_dim 64, 128 or 256, q_heads / kv_heads <= 16 (KVC_ERR_UNSUPPORTED).
+ * workspace  device, kvc_gqa_decode_quant_workspace_size(...) bytes on the
+ *            current device, 256-byte aligned (0 bytes: may be NULL).  Calls
+ *            that may overlap on the GPU need workspaces of their own.
+ * Every CTA takes the same share of the batch's visible rows, whatever the
+ * lengths; rows that several CTAs worked on are joined by a second launch, in
+ * a fixed order.
+ */
+kvc_status kvc_gqa_decode_quant(void *out, const void *q, const void *kq_cache,
+                                const void *vq_cache, const float *k_scale, const float *v_scale,
+                                kvc_lengths len, int batch, int q_heads, int kv_heads,
+                                int64_t capacity, int head_dim, int dtype, int format, int windowed,
+                                int local_window_size, float scale, const float *rope_cos,
+                                const float *rope_sin, int64_t rope_max_pos, void *workspace,
+                                size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* Bytes of workspace kvc_gqa_decode_quant needs for these sizes (0 on bad sizes). */
+size_t kvc_gqa_decode_quant_workspace_size(int batch, int q_heads, int kv_heads, int64_t capacity,
+                                           int head_dim);
 
 /* Human-readable name of a status code (static storage). */
 const char *kvc_status_string(kvc_status status);

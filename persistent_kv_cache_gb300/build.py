@@ -16,8 +16,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libkvc.so")
-SOURCES = ["kvc_scatter.cu", "kvc_cache.cu", "kvc_decode.cu", "kvc_prefill.cu"]
-HEADERS = [os.path.join(CSRC, "kvc_common.cuh"), os.path.join(ROOT, "include", "kvc.h")]
+SOURCES = ["kvc_scatter.cu", "kvc_cache.cu", "kvc_decode.cu", "kvc_prefill.cu", "kvc_quant.cu"]
+HEADERS = [os.path.join(CSRC, "kvc_common.cuh"), os.path.join(CSRC, "kvc_flat.cuh"),
+           os.path.join(ROOT, "include", "kvc.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
               "--expt-relaxed-constexpr"]

@@ -1,0 +1,1105 @@
+// kvc_quant.cu -- a KV cache whose rows are quantised as they are written, and
+// its readers ("Persistent KV Cache and Decode Performance Roadmap", "Phase 3:
+// cache quantization and fusion"; the ring of "Stateful decode & KV cache",
+// "Sliding-window ring buffer").
+//
+// A row x of head_dim values (K rotated at its absolute position, in float32)
+// is held as 8-bit codes and one float32 scale:
+//     s = max|x| / 127 (int8) or / 448 (e4m3),  code = nearest(x / s)
+// so that code * s is the row read back.  A row of zeros has s = 0; a row with
+// a NaN or an infinity has s = NaN and codes 0, so it reads back as NaN.
+//
+//   quant_append_kernel   new rows -> codes and scales
+//   dequant_rows_kernel   rows [0, L) back to 16 or 32 bits
+//   quant_decode_kernel   one-token GQA attention over the codes
+//   quant_merge_kernel    joins the partial results of rows that several CTAs
+//                         worked on
+#include <algorithm>
+#include <type_traits>
+
+#include <cuda_fp8.h>
+
+#include "kvc_common.cuh"
+#include "kvc_flat.cuh"
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int FMT> constexpr float kTop = FMT == KVC_INT8 ? 127.f : 448.f;
+
+// --------------------------------------------------------------------------
+// writing
+// --------------------------------------------------------------------------
+
+template <typename T> struct alignas(16) Row8 { T e[8]; };
+
+template <typename T> __device__ __forceinline__ void load8(const T *p, float (&x)[8])
+{
+    if constexpr (sizeof(T) == 2) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
+        const T *e = reinterpret_cast<const T *>(&v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] = kvc::Elem<T>::to_f32(e[i]);
+    } else {
+        const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
+        const float4 b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+}
+
+// eight values of a row, LPR lanes a row, to codes: the row's scale by the
+// lanes' maximum, taken on the bit patterns of |x| so that a NaN or an
+// infinity (patterns from 0x7f800000 on) is the largest of all
+template <int FMT, int LPR>
+__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float &scale)
+{
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+#pragma unroll
+    for (int d = 1; d < LPR; d <<= 1)
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+    uint2 out = make_uint2(0, 0);
+    if (top >= 0x7f800000u) {
+        scale = __uint_as_float(0x7fc00000u);
+        return out;
+    }
+    scale = __fdiv_rn(__uint_as_float(top), kTop<FMT>);
+    if (scale == 0.f)
+        return out;
+    if constexpr (FMT == KVC_INT8) {
+        uint32_t w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            w[h] = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // a subnormal scale may round the quotient past 127
+                const int c = max(-127, min(127, __float2int_rn(__fdiv_rn(x[4 * h + i], scale))));
+                w[h] |= (uint32_t)(c & 0xff) << (8 * i);
+            }
+        }
+        out = make_uint2(w[0], w[1]);
+    } else {
+        uint32_t w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float2 lo = make_float2(__fdiv_rn(x[4 * h], scale), __fdiv_rn(x[4 * h + 1], scale));
+            const float2 hi = make_float2(__fdiv_rn(x[4 * h + 2], scale), __fdiv_rn(x[4 * h + 3], scale));
+            w[h] = (uint32_t)__nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3) |
+                   (uint32_t)__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3) << 16;
+        }
+        out = make_uint2(w[0], w[1]);
+    }
+    return out;
+}
+
+struct AppendArgs {
+    uint8_t *kq, *vq;
+    float *ks, *vs;
+    const void *new_k, *new_v;
+    kvc_lengths len;
+    int batch, kv_heads, S, D;
+    int64_t C;
+    int ring;
+    const float *cos_t, *sin_t;
+    int64_t rope_max_pos;
+    int32_t *status;
+};
+
+// LPR lanes write one row of K and the same row of V: eight columns a lane
+// (lanes past head_dim idle along), the rotation's partner columns c +- D / 2
+// fetched from the lane that holds them.
+template <typename T, int FMT, int LPR>
+__global__ void __launch_bounds__(256)
+quant_append_kernel(const AppendArgs a)
+{
+    constexpr int RPB = 256 / LPR;
+    const int sub = threadIdx.x % LPR;
+    const int64_t rows = (int64_t)a.batch * a.kv_heads * a.S;
+    const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR;
+    const bool in = row < rows;
+    const int64_t slice = in ? row / a.S : 0;
+    const int i = in ? (int)(row % a.S) : 0;
+    const int b = (int)(slice / a.kv_heads);
+    const int P = a.len.past_abs[b];
+    bool write = in && a.len.cache_total[b] >= 0 && P >= 0;
+    const bool lead = sub == 0 && i == 0 && slice % a.kv_heads == 0;
+    if (write && a.cos_t && (int64_t)P + a.S > a.rope_max_pos) {
+        if (lead)
+            kvc::raise_status(a.status, KVC_DEV_ROPE_RANGE);
+        write = false;
+    }
+    if (write && !a.ring && (int64_t)P + a.S > a.C) {
+        // lengths computed for another capacity: refuse rather than overrun
+        if (lead)
+            kvc::raise_status(a.status, KVC_DEV_CAPACITY);
+        write = false;
+    }
+    // a ring keeps only the last C rows of the step
+    write = write && !(a.ring && (int64_t)i < (int64_t)a.S - a.C);
+    const int c0 = 8 * sub;
+    const bool col = write && c0 < a.D;
+    float k[8] = {}, v[8] = {};
+    if (col) {
+        load8(static_cast<const T *>(a.new_k) + row * a.D + c0, k);
+        load8(static_cast<const T *>(a.new_v) + row * a.D + c0, v);
+    }
+    const int64_t pos = (int64_t)P + i;
+    if (a.cos_t) {
+        const int half = a.D / 2;
+        const bool low = c0 < half;
+        // D is a multiple of 16, so the partner columns are one lane's
+        const int from = (threadIdx.x & 31) - sub + (low ? sub + half / 8 : sub - half / 8);
+        float other[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            other[e] = __shfl_sync(0xffffffffu, k[e], from & 31);
+        if (col) {
+            float cs[8], sn[8];
+            const int64_t at = pos * half + (low ? c0 : c0 - half);
+            load8(a.cos_t + at, cs);
+            load8(a.sin_t + at, sn);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float lo = low ? k[e] : other[e], hi = low ? other[e] : k[e];
+                kvc::rope_pair(lo, hi, cs[e], sn[e]);
+                k[e] = low ? lo : hi;
+            }
+        }
+    }
+    float ks, vs;
+    const uint2 kc = quantise8<FMT, LPR>(k, ks);
+    const uint2 vc = quantise8<FMT, LPR>(v, vs);
+    if (col) {
+        const int64_t r = slice * a.C + (a.ring ? pos % a.C : pos);
+        *reinterpret_cast<uint2 *>(a.kq + r * a.D + c0) = kc;
+        *reinterpret_cast<uint2 *>(a.vq + r * a.D + c0) = vc;
+        if (sub == 0) {
+            a.ks[r] = ks;
+            a.vs[r] = vs;
+        }
+    }
+}
+
+// --------------------------------------------------------------------------
+// reading back
+// --------------------------------------------------------------------------
+
+// four codes of a word as floats
+template <int FMT> __device__ __forceinline__ void codes4(uint32_t w, float (&f)[4])
+{
+    if constexpr (FMT == KVC_INT8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            f[i] = (float)(int)(signed char)(w >> (8 * i));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * i)), __NV_E4M3);
+            const float2 v = __half22float2(__half2(h));
+            f[2 * i] = v.x;
+            f[2 * i + 1] = v.y;
+        }
+    }
+}
+
+struct DequantArgs {
+    void *k_out, *v_out;
+    const uint8_t *kq, *vq;
+    const float *ks, *vs;
+    kvc_lengths len;
+    int batch, kv_heads, D;
+    int64_t C, R;
+    int ring;
+    int32_t *status;
+};
+
+// 16-byte pieces of the codes of rows [0, L): D / 16 lanes a row
+template <typename T, int FMT>
+__global__ void __launch_bounds__(256)
+dequant_rows_kernel(const DequantArgs a)
+{
+    const int slice = blockIdx.y;
+    const int b = slice / a.kv_heads;
+    const int L = a.len.cache_total[b], total = a.len.total_abs[b];
+    if (L < 0)
+        return;
+    if (L > a.R || L > a.C || total < L) {
+        if (threadIdx.x == 0 && blockIdx.x == 0 && slice % a.kv_heads == 0)
+            kvc::raise_status(a.status, KVC_DEV_CAPACITY);
+        return;
+    }
+    const int pieces = a.D / 16;
+    const int64_t first = a.ring ? (int64_t)(total - L) % a.C : 0;
+    const uint8_t *src = blockIdx.z == 0 ? a.kq : a.vq;
+    const float *scales = blockIdx.z == 0 ? a.ks : a.vs;
+    T *dst = static_cast<T *>(blockIdx.z == 0 ? a.k_out : a.v_out) + (int64_t)slice * a.R * a.D;
+    const int64_t work = (int64_t)L * pieces;
+    for (int64_t w = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; w < work;
+         w += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t r = w / pieces;
+        const int c0 = (int)(w % pieces) * 16;
+        int64_t slot = first + r;
+        if (slot >= a.C)
+            slot -= a.C;
+        slot += (int64_t)slice * a.C;
+        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(src + slot * a.D + c0));
+        const float s = __ldg(scales + slot);
+        const uint32_t word[4] = {q.x, q.y, q.z, q.w};
+        T out[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float f[4];
+            codes4<FMT>(word[i], f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                out[4 * i + e] = kvc::Elem<T>::from_f32(f[e] * s);
+        }
+        uint4 *to = reinterpret_cast<uint4 *>(dst + r * a.D + c0);
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T); ++i)
+            to[i] = reinterpret_cast<const uint4 *>(out)[i];
+    }
+}
+
+// --------------------------------------------------------------------------
+// one-token attention over the codes
+// --------------------------------------------------------------------------
+
+constexpr int kUnit = 64;           // keys of one unit of work: 16 for each warp
+constexpr int kWarps = 4;
+constexpr float kSlack = 8.f;       // log2 units a score may exceed its reference by
+
+struct QuantDecodeArgs {
+    void *out;
+    const void *q;
+    const uint8_t *kq, *vq;
+    const float *ks, *vs;
+    kvc_lengths len;
+    int batch, q_heads, kv_heads, group;
+    int64_t C;
+    int ring, window;
+    float scale_log2;
+    const float *cos_t, *sin_t;
+    int64_t rope_max_pos;
+    int grid;                        // CTAs of the attention launch
+    float *ws_o, *ws_m, *ws_l;       // [2 * grid][group] (x D)
+    int32_t *status;
+};
+
+// the visible keys of batch row b: n of them from slot `first` on, wrapping at C
+__device__ __forceinline__ int visible(const QuantDecodeArgs &a, int b, int64_t &first, uint32_t &bad)
+{
+    const int L = a.len.cache_total[b], T = a.len.total_abs[b];
+    bad = 0;
+    first = 0;
+    if (L < 0)
+        return 0;
+    if (L > a.C || T < L) {
+        bad = KVC_DEV_CAPACITY;
+        return 0;
+    }
+    if (a.cos_t && (int64_t)T > a.rope_max_pos) {
+        bad = KVC_DEV_ROPE_RANGE;
+        return 0;
+    }
+    const int n = a.window > 0 ? min(L, a.window) : L;
+    first = a.ring ? (int64_t)(T - n) % a.C : (int64_t)(L - n);
+    return n;
+}
+
+__device__ __forceinline__ float fast_exp2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float fast_log2(float x)
+{
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+                 "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t movm_trans(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// four codes as two pairs of halves, exactly: an int8 code c, its sign bit
+// flipped, is the byte c + 128, which under the high byte 0x64 is the half
+// 1024 + (c + 128); subtracting 1152 leaves c.  Every e4m3 value is a half.
+template <int FMT> __device__ __forceinline__ void codes_to_halves(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    if constexpr (FMT == KVC_INT8) {
+        const uint32_t u = w ^ 0x80808080u;
+        const uint32_t l = __byte_perm(u, 0x64646464u, 0x4140);
+        const uint32_t h = __byte_perm(u, 0x64646464u, 0x4342);
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(l), "r"(0x64806480u));
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(h), "r"(0x64806480u));
+    } else {
+        asm("{\n\t.reg .b16 l, h;\n\t"
+            "mov.b32 {l, h}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(w));
+    }
+}
+
+__device__ __forceinline__ uint4 ldg_stream(const uint8_t *p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 ldg_stream8(const uint8_t *p)
+{
+    uint2 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+
+// resident CTAs an SM, by the registers that O and the query fragments take
+__host__ __device__ constexpr int ctas_per_sm(int D, int HB)
+{
+    return D * HB <= 128 ? 4 : D * HB <= 256 ? 3 : 2;
+}
+
+template <int D, int HB> struct QuantSmem {
+    static constexpr int HEADS = 8 * HB;
+    static constexpr int Q_PITCH = D * 2 + 8;     // bytes: a fragment's 16 half-warp reads hit 16 distinct 8-byte banks
+    static constexpr int Q_BYTES = HEADS * Q_PITCH;
+    static constexpr int O_PITCH = D + 4;         // floats
+    static constexpr int O_OFF = (Q_BYTES + 15) / 16 * 16;
+    static constexpr int O_BYTES = HEADS * O_PITCH * 4;
+    static constexpr int ML_OFF = O_OFF + O_BYTES;
+    // factor of each head's query, then m and l of each warp
+    static constexpr int TOTAL = ML_OFF + (1 + 2 * kWarps) * HEADS * 4;
+};
+
+// Attention of one query over the codes of a flat share of the batch
+// (kvc_flat.cuh), a warp taking 16 keys at a time straight from global memory
+// into the operands of mma.sync m16n8k16:
+//   scores  S^T[key][head] = K[key][:] . Q[head][:]    A = K codes as halves
+//   output  O^T[d][head] += V^T[d][key] w[key][head]   A = V codes as halves
+// The sum over d does not care for the order of d, so lane (g, t) takes 16
+// consecutive codes of key g (and g + 8) as its share of four k-steps, and the
+// query's fragments are laid out to match: one 16-byte load feeds four MMAs.
+// Likewise the rows d of O^T are taken in the order in which lane (g, .) holds
+// the 16 (or 8) consecutive codes of its keys' V rows; the bytes of two keys
+// are interleaved with one permute for each two codes.
+// The keys' scales stay out of the products: s = (q . code) * ks in float32,
+// and a value's weight is 2^(s + log2(vs) - mo), with a reference maximum mo
+// of its own beside the m of the sum l = sum 2^(s - m).  So the weights are
+// rounded to halves near 1 however the rows' scales differ (a value row of
+// tiny scale may carry all of the probability).
+// The query is scaled by a power of two to [2^14, 2^15) at its largest and
+// rounded to halves: 11 bits, three more than a bf16 query has.
+template <typename T, int FMT, int D, int HB>
+__global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(D, HB))
+quant_decode_kernel(const QuantDecodeArgs a)
+{
+    using SM = QuantSmem<D, HB>;
+    constexpr int HEADS = SM::HEADS;
+    constexpr int KV4 = D / 64;               // 16-byte pieces of K a lane takes of one key
+    constexpr int VW = D / 32;                // 32-bit words of V a lane takes of one key
+    constexpr bool QREG = D * HB <= 128;      // query fragments in registers
+    extern __shared__ __align__(16) uint8_t smem[];
+    float *o_sh = reinterpret_cast<float *>(smem + SM::O_OFF);
+    float *q_factor = reinterpret_cast<float *>(smem + SM::ML_OFF);
+    float *m_sh = q_factor + HEADS, *l_sh = m_sh + kWarps * HEADS;
+
+    kvc::grid_dep_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int c = blockIdx.x;
+    auto units = [&](int b) {
+        int64_t first;
+        uint32_t bad;
+        const int n = visible(a, b, first, bad);
+        if (bad && c == 0 && warp == 0)
+            kvc::raise_status(a.status, bad);
+        return (n + kUnit - 1) / kUnit;
+    };
+    int b, base;
+    const int U = kvc_flat::locate(a.batch, a.kv_heads, units, -1, b, base);
+    int x = kvc_flat::share_begin(c, a.grid, U);
+    const int x_end = kvc_flat::share_begin(c + 1, a.grid, U);
+    if (x >= x_end)
+        return;
+    kvc_flat::row_of(a.batch, a.kv_heads, units, x, b, base);
+
+    for (int seg = 0; x < x_end; ++seg) {
+        int64_t first;
+        uint32_t bad;
+        const int n = visible(a, b, first, bad);
+        const int nu = (n + kUnit - 1) / kUnit;
+        const int h = (x - base) / nu;
+        const int u0 = (x - base) - h * nu;
+        const int u1 = min(nu, u0 + (x_end - x));
+        const int64_t slice = (int64_t)b * a.kv_heads + h;
+
+        // ---- the group's queries: rotated, scaled by a power of two, halves ----
+        __syncthreads();  // the last segment's reads of shared memory are done
+        {
+            const int64_t pos = (int64_t)a.len.total_abs[b] - 1;
+            const T *q = static_cast<const T *>(a.q) + slice * a.group * D;
+            for (int r = warp; r < HEADS; r += kWarps) {
+                constexpr int PPL = D / 64;  // rotation pairs a lane
+                float lo[PPL], hi[PPL], top = 0.f;
+#pragma unroll
+                for (int e = 0; e < PPL; ++e) {
+                    const int p = lane + 32 * e;
+                    lo[e] = hi[e] = 0.f;
+                    if (r < a.group) {
+                        lo[e] = kvc::Elem<T>::to_f32(q[r * D + p]);
+                        hi[e] = kvc::Elem<T>::to_f32(q[r * D + D / 2 + p]);
+                        if (a.cos_t)
+                            kvc::rope_pair(lo[e], hi[e], a.cos_t[pos * (D / 2) + p], a.sin_t[pos * (D / 2) + p]);
+                    }
+                    top = fmaxf(top, fmaxf(fabsf(lo[e]), fabsf(hi[e])));
+                }
+#pragma unroll
+                for (int d = 16; d; d >>= 1)
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                // top in [2^(ex - 127), 2^(ex - 126)); both powers of two stay normal
+                const int ex = min(max((int)(__float_as_uint(top) >> 23), 40), 250);
+                const float up = __uint_as_float((uint32_t)(127 + 14 + 127 - ex) << 23);
+                const float down = __uint_as_float((uint32_t)(ex - 14) << 23);
+#pragma unroll
+                for (int e = 0; e < PPL; ++e) {
+                    __half *row = reinterpret_cast<__half *>(smem + r * SM::Q_PITCH);
+                    row[lane + 32 * e] = __float2half_rn(lo[e] * up);
+                    row[D / 2 + lane + 32 * e] = __float2half_rn(hi[e] * up);
+                }
+                if (lane == 0)
+                    q_factor[r] = down;
+            }
+        }
+        __syncthreads();
+        auto q_frag = [&](int hb, int step) {
+            // k-step `step` = (span of 64 columns, word of the 16-byte piece)
+            return *reinterpret_cast<const uint2 *>(smem + (hb * 8 + g) * SM::Q_PITCH +
+                                                    2 * (64 * (step >> 2) + 16 * t + 4 * (step & 3)));
+        };
+        uint2 qf[QREG ? HB : 1][QREG ? D / 16 : 1];
+        if constexpr (QREG) {
+#pragma unroll
+            for (int hb = 0; hb < HB; ++hb)
+#pragma unroll
+                for (int st = 0; st < D / 16; ++st)
+                    qf[hb][st] = q_frag(hb, st);
+        }
+        float qs[HB][2];
+#pragma unroll
+        for (int hb = 0; hb < HB; ++hb) {
+            qs[hb][0] = q_factor[hb * 8 + 2 * t] * a.scale_log2;
+            qs[hb][1] = q_factor[hb * 8 + 2 * t + 1] * a.scale_log2;
+        }
+
+        const uint8_t *kb = a.kq + slice * a.C * D, *vb = a.vq + slice * a.C * D;
+        const float *ksb = a.ks + slice * a.C, *vsb = a.vs + slice * a.C;
+        auto slot = [&](int j) {
+            const int64_t r = first + j;
+            return r >= a.C ? r - a.C : r;
+        };
+
+        uint4 kr[2][KV4];
+        uint32_t vr[4][VW];
+        float ksr[2], vsr[2];
+        auto load_k = [&](int j0) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int j = j0 + g + 8 * e;
+                const bool ok = j < n;
+                const int64_t r = slot(j);
+#pragma unroll
+                for (int i = 0; i < KV4; ++i)
+                    kr[e][i] = ok ? ldg_stream(kb + r * D + 64 * i + 16 * t) : make_uint4(0, 0, 0, 0);
+                ksr[e] = ok ? __ldg(ksb + r) : 0.f;
+                vsr[e] = ok ? __ldg(vsb + r) : 0.f;
+            }
+        };
+        auto load_v = [&](int j0) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int j = j0 + 2 * t + (e & 1) + 8 * (e >> 1);
+                const bool ok = j < n;
+                const int64_t r = slot(j);
+                if constexpr (D == 64) {
+                    const uint2 v = ok ? ldg_stream8(vb + r * D + 8 * g) : make_uint2(0, 0);
+                    vr[e][0] = v.x;
+                    vr[e][1] = v.y;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < D / 128; ++i) {
+                        const uint4 v = ok ? ldg_stream(vb + r * D + 128 * i + 16 * g) : make_uint4(0, 0, 0, 0);
+                        vr[e][4 * i] = v.x;
+                        vr[e][4 * i + 1] = v.y;
+                        vr[e][4 * i + 2] = v.z;
+                        vr[e][4 * i + 3] = v.w;
+                    }
+                }
+            }
+        };
+
+        float o[HB][D / 16][4], m[HB][2], mo[HB][2], l[HB][2];
+#pragma unroll
+        for (int hb = 0; hb < HB; ++hb) {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+                o[hb][i][0] = o[hb][i][1] = o[hb][i][2] = o[hb][i][3] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                m[hb][e] = mo[hb][e] = -INFINITY;
+                l[hb][e] = 0.f;
+            }
+        }
+
+        const int j_end = min(n, u1 * kUnit);
+        int j0 = u0 * kUnit + 16 * warp;
+        if (j0 < j_end) {
+            load_k(j0);
+            load_v(j0);
+        }
+        for (; j0 < j_end; j0 += kUnit) {
+            // ---- scores ----
+            float s[HB][4];
+#pragma unroll
+            for (int hb = 0; hb < HB; ++hb)
+                s[hb][0] = s[hb][1] = s[hb][2] = s[hb][3] = 0.f;
+#pragma unroll
+            for (int i = 0; i < KV4; ++i) {
+                const uint32_t wa[4] = {kr[0][i].x, kr[0][i].y, kr[0][i].z, kr[0][i].w};
+                const uint32_t wb[4] = {kr[1][i].x, kr[1][i].y, kr[1][i].z, kr[1][i].w};
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    uint32_t a0, a1, a2, a3;
+                    codes_to_halves<FMT>(wa[w], a0, a2);
+                    codes_to_halves<FMT>(wb[w], a1, a3);
+#pragma unroll
+                    for (int hb = 0; hb < HB; ++hb) {
+                        uint2 f;
+                        if constexpr (QREG)
+                            f = qf[hb][4 * i + w];
+                        else
+                            f = q_frag(hb, 4 * i + w);
+                        mma_f16(s[hb], a0, a1, a2, a3, f.x, f.y);
+                    }
+                }
+            }
+            const bool in0 = j0 + g < n, in1 = j0 + g + 8 < n;
+            const float k0 = ksr[0], k1 = ksr[1];
+            const float lv0 = fast_log2(vsr[0]), lv1 = fast_log2(vsr[1]);
+            if (j0 + kUnit < j_end)
+                load_k(j0 + kUnit);
+
+            // ---- softmax ----
+            bool raise = false;
+#pragma unroll
+            for (int hb = 0; hb < HB; ++hb) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    s[hb][e] = in0 ? s[hb][e] * (k0 * qs[hb][e]) : -INFINITY;
+                    s[hb][2 + e] = in1 ? s[hb][2 + e] * (k1 * qs[hb][e]) : -INFINITY;
+                    raise |= s[hb][e] > m[hb][e] + kSlack || s[hb][2 + e] > m[hb][e] + kSlack ||
+                             s[hb][e] + lv0 > mo[hb][e] + kSlack || s[hb][2 + e] + lv1 > mo[hb][e] + kSlack;
+                }
+            }
+            if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                for (int hb = 0; hb < HB; ++hb) {
+                    float shrink[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float top = fmaxf(s[hb][e], s[hb][2 + e]);
+                        float top_o = fmaxf(s[hb][e] + lv0, s[hb][2 + e] + lv1);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) {
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                            top_o = fmaxf(top_o, __shfl_xor_sync(0xffffffffu, top_o, d));
+                        }
+                        const float m_new = fmaxf(m[hb][e], top), mo_new = fmaxf(mo[hb][e], top_o);
+                        l[hb][e] *= m[hb][e] == m_new ? 1.f : fast_exp2(m[hb][e] - m_new);
+                        shrink[e] = mo[hb][e] == mo_new ? 1.f : fast_exp2(mo[hb][e] - mo_new);
+                        m[hb][e] = m_new;
+                        mo[hb][e] = mo_new;
+                    }
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        o[hb][i][0] *= shrink[0];
+                        o[hb][i][1] *= shrink[1];
+                        o[hb][i][2] *= shrink[0];
+                        o[hb][i][3] *= shrink[1];
+                    }
+                }
+            }
+            uint32_t b0[HB], b1[HB];
+#pragma unroll
+            for (int hb = 0; hb < HB; ++hb) {
+                float w[4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float rm = m[hb][e] == -INFINITY ? 0.f : m[hb][e];
+                    const float ro = mo[hb][e] == -INFINITY ? 0.f : mo[hb][e];
+                    l[hb][e] += fast_exp2(s[hb][e] - rm) + fast_exp2(s[hb][2 + e] - rm);
+                    w[e] = fast_exp2(s[hb][e] + lv0 - ro);
+                    w[2 + e] = fast_exp2(s[hb][2 + e] + lv1 - ro);
+                }
+                const __half2 h0 = __floats2half2_rn(w[0], w[1]), h1 = __floats2half2_rn(w[2], w[3]);
+                b0[hb] = movm_trans(*reinterpret_cast<const uint32_t *>(&h0));
+                b1[hb] = movm_trans(*reinterpret_cast<const uint32_t *>(&h1));
+            }
+
+            // ---- output ----
+#pragma unroll
+            for (int w = 0; w < VW; ++w) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    // columns 4 w + 2 e and + 1 of keys 2 t, 2 t + 1 and of 2 t + 8, 2 t + 9
+                    const uint32_t sel = e ? 0x7362 : 0x5140;
+                    uint32_t a0, a1, a2, a3;
+                    codes_to_halves<FMT>(__byte_perm(vr[0][w], vr[1][w], sel), a0, a1);
+                    codes_to_halves<FMT>(__byte_perm(vr[2][w], vr[3][w], sel), a2, a3);
+#pragma unroll
+                    for (int hb = 0; hb < HB; ++hb)
+                        mma_f16(o[hb][2 * w + e], a0, a1, a2, a3, b0[hb], b1[hb]);
+                }
+            }
+            if (j0 + kUnit < j_end)
+                load_v(j0 + kUnit);
+        }
+
+        // ---- join the warps: m, l, then O relative to the common m, in warp order ----
+#pragma unroll
+        for (int hb = 0; hb < HB; ++hb) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1)
+                    l[hb][e] += __shfl_xor_sync(0xffffffffu, l[hb][e], d);
+                if (g == 0) {
+                    m_sh[warp * HEADS + hb * 8 + 2 * t + e] = m[hb][e];
+                    l_sh[warp * HEADS + hb * 8 + 2 * t + e] = l[hb][e];
+                }
+            }
+        }
+        __syncthreads();
+        float f[HB][2];
+#pragma unroll
+        for (int hb = 0; hb < HB; ++hb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w)
+                    top = fmaxf(top, m_sh[w * HEADS + hb * 8 + 2 * t + e]);
+                // O is relative to mo; a warp without keys holds zeros
+                f[hb][e] = mo[hb][e] == -INFINITY ? (m[hb][e] == -INFINITY ? 1.f : 0.f) : exp2f(mo[hb][e] - top);
+            }
+        for (int w = 0; w < kWarps; ++w) {
+            if (warp == w) {
+#pragma unroll
+                for (int hb = 0; hb < HB; ++hb)
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            // tile i holds columns 2 i and 2 i + 1 of the lane's run of consecutive columns
+                            constexpr int RUN = D == 64 ? 8 : 16;
+                            const int col = (2 * i / RUN) * 128 + RUN * g + 2 * i % RUN + (e >> 1);
+                            float *to = o_sh + (hb * 8 + 2 * t + (e & 1)) * SM::O_PITCH + col;
+                            const float v = o[hb][i][e] * f[hb][e & 1];
+                            *to = w ? *to + v : v;
+                        }
+            }
+            __syncthreads();
+        }
+        const bool whole = u0 == 0 && u1 == nu;
+        const int64_t part = 2 * (int64_t)c + (seg == 0 ? 0 : 1);
+        for (int idx = threadIdx.x; idx < a.group * D; idx += 32 * kWarps) {
+            const int r = idx / D, d = idx % D;
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+                top = fmaxf(top, m_sh[w * HEADS + r]);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float mw = m_sh[w * HEADS + r];
+                // (a warp whose scores are all NaN keeps m = -inf and a NaN sum)
+                sum += l_sh[w * HEADS + r] * (mw == top || mw == -INFINITY ? 1.f : exp2f(mw - top));
+            }
+            const float v = o_sh[r * SM::O_PITCH + d];
+            if (whole) {
+                static_cast<T *>(a.out)[slice * a.group * D + idx] = kvc::Elem<T>::from_f32(v / sum);
+            } else {
+                a.ws_o[(part * a.group + r) * D + d] = v;
+                if (d == 0) {
+                    a.ws_m[part * a.group + r] = top;
+                    a.ws_l[part * a.group + r] = sum;
+                }
+            }
+        }
+        x += u1 - u0;
+        if (x == base + nu * a.kv_heads && x < x_end) {
+            base = x;
+            do {
+                ++b;
+            } while (visible(a, b, first, bad) == 0);
+        }
+    }
+}
+
+// Joins the partial results of one query head: out = sum_i 2^(m_i - m) o_i /
+// sum_i 2^(m_i - m) l_i over the CTAs whose shares cover its row.
+template <typename T, int D>
+__global__ void __launch_bounds__(D)
+quant_merge_kernel(const QuantDecodeArgs a)
+{
+    const int slice = blockIdx.x, r = blockIdx.y, d = threadIdx.x;
+    const int b = slice / a.kv_heads, h = slice % a.kv_heads;
+    auto units = [&](int bb) {
+        int64_t first;
+        uint32_t bad;
+        return (visible(a, bb, first, bad) + kUnit - 1) / kUnit;
+    };
+    int b_out, base;
+    const int U = kvc_flat::locate(a.batch, a.kv_heads, units, b, b_out, base);
+    const int nu = units(b);
+    kvc::grid_dep_wait();
+    if (nu == 0)
+        return;
+    const int x0 = base + h * nu, x1 = x0 + nu;
+    const int c0 = kvc_flat::share_of(x0, a.grid, U), c1 = kvc_flat::share_of(x1 - 1, a.grid, U);
+    if (c0 == c1)
+        return;  // written by that CTA
+    auto part_of = [&](int c) {
+        // the row's segment is the first of CTA c unless c began before the row
+        return 2 * (int64_t)c + (kvc_flat::share_begin(c, a.grid, U) < x0 ? 1 : 0);
+    };
+    float top = -INFINITY;
+    for (int c = c0; c <= c1; ++c)
+        if (kvc_flat::share_begin(c, a.grid, U) < kvc_flat::share_begin(c + 1, a.grid, U))
+            top = fmaxf(top, a.ws_m[part_of(c) * a.group + r]);
+    float acc = 0.f, sum = 0.f;
+    for (int c = c0; c <= c1; ++c) {
+        if (kvc_flat::share_begin(c, a.grid, U) == kvc_flat::share_begin(c + 1, a.grid, U))
+            continue;
+        const int64_t p = part_of(c) * a.group + r;
+        const float mc = a.ws_m[p];
+        const float w = mc == top || mc == -INFINITY ? 1.f : exp2f(mc - top);
+        acc += a.ws_o[p * D + d] * w;
+        sum += a.ws_l[p] * w;
+    }
+    static_cast<T *>(a.out)[((int64_t)slice * a.group + r) * D + d] = kvc::Elem<T>::from_f32(acc / sum);
+}
+
+// one wave of resident CTAs, or one CTA a unit where the cache has fewer
+int decode_grid(int batch, int kv_heads, int group, int64_t C, int D)
+{
+    const int64_t most = (int64_t)batch * kv_heads * ((C + kUnit - 1) / kUnit);
+    const int64_t wave = (int64_t)kvc_host::sm_count() * ctas_per_sm(D, group > 8 ? 2 : 1);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(most, wave));
+}
+
+template <typename T, int FMT, int D, int HB> kvc_status launch_decode(const QuantDecodeArgs &a, cudaStream_t stream)
+{
+    constexpr int smem = QuantSmem<D, HB>::TOTAL;
+    auto kern = quant_decode_kernel<T, FMT, D, HB>;
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return KVC_ERR_CUDA;
+    kern<<<a.grid, 32 * kWarps, smem, stream>>>(a);
+    // a row of one unit is never split
+    if (a.C > kUnit) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(a.batch * a.kv_heads, a.group);
+        cfg.blockDim = dim3(D);
+        cfg.stream = stream;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, quant_merge_kernel<T, D>, a) != cudaSuccess)
+            return KVC_ERR_CUDA;
+    }
+    return kvc_host::launch_status();
+}
+
+template <typename T, int FMT> kvc_status launch_decode_dim(const QuantDecodeArgs &a, int D, cudaStream_t stream)
+{
+    const bool two = a.group > 8;
+    switch (D) {
+    case 64:
+        return two ? launch_decode<T, FMT, 64, 2>(a, stream) : launch_decode<T, FMT, 64, 1>(a, stream);
+    case 128:
+        return two ? launch_decode<T, FMT, 128, 2>(a, stream) : launch_decode<T, FMT, 128, 1>(a, stream);
+    default:
+        return two ? launch_decode<T, FMT, 256, 2>(a, stream) : launch_decode<T, FMT, 256, 1>(a, stream);
+    }
+}
+
+bool format_ok(int format) { return format == KVC_INT8 || format == KVC_E4M3; }
+
+template <typename T> kvc_status launch_append(const AppendArgs &a, int format, cudaStream_t stream)
+{
+    const int lpr = a.D <= 64 ? 8 : a.D <= 128 ? 16 : 32;
+    const int64_t rows = (int64_t)a.batch * a.kv_heads * a.S;
+    const int64_t blocks = (rows * lpr + 255) / 256;
+    if (blocks > (int64_t)INT32_MAX)
+        return KVC_ERR_SHAPE;
+    const unsigned n = (unsigned)blocks;
+    if (format == KVC_INT8) {
+        if (lpr == 8)
+            quant_append_kernel<T, KVC_INT8, 8><<<n, 256, 0, stream>>>(a);
+        else if (lpr == 16)
+            quant_append_kernel<T, KVC_INT8, 16><<<n, 256, 0, stream>>>(a);
+        else
+            quant_append_kernel<T, KVC_INT8, 32><<<n, 256, 0, stream>>>(a);
+    } else {
+        if (lpr == 8)
+            quant_append_kernel<T, KVC_E4M3, 8><<<n, 256, 0, stream>>>(a);
+        else if (lpr == 16)
+            quant_append_kernel<T, KVC_E4M3, 16><<<n, 256, 0, stream>>>(a);
+        else
+            quant_append_kernel<T, KVC_E4M3, 32><<<n, 256, 0, stream>>>(a);
+    }
+    return kvc_host::launch_status();
+}
+
+template <typename T> kvc_status launch_dequant(const DequantArgs &a, int format, cudaStream_t stream)
+{
+    const int64_t most = std::min(a.C, a.R) * (a.D / 16);
+    const int slices = a.batch * a.kv_heads;
+    // enough blocks for the longest rows, at most 16 an SM over all slices
+    int64_t nx = (most + 255) / 256;
+    nx = std::min<int64_t>(nx, std::max<int64_t>(1, (int64_t)kvc_host::sm_count() * 16 / (2 * slices) + 1));
+    const dim3 grid((unsigned)nx, slices, 2);
+    if (format == KVC_INT8)
+        dequant_rows_kernel<T, KVC_INT8><<<grid, 256, 0, stream>>>(a);
+    else
+        dequant_rows_kernel<T, KVC_E4M3><<<grid, 256, 0, stream>>>(a);
+    return kvc_host::launch_status();
+}
+
+// what the three calls ask of the quantised cache's buffers
+kvc_status check_cache(const void *kq, const void *vq, const void *ks, const void *vs, int batch, int kv_heads,
+                       int64_t C, int D)
+{
+    if (!kq || !vq || !ks || !vs)
+        return KVC_ERR_NULL;
+    for (const void *p : {kq, vq, ks, vs})
+        if (!kvc_host::aligned16(p))
+            return KVC_ERR_ALIGN;
+    const size_t rows = (size_t)batch * kv_heads * C;
+    const void *at[4] = {kq, vq, ks, vs};
+    const size_t bytes[4] = {rows * D, rows * D, rows * 4, rows * 4};
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < i; ++j)
+            if (kvc_host::overlaps(at[i], bytes[i], at[j], bytes[j]))
+                return KVC_ERR_SHAPE;
+    return KVC_OK;
+}
+
+} // namespace
+
+KVC_API kvc_status kvc_quant_append(void *kq_cache, void *vq_cache, float *k_scale, float *v_scale,
+                                    const void *new_k, const void *new_v, kvc_lengths len, int batch,
+                                    int kv_heads, int new_tokens, int64_t capacity, int head_dim, int dtype,
+                                    int format, int windowed, const float *rope_cos, const float *rope_sin,
+                                    int64_t rope_max_pos, int32_t *dev_status, void *stream_)
+{
+    if (kvc_host::elem_bytes_of(dtype) == 0 || !format_ok(format))
+        return KVC_ERR_DTYPE;
+    if (batch < 0 || kv_heads < 1 || new_tokens < 1 || head_dim < 1)
+        return KVC_ERR_SHAPE;
+    if (windowed != KVC_CONTIGUOUS && windowed != KVC_RING)
+        return KVC_ERR_UNSUPPORTED;
+    if (head_dim > 256 || head_dim % 16 != 0)
+        return KVC_ERR_UNSUPPORTED;
+    if (capacity < 1 || capacity > (int64_t)INT32_MAX)
+        return KVC_ERR_CAPACITY;
+    if ((rope_cos == nullptr) != (rope_sin == nullptr))
+        return KVC_ERR_NULL;
+    if (rope_cos && rope_max_pos < 1)
+        return KVC_ERR_SHAPE;
+    if (batch == 0)
+        return KVC_OK;
+    if (!new_k || !new_v || !kvc_host::lengths_ok(len))
+        return KVC_ERR_NULL;
+    const kvc_status st = check_cache(kq_cache, vq_cache, k_scale, v_scale, batch, kv_heads, capacity, head_dim);
+    if (st != KVC_OK)
+        return st;
+    for (const void *p : {new_k, new_v, (const void *)rope_cos, (const void *)rope_sin})
+        if (p && !kvc_host::aligned16(p))
+            return KVC_ERR_ALIGN;
+    AppendArgs a{static_cast<uint8_t *>(kq_cache), static_cast<uint8_t *>(vq_cache), k_scale, v_scale, new_k, new_v,
+                 len, batch, kv_heads, new_tokens, head_dim, capacity, windowed == KVC_RING, rope_cos, rope_sin,
+                 rope_max_pos, dev_status};
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    switch (dtype) {
+    case KVC_F32:
+        return launch_append<float>(a, format, stream);
+    case KVC_BF16:
+        return launch_append<__nv_bfloat16>(a, format, stream);
+    default:
+        return launch_append<__half>(a, format, stream);
+    }
+}
+
+KVC_API kvc_status kvc_dequant_rows(void *k_out, void *v_out, const void *kq_cache, const void *vq_cache,
+                                    const float *k_scale, const float *v_scale, kvc_lengths len, int batch,
+                                    int kv_heads, int64_t capacity, int64_t rows_out, int head_dim, int dtype,
+                                    int format, int windowed, int32_t *dev_status, void *stream_)
+{
+    const int eb = kvc_host::elem_bytes_of(dtype);
+    if (eb == 0 || !format_ok(format))
+        return KVC_ERR_DTYPE;
+    if (batch < 0 || kv_heads < 1 || head_dim < 1 || (int64_t)batch * kv_heads > 65535)
+        return KVC_ERR_SHAPE;
+    if (windowed != KVC_CONTIGUOUS && windowed != KVC_RING)
+        return KVC_ERR_UNSUPPORTED;
+    if (head_dim > 256 || head_dim % 16 != 0)
+        return KVC_ERR_UNSUPPORTED;
+    if (capacity < 1 || capacity > (int64_t)INT32_MAX || rows_out < 1 || rows_out > (int64_t)INT32_MAX)
+        return KVC_ERR_CAPACITY;
+    if (batch == 0)
+        return KVC_OK;
+    if (!k_out || !v_out || !kvc_host::lengths_ok(len))
+        return KVC_ERR_NULL;
+    const kvc_status st = check_cache(kq_cache, vq_cache, k_scale, v_scale, batch, kv_heads, capacity, head_dim);
+    if (st != KVC_OK)
+        return st;
+    for (const void *p : {(const void *)k_out, (const void *)v_out})
+        if (!kvc_host::aligned16(p))
+            return KVC_ERR_ALIGN;
+    const size_t in_rows = (size_t)batch * kv_heads * capacity;
+    const size_t out_bytes = (size_t)batch * kv_heads * rows_out * head_dim * eb;
+    if (kvc_host::overlaps(k_out, out_bytes, v_out, out_bytes))
+        return KVC_ERR_SHAPE;
+    for (const void *o : {(const void *)k_out, (const void *)v_out}) {
+        for (const void *p : {kq_cache, vq_cache})
+            if (kvc_host::overlaps(o, out_bytes, p, in_rows * head_dim))
+                return KVC_ERR_SHAPE;
+        for (const void *p : {(const void *)k_scale, (const void *)v_scale})
+            if (kvc_host::overlaps(o, out_bytes, p, in_rows * 4))
+                return KVC_ERR_SHAPE;
+    }
+    DequantArgs a{k_out, v_out, static_cast<const uint8_t *>(kq_cache), static_cast<const uint8_t *>(vq_cache),
+                  k_scale, v_scale, len, batch, kv_heads, head_dim, capacity, rows_out, windowed == KVC_RING,
+                  dev_status};
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    switch (dtype) {
+    case KVC_F32:
+        return launch_dequant<float>(a, format, stream);
+    case KVC_BF16:
+        return launch_dequant<__nv_bfloat16>(a, format, stream);
+    default:
+        return launch_dequant<__half>(a, format, stream);
+    }
+}
+
+KVC_API size_t kvc_gqa_decode_quant_workspace_size(int batch, int q_heads, int kv_heads, int64_t capacity,
+                                                   int head_dim)
+{
+    if (batch < 1 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || capacity < 1 || head_dim < 1)
+        return 0;
+    if (capacity <= kUnit)
+        return 0;
+    const size_t parts = 2 * (size_t)decode_grid(batch, kv_heads, q_heads / kv_heads, capacity, head_dim) * (q_heads / kv_heads);
+    return parts * (head_dim + 2) * sizeof(float);
+}
+
+KVC_API kvc_status kvc_gqa_decode_quant(void *out, const void *q, const void *kq_cache, const void *vq_cache,
+                                        const float *k_scale, const float *v_scale, kvc_lengths len, int batch,
+                                        int q_heads, int kv_heads, int64_t capacity, int head_dim, int dtype,
+                                        int format, int windowed, int local_window_size, float scale,
+                                        const float *rope_cos, const float *rope_sin, int64_t rope_max_pos,
+                                        void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream_)
+{
+    if (kvc_host::elem_bytes_of(dtype) == 0 || !format_ok(format))
+        return KVC_ERR_DTYPE;
+    if (dtype == KVC_F32)
+        return KVC_ERR_UNSUPPORTED;
+    if (batch < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0)
+        return KVC_ERR_SHAPE;
+    if (windowed != KVC_CONTIGUOUS && windowed != KVC_RING)
+        return KVC_ERR_UNSUPPORTED;
+    if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || q_heads / kv_heads > 16)
+        return KVC_ERR_UNSUPPORTED;
+    if (capacity < 1 || capacity > (int64_t)INT32_MAX)
+        return KVC_ERR_CAPACITY;
+    if ((int64_t)batch * kv_heads * ((capacity + kUnit - 1) / kUnit) > (int64_t)INT32_MAX)
+        return KVC_ERR_SHAPE;
+    if ((rope_cos == nullptr) != (rope_sin == nullptr))
+        return KVC_ERR_NULL;
+    if (rope_cos && rope_max_pos < 1)
+        return KVC_ERR_SHAPE;
+    if (batch == 0)
+        return KVC_OK;
+    if (!out || !q || !kvc_host::lengths_ok(len))
+        return KVC_ERR_NULL;
+    const kvc_status st = check_cache(kq_cache, vq_cache, k_scale, v_scale, batch, kv_heads, capacity, head_dim);
+    if (st != KVC_OK)
+        return st;
+    for (const void *p : {(const void *)out, q})
+        if (!kvc_host::aligned16(p))
+            return KVC_ERR_ALIGN;
+    const size_t need = kvc_gqa_decode_quant_workspace_size(batch, q_heads, kv_heads, capacity, head_dim);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return KVC_ERR_WORKSPACE;
+    if (need > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return KVC_ERR_ALIGN;
+    QuantDecodeArgs a{};
+    a.out = out;
+    a.q = q;
+    a.kq = static_cast<const uint8_t *>(kq_cache);
+    a.vq = static_cast<const uint8_t *>(vq_cache);
+    a.ks = k_scale;
+    a.vs = v_scale;
+    a.len = len;
+    a.batch = batch;
+    a.q_heads = q_heads;
+    a.kv_heads = kv_heads;
+    a.group = q_heads / kv_heads;
+    a.C = capacity;
+    a.ring = windowed == KVC_RING;
+    a.window = local_window_size;
+    a.scale_log2 = (scale == 0.f ? 1.0f / sqrtf((float)head_dim) : scale) * kLog2e;
+    a.cos_t = rope_cos;
+    a.sin_t = rope_sin;
+    a.rope_max_pos = rope_max_pos;
+    a.grid = decode_grid(batch, kv_heads, a.group, capacity, head_dim);
+    const int64_t parts = 2 * (int64_t)a.grid * a.group;
+    a.ws_o = static_cast<float *>(workspace);
+    a.ws_m = a.ws_o ? a.ws_o + parts * head_dim : nullptr;
+    a.ws_l = a.ws_m ? a.ws_m + parts : nullptr;
+    a.status = dev_status;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    if (dtype == KVC_BF16)
+        return format == KVC_INT8 ? launch_decode_dim<__nv_bfloat16, KVC_INT8>(a, head_dim, stream)
+                                  : launch_decode_dim<__nv_bfloat16, KVC_E4M3>(a, head_dim, stream);
+    return format == KVC_INT8 ? launch_decode_dim<__half, KVC_INT8>(a, head_dim, stream)
+                              : launch_decode_dim<__half, KVC_E4M3>(a, head_dim, stream);
+}

@@ -17,6 +17,7 @@ LIB_PATH = os.path.join(_HERE, "libkvc.so")
 KVC_F32, KVC_BF16, KVC_F16 = 0, 1, 2
 KVC_LINEAR, KVC_CIRCULAR = 0, 1
 KVC_APPEND, KVC_COPY_BACK = 0, 1
+KVC_INT8, KVC_E4M3 = 0, 1
 
 KVC_OK = 0
 STATUS_NAMES = {
@@ -39,6 +40,8 @@ EXPORTS = ("kvc_tensor_scatter", "kvc_seq_lengths", "kvc_window_append", "kvc_gq
            "kvc_paged_append", "kvc_gqa_decode_paged", "kvc_window_append_inplace",
            "kvc_quantize_pages", "kvc_gqa_decode_paged_q",
            "kvc_gqa_prefill_chunk", "kvc_gqa_prefill_workspace_size", "kvc_window_prefill_step",
+           "kvc_quant_append", "kvc_dequant_rows", "kvc_gqa_decode_quant",
+           "kvc_gqa_decode_quant_workspace_size",
            "kvc_status_string", "kvc_abi_version")
 KVC_DECODE_STATIC_SCRATCH_BYTES = 16 << 20
 KVC_PAGE_QUANT = 0x40000000  # block-table flag: the entry names an int8 page
@@ -121,6 +124,11 @@ def library() -> ctypes.CDLL:
             "kvc_gqa_prefill_workspace_size": [I, I, I, I, I64, I, I, I],
             "kvc_window_prefill_step": [P, P, P, P, P, P, P, P, L, I, I, I, I, I64, I, I, I, I,
                                         F, P, P, I64, P, SZ, P, P],
+            "kvc_quant_append": [P, P, P, P, P, P, L, I, I, I, I64, I, I, I, I, P, P, I64, P, P],
+            "kvc_dequant_rows": [P, P, P, P, P, P, L, I, I, I64, I64, I, I, I, I, P, P],
+            "kvc_gqa_decode_quant": [P, P, P, P, P, P, L, I, I, I, I64, I, I, I, I, I, F, P, P, I64,
+                                     P, SZ, P, P],
+            "kvc_gqa_decode_quant_workspace_size": [I, I, I, I64, I],
             "kvc_status_string": [I],
             "kvc_abi_version": [],
         }
@@ -132,6 +140,7 @@ def library() -> ctypes.CDLL:
         lib.kvc_decode_step_workspace_size.restype = SZ
         lib.kvc_window_decode_step_workspace_size.restype = SZ
         lib.kvc_gqa_prefill_workspace_size.restype = SZ
+        lib.kvc_gqa_decode_quant_workspace_size.restype = SZ
         lib.kvc_status_string.restype = ctypes.c_char_p
         _lib = lib
     return _lib
@@ -443,4 +452,82 @@ def kvc_window_prefill_step(out, q, k_cache, v_cache, new_k, new_v, lengths, win
         _ptr(k_stage), _ptr(v_stage), lengths.c(), B, Hq, Hkv, S, C, D, _dtype_code(q),
         int(windowed), local_window_size, scale, cs, sn, rmax, _ptr(workspace),
         0 if workspace is None else workspace.numel(), _ptr(status), _stream(stream)))
+    return out
+
+
+def _same(name, t, shape, dtype=None):
+    """t has the shape (and type) that the other arguments fix: the library
+    gets sizes once, from one of them, and cannot see the others'."""
+    if tuple(t.shape) != tuple(shape) or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name}: expected {tuple(shape)}{'' if dtype is None else f' {dtype}'}, "
+                         f"got {tuple(t.shape)} {t.dtype}")
+
+
+def _code_format(kq):
+    if kq.dtype not in (torch.int8, torch.float8_e4m3fn):
+        raise ValueError(f"a quantised cache is torch.int8 or torch.float8_e4m3fn, got {kq.dtype}")
+    return KVC_INT8 if kq.dtype == torch.int8 else KVC_E4M3
+
+
+def _quant_cache(kq, vq, k_scale, v_scale):
+    """The sizes and format of a quantised cache: kq, vq [B, Hkv, C, D] codes and k_scale,
+    v_scale [B, Hkv, C] float32."""
+    fmt = _code_format(kq)
+    _same("vq", vq, kq.shape, kq.dtype)
+    _same("k_scale", k_scale, kq.shape[:3], torch.float32)
+    _same("v_scale", v_scale, kq.shape[:3], torch.float32)
+    return kq.shape, fmt
+
+
+def kvc_quant_append(kq, vq, k_scale, v_scale, new_k, new_v, lengths, windowed, rope=None,
+                     status=None, stream=None):
+    """Write new rows [B, Hkv, S, D] into a quantised cache (include/kvc.h): kq, vq
+    [B, Hkv, C, D] int8 or float8_e4m3fn, k_scale, v_scale [B, Hkv, C] float32."""
+    (B, Hkv, C, D), fmt = _quant_cache(kq, vq, k_scale, v_scale)
+    S = new_k.shape[2]
+    _same("new_k", new_k, (B, Hkv, S, D))
+    _same("new_v", new_v, (B, Hkv, S, D), new_k.dtype)
+    cs, sn, rmax = _rope(rope)
+    _check("kvc_quant_append", library().kvc_quant_append(
+        _ptr(kq), _ptr(vq), _ptr(k_scale), _ptr(v_scale), _ptr(new_k), _ptr(new_v), lengths.c(), B,
+        Hkv, S, C, D, _dtype_code(new_k), fmt, int(windowed), cs, sn, rmax, _ptr(status),
+        _stream(stream)))
+
+
+def kvc_dequant_rows(k_out, v_out, kq, vq, k_scale, v_scale, lengths, windowed, status=None,
+                     stream=None):
+    """The resident rows of a quantised cache, oldest first, into k_out, v_out
+    [B, Hkv, rows, D] (include/kvc.h)."""
+    (B, Hkv, C, D), fmt = _quant_cache(kq, vq, k_scale, v_scale)
+    R = k_out.shape[2]
+    _same("k_out", k_out, (B, Hkv, R, D))
+    _same("v_out", v_out, (B, Hkv, R, D), k_out.dtype)
+    _check("kvc_dequant_rows", library().kvc_dequant_rows(
+        _ptr(k_out), _ptr(v_out), _ptr(kq), _ptr(vq), _ptr(k_scale), _ptr(v_scale), lengths.c(), B,
+        Hkv, C, R, D, _dtype_code(k_out), fmt, int(windowed), _ptr(status), _stream(stream)))
+
+
+def quant_decode_workspace(q, kq):
+    """Workspace for kvc_gqa_decode_quant (None when it needs none)."""
+    B, Hq, _, D = q.shape
+    n = library().kvc_gqa_decode_quant_workspace_size(B, Hq, kq.shape[1], kq.shape[2], D)
+    return torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+
+
+def kvc_gqa_decode_quant(out, q, kq, vq, k_scale, v_scale, lengths, windowed, local_window_size=0,
+                         scale=0.0, rope=None, workspace="auto", status=None, stream=None):
+    """One-token attention over a quantised cache (include/kvc.h).  workspace: "auto" allocates
+    what the call needs."""
+    (B, Hkv, C, D), fmt = _quant_cache(kq, vq, k_scale, v_scale)
+    Hq = q.shape[1]
+    _same("q", q, (B, Hq, 1, D))
+    _same("out", out, q.shape, q.dtype)
+    if isinstance(workspace, str):
+        workspace = quant_decode_workspace(q, kq)
+    cs, sn, rmax = _rope(rope)
+    _check("kvc_gqa_decode_quant", library().kvc_gqa_decode_quant(
+        _ptr(out), _ptr(q), _ptr(kq), _ptr(vq), _ptr(k_scale), _ptr(v_scale), lengths.c(), B, Hq,
+        Hkv, C, D, _dtype_code(q), fmt, int(windowed), local_window_size, scale, cs, sn, rmax,
+        _ptr(workspace), 0 if workspace is None else workspace.numel(), _ptr(status),
+        _stream(stream)))
     return out
