@@ -24,6 +24,10 @@
  *     kvc_quant_append, kvc_dequant_rows, kvc_gqa_decode_quant  a cache whose
  *                          rows are quantised as they are written, read back
  *                          in 16 bits or attended over as codes
+ *     kvc_tree_mask, kvc_tree_append, kvc_gqa_tree, kvc_tree_commit  a tree of
+ *                          drafted tokens verified over the cache
+ *     kvc_page_bounds, kvc_gqa_decode_sparse  one-token attention over the
+ *                          pages that a cheap score selects
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -735,6 +739,152 @@ kvc_status kvc_gqa_decode_quant(void *out, const void *q, const void *kq_cache,
 /* Bytes of workspace kvc_gqa_decode_quant needs for these sizes (0 on bad sizes). */
 size_t kvc_gqa_decode_quant_workspace_size(int batch, int q_heads, int kv_heads, int64_t capacity,
                                            int head_dim);
+
+/*
+ * One-token attention over selected pages of a paged cache ("Persistent KV
+ * Cache and Decode Performance Roadmap", "Phase 2").  Every full page holds,
+ * for each kv head, 8-bit bounds of its keys (as stored, K rotated):
+ *     s = max|k| / 127,  hi_d = ceil(max_r k[r][d] / s),  lo_d = floor(min_r k[r][d] / s)
+ * (float32 divisions; s = 0 for a page of zeros, s = infinity and zero codes
+ * for a page with a NaN or an infinity, which is then always taken before
+ * others).
+ *   bounds       device int8 [n_pool_pages, kv_heads, 2, head_dim] (hi, lo)
+ *   bound_scale  device float32 [n_pool_pages, kv_heads]
+ *
+ * kvc_page_bounds -- write the bounds of the pages that the step of S tokens
+ * filled: logical pages [P / page_size, T / page_size) of each batch row
+ * (after kvc_paged_append; a one-token step that fills no page writes
+ * nothing).  Other pages' bounds are left as they were.  A page id outside the
+ * pool sets KVC_DEV_INDEX_OOB and is skipped.  KVC_BF16/KVC_F16, head_dim 64,
+ * 128 or 256 (KVC_ERR_UNSUPPORTED); bounds, bound_scale, k_pool 16-byte aligned.
+ */
+kvc_status kvc_page_bounds(void *bounds, float *bound_scale, const void *k_pool,
+                           const int32_t *block_table, int max_pages, int64_t n_pool_pages,
+                           int page_size, kvc_lengths len, int batch, int kv_heads, int new_tokens,
+                           int head_dim, int dtype, int32_t *dev_status, void *stream);
+
+/*
+ * kvc_gqa_decode_sparse -- kvc_gqa_decode_paged over min(n_select, pages) of the
+ * ceil(T / page_size) pages of each (batch row, kv head): the first sink_pages,
+ * the last recent_pages (that of the newest token among them), and of the
+ * others those with the largest scores, ties to the lower page.  With q the
+ * rotated queries of the group (float32),
+ *     u_d = sum_h max(q_hd, 0), w_d = sum_h min(q_hd, 0), rounded to float32,
+ *     sq = max(|u|, |w|) / 127, both rounded to codes rint(. / sq),
+ *     score = s * float(sum_d code(u_d) hi_d + code(w_d) lo_d)
+ * the 8-bit form of sum_d max(q_d hi_d, q_d lo_d), which no key of the page
+ * exceeds.  The sum is of whole numbers, so the choice is the same on every run.
+ * Every page but the last recent_pages must have had its bounds written.
+ * selected     device int32 [batch, kv_heads, n_select]: the logical pages taken,
+ *              ascending, then -1.  A batch row that kvc_seq_lengths rejected, or
+ *              whose position is past rope_max_pos (KVC_DEV_ROPE_RANGE) or beyond
+ *              the table (KVC_DEV_CAPACITY), leaves its part of it and of out
+ *              as they were.  A page id outside the pool sets KVC_DEV_INDEX_OOB
+ *              (that row's output is then undefined, as in kvc_gqa_decode_paged).
+ * sink_pages >= 0, recent_pages >= 1, their sum at most n_select (KVC_ERR_SHAPE);
+ * max_pages <= 49152 (KVC_ERR_CAPACITY); batch * kv_heads <= 65535.
+ * Types and sizes as kvc_gqa_decode_paged; with n_select >= pages its results.
+ * workspace    device, kvc_gqa_decode_sparse_workspace_size(...) bytes, 256-byte
+ *              aligned.  Calls that may overlap on the GPU need their own.
+ */
+kvc_status kvc_gqa_decode_sparse(void *out, const void *q, const void *k_pool, const void *v_pool,
+                                 const void *bounds, const float *bound_scale,
+                                 const int32_t *block_table, int max_pages, int64_t n_pool_pages,
+                                 int page_size, kvc_lengths len, int batch, int q_heads,
+                                 int kv_heads, int head_dim, int dtype, int n_select,
+                                 int sink_pages, int recent_pages, int32_t *selected, float scale,
+                                 const float *rope_cos, const float *rope_sin, int64_t rope_max_pos,
+                                 void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                                 void *stream);
+
+/* Bytes of workspace kvc_gqa_decode_sparse needs for these sizes (0 on bad sizes). */
+size_t kvc_gqa_decode_sparse_workspace_size(int batch, int q_heads, int kv_heads, int page_size,
+                                            int n_select, int head_dim, int dtype);
+
+/*
+ * A tree of drafted tokens over a cache ("Persistent KV Cache and Decode
+ * Performance Roadmap", "Phase 1", "Phase 2").  N nodes follow the P tokens of
+ * each batch row (kvc_seq_lengths with new_tokens = N and KVC_CONTIGUOUS, so
+ * P = T - N).  Node i continues the line of its parent: it stands at position
+ * P + depth_i, its K and V rows lie at row P + i, and it sees every row of the
+ * cache, its ancestors and itself (with a local window W only what is less than
+ * W positions back).  The cache is contiguous, [batch, kv_heads, capacity,
+ * head_dim] with block_table NULL, or paged as above (block_table, max_pages,
+ * n_pool_pages and a page_size that is a multiple of 64; capacity is then
+ * ignored).  KVC_BF16/KVC_F16, head_dim 64, 128 or 256, N <= 256
+ * (KVC_ERR_UNSUPPORTED).
+ *
+ * kvc_tree_mask -- what the other calls read of the tree:
+ *   parents  device int32 [batch, nodes]: the index of an earlier node, -1 (the
+ *            node follows the cache), or -2 (no node: trees of a batch may
+ *            differ in size).  Other values set KVC_DEV_INDEX_OOB and count as -2.
+ *   mask     device uint32 [batch, nodes, ceil(nodes / 32)]: bit j % 32 of word
+ *            j / 32 of node i is set when j is i or an ancestor of i.
+ *   depth    device int32 [batch, nodes]: ancestors of the node, -1 for an
+ *            absent node or one below it (its mask is zero).
+ * mask and depth may also be written by the caller: any set of drafts may be
+ * visible to a node (not only a line), at any depth in [0, nodes); a node whose
+ * depth is outside is absent (KVC_DEV_INDEX_OOB when it is nodes or more), and
+ * no node sees it whatever its mask says.
+ */
+kvc_status kvc_tree_mask(const int32_t *parents, int batch, int nodes, uint32_t *mask,
+                         int32_t *depth, int32_t *dev_status, void *stream);
+
+/*
+ * kvc_tree_append -- rows P + i <- the nodes' K (rotated at P + depth_i) and V;
+ * rows of absent nodes are left as they were.  A batch row with P + nodes past
+ * the capacity (KVC_DEV_CAPACITY) or rope_max_pos (KVC_DEV_ROPE_RANGE), or with a
+ * page id outside the pool among its new rows' (KVC_DEV_INDEX_OOB), writes
+ * nothing.
+ * new_k, new_v  device [batch, kv_heads, nodes, head_dim].
+ */
+kvc_status kvc_tree_append(void *k_cache, void *v_cache, const void *new_k, const void *new_v,
+                           const int32_t *depth, const int32_t *block_table, int max_pages,
+                           int64_t n_pool_pages, int page_size, kvc_lengths len, int batch,
+                           int kv_heads, int nodes, int64_t capacity, int head_dim, int dtype,
+                           const float *rope_cos, const float *rope_sin, int64_t rope_max_pos,
+                           int32_t *dev_status, void *stream);
+
+/*
+ * kvc_gqa_tree -- the attention of the nodes after kvc_tree_append: queries
+ * rotated at P + depth_i; an absent node, or one that sees nothing, gives zeros.
+ * A batch row that kvc_seq_lengths rejected, or that kvc_tree_append would
+ * refuse, keeps its output; a page id outside the pool among the rows read sets
+ * KVC_DEV_INDEX_OOB (that row's output is then undefined).
+ * out, q     device [batch, q_heads, nodes, head_dim]; q_heads / kv_heads <= 16,
+ *            any whole number.
+ * workspace  device, kvc_gqa_tree_workspace_size(...) bytes on the current device,
+ *            256-byte aligned.  Calls that may overlap on the GPU need their own.
+ */
+kvc_status kvc_gqa_tree(void *out, const void *q, const void *k_cache, const void *v_cache,
+                        const uint32_t *mask, const int32_t *depth, const int32_t *block_table,
+                        int max_pages, int64_t n_pool_pages, int page_size, kvc_lengths len,
+                        int batch, int q_heads, int kv_heads, int nodes, int64_t capacity,
+                        int head_dim, int dtype, int local_window_size, float scale,
+                        const float *rope_cos, const float *rope_sin, int64_t rope_max_pos,
+                        void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                        void *stream);
+
+/* Bytes of workspace kvc_gqa_tree needs for these sizes (0 on bad sizes). */
+size_t kvc_gqa_tree_workspace_size(int batch, int q_heads, int kv_heads, int nodes, int head_dim);
+
+/*
+ * kvc_tree_commit -- keep one line of the tree: rows P + path[j] move to P + j for
+ * j < accepted, in place (K was rotated at its depth, so a line from the root on
+ * is then as one-token steps would have left it), and seqlens_k <- P + accepted - 1,
+ * the value from which the next step's starts.  The rows behind are scratch.
+ * path       device int32 [batch, path_len], ascending nodes (path[j] >= j).
+ * accepted   device int32 [batch], 0 <= accepted <= min(path_len, nodes).
+ * seqlens_k  device int32 [batch], written (may be the step's own input).
+ * A batch row whose path or count is not such, or whose pages [P, P + nodes) are
+ * not all in the pool, sets KVC_DEV_INDEX_OOB and is left as it was, seqlens_k
+ * too (KVC_DEV_CAPACITY when P + nodes is past the capacity).
+ */
+kvc_status kvc_tree_commit(void *k_cache, void *v_cache, const int32_t *path,
+                           const int32_t *accepted, int path_len, const int32_t *block_table,
+                           int max_pages, int64_t n_pool_pages, int page_size, kvc_lengths len,
+                           int32_t *seqlens_k, int batch, int kv_heads, int nodes, int64_t capacity,
+                           int head_dim, int dtype, int32_t *dev_status, void *stream);
 
 /* Human-readable name of a status code (static storage). */
 const char *kvc_status_string(kvc_status status);

@@ -16,7 +16,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libkvc.so")
-SOURCES = ["kvc_scatter.cu", "kvc_cache.cu", "kvc_decode.cu", "kvc_prefill.cu", "kvc_quant.cu"]
+SOURCES = ["kvc_scatter.cu", "kvc_cache.cu", "kvc_decode.cu", "kvc_prefill.cu", "kvc_quant.cu",
+           "kvc_sparse.cu", "kvc_tree.cu"]
 HEADERS = [os.path.join(CSRC, "kvc_common.cuh"), os.path.join(CSRC, "kvc_flat.cuh"),
            os.path.join(ROOT, "include", "kvc.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -1,0 +1,567 @@
+// kvc_sparse.cu -- one-token attention over the pages of a paged cache that a
+// cheap score selects ("Persistent KV Cache and Decode Performance Roadmap",
+// "Phase 2": fixed-size pages read through a page table).
+//
+// Every full page keeps, per kv head, 8-bit bounds of its keys: with
+// s = max|k| / 127 over the page, hi_d = ceil(max_r k_rd / s) and
+// lo_d = floor(min_r k_rd / s).  For a query q no key of the page can exceed
+//     q . k <= s * sum_d max(q_d hi_d, q_d lo_d)
+//            = s * (sum_d max(q_d, 0) hi_d + sum_d min(q_d, 0) lo_d).
+// Summed over the heads of a group this needs only the group's sums of the
+// positive and of the negative parts of the query, rounded to 8 bits: one
+// integer dot product of 2 D codes a page, exact, so that which pages are
+// taken does not depend on the order of any sum.
+//
+//   page_bounds_kernel   the bounds of the pages that a step filled
+//   page_select_kernel   scores, the choice of n pages, and the page table and
+//                        lengths under which the paged decode reads them
+#include <algorithm>
+#include <type_traits>
+
+#include "kvc_common.cuh"
+
+namespace {
+
+// --------------------------------------------------------------------------
+// bounds
+// --------------------------------------------------------------------------
+
+struct BoundsArgs {
+    int8_t *bounds;   // [n_pool, kv_heads, 2, D]
+    float *scale;     // [n_pool, kv_heads]
+    const void *k_pool;
+    const int32_t *table;
+    int max_pages, page_size;
+    int64_t n_pool;
+    kvc_lengths len;
+    int kv_heads, D;
+    int32_t *status;
+};
+
+// x / s rounded up (or down) to a code
+__device__ __forceinline__ int bound_code(float x, float s, bool up)
+{
+    const float y = __fdiv_rn(x, s);
+    return max(-127, min(127, up ? __float2int_ru(y) : __float2int_rd(y)));
+}
+
+// One block per (page of the step, kv head, batch row): 8 columns a thread,
+// the rows dealt over 256 / (D / 8) groups of threads, then joined.
+template <typename T, int D>
+__global__ void __launch_bounds__(256)
+page_bounds_kernel(const BoundsArgs a)
+{
+    constexpr int CT = D / 8, GROUPS = 256 / CT;
+    __shared__ float hi_sh[GROUPS][D], lo_sh[GROUPS][D];
+    __shared__ uint32_t top_sh[8];
+    const int b = blockIdx.z, h = blockIdx.y;
+    const int P = a.len.past_abs[b], total = a.len.total_abs[b];
+    if (a.len.cache_total[b] < 0)
+        return;
+    if (total > (int64_t)a.max_pages * a.page_size || P < 0 || P > total) {
+        if (threadIdx.x == 0 && blockIdx.x == 0 && h == 0)
+            kvc::raise_status(a.status, KVC_DEV_CAPACITY);
+        return;
+    }
+    // pages [P / page, T / page) became full with this step
+    for (int64_t j = P / a.page_size + blockIdx.x; j < total / a.page_size; j += gridDim.x) {
+        const int64_t id = a.table[(int64_t)b * a.max_pages + j];
+        if (id < 0 || id >= a.n_pool) {
+            if (threadIdx.x == 0 && h == 0)
+                kvc::raise_status(a.status, KVC_DEV_INDEX_OOB);
+            continue;
+        }
+        const int64_t slice = id * a.kv_heads + h;
+        const T *k = static_cast<const T *>(a.k_pool) + slice * a.page_size * D;
+        const int col = threadIdx.x % CT * 8, grp = threadIdx.x / CT;
+        float hi[8], lo[8];
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            hi[e] = -INFINITY;
+            lo[e] = INFINITY;
+        }
+        for (int r = grp; r < a.page_size; r += GROUPS) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(k + (int64_t)r * D + col));
+            const T *x = reinterpret_cast<const T *>(&v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float f = kvc::Elem<T>::to_f32(x[e]);
+                hi[e] = fmaxf(hi[e], f);
+                lo[e] = fminf(lo[e], f);
+                top = max(top, __float_as_uint(f) & 0x7fffffffu);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            hi_sh[grp][col + e] = hi[e];
+            lo_sh[grp][col + e] = lo[e];
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1)
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+        if ((threadIdx.x & 31) == 0)
+            top_sh[threadIdx.x >> 5] = top;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < 8; ++w)
+            top = max(top, top_sh[w]);
+        // a page with a NaN or an infinity: scale infinity, the page is taken first
+        const bool finite = top < 0x7f800000u;
+        const float s = finite ? __fdiv_rn(__uint_as_float(top), 127.f) : INFINITY;
+        if (threadIdx.x < D) {
+            const int d = threadIdx.x;
+            float mx = -INFINITY, mn = INFINITY;
+#pragma unroll
+            for (int w = 0; w < GROUPS; ++w) {
+                mx = fmaxf(mx, hi_sh[w][d]);
+                mn = fminf(mn, lo_sh[w][d]);
+            }
+            const bool any = finite && s > 0.f;
+            a.bounds[slice * 2 * D + d] = (int8_t)(any ? bound_code(mx, s, true) : 0);
+            a.bounds[slice * 2 * D + D + d] = (int8_t)(any ? bound_code(mn, s, false) : 0);
+        }
+        if (threadIdx.x == 0)
+            a.scale[slice] = s;
+        __syncthreads();
+    }
+}
+
+// --------------------------------------------------------------------------
+// selection
+// --------------------------------------------------------------------------
+
+constexpr int kSelThreads = 512;
+constexpr int kMaxPages = 49152;   // pages a sequence may have: their scores stay in shared memory
+
+struct SelectArgs {
+    const void *q;
+    const int8_t *bounds;
+    const float *scale;
+    const int32_t *table;
+    int max_pages, page_size;
+    int64_t n_pool;
+    kvc_lengths len;
+    int batch, kv_heads, group, n_select, sink, recent;
+    const float *cos_t, *sin_t;
+    int64_t rope_max_pos;
+    int32_t *selected;     // [B, kv_heads, n_select] logical pages
+    int32_t *sub_table;    // the same as pages of the pool seen one head at a time
+    kvc_lengths sub_len;   // lengths of the B * kv_heads one-head rows
+    int32_t *status;
+};
+
+// scores as unsigned keys that order as the scores do; a NaN score orders
+// above all (its page holds what the attention has to see)
+__device__ __forceinline__ uint32_t order_key(float f)
+{
+    if (f != f)
+        return 0xffffffffu;
+    const uint32_t u = __float_as_uint(f + 0.f);  // -0 as 0
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// the block's sum of v, and in `before` that of the threads before this one
+__device__ __forceinline__ int block_scan(int v, int *warp_sum, int &before)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int inc = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d)
+            inc += u;
+    }
+    __syncthreads();
+    if (lane == 31)
+        warp_sum[warp] = inc;
+    __syncthreads();
+    int total = 0, base = 0;
+#pragma unroll
+    for (int w = 0; w < kSelThreads / 32; ++w) {
+        base += w < warp ? warp_sum[w] : 0;
+        total += warp_sum[w];
+    }
+    before = base + inc - v;
+    return total;
+}
+
+// One block per (batch row, kv head).
+template <typename T, int D>
+__global__ void __launch_bounds__(kSelThreads)
+page_select_kernel(const SelectArgs a)
+{
+    extern __shared__ uint32_t keys[];            // the middle pages' scores, as order_key
+    __shared__ float part[2][D];                  // sums of the positive and negative parts
+    __shared__ __align__(16) int8_t code[2 * D];  // their codes
+    __shared__ int warp_sum[kSelThreads / 32];
+    __shared__ uint32_t hist[256];
+    __shared__ uint32_t pick[2];
+    __shared__ float top_sh[kSelThreads / 32];
+    const int h = blockIdx.x, b = blockIdx.y, row = b * a.kv_heads + h;
+    const int total = a.len.total_abs[b];
+    int L = a.len.cache_total[b];
+    const bool lead = threadIdx.x == 0 && h == 0;
+    if (L >= 0 && (total < 1 || total > (int64_t)a.max_pages * a.page_size)) {
+        if (lead)
+            kvc::raise_status(a.status, KVC_DEV_CAPACITY);
+        L = -1;
+    }
+    if (L >= 0 && a.cos_t && (int64_t)total > a.rope_max_pos) {
+        if (lead)
+            kvc::raise_status(a.status, KVC_DEV_ROPE_RANGE);
+        L = -1;
+    }
+    int32_t *sel = a.selected + (int64_t)row * a.n_select, *sub = a.sub_table + (int64_t)row * a.n_select;
+    if (L < 0) {
+        if (threadIdx.x == 0) {
+            a.sub_len.past_abs[row] = a.sub_len.total_abs[row] = a.sub_len.cache_past[row] =
+                a.sub_len.cache_total[row] = a.sub_len.evict[row] = -1;
+        }
+        return;
+    }
+    const int pages = (total + a.page_size - 1) / a.page_size;
+    const int take = min(pages, a.n_select);
+    // pages [0, sink) and [tail, pages) are always taken
+    const int tail = max(0, pages - a.recent), sink = min(a.sink, tail);
+    const int rest = take - sink - (pages - tail);  // to choose out of [sink, tail)
+    const int middle = tail - sink;
+    uint32_t least = 0;   // a page with a key above it is taken,
+    int ties = 0;         // and the first `ties` pages with that key
+    if (rest > 0 && rest < middle) {
+        // ---- the group's query, in 8 bits ----
+        if (threadIdx.x < D / 2) {
+            const int p = threadIdx.x;
+            const int64_t pos = (int64_t)total - 1;
+            const T *q = static_cast<const T *>(a.q) + (int64_t)row * a.group * D;
+            // in 64 bits, so that a sum does not hang on the order of the heads
+            double up[2] = {0., 0.}, down[2] = {0., 0.};
+            for (int r = 0; r < a.group; ++r) {
+                float x[2] = {kvc::Elem<T>::to_f32(q[r * D + p]), kvc::Elem<T>::to_f32(q[r * D + D / 2 + p])};
+                if (a.cos_t)
+                    kvc::rope_pair(x[0], x[1], a.cos_t[pos * (D / 2) + p], a.sin_t[pos * (D / 2) + p]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    up[e] += x[e] > 0.f ? x[e] : 0.f;
+                    down[e] += x[e] < 0.f ? x[e] : 0.f;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                part[0][p + e * (D / 2)] = (float)up[e];
+                part[1][p + e * (D / 2)] = (float)down[e];
+            }
+        }
+        __syncthreads();
+        float top = 0.f;
+        for (int i = threadIdx.x; i < 2 * D; i += kSelThreads)
+            top = fmaxf(top, fabsf(part[i / D][i % D]));
+#pragma unroll
+        for (int d = 16; d; d >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        if ((threadIdx.x & 31) == 0)
+            top_sh[threadIdx.x >> 5] = top;
+        __syncthreads();
+        for (int w = 0; w < kSelThreads / 32; ++w)
+            top = fmaxf(top, top_sh[w]);
+        const float sq = __fdiv_rn(top, 127.f);
+        for (int i = threadIdx.x; i < 2 * D; i += kSelThreads) {
+            const float x = part[i / D][i % D];
+            code[i] = (int8_t)(sq > 0.f ? max(-127, min(127, __float2int_rn(__fdiv_rn(x, sq)))) : 0);
+        }
+        __syncthreads();
+
+        // ---- scores: 16 codes a lane, D / 8 lanes a page ----
+        constexpr int LPP = D / 8;
+        const int sub_lane = threadIdx.x % LPP;
+        const uint4 qc = reinterpret_cast<const uint4 *>(code)[sub_lane];
+        constexpr int PPB = kSelThreads / LPP;
+        for (int j0 = 0; j0 < middle; j0 += PPB) {
+            const int j = j0 + threadIdx.x / LPP;
+            int sum = 0;
+            float s = 0.f;
+            bool bad = false;
+            if (j < middle) {
+                const int64_t id = a.table[(int64_t)b * a.max_pages + sink + j];
+                bad = id < 0 || id >= a.n_pool;
+                if (!bad) {
+                    const int64_t slice = id * a.kv_heads + h;
+                    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(a.bounds + slice * 2 * D) + sub_lane);
+                    sum = __dp4a((int)v.x, (int)qc.x, 0);
+                    sum = __dp4a((int)v.y, (int)qc.y, sum);
+                    sum = __dp4a((int)v.z, (int)qc.z, sum);
+                    sum = __dp4a((int)v.w, (int)qc.w, sum);
+                    s = __ldg(a.scale + slice);
+                }
+            }
+#pragma unroll
+            for (int d = 1; d < LPP; d <<= 1)
+                sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            if (j < middle && sub_lane == 0) {
+                if (bad)
+                    kvc::raise_status(a.status, KVC_DEV_INDEX_OOB);
+                // a page that does not exist orders first too: the attention reports it
+                keys[j] = bad || isinf(s) ? 0xffffffffu : order_key(__fmul_rn(s, (float)sum));
+            }
+        }
+        __syncthreads();
+
+        // ---- the rest-th largest key, 8 bits at a time ----
+        uint32_t prefix = 0, mask = 0;
+        int want = rest;
+        for (int shift = 24; shift >= 0; shift -= 8) {
+            if (threadIdx.x < 256)
+                hist[threadIdx.x] = 0;
+            __syncthreads();
+            for (int j = threadIdx.x; j < middle; j += kSelThreads)
+                if ((keys[j] & mask) == prefix)
+                    atomicAdd(&hist[keys[j] >> shift & 255u], 1u);
+            __syncthreads();
+            // bins from the top: thread i looks at bin 255 - i
+            const int n = threadIdx.x < 256 ? (int)hist[255 - threadIdx.x] : 0;
+            int before;
+            block_scan(n, warp_sum, before);
+            if (threadIdx.x < 256 && before < want && before + n >= want) {
+                pick[0] = 255 - threadIdx.x;
+                pick[1] = want - before;
+            }
+            __syncthreads();
+            prefix |= pick[0] << shift;
+            mask |= 255u << shift;
+            want = (int)pick[1];
+            __syncthreads();
+        }
+        least = prefix;
+        ties = want;
+    }
+
+    // ---- the chosen pages in ascending order ----
+    // (rest == middle: all of them; rest <= 0: none of the middle)
+    int out = 0, tied = 0;
+    for (int j0 = 0; j0 < pages; j0 += kSelThreads) {
+        const int j = j0 + threadIdx.x;
+        bool chosen = false, tie = false;
+        if (j < pages) {
+            if (j < sink || j >= tail)
+                chosen = true;
+            else if (rest >= middle)
+                chosen = true;
+            else if (rest > 0) {
+                chosen = keys[j - sink] > least;
+                tie = keys[j - sink] == least;
+            }
+        }
+        int before;
+        const int n_tie = block_scan(tie, warp_sum, before);
+        if (tie && tied + before < ties)
+            chosen = true;
+        tied += n_tie;
+        const int n = block_scan(chosen, warp_sum, before);
+        if (chosen && out + before < a.n_select) {
+            const int64_t id = a.table[(int64_t)b * a.max_pages + j];
+            sel[out + before] = j;
+            // an id outside the pool stays outside the one-head pool
+            sub[out + before] = id < 0 || id >= a.n_pool ? -1 : (int32_t)(id * a.kv_heads + h);
+        }
+        out += n;
+    }
+    for (int i = take + threadIdx.x; i < a.n_select; i += kSelThreads) {
+        sel[i] = -1;
+        sub[i] = -1;
+    }
+    if (threadIdx.x == 0) {
+        // the page of the newest token is the last one taken
+        const int rows = (take - 1) * a.page_size + total - (pages - 1) * a.page_size;
+        a.sub_len.past_abs[row] = total - 1;
+        a.sub_len.total_abs[row] = total;
+        a.sub_len.cache_past[row] = rows - 1;
+        a.sub_len.cache_total[row] = rows;
+        a.sub_len.evict[row] = 0;
+    }
+}
+
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// the parts of the workspace: the sub-table, the sub-lengths, the decode's
+// own scratch
+struct SparseLayout {
+    size_t lens, decode, total;
+};
+SparseLayout sparse_layout(int batch, int q_heads, int kv_heads, int page_size, int n_select, int D, int dtype)
+{
+    SparseLayout l;
+    const size_t rows = (size_t)batch * kv_heads;
+    l.lens = align256(rows * n_select * 4);
+    l.decode = l.lens + align256(5 * rows * 4);
+    l.total = l.decode + kvc_gqa_decode_workspace_size((int)rows, q_heads / kv_heads, 1, (int64_t)n_select * page_size,
+                                                       D, dtype);
+    return l;
+}
+
+bool sizes_ok(int batch, int q_heads, int kv_heads, int page_size, int n_select, int D)
+{
+    return batch >= 0 && q_heads >= 1 && kv_heads >= 1 && q_heads % kv_heads == 0 && n_select >= 1 &&
+           page_size >= 64 && page_size % 64 == 0 && D >= 1;
+}
+
+template <typename T, int D> kvc_status launch_select_dim(const SelectArgs &a, cudaStream_t stream)
+{
+    const int smem = a.max_pages * 4;
+    if (smem > 32 * 1024 && cudaFuncSetAttribute(page_select_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 smem) != cudaSuccess)
+        return KVC_ERR_CUDA;
+    page_select_kernel<T, D><<<dim3(a.kv_heads, a.batch), kSelThreads, smem, stream>>>(a);
+    return kvc_host::launch_status();
+}
+
+template <typename T> kvc_status launch_select(const SelectArgs &a, int D, cudaStream_t stream)
+{
+    switch (D) {
+    case 64:
+        return launch_select_dim<T, 64>(a, stream);
+    case 128:
+        return launch_select_dim<T, 128>(a, stream);
+    default:
+        return launch_select_dim<T, 256>(a, stream);
+    }
+}
+
+template <typename T> kvc_status launch_bounds(const BoundsArgs &a, int batch, int S, cudaStream_t stream)
+{
+    // at most ceil(S / page) pages of a batch row become full, one block each up to 8 blocks an SM
+    const int64_t most = ((int64_t)S + a.page_size - 1) / a.page_size;
+    const int64_t cap = std::max<int64_t>(1, (int64_t)kvc_host::sm_count() * 8 / ((int64_t)batch * a.kv_heads) + 1);
+    const dim3 grid((unsigned)std::min(most, cap), a.kv_heads, batch);
+    switch (a.D) {
+    case 64:
+        page_bounds_kernel<T, 64><<<grid, 256, 0, stream>>>(a);
+        break;
+    case 128:
+        page_bounds_kernel<T, 128><<<grid, 256, 0, stream>>>(a);
+        break;
+    default:
+        page_bounds_kernel<T, 256><<<grid, 256, 0, stream>>>(a);
+    }
+    return kvc_host::launch_status();
+}
+
+} // namespace
+
+KVC_API kvc_status kvc_page_bounds(void *bounds, float *bound_scale, const void *k_pool, const int32_t *block_table,
+                                   int max_pages, int64_t n_pool_pages, int page_size, kvc_lengths len, int batch,
+                                   int kv_heads, int new_tokens, int head_dim, int dtype, int32_t *dev_status,
+                                   void *stream_)
+{
+    if (kvc_host::elem_bytes_of(dtype) == 0)
+        return KVC_ERR_DTYPE;
+    if (dtype == KVC_F32 || (head_dim != 64 && head_dim != 128 && head_dim != 256))
+        return KVC_ERR_UNSUPPORTED;
+    if (batch < 0 || batch > 65535 || kv_heads < 1 || kv_heads > 65535 || new_tokens < 1 || max_pages < 1 ||
+        n_pool_pages < 1 || page_size < 1)
+        return KVC_ERR_SHAPE;
+    if ((int64_t)max_pages * page_size > (int64_t)INT32_MAX)
+        return KVC_ERR_CAPACITY;
+    if (batch == 0)
+        return KVC_OK;
+    if (!bounds || !bound_scale || !k_pool || !block_table || !kvc_host::lengths_ok(len))
+        return KVC_ERR_NULL;
+    for (const void *p : {(const void *)bounds, (const void *)bound_scale, k_pool})
+        if (!kvc_host::aligned16(p))
+            return KVC_ERR_ALIGN;
+    const size_t slices = (size_t)n_pool_pages * kv_heads;
+    if (kvc_host::overlaps(bounds, slices * 2 * head_dim, bound_scale, slices * 4) ||
+        kvc_host::overlaps(bounds, slices * 2 * head_dim, k_pool, slices * page_size * head_dim * 2) ||
+        kvc_host::overlaps(bound_scale, slices * 4, k_pool, slices * page_size * head_dim * 2))
+        return KVC_ERR_SHAPE;
+    BoundsArgs a{static_cast<int8_t *>(bounds), bound_scale, k_pool, block_table, max_pages, page_size, n_pool_pages,
+                 len, kv_heads, head_dim, dev_status};
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    return dtype == KVC_BF16 ? launch_bounds<__nv_bfloat16>(a, batch, new_tokens, stream)
+                             : launch_bounds<__half>(a, batch, new_tokens, stream);
+}
+
+KVC_API size_t kvc_gqa_decode_sparse_workspace_size(int batch, int q_heads, int kv_heads, int page_size,
+                                                    int n_select, int head_dim, int dtype)
+{
+    if (!sizes_ok(batch, q_heads, kv_heads, page_size, n_select, head_dim) || batch < 1 ||
+        (int64_t)n_select * page_size > (int64_t)INT32_MAX || (int64_t)batch * kv_heads > 65535)
+        return 0;
+    return sparse_layout(batch, q_heads, kv_heads, page_size, n_select, head_dim, dtype).total;
+}
+
+KVC_API kvc_status kvc_gqa_decode_sparse(void *out, const void *q, const void *k_pool, const void *v_pool,
+                                         const void *bounds, const float *bound_scale, const int32_t *block_table,
+                                         int max_pages, int64_t n_pool_pages, int page_size, kvc_lengths len, int batch,
+                                         int q_heads, int kv_heads, int head_dim, int dtype, int n_select,
+                                         int sink_pages, int recent_pages, int32_t *selected, float scale,
+                                         const float *rope_cos, const float *rope_sin, int64_t rope_max_pos,
+                                         void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream_)
+{
+    if (kvc_host::elem_bytes_of(dtype) == 0)
+        return KVC_ERR_DTYPE;
+    if (dtype == KVC_F32)
+        return KVC_ERR_UNSUPPORTED;
+    if (!sizes_ok(batch, q_heads, kv_heads, page_size, n_select, head_dim) || max_pages < 1 || n_pool_pages < 1 ||
+        sink_pages < 0 || recent_pages < 1 || (int64_t)sink_pages + recent_pages > n_select)
+        return KVC_ERR_SHAPE;
+    if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || q_heads / kv_heads > 16)
+        return KVC_ERR_UNSUPPORTED;
+    if ((int64_t)batch * kv_heads > 65535)
+        return KVC_ERR_SHAPE;
+    if (max_pages > kMaxPages || (int64_t)max_pages * page_size > (int64_t)INT32_MAX || (int64_t)n_select * page_size > (int64_t)INT32_MAX ||
+        n_pool_pages * kv_heads * (int64_t)page_size > (int64_t)INT32_MAX)
+        return KVC_ERR_CAPACITY;
+    if ((rope_cos == nullptr) != (rope_sin == nullptr))
+        return KVC_ERR_NULL;
+    if (rope_cos && rope_max_pos < 1)
+        return KVC_ERR_SHAPE;
+    if (batch == 0)
+        return KVC_OK;
+    if (!out || !q || !k_pool || !v_pool || !bounds || !bound_scale || !block_table || !selected ||
+        !kvc_host::lengths_ok(len))
+        return KVC_ERR_NULL;
+    for (const void *p : {(const void *)out, q, k_pool, v_pool, bounds, (const void *)bound_scale})
+        if (!kvc_host::aligned16(p))
+            return KVC_ERR_ALIGN;
+    const SparseLayout l = sparse_layout(batch, q_heads, kv_heads, page_size, n_select, head_dim, dtype);
+    if (!workspace || workspace_bytes < l.total)
+        return KVC_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+        return KVC_ERR_ALIGN;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const int rows = batch * kv_heads;
+    int32_t *lens = reinterpret_cast<int32_t *>(ws + l.lens);
+    SelectArgs a{};
+    a.q = q;
+    a.bounds = static_cast<const int8_t *>(bounds);
+    a.scale = bound_scale;
+    a.table = block_table;
+    a.max_pages = max_pages;
+    a.page_size = page_size;
+    a.n_pool = n_pool_pages;
+    a.len = len;
+    a.batch = batch;
+    a.kv_heads = kv_heads;
+    a.group = q_heads / kv_heads;
+    a.n_select = n_select;
+    a.sink = sink_pages;
+    a.recent = recent_pages;
+    a.cos_t = rope_cos;
+    a.sin_t = rope_sin;
+    a.rope_max_pos = rope_max_pos;
+    a.selected = selected;
+    a.sub_table = reinterpret_cast<int32_t *>(ws);
+    a.sub_len = kvc_lengths{lens, lens + rows, lens + 2 * rows, lens + 3 * rows, lens + 4 * rows};
+    a.status = dev_status;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    const kvc_status st =
+        dtype == KVC_BF16 ? launch_select<__nv_bfloat16>(a, head_dim, stream) : launch_select<__half>(a, head_dim, stream);
+    if (st != KVC_OK)
+        return st;
+    // Page id of head h is page id * kv_heads + h of the same pool seen as
+    // one-head pages, and (b, h) a batch row of `group` query heads: the paged
+    // decode reads the chosen pages of every head as they lie.
+    return kvc_gqa_decode_paged(out, q, k_pool, v_pool, a.sub_table, n_select, n_pool_pages * kv_heads, page_size,
+                                a.sub_len, rows, a.group, 1, head_dim, dtype, 0, scale, rope_cos, rope_sin,
+                                rope_max_pos, ws + l.decode, workspace_bytes - l.decode, dev_status, stream_);
+}

@@ -41,7 +41,9 @@ EXPORTS = ("kvc_tensor_scatter", "kvc_seq_lengths", "kvc_window_append", "kvc_gq
            "kvc_quantize_pages", "kvc_gqa_decode_paged_q",
            "kvc_gqa_prefill_chunk", "kvc_gqa_prefill_workspace_size", "kvc_window_prefill_step",
            "kvc_quant_append", "kvc_dequant_rows", "kvc_gqa_decode_quant",
-           "kvc_gqa_decode_quant_workspace_size",
+           "kvc_gqa_decode_quant_workspace_size", "kvc_page_bounds", "kvc_gqa_decode_sparse",
+           "kvc_gqa_decode_sparse_workspace_size", "kvc_tree_mask", "kvc_tree_append",
+           "kvc_gqa_tree", "kvc_gqa_tree_workspace_size", "kvc_tree_commit",
            "kvc_status_string", "kvc_abi_version")
 KVC_DECODE_STATIC_SCRATCH_BYTES = 16 << 20
 KVC_PAGE_QUANT = 0x40000000  # block-table flag: the entry names an int8 page
@@ -129,6 +131,16 @@ def library() -> ctypes.CDLL:
             "kvc_gqa_decode_quant": [P, P, P, P, P, P, L, I, I, I, I64, I, I, I, I, I, F, P, P, I64,
                                      P, SZ, P, P],
             "kvc_gqa_decode_quant_workspace_size": [I, I, I, I64, I],
+            "kvc_page_bounds": [P, P, P, P, I, I64, I, L, I, I, I, I, I, P, P],
+            "kvc_gqa_decode_sparse": [P, P, P, P, P, P, P, I, I64, I, L, I, I, I, I, I, I, I, I, P, F,
+                                      P, P, I64, P, SZ, P, P],
+            "kvc_gqa_decode_sparse_workspace_size": [I, I, I, I, I, I, I],
+            "kvc_tree_mask": [P, I, I, P, P, P, P],
+            "kvc_tree_append": [P, P, P, P, P, P, I, I64, I, L, I, I, I, I64, I, I, P, P, I64, P, P],
+            "kvc_gqa_tree": [P, P, P, P, P, P, P, I, I64, I, L, I, I, I, I, I64, I, I, I, F, P, P, I64,
+                             P, SZ, P, P],
+            "kvc_gqa_tree_workspace_size": [I, I, I, I, I],
+            "kvc_tree_commit": [P, P, P, P, I, P, I, I64, I, L, P, I, I, I, I64, I, I, P, P],
             "kvc_status_string": [I],
             "kvc_abi_version": [],
         }
@@ -141,6 +153,8 @@ def library() -> ctypes.CDLL:
         lib.kvc_window_decode_step_workspace_size.restype = SZ
         lib.kvc_gqa_prefill_workspace_size.restype = SZ
         lib.kvc_gqa_decode_quant_workspace_size.restype = SZ
+        lib.kvc_gqa_decode_sparse_workspace_size.restype = SZ
+        lib.kvc_gqa_tree_workspace_size.restype = SZ
         lib.kvc_status_string.restype = ctypes.c_char_p
         _lib = lib
     return _lib
@@ -531,3 +545,142 @@ def kvc_gqa_decode_quant(out, q, kq, vq, k_scale, v_scale, lengths, windowed, lo
         _ptr(workspace), 0 if workspace is None else workspace.numel(), _ptr(status),
         _stream(stream)))
     return out
+
+
+def kvc_page_bounds(bounds, bound_scale, k_pool, block_table, lengths, new_tokens, status=None,
+                    stream=None):
+    """Bounds of the pages that a step of new_tokens filled (include/kvc.h): bounds int8
+    [pages, Hkv, 2, D], bound_scale float32 [pages, Hkv], k_pool [pages, Hkv, page_size, D]."""
+    n_pages, Hkv, ps, D = k_pool.shape
+    B, max_pages = block_table.shape
+    _same("bounds", bounds, (n_pages, Hkv, 2, D), torch.int8)
+    _same("bound_scale", bound_scale, (n_pages, Hkv), torch.float32)
+    _same("block_table", block_table, (B, max_pages), torch.int32)
+    _check("kvc_page_bounds", library().kvc_page_bounds(
+        _ptr(bounds), _ptr(bound_scale), _ptr(k_pool), _ptr(block_table), max_pages, n_pages, ps,
+        lengths.c(), B, Hkv, new_tokens, D, _dtype_code(k_pool), _ptr(status), _stream(stream)))
+
+
+def sparse_workspace(q, k_pool, selected):
+    """Workspace for kvc_gqa_decode_sparse."""
+    B, Hq, _, D = q.shape
+    n = library().kvc_gqa_decode_sparse_workspace_size(B, Hq, k_pool.shape[1], k_pool.shape[2],
+                                                       selected.shape[2], D, _dtype_code(q))
+    return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
+def kvc_gqa_decode_sparse(out, q, k_pool, v_pool, bounds, bound_scale, block_table, lengths,
+                          selected, sink_pages=1, recent_pages=1, scale=0.0, rope=None,
+                          workspace="auto", status=None, stream=None):
+    """One-token attention over the pages that their bounds select (include/kvc.h); the pages
+    taken go to selected, int32 [B, Hkv, n]."""
+    n_pages, Hkv, ps, D = k_pool.shape
+    B, Hq = q.shape[:2]
+    _same("q", q, (B, Hq, 1, D), k_pool.dtype)
+    _same("out", out, q.shape, q.dtype)
+    _same("v_pool", v_pool, k_pool.shape, k_pool.dtype)
+    _same("bounds", bounds, (n_pages, Hkv, 2, D), torch.int8)
+    _same("bound_scale", bound_scale, (n_pages, Hkv), torch.float32)
+    _same("block_table", block_table, (B, block_table.shape[-1]), torch.int32)
+    _same("selected", selected, (B, Hkv, selected.shape[-1]), torch.int32)
+    if isinstance(workspace, str):
+        workspace = sparse_workspace(q, k_pool, selected)
+    cs, sn, rmax = _rope(rope)
+    _check("kvc_gqa_decode_sparse", library().kvc_gqa_decode_sparse(
+        _ptr(out), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(bounds), _ptr(bound_scale),
+        _ptr(block_table), block_table.shape[1], n_pages, ps, lengths.c(), B, Hq, Hkv, D,
+        _dtype_code(q), selected.shape[2], sink_pages, recent_pages, _ptr(selected), scale, cs, sn,
+        rmax, _ptr(workspace), 0 if workspace is None else workspace.numel(), _ptr(status),
+        _stream(stream)))
+    return out
+
+
+def tree_buffers(parents):
+    """(mask, depth) for kvc_tree_mask: int32 [B, N, ceil(N / 32)] (the bit words) and [B, N]."""
+    B, N = parents.shape
+    return (torch.empty((B, N, (N + 31) // 32), dtype=torch.int32, device=parents.device),
+            torch.empty((B, N), dtype=torch.int32, device=parents.device))
+
+
+def kvc_tree_mask(parents, mask=None, depth=None, status=None, stream=None):
+    """Ancestor bits and depths of the drafted trees parents, int32 [B, N] (include/kvc.h)."""
+    B, N = parents.shape
+    if mask is None:
+        mask, depth = tree_buffers(parents)
+    _same("parents", parents, (B, N), torch.int32)
+    _same("mask", mask, (B, N, (N + 31) // 32), torch.int32)
+    _same("depth", depth, (B, N), torch.int32)
+    _check("kvc_tree_mask", library().kvc_tree_mask(
+        _ptr(parents), B, N, _ptr(mask), _ptr(depth), _ptr(status), _stream(stream)))
+    return mask, depth
+
+
+def _cache_rows(k_cache, v_cache, block_table, B):
+    """(table pointer, max_pages, pool pages, page_size, kv heads, capacity, D) of a contiguous
+    cache [B, Hkv, C, D] (no block table) or of page pools [pages, Hkv, page_size, D]."""
+    _same("v_cache", v_cache, k_cache.shape, k_cache.dtype)
+    n, Hkv, rows, D = k_cache.shape
+    if block_table is None:
+        _same("k_cache", k_cache, (B, Hkv, rows, D))
+        return None, 0, 0, 0, Hkv, rows, D
+    _same("block_table", block_table, (B, block_table.shape[-1]), torch.int32)
+    return _ptr(block_table), block_table.shape[1], n, rows, Hkv, 0, D
+
+
+def kvc_tree_append(k_cache, v_cache, new_k, new_v, depth, lengths, block_table=None, rope=None,
+                    status=None, stream=None):
+    """The drafted nodes' rows [B, Hkv, N, D] behind the cache, K rotated at P + depth
+    (include/kvc.h)."""
+    B, _, N, _ = new_k.shape
+    table, m, n, ps, Hkv, C, D = _cache_rows(k_cache, v_cache, block_table, B)
+    _same("new_k", new_k, (B, Hkv, N, D), k_cache.dtype)
+    _same("new_v", new_v, (B, Hkv, N, D), k_cache.dtype)
+    _same("depth", depth, (B, N), torch.int32)
+    cs, sn, rmax = _rope(rope)
+    _check("kvc_tree_append", library().kvc_tree_append(
+        _ptr(k_cache), _ptr(v_cache), _ptr(new_k), _ptr(new_v), _ptr(depth), table, m, n, ps,
+        lengths.c(), B, Hkv, N, C, D, _dtype_code(k_cache), cs, sn, rmax, _ptr(status),
+        _stream(stream)))
+
+
+def tree_workspace(q, k_cache):
+    """Workspace for kvc_gqa_tree."""
+    B, Hq, N, D = q.shape
+    n = library().kvc_gqa_tree_workspace_size(B, Hq, k_cache.shape[1], N, D)
+    return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
+def kvc_gqa_tree(out, q, k_cache, v_cache, mask, depth, lengths, block_table=None,
+                 local_window_size=0, scale=0.0, rope=None, workspace="auto", status=None,
+                 stream=None):
+    """Attention of the drafted nodes' queries [B, Hq, N, D] (include/kvc.h)."""
+    B, Hq, N, _ = q.shape
+    table, m, n, ps, Hkv, C, D = _cache_rows(k_cache, v_cache, block_table, B)
+    _same("q", q, (B, Hq, N, D), k_cache.dtype)
+    _same("out", out, q.shape, q.dtype)
+    _same("mask", mask, (B, N, (N + 31) // 32), torch.int32)
+    _same("depth", depth, (B, N), torch.int32)
+    if isinstance(workspace, str):
+        workspace = tree_workspace(q, k_cache)
+    cs, sn, rmax = _rope(rope)
+    _check("kvc_gqa_tree", library().kvc_gqa_tree(
+        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(mask), _ptr(depth), table, m, n, ps,
+        lengths.c(), B, Hq, Hkv, N, C, D, _dtype_code(q), local_window_size, scale, cs, sn, rmax,
+        _ptr(workspace), 0 if workspace is None else workspace.numel(), _ptr(status),
+        _stream(stream)))
+    return out
+
+
+def kvc_tree_commit(k_cache, v_cache, path, accepted, lengths, seqlens_k, nodes, block_table=None,
+                    status=None, stream=None):
+    """Keep the nodes path[b, :accepted[b]] of each tree (include/kvc.h): their rows follow the
+    cache, seqlens_k holds the total so far minus one."""
+    B, path_len = path.shape
+    table, m, n, ps, Hkv, C, D = _cache_rows(k_cache, v_cache, block_table, B)
+    _same("path", path, (B, path_len), torch.int32)
+    _same("accepted", accepted, (B,), torch.int32)
+    _same("seqlens_k", seqlens_k, (B,), torch.int32)
+    _check("kvc_tree_commit", library().kvc_tree_commit(
+        _ptr(k_cache), _ptr(v_cache), _ptr(path), _ptr(accepted), path_len, table, m, n, ps,
+        lengths.c(), _ptr(seqlens_k), B, Hkv, nodes, C, D, _dtype_code(k_cache), _ptr(status),
+        _stream(stream)))
