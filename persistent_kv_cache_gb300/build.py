@@ -18,7 +18,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libkvc.so")
 SOURCES = ["kvc_scatter.cu", "kvc_cache.cu", "kvc_decode.cu", "kvc_prefill.cu", "kvc_quant.cu",
            "kvc_sparse.cu", "kvc_tree.cu"]
-HEADERS = [os.path.join(CSRC, "kvc_common.cuh"), os.path.join(CSRC, "kvc_flat.cuh"),
+HEADERS = [os.path.join(CSRC, h) for h in ("kvc_common.cuh", "kvc_flat.cuh", "kvc_tc.cuh")] + [
            os.path.join(ROOT, "include", "kvc.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",

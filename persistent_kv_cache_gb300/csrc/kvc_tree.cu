@@ -16,6 +16,8 @@
 #include <type_traits>
 
 #include "kvc_common.cuh"
+#include "kvc_flat.cuh"
+#include "kvc_tc.cuh"
 
 namespace {
 
@@ -235,156 +237,732 @@ tree_commit_kernel(const CommitArgs a)
 // --------------------------------------------------------------------------
 // attention
 // --------------------------------------------------------------------------
+//
+// The group's G heads x N nodes are the rows of the query matrix of one (batch
+// row, kv head), in tiles of 128: row m is head m / N, node m % N, as they lie
+// in memory.  Each (batch row, kv head, row tile) streams its keys past the
+// tensor cores in tiles of 128, and every CTA (one an SM) takes the same number
+// of key tiles, whatever the lengths (kvc_flat.cuh); rows that several CTAs
+// worked on are joined by tree_merge_kernel.
+//
+//   TMEM columns  O [0, D) fp32 | S / P double buffer [D, D + 256)
+//   shared        Q (128 x D, 128-byte swizzled) | ring of half tiles (64 rows)
+//   warp 0        issues tcgen05.mma in the order S_0, S_1, PV_0, S_2, PV_1, ...
+//   warps 1-8     query rows in, softmax, output rows out: two threads a row
+//                 (= TMEM lane), each half of the columns
+//   warp 9        TMA producer of the ring in the order of use (K_0, K_1, V_0,
+//                 K_2, ...), through the next segment's tiles without a stop
+//
+// Half tiles are 64 rows, so that one lies inside a page.  Only key tiles that
+// hold drafts, or that a window's edge may cut, are masked ("cut" tiles).  A row
+// of V that not every query row sees may hold anything: 0 x NaN would reach the
+// rows that do not see it.  So in the cut tiles the softmax warps look through V
+// in shared memory, put zeros in the place of NaN and infinity, and make the rows
+// that do see such a value NaN.
+
+constexpr int kBM = 128, kBN = 128, kHalf = 64;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kAttnThreads = 32 * (1 + kSoftmaxWarps + 1);
+constexpr float kRescale = 8.f;  // log2 units by which a score may exceed the reference maximum
 
 struct TreeArgs {
     void *out;
     const void *q;
-    const void *k, *v;
     const uint32_t *mask;
     const int32_t *depth;
     CacheRows at;
     kvc_lengths len;
     int batch, q_heads, kv_heads, group, nodes;
+    int row_tiles;  // ceil(group * nodes / 128)
     int window;
     float scale_log2;
     const float *cos_t, *sin_t;
     int64_t rope_max_pos;
+    int grid;
+    float *ws_o, *ws_m, *ws_l;  // [2 * grid][128] (x D)
     int32_t *status;
 };
 
-// One block per (node, kv head, batch row), a warp per query head: 32 keys at
-// a time, one a lane for the scores, then all lanes over the columns.
-template <typename T, int D>
-__global__ void __launch_bounds__(128)
-tree_attn_kernel(const TreeArgs a)
+template <int D> struct TreeSmem {
+    static constexpr int Q_BYTES = kBM * D * 2;
+    static constexpr int SLAB = kHalf * D * 2;
+    static constexpr int BUDGET = 227 * 1024;
+    static constexpr int MISC = (2 * 12 + 8) * 8 + 16 + 4 * kBM * 4 + kMaxNodes * 2 + 16;
+    static constexpr int FIT = (BUDGET - Q_BYTES - MISC) / SLAB;
+    static constexpr int NSLAB = FIT < 12 ? FIT : 12;
+    static constexpr int RING_OFF = Q_BYTES;
+    static constexpr int BAR_OFF = RING_OFF + NSLAB * SLAB;
+    // full[NSLAB], empty[NSLAB], s_full[2], p_full[2], o_done[2], q_full, drain
+    static constexpr int MISC_OFF = BAR_OFF + (2 * NSLAB + 8) * 8;
+    static constexpr int RED_OFF = MISC_OFF + 16;            // row maximum / sum exchange
+    static constexpr int DEPTH_OFF = RED_OFF + 4 * kBM * 4;  // int16 depths of the segment's nodes
+    static constexpr int BAD_OFF = DEPTH_OFF + kMaxNodes * 2;
+    static constexpr int TOTAL = BAD_OFF + 16;
+    static_assert(TOTAL <= BUDGET && NSLAB >= 4, "a tile of K and one of V must fit");
+    static constexpr uint32_t COL_O = 0, COL_S = D, TMEM_COLS = 512;
+};
+
+// first key row of batch row b's tiles and their number (0: nothing to do)
+__device__ __forceinline__ int tree_tiles(const TreeArgs &a, int b, int &lo, uint32_t &bad)
 {
-    __shared__ float q_sh[4][D], p_sh[4][32];
-    __shared__ int64_t row_sh[4][32];
-    const int i = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int P = a.len.past_abs[b];
+    bad = 0;
+    lo = 0;
     if (a.len.cache_total[b] < 0 || P < 0)
-        return;
-    const bool lead = threadIdx.x == 0 && i == 0 && h == 0;
-    if (a.cos_t && (int64_t)P + a.nodes > a.rope_max_pos) {
-        if (lead)
-            kvc::raise_status(a.status, KVC_DEV_ROPE_RANGE);
-        return;
-    }
-    if ((int64_t)P + a.nodes > a.at.rows) {
-        if (lead)
-            kvc::raise_status(a.status, KVC_DEV_CAPACITY);
-        return;
-    }
-    const int d = a.depth[(int64_t)b * a.nodes + i];
-    const bool there = d >= 0 && d < a.nodes;
-    if (d >= a.nodes && threadIdx.x == 0 && h == 0)
-        kvc::raise_status(a.status, KVC_DEV_INDEX_OOB);
-    const int words = (a.nodes + 31) / 32;
-    const uint32_t *mask = a.mask + ((int64_t)b * a.nodes + i) * words;
-    const int64_t pos = (int64_t)P + d;
-    for (int r = warp; r < a.group; r += 4) {
-        const int64_t qrow = (((int64_t)b * a.q_heads + h * a.group + r) * a.nodes + i) * D;
-        const T *q = static_cast<const T *>(a.q) + qrow;
-        T *out = static_cast<T *>(a.out) + qrow;
-        if (!there) {
-            for (int c = lane; c < D; c += 32)
-                out[c] = kvc::Elem<T>::from_f32(0.f);
-            continue;
+        return 0;
+    const int64_t T = (int64_t)P + a.nodes;
+    if (a.cos_t && T > a.rope_max_pos)
+        bad = KVC_DEV_ROPE_RANGE;
+    else if (T > a.at.rows)
+        bad = KVC_DEV_CAPACITY;
+    if (bad)
+        return 0;
+    if (a.window > 0)
+        lo = max(0, P - a.window + 1) & ~(kHalf - 1);  // what a node of depth 0 sees
+    return (int)((T - lo + kBN - 1) / kBN);
+}
+
+// The segments of a CTA's share: tiles [t0, t1) of the n tiles of line row
+// (b, head, row tile).
+struct Segments {
+    int x, x_end, b, base;
+    __device__ __forceinline__ bool next(const TreeArgs &a, int &row, int &n, int &lo, int &t0, int &t1)
+    {
+        if (x >= x_end)
+            return false;
+        uint32_t bad;
+        const int rows = a.kv_heads * a.row_tiles;
+        n = tree_tiles(a, b, lo, bad);
+        while (x >= base + n * rows) {
+            base += n * rows;
+            ++b;
+            n = tree_tiles(a, b, lo, bad);
         }
-        for (int c = lane; c < D / 2; c += 32) {
-            float lo = kvc::Elem<T>::to_f32(q[c]), hi = kvc::Elem<T>::to_f32(q[c + D / 2]);
-            if (a.cos_t)
-                kvc::rope_pair(lo, hi, a.cos_t[pos * (D / 2) + c], a.sin_t[pos * (D / 2) + c]);
-            q_sh[warp][c] = lo;
-            q_sh[warp][c + D / 2] = hi;
+        row = (x - base) / n;
+        t0 = (x - base) - row * n;
+        t1 = min(n, t0 + (x_end - x));
+        x += t1 - t0;
+        return true;
+    }
+};
+
+// The ring holds, for a segment of n tiles, K_0, K_1, then V_j and K_{j+2} while
+// there is one, then the last V's: group g of that order, and the place of V_j.
+__device__ __forceinline__ void ring_group(int g, int n, bool &is_v, int &tile)
+{
+    const int lead = n < 2 ? n : 2, paired = n - lead;
+    if (g < lead) {
+        is_v = false;
+        tile = g;
+    } else if (g - lead < 2 * paired) {
+        is_v = ((g - lead) & 1) == 0;
+        tile = (g - lead) / 2 + (is_v ? 0 : 2);
+    } else {
+        is_v = true;
+        tile = g - lead - paired;
+    }
+}
+__device__ __forceinline__ int v_group(int j, int n)
+{
+    const int lead = n < 2 ? n : 2, paired = n - lead;
+    return j < paired ? lead + 2 * j : lead + paired + j;
+}
+
+// the 16-bit halves of w that are NaN or infinite, as 0xffff each
+template <typename T> __device__ __forceinline__ uint32_t not_finite(uint32_t w)
+{
+    constexpr uint32_t ex = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
+    return __vcmpeq2(w & ex, ex);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                 const TreeArgs a)
+{
+    using SM = TreeSmem<D>;
+    using kvc_tc::wait_or_abort;
+    constexpr int NSLAB = SM::NSLAB;
+    constexpr uint32_t AB = std::is_same<T, __half>::value ? 0u : 1u;
+    constexpr uint32_t IDESC_S = kvc_tc::f16_idesc(AB, 0, kBM, kHalf);
+    constexpr uint32_t IDESC_O = kvc_tc::f16_idesc(AB, 1, kBM, D);
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    {
+        // the swizzled tiles need a 1024-byte aligned base
+        uint32_t dyn;
+        asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(dyn));
+        if ((uint32_t)(smem - smem_raw) + SM::TOTAL > dyn) {
+            if (threadIdx.x == 0)
+                kvc::raise_status(a.status, KVC_DEV_CAPACITY);
+            return;
         }
-        __syncwarp();
-        float acc[D / 32], m = -INFINITY, l = 0.f;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e)
-            acc[e] = 0.f;
-        const int64_t lo = a.window > 0 ? max((int64_t)0, pos - a.window + 1) : 0;
-        for (int64_t r0 = min(lo, (int64_t)P); r0 < (int64_t)P + a.nodes; r0 += 32) {
-            const int64_t row = r0 + lane;
-            bool see = row < P;
-            if (row >= P && row < (int64_t)P + a.nodes) {
-                const int j = (int)(row - P);
-                const int dj = a.depth[(int64_t)b * a.nodes + j];
-                see = (mask[j >> 5] >> (j & 31) & 1u) && dj >= 0 && dj < a.nodes &&
-                      (a.window <= 0 || d - dj < a.window);
+    }
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + SM::BAR_OFF), *empty = full + NSLAB,
+             *s_full = full + 2 * NSLAB, *p_full = s_full + 2, *o_done = s_full + 4, *q_full = s_full + 6,
+             *drain = s_full + 7;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + SM::MISC_OFF);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + SM::MISC_OFF + 4);
+
+    kvc::grid_dep_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int N = a.nodes, rows = a.group * N, line_rows = a.kv_heads * a.row_tiles;
+    auto count = [&](int b) {
+        int lo;
+        uint32_t bad;
+        const int n = tree_tiles(a, b, lo, bad);
+        if (bad && blockIdx.x == 0 && warp == 0)
+            kvc::raise_status(a.status, bad);
+        return n;
+    };
+    Segments seg;
+    const int U = kvc_flat::locate(a.batch, line_rows, count, -1, seg.b, seg.base);
+    seg.x = kvc_flat::share_begin(blockIdx.x, a.grid, U);
+    seg.x_end = kvc_flat::share_begin(blockIdx.x + 1, a.grid, U);
+    if (seg.x >= seg.x_end)
+        return;
+    kvc_flat::row_of(a.batch, line_rows, count, seg.x, seg.b, seg.base);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NSLAB; ++i) {
+            kvc::mbar_init(&full[i], 1);
+            kvc::mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            kvc::mbar_init(&s_full[i], 1);
+            kvc::mbar_init(&p_full[i], kSoftmaxWarps);
+            kvc::mbar_init(&o_done[i], 1);
+        }
+        kvc::mbar_init(q_full, kSoftmaxWarps);
+        kvc::mbar_init(drain, 1);
+        *abort_flag = 0;
+        kvc::fence_mbar_init();
+    }
+    if (warp == 0) {
+        kvc_tc::tmem_alloc(tmem_slot, SM::TMEM_COLS);
+        kvc_tc::fence_before();
+    }
+    __syncthreads();
+    kvc_tc::fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t smem_base = kvc::smem_u32(smem);
+    int row, n, lo, t0, t1;  // the segment: line row, its tiles, first key row, own tiles
+
+    if (warp == 1 + kSoftmaxWarps) {
+        // ======================= TMA producer =======================
+        if (lane == 0) {
+            kvc::tma_prefetch_desc(&tmap_k);
+            kvc::tma_prefetch_desc(&tmap_v);
+            int q = 0;  // half tiles put into the ring so far
+            bool ok = true;
+            while (ok && seg.next(a, row, n, lo, t0, t1)) {
+                const int b = seg.b, h = row / a.row_tiles;
+                const int64_t end = (int64_t)a.len.past_abs[b] + N;
+                for (int u = 0; ok && u < 4 * (t1 - t0); ++u, ++q) {
+                    const int slot = q % NSLAB;
+                    if (q >= NSLAB && !wait_or_abort(&empty[slot], ((q / NSLAB) - 1) & 1, abort_flag, a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    bool is_v;
+                    int tile;
+                    ring_group(u >> 1, t1 - t0, is_v, tile);
+                    const int64_t r = (int64_t)lo + (t0 + tile) * kBN + (u & 1) * kHalf;
+                    int64_t y = -1;
+                    if (r < end) {
+                        if (a.at.table) {
+                            const int64_t id = __ldg(a.at.table + (int64_t)b * a.at.max_pages + r / a.at.page_size);
+                            if (id >= 0 && id < a.at.n_pool)
+                                y = (id * a.kv_heads + h) * a.at.page_size + r % a.at.page_size;
+                            else
+                                kvc::raise_status(a.status, KVC_DEV_INDEX_OOB);
+                        } else {
+                            y = ((int64_t)b * a.kv_heads + h) * a.at.rows + r;
+                        }
+                    }
+                    if (y < 0) {
+                        // nothing to read: the slot keeps what it holds, and its columns are masked
+                        kvc::mbar_arrive(&full[slot]);
+                        continue;
+                    }
+                    kvc::mbar_arrive_expect_tx(&full[slot], SM::SLAB);
+                    kvc::tma_load_3d(smem + SM::RING_OFF + slot * SM::SLAB, is_v ? &tmap_v : &tmap_k, 0, (int32_t)y, 0,
+                                     &full[slot]);
+                }
             }
-            int64_t at = -1;
-            if (see) {
-                if (a.at.table) {
-                    const int64_t id = a.at.table[(int64_t)b * a.at.max_pages + row / a.at.page_size];
-                    if (id < 0 || id >= a.at.n_pool) {
-                        kvc::raise_status(a.status, KVC_DEV_INDEX_OOB);
-                        see = false;
+            if (*abort_flag)
+                // wind-down: let the loads in flight land before the CTA exits
+                for (int i = max(0, q - NSLAB); i < q; ++i)
+                    kvc::mbar_wait(&full[i % NSLAB], (i / NSLAB) & 1);
+        }
+    } else if (warp == 0) {
+        // ======================= MMA issuer =======================
+        if (lane == 0) {
+            int q = 0, J = 0, s_no = 0;  // half tiles, tiles and segments taken so far
+            bool ok = true;
+            const uint64_t q_desc = kvc_tc::sw128_desc(smem_base, 16);
+            const uint64_t k_ring = kvc_tc::sw128_desc(smem_base + SM::RING_OFF, 16);
+            const uint64_t v_ring = kvc_tc::sw128_desc(smem_base + SM::RING_OFF, kHalf * 128);
+            auto issue_s = [&](int buf) -> bool {
+                for (int hf = 0; hf < 2; ++hf, ++q) {
+                    const int slot = q % NSLAB;
+                    if (!wait_or_abort(&full[slot], (q / NSLAB) & 1, abort_flag, a.status))
+                        return false;
+                    kvc_tc::fence_after();
+                    const uint64_t kd = k_ring + (uint64_t)(slot * (SM::SLAB / 16));
+                    const uint32_t d_s = tmem + SM::COL_S + buf * kBN + hf * kHalf;
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        kvc_tc::mma_ss(d_s, q_desc + (uint64_t)(((ks >> 2) * (kBM * 128) + (ks & 3) * 32) / 16),
+                                       kd + (uint64_t)(((ks >> 2) * (kHalf * 128) + (ks & 3) * 32) / 16), IDESC_S, ks > 0);
+                    kvc_tc::commit(&empty[slot]);
+                }
+                kvc_tc::commit(&s_full[buf]);
+                return true;
+            };
+            while (ok && seg.next(a, row, n, lo, t0, t1)) {
+                const int nt = t1 - t0;
+                ok = wait_or_abort(q_full, s_no & 1, abort_flag, a.status);
+                kvc_tc::fence_after();
+                for (int j = 0; ok && j < 2 && j < nt; ++j)
+                    ok = issue_s((J + j) & 1);
+                for (int j = 0; ok && j < nt; ++j, ++J) {
+                    const int s = J & 1;
+                    if (!(ok = wait_or_abort(&p_full[s], (J >> 1) & 1, abort_flag, a.status)))
+                        break;
+                    kvc_tc::fence_after();
+                    for (int hf = 0; hf < 2; ++hf, ++q) {
+                        const int slot = q % NSLAB;
+                        if (!(ok = wait_or_abort(&full[slot], (q / NSLAB) & 1, abort_flag, a.status)))
+                            break;
+                        kvc_tc::fence_after();
+                        const uint64_t vd = v_ring + (uint64_t)(slot * (SM::SLAB / 16));
+                        const uint32_t pa = tmem + SM::COL_S + s * kBN + hf * (kHalf / 2);
+#pragma unroll
+                        for (int k2 = 0; k2 < kHalf / 16; ++k2)
+                            kvc_tc::mma_ts(tmem + SM::COL_O, pa + k2 * 8, vd + (uint64_t)(k2 * (2048 / 16)), IDESC_O,
+                                           j > 0 || hf > 0 || k2 > 0);
+                        kvc_tc::commit(&empty[slot]);
+                    }
+                    if (!ok)
+                        break;
+                    kvc_tc::commit(&o_done[s]);
+                    if (j + 2 < nt)
+                        ok = issue_s(s);
+                }
+                ++s_no;
+            }
+            // everything issued above has completed once this arrives
+            kvc_tc::commit(drain);
+            kvc::mbar_wait(drain, 0);
+        }
+    } else {
+        // ======================= softmax =======================
+        const int sw = warp - 1, tid = threadIdx.x - 32;
+        const int quad = warp & 3, half = sw >> 2;   // TMEM lane quadrant; columns [0, 64) or [64, 128)
+        const int m = quad * 32 + lane;
+        const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
+        float *red = reinterpret_cast<float *>(smem + SM::RED_OFF);
+        int16_t *depth_sh = reinterpret_cast<int16_t *>(smem + SM::DEPTH_OFF);
+        uint32_t *bad_sh = reinterpret_cast<uint32_t *>(smem + SM::BAD_OFF);
+        constexpr uint32_t all_bar = 1;
+        const int words = (N + 31) / 32;
+        int q0 = 0, J = 0;  // half tiles before the segment, tiles so far
+        // `ok` is the warp's own; the softmax warps leave their loops together, at a barrier
+        bool ok = true, stop = false;
+        for (int s_no = 0; seg.next(a, row, n, lo, t0, t1); ++s_no) {
+            const int b = seg.b, h = row / a.row_tiles, mt = row % a.row_tiles, nt = t1 - t0;
+            const int P = a.len.past_abs[b];
+            const int64_t q_row0 = ((int64_t)b * a.kv_heads + h) * rows + (int64_t)mt * kBM;
+            const int32_t *depth = a.depth + (int64_t)b * N;
+
+            // ---- query rows: rotated at P + depth, into the MMA's layout ----
+            // (a negative scale goes into the query's sign, so that larger is nearer below)
+            {
+                constexpr int PPL = D / 64, RW = kBM / kSoftmaxWarps;  // rotation pairs a lane, rows a warp
+                constexpr int STEP = D == 256 ? 4 : 8;                 // rows in flight
+                struct alignas(2 * PPL) QV { T e[PPL]; };
+                struct alignas(4 * PPL) FV { float e[PPL]; };
+                const int c0 = PPL * lane, c1 = c0 + D / 2;
+                const float sign = a.scale_log2 < 0.f ? -1.f : 1.f;
+                const T *q = static_cast<const T *>(a.q) + q_row0 * D + c0;
+#pragma unroll 1
+                for (int u0 = sw * RW; u0 < (sw + 1) * RW; u0 += STEP) {
+                    QV lo_v[STEP], hi_v[STEP];
+                    int dv[STEP];
+#pragma unroll
+                    for (int u = 0; u < STEP; ++u) {
+                        const int rr = mt * kBM + u0 + u;
+                        dv[u] = -1;
+                        if (rr < rows) {
+                            dv[u] = depth[rr % N];
+                            lo_v[u] = *reinterpret_cast<const QV *>(q + (int64_t)(u0 + u) * D);
+                            hi_v[u] = *reinterpret_cast<const QV *>(q + (int64_t)(u0 + u) * D + D / 2);
+                        }
+                    }
+                    FV cv[STEP], sv[STEP];
+#pragma unroll
+                    for (int u = 0; u < STEP; ++u) {
+                        if (dv[u] >= 0 && dv[u] < N && a.cos_t) {
+                            const int64_t o = ((int64_t)P + dv[u]) * (D / 2) + c0;
+                            cv[u] = *reinterpret_cast<const FV *>(a.cos_t + o);
+                            sv[u] = *reinterpret_cast<const FV *>(a.sin_t + o);
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < STEP; ++u) {
+                        const bool there = dv[u] >= 0 && dv[u] < N;
+#pragma unroll
+                        for (int e = 0; e < PPL; ++e) {
+                            float x = there ? kvc::Elem<T>::to_f32(lo_v[u].e[e]) : 0.f;
+                            float y = there ? kvc::Elem<T>::to_f32(hi_v[u].e[e]) : 0.f;
+                            if (there && a.cos_t)
+                                kvc::rope_pair(x, y, cv[u].e[e], sv[u].e[e]);
+                            lo_v[u].e[e] = kvc::Elem<T>::from_f32(x * sign);
+                            hi_v[u].e[e] = kvc::Elem<T>::from_f32(y * sign);
+                        }
+                        *reinterpret_cast<QV *>(smem + (c0 >> 6) * (kBM * 128) + kvc::sw128(u0 + u, (c0 & 63) >> 3) +
+                                                (c0 & 7) * 2) = lo_v[u];
+                        *reinterpret_cast<QV *>(smem + (c1 >> 6) * (kBM * 128) + kvc::sw128(u0 + u, (c1 & 63) >> 3) +
+                                                (c1 & 7) * 2) = hi_v[u];
                     }
                 }
-                if (see)
-                    at = row_index(a.at, b, h, a.kv_heads, row) * D;
             }
-            float s = -INFINITY;
-            if (see) {
-                s = 0.f;
-                const T *k = static_cast<const T *>(a.k) + at;
-                for (int c = 0; c < D; c += 8) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(k + c);
-                    const T *e = reinterpret_cast<const T *>(&x);
+            for (int i = tid; i < N; i += 32 * kSoftmaxWarps) {
+                const int d = depth[i];
+                depth_sh[i] = (int16_t)(d >= 0 && d < N ? d : -1);
+                if (d >= N)
+                    kvc::raise_status(a.status, KVC_DEV_INDEX_OOB);
+            }
+            kvc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                kvc::mbar_arrive(q_full);
+            kvc_tc::named_bar_sync(all_bar, 32 * kSoftmaxWarps);  // the depths are there
+
+            // ---- this thread's row ----
+            const int r = mt * kBM + m;
+            const bool active = mt * kBM + quad * 32 < rows;  // of the warp: it has rows at all
+            const int node = r % N;
+            const int d = r < rows ? depth_sh[node] : -1;
+            const uint32_t *mask = a.mask + ((int64_t)b * N + node) * words;
+            // cache rows from r_lo on are visible
+            const int r_lo = a.window > 0 ? max(0, P + d - a.window + 1) : 0;
+            float m_run = -INFINITY, l_run = 0.f;
+            const float c_log2 = fabsf(a.scale_log2);
+            for (int j = 0; j < nt; ++j, ++J) {
+                const int s = J & 1;
+                const int t_lo = lo + (t0 + j) * kBN, c0 = t_lo + 64 * half;
+                ok = ok && wait_or_abort(&s_full[s], (J >> 1) & 1, abort_flag, a.status);
+                kvc_tc::fence_after();
+                const bool cut = t_lo + kBN > P || (a.window > 0 && t_lo < P + N - a.window);
+                uint64_t bad[2] = {0, 0};  // V rows of the tile in which this thread found one not finite
+                if (cut && ok) {
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const int qi = q0 + 2 * v_group(j, nt) + hf;
+                        if (!(ok = wait_or_abort(&full[qi % NSLAB], (qi / NSLAB) & 1, abort_flag, a.status)))
+                            break;
+                        uint4 *v = reinterpret_cast<uint4 *>(smem + SM::RING_OFF + (qi % NSLAB) * SM::SLAB);
 #pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        s += q_sh[warp][c + u] * kvc::Elem<T>::to_f32(e[u]);
+                        for (int e = 0; e < SM::SLAB / 16 / 256; ++e) {
+                            const int at = tid + 256 * e;
+                            const uint4 x = v[at];
+                            const uint4 nf = make_uint4(not_finite<T>(x.x), not_finite<T>(x.y), not_finite<T>(x.z),
+                                                        not_finite<T>(x.w));
+                            if (nf.x | nf.y | nf.z | nf.w) {
+                                v[at] = make_uint4(x.x & ~nf.x, x.y & ~nf.y, x.z & ~nf.z, x.w & ~nf.w);
+                                bad[hf] |= 1ull << ((at >> 3) & 63);
+                            }
+                        }
+                    }
+                    kvc::fence_proxy_async_smem();
                 }
-                s *= a.scale_log2;
+                // the keys that this row sees, a bit a column
+                uint32_t see[2] = {~0u, ~0u};
+                if (active && (cut || d < 0)) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int k0 = c0 + 32 * e;  // key row of bit 0
+                        uint32_t bits = 0;
+                        if (d >= 0 && k0 < P && k0 + 32 > r_lo) {
+                            // cache rows [r_lo, P)
+                            bits = k0 < r_lo ? ~0u << (r_lo - k0) : ~0u;
+                            if (k0 + 32 > P)
+                                bits &= ~0u >> (k0 + 32 - P);
+                        }
+                        if (d >= 0 && k0 + 32 > P && k0 < P + N) {
+                            // drafts k0 - P + c
+                            const int w0 = (k0 - P) >> 5;
+                            const uint32_t x0 = w0 >= 0 ? mask[w0] : 0u;
+                            const uint32_t x1 = w0 + 1 < words ? mask[w0 + 1] : 0u;
+                            uint32_t left = __funnelshift_r(x0, x1, (k0 - P) & 31);
+                            while (left) {
+                                const int c = __ffs(left) - 1;
+                                left &= left - 1;
+                                const int jd = k0 - P + c;
+                                const int dj = jd < N ? depth_sh[jd] : -1;
+                                if (dj >= 0 && (a.window <= 0 || d - dj < a.window))
+                                    bits |= 1u << c;
+                            }
+                        }
+                        see[e] = bits;
+                    }
+                }
+                float v[64];
+                if (active) {
+                    uint32_t *raw = reinterpret_cast<uint32_t *>(v);
+                    kvc_tc::ld32(lane_addr + SM::COL_S + s * kBN + 64 * half, raw);
+                    kvc_tc::ld32(lane_addr + SM::COL_S + s * kBN + 64 * half + 32, raw + 32);
+                    kvc_tc::wait_ld();
+                    if (cut || d < 0) {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c)
+                            v[c] = see[c >> 5] >> (c & 31) & 1u ? v[c] : -INFINITY;
+                    }
+                    float mx0 = fmaxf(v[0], v[1]), mx1 = fmaxf(v[2], v[3]);
+#pragma unroll
+                    for (int c = 4; c < 64; c += 4) {
+                        mx0 = fmaxf(mx0, fmaxf(v[c], v[c + 1]));
+                        mx1 = fmaxf(mx1, fmaxf(v[c + 2], v[c + 3]));
+                    }
+                    red[(s * 2 + half) * kBM + m] = fmaxf(mx0, mx1);
+                }
+                // One barrier a tile of all softmax warps: the maxima are there, both halves' S has been
+                // read before either writes P, and a warp whose wait gave up takes the others with it.
+                bool spoiled = false;
+                if (kvc_tc::named_bar_any(all_bar, 32 * kSoftmaxWarps, !ok || (bad[0] | bad[1]))) {
+                    if (tid < 4)
+                        bad_sh[tid] = 0;
+                    if (kvc_tc::named_bar_any(all_bar, 32 * kSoftmaxWarps, !ok)) {
+                        stop = true;
+                        break;
+                    }
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf)
+                        if (bad[hf]) {
+                            atomicOr(&bad_sh[2 * hf], (uint32_t)bad[hf]);
+                            atomicOr(&bad_sh[2 * hf + 1], (uint32_t)(bad[hf] >> 32));
+                        }
+                    kvc_tc::named_bar_sync(all_bar, 32 * kSoftmaxWarps);
+                    spoiled = ((see[0] & bad_sh[2 * half]) | (see[1] & bad_sh[2 * half + 1])) != 0;
+                }
+                if (active) {
+                    const float top = fmaxf(red[(s * 2 + half) * kBM + m], red[(s * 2 + (half ^ 1)) * kBM + m]) * c_log2;
+                    float alpha = 1.f;
+                    bool rescale = false;
+                    if (top > m_run + kRescale || (m_run == -INFINITY && top > -INFINITY)) {
+                        if (j > 0 && m_run > -INFINITY) {
+                            alpha = kvc_tc::fast_exp2(m_run - top);
+                            rescale = true;
+                        }
+                        m_run = top;
+                    }
+                    const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+                    float ps0 = 0.f, ps1 = 0.f;
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int c = 0; c < 64; c += 2) {
+                        const float p0 = kvc_tc::fast_exp2(fmaf(v[c], c_log2, neg_m));
+                        const float p1 = kvc_tc::fast_exp2(fmaf(v[c + 1], c_log2, neg_m));
+                        ps0 += p0;
+                        ps1 += p1;
+                        pk[c / 2] = kvc_tc::pack2<T>(p0, p1);
+                    }
+                    l_run = spoiled ? NAN : l_run * alpha + (ps0 + ps1);
+                    kvc_tc::st32(lane_addr + SM::COL_S + s * kBN + 32 * half, pk);
+                    if (__any_sync(0xffffffffu, rescale)) {
+                        // the reference moved: rescale this half of the O row (PV of the tile before is done;
+                        // a wait that gives up is reported at the next barrier)
+                        ok = wait_or_abort(&o_done[(J - 1) & 1], ((J - 1) >> 1) & 1, abort_flag, a.status);
+                        kvc_tc::fence_after();
+#pragma unroll 1
+                        for (int cc = half * (D / 2); cc < (half + 1) * (D / 2); cc += 32) {
+                            uint32_t o[32];
+                            kvc_tc::ld32(lane_addr + SM::COL_O + cc, o);
+                            kvc_tc::wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                            kvc_tc::st32(lane_addr + SM::COL_O + cc, o);
+                        }
+                    }
+                    kvc_tc::wait_st();
+                }
+                kvc_tc::fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    kvc::mbar_arrive(&p_full[s]);
             }
-            float top = s;
+            if (stop)
+                break;
+            q0 += 4 * nt;
+
+            // ---- output rows ----
+            // (every MMA of the segment has completed after this wait: Q and O may be used)
+            ok = ok && wait_or_abort(&o_done[(J - 1) & 1], ((J - 1) >> 1) & 1, abort_flag, a.status);
+            kvc_tc::fence_after();
+            if (active)
+                red[((J & 1) * 2 + half) * kBM + m] = l_run;
+            if (kvc_tc::named_bar_any(all_bar, 32 * kSoftmaxWarps, !ok))
+                break;
+            if (active) {
+                const float l = l_run + red[((J & 1) * 2 + (half ^ 1)) * kBM + m];
+                const bool whole = nt == n;
+                const int64_t part = (2 * (int64_t)blockIdx.x + (s_no == 0 ? 0 : 1)) * kBM + m;
+                // a row that saw nothing holds no sum: zeros, whatever O is
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+                for (int cc = half * (D / 2); cc < (half + 1) * (D / 2); cc += 32) {
+                    uint32_t o[32];
+                    kvc_tc::ld32(lane_addr + SM::COL_O + cc, o);
+                    kvc_tc::wait_ld();
+                    if (r >= rows)
+                        continue;
+                    if (whole) {
+                        T *to = static_cast<T *>(a.out) + (q_row0 + m) * D + cc;
 #pragma unroll
-            for (int x = 16; x; x >>= 1)
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-            const float m_new = fmaxf(m, top);
-            const float f = m == m_new ? 1.f : exp2f(m - m_new);
-            m = m_new;
-            const float p = see ? exp2f(s - (m == -INFINITY ? 0.f : m)) : 0.f;
-            l = l * f + p;
+                        for (int c = 0; c < 32; c += 8) {
+                            uint4 x;
+                            uint32_t *w = reinterpret_cast<uint32_t *>(&x);
 #pragma unroll
-            for (int e = 0; e < D / 32; ++e)
-                acc[e] *= f;
-            p_sh[warp][lane] = p;
-            row_sh[warp][lane] = at;
-            __syncwarp();
-            for (int j = 0; j < 32; ++j) {
-                const int64_t vr = row_sh[warp][j];
-                if (vr < 0)
-                    continue;
-                const float w = p_sh[warp][j];
+                            for (int e = 0; e < 4; ++e) {
+                                const float f0 = l == 0.f ? 0.f : __uint_as_float(o[c + 2 * e]) * inv;
+                                const float f1 = l == 0.f ? 0.f : __uint_as_float(o[c + 2 * e + 1]) * inv;
+                                w[e] = kvc_tc::pack2<T>(f0, f1);
+                            }
+                            *reinterpret_cast<uint4 *>(to + c) = x;
+                        }
+                    } else {
+                        uint4 *to = reinterpret_cast<uint4 *>(a.ws_o + part * D + cc);
 #pragma unroll
-                for (int e = 0; e < D / 32; ++e)
-                    acc[e] += w * kvc::Elem<T>::to_f32(static_cast<const T *>(a.v)[vr + lane + 32 * e]);
+                        for (int c = 0; c < 32; c += 4)
+                            to[c / 4] = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                    }
+                }
+                if (!whole && half == 0 && r < rows) {
+                    a.ws_m[part] = m_run;
+                    a.ws_l[part] = l;
+                }
             }
-            __syncwarp();
+            kvc_tc::fence_before();
         }
-#pragma unroll
-        for (int x = 16; x; x >>= 1)
-            l += __shfl_xor_sync(0xffffffffu, l, x);
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e)
-            out[lane + 32 * e] = kvc::Elem<T>::from_f32(l == 0.f ? 0.f : acc[e] / l);
-        __syncwarp();
+    }
+
+    __syncthreads();
+    if (warp == 0) {
+        kvc_tc::fence_after();
+        kvc_tc::tmem_dealloc(tmem, SM::TMEM_COLS);
     }
 }
 
-template <typename T> kvc_status launch_attn(const TreeArgs &a, int D, cudaStream_t stream)
+// Joins the partial results of a query row that several CTAs worked on, a warp
+// a row: out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.  A split row begins
+// in the share of exactly one CTA, which the block takes its number from.
+template <typename T, int D>
+__global__ void __launch_bounds__(256)
+tree_merge_kernel(const TreeArgs a)
 {
-    const dim3 grid(a.nodes, a.kv_heads, a.batch);
-    if (D == 64)
-        tree_attn_kernel<T, 64><<<grid, 128, 0, stream>>>(a);
-    else if (D == 128)
-        tree_attn_kernel<T, 128><<<grid, 128, 0, stream>>>(a);
-    else
-        tree_attn_kernel<T, 256><<<grid, 128, 0, stream>>>(a);
+    const int c0 = blockIdx.x, lane = threadIdx.x & 31, m = blockIdx.y * 8 + (threadIdx.x >> 5);
+    const int rows = a.group * a.nodes, line_rows = a.kv_heads * a.row_tiles;
+    auto count = [&](int b) {
+        int lo;
+        uint32_t bad;
+        return tree_tiles(a, b, lo, bad);
+    };
+    int b, base;
+    const int U = kvc_flat::locate(a.batch, line_rows, count, -1, b, base);
+    const int x0 = kvc_flat::share_begin(c0, a.grid, U), x1 = kvc_flat::share_begin(c0 + 1, a.grid, U);
+    kvc::grid_dep_wait();
+    if (x0 == x1 || x1 == U)
+        return;
+    kvc_flat::row_of(a.batch, line_rows, count, x1, b, base);  // the row that the next CTA goes on with
+    const int n = count(b);
+    const int row = (x1 - base) / n, first = base + row * n;
+    if (first == x1 || first < x0)
+        return;  // it begins there, or began before this CTA
+    const int c1 = kvc_flat::share_of(first + n - 1, a.grid, U);
+    const int mt = row % a.row_tiles;
+    if (mt * kBM + m >= rows)
+        return;
+    float top = -INFINITY;
+    for (int c = c0; c <= c1; ++c) {
+        const int s = kvc_flat::share_begin(c, a.grid, U);
+        if (s == kvc_flat::share_begin(c + 1, a.grid, U))
+            continue;
+        const int64_t p = (2 * (int64_t)c + (s < first ? 1 : 0)) * kBM + m;
+        top = fmaxf(top, a.ws_l[p] == 0.f ? -INFINITY : a.ws_m[p]);
+    }
+    float acc[D / 32], sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e)
+        acc[e] = 0.f;
+    for (int c = c0; c <= c1; ++c) {
+        const int s = kvc_flat::share_begin(c, a.grid, U);
+        if (s == kvc_flat::share_begin(c + 1, a.grid, U))
+            continue;
+        const int64_t p = (2 * (int64_t)c + (s < first ? 1 : 0)) * kBM + m;
+        const float l = a.ws_l[p], mc = a.ws_m[p];
+        if (l == 0.f)
+            continue;  // nothing seen
+        const float w = mc == top || mc == -INFINITY ? 1.f : exp2f(mc - top);
+        sum += l * w;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e)
+            acc[e] += a.ws_o[p * D + lane + 32 * e] * w;
+    }
+    const int64_t out_row = ((int64_t)b * a.kv_heads + row / a.row_tiles) * rows + (int64_t)mt * kBM + m;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e)
+        static_cast<T *>(a.out)[out_row * D + lane + 32 * e] =
+            kvc::Elem<T>::from_f32(sum == 0.f ? 0.f : acc[e] / sum);
+}
+
+template <typename T, int D>
+kvc_status launch_attn_dim(const TreeArgs &a, const void *k, const void *v, cudaStream_t stream)
+{
+    using SM = TreeSmem<D>;
+    const CUtensorMapDataType tt = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                  : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const uint64_t rows = (a.at.table ? (uint64_t)a.at.n_pool * a.at.page_size : (uint64_t)a.batch * a.at.rows) *
+                          a.kv_heads;
+    CUtensorMap tk, tv;
+    if (!kvc_host::encode_3d_sw128(&tk, k, rows, D, kHalf, D / 64, tt) ||
+        !kvc_host::encode_3d_sw128(&tv, v, rows, D, kHalf, D / 64, tt))
+        return KVC_ERR_CUDA;
+    int dev = 0, optin = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess)
+        return KVC_ERR_CUDA;
+    const size_t smem = std::min<size_t>((size_t)SM::TOTAL + 1024, (size_t)optin);
+    if (smem < (size_t)SM::TOTAL)
+        return KVC_ERR_UNSUPPORTED;
+    auto kern = tree_attn_kernel<T, D>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return KVC_ERR_CUDA;
+    kern<<<a.grid, kAttnThreads, smem, stream>>>(tk, tv, a);
+    if (a.grid > 1) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(a.grid - 1, (std::min(kBM, a.group * a.nodes) + 7) / 8);
+        cfg.blockDim = dim3(256);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, tree_merge_kernel<T, D>, a) != cudaSuccess)
+            return KVC_ERR_CUDA;
+    }
     return kvc_host::launch_status();
+}
+
+template <typename T>
+kvc_status launch_attn(const TreeArgs &a, const void *k, const void *v, int D, cudaStream_t stream)
+{
+    return D == 64    ? launch_attn_dim<T, 64>(a, k, v, stream)
+           : D == 128 ? launch_attn_dim<T, 128>(a, k, v, stream)
+                      : launch_attn_dim<T, 256>(a, k, v, stream);
 }
 
 // sizes that the calls on the cache's rows share; rows_out: rows a sequence may have
@@ -491,7 +1069,8 @@ KVC_API size_t kvc_gqa_tree_workspace_size(int batch, int q_heads, int kv_heads,
 {
     if (batch < 1 || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads != 0 || nodes < 1 || head_dim < 1)
         return 0;
-    return 256;
+    // one CTA an SM, two partial results of a row tile each
+    return 2 * (size_t)kvc_host::sm_count() * kBM * (head_dim + 2) * sizeof(float);
 }
 
 KVC_API kvc_status kvc_gqa_tree(void *out, const void *q, const void *k_cache, const void *v_cache,
@@ -530,8 +1109,6 @@ KVC_API kvc_status kvc_gqa_tree(void *out, const void *q, const void *k_cache, c
     TreeArgs a{};
     a.out = out;
     a.q = q;
-    a.k = k_cache;
-    a.v = v_cache;
     a.mask = mask;
     a.depth = depth;
     a.at = at;
@@ -547,8 +1124,18 @@ KVC_API kvc_status kvc_gqa_tree(void *out, const void *q, const void *k_cache, c
     a.sin_t = rope_sin;
     a.rope_max_pos = rope_max_pos;
     a.status = dev_status;
+    a.row_tiles = (a.group * nodes + kBM - 1) / kBM;
+    const int64_t units = (int64_t)batch * kv_heads * a.row_tiles * ((at.rows + kBN - 1) / kBN);
+    if (units > (int64_t)INT32_MAX)
+        return KVC_ERR_SHAPE;
+    a.grid = (int)std::min<int64_t>(units, kvc_host::sm_count());
+    const int64_t parts = 2 * (int64_t)kvc_host::sm_count() * kBM;
+    a.ws_o = static_cast<float *>(workspace);
+    a.ws_m = a.ws_o + parts * head_dim;
+    a.ws_l = a.ws_m + parts;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-    return dtype == KVC_BF16 ? launch_attn<__nv_bfloat16>(a, head_dim, stream) : launch_attn<__half>(a, head_dim, stream);
+    return dtype == KVC_BF16 ? launch_attn<__nv_bfloat16>(a, k_cache, v_cache, head_dim, stream)
+                             : launch_attn<__half>(a, k_cache, v_cache, head_dim, stream);
 }
 
 KVC_API kvc_status kvc_tree_commit(void *k_cache, void *v_cache, const int32_t *path, const int32_t *accepted,
