@@ -3,9 +3,10 @@
 // The attention over a batch is B x heads independent rows, row (b, h) made
 // of n_b equal units of keys; the lengths, and with them n_b, are known on
 // the device only.  Laid end to end (b outermost, then h, then the unit) the
-// rows are one line of U = heads * sum_b n_b units, and CTA c of a grid of G
-// takes units [c U / G, (c + 1) U / G): every CTA gets the same work whatever
-// the lengths, with no queue, no counters and the same split on every run.
+// rows are one line of U = heads * sum_b n_b units, cut into G shares of U / G
+// units, the first U % G of them one longer: every CTA gets the same work
+// whatever the lengths, with no queue, no counters and the same split on every
+// run.
 // A CTA's share is a tail of one row, whole rows, and a head of another, so
 // it leaves at most two partial results (slot 0: its first segment, slot 1:
 // its last), and the scratch for them depends on the grid alone.
@@ -15,16 +16,18 @@
 
 namespace kvc_flat {
 
-__device__ __forceinline__ int share_begin(int c, int grid, int U)
-{
-    return (int)((int64_t)c * U / grid);
-}
-
-// the CTA whose share holds unit x
-__device__ __forceinline__ int share_of(int x, int grid, int U)
-{
-    return (int)((((int64_t)x + 1) * grid - 1) / U);
-}
+struct Shares {
+    int each, longer;  // shares [0, longer) are of each + 1 units, the others of each
+    __device__ __forceinline__ Shares(int U, int grid) : each(U / grid), longer(U % grid) {}
+    __device__ __forceinline__ int begin(int c) const { return c * each + min(c, longer); }
+    // the share that holds unit x (0 <= x < U); the shares of a row are
+    // consecutive, and none of them is empty
+    __device__ __forceinline__ int of(int x) const
+    {
+        const int head = longer * (each + 1);
+        return x < head ? x / (each + 1) : longer + (x - head) / each;
+    }
+};
 
 // Walks the batch with one warp.  `count(b)` is n_b (>= 0).  Returns U; for
 // the unit x (or, when x < 0, for the row b_in) gives the batch row and the

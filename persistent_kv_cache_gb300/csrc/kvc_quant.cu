@@ -443,8 +443,9 @@ quant_decode_kernel(const QuantDecodeArgs a)
     };
     int b, base;
     const int U = kvc_flat::locate(a.batch, a.kv_heads, units, -1, b, base);
-    int x = kvc_flat::share_begin(c, a.grid, U);
-    const int x_end = kvc_flat::share_begin(c + 1, a.grid, U);
+    const kvc_flat::Shares shares(U, a.grid);
+    int x = shares.begin(c);
+    const int x_end = shares.begin(c + 1);
     if (x >= x_end)
         return;
     kvc_flat::row_of(a.batch, a.kv_heads, units, x, b, base);
@@ -771,13 +772,23 @@ quant_decode_kernel(const QuantDecodeArgs a)
 }
 
 // Joins the partial results of one query head: out = sum_i 2^(m_i - m) o_i /
-// sum_i 2^(m_i - m) l_i over the CTAs whose shares cover its row.
+// sum_i 2^(m_i - m) l_i over the CTAs whose shares cover its row.  The parts'
+// m and l are read at once, a part a thread; then D / 4 threads take the
+// columns of a part and the block's groups of them the parts in turn.
+constexpr int kMergeThreads = 128;
+constexpr int kMaxParts = 1024;  // at least the CTAs of the attention launch
+
 template <typename T, int D>
-__global__ void __launch_bounds__(D)
+__global__ void __launch_bounds__(kMergeThreads)
 quant_merge_kernel(const QuantDecodeArgs a)
 {
-    const int slice = blockIdx.x, r = blockIdx.y, d = threadIdx.x;
+    constexpr int CT = D / 4, GROUPS = kMergeThreads / CT;
+    __shared__ float w_sh[kMaxParts];
+    __shared__ float red[2][kMergeThreads / 32];
+    __shared__ float4 o_sh[GROUPS][CT];
+    const int slice = blockIdx.x, r = blockIdx.y;
     const int b = slice / a.kv_heads, h = slice % a.kv_heads;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     auto units = [&](int bb) {
         int64_t first;
         uint32_t bad;
@@ -786,32 +797,76 @@ quant_merge_kernel(const QuantDecodeArgs a)
     int b_out, base;
     const int U = kvc_flat::locate(a.batch, a.kv_heads, units, b, b_out, base);
     const int nu = units(b);
+    const kvc_flat::Shares shares(U, a.grid);
+    const int x0 = base + h * nu;
     kvc::grid_dep_wait();
     if (nu == 0)
         return;
-    const int x0 = base + h * nu, x1 = x0 + nu;
-    const int c0 = kvc_flat::share_of(x0, a.grid, U), c1 = kvc_flat::share_of(x1 - 1, a.grid, U);
-    if (c0 == c1)
+    const int c0 = shares.of(x0), n = shares.of(x0 + nu - 1) - c0 + 1;
+    if (n == 1)
         return;  // written by that CTA
-    auto part_of = [&](int c) {
-        // the row's segment is the first of CTA c unless c began before the row
-        return 2 * (int64_t)c + (kvc_flat::share_begin(c, a.grid, U) < x0 ? 1 : 0);
-    };
+    // the row's segment is the first of its CTA, but in CTA c0 if that began before the row
+    const int slot0 = shares.begin(c0) < x0 ? 1 : 0;
+    auto part = [&](int i) { return ((int64_t)2 * (c0 + i) + (i == 0 ? slot0 : 0)) * a.group + r; };
     float top = -INFINITY;
-    for (int c = c0; c <= c1; ++c)
-        if (kvc_flat::share_begin(c, a.grid, U) < kvc_flat::share_begin(c + 1, a.grid, U))
-            top = fmaxf(top, a.ws_m[part_of(c) * a.group + r]);
-    float acc = 0.f, sum = 0.f;
-    for (int c = c0; c <= c1; ++c) {
-        if (kvc_flat::share_begin(c, a.grid, U) == kvc_flat::share_begin(c + 1, a.grid, U))
-            continue;
-        const int64_t p = part_of(c) * a.group + r;
-        const float mc = a.ws_m[p];
-        const float w = mc == top || mc == -INFINITY ? 1.f : exp2f(mc - top);
-        acc += a.ws_o[p * D + d] * w;
-        sum += a.ws_l[p] * w;
+    for (int i = threadIdx.x; i < n; i += kMergeThreads) {
+        w_sh[i] = a.ws_m[part(i)];
+        top = fmaxf(top, w_sh[i]);
     }
-    static_cast<T *>(a.out)[((int64_t)slice * a.group + r) * D + d] = kvc::Elem<T>::from_f32(acc / sum);
+#pragma unroll
+    for (int d = 16; d; d >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    if (lane == 0)
+        red[0][warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kMergeThreads / 32; ++w)
+        top = fmaxf(top, red[0][w]);
+    float sum = 0.f;
+    for (int i = threadIdx.x; i < n; i += kMergeThreads) {
+        // (a part whose scores are all NaN has m = -inf and a NaN sum, which has to be seen)
+        const float m = w_sh[i], w = m == top || m == -INFINITY ? 1.f : exp2f(m - top);
+        w_sh[i] = w;
+        sum += w * a.ws_l[part(i)];
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (lane == 0)
+        red[1][warp] = sum;
+    __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kMergeThreads / 32; ++w)
+        sum += red[1][w];
+    const int col = threadIdx.x % CT, grp = threadIdx.x / CT;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = grp; i < n; i += GROUPS) {
+        const float4 o = *(reinterpret_cast<const float4 *>(a.ws_o + part(i) * D) + col);
+        const float w = w_sh[i];
+        acc.x += w * o.x;
+        acc.y += w * o.y;
+        acc.z += w * o.z;
+        acc.w += w * o.w;
+    }
+    o_sh[grp][col] = acc;
+    __syncthreads();
+    if (grp == 0) {
+#pragma unroll
+        for (int e = 1; e < GROUPS; ++e) {
+            const float4 o = o_sh[e][col];
+            acc.x += o.x;
+            acc.y += o.y;
+            acc.z += o.z;
+            acc.w += o.w;
+        }
+        T *to = static_cast<T *>(a.out) + ((int64_t)slice * a.group + r) * D + 4 * col;
+        to[0] = kvc::Elem<T>::from_f32(acc.x / sum);
+        to[1] = kvc::Elem<T>::from_f32(acc.y / sum);
+        to[2] = kvc::Elem<T>::from_f32(acc.z / sum);
+        to[3] = kvc::Elem<T>::from_f32(acc.w / sum);
+    }
 }
 
 // one wave of resident CTAs, or one CTA a unit where the cache has fewer
@@ -819,7 +874,7 @@ int decode_grid(int batch, int kv_heads, int group, int64_t C, int D)
 {
     const int64_t most = (int64_t)batch * kv_heads * ((C + kUnit - 1) / kUnit);
     const int64_t wave = (int64_t)kvc_host::sm_count() * ctas_per_sm(D, group > 8 ? 2 : 1);
-    return (int)std::max<int64_t>(1, std::min<int64_t>(most, wave));
+    return (int)std::max<int64_t>(1, std::min<int64_t>({most, wave, kMaxParts}));
 }
 
 template <typename T, int FMT, int D, int HB> kvc_status launch_decode(const QuantDecodeArgs &a, cudaStream_t stream)
@@ -834,7 +889,7 @@ template <typename T, int FMT, int D, int HB> kvc_status launch_decode(const Qua
     if (a.C > kUnit) {
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(a.batch * a.kv_heads, a.group);
-        cfg.blockDim = dim3(D);
+        cfg.blockDim = dim3(kMergeThreads);
         cfg.stream = stream;
         cudaLaunchAttribute at[1];
         at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

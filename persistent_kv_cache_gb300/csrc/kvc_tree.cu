@@ -418,8 +418,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     };
     Segments seg;
     const int U = kvc_flat::locate(a.batch, line_rows, count, -1, seg.b, seg.base);
-    seg.x = kvc_flat::share_begin(blockIdx.x, a.grid, U);
-    seg.x_end = kvc_flat::share_begin(blockIdx.x + 1, a.grid, U);
+    const kvc_flat::Shares shares(U, a.grid);
+    seg.x = shares.begin(blockIdx.x);
+    seg.x_end = shares.begin(blockIdx.x + 1);
     if (seg.x >= seg.x_end)
         return;
     kvc_flat::row_of(a.batch, line_rows, count, seg.x, seg.b, seg.base);
@@ -583,49 +584,83 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                 constexpr int PPL = D / 64, RW = kBM / kSoftmaxWarps;  // rotation pairs a lane, rows a warp
                 constexpr int STEP = D == 256 ? 4 : 8;                 // rows in flight
                 struct alignas(2 * PPL) QV { T e[PPL]; };
-                struct alignas(4 * PPL) FV { float e[PPL]; };
                 const int c0 = PPL * lane, c1 = c0 + D / 2;
                 const float sign = a.scale_log2 < 0.f ? -1.f : 1.f;
                 const T *q = static_cast<const T *>(a.q) + q_row0 * D + c0;
+                int node = (mt * kBM + sw * RW) % N;
 #pragma unroll 1
                 for (int u0 = sw * RW; u0 < (sw + 1) * RW; u0 += STEP) {
-                    QV lo_v[STEP], hi_v[STEP];
+                    // Every load is of an address inside its array, wanted or not, so that none waits for
+                    // another but the tables' for the depths: rows past the last are the last again,
+                    // depths outside [0, N) are moved inside
                     int dv[STEP];
+                    bool there[STEP];
 #pragma unroll
                     for (int u = 0; u < STEP; ++u) {
-                        const int rr = mt * kBM + u0 + u;
-                        dv[u] = -1;
-                        if (rr < rows) {
-                            dv[u] = depth[rr % N];
-                            lo_v[u] = *reinterpret_cast<const QV *>(q + (int64_t)(u0 + u) * D);
-                            hi_v[u] = *reinterpret_cast<const QV *>(q + (int64_t)(u0 + u) * D + D / 2);
+                        dv[u] = __ldg(depth + node);
+                        node = node + 1 == N ? 0 : node + 1;
+                    }
+                    uint32_t qr[2][STEP][PPL == 4 ? 2 : 1];
+#pragma unroll
+                    for (int u = 0; u < STEP; ++u) {
+                        const int64_t at = (int64_t)min(u0 + u, rows - 1 - mt * kBM) * D;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const T *from = q + at + e * (D / 2);
+                            if constexpr (PPL == 4) {
+                                const uint2 x = __ldg(reinterpret_cast<const uint2 *>(from));
+                                qr[e][u][0] = x.x;
+                                qr[e][u][1] = x.y;
+                            } else if constexpr (PPL == 2) {
+                                qr[e][u][0] = __ldg(reinterpret_cast<const uint32_t *>(from));
+                            } else {
+                                qr[e][u][0] = __ldg(reinterpret_cast<const unsigned short *>(from));
+                            }
                         }
                     }
-                    FV cv[STEP], sv[STEP];
+                    float cv[STEP][PPL], sv[STEP][PPL];
 #pragma unroll
                     for (int u = 0; u < STEP; ++u) {
-                        if (dv[u] >= 0 && dv[u] < N && a.cos_t) {
-                            const int64_t o = ((int64_t)P + dv[u]) * (D / 2) + c0;
-                            cv[u] = *reinterpret_cast<const FV *>(a.cos_t + o);
-                            sv[u] = *reinterpret_cast<const FV *>(a.sin_t + o);
-                        }
-                    }
-#pragma unroll
-                    for (int u = 0; u < STEP; ++u) {
-                        const bool there = dv[u] >= 0 && dv[u] < N;
+                        there[u] = mt * kBM + u0 + u < rows && dv[u] >= 0 && dv[u] < N;
+                        const int64_t o = ((int64_t)P + min(max(dv[u], 0), N - 1)) * (D / 2) + c0;
 #pragma unroll
                         for (int e = 0; e < PPL; ++e) {
-                            float x = there ? kvc::Elem<T>::to_f32(lo_v[u].e[e]) : 0.f;
-                            float y = there ? kvc::Elem<T>::to_f32(hi_v[u].e[e]) : 0.f;
-                            if (there && a.cos_t)
-                                kvc::rope_pair(x, y, cv[u].e[e], sv[u].e[e]);
-                            lo_v[u].e[e] = kvc::Elem<T>::from_f32(x * sign);
-                            hi_v[u].e[e] = kvc::Elem<T>::from_f32(y * sign);
+                            cv[u][e] = 1.f;
+                            sv[u][e] = 0.f;
+                        }
+                        if (a.cos_t) {
+                            if constexpr (PPL == 4) {
+                                const float4 x = __ldg(reinterpret_cast<const float4 *>(a.cos_t + o));
+                                const float4 y = __ldg(reinterpret_cast<const float4 *>(a.sin_t + o));
+                                cv[u][0] = x.x, cv[u][1] = x.y, cv[u][2] = x.z, cv[u][3] = x.w;
+                                sv[u][0] = y.x, sv[u][1] = y.y, sv[u][2] = y.z, sv[u][3] = y.w;
+                            } else if constexpr (PPL == 2) {
+                                const float2 x = __ldg(reinterpret_cast<const float2 *>(a.cos_t + o));
+                                const float2 y = __ldg(reinterpret_cast<const float2 *>(a.sin_t + o));
+                                cv[u][0] = x.x, cv[u][1] = x.y;
+                                sv[u][0] = y.x, sv[u][1] = y.y;
+                            } else {
+                                cv[u][0] = __ldg(a.cos_t + o);
+                                sv[u][0] = __ldg(a.sin_t + o);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < STEP; ++u) {
+                        QV out[2];
+#pragma unroll
+                        for (int e = 0; e < PPL; ++e) {
+                            const T *xl = reinterpret_cast<const T *>(qr[0][u]), *xh = reinterpret_cast<const T *>(qr[1][u]);
+                            float x = kvc::Elem<T>::to_f32(xl[e]), y = kvc::Elem<T>::to_f32(xh[e]);
+                            if (a.cos_t)
+                                kvc::rope_pair(x, y, cv[u][e], sv[u][e]);
+                            out[0].e[e] = kvc::Elem<T>::from_f32(there[u] ? x * sign : 0.f);
+                            out[1].e[e] = kvc::Elem<T>::from_f32(there[u] ? y * sign : 0.f);
                         }
                         *reinterpret_cast<QV *>(smem + (c0 >> 6) * (kBM * 128) + kvc::sw128(u0 + u, (c0 & 63) >> 3) +
-                                                (c0 & 7) * 2) = lo_v[u];
+                                                (c0 & 7) * 2) = out[0];
                         *reinterpret_cast<QV *>(smem + (c1 >> 6) * (kBM * 128) + kvc::sw128(u0 + u, (c1 & 63) >> 3) +
-                                                (c1 & 7) * 2) = hi_v[u];
+                                                (c1 & 7) * 2) = out[1];
                     }
                 }
             }
@@ -872,45 +907,56 @@ tree_merge_kernel(const TreeArgs a)
     };
     int b, base;
     const int U = kvc_flat::locate(a.batch, line_rows, count, -1, b, base);
-    const int x0 = kvc_flat::share_begin(c0, a.grid, U), x1 = kvc_flat::share_begin(c0 + 1, a.grid, U);
-    kvc::grid_dep_wait();
-    if (x0 == x1 || x1 == U)
-        return;
-    kvc_flat::row_of(a.batch, line_rows, count, x1, b, base);  // the row that the next CTA goes on with
-    const int n = count(b);
-    const int row = (x1 - base) / n, first = base + row * n;
-    if (first == x1 || first < x0)
-        return;  // it begins there, or began before this CTA
-    const int c1 = kvc_flat::share_of(first + n - 1, a.grid, U);
-    const int mt = row % a.row_tiles;
-    if (mt * kBM + m >= rows)
-        return;
-    float top = -INFINITY;
-    for (int c = c0; c <= c1; ++c) {
-        const int s = kvc_flat::share_begin(c, a.grid, U);
-        if (s == kvc_flat::share_begin(c + 1, a.grid, U))
-            continue;
-        const int64_t p = (2 * (int64_t)c + (s < first ? 1 : 0)) * kBM + m;
-        top = fmaxf(top, a.ws_l[p] == 0.f ? -INFINITY : a.ws_m[p]);
+    const kvc_flat::Shares shares(U, a.grid);
+    const int x0 = shares.begin(c0), x1 = shares.begin(c0 + 1);
+    int n = 0, row = 0, first = 0;
+    if (x0 < x1 && x1 < U) {
+        kvc_flat::row_of(a.batch, line_rows, count, x1, b, base);  // the row that the next CTA goes on with
+        n = count(b);
+        row = (x1 - base) / n;
+        first = base + row * n;
     }
+    kvc::grid_dep_wait();
+    // (first == x1: it begins there; first < x0: it began before this CTA)
+    const int mt = row % a.row_tiles;
+    if (n == 0 || first == x1 || first < x0 || mt * kBM + m >= rows)
+        return;
+    const int parts = shares.of(first + n - 1) - c0 + 1;
+    // the row's segment is the first of its CTA, but in CTA c0 if that began before the row
+    auto part = [&](int i) { return (2 * ((int64_t)c0 + i) + (i == 0 && x0 < first ? 1 : 0)) * kBM + m; };
+    float top = -INFINITY;
+    for (int i = lane; i < parts; i += 32)
+        top = fmaxf(top, a.ws_l[part(i)] == 0.f ? -INFINITY : a.ws_m[part(i)]);
+#pragma unroll
+    for (int x = 16; x; x >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
     float acc[D / 32], sum = 0.f;
 #pragma unroll
     for (int e = 0; e < D / 32; ++e)
         acc[e] = 0.f;
-    for (int c = c0; c <= c1; ++c) {
-        const int s = kvc_flat::share_begin(c, a.grid, U);
-        if (s == kvc_flat::share_begin(c + 1, a.grid, U))
-            continue;
-        const int64_t p = (2 * (int64_t)c + (s < first ? 1 : 0)) * kBM + m;
-        const float l = a.ws_l[p], mc = a.ws_m[p];
-        if (l == 0.f)
-            continue;  // nothing seen
-        const float w = mc == top || mc == -INFINITY ? 1.f : exp2f(mc - top);
-        sum += l * w;
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+        // a part's weight a lane; a part that saw nothing (no sum) has none, whatever its O holds
+        float w = 0.f;
+        if (i0 + lane < parts) {
+            const float l = a.ws_l[part(i0 + lane)], mc = a.ws_m[part(i0 + lane)];
+            w = l == 0.f ? 0.f : mc == top || mc == -INFINITY ? 1.f : exp2f(mc - top);
+            sum += l * w;
+        }
+        const int here = min(32, parts - i0);
+#pragma unroll 4
+        for (int i = 0; i < here; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+            const float *o = a.ws_o + part(i0 + i) * D;
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e)
-            acc[e] += a.ws_o[p * D + lane + 32 * e] * w;
+            for (int e = 0; e < D / 32; ++e) {
+                const float x = o[lane + 32 * e];
+                acc[e] += wi == 0.f ? 0.f : x * wi;
+            }
+        }
     }
+#pragma unroll
+    for (int x = 16; x; x >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, x);
     const int64_t out_row = ((int64_t)b * a.kv_heads + row / a.row_tiles) * rows + (int64_t)mt * kBM + m;
 #pragma unroll
     for (int e = 0; e < D / 32; ++e)
