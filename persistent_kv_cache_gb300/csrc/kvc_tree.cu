@@ -246,21 +246,24 @@ tree_commit_kernel(const CommitArgs a)
 // worked on are joined by tree_merge_kernel.
 //
 //   TMEM columns  O [0, D) fp32 | S / P double buffer [D, D + 256)
-//   shared        Q (128 x D, 128-byte swizzled) | ring of half tiles (64 rows)
+//   shared        Q (128 x D, 128-byte swizzled) | ring of slabs of 64 or 128 rows
 //   warp 0        issues tcgen05.mma in the order S_0, S_1, PV_0, S_2, PV_1, ...
 //   warps 1-8     query rows in, softmax, output rows out: two threads a row
 //                 (= TMEM lane), each half of the columns
 //   warp 9        TMA producer of the ring in the order of use (K_0, K_1, V_0,
 //                 K_2, ...), through the next segment's tiles without a stop
 //
-// Half tiles are 64 rows, so that one lies inside a page.  Only key tiles that
-// hold drafts, or that a window's edge may cut, are masked ("cut" tiles).  A row
+// A slab is one TMA box: KR = 128 rows (a whole tile of K or of V) where that is
+// 32 KB at most and, in a paged cache, pages are whole tiles; else 64 rows, so
+// that it lies inside a page.  (A box costs its issuing thread about 640 clocks
+// whatever its size: with 16 KB boxes that bound the kernel.)  Only key tiles
+// that hold drafts, or that a window's edge may cut, are masked ("cut" tiles).  A row
 // of V that not every query row sees may hold anything: 0 x NaN would reach the
 // rows that do not see it.  So in the cut tiles the softmax warps look through V
 // in shared memory, put zeros in the place of NaN and infinity, and make the rows
 // that do see such a value NaN.
 
-constexpr int kBM = 128, kBN = 128, kHalf = 64;
+constexpr int kBM = 128, kBN = 128;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kAttnThreads = 32 * (1 + kSoftmaxWarps + 1);
 constexpr float kRescale = 8.f;  // log2 units by which a score may exceed the reference maximum
@@ -274,6 +277,7 @@ struct TreeArgs {
     kvc_lengths len;
     int batch, q_heads, kv_heads, group, nodes;
     int row_tiles;  // ceil(group * nodes / 128)
+    int slab_rows;  // KR
     int window;
     float scale_log2;
     const float *cos_t, *sin_t;
@@ -283,9 +287,10 @@ struct TreeArgs {
     int32_t *status;
 };
 
-template <int D> struct TreeSmem {
+template <int D, int KR> struct TreeSmem {
     static constexpr int Q_BYTES = kBM * D * 2;
-    static constexpr int SLAB = kHalf * D * 2;
+    static constexpr int SLAB = KR * D * 2;
+    static constexpr int SPT = kBN / KR;  // slabs of a tile of K (or V)
     static constexpr int BUDGET = 227 * 1024;
     static constexpr int MISC = (2 * 12 + 8) * 8 + 16 + 4 * kBM * 4 + kMaxNodes * 2 + 16;
     static constexpr int FIT = (BUDGET - Q_BYTES - MISC) / SLAB;
@@ -298,7 +303,7 @@ template <int D> struct TreeSmem {
     static constexpr int DEPTH_OFF = RED_OFF + 4 * kBM * 4;  // int16 depths of the segment's nodes
     static constexpr int BAD_OFF = DEPTH_OFF + kMaxNodes * 2;
     static constexpr int TOTAL = BAD_OFF + 16;
-    static_assert(TOTAL <= BUDGET && NSLAB >= 4, "a tile of K and one of V must fit");
+    static_assert(TOTAL <= BUDGET && NSLAB >= 2 * SPT, "a tile of K and one of V must fit");
     static constexpr uint32_t COL_O = 0, COL_S = D, TMEM_COLS = 512;
 };
 
@@ -318,7 +323,7 @@ __device__ __forceinline__ int tree_tiles(const TreeArgs &a, int b, int &lo, uin
     if (bad)
         return 0;
     if (a.window > 0)
-        lo = max(0, P - a.window + 1) & ~(kHalf - 1);  // what a node of depth 0 sees
+        lo = max(0, P - a.window + 1) & ~(a.slab_rows - 1);  // what a node of depth 0 sees
     return (int)((T - lo + kBN - 1) / kBN);
 }
 
@@ -375,16 +380,16 @@ template <typename T> __device__ __forceinline__ uint32_t not_finite(uint32_t w)
     return __vcmpeq2(w & ex, ex);
 }
 
-template <typename T, int D>
+template <typename T, int D, int KR>
 __global__ void __launch_bounds__(kAttnThreads, 1)
 tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                  const TreeArgs a)
 {
-    using SM = TreeSmem<D>;
+    using SM = TreeSmem<D, KR>;
     using kvc_tc::wait_or_abort;
-    constexpr int NSLAB = SM::NSLAB;
+    constexpr int NSLAB = SM::NSLAB, SPT = SM::SPT;
     constexpr uint32_t AB = std::is_same<T, __half>::value ? 0u : 1u;
-    constexpr uint32_t IDESC_S = kvc_tc::f16_idesc(AB, 0, kBM, kHalf);
+    constexpr uint32_t IDESC_S = kvc_tc::f16_idesc(AB, 0, kBM, KR);
     constexpr uint32_t IDESC_O = kvc_tc::f16_idesc(AB, 1, kBM, D);
 
     extern __shared__ uint8_t smem_raw[];
@@ -455,12 +460,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         if (lane == 0) {
             kvc::tma_prefetch_desc(&tmap_k);
             kvc::tma_prefetch_desc(&tmap_v);
-            int q = 0;  // half tiles put into the ring so far
+            int q = 0;  // slabs put into the ring so far
             bool ok = true;
             while (ok && seg.next(a, row, n, lo, t0, t1)) {
                 const int b = seg.b, h = row / a.row_tiles;
                 const int64_t end = (int64_t)a.len.past_abs[b] + N;
-                for (int u = 0; ok && u < 4 * (t1 - t0); ++u, ++q) {
+                for (int u = 0; ok && u < 2 * SPT * (t1 - t0); ++u, ++q) {
                     const int slot = q % NSLAB;
                     if (q >= NSLAB && !wait_or_abort(&empty[slot], ((q / NSLAB) - 1) & 1, abort_flag, a.status)) {
                         ok = false;
@@ -468,8 +473,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                     }
                     bool is_v;
                     int tile;
-                    ring_group(u >> 1, t1 - t0, is_v, tile);
-                    const int64_t r = (int64_t)lo + (t0 + tile) * kBN + (u & 1) * kHalf;
+                    ring_group(u / SPT, t1 - t0, is_v, tile);
+                    const int64_t r = (int64_t)lo + (t0 + tile) * kBN + (u % SPT) * KR;
                     int64_t y = -1;
                     if (r < end) {
                         if (a.at.table) {
@@ -500,23 +505,23 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     } else if (warp == 0) {
         // ======================= MMA issuer =======================
         if (lane == 0) {
-            int q = 0, J = 0, s_no = 0;  // half tiles, tiles and segments taken so far
+            int q = 0, J = 0, s_no = 0;  // slabs, tiles and segments taken so far
             bool ok = true;
             const uint64_t q_desc = kvc_tc::sw128_desc(smem_base, 16);
             const uint64_t k_ring = kvc_tc::sw128_desc(smem_base + SM::RING_OFF, 16);
-            const uint64_t v_ring = kvc_tc::sw128_desc(smem_base + SM::RING_OFF, kHalf * 128);
+            const uint64_t v_ring = kvc_tc::sw128_desc(smem_base + SM::RING_OFF, KR * 128);
             auto issue_s = [&](int buf) -> bool {
-                for (int hf = 0; hf < 2; ++hf, ++q) {
+                for (int hf = 0; hf < SPT; ++hf, ++q) {
                     const int slot = q % NSLAB;
                     if (!wait_or_abort(&full[slot], (q / NSLAB) & 1, abort_flag, a.status))
                         return false;
                     kvc_tc::fence_after();
                     const uint64_t kd = k_ring + (uint64_t)(slot * (SM::SLAB / 16));
-                    const uint32_t d_s = tmem + SM::COL_S + buf * kBN + hf * kHalf;
+                    const uint32_t d_s = tmem + SM::COL_S + buf * kBN + hf * KR;
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks)
                         kvc_tc::mma_ss(d_s, q_desc + (uint64_t)(((ks >> 2) * (kBM * 128) + (ks & 3) * 32) / 16),
-                                       kd + (uint64_t)(((ks >> 2) * (kHalf * 128) + (ks & 3) * 32) / 16), IDESC_S, ks > 0);
+                                       kd + (uint64_t)(((ks >> 2) * (KR * 128) + (ks & 3) * 32) / 16), IDESC_S, ks > 0);
                     kvc_tc::commit(&empty[slot]);
                 }
                 kvc_tc::commit(&s_full[buf]);
@@ -533,15 +538,15 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                     if (!(ok = wait_or_abort(&p_full[s], (J >> 1) & 1, abort_flag, a.status)))
                         break;
                     kvc_tc::fence_after();
-                    for (int hf = 0; hf < 2; ++hf, ++q) {
+                    for (int hf = 0; hf < SPT; ++hf, ++q) {
                         const int slot = q % NSLAB;
                         if (!(ok = wait_or_abort(&full[slot], (q / NSLAB) & 1, abort_flag, a.status)))
                             break;
                         kvc_tc::fence_after();
                         const uint64_t vd = v_ring + (uint64_t)(slot * (SM::SLAB / 16));
-                        const uint32_t pa = tmem + SM::COL_S + s * kBN + hf * (kHalf / 2);
+                        const uint32_t pa = tmem + SM::COL_S + s * kBN + hf * (KR / 2);
 #pragma unroll
-                        for (int k2 = 0; k2 < kHalf / 16; ++k2)
+                        for (int k2 = 0; k2 < KR / 16; ++k2)
                             kvc_tc::mma_ts(tmem + SM::COL_O, pa + k2 * 8, vd + (uint64_t)(k2 * (2048 / 16)), IDESC_O,
                                            j > 0 || hf > 0 || k2 > 0);
                         kvc_tc::commit(&empty[slot]);
@@ -569,7 +574,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         uint32_t *bad_sh = reinterpret_cast<uint32_t *>(smem + SM::BAD_OFF);
         constexpr uint32_t all_bar = 1;
         const int words = (N + 31) / 32;
-        int q0 = 0, J = 0;  // half tiles before the segment, tiles so far
+        int q0 = 0, J = 0;  // slabs before the segment, tiles so far
         // `ok` is the warp's own; the softmax warps leave their loops together, at a barrier
         bool ok = true, stop = false;
         for (int s_no = 0; seg.next(a, row, n, lo, t0, t1); ++s_no) {
@@ -694,8 +699,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                 const bool cut = t_lo + kBN > P || (a.window > 0 && t_lo < P + N - a.window);
                 uint64_t bad[2] = {0, 0};  // V rows of the tile in which this thread found one not finite
                 if (cut && ok) {
-                    for (int hf = 0; hf < 2; ++hf) {
-                        const int qi = q0 + 2 * v_group(j, nt) + hf;
+#pragma unroll
+                    for (int hf = 0; hf < SPT; ++hf) {
+                        const int qi = q0 + SPT * v_group(j, nt) + hf;
                         if (!(ok = wait_or_abort(&full[qi % NSLAB], (qi / NSLAB) & 1, abort_flag, a.status)))
                             break;
                         uint4 *v = reinterpret_cast<uint4 *>(smem + SM::RING_OFF + (qi % NSLAB) * SM::SLAB);
@@ -707,7 +713,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                                                         not_finite<T>(x.w));
                             if (nf.x | nf.y | nf.z | nf.w) {
                                 v[at] = make_uint4(x.x & ~nf.x, x.y & ~nf.y, x.z & ~nf.z, x.w & ~nf.w);
-                                bad[hf] |= 1ull << ((at >> 3) & 63);
+                                const int row = hf * KR + ((at >> 3) & (KR - 1));
+                                bad[row >> 6] |= 1ull << (row & 63);
                             }
                         }
                     }
@@ -831,7 +838,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
             }
             if (stop)
                 break;
-            q0 += 4 * nt;
+            q0 += 2 * SPT * nt;
 
             // ---- output rows ----
             // (every MMA of the segment has completed after this wait: Q and O may be used)
@@ -964,17 +971,17 @@ tree_merge_kernel(const TreeArgs a)
             kvc::Elem<T>::from_f32(sum == 0.f ? 0.f : acc[e] / sum);
 }
 
-template <typename T, int D>
+template <typename T, int D, int KR>
 kvc_status launch_attn_dim(const TreeArgs &a, const void *k, const void *v, cudaStream_t stream)
 {
-    using SM = TreeSmem<D>;
+    using SM = TreeSmem<D, KR>;
     const CUtensorMapDataType tt = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                                   : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const uint64_t rows = (a.at.table ? (uint64_t)a.at.n_pool * a.at.page_size : (uint64_t)a.batch * a.at.rows) *
                           a.kv_heads;
     CUtensorMap tk, tv;
-    if (!kvc_host::encode_3d_sw128(&tk, k, rows, D, kHalf, D / 64, tt) ||
-        !kvc_host::encode_3d_sw128(&tv, v, rows, D, kHalf, D / 64, tt))
+    if (!kvc_host::encode_3d_sw128(&tk, k, rows, D, KR, D / 64, tt) ||
+        !kvc_host::encode_3d_sw128(&tv, v, rows, D, KR, D / 64, tt))
         return KVC_ERR_CUDA;
     int dev = 0, optin = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -983,7 +990,7 @@ kvc_status launch_attn_dim(const TreeArgs &a, const void *k, const void *v, cuda
     const size_t smem = std::min<size_t>((size_t)SM::TOTAL + 1024, (size_t)optin);
     if (smem < (size_t)SM::TOTAL)
         return KVC_ERR_UNSUPPORTED;
-    auto kern = tree_attn_kernel<T, D>;
+    auto kern = tree_attn_kernel<T, D, KR>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return KVC_ERR_CUDA;
     kern<<<a.grid, kAttnThreads, smem, stream>>>(tk, tv, a);
@@ -1004,11 +1011,18 @@ kvc_status launch_attn_dim(const TreeArgs &a, const void *k, const void *v, cuda
 }
 
 template <typename T>
-kvc_status launch_attn(const TreeArgs &a, const void *k, const void *v, int D, cudaStream_t stream)
+kvc_status launch_attn(TreeArgs &a, const void *k, const void *v, int D, cudaStream_t stream)
 {
-    return D == 64    ? launch_attn_dim<T, 64>(a, k, v, stream)
-           : D == 128 ? launch_attn_dim<T, 128>(a, k, v, stream)
-                      : launch_attn_dim<T, 256>(a, k, v, stream);
+    const bool whole = D <= 128 && (!a.at.table || a.at.page_size % kBN == 0);
+    a.slab_rows = whole ? kBN : 64;
+    switch (D) {
+    case 64:
+        return whole ? launch_attn_dim<T, 64, 128>(a, k, v, stream) : launch_attn_dim<T, 64, 64>(a, k, v, stream);
+    case 128:
+        return whole ? launch_attn_dim<T, 128, 128>(a, k, v, stream) : launch_attn_dim<T, 128, 64>(a, k, v, stream);
+    default:
+        return launch_attn_dim<T, 256, 64>(a, k, v, stream);
+    }
 }
 
 // sizes that the calls on the cache's rows share; rows_out: rows a sequence may have
