@@ -242,30 +242,38 @@ tree_commit_kernel(const CommitArgs a)
 // row, kv head), in tiles of 128: row m is head m / N, node m % N, as they lie
 // in memory.  Each (batch row, kv head, row tile) streams its keys past the
 // tensor cores in tiles of 128, and every CTA (one an SM) takes the same number
-// of key tiles, whatever the lengths (kvc_flat.cuh); rows that several CTAs
-// worked on are joined by tree_merge_kernel.
+// of key tiles, whatever the lengths (kvc_flat.cuh), in segments of one row
+// each; rows that several CTAs worked on are joined by tree_merge_kernel.
 //
+//   tree_prep_kernel  the queries rotated at their positions, and for each node
+//                     the drafts that it sees (mask, window and absences in one)
 //   TMEM columns  O [0, D) fp32 | S / P double buffer [D, D + 256)
 //   shared        Q (128 x D, 128-byte swizzled) | ring of slabs of 64 or 128 rows
 //   warp 0        issues tcgen05.mma in the order S_0, S_1, PV_0, S_2, PV_1, ...
-//   warps 1-8     query rows in, softmax, output rows out: two threads a row
-//                 (= TMEM lane), each half of the columns
+//   warps 1-8     softmax and output: two threads a row (= TMEM lane), each half
+//                 of the columns
 //   warp 9        TMA producer of the ring in the order of use (K_0, K_1, V_0,
 //                 K_2, ...), through the next segment's tiles without a stop
+//   warp 10       TMA of the next segment's queries once this one's last scores
+//                 have been issued and are done
+// so that from one segment to the next the stream of keys does not stop: while
+// the softmax warps write one segment's output, the next one's first scores are
+// on their way.  (With the queries loaded and rotated by the softmax warps
+// between segments, each segment cost 22,000 clocks, as much as ten tiles.)
 //
 // A slab is one TMA box: KR = 128 rows (a whole tile of K or of V) where that is
 // 32 KB at most and, in a paged cache, pages are whole tiles; else 64 rows, so
 // that it lies inside a page.  (A box costs its issuing thread about 640 clocks
 // whatever its size: with 16 KB boxes that bound the kernel.)  Only key tiles
-// that hold drafts, or that a window's edge may cut, are masked ("cut" tiles).  A row
-// of V that not every query row sees may hold anything: 0 x NaN would reach the
-// rows that do not see it.  So in the cut tiles the softmax warps look through V
-// in shared memory, put zeros in the place of NaN and infinity, and make the rows
-// that do see such a value NaN.
+// that hold drafts, or that a window's edge may cut, are masked ("cut" tiles).  A
+// row of V that not every query row sees may hold anything: 0 x NaN would reach
+// the rows that do not see it.  So in the cut tiles the softmax warps look
+// through V in shared memory, put zeros in the place of NaN and infinity, and
+// make the rows that do see such a value NaN.
 
 constexpr int kBM = 128, kBN = 128;
 constexpr int kSoftmaxWarps = 8;
-constexpr int kAttnThreads = 32 * (1 + kSoftmaxWarps + 1);
+constexpr int kAttnThreads = 32 * (1 + kSoftmaxWarps + 2);
 constexpr float kRescale = 8.f;  // log2 units by which a score may exceed the reference maximum
 
 struct TreeArgs {
@@ -284,6 +292,8 @@ struct TreeArgs {
     int64_t rope_max_pos;
     int grid;
     float *ws_o, *ws_m, *ws_l;  // [2 * grid][128] (x D)
+    void *ws_q;                 // rotated queries, as q
+    uint32_t *see;              // drafts that each node sees, as mask
     int32_t *status;
 };
 
@@ -292,28 +302,30 @@ template <int D, int KR> struct TreeSmem {
     static constexpr int SLAB = KR * D * 2;
     static constexpr int SPT = kBN / KR;  // slabs of a tile of K (or V)
     static constexpr int BUDGET = 227 * 1024;
-    static constexpr int MISC = (2 * 12 + 8) * 8 + 16 + 4 * kBM * 4 + kMaxNodes * 2 + 16;
+    static constexpr int NBAR = 9;        // beside the ring's
+    static constexpr int MISC = (2 * 12 + NBAR) * 8 + 16 + 4 * kBM * 4 + 16;
     static constexpr int FIT = (BUDGET - Q_BYTES - MISC) / SLAB;
     static constexpr int NSLAB = FIT < 12 ? FIT : 12;
     static constexpr int RING_OFF = Q_BYTES;
     static constexpr int BAR_OFF = RING_OFF + NSLAB * SLAB;
-    // full[NSLAB], empty[NSLAB], s_full[2], p_full[2], o_done[2], q_full, drain
-    static constexpr int MISC_OFF = BAR_OFF + (2 * NSLAB + 8) * 8;
-    static constexpr int RED_OFF = MISC_OFF + 16;            // row maximum / sum exchange
-    static constexpr int DEPTH_OFF = RED_OFF + 4 * kBM * 4;  // int16 depths of the segment's nodes
-    static constexpr int BAD_OFF = DEPTH_OFF + kMaxNodes * 2;
+    // full[NSLAB], empty[NSLAB], s_full[2], p_full[2], o_done[2], q_full, q_empty, drain
+    static constexpr int MISC_OFF = BAR_OFF + (2 * NSLAB + NBAR) * 8;
+    static constexpr int RED_OFF = (MISC_OFF + 8 + 15) / 16 * 16;  // row maximum / sum exchange
+    static constexpr int BAD_OFF = RED_OFF + 4 * kBM * 4;
     static constexpr int TOTAL = BAD_OFF + 16;
     static_assert(TOTAL <= BUDGET && NSLAB >= 2 * SPT, "a tile of K and one of V must fit");
     static constexpr uint32_t COL_O = 0, COL_S = D, TMEM_COLS = 512;
 };
 
-// first key row of batch row b's tiles and their number (0: nothing to do)
-__device__ __forceinline__ int tree_tiles(const TreeArgs &a, int b, int &lo, uint32_t &bad)
+// batch row b: its past length, first key row of its tiles and their number (0:
+// nothing to do)
+__device__ __forceinline__ int tree_tiles(const TreeArgs &a, int b, int &P, int &lo, uint32_t &bad)
 {
-    const int P = a.len.past_abs[b];
+    P = a.len.past_abs[b];
+    const int L = a.len.cache_total[b];
     bad = 0;
     lo = 0;
-    if (a.len.cache_total[b] < 0 || P < 0)
+    if (L < 0 || P < 0)
         return 0;
     const int64_t T = (int64_t)P + a.nodes;
     if (a.cos_t && T > a.rope_max_pos)
@@ -327,26 +339,36 @@ __device__ __forceinline__ int tree_tiles(const TreeArgs &a, int b, int &lo, uin
     return (int)((T - lo + kBN - 1) / kBN);
 }
 
-// The segments of a CTA's share: tiles [t0, t1) of the n tiles of line row
-// (b, head, row tile).
-struct Segments {
-    int x, x_end, b, base;
-    __device__ __forceinline__ bool next(const TreeArgs &a, int &row, int &n, int &lo, int &t0, int &t1)
+// The segments of a CTA's share, one at a time: tiles [t0, t1) of the n tiles of
+// line row (b, head, row tile).
+struct Segment {
+    int b, row, P, lo, n, t0, t1;
+};
+struct Walk {
+    int x, x_end, b, base, P, lo, n;
+    __device__ __forceinline__ void load(const TreeArgs &a)
+    {
+        uint32_t bad;
+        n = tree_tiles(a, b, P, lo, bad);
+    }
+    __device__ __forceinline__ bool next(const TreeArgs &a, Segment &s)
     {
         if (x >= x_end)
             return false;
-        uint32_t bad;
         const int rows = a.kv_heads * a.row_tiles;
-        n = tree_tiles(a, b, lo, bad);
         while (x >= base + n * rows) {
             base += n * rows;
             ++b;
-            n = tree_tiles(a, b, lo, bad);
+            load(a);
         }
-        row = (x - base) / n;
-        t0 = (x - base) - row * n;
-        t1 = min(n, t0 + (x_end - x));
-        x += t1 - t0;
+        s.b = b;
+        s.P = P;
+        s.lo = lo;
+        s.n = n;
+        s.row = (x - base) / n;
+        s.t0 = (x - base) - s.row * n;
+        s.t1 = min(n, s.t0 + (x_end - x));
+        x += s.t1 - s.t0;
         return true;
     }
 };
@@ -380,10 +402,78 @@ template <typename T> __device__ __forceinline__ uint32_t not_finite(uint32_t w)
     return __vcmpeq2(w & ex, ex);
 }
 
+// Blocks [0, q_blocks): eight rotation pairs of a query row a thread.  The others:
+// a word of a node's drafts a thread.
+template <typename T>
+__global__ void __launch_bounds__(256)
+tree_prep_kernel(const TreeArgs a, int D, unsigned q_blocks)
+{
+    kvc::grid_dep_launch();
+    const int N = a.nodes;
+    if (blockIdx.x < q_blocks) {
+        const int pieces = D / 16;
+        const int64_t w = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+        const int64_t row = w / pieces;
+        const int c0 = (int)(w % pieces) * 8;
+        if (row >= (int64_t)a.batch * a.q_heads * N)
+            return;
+        const int b = (int)(row / ((int64_t)a.q_heads * N));
+        const int d = __ldg(a.depth + (int64_t)b * N + row % N);
+        const T *q = static_cast<const T *>(a.q) + row * D + c0;
+        uint4 lo = __ldg(reinterpret_cast<const uint4 *>(q)), hi = __ldg(reinterpret_cast<const uint4 *>(q + D / 2));
+        int P, first;
+        uint32_t bad;
+        if (tree_tiles(a, b, P, first, bad) == 0 || d < 0 || d >= N)
+            return;  // never looked at
+        const int64_t at = ((int64_t)P + d) * (D / 2) + c0;
+        float cs[8], sn[8];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float4 x = __ldg(reinterpret_cast<const float4 *>(a.cos_t + at) + e);
+            const float4 y = __ldg(reinterpret_cast<const float4 *>(a.sin_t + at) + e);
+            cs[4 * e] = x.x, cs[4 * e + 1] = x.y, cs[4 * e + 2] = x.z, cs[4 * e + 3] = x.w;
+            sn[4 * e] = y.x, sn[4 * e + 1] = y.y, sn[4 * e + 2] = y.z, sn[4 * e + 3] = y.w;
+        }
+        T *x = reinterpret_cast<T *>(&lo), *y = reinterpret_cast<T *>(&hi);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float u = kvc::Elem<T>::to_f32(x[e]), v = kvc::Elem<T>::to_f32(y[e]);
+            kvc::rope_pair(u, v, cs[e], sn[e]);
+            x[e] = kvc::Elem<T>::from_f32(u);
+            y[e] = kvc::Elem<T>::from_f32(v);
+        }
+        T *to = static_cast<T *>(a.ws_q) + row * D + c0;
+        *reinterpret_cast<uint4 *>(to) = lo;
+        *reinterpret_cast<uint4 *>(to + D / 2) = hi;
+        return;
+    }
+    const int words = (N + 31) / 32;
+    const int64_t w = (int64_t)(blockIdx.x - q_blocks) * blockDim.x + threadIdx.x;
+    if (w >= (int64_t)a.batch * N * words)
+        return;
+    const int64_t row = w / words;
+    const int b = (int)(row / N), j0 = (int)(w % words) * 32;
+    const int32_t *depth = a.depth + (int64_t)b * N;
+    const int d = __ldg(depth + row % N);
+    uint32_t left = a.mask[w], bits = 0;
+    if (d >= N && j0 == 0)
+        kvc::raise_status(a.status, KVC_DEV_INDEX_OOB);
+    if (d < 0 || d >= N)
+        left = 0;
+    while (left) {
+        const int c = __ffs(left) - 1;
+        left &= left - 1;
+        const int dj = j0 + c < N ? __ldg(depth + j0 + c) : -1;
+        if (dj >= 0 && dj < N && (a.window <= 0 || d - dj < a.window))
+            bits |= 1u << c;
+    }
+    a.see[w] = bits;
+}
+
 template <typename T, int D, int KR>
 __global__ void __launch_bounds__(kAttnThreads, 1)
-tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
-                 const TreeArgs a)
+tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                 const __grid_constant__ CUtensorMap tmap_v, const TreeArgs a)
 {
     using SM = TreeSmem<D, KR>;
     using kvc_tc::wait_or_abort;
@@ -406,30 +496,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     }
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + SM::BAR_OFF), *empty = full + NSLAB,
              *s_full = full + 2 * NSLAB, *p_full = s_full + 2, *o_done = s_full + 4, *q_full = s_full + 6,
-             *drain = s_full + 7;
+             *q_empty = s_full + 7, *drain = s_full + 8;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + SM::MISC_OFF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + SM::MISC_OFF + 4);
 
     kvc::grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int N = a.nodes, rows = a.group * N, line_rows = a.kv_heads * a.row_tiles;
-    auto count = [&](int b) {
-        int lo;
-        uint32_t bad;
-        const int n = tree_tiles(a, b, lo, bad);
-        if (bad && blockIdx.x == 0 && warp == 0)
-            kvc::raise_status(a.status, bad);
-        return n;
-    };
-    Segments seg;
-    const int U = kvc_flat::locate(a.batch, line_rows, count, -1, seg.b, seg.base);
-    const kvc_flat::Shares shares(U, a.grid);
-    seg.x = shares.begin(blockIdx.x);
-    seg.x_end = shares.begin(blockIdx.x + 1);
-    if (seg.x >= seg.x_end)
-        return;
-    kvc_flat::row_of(a.batch, line_rows, count, seg.x, seg.b, seg.base);
-
     if (threadIdx.x == 0) {
         for (int i = 0; i < NSLAB; ++i) {
             kvc::mbar_init(&full[i], 1);
@@ -440,7 +512,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
             kvc::mbar_init(&p_full[i], kSoftmaxWarps);
             kvc::mbar_init(&o_done[i], 1);
         }
-        kvc::mbar_init(q_full, kSoftmaxWarps);
+        kvc::mbar_init(q_full, 1);
+        kvc::mbar_init(q_empty, 1);
         kvc::mbar_init(drain, 1);
         *abort_flag = 0;
         kvc::fence_mbar_init();
@@ -449,23 +522,48 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         kvc_tc::tmem_alloc(tmem_slot, SM::TMEM_COLS);
         kvc_tc::fence_before();
     }
+    const int N = a.nodes, rows = a.group * N, line_rows = a.kv_heads * a.row_tiles;
+    Walk walk;
+    {
+        auto count = [&](int b) {
+            int P, lo;
+            uint32_t bad;
+            const int n = tree_tiles(a, b, P, lo, bad);
+            if (bad && blockIdx.x == 0 && warp == 0)
+                kvc::raise_status(a.status, bad);
+            return n;
+        };
+        const int U = kvc_flat::locate(a.batch, line_rows, count, -1, walk.b, walk.base);
+        const kvc_flat::Shares shares(U, a.grid);
+        walk.x = shares.begin(blockIdx.x);
+        walk.x_end = shares.begin(blockIdx.x + 1);
+        // (a CTA without a share falls through its loops)
+        if (walk.x < walk.x_end) {
+            kvc_flat::row_of(a.batch, line_rows, count, walk.x, walk.b, walk.base);
+            walk.load(a);
+        }
+    }
     __syncthreads();
     kvc_tc::fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t smem_base = kvc::smem_u32(smem);
-    int row, n, lo, t0, t1;  // the segment: line row, its tiles, first key row, own tiles
+    // each role looks one segment ahead, so that the lengths are there when it gets to it
+    Segment cur, nxt;
+    bool more = walk.next(a, cur);
 
     if (warp == 1 + kSoftmaxWarps) {
-        // ======================= TMA producer =======================
+        // ======================= TMA producer of K and V =======================
+        // (the cache's rows are those of the kernels before tree_prep_kernel: no wait for it)
         if (lane == 0) {
             kvc::tma_prefetch_desc(&tmap_k);
             kvc::tma_prefetch_desc(&tmap_v);
             int q = 0;  // slabs put into the ring so far
             bool ok = true;
-            while (ok && seg.next(a, row, n, lo, t0, t1)) {
-                const int b = seg.b, h = row / a.row_tiles;
-                const int64_t end = (int64_t)a.len.past_abs[b] + N;
-                for (int u = 0; ok && u < 2 * SPT * (t1 - t0); ++u, ++q) {
+            while (ok && more) {
+                const int h = cur.row / a.row_tiles, nt = cur.t1 - cur.t0;
+                const int64_t end = (int64_t)cur.P + N;
+                bool again = false;
+                for (int u = 0; u < 2 * SPT * nt; ++u, ++q) {
                     const int slot = q % NSLAB;
                     if (q >= NSLAB && !wait_or_abort(&empty[slot], ((q / NSLAB) - 1) & 1, abort_flag, a.status)) {
                         ok = false;
@@ -473,44 +571,65 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                     }
                     bool is_v;
                     int tile;
-                    ring_group(u / SPT, t1 - t0, is_v, tile);
-                    const int64_t r = (int64_t)lo + (t0 + tile) * kBN + (u % SPT) * KR;
+                    ring_group(u / SPT, nt, is_v, tile);
+                    const int64_t r = (int64_t)cur.lo + (cur.t0 + tile) * kBN + (u % SPT) * KR;
                     int64_t y = -1;
                     if (r < end) {
                         if (a.at.table) {
-                            const int64_t id = __ldg(a.at.table + (int64_t)b * a.at.max_pages + r / a.at.page_size);
+                            const int64_t id = __ldg(a.at.table + (int64_t)cur.b * a.at.max_pages + r / a.at.page_size);
                             if (id >= 0 && id < a.at.n_pool)
                                 y = (id * a.kv_heads + h) * a.at.page_size + r % a.at.page_size;
                             else
                                 kvc::raise_status(a.status, KVC_DEV_INDEX_OOB);
                         } else {
-                            y = ((int64_t)b * a.kv_heads + h) * a.at.rows + r;
+                            y = ((int64_t)cur.b * a.kv_heads + h) * a.at.rows + r;
                         }
                     }
                     if (y < 0) {
                         // nothing to read: the slot keeps what it holds, and its columns are masked
                         kvc::mbar_arrive(&full[slot]);
-                        continue;
+                    } else {
+                        kvc::mbar_arrive_expect_tx(&full[slot], SM::SLAB);
+                        kvc::tma_load_3d(smem + SM::RING_OFF + slot * SM::SLAB, is_v ? &tmap_v : &tmap_k, 0, (int32_t)y,
+                                         0, &full[slot]);
                     }
-                    kvc::mbar_arrive_expect_tx(&full[slot], SM::SLAB);
-                    kvc::tma_load_3d(smem + SM::RING_OFF + slot * SM::SLAB, is_v ? &tmap_v : &tmap_k, 0, (int32_t)y, 0,
-                                     &full[slot]);
+                    if (u == 0)
+                        again = walk.next(a, nxt);
                 }
+                cur = nxt;
+                more = again;
             }
             if (*abort_flag)
                 // wind-down: let the loads in flight land before the CTA exits
                 for (int i = max(0, q - NSLAB); i < q; ++i)
                     kvc::mbar_wait(&full[i % NSLAB], (i / NSLAB) & 1);
         }
+    } else if (warp == 2 + kSoftmaxWarps) {
+        // ======================= TMA of the queries =======================
+        if (lane == 0) {
+            kvc::tma_prefetch_desc(&tmap_q);
+            kvc::grid_dep_wait();  // tree_prep_kernel's
+            int s_no = 0;
+            for (; more; ++s_no) {
+                if (s_no > 0 && !wait_or_abort(q_empty, (s_no - 1) & 1, abort_flag, a.status))
+                    break;
+                const int h = cur.row / a.row_tiles, mt = cur.row % a.row_tiles;
+                kvc::mbar_arrive_expect_tx(q_full, SM::Q_BYTES);
+                kvc::tma_load_3d(smem, &tmap_q, 0, (cur.b * a.kv_heads + h) * rows + mt * kBM, 0, q_full);
+                more = walk.next(a, cur);
+            }
+            if (*abort_flag && s_no > 0)
+                kvc::mbar_wait(q_full, (s_no - 1) & 1);
+        }
     } else if (warp == 0) {
         // ======================= MMA issuer =======================
         if (lane == 0) {
-            int q = 0, J = 0, s_no = 0;  // slabs, tiles and segments taken so far
+            int q = 0, J = 0;  // slabs and tiles taken so far
             bool ok = true;
             const uint64_t q_desc = kvc_tc::sw128_desc(smem_base, 16);
             const uint64_t k_ring = kvc_tc::sw128_desc(smem_base + SM::RING_OFF, 16);
             const uint64_t v_ring = kvc_tc::sw128_desc(smem_base + SM::RING_OFF, KR * 128);
-            auto issue_s = [&](int buf) -> bool {
+            auto issue_s = [&](int buf, bool last) -> bool {
                 for (int hf = 0; hf < SPT; ++hf, ++q) {
                     const int slot = q % NSLAB;
                     if (!wait_or_abort(&full[slot], (q / NSLAB) & 1, abort_flag, a.status))
@@ -525,14 +644,17 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                     kvc_tc::commit(&empty[slot]);
                 }
                 kvc_tc::commit(&s_full[buf]);
+                if (last)
+                    kvc_tc::commit(q_empty);  // the segment's last scores: its queries have been read
                 return true;
             };
-            while (ok && seg.next(a, row, n, lo, t0, t1)) {
-                const int nt = t1 - t0;
+            for (int s_no = 0; ok && more; ++s_no) {
+                const int nt = cur.t1 - cur.t0;
                 ok = wait_or_abort(q_full, s_no & 1, abort_flag, a.status);
                 kvc_tc::fence_after();
                 for (int j = 0; ok && j < 2 && j < nt; ++j)
-                    ok = issue_s((J + j) & 1);
+                    ok = issue_s((J + j) & 1, j == nt - 1);
+                more = walk.next(a, nxt);
                 for (int j = 0; ok && j < nt; ++j, ++J) {
                     const int s = J & 1;
                     if (!(ok = wait_or_abort(&p_full[s], (J >> 1) & 1, abort_flag, a.status)))
@@ -555,9 +677,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                         break;
                     kvc_tc::commit(&o_done[s]);
                     if (j + 2 < nt)
-                        ok = issue_s(s);
+                        ok = issue_s(s, j + 2 == nt - 1);
                 }
-                ++s_no;
+                cur = nxt;
             }
             // everything issued above has completed once this arrives
             kvc_tc::commit(drain);
@@ -570,133 +692,69 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         const int m = quad * 32 + lane;
         const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
         float *red = reinterpret_cast<float *>(smem + SM::RED_OFF);
-        int16_t *depth_sh = reinterpret_cast<int16_t *>(smem + SM::DEPTH_OFF);
         uint32_t *bad_sh = reinterpret_cast<uint32_t *>(smem + SM::BAD_OFF);
         constexpr uint32_t all_bar = 1;
         const int words = (N + 31) / 32;
-        int q0 = 0, J = 0;  // slabs before the segment, tiles so far
+        const float c_log2 = fabsf(a.scale_log2);
+        // this thread's row of a segment: its node's depth (-1: absent, or no row)
+        auto row_depth = [&](const Segment &sg) {
+            const int r = sg.row % a.row_tiles * kBM + m;
+            return r < rows ? __ldg(a.depth + (int64_t)sg.b * N + r % N) : -1;
+        };
+        int d_next = more ? row_depth(cur) : -1;
+        kvc::grid_dep_wait();  // tree_prep_kernel's
+        int q0 = 0, J = 0;     // slabs before the segment, tiles so far
         // `ok` is the warp's own; the softmax warps leave their loops together, at a barrier
         bool ok = true, stop = false;
-        for (int s_no = 0; seg.next(a, row, n, lo, t0, t1); ++s_no) {
-            const int b = seg.b, h = row / a.row_tiles, mt = row % a.row_tiles, nt = t1 - t0;
-            const int P = a.len.past_abs[b];
-            const int64_t q_row0 = ((int64_t)b * a.kv_heads + h) * rows + (int64_t)mt * kBM;
-            const int32_t *depth = a.depth + (int64_t)b * N;
-
-            // ---- query rows: rotated at P + depth, into the MMA's layout ----
-            // (a negative scale goes into the query's sign, so that larger is nearer below)
-            {
-                constexpr int PPL = D / 64, RW = kBM / kSoftmaxWarps;  // rotation pairs a lane, rows a warp
-                constexpr int STEP = D == 256 ? 4 : 8;                 // rows in flight
-                struct alignas(2 * PPL) QV { T e[PPL]; };
-                const int c0 = PPL * lane, c1 = c0 + D / 2;
-                const float sign = a.scale_log2 < 0.f ? -1.f : 1.f;
-                const T *q = static_cast<const T *>(a.q) + q_row0 * D + c0;
-                int node = (mt * kBM + sw * RW) % N;
-#pragma unroll 1
-                for (int u0 = sw * RW; u0 < (sw + 1) * RW; u0 += STEP) {
-                    // Every load is of an address inside its array, wanted or not, so that none waits for
-                    // another but the tables' for the depths: rows past the last are the last again,
-                    // depths outside [0, N) are moved inside
-                    int dv[STEP];
-                    bool there[STEP];
-#pragma unroll
-                    for (int u = 0; u < STEP; ++u) {
-                        dv[u] = __ldg(depth + node);
-                        node = node + 1 == N ? 0 : node + 1;
-                    }
-                    uint32_t qr[2][STEP][PPL == 4 ? 2 : 1];
-#pragma unroll
-                    for (int u = 0; u < STEP; ++u) {
-                        const int64_t at = (int64_t)min(u0 + u, rows - 1 - mt * kBM) * D;
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const T *from = q + at + e * (D / 2);
-                            if constexpr (PPL == 4) {
-                                const uint2 x = __ldg(reinterpret_cast<const uint2 *>(from));
-                                qr[e][u][0] = x.x;
-                                qr[e][u][1] = x.y;
-                            } else if constexpr (PPL == 2) {
-                                qr[e][u][0] = __ldg(reinterpret_cast<const uint32_t *>(from));
-                            } else {
-                                qr[e][u][0] = __ldg(reinterpret_cast<const unsigned short *>(from));
-                            }
-                        }
-                    }
-                    float cv[STEP][PPL], sv[STEP][PPL];
-#pragma unroll
-                    for (int u = 0; u < STEP; ++u) {
-                        there[u] = mt * kBM + u0 + u < rows && dv[u] >= 0 && dv[u] < N;
-                        const int64_t o = ((int64_t)P + min(max(dv[u], 0), N - 1)) * (D / 2) + c0;
-#pragma unroll
-                        for (int e = 0; e < PPL; ++e) {
-                            cv[u][e] = 1.f;
-                            sv[u][e] = 0.f;
-                        }
-                        if (a.cos_t) {
-                            if constexpr (PPL == 4) {
-                                const float4 x = __ldg(reinterpret_cast<const float4 *>(a.cos_t + o));
-                                const float4 y = __ldg(reinterpret_cast<const float4 *>(a.sin_t + o));
-                                cv[u][0] = x.x, cv[u][1] = x.y, cv[u][2] = x.z, cv[u][3] = x.w;
-                                sv[u][0] = y.x, sv[u][1] = y.y, sv[u][2] = y.z, sv[u][3] = y.w;
-                            } else if constexpr (PPL == 2) {
-                                const float2 x = __ldg(reinterpret_cast<const float2 *>(a.cos_t + o));
-                                const float2 y = __ldg(reinterpret_cast<const float2 *>(a.sin_t + o));
-                                cv[u][0] = x.x, cv[u][1] = x.y;
-                                sv[u][0] = y.x, sv[u][1] = y.y;
-                            } else {
-                                cv[u][0] = __ldg(a.cos_t + o);
-                                sv[u][0] = __ldg(a.sin_t + o);
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int u = 0; u < STEP; ++u) {
-                        QV out[2];
-#pragma unroll
-                        for (int e = 0; e < PPL; ++e) {
-                            const T *xl = reinterpret_cast<const T *>(qr[0][u]), *xh = reinterpret_cast<const T *>(qr[1][u]);
-                            float x = kvc::Elem<T>::to_f32(xl[e]), y = kvc::Elem<T>::to_f32(xh[e]);
-                            if (a.cos_t)
-                                kvc::rope_pair(x, y, cv[u][e], sv[u][e]);
-                            out[0].e[e] = kvc::Elem<T>::from_f32(there[u] ? x * sign : 0.f);
-                            out[1].e[e] = kvc::Elem<T>::from_f32(there[u] ? y * sign : 0.f);
-                        }
-                        *reinterpret_cast<QV *>(smem + (c0 >> 6) * (kBM * 128) + kvc::sw128(u0 + u, (c0 & 63) >> 3) +
-                                                (c0 & 7) * 2) = out[0];
-                        *reinterpret_cast<QV *>(smem + (c1 >> 6) * (kBM * 128) + kvc::sw128(u0 + u, (c1 & 63) >> 3) +
-                                                (c1 & 7) * 2) = out[1];
-                    }
-                }
-            }
-            for (int i = tid; i < N; i += 32 * kSoftmaxWarps) {
-                const int d = depth[i];
-                depth_sh[i] = (int16_t)(d >= 0 && d < N ? d : -1);
-                if (d >= N)
-                    kvc::raise_status(a.status, KVC_DEV_INDEX_OOB);
-            }
-            kvc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                kvc::mbar_arrive(q_full);
-            kvc_tc::named_bar_sync(all_bar, 32 * kSoftmaxWarps);  // the depths are there
-
-            // ---- this thread's row ----
+        for (int s_no = 0; more; ++s_no) {
+            const int mt = cur.row % a.row_tiles, h = cur.row / a.row_tiles, nt = cur.t1 - cur.t0;
+            const int P = cur.P;
             const int r = mt * kBM + m;
             const bool active = mt * kBM + quad * 32 < rows;  // of the warp: it has rows at all
-            const int node = r % N;
-            const int d = r < rows ? depth_sh[node] : -1;
-            const uint32_t *mask = a.mask + ((int64_t)b * N + node) * words;
+            const int d = d_next >= 0 && d_next < N ? d_next : -1;
+            const uint32_t *see_words = a.see + ((int64_t)cur.b * N + r % N) * words;
+            // the words that hold the drafts of this thread's columns of tile j
+            uint32_t w_next[3];
+            auto load_words = [&](int j) {
+                const int j0 = cur.lo + (cur.t0 + j) * kBN + 64 * half - P;  // draft of the first column
+                w_next[0] = w_next[1] = w_next[2] = 0;
+                if (j0 + 64 > 0 && r < rows) {
+                    const int w0 = j0 >> 5;
+#pragma unroll
+                    for (int e = 0; e < 3; ++e)
+                        w_next[e] = w0 + e >= 0 && w0 + e < words ? __ldg(see_words + w0 + e) : 0u;
+                }
+            };
+            load_words(0);
+            more = walk.next(a, nxt);
+            d_next = more ? row_depth(nxt) : -1;
             // cache rows from r_lo on are visible
             const int r_lo = a.window > 0 ? max(0, P + d - a.window + 1) : 0;
             float m_run = -INFINITY, l_run = 0.f;
-            const float c_log2 = fabsf(a.scale_log2);
             for (int j = 0; j < nt; ++j, ++J) {
                 const int s = J & 1;
-                const int t_lo = lo + (t0 + j) * kBN, c0 = t_lo + 64 * half;
+                const int t_lo = cur.lo + (cur.t0 + j) * kBN, c0 = t_lo + 64 * half;
+                const bool cut = t_lo + kBN > P || (a.window > 0 && t_lo < P + N - a.window);
+                // the keys that this row sees, a bit a column
+                uint32_t see[2] = {~0u, ~0u};
+                if (cut || d < 0) {
+                    const int sh = (c0 - P) & 31;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int k0 = c0 + 32 * e;  // key row of bit 0
+                        uint32_t bits = 0;
+                        if (d >= 0 && k0 < P && k0 + 32 > r_lo) {
+                            // cache rows [r_lo, P)
+                            bits = k0 < r_lo ? ~0u << (r_lo - k0) : ~0u;
+                            if (k0 + 32 > P)
+                                bits &= ~0u >> (k0 + 32 - P);
+                        }
+                        see[e] = bits | __funnelshift_r(w_next[e], w_next[e + 1], sh);
+                    }
+                }
+                load_words(j + 1);
                 ok = ok && wait_or_abort(&s_full[s], (J >> 1) & 1, abort_flag, a.status);
                 kvc_tc::fence_after();
-                const bool cut = t_lo + kBN > P || (a.window > 0 && t_lo < P + N - a.window);
                 uint64_t bad[2] = {0, 0};  // V rows of the tile in which this thread found one not finite
                 if (cut && ok) {
 #pragma unroll
@@ -713,43 +771,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                                                         not_finite<T>(x.w));
                             if (nf.x | nf.y | nf.z | nf.w) {
                                 v[at] = make_uint4(x.x & ~nf.x, x.y & ~nf.y, x.z & ~nf.z, x.w & ~nf.w);
-                                const int row = hf * KR + ((at >> 3) & (KR - 1));
-                                bad[row >> 6] |= 1ull << (row & 63);
+                                const int vr = hf * KR + ((at >> 3) & (KR - 1));
+                                bad[vr >> 6] |= 1ull << (vr & 63);
                             }
                         }
                     }
                     kvc::fence_proxy_async_smem();
-                }
-                // the keys that this row sees, a bit a column
-                uint32_t see[2] = {~0u, ~0u};
-                if (active && (cut || d < 0)) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int k0 = c0 + 32 * e;  // key row of bit 0
-                        uint32_t bits = 0;
-                        if (d >= 0 && k0 < P && k0 + 32 > r_lo) {
-                            // cache rows [r_lo, P)
-                            bits = k0 < r_lo ? ~0u << (r_lo - k0) : ~0u;
-                            if (k0 + 32 > P)
-                                bits &= ~0u >> (k0 + 32 - P);
-                        }
-                        if (d >= 0 && k0 + 32 > P && k0 < P + N) {
-                            // drafts k0 - P + c
-                            const int w0 = (k0 - P) >> 5;
-                            const uint32_t x0 = w0 >= 0 ? mask[w0] : 0u;
-                            const uint32_t x1 = w0 + 1 < words ? mask[w0 + 1] : 0u;
-                            uint32_t left = __funnelshift_r(x0, x1, (k0 - P) & 31);
-                            while (left) {
-                                const int c = __ffs(left) - 1;
-                                left &= left - 1;
-                                const int jd = k0 - P + c;
-                                const int dj = jd < N ? depth_sh[jd] : -1;
-                                if (dj >= 0 && (a.window <= 0 || d - dj < a.window))
-                                    bits |= 1u << c;
-                            }
-                        }
-                        see[e] = bits;
-                    }
                 }
                 float v[64];
                 if (active) {
@@ -757,6 +784,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                     kvc_tc::ld32(lane_addr + SM::COL_S + s * kBN + 64 * half, raw);
                     kvc_tc::ld32(lane_addr + SM::COL_S + s * kBN + 64 * half + 32, raw + 32);
                     kvc_tc::wait_ld();
+                    if (a.scale_log2 < 0.f) {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c)
+                            v[c] = -v[c];
+                    }
                     if (cut || d < 0) {
 #pragma unroll
                         for (int c = 0; c < 64; ++c)
@@ -781,10 +813,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                         break;
                     }
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf)
-                        if (bad[hf]) {
-                            atomicOr(&bad_sh[2 * hf], (uint32_t)bad[hf]);
-                            atomicOr(&bad_sh[2 * hf + 1], (uint32_t)(bad[hf] >> 32));
+                    for (int e = 0; e < 2; ++e)
+                        if (bad[e]) {
+                            atomicOr(&bad_sh[2 * e], (uint32_t)bad[e]);
+                            atomicOr(&bad_sh[2 * e + 1], (uint32_t)(bad[e] >> 32));
                         }
                     kvc_tc::named_bar_sync(all_bar, 32 * kSoftmaxWarps);
                     spoiled = ((see[0] & bad_sh[2 * half]) | (see[1] & bad_sh[2 * half + 1])) != 0;
@@ -841,7 +873,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
             q0 += 2 * SPT * nt;
 
             // ---- output rows ----
-            // (every MMA of the segment has completed after this wait: Q and O may be used)
+            // (the next segment's first PV waits for its p_full, which every warp gives after this)
             ok = ok && wait_or_abort(&o_done[(J - 1) & 1], ((J - 1) >> 1) & 1, abort_flag, a.status);
             kvc_tc::fence_after();
             if (active)
@@ -850,7 +882,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                 break;
             if (active) {
                 const float l = l_run + red[((J & 1) * 2 + (half ^ 1)) * kBM + m];
-                const bool whole = nt == n;
+                const bool whole = nt == cur.n;
                 const int64_t part = (2 * (int64_t)blockIdx.x + (s_no == 0 ? 0 : 1)) * kBM + m;
                 // a row that saw nothing holds no sum: zeros, whatever O is
                 const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -862,7 +894,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                     if (r >= rows)
                         continue;
                     if (whole) {
-                        T *to = static_cast<T *>(a.out) + (q_row0 + m) * D + cc;
+                        const int64_t row0 = ((int64_t)cur.b * a.kv_heads + h) * rows + (int64_t)mt * kBM;
+                        T *to = static_cast<T *>(a.out) + (row0 + m) * D + cc;
 #pragma unroll
                         for (int c = 0; c < 32; c += 8) {
                             uint4 x;
@@ -888,9 +921,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                 }
             }
             kvc_tc::fence_before();
+            cur = nxt;
         }
     }
 
+    kvc::grid_dep_wait();
     __syncthreads();
     if (warp == 0) {
         kvc_tc::fence_after();
@@ -908,9 +943,9 @@ tree_merge_kernel(const TreeArgs a)
     const int c0 = blockIdx.x, lane = threadIdx.x & 31, m = blockIdx.y * 8 + (threadIdx.x >> 5);
     const int rows = a.group * a.nodes, line_rows = a.kv_heads * a.row_tiles;
     auto count = [&](int b) {
-        int lo;
+        int P, lo;
         uint32_t bad;
-        return tree_tiles(a, b, lo, bad);
+        return tree_tiles(a, b, P, lo, bad);
     };
     int b, base;
     const int U = kvc_flat::locate(a.batch, line_rows, count, -1, b, base);
@@ -971,6 +1006,23 @@ tree_merge_kernel(const TreeArgs a)
             kvc::Elem<T>::from_f32(sum == 0.f ? 0.f : acc[e] / sum);
 }
 
+template <typename... A>
+cudaError_t launch_after(void (*kern)(A...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args)
+{
+    // may start while the kernel before it runs, and waits for it where it needs it
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 template <typename T, int D, int KR>
 kvc_status launch_attn_dim(const TreeArgs &a, const void *k, const void *v, cudaStream_t stream)
 {
@@ -979,8 +1031,10 @@ kvc_status launch_attn_dim(const TreeArgs &a, const void *k, const void *v, cuda
                                                                   : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const uint64_t rows = (a.at.table ? (uint64_t)a.at.n_pool * a.at.page_size : (uint64_t)a.batch * a.at.rows) *
                           a.kv_heads;
-    CUtensorMap tk, tv;
-    if (!kvc_host::encode_3d_sw128(&tk, k, rows, D, KR, D / 64, tt) ||
+    const int64_t q_rows = (int64_t)a.batch * a.q_heads * a.nodes;
+    CUtensorMap tq, tk, tv;
+    if (!kvc_host::encode_3d_sw128(&tq, a.cos_t ? a.ws_q : a.q, (uint64_t)q_rows, D, kBM, D / 64, tt) ||
+        !kvc_host::encode_3d_sw128(&tk, k, rows, D, KR, D / 64, tt) ||
         !kvc_host::encode_3d_sw128(&tv, v, rows, D, KR, D / 64, tt))
         return KVC_ERR_CUDA;
     int dev = 0, optin = 0;
@@ -993,20 +1047,15 @@ kvc_status launch_attn_dim(const TreeArgs &a, const void *k, const void *v, cuda
     auto kern = tree_attn_kernel<T, D, KR>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return KVC_ERR_CUDA;
-    kern<<<a.grid, kAttnThreads, smem, stream>>>(tk, tv, a);
-    if (a.grid > 1) {
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(a.grid - 1, (std::min(kBM, a.group * a.nodes) + 7) / 8);
-        cfg.blockDim = dim3(256);
-        cfg.stream = stream;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaLaunchKernelEx(&cfg, tree_merge_kernel<T, D>, a) != cudaSuccess)
-            return KVC_ERR_CUDA;
-    }
+    const unsigned q_blocks = a.cos_t ? (unsigned)((q_rows * (D / 16) + 255) / 256) : 0u;
+    const int64_t words = (int64_t)a.batch * a.nodes * ((a.nodes + 31) / 32);
+    tree_prep_kernel<T><<<q_blocks + (unsigned)((words + 255) / 256), 256, 0, stream>>>(a, D, q_blocks);
+    if (launch_after(kern, dim3(a.grid), kAttnThreads, smem, stream, tq, tk, tv, a) != cudaSuccess)
+        return KVC_ERR_CUDA;
+    if (a.grid > 1 && launch_after(tree_merge_kernel<T, D>,
+                                   dim3(a.grid - 1, (std::min(kBM, a.group * a.nodes) + 7) / 8), 256, 0, stream,
+                                   a) != cudaSuccess)
+        return KVC_ERR_CUDA;
     return kvc_host::launch_status();
 }
 
@@ -1064,6 +1113,20 @@ kvc_status check_rope(const float *cos_t, const float *sin_t, int64_t max_pos)
     if (cos_t && max_pos < 1)
         return KVC_ERR_SHAPE;
     return KVC_OK;
+}
+
+// the workspace: two partial results of a row tile for each CTA (one an SM), the
+// rotated queries, the drafts that each node sees
+struct TreeLayout {
+    size_t q, see, total;
+};
+TreeLayout tree_layout(int batch, int q_heads, int nodes, int D)
+{
+    TreeLayout l;
+    l.q = 2 * (size_t)kvc_host::sm_count() * kBM * (D + 2) * sizeof(float);
+    l.see = l.q + (size_t)batch * q_heads * nodes * D * 2;
+    l.total = l.see + (size_t)batch * nodes * ((nodes + 31) / 32) * 4;
+    return l;
 }
 
 bool all_aligned(std::initializer_list<const void *> ptrs)
@@ -1129,8 +1192,8 @@ KVC_API size_t kvc_gqa_tree_workspace_size(int batch, int q_heads, int kv_heads,
 {
     if (batch < 1 || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads != 0 || nodes < 1 || head_dim < 1)
         return 0;
-    // one CTA an SM, two partial results of a row tile each
-    return 2 * (size_t)kvc_host::sm_count() * kBM * (head_dim + 2) * sizeof(float);
+    // (o, m, l), then the rotated queries and the words of the drafts seen
+    return tree_layout(batch, q_heads, nodes, head_dim).total;
 }
 
 KVC_API kvc_status kvc_gqa_tree(void *out, const void *q, const void *k_cache, const void *v_cache,
@@ -1186,13 +1249,16 @@ KVC_API kvc_status kvc_gqa_tree(void *out, const void *q, const void *k_cache, c
     a.status = dev_status;
     a.row_tiles = (a.group * nodes + kBM - 1) / kBM;
     const int64_t units = (int64_t)batch * kv_heads * a.row_tiles * ((at.rows + kBN - 1) / kBN);
-    if (units > (int64_t)INT32_MAX)
+    if (units > (int64_t)INT32_MAX || (int64_t)batch * q_heads * nodes > (int64_t)INT32_MAX / 32)
         return KVC_ERR_SHAPE;
     a.grid = (int)std::min<int64_t>(units, kvc_host::sm_count());
     const int64_t parts = 2 * (int64_t)kvc_host::sm_count() * kBM;
     a.ws_o = static_cast<float *>(workspace);
     a.ws_m = a.ws_o + parts * head_dim;
     a.ws_l = a.ws_m + parts;
+    const TreeLayout layout = tree_layout(batch, q_heads, nodes, head_dim);
+    a.ws_q = static_cast<uint8_t *>(workspace) + layout.q;
+    a.see = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(workspace) + layout.see);
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     return dtype == KVC_BF16 ? launch_attn<__nv_bfloat16>(a, k_cache, v_cache, head_dim, stream)
                              : launch_attn<__half>(a, k_cache, v_cache, head_dim, stream);
