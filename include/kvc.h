@@ -689,7 +689,8 @@ size_t kvc_gqa_prefill_workspace_size(int batch, int q_heads, int kv_heads, int 
  * that do not fit the capacity KVC_DEV_CAPACITY; that batch row writes nothing.
  * new_k, new_v  device [batch, kv_heads, new_tokens, head_dim], any kvc_dtype.
  * len           outputs of kvc_seq_lengths for the same S, C and policy.
- * head_dim      a multiple of 16, at most 256 (KVC_ERR_UNSUPPORTED).
+ * head_dim      a multiple of 16, at most 256 (KVC_ERR_UNSUPPORTED);
+ * batch * kv_heads <= 65535 (KVC_ERR_SHAPE).
  */
 kvc_status kvc_quant_append(void *kq_cache, void *vq_cache, float *k_scale, float *v_scale,
                             const void *new_k, const void *new_v, kvc_lengths len, int batch,

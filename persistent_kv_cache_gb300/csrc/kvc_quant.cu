@@ -32,70 +32,94 @@ template <int FMT> constexpr float kTop = FMT == KVC_INT8 ? 127.f : 448.f;
 // writing
 // --------------------------------------------------------------------------
 
-template <typename T> struct alignas(16) Row8 { T e[8]; };
+// eight values of a row, as they lie in memory
+template <typename T> struct Raw8 { uint32_t w[sizeof(T) * 2]; };
 
-template <typename T> __device__ __forceinline__ void load8(const T *p, float (&x)[8])
+template <typename T> __device__ __forceinline__ Raw8<T> load8(const T *p)
 {
-    if constexpr (sizeof(T) == 2) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
-        const T *e = reinterpret_cast<const T *>(&v);
+    Raw8<T> r;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            x[i] = kvc::Elem<T>::to_f32(e[i]);
-    } else {
-        const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
-        const float4 b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+        r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
     }
+    return r;
+}
+template <typename T> __device__ __forceinline__ void to_f32(const Raw8<T> &r, float (&x)[8])
+{
+    const T *e = reinterpret_cast<const T *>(r.w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        x[i] = kvc::Elem<T>::to_f32(e[i]);
 }
 
-// eight values of a row, LPR lanes a row, to codes: the row's scale by the
-// lanes' maximum, taken on the bit patterns of |x| so that a NaN or an
-// infinity (patterns from 0x7f800000 on) is the largest of all
+__device__ __forceinline__ float max_nan(float x, float y)
+{
+    float z;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+    return z;
+}
+
+// Eight values of a row, LPR lanes a row, to codes.  The maximum carries a NaN,
+// so a row that is not finite shows in it.  x / s is needed to the last bit (a
+// code hangs on it), and s is a row's: with r the correctly rounded 1 / s, and no
+// overflow or underflow on the way, q = x r corrected by its remainder,
+// q + (x - q s) r, is the correctly rounded quotient (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990): three
+// operations a value in the place of a division's ten or more.  Rows with a scale
+// outside [2^-100, 2^100] divide.
 template <int FMT, int LPR>
 __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float &scale)
 {
-    uint32_t top = 0;
+    float top = fabsf(x[0]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+    for (int i = 1; i < 8; ++i)
+        top = max_nan(top, fabsf(x[i]));
 #pragma unroll
     for (int d = 1; d < LPR; d <<= 1)
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+        top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
     uint2 out = make_uint2(0, 0);
-    if (top >= 0x7f800000u) {
+    if (!(top < INFINITY)) {
         scale = __uint_as_float(0x7fc00000u);
         return out;
     }
-    scale = __fdiv_rn(__uint_as_float(top), kTop<FMT>);
+    scale = __fdiv_rn(top, kTop<FMT>);
     if (scale == 0.f)
         return out;
-    if constexpr (FMT == KVC_INT8) {
-        uint32_t w[2];
+    float y[8];
+    const bool usual = scale >= 7.8886091e-31f && scale <= 1.2676506e30f;  // 2^-100, 2^100
+    if (usual) {
+        const float r = __frcp_rn(scale);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            w[h] = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                // a subnormal scale may round the quotient past 127
-                const int c = max(-127, min(127, __float2int_rn(__fdiv_rn(x[4 * h + i], scale))));
-                w[h] |= (uint32_t)(c & 0xff) << (8 * i);
-            }
+        for (int i = 0; i < 8; ++i) {
+            const float q = __fmul_rn(x[i], r);
+            y[i] = __fmaf_rn(__fmaf_rn(-q, scale, x[i]), r, q);
         }
-        out = make_uint2(w[0], w[1]);
     } else {
-        uint32_t w[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float2 lo = make_float2(__fdiv_rn(x[4 * h], scale), __fdiv_rn(x[4 * h + 1], scale));
-            const float2 hi = make_float2(__fdiv_rn(x[4 * h + 2], scale), __fdiv_rn(x[4 * h + 3], scale));
-            w[h] = (uint32_t)__nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3) |
-                   (uint32_t)__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3) << 16;
-        }
-        out = make_uint2(w[0], w[1]);
+        for (int i = 0; i < 8; ++i)
+            y[i] = __fdiv_rn(x[i], scale);
     }
-    return out;
+    uint32_t w[2];
+    if constexpr (FMT == KVC_INT8) {
+        uint32_t n[8];
+        // y + 1.5 2^23 rounds y to a whole number, ties to even, in the low bits
+        // (a subnormal scale may have rounded the quotient past 127)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            n[i] = __float_as_uint(fminf(fmaxf(y[i], -127.f), 127.f) + 12582912.f);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            w[h] = __byte_perm(__byte_perm(n[4 * h], n[4 * h + 1], 0x0040), __byte_perm(n[4 * h + 2], n[4 * h + 3], 0x0040),
+                               0x5410);
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            w[h] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(y[4 * h], y[4 * h + 1]), __NV_SATFINITE, __NV_E4M3) |
+                   (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(y[4 * h + 2], y[4 * h + 3]), __NV_SATFINITE, __NV_E4M3)
+                       << 16;
+    }
+    return make_uint2(w[0], w[1]);
 }
 
 struct AppendArgs {
@@ -113,22 +137,30 @@ struct AppendArgs {
 
 // LPR lanes write one row of K and the same row of V: eight columns a lane
 // (lanes past head_dim idle along), the rotation's partner columns c +- D / 2
-// fetched from the lane that holds them.
+// fetched from the lane that holds them.  A block walks the rows of one (batch
+// row, head) with the next rows under way while it works on these; the first
+// are asked for before the lengths say where they go.
+constexpr int kAppendThreads = 256;
 template <typename T, int FMT, int LPR>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kAppendThreads)
 quant_append_kernel(const AppendArgs a)
 {
-    constexpr int RPB = 256 / LPR;
-    const int sub = threadIdx.x % LPR;
-    const int64_t rows = (int64_t)a.batch * a.kv_heads * a.S;
-    const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR;
-    const bool in = row < rows;
-    const int64_t slice = in ? row / a.S : 0;
-    const int i = in ? (int)(row % a.S) : 0;
-    const int b = (int)(slice / a.kv_heads);
+    constexpr int RPB = kAppendThreads / LPR;
+    const int sub = threadIdx.x % LPR, t = threadIdx.x / LPR;
+    const int slice = blockIdx.y, b = slice / a.kv_heads;
+    const int c0 = 8 * sub, half = a.D / 2;
+    const bool low = c0 < half, col = c0 < a.D;
+    const T *nk = static_cast<const T *>(a.new_k) + (int64_t)slice * a.S * a.D + c0;
+    const T *nv = static_cast<const T *>(a.new_v) + (int64_t)slice * a.S * a.D + c0;
+    Raw8<T> kn = {}, vn = {};
+    int base = blockIdx.x * RPB;
+    if (col && base + t < a.S) {
+        kn = load8(nk + (int64_t)(base + t) * a.D);
+        vn = load8(nv + (int64_t)(base + t) * a.D);
+    }
     const int P = a.len.past_abs[b];
-    bool write = in && a.len.cache_total[b] >= 0 && P >= 0;
-    const bool lead = sub == 0 && i == 0 && slice % a.kv_heads == 0;
+    bool write = a.len.cache_total[b] >= 0 && P >= 0;
+    const bool lead = threadIdx.x == 0 && blockIdx.x == 0 && slice % a.kv_heads == 0;
     if (write && a.cos_t && (int64_t)P + a.S > a.rope_max_pos) {
         if (lead)
             kvc::raise_status(a.status, KVC_DEV_ROPE_RANGE);
@@ -140,48 +172,54 @@ quant_append_kernel(const AppendArgs a)
             kvc::raise_status(a.status, KVC_DEV_CAPACITY);
         write = false;
     }
-    // a ring keeps only the last C rows of the step
-    write = write && !(a.ring && (int64_t)i < (int64_t)a.S - a.C);
-    const int c0 = 8 * sub;
-    const bool col = write && c0 < a.D;
-    float k[8] = {}, v[8] = {};
-    if (col) {
-        load8(static_cast<const T *>(a.new_k) + row * a.D + c0, k);
-        load8(static_cast<const T *>(a.new_v) + row * a.D + c0, v);
-    }
-    const int64_t pos = (int64_t)P + i;
-    if (a.cos_t) {
-        const int half = a.D / 2;
-        const bool low = c0 < half;
-        // D is a multiple of 16, so the partner columns are one lane's
-        const int from = (threadIdx.x & 31) - sub + (low ? sub + half / 8 : sub - half / 8);
-        float other[8];
+    if (!write)
+        return;  // the whole block
+    // D is a multiple of 16, so the partner columns are one lane's
+    const int from = ((threadIdx.x & 31) - sub + (low ? sub + half / 8 : sub - half / 8)) & 31;
+    const int step = gridDim.x * RPB;
+    for (; base < a.S; base += step) {
+        const int i = base + t;
+        const bool in = col && i < a.S;
+        const int pos = P + i;
+        const Raw8<T> kr = kn, vr = vn;
+        float cs[8] = {}, sn[8] = {};
+        if (a.cos_t && in) {
+            const int64_t at = (int64_t)pos * half + (low ? c0 : c0 - half);
+            to_f32(load8(a.cos_t + at), cs);
+            to_f32(load8(a.sin_t + at), sn);
+        }
+        if (col && i + step < a.S) {
+            kn = load8(nk + (int64_t)(i + step) * a.D);
+            vn = load8(nv + (int64_t)(i + step) * a.D);
+        }
+        float k[8], v[8], vs, ks;
+        to_f32(vr, v);
+        const uint2 vc = quantise8<FMT, LPR>(v, vs);
+        to_f32(kr, k);
+        if (a.cos_t) {
+            Raw8<T> orow;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            other[e] = __shfl_sync(0xffffffffu, k[e], from & 31);
-        if (col) {
-            float cs[8], sn[8];
-            const int64_t at = pos * half + (low ? c0 : c0 - half);
-            load8(a.cos_t + at, cs);
-            load8(a.sin_t + at, sn);
+            for (int e = 0; e < (int)sizeof(T) * 2; ++e)
+                orow.w[e] = __shfl_sync(0xffffffffu, kr.w[e], from);
+            float other[8];
+            to_f32(orow, other);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 float lo = low ? k[e] : other[e], hi = low ? other[e] : k[e];
                 kvc::rope_pair(lo, hi, cs[e], sn[e]);
-                k[e] = low ? lo : hi;
+                k[e] = !in ? 0.f : low ? lo : hi;
             }
         }
-    }
-    float ks, vs;
-    const uint2 kc = quantise8<FMT, LPR>(k, ks);
-    const uint2 vc = quantise8<FMT, LPR>(v, vs);
-    if (col) {
-        const int64_t r = slice * a.C + (a.ring ? pos % a.C : pos);
-        *reinterpret_cast<uint2 *>(a.kq + r * a.D + c0) = kc;
-        *reinterpret_cast<uint2 *>(a.vq + r * a.D + c0) = vc;
-        if (sub == 0) {
-            a.ks[r] = ks;
-            a.vs[r] = vs;
+        const uint2 kc = quantise8<FMT, LPR>(k, ks);
+        // a ring keeps only the last C rows of the step
+        if (in && !(a.ring && (int64_t)i < (int64_t)a.S - a.C)) {
+            const int64_t r = (int64_t)slice * a.C + (a.ring ? (int)((uint32_t)pos % (uint32_t)a.C) : pos);
+            *reinterpret_cast<uint2 *>(a.kq + r * a.D + c0) = kc;
+            *reinterpret_cast<uint2 *>(a.vq + r * a.D + c0) = vc;
+            if (sub == 0) {
+                a.ks[r] = ks;
+                a.vs[r] = vs;
+            }
         }
     }
 }
@@ -219,7 +257,8 @@ struct DequantArgs {
     int32_t *status;
 };
 
-// 16-byte pieces of the codes of rows [0, L): D / 16 lanes a row
+// 16 codes a thread, D / 16 threads a row, kRowsAhead rows under way
+constexpr int kRowsAhead = 4;
 template <typename T, int FMT>
 __global__ void __launch_bounds__(256)
 dequant_rows_kernel(const DequantArgs a)
@@ -234,36 +273,46 @@ dequant_rows_kernel(const DequantArgs a)
             kvc::raise_status(a.status, KVC_DEV_CAPACITY);
         return;
     }
-    const int pieces = a.D / 16;
-    const int64_t first = a.ring ? (int64_t)(total - L) % a.C : 0;
-    const uint8_t *src = blockIdx.z == 0 ? a.kq : a.vq;
-    const float *scales = blockIdx.z == 0 ? a.ks : a.vs;
-    T *dst = static_cast<T *>(blockIdx.z == 0 ? a.k_out : a.v_out) + (int64_t)slice * a.R * a.D;
-    const int64_t work = (int64_t)L * pieces;
-    for (int64_t w = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; w < work;
-         w += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t r = w / pieces;
-        const int c0 = (int)(w % pieces) * 16;
-        int64_t slot = first + r;
-        if (slot >= a.C)
-            slot -= a.C;
-        slot += (int64_t)slice * a.C;
-        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(src + slot * a.D + c0));
-        const float s = __ldg(scales + slot);
-        const uint32_t word[4] = {q.x, q.y, q.z, q.w};
-        T out[16];
+    const int pieces = a.D / 16, rpb = 256 / pieces;
+    const int c0 = threadIdx.x % pieces * 16, sub = threadIdx.x / pieces;
+    if (sub >= rpb)
+        return;
+    const int64_t first = a.ring ? (int64_t)((uint32_t)(total - L) % (uint32_t)a.C) : 0;
+    const uint8_t *src = (blockIdx.z == 0 ? a.kq : a.vq) + (int64_t)slice * a.C * a.D + c0;
+    const float *scales = (blockIdx.z == 0 ? a.ks : a.vs) + (int64_t)slice * a.C;
+    T *dst = static_cast<T *>(blockIdx.z == 0 ? a.k_out : a.v_out) + (int64_t)slice * a.R * a.D + c0;
+    for (int64_t r0 = (int64_t)blockIdx.x * kRowsAhead * rpb + sub; r0 < L; r0 += (int64_t)gridDim.x * kRowsAhead * rpb) {
+        uint4 q[kRowsAhead];
+        float s[kRowsAhead];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float f[4];
-            codes4<FMT>(word[i], f);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                out[4 * i + e] = kvc::Elem<T>::from_f32(f[e] * s);
+        for (int u = 0; u < kRowsAhead; ++u) {
+            const int64_t r = r0 + u * rpb;
+            if (r < L) {
+                const int64_t slot = first + r >= a.C ? first + r - a.C : first + r;
+                q[u] = __ldg(reinterpret_cast<const uint4 *>(src + slot * a.D));
+                s[u] = __ldg(scales + slot);
+            }
         }
-        uint4 *to = reinterpret_cast<uint4 *>(dst + r * a.D + c0);
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T); ++i)
-            to[i] = reinterpret_cast<const uint4 *>(out)[i];
+        for (int u = 0; u < kRowsAhead; ++u) {
+            const int64_t r = r0 + u * rpb;
+            if (r >= L)
+                break;
+            const uint32_t word[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+            T out[16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float f[4];
+                codes4<FMT>(word[i], f);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    out[4 * i + e] = kvc::Elem<T>::from_f32(f[e] * s[u]);
+            }
+            uint4 *to = reinterpret_cast<uint4 *>(dst + r * a.D);
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T); ++i)
+                to[i] = reinterpret_cast<const uint4 *>(out)[i];
+        }
     }
 }
 
@@ -330,46 +379,58 @@ __device__ __forceinline__ float fast_log2(float x)
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-                 "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint32_t movm_trans(uint32_t x)
 {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 
-// four codes as two pairs of halves, exactly: an int8 code c, its sign bit
-// flipped, is the byte c + 128, which under the high byte 0x64 is the half
-// 1024 + (c + 128); subtracting 1152 leaves c.  Every e4m3 value is a half.
-template <int FMT> __device__ __forceinline__ void codes_to_halves(uint32_t w, uint32_t &lo, uint32_t &hi)
+// Four codes as two pairs of halves, exactly: bytes 0 and 2 in `even`, 1 and 3 in
+// `odd` for int8, bytes 0, 1 and 2, 3 for e4m3 (its conversion takes neighbours).
+// An int8 code c with its sign bit flipped is the byte c + 128, which under the
+// high byte 0x64 is the half 1024 + (c + 128); subtracting 1152 leaves c.  One
+// logic operation masks, flips and adds the high bytes of two codes at once, and
+// the shift of the odd ones is a multiplication, for the pipe that has room: the
+// kernel is bound by the logic pipe, which takes a warp's instruction in two
+// clocks.  Every e4m3 value is a half.
+template <int FMT> __device__ __forceinline__ void codes_to_halves(uint32_t w, uint32_t &even, uint32_t &odd)
 {
     if constexpr (FMT == KVC_INT8) {
-        const uint32_t u = w ^ 0x80808080u;
-        const uint32_t l = __byte_perm(u, 0x64646464u, 0x4140);
-        const uint32_t h = __byte_perm(u, 0x64646464u, 0x4342);
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(l), "r"(0x64806480u));
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(h), "r"(0x64806480u));
+        const uint32_t l = (w & 0x00ff00ffu) ^ 0x64806480u;
+        const uint32_t h = (__umulhi(w, 1u << 24) & 0x00ff00ffu) ^ 0x64806480u;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(even) : "r"(l), "r"(0x64806480u));
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(odd) : "r"(h), "r"(0x64806480u));
     } else {
         asm("{\n\t.reg .b16 l, h;\n\t"
             "mov.b32 {l, h}, %2;\n\t"
             "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
             "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-            : "=r"(lo), "=r"(hi)
+            : "=r"(even), "=r"(odd)
             : "r"(w));
     }
+}
+// the codes of columns 2 e and 2 e + 1 of two keys' words x, y as the pairs
+// (x_2e, y_2e), (x_2e+1, y_2e+1)
+template <int FMT>
+__device__ __forceinline__ void pairs_of(uint32_t x, uint32_t y, int e, uint32_t &first, uint32_t &second)
+{
+    constexpr uint32_t sel[2] = {FMT == KVC_INT8 ? 0x5410u : 0x5140u, FMT == KVC_INT8 ? 0x7632u : 0x7362u};
+    codes_to_halves<FMT>(__byte_perm(x, y, sel[e]), first, second);
 }
 
 __device__ __forceinline__ uint4 ldg_stream(const uint8_t *p)
 {
     uint4 v;
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
+        : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+        : "l"(p));
     return v;
 }
 __device__ __forceinline__ uint2 ldg_stream8(const uint8_t *p)
@@ -391,7 +452,8 @@ template <int D, int HB> struct QuantSmem {
     static constexpr int Q_BYTES = HEADS * Q_PITCH;
     static constexpr int O_PITCH = D + 4;         // floats
     static constexpr int O_OFF = (Q_BYTES + 15) / 16 * 16;
-    static constexpr int O_BYTES = HEADS * O_PITCH * 4;
+    static constexpr int O_WARP = HEADS * O_PITCH;  // floats of a warp's O
+    static constexpr int O_BYTES = kWarps * O_WARP * 4;
     static constexpr int ML_OFF = O_OFF + O_BYTES;
     // factor of each head's query, then m and l of each warp
     static constexpr int TOTAL = ML_OFF + (1 + 2 * kWarps) * HEADS * 4;
@@ -460,6 +522,60 @@ quant_decode_kernel(const QuantDecodeArgs a)
         const int u1 = min(nu, u0 + (x_end - x));
         const int64_t slice = (int64_t)b * a.kv_heads + h;
 
+        const uint8_t *kb = a.kq + slice * a.C * D + 16 * t, *vb = a.vq + slice * a.C * D + (D == 64 ? 8 : 16) * g;
+        const float *ksb = a.ks + slice * a.C, *vsb = a.vs + slice * a.C;
+        // A key past the last is the last again (its score is masked, and what is loaded is finite or
+        // seen): no load waits for a comparison.  first + j wraps at C at most once.
+        const uint32_t cap = (uint32_t)a.C, start = (uint32_t)first;
+        auto slot = [&](int j) {
+            const uint32_t r = start + (uint32_t)min(j, n - 1);
+            return min(r, r - cap);  // (r - cap is huge below cap)
+        };
+
+        uint4 kr[2][KV4];
+        uint32_t vr[4][VW];
+        float ksr[2], vsr[2];
+        auto load_k = [&](int j0) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t r = slot(j0 + g + 8 * e);
+                const uint8_t *p = kb + (uint64_t)r * D;
+#pragma unroll
+                for (int i = 0; i < KV4; ++i)
+                    kr[e][i] = ldg_stream(p + 64 * i);
+                ksr[e] = __ldg(ksb + r);
+                vsr[e] = __ldg(vsb + r);
+            }
+        };
+        auto load_v = [&](int j0) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t r = slot(j0 + 2 * t + (e & 1) + 8 * (e >> 1));
+                const uint8_t *p = vb + (uint64_t)r * D;
+                if constexpr (D == 64) {
+                    const uint2 v = ldg_stream8(p);
+                    vr[e][0] = v.x;
+                    vr[e][1] = v.y;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < D / 128; ++i) {
+                        const uint4 v = ldg_stream(p + 128 * i);
+                        vr[e][4 * i] = v.x;
+                        vr[e][4 * i + 1] = v.y;
+                        vr[e][4 * i + 2] = v.z;
+                        vr[e][4 * i + 3] = v.w;
+                    }
+                }
+            }
+        };
+        // the first keys are under way while the queries are made ready
+        const int j_end = min(n, u1 * kUnit);
+        int j0 = u0 * kUnit + 16 * warp;
+        if (j0 < j_end) {
+            load_k(j0);
+            load_v(j0);
+        }
+
         // ---- the group's queries: rotated, scaled by a power of two, halves ----
         __syncthreads();  // the last segment's reads of shared memory are done
         {
@@ -484,14 +600,16 @@ quant_decode_kernel(const QuantDecodeArgs a)
                 for (int d = 16; d; d >>= 1)
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
                 // top in [2^(ex - 127), 2^(ex - 126)); both powers of two stay normal
+                // (column d of the row goes where codes_to_halves() leaves the code of column d)
+                auto place = [](int d) { return FMT == KVC_INT8 ? (d & ~3) | ((d & 1) << 1) | ((d >> 1) & 1) : d; };
                 const int ex = min(max((int)(__float_as_uint(top) >> 23), 40), 250);
                 const float up = __uint_as_float((uint32_t)(127 + 14 + 127 - ex) << 23);
                 const float down = __uint_as_float((uint32_t)(ex - 14) << 23);
 #pragma unroll
                 for (int e = 0; e < PPL; ++e) {
                     __half *row = reinterpret_cast<__half *>(smem + r * SM::Q_PITCH);
-                    row[lane + 32 * e] = __float2half_rn(lo[e] * up);
-                    row[D / 2 + lane + 32 * e] = __float2half_rn(hi[e] * up);
+                    row[place(lane + 32 * e)] = __float2half_rn(lo[e] * up);
+                    row[place(D / 2 + lane + 32 * e)] = __float2half_rn(hi[e] * up);
                 }
                 if (lane == 0)
                     q_factor[r] = down;
@@ -518,52 +636,6 @@ quant_decode_kernel(const QuantDecodeArgs a)
             qs[hb][1] = q_factor[hb * 8 + 2 * t + 1] * a.scale_log2;
         }
 
-        const uint8_t *kb = a.kq + slice * a.C * D, *vb = a.vq + slice * a.C * D;
-        const float *ksb = a.ks + slice * a.C, *vsb = a.vs + slice * a.C;
-        auto slot = [&](int j) {
-            const int64_t r = first + j;
-            return r >= a.C ? r - a.C : r;
-        };
-
-        uint4 kr[2][KV4];
-        uint32_t vr[4][VW];
-        float ksr[2], vsr[2];
-        auto load_k = [&](int j0) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int j = j0 + g + 8 * e;
-                const bool ok = j < n;
-                const int64_t r = slot(j);
-#pragma unroll
-                for (int i = 0; i < KV4; ++i)
-                    kr[e][i] = ok ? ldg_stream(kb + r * D + 64 * i + 16 * t) : make_uint4(0, 0, 0, 0);
-                ksr[e] = ok ? __ldg(ksb + r) : 0.f;
-                vsr[e] = ok ? __ldg(vsb + r) : 0.f;
-            }
-        };
-        auto load_v = [&](int j0) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int j = j0 + 2 * t + (e & 1) + 8 * (e >> 1);
-                const bool ok = j < n;
-                const int64_t r = slot(j);
-                if constexpr (D == 64) {
-                    const uint2 v = ok ? ldg_stream8(vb + r * D + 8 * g) : make_uint2(0, 0);
-                    vr[e][0] = v.x;
-                    vr[e][1] = v.y;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < D / 128; ++i) {
-                        const uint4 v = ok ? ldg_stream(vb + r * D + 128 * i + 16 * g) : make_uint4(0, 0, 0, 0);
-                        vr[e][4 * i] = v.x;
-                        vr[e][4 * i + 1] = v.y;
-                        vr[e][4 * i + 2] = v.z;
-                        vr[e][4 * i + 3] = v.w;
-                    }
-                }
-            }
-        };
-
         float o[HB][D / 16][4], m[HB][2], mo[HB][2], l[HB][2];
 #pragma unroll
         for (int hb = 0; hb < HB; ++hb) {
@@ -577,12 +649,6 @@ quant_decode_kernel(const QuantDecodeArgs a)
             }
         }
 
-        const int j_end = min(n, u1 * kUnit);
-        int j0 = u0 * kUnit + 16 * warp;
-        if (j0 < j_end) {
-            load_k(j0);
-            load_v(j0);
-        }
         for (; j0 < j_end; j0 += kUnit) {
             // ---- scores ----
             float s[HB][4];
@@ -623,8 +689,8 @@ quant_decode_kernel(const QuantDecodeArgs a)
                 for (int e = 0; e < 2; ++e) {
                     s[hb][e] = in0 ? s[hb][e] * (k0 * qs[hb][e]) : -INFINITY;
                     s[hb][2 + e] = in1 ? s[hb][2 + e] * (k1 * qs[hb][e]) : -INFINITY;
-                    raise |= s[hb][e] > m[hb][e] + kSlack || s[hb][2 + e] > m[hb][e] + kSlack ||
-                             s[hb][e] + lv0 > mo[hb][e] + kSlack || s[hb][2 + e] + lv1 > mo[hb][e] + kSlack;
+                    raise |= fmaxf(s[hb][e], s[hb][2 + e]) > m[hb][e] + kSlack ||
+                             fmaxf(s[hb][e] + lv0, s[hb][2 + e] + lv1) > mo[hb][e] + kSlack;
                 }
             }
             if (__any_sync(0xffffffffu, raise)) {
@@ -678,10 +744,9 @@ quant_decode_kernel(const QuantDecodeArgs a)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     // columns 4 w + 2 e and + 1 of keys 2 t, 2 t + 1 and of 2 t + 8, 2 t + 9
-                    const uint32_t sel = e ? 0x7362 : 0x5140;
                     uint32_t a0, a1, a2, a3;
-                    codes_to_halves<FMT>(__byte_perm(vr[0][w], vr[1][w], sel), a0, a1);
-                    codes_to_halves<FMT>(__byte_perm(vr[2][w], vr[3][w], sel), a2, a3);
+                    pairs_of<FMT>(vr[0][w], vr[1][w], e, a0, a1);
+                    pairs_of<FMT>(vr[2][w], vr[3][w], e, a2, a3);
 #pragma unroll
                     for (int hb = 0; hb < HB; ++hb)
                         mma_f16(o[hb][2 * w + e], a0, a1, a2, a3, b0[hb], b1[hb]);
@@ -691,7 +756,7 @@ quant_decode_kernel(const QuantDecodeArgs a)
                 load_v(j0 + kUnit);
         }
 
-        // ---- join the warps: m, l, then O relative to the common m, in warp order ----
+        // ---- join the warps: m, l, then O relative to the common m ----
 #pragma unroll
         for (int hb = 0; hb < HB; ++hb) {
 #pragma unroll
@@ -718,24 +783,22 @@ quant_decode_kernel(const QuantDecodeArgs a)
                 // O is relative to mo; a warp without keys holds zeros
                 f[hb][e] = mo[hb][e] == -INFINITY ? (m[hb][e] == -INFINITY ? 1.f : 0.f) : exp2f(mo[hb][e] - top);
             }
-        for (int w = 0; w < kWarps; ++w) {
-            if (warp == w) {
+        {
+            // tile i holds columns 2 i and 2 i + 1 of the lane's run of consecutive columns
+            constexpr int RUN = D == 64 ? 8 : 16;
 #pragma unroll
-                for (int hb = 0; hb < HB; ++hb)
+            for (int hb = 0; hb < HB; ++hb)
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i)
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            // tile i holds columns 2 i and 2 i + 1 of the lane's run of consecutive columns
-                            constexpr int RUN = D == 64 ? 8 : 16;
-                            const int col = (2 * i / RUN) * 128 + RUN * g + 2 * i % RUN + (e >> 1);
-                            float *to = o_sh + (hb * 8 + 2 * t + (e & 1)) * SM::O_PITCH + col;
-                            const float v = o[hb][i][e] * f[hb][e & 1];
-                            *to = w ? *to + v : v;
-                        }
-            }
-            __syncthreads();
+                    for (int i = 0; i < D / 16; i += 2) {
+                        const int col = (2 * i / RUN) * 128 + RUN * g + 2 * i % RUN;
+                        const float x = f[hb][e];
+                        *reinterpret_cast<float4 *>(o_sh + warp * SM::O_WARP + (hb * 8 + 2 * t + e) * SM::O_PITCH + col) =
+                            make_float4(o[hb][i][e] * x, o[hb][i][2 + e] * x, o[hb][i + 1][e] * x, o[hb][i + 1][2 + e] * x);
+                    }
         }
+        __syncthreads();
         const bool whole = u0 == 0 && u1 == nu;
         const int64_t part = 2 * (int64_t)c + (seg == 0 ? 0 : 1);
         for (int idx = threadIdx.x; idx < a.group * D; idx += 32 * kWarps) {
@@ -750,7 +813,10 @@ quant_decode_kernel(const QuantDecodeArgs a)
                 // (a warp whose scores are all NaN keeps m = -inf and a NaN sum)
                 sum += l_sh[w * HEADS + r] * (mw == top || mw == -INFINITY ? 1.f : exp2f(mw - top));
             }
-            const float v = o_sh[r * SM::O_PITCH + d];
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+                v += o_sh[w * SM::O_WARP + r * SM::O_PITCH + d];
             if (whole) {
                 static_cast<T *>(a.out)[slice * a.group * D + idx] = kvc::Elem<T>::from_f32(v / sum);
             } else {
@@ -881,7 +947,7 @@ template <typename T, int FMT, int D, int HB> kvc_status launch_decode(const Qua
 {
     constexpr int smem = QuantSmem<D, HB>::TOTAL;
     auto kern = quant_decode_kernel<T, FMT, D, HB>;
-    if (smem > 48 * 1024 &&
+    if (smem > 32 * 1024 &&
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return KVC_ERR_CUDA;
     kern<<<a.grid, 32 * kWarps, smem, stream>>>(a);
@@ -920,36 +986,34 @@ bool format_ok(int format) { return format == KVC_INT8 || format == KVC_E4M3; }
 template <typename T> kvc_status launch_append(const AppendArgs &a, int format, cudaStream_t stream)
 {
     const int lpr = a.D <= 64 ? 8 : a.D <= 128 ? 16 : 32;
-    const int64_t rows = (int64_t)a.batch * a.kv_heads * a.S;
-    const int64_t blocks = (rows * lpr + 255) / 256;
-    if (blocks > (int64_t)INT32_MAX)
-        return KVC_ERR_SHAPE;
-    const unsigned n = (unsigned)blocks;
+    // one wave of resident blocks (4 an SM) over all slices, or a block for every row tile
+    const int slices = a.batch * a.kv_heads;
+    const int64_t tiles = ((int64_t)a.S * lpr + kAppendThreads - 1) / kAppendThreads;
+    const dim3 n((unsigned)std::min<int64_t>(tiles, (int64_t)kvc_host::sm_count() * 4 / slices + 1), slices);
     if (format == KVC_INT8) {
         if (lpr == 8)
-            quant_append_kernel<T, KVC_INT8, 8><<<n, 256, 0, stream>>>(a);
+            quant_append_kernel<T, KVC_INT8, 8><<<n, kAppendThreads, 0, stream>>>(a);
         else if (lpr == 16)
-            quant_append_kernel<T, KVC_INT8, 16><<<n, 256, 0, stream>>>(a);
+            quant_append_kernel<T, KVC_INT8, 16><<<n, kAppendThreads, 0, stream>>>(a);
         else
-            quant_append_kernel<T, KVC_INT8, 32><<<n, 256, 0, stream>>>(a);
+            quant_append_kernel<T, KVC_INT8, 32><<<n, kAppendThreads, 0, stream>>>(a);
     } else {
         if (lpr == 8)
-            quant_append_kernel<T, KVC_E4M3, 8><<<n, 256, 0, stream>>>(a);
+            quant_append_kernel<T, KVC_E4M3, 8><<<n, kAppendThreads, 0, stream>>>(a);
         else if (lpr == 16)
-            quant_append_kernel<T, KVC_E4M3, 16><<<n, 256, 0, stream>>>(a);
+            quant_append_kernel<T, KVC_E4M3, 16><<<n, kAppendThreads, 0, stream>>>(a);
         else
-            quant_append_kernel<T, KVC_E4M3, 32><<<n, 256, 0, stream>>>(a);
+            quant_append_kernel<T, KVC_E4M3, 32><<<n, kAppendThreads, 0, stream>>>(a);
     }
     return kvc_host::launch_status();
 }
 
 template <typename T> kvc_status launch_dequant(const DequantArgs &a, int format, cudaStream_t stream)
 {
-    const int64_t most = std::min(a.C, a.R) * (a.D / 16);
-    const int slices = a.batch * a.kv_heads;
-    // enough blocks for the longest rows, at most 16 an SM over all slices
-    int64_t nx = (most + 255) / 256;
-    nx = std::min<int64_t>(nx, std::max<int64_t>(1, (int64_t)kvc_host::sm_count() * 16 / (2 * slices) + 1));
+    // a block for every kRowsAhead * rpb rows, at most 64 an SM over all slices of K and V
+    const int slices = a.batch * a.kv_heads, rpb = 256 / (a.D / 16);
+    int64_t nx = (std::min(a.C, a.R) + kRowsAhead * rpb - 1) / (kRowsAhead * rpb);
+    nx = std::min<int64_t>(nx, (int64_t)kvc_host::sm_count() * 64 / (2 * slices) + 1);
     const dim3 grid((unsigned)nx, slices, 2);
     if (format == KVC_INT8)
         dequant_rows_kernel<T, KVC_INT8><<<grid, 256, 0, stream>>>(a);
@@ -987,7 +1051,7 @@ KVC_API kvc_status kvc_quant_append(void *kq_cache, void *vq_cache, float *k_sca
 {
     if (kvc_host::elem_bytes_of(dtype) == 0 || !format_ok(format))
         return KVC_ERR_DTYPE;
-    if (batch < 0 || kv_heads < 1 || new_tokens < 1 || head_dim < 1)
+    if (batch < 0 || kv_heads < 1 || new_tokens < 1 || head_dim < 1 || (int64_t)batch * kv_heads > 65535)
         return KVC_ERR_SHAPE;
     if (windowed != KVC_CONTIGUOUS && windowed != KVC_RING)
         return KVC_ERR_UNSUPPORTED;

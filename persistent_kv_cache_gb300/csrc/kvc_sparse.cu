@@ -45,85 +45,121 @@ __device__ __forceinline__ int bound_code(float x, float s, bool up)
     return max(-127, min(127, up ? __float2int_ru(y) : __float2int_rd(y)));
 }
 
-// One block per (page of the step, kv head, batch row): 8 columns a thread,
-// the rows dealt over 256 / (D / 8) groups of threads, then joined.
+// Packed maximum and minimum in which a NaN wins
+template <typename T> __device__ __forceinline__ uint32_t pair_max(uint32_t x, uint32_t y)
+{
+    uint32_t z;
+    if constexpr (std::is_same<T, __half>::value)
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(z) : "r"(x), "r"(y));
+    else
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(z) : "r"(x), "r"(y));
+    return z;
+}
+template <typename T> __device__ __forceinline__ uint32_t pair_min(uint32_t x, uint32_t y)
+{
+    uint32_t z;
+    if constexpr (std::is_same<T, __half>::value)
+        asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(z) : "r"(x), "r"(y));
+    else
+        asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(z) : "r"(x), "r"(y));
+    return z;
+}
+
+// A warp takes the page of one head: D / 8 lanes a row, eight columns a lane,
+// maximum and minimum of two columns at once, kAhead loads of 16 bytes under way.
+// It reads 2 D bytes a row once and no block waits for another warp.
+constexpr int kBoundWarps = 8;
 template <typename T, int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32 * kBoundWarps)
 page_bounds_kernel(const BoundsArgs a)
 {
-    constexpr int CT = D / 8, GROUPS = 256 / CT;
-    __shared__ float hi_sh[GROUPS][D], lo_sh[GROUPS][D];
-    __shared__ uint32_t top_sh[8];
-    const int b = blockIdx.z, h = blockIdx.y;
+    constexpr int LPR = D / 8, ROWS = 32 / LPR, kAhead = 16;
+    const int lane = threadIdx.x & 31, b = blockIdx.y;
+    const int item = blockIdx.x * kBoundWarps + (threadIdx.x >> 5);
+    const int h = item % a.kv_heads;
     const int P = a.len.past_abs[b], total = a.len.total_abs[b];
     if (a.len.cache_total[b] < 0)
         return;
+    const bool lead = lane == 0 && item < a.kv_heads;
     if (total > (int64_t)a.max_pages * a.page_size || P < 0 || P > total) {
-        if (threadIdx.x == 0 && blockIdx.x == 0 && h == 0)
+        if (lead && h == 0)
             kvc::raise_status(a.status, KVC_DEV_CAPACITY);
         return;
     }
     // pages [P / page, T / page) became full with this step
-    for (int64_t j = P / a.page_size + blockIdx.x; j < total / a.page_size; j += gridDim.x) {
-        const int64_t id = a.table[(int64_t)b * a.max_pages + j];
-        if (id < 0 || id >= a.n_pool) {
-            if (threadIdx.x == 0 && h == 0)
-                kvc::raise_status(a.status, KVC_DEV_INDEX_OOB);
-            continue;
-        }
-        const int64_t slice = id * a.kv_heads + h;
-        const T *k = static_cast<const T *>(a.k_pool) + slice * a.page_size * D;
-        const int col = threadIdx.x % CT * 8, grp = threadIdx.x / CT;
-        float hi[8], lo[8];
-        uint32_t top = 0;
+    const int j = P / a.page_size + item / a.kv_heads;
+    if (j >= total / a.page_size)
+        return;
+    const int64_t id = a.table[(int64_t)b * a.max_pages + j];
+    if (id < 0 || id >= a.n_pool) {
+        if (lane == 0)
+            kvc::raise_status(a.status, KVC_DEV_INDEX_OOB);
+        return;
+    }
+    const int64_t slice = id * a.kv_heads + h;
+    const int col = lane % LPR * 8, r0 = lane / LPR;
+    const T *k = static_cast<const T *>(a.k_pool) + (slice * a.page_size + r0) * D + col;
+    constexpr uint32_t low = std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;  // -infinity
+    uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            hi[e] = -INFINITY;
-            lo[e] = INFINITY;
+    for (int e = 0; e < 4; ++e) {
+        hi[e] = low;
+        lo[e] = low & 0x7fff7fffu;
+    }
+    auto take = [&](const uint4 &v) {
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            hi[e] = pair_max<T>(hi[e], x[e]);
+            lo[e] = pair_min<T>(lo[e], x[e]);
         }
-        for (int r = grp; r < a.page_size; r += GROUPS) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(k + (int64_t)r * D + col));
-            const T *x = reinterpret_cast<const T *>(&v);
+    };
+    int r = 0;
+    for (; r + kAhead * ROWS <= a.page_size; r += kAhead * ROWS) {
+        uint4 v[kAhead];
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e)
+            v[e] = __ldg(reinterpret_cast<const uint4 *>(k + (int64_t)(r + e * ROWS) * D));
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e)
+            take(v[e]);
+    }
+    for (; r + r0 < a.page_size; r += ROWS)
+        take(__ldg(reinterpret_cast<const uint4 *>(k + (int64_t)r * D)));
+#pragma unroll
+    for (int d = LPR; d < 32; d <<= 1)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            hi[e] = pair_max<T>(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], d));
+            lo[e] = pair_min<T>(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], d));
+        }
+    const T *mx = reinterpret_cast<const T *>(hi), *mn = reinterpret_cast<const T *>(lo);
+    // |x| by its bits, so that a NaN or an infinity is the largest
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        top = max(top, max(__float_as_uint(kvc::Elem<T>::to_f32(mx[e])) & 0x7fffffffu,
+                           __float_as_uint(kvc::Elem<T>::to_f32(mn[e])) & 0x7fffffffu));
+#pragma unroll
+    for (int d = 1; d < LPR; d <<= 1)
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+    // a page with a NaN or an infinity: scale infinity, the page is taken first
+    const bool finite = top < 0x7f800000u;
+    const float s = finite ? __fdiv_rn(__uint_as_float(top), 127.f) : INFINITY;
+    if (r0 == 0) {
+        uint2 out[2] = {};
+        if (finite && s > 0.f) {
+            int8_t *c = reinterpret_cast<int8_t *>(out);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float f = kvc::Elem<T>::to_f32(x[e]);
-                hi[e] = fmaxf(hi[e], f);
-                lo[e] = fminf(lo[e], f);
-                top = max(top, __float_as_uint(f) & 0x7fffffffu);
+                c[e] = (int8_t)bound_code(kvc::Elem<T>::to_f32(mx[e]), s, true);
+                c[8 + e] = (int8_t)bound_code(kvc::Elem<T>::to_f32(mn[e]), s, false);
             }
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            hi_sh[grp][col + e] = hi[e];
-            lo_sh[grp][col + e] = lo[e];
-        }
-#pragma unroll
-        for (int d = 16; d; d >>= 1)
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-        if ((threadIdx.x & 31) == 0)
-            top_sh[threadIdx.x >> 5] = top;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < 8; ++w)
-            top = max(top, top_sh[w]);
-        // a page with a NaN or an infinity: scale infinity, the page is taken first
-        const bool finite = top < 0x7f800000u;
-        const float s = finite ? __fdiv_rn(__uint_as_float(top), 127.f) : INFINITY;
-        if (threadIdx.x < D) {
-            const int d = threadIdx.x;
-            float mx = -INFINITY, mn = INFINITY;
-#pragma unroll
-            for (int w = 0; w < GROUPS; ++w) {
-                mx = fmaxf(mx, hi_sh[w][d]);
-                mn = fminf(mn, lo_sh[w][d]);
-            }
-            const bool any = finite && s > 0.f;
-            a.bounds[slice * 2 * D + d] = (int8_t)(any ? bound_code(mx, s, true) : 0);
-            a.bounds[slice * 2 * D + D + d] = (int8_t)(any ? bound_code(mn, s, false) : 0);
-        }
-        if (threadIdx.x == 0)
+        *reinterpret_cast<uint2 *>(a.bounds + slice * 2 * D + col) = out[0];
+        *reinterpret_cast<uint2 *>(a.bounds + slice * 2 * D + D + col) = out[1];
+        if (lane == 0)
             a.scale[slice] = s;
-        __syncthreads();
     }
 }
 
@@ -428,19 +464,20 @@ template <typename T> kvc_status launch_select(const SelectArgs &a, int D, cudaS
 
 template <typename T> kvc_status launch_bounds(const BoundsArgs &a, int batch, int S, cudaStream_t stream)
 {
-    // at most ceil(S / page) pages of a batch row become full, one block each up to 8 blocks an SM
-    const int64_t most = ((int64_t)S + a.page_size - 1) / a.page_size;
-    const int64_t cap = std::max<int64_t>(1, (int64_t)kvc_host::sm_count() * 8 / ((int64_t)batch * a.kv_heads) + 1);
-    const dim3 grid((unsigned)std::min(most, cap), a.kv_heads, batch);
+    // at most ceil(S / page) pages of a batch row become full, a warp for each of their heads
+    const int64_t most = ((int64_t)S + a.page_size - 1) / a.page_size * a.kv_heads;
+    if (most > (int64_t)INT32_MAX - kBoundWarps)
+        return KVC_ERR_SHAPE;
+    const dim3 grid((unsigned)((most + kBoundWarps - 1) / kBoundWarps), batch);
     switch (a.D) {
     case 64:
-        page_bounds_kernel<T, 64><<<grid, 256, 0, stream>>>(a);
+        page_bounds_kernel<T, 64><<<grid, 32 * kBoundWarps, 0, stream>>>(a);
         break;
     case 128:
-        page_bounds_kernel<T, 128><<<grid, 256, 0, stream>>>(a);
+        page_bounds_kernel<T, 128><<<grid, 32 * kBoundWarps, 0, stream>>>(a);
         break;
     default:
-        page_bounds_kernel<T, 256><<<grid, 256, 0, stream>>>(a);
+        page_bounds_kernel<T, 256><<<grid, 32 * kBoundWarps, 0, stream>>>(a);
     }
     return kvc_host::launch_status();
 }
@@ -456,7 +493,7 @@ KVC_API kvc_status kvc_page_bounds(void *bounds, float *bound_scale, const void 
         return KVC_ERR_DTYPE;
     if (dtype == KVC_F32 || (head_dim != 64 && head_dim != 128 && head_dim != 256))
         return KVC_ERR_UNSUPPORTED;
-    if (batch < 0 || batch > 65535 || kv_heads < 1 || kv_heads > 65535 || new_tokens < 1 || max_pages < 1 ||
+    if (batch < 0 || batch > 65535 || kv_heads < 1 || new_tokens < 1 || max_pages < 1 ||
         n_pool_pages < 1 || page_size < 1)
         return KVC_ERR_SHAPE;
     if ((int64_t)max_pages * page_size > (int64_t)INT32_MAX)
