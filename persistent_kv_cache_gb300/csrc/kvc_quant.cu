@@ -96,18 +96,18 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float &scale)
             y[i] = __fmaf_rn(__fmaf_rn(-q, scale, x[i]), r, q);
         }
     } else {
+        // (a subnormal scale may round the quotient past the largest code)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            y[i] = __fdiv_rn(x[i], scale);
+            y[i] = fminf(fmaxf(__fdiv_rn(x[i], scale), -kTop<FMT>), kTop<FMT>);
     }
     uint32_t w[2];
     if constexpr (FMT == KVC_INT8) {
         uint32_t n[8];
         // y + 1.5 2^23 rounds y to a whole number, ties to even, in the low bits
-        // (a subnormal scale may have rounded the quotient past 127)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            n[i] = __float_as_uint(fminf(fmaxf(y[i], -127.f), 127.f) + 12582912.f);
+            n[i] = __float_as_uint(y[i] + 12582912.f);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
             w[h] = __byte_perm(__byte_perm(n[4 * h], n[4 * h + 1], 0x0040), __byte_perm(n[4 * h + 2], n[4 * h + 3], 0x0040),
@@ -203,11 +203,11 @@ quant_append_kernel(const AppendArgs a)
                 orow.w[e] = __shfl_sync(0xffffffffu, kr.w[e], from);
             float other[8];
             to_f32(orow, other);
+            // lo cos - hi sin for a column of the lower half, hi cos + lo sin for one of the upper
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                float lo = low ? k[e] : other[e], hi = low ? other[e] : k[e];
-                kvc::rope_pair(lo, hi, cs[e], sn[e]);
-                k[e] = !in ? 0.f : low ? lo : hi;
+                const float turned = __fadd_rn(__fmul_rn(k[e], cs[e]), __fmul_rn(other[e], low ? -sn[e] : sn[e]));
+                k[e] = in ? turned : 0.f;
             }
         }
         const uint2 kc = quantise8<FMT, LPR>(k, ks);
@@ -257,8 +257,9 @@ struct DequantArgs {
     int32_t *status;
 };
 
-// 16 codes a thread, D / 16 threads a row, kRowsAhead rows under way
-constexpr int kRowsAhead = 4;
+// Eight codes a thread (16 bytes out, side by side over a warp), D / 8 threads a
+// row, kRowsAhead rows under way
+constexpr int kRowsAhead = 8;
 template <typename T, int FMT>
 __global__ void __launch_bounds__(256)
 dequant_rows_kernel(const DequantArgs a)
@@ -273,45 +274,42 @@ dequant_rows_kernel(const DequantArgs a)
             kvc::raise_status(a.status, KVC_DEV_CAPACITY);
         return;
     }
-    const int pieces = a.D / 16, rpb = 256 / pieces;
-    const int c0 = threadIdx.x % pieces * 16, sub = threadIdx.x / pieces;
+    const int pieces = a.D / 8, rpb = 256 / pieces;
+    const int c0 = threadIdx.x % pieces * 8, sub = threadIdx.x / pieces;
     if (sub >= rpb)
         return;
-    const int64_t first = a.ring ? (int64_t)((uint32_t)(total - L) % (uint32_t)a.C) : 0;
+    const uint32_t cap = (uint32_t)a.C, first = a.ring ? (uint32_t)(total - L) % cap : 0u;
     const uint8_t *src = (blockIdx.z == 0 ? a.kq : a.vq) + (int64_t)slice * a.C * a.D + c0;
     const float *scales = (blockIdx.z == 0 ? a.ks : a.vs) + (int64_t)slice * a.C;
     T *dst = static_cast<T *>(blockIdx.z == 0 ? a.k_out : a.v_out) + (int64_t)slice * a.R * a.D + c0;
     for (int64_t r0 = (int64_t)blockIdx.x * kRowsAhead * rpb + sub; r0 < L; r0 += (int64_t)gridDim.x * kRowsAhead * rpb) {
-        uint4 q[kRowsAhead];
+        uint2 q[kRowsAhead];
         float s[kRowsAhead];
 #pragma unroll
         for (int u = 0; u < kRowsAhead; ++u) {
-            const int64_t r = r0 + u * rpb;
-            if (r < L) {
-                const int64_t slot = first + r >= a.C ? first + r - a.C : first + r;
-                q[u] = __ldg(reinterpret_cast<const uint4 *>(src + slot * a.D));
-                s[u] = __ldg(scales + slot);
-            }
+            // (a row past the last is the last again)
+            const uint32_t r = (uint32_t)min(r0 + u * rpb, (int64_t)L - 1) + first;
+            const uint32_t slot = min(r, r - cap);
+            q[u] = __ldg(reinterpret_cast<const uint2 *>(src + (uint64_t)slot * a.D));
+            s[u] = __ldg(scales + slot);
         }
 #pragma unroll
         for (int u = 0; u < kRowsAhead; ++u) {
             const int64_t r = r0 + u * rpb;
             if (r >= L)
                 break;
-            const uint32_t word[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
-            T out[16];
+            float f[8];
+            codes4<FMT>(q[u].x, *reinterpret_cast<float (*)[4]>(f));
+            codes4<FMT>(q[u].y, *reinterpret_cast<float (*)[4]>(f + 4));
+            Raw8<T> out;
+            T *e = reinterpret_cast<T *>(out.w);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float f[4];
-                codes4<FMT>(word[i], f);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    out[4 * i + e] = kvc::Elem<T>::from_f32(f[e] * s[u]);
-            }
+            for (int i = 0; i < 8; ++i)
+                e[i] = kvc::Elem<T>::from_f32(f[i] * s[u]);
             uint4 *to = reinterpret_cast<uint4 *>(dst + r * a.D);
 #pragma unroll
-            for (int i = 0; i < (int)sizeof(T); ++i)
-                to[i] = reinterpret_cast<const uint4 *>(out)[i];
+            for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+                to[i] = make_uint4(out.w[4 * i], out.w[4 * i + 1], out.w[4 * i + 2], out.w[4 * i + 3]);
         }
     }
 }
@@ -322,6 +320,7 @@ dequant_rows_kernel(const DequantArgs a)
 
 constexpr int kUnit = 64;           // keys of one unit of work: 16 for each warp
 constexpr int kWarps = 4;
+constexpr float kNone = -1e30f;     // a reference maximum before any score (finite: differences stay numbers)
 constexpr float kSlack = 8.f;       // log2 units a score may exceed its reference by
 
 struct QuantDecodeArgs {
@@ -392,21 +391,29 @@ __device__ __forceinline__ uint32_t movm_trans(uint32_t x)
     return y;
 }
 
-// Four codes as two pairs of halves, exactly: bytes 0 and 2 in `even`, 1 and 3 in
-// `odd` for int8, bytes 0, 1 and 2, 3 for e4m3 (its conversion takes neighbours).
-// An int8 code c with its sign bit flipped is the byte c + 128, which under the
-// high byte 0x64 is the half 1024 + (c + 128); subtracting 1152 leaves c.  One
-// logic operation masks, flips and adds the high bytes of two codes at once, and
-// the shift of the odd ones is a multiplication, for the pipe that has room: the
-// kernel is bound by the logic pipe, which takes a warp's instruction in two
-// clocks.  Every e4m3 value is a half.
-template <int FMT> __device__ __forceinline__ void codes_to_halves(uint32_t w, uint32_t &even, uint32_t &odd)
+// Four codes as two pairs of halves: bytes 0 and 2 in `even`, 1 and 3 in `odd` for
+// int8, bytes 0, 1 and 2, 3 for e4m3 (its conversion takes neighbours).  Every
+// e4m3 value is a half.  An int8 code c with its sign bit flipped is the byte
+// u = c + 128:
+//   BIASED: u alone in a half is the subnormal u 2^-24, so one logic operation
+//     masks and flips two codes at once, and the sum over d of q_d u_d is
+//     corrected by 128 sum q_d, a constant of the head (both are sums of about the
+//     same size, so no digits go);
+//   else: under the high byte 0x64 it is the half 1024 + u; subtracting 1152
+//     leaves c.  (A bias of 128 on the values would be far above what their
+//     weighted mean leaves.)
+// The shift of the odd bytes is a multiplication, for the pipe that has room: the
+// logic pipe takes a warp's instruction in two clocks and bounds the kernel.
+template <int FMT, bool BIASED> __device__ __forceinline__ void codes_to_halves(uint32_t w, uint32_t &even, uint32_t &odd)
 {
     if constexpr (FMT == KVC_INT8) {
-        const uint32_t l = (w & 0x00ff00ffu) ^ 0x64806480u;
-        const uint32_t h = (__umulhi(w, 1u << 24) & 0x00ff00ffu) ^ 0x64806480u;
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(even) : "r"(l), "r"(0x64806480u));
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(odd) : "r"(h), "r"(0x64806480u));
+        constexpr uint32_t flip = BIASED ? 0x00800080u : 0x64806480u;
+        even = (w & 0x00ff00ffu) ^ flip;
+        odd = (__umulhi(w, 1u << 24) & 0x00ff00ffu) ^ flip;
+        if constexpr (!BIASED) {
+            asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(even) : "r"(0x64806480u));
+            asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(odd) : "r"(0x64806480u));
+        }
     } else {
         asm("{\n\t.reg .b16 l, h;\n\t"
             "mov.b32 {l, h}, %2;\n\t"
@@ -422,7 +429,7 @@ template <int FMT>
 __device__ __forceinline__ void pairs_of(uint32_t x, uint32_t y, int e, uint32_t &first, uint32_t &second)
 {
     constexpr uint32_t sel[2] = {FMT == KVC_INT8 ? 0x5410u : 0x5140u, FMT == KVC_INT8 ? 0x7632u : 0x7362u};
-    codes_to_halves<FMT>(__byte_perm(x, y, sel[e]), first, second);
+    codes_to_halves<FMT, false>(__byte_perm(x, y, sel[e]), first, second);
 }
 
 __device__ __forceinline__ uint4 ldg_stream(const uint8_t *p)
@@ -455,8 +462,8 @@ template <int D, int HB> struct QuantSmem {
     static constexpr int O_WARP = HEADS * O_PITCH;  // floats of a warp's O
     static constexpr int O_BYTES = kWarps * O_WARP * 4;
     static constexpr int ML_OFF = O_OFF + O_BYTES;
-    // factor of each head's query, then m and l of each warp
-    static constexpr int TOTAL = ML_OFF + (1 + 2 * kWarps) * HEADS * 4;
+    // each head's factor and bias, then m and l of each warp
+    static constexpr int TOTAL = ML_OFF + (2 + 2 * kWarps) * HEADS * 4;
 };
 
 // Attention of one query over the codes of a flat share of the batch
@@ -489,7 +496,8 @@ quant_decode_kernel(const QuantDecodeArgs a)
     extern __shared__ __align__(16) uint8_t smem[];
     float *o_sh = reinterpret_cast<float *>(smem + SM::O_OFF);
     float *q_factor = reinterpret_cast<float *>(smem + SM::ML_OFF);
-    float *m_sh = q_factor + HEADS, *l_sh = m_sh + kWarps * HEADS;
+    float *q_bias = q_factor + HEADS;
+    float *m_sh = q_bias + HEADS, *l_sh = m_sh + kWarps * HEADS;
 
     kvc::grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -524,18 +532,36 @@ quant_decode_kernel(const QuantDecodeArgs a)
 
         const uint8_t *kb = a.kq + slice * a.C * D + 16 * t, *vb = a.vq + slice * a.C * D + (D == 64 ? 8 : 16) * g;
         const float *ksb = a.ks + slice * a.C, *vsb = a.vs + slice * a.C;
-        // A key past the last is the last again (its score is masked, and what is loaded is finite or
-        // seen): no load waits for a comparison.  first + j wraps at C at most once.
         const uint32_t cap = (uint32_t)a.C, start = (uint32_t)first;
+        uint4 kr[2][KV4];
+        uint32_t vr[4][VW];
+        float ksr[2], vsr[2];
+        // 16 keys whose rows follow one another: one address each for the keys, the values and the
+        // scales, and constant steps.  Else (the last keys, or a ring's end among them) each row has its
+        // own, a key past the last being the last again: its score is masked, and what is loaded is
+        // finite or seen.  start + j wraps at C at most once.
+        auto in_line = [&](int j0) {
+            const uint32_t r = start + (uint32_t)j0;
+            return j0 + 16 <= n && (r >= cap || r + 16 <= cap);
+        };
         auto slot = [&](int j) {
             const uint32_t r = start + (uint32_t)min(j, n - 1);
             return min(r, r - cap);  // (r - cap is huge below cap)
         };
-
-        uint4 kr[2][KV4];
-        uint32_t vr[4][VW];
-        float ksr[2], vsr[2];
         auto load_k = [&](int j0) {
+            if (in_line(j0)) {
+                const uint32_t r = slot(j0 + g);
+                const uint8_t *p = kb + (uint64_t)r * D;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int i = 0; i < KV4; ++i)
+                        kr[e][i] = ldg_stream(p + 8 * e * D + 64 * i);
+                    ksr[e] = __ldg(ksb + r + 8 * e);
+                    vsr[e] = __ldg(vsb + r + 8 * e);
+                }
+                return;
+            }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const uint32_t r = slot(j0 + g + 8 * e);
@@ -547,26 +573,33 @@ quant_decode_kernel(const QuantDecodeArgs a)
                 vsr[e] = __ldg(vsb + r);
             }
         };
-        auto load_v = [&](int j0) {
+        auto take_v = [&](int e, const uint8_t *p) {
+            if constexpr (D == 64) {
+                const uint2 v = ldg_stream8(p);
+                vr[e][0] = v.x;
+                vr[e][1] = v.y;
+            } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t r = slot(j0 + 2 * t + (e & 1) + 8 * (e >> 1));
-                const uint8_t *p = vb + (uint64_t)r * D;
-                if constexpr (D == 64) {
-                    const uint2 v = ldg_stream8(p);
-                    vr[e][0] = v.x;
-                    vr[e][1] = v.y;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < D / 128; ++i) {
-                        const uint4 v = ldg_stream(p + 128 * i);
-                        vr[e][4 * i] = v.x;
-                        vr[e][4 * i + 1] = v.y;
-                        vr[e][4 * i + 2] = v.z;
-                        vr[e][4 * i + 3] = v.w;
-                    }
+                for (int i = 0; i < D / 128; ++i) {
+                    const uint4 v = ldg_stream(p + 128 * i);
+                    vr[e][4 * i] = v.x;
+                    vr[e][4 * i + 1] = v.y;
+                    vr[e][4 * i + 2] = v.z;
+                    vr[e][4 * i + 3] = v.w;
                 }
             }
+        };
+        auto load_v = [&](int j0) {
+            if (in_line(j0)) {
+                const uint8_t *p = vb + (uint64_t)slot(j0 + 2 * t) * D;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    take_v(e, p + ((e & 1) + 8 * (e >> 1)) * D);
+                return;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                take_v(e, vb + (uint64_t)slot(j0 + 2 * t + (e & 1) + 8 * (e >> 1)) * D);
         };
         // the first keys are under way while the queries are made ready
         const int j_end = min(n, u1 * kUnit);
@@ -605,14 +638,25 @@ quant_decode_kernel(const QuantDecodeArgs a)
                 const int ex = min(max((int)(__float_as_uint(top) >> 23), 40), 250);
                 const float up = __uint_as_float((uint32_t)(127 + 14 + 127 - ex) << 23);
                 const float down = __uint_as_float((uint32_t)(ex - 14) << 23);
+                float sum = 0.f;
 #pragma unroll
                 for (int e = 0; e < PPL; ++e) {
                     __half *row = reinterpret_cast<__half *>(smem + r * SM::Q_PITCH);
-                    row[place(lane + 32 * e)] = __float2half_rn(lo[e] * up);
-                    row[place(D / 2 + lane + 32 * e)] = __float2half_rn(hi[e] * up);
+                    const __half x = __float2half_rn(lo[e] * up), y = __float2half_rn(hi[e] * up);
+                    row[place(lane + 32 * e)] = x;
+                    row[place(D / 2 + lane + 32 * e)] = y;
+                    sum += __half2float(x) + __half2float(y);
                 }
-                if (lane == 0)
-                    q_factor[r] = down;
+                if constexpr (FMT == KVC_INT8) {
+#pragma unroll
+                    for (int d = 16; d; d >>= 1)
+                        sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                }
+                if (lane == 0) {
+                    // score / scale of the key = factor * (products) - bias
+                    q_factor[r] = down * a.scale_log2 * (FMT == KVC_INT8 ? 16777216.f : 1.f);
+                    q_bias[r] = FMT == KVC_INT8 ? down * a.scale_log2 * 128.f * sum : 0.f;
+                }
             }
         }
         __syncthreads();
@@ -629,12 +673,14 @@ quant_decode_kernel(const QuantDecodeArgs a)
                 for (int st = 0; st < D / 16; ++st)
                     qf[hb][st] = q_frag(hb, st);
         }
-        float qs[HB][2];
+        float qs[HB][2], qb[HB][2];
 #pragma unroll
-        for (int hb = 0; hb < HB; ++hb) {
-            qs[hb][0] = q_factor[hb * 8 + 2 * t] * a.scale_log2;
-            qs[hb][1] = q_factor[hb * 8 + 2 * t + 1] * a.scale_log2;
-        }
+        for (int hb = 0; hb < HB; ++hb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                qs[hb][e] = q_factor[hb * 8 + 2 * t + e];
+                qb[hb][e] = q_bias[hb * 8 + 2 * t + e];
+            }
 
         float o[HB][D / 16][4], m[HB][2], mo[HB][2], l[HB][2];
 #pragma unroll
@@ -644,17 +690,19 @@ quant_decode_kernel(const QuantDecodeArgs a)
                 o[hb][i][0] = o[hb][i][1] = o[hb][i][2] = o[hb][i][3] = 0.f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                m[hb][e] = mo[hb][e] = -INFINITY;
+                m[hb][e] = mo[hb][e] = kNone;
                 l[hb][e] = 0.f;
             }
         }
 
         for (; j0 < j_end; j0 += kUnit) {
-            // ---- scores ----
-            float s[HB][4];
+            // ---- scores: two chains of products a head block ----
+            float s[HB][4], s2[HB][4];
 #pragma unroll
             for (int hb = 0; hb < HB; ++hb)
-                s[hb][0] = s[hb][1] = s[hb][2] = s[hb][3] = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    s[hb][e] = s2[hb][e] = 0.f;
 #pragma unroll
             for (int i = 0; i < KV4; ++i) {
                 const uint32_t wa[4] = {kr[0][i].x, kr[0][i].y, kr[0][i].z, kr[0][i].w};
@@ -662,8 +710,8 @@ quant_decode_kernel(const QuantDecodeArgs a)
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     uint32_t a0, a1, a2, a3;
-                    codes_to_halves<FMT>(wa[w], a0, a2);
-                    codes_to_halves<FMT>(wb[w], a1, a3);
+                    codes_to_halves<FMT, true>(wa[w], a0, a2);
+                    codes_to_halves<FMT, true>(wb[w], a1, a3);
 #pragma unroll
                     for (int hb = 0; hb < HB; ++hb) {
                         uint2 f;
@@ -671,46 +719,58 @@ quant_decode_kernel(const QuantDecodeArgs a)
                             f = qf[hb][4 * i + w];
                         else
                             f = q_frag(hb, 4 * i + w);
-                        mma_f16(s[hb], a0, a1, a2, a3, f.x, f.y);
+                        mma_f16(w & 1 ? s2[hb] : s[hb], a0, a1, a2, a3, f.x, f.y);
                     }
                 }
             }
+            const bool tail = j0 + 16 > n;
             const bool in0 = j0 + g < n, in1 = j0 + g + 8 < n;
             const float k0 = ksr[0], k1 = ksr[1];
             const float lv0 = fast_log2(vsr[0]), lv1 = fast_log2(vsr[1]);
             if (j0 + kUnit < j_end)
                 load_k(j0 + kUnit);
 
-            // ---- softmax ----
-            bool raise = false;
+            // ---- softmax: x = s - m, y = s + log2(vs) - mo ----
+            float x[HB][4], y[HB][4], top = kNone;
 #pragma unroll
             for (int hb = 0; hb < HB; ++hb) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    s[hb][e] = in0 ? s[hb][e] * (k0 * qs[hb][e]) : -INFINITY;
-                    s[hb][2 + e] = in1 ? s[hb][2 + e] * (k1 * qs[hb][e]) : -INFINITY;
-                    raise |= fmaxf(s[hb][e], s[hb][2 + e]) > m[hb][e] + kSlack ||
-                             fmaxf(s[hb][e] + lv0, s[hb][2 + e] + lv1) > mo[hb][e] + kSlack;
+                for (int e = 0; e < 4; ++e) {
+                    const float sum = s[hb][e] + s2[hb][e];
+                    s[hb][e] = (FMT == KVC_INT8 ? fmaf(sum, qs[hb][e & 1], -qb[hb][e & 1]) : sum * qs[hb][e & 1]) *
+                               (e < 2 ? k0 : k1);
+                    if (tail)
+                        s[hb][e] = (e < 2 ? in0 : in1) ? s[hb][e] : -INFINITY;
+                    x[hb][e] = s[hb][e] - m[hb][e & 1];
+                    y[hb][e] = s[hb][e] + (e < 2 ? lv0 : lv1) - mo[hb][e & 1];
+                    top = fmaxf(top, fmaxf(x[hb][e], y[hb][e]));
                 }
             }
-            if (__any_sync(0xffffffffu, raise)) {
+            if (__any_sync(0xffffffffu, top > kSlack)) {
+                // a reference is left behind: raise both to the tile's maxima
 #pragma unroll
                 for (int hb = 0; hb < HB; ++hb) {
                     float shrink[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float top = fmaxf(s[hb][e], s[hb][2 + e]);
-                        float top_o = fmaxf(s[hb][e] + lv0, s[hb][2 + e] + lv1);
+                        float mx = fmaxf(s[hb][e], s[hb][2 + e]), my = fmaxf(s[hb][e] + lv0, s[hb][2 + e] + lv1);
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) {
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                            top_o = fmaxf(top_o, __shfl_xor_sync(0xffffffffu, top_o, d));
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                            my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, d));
                         }
-                        const float m_new = fmaxf(m[hb][e], top), mo_new = fmaxf(mo[hb][e], top_o);
-                        l[hb][e] *= m[hb][e] == m_new ? 1.f : fast_exp2(m[hb][e] - m_new);
-                        shrink[e] = mo[hb][e] == mo_new ? 1.f : fast_exp2(mo[hb][e] - mo_new);
-                        m[hb][e] = m_new;
-                        mo[hb][e] = mo_new;
+                        // (fmaxf drops a NaN: the references stay numbers)
+                        mx = fmaxf(mx, m[hb][e]);
+                        my = fmaxf(my, mo[hb][e]);
+                        l[hb][e] *= fast_exp2(m[hb][e] - mx);
+                        shrink[e] = fast_exp2(mo[hb][e] - my);
+                        m[hb][e] = mx;
+                        mo[hb][e] = my;
+#pragma unroll
+                        for (int u = 0; u < 4; u += 2) {
+                            x[hb][u + e] = s[hb][u + e] - m[hb][e];
+                            y[hb][u + e] = s[hb][u + e] + (u ? lv1 : lv0) - mo[hb][e];
+                        }
                     }
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {
@@ -724,16 +784,11 @@ quant_decode_kernel(const QuantDecodeArgs a)
             uint32_t b0[HB], b1[HB];
 #pragma unroll
             for (int hb = 0; hb < HB; ++hb) {
-                float w[4];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float rm = m[hb][e] == -INFINITY ? 0.f : m[hb][e];
-                    const float ro = mo[hb][e] == -INFINITY ? 0.f : mo[hb][e];
-                    l[hb][e] += fast_exp2(s[hb][e] - rm) + fast_exp2(s[hb][2 + e] - rm);
-                    w[e] = fast_exp2(s[hb][e] + lv0 - ro);
-                    w[2 + e] = fast_exp2(s[hb][2 + e] + lv1 - ro);
-                }
-                const __half2 h0 = __floats2half2_rn(w[0], w[1]), h1 = __floats2half2_rn(w[2], w[3]);
+                for (int e = 0; e < 2; ++e)
+                    l[hb][e] += fast_exp2(x[hb][e]) + fast_exp2(x[hb][2 + e]);
+                const __half2 h0 = __floats2half2_rn(fast_exp2(y[hb][0]), fast_exp2(y[hb][1]));
+                const __half2 h1 = __floats2half2_rn(fast_exp2(y[hb][2]), fast_exp2(y[hb][3]));
                 b0[hb] = movm_trans(*reinterpret_cast<const uint32_t *>(&h0));
                 b1[hb] = movm_trans(*reinterpret_cast<const uint32_t *>(&h1));
             }
@@ -780,8 +835,7 @@ quant_decode_kernel(const QuantDecodeArgs a)
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w)
                     top = fmaxf(top, m_sh[w * HEADS + hb * 8 + 2 * t + e]);
-                // O is relative to mo; a warp without keys holds zeros
-                f[hb][e] = mo[hb][e] == -INFINITY ? (m[hb][e] == -INFINITY ? 1.f : 0.f) : exp2f(mo[hb][e] - top);
+                f[hb][e] = exp2f(mo[hb][e] - top);  // O is relative to mo
             }
         {
             // tile i holds columns 2 i and 2 i + 1 of the lane's run of consecutive columns
@@ -809,9 +863,7 @@ quant_decode_kernel(const QuantDecodeArgs a)
                 top = fmaxf(top, m_sh[w * HEADS + r]);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float mw = m_sh[w * HEADS + r];
-                // (a warp whose scores are all NaN keeps m = -inf and a NaN sum)
-                sum += l_sh[w * HEADS + r] * (mw == top || mw == -INFINITY ? 1.f : exp2f(mw - top));
+                sum += l_sh[w * HEADS + r] * exp2f(m_sh[w * HEADS + r] - top);
             }
             float v = 0.f;
 #pragma unroll
@@ -890,8 +942,7 @@ quant_merge_kernel(const QuantDecodeArgs a)
         top = fmaxf(top, red[0][w]);
     float sum = 0.f;
     for (int i = threadIdx.x; i < n; i += kMergeThreads) {
-        // (a part whose scores are all NaN has m = -inf and a NaN sum, which has to be seen)
-        const float m = w_sh[i], w = m == top || m == -INFINITY ? 1.f : exp2f(m - top);
+        const float w = exp2f(w_sh[i] - top);
         w_sh[i] = w;
         sum += w * a.ws_l[part(i)];
     }
@@ -1011,7 +1062,7 @@ template <typename T> kvc_status launch_append(const AppendArgs &a, int format, 
 template <typename T> kvc_status launch_dequant(const DequantArgs &a, int format, cudaStream_t stream)
 {
     // a block for every kRowsAhead * rpb rows, at most 64 an SM over all slices of K and V
-    const int slices = a.batch * a.kv_heads, rpb = 256 / (a.D / 16);
+    const int slices = a.batch * a.kv_heads, rpb = 256 / (a.D / 8);
     int64_t nx = (std::min(a.C, a.R) + kRowsAhead * rpb - 1) / (kRowsAhead * rpb);
     nx = std::min<int64_t>(nx, (int64_t)kvc_host::sm_count() * 64 / (2 * slices) + 1);
     const dim3 grid((unsigned)nx, slices, 2);
