@@ -167,8 +167,10 @@ page_bounds_kernel(const BoundsArgs a)
 // selection
 // --------------------------------------------------------------------------
 
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 256;
 constexpr int kMaxPages = 49152;   // pages a sequence may have: their scores stay in shared memory
+constexpr int kMaxCluster = 8;
+constexpr int kPagesPerCta = 128;  // pages from which a row is worth another CTA
 
 struct SelectArgs {
     const void *q;
@@ -222,38 +224,71 @@ __device__ __forceinline__ int block_scan(int v, int *warp_sum, int &before)
     return total;
 }
 
-// One block per (batch row, kv head).
+// thread-block clusters: rank, size, barrier, and a 32-bit load from the shared
+// memory of another CTA of the cluster
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_load(const uint32_t *p, uint32_t rank)
+{
+    uint32_t at, v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(kvc::smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+
+// One cluster per (batch row, kv head), of one CTA for every kPagesPerCta pages that
+// the table holds, eight at most: each CTA scores a run of the pages and keeps the
+// scores in its shared memory.  The page ids are fetched first and kAhead pages'
+// bounds are under way at once (with one CTA a row and a page at a time, two loads
+// one after the other for each, 64 rows of 2048 pages took 71 us).  The rest-th
+// largest score is found 8 bits at a time from the histograms of all CTAs.
 template <typename T, int D>
 __global__ void __launch_bounds__(kSelThreads)
-page_select_kernel(const SelectArgs a)
+page_select_kernel(const SelectArgs a, int run_max)
 {
-    extern __shared__ uint32_t keys[];            // the middle pages' scores, as order_key
+    extern __shared__ uint32_t keys[];            // the run's scores, as order_key, then its page ids
     __shared__ float part[2][D];                  // sums of the positive and negative parts
     __shared__ __align__(16) int8_t code[2 * D];  // their codes
     __shared__ int warp_sum[kSelThreads / 32];
-    __shared__ uint32_t hist[256];
-    __shared__ uint32_t pick[2];
+    __shared__ uint32_t hist[2][256];
+    __shared__ uint32_t pick[2], taken[2];        // taken: pages above the last key, pages with it
     __shared__ float top_sh[kSelThreads / 32];
-    const int h = blockIdx.x, b = blockIdx.y, row = b * a.kv_heads + h;
+    int32_t *ids = reinterpret_cast<int32_t *>(keys + run_max);
+    const uint32_t rank = cluster_rank(), ctas = cluster_size();
+    const int h = blockIdx.x / ctas, b = blockIdx.y, row = b * a.kv_heads + h;
+    const int tid = threadIdx.x;
     const int total = a.len.total_abs[b];
     int L = a.len.cache_total[b];
-    const bool lead = threadIdx.x == 0 && h == 0;
+    const bool lead = tid == 0 && rank == 0;
     if (L >= 0 && (total < 1 || total > (int64_t)a.max_pages * a.page_size)) {
-        if (lead)
+        if (lead && h == 0)
             kvc::raise_status(a.status, KVC_DEV_CAPACITY);
         L = -1;
     }
     if (L >= 0 && a.cos_t && (int64_t)total > a.rope_max_pos) {
-        if (lead)
+        if (lead && h == 0)
             kvc::raise_status(a.status, KVC_DEV_ROPE_RANGE);
         L = -1;
     }
     int32_t *sel = a.selected + (int64_t)row * a.n_select, *sub = a.sub_table + (int64_t)row * a.n_select;
-    if (L < 0) {
-        if (threadIdx.x == 0) {
+    if (L < 0) {  // (every CTA of the cluster)
+        if (lead)
             a.sub_len.past_abs[row] = a.sub_len.total_abs[row] = a.sub_len.cache_past[row] =
                 a.sub_len.cache_total[row] = a.sub_len.evict[row] = -1;
-        }
         return;
     }
     const int pages = (total + a.page_size - 1) / a.page_size;
@@ -262,20 +297,38 @@ page_select_kernel(const SelectArgs a)
     const int tail = max(0, pages - a.recent), sink = min(a.sink, tail);
     const int rest = take - sink - (pages - tail);  // to choose out of [sink, tail)
     const int middle = tail - sink;
+    const bool choose = rest > 0 && rest < middle;
+    // this CTA's run of the middle pages
+    const int run = (middle + (int)ctas - 1) / (int)ctas;
+    const int first = sink + min(middle, (int)rank * run), mine = min(run, tail - first);
+    const int32_t *table = a.table + (int64_t)b * a.max_pages;
+    auto sub_page = [&](int32_t id) {
+        // an id outside the pool stays outside the one-head pool
+        return id < 0 || id >= a.n_pool ? -1 : (int32_t)((int64_t)id * a.kv_heads + h);
+    };
+    for (int j = tid; j < mine; j += kSelThreads)
+        ids[j] = __ldg(table + first + j);
+
     uint32_t least = 0;   // a page with a key above it is taken,
     int ties = 0;         // and the first `ties` pages with that key
-    if (rest > 0 && rest < middle) {
+    if (choose) {
         // ---- the group's query, in 8 bits ----
-        if (threadIdx.x < D / 2) {
-            const int p = threadIdx.x;
+        if (tid < D / 2) {
+            const int p = tid;
             const int64_t pos = (int64_t)total - 1;
             const T *q = static_cast<const T *>(a.q) + (int64_t)row * a.group * D;
+            float cs = 1.f, sn = 0.f;
+            if (a.cos_t) {
+                cs = __ldg(a.cos_t + pos * (D / 2) + p);
+                sn = __ldg(a.sin_t + pos * (D / 2) + p);
+            }
             // in 64 bits, so that a sum does not hang on the order of the heads
             double up[2] = {0., 0.}, down[2] = {0., 0.};
+#pragma unroll 4
             for (int r = 0; r < a.group; ++r) {
                 float x[2] = {kvc::Elem<T>::to_f32(q[r * D + p]), kvc::Elem<T>::to_f32(q[r * D + D / 2 + p])};
                 if (a.cos_t)
-                    kvc::rope_pair(x[0], x[1], a.cos_t[pos * (D / 2) + p], a.sin_t[pos * (D / 2) + p]);
+                    kvc::rope_pair(x[0], x[1], cs, sn);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     up[e] += x[e] > 0.f ? x[e] : 0.f;
@@ -290,129 +343,159 @@ page_select_kernel(const SelectArgs a)
         }
         __syncthreads();
         float top = 0.f;
-        for (int i = threadIdx.x; i < 2 * D; i += kSelThreads)
+        for (int i = tid; i < 2 * D; i += kSelThreads)
             top = fmaxf(top, fabsf(part[i / D][i % D]));
 #pragma unroll
         for (int d = 16; d; d >>= 1)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        if ((threadIdx.x & 31) == 0)
-            top_sh[threadIdx.x >> 5] = top;
+        if ((tid & 31) == 0)
+            top_sh[tid >> 5] = top;
         __syncthreads();
+#pragma unroll
         for (int w = 0; w < kSelThreads / 32; ++w)
             top = fmaxf(top, top_sh[w]);
         const float sq = __fdiv_rn(top, 127.f);
-        for (int i = threadIdx.x; i < 2 * D; i += kSelThreads) {
+        for (int i = tid; i < 2 * D; i += kSelThreads) {
             const float x = part[i / D][i % D];
             code[i] = (int8_t)(sq > 0.f ? max(-127, min(127, __float2int_rn(__fdiv_rn(x, sq)))) : 0);
         }
         __syncthreads();
 
         // ---- scores: 16 codes a lane, D / 8 lanes a page ----
-        constexpr int LPP = D / 8;
-        const int sub_lane = threadIdx.x % LPP;
+        constexpr int LPP = D / 8, PPB = kSelThreads / LPP, kAhead = 4;
+        const int sub_lane = tid % LPP;
         const uint4 qc = reinterpret_cast<const uint4 *>(code)[sub_lane];
-        constexpr int PPB = kSelThreads / LPP;
-        for (int j0 = 0; j0 < middle; j0 += PPB) {
-            const int j = j0 + threadIdx.x / LPP;
-            int sum = 0;
-            float s = 0.f;
-            bool bad = false;
-            if (j < middle) {
-                const int64_t id = a.table[(int64_t)b * a.max_pages + sink + j];
-                bad = id < 0 || id >= a.n_pool;
-                if (!bad) {
-                    const int64_t slice = id * a.kv_heads + h;
-                    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(a.bounds + slice * 2 * D) + sub_lane);
-                    sum = __dp4a((int)v.x, (int)qc.x, 0);
-                    sum = __dp4a((int)v.y, (int)qc.y, sum);
-                    sum = __dp4a((int)v.z, (int)qc.z, sum);
-                    sum = __dp4a((int)v.w, (int)qc.w, sum);
-                    s = __ldg(a.scale + slice);
-                }
+        for (int j0 = tid / LPP; j0 - tid / LPP < mine; j0 += kAhead * PPB) {
+            uint4 v[kAhead];
+            float s[kAhead];
+            bool bad[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int32_t id = ids[min(j0 + u * PPB, mine - 1)];
+                bad[u] = id < 0 || id >= a.n_pool;
+                const int64_t slice = (int64_t)(bad[u] ? 0 : id) * a.kv_heads + h;
+                v[u] = __ldg(reinterpret_cast<const uint4 *>(a.bounds + slice * 2 * D) + sub_lane);
+                s[u] = __ldg(a.scale + slice);
             }
 #pragma unroll
-            for (int d = 1; d < LPP; d <<= 1)
-                sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            if (j < middle && sub_lane == 0) {
-                if (bad)
-                    kvc::raise_status(a.status, KVC_DEV_INDEX_OOB);
-                // a page that does not exist orders first too: the attention reports it
-                keys[j] = bad || isinf(s) ? 0xffffffffu : order_key(__fmul_rn(s, (float)sum));
+            for (int u = 0; u < kAhead; ++u) {
+                int sum = __dp4a((int)v[u].x, (int)qc.x, 0);
+                sum = __dp4a((int)v[u].y, (int)qc.y, sum);
+                sum = __dp4a((int)v[u].z, (int)qc.z, sum);
+                sum = __dp4a((int)v[u].w, (int)qc.w, sum);
+#pragma unroll
+                for (int d = 1; d < LPP; d <<= 1)
+                    sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                const int j = j0 + u * PPB;
+                if (j < mine && sub_lane == 0) {
+                    if (bad[u])
+                        kvc::raise_status(a.status, KVC_DEV_INDEX_OOB);
+                    // a page that does not exist orders first too: the attention reports it
+                    keys[j] = bad[u] || isinf(s[u]) ? 0xffffffffu : order_key(__fmul_rn(s[u], (float)sum));
+                }
             }
         }
-        __syncthreads();
 
         // ---- the rest-th largest key, 8 bits at a time ----
         uint32_t prefix = 0, mask = 0;
         int want = rest;
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            if (threadIdx.x < 256)
-                hist[threadIdx.x] = 0;
-            __syncthreads();
-            for (int j = threadIdx.x; j < middle; j += kSelThreads)
+        hist[0][tid] = 0;
+        for (int pass = 0; pass < 4; ++pass) {
+            const int shift = 24 - 8 * pass;
+            uint32_t *bins = hist[pass & 1];
+            __syncthreads();  // the scores, and zeros in the bins
+            for (int j = tid; j < mine; j += kSelThreads)
                 if ((keys[j] & mask) == prefix)
-                    atomicAdd(&hist[keys[j] >> shift & 255u], 1u);
-            __syncthreads();
-            // bins from the top: thread i looks at bin 255 - i
-            const int n = threadIdx.x < 256 ? (int)hist[255 - threadIdx.x] : 0;
+                    atomicAdd(&bins[keys[j] >> shift & 255u], 1u);
+            cluster_sync();
+            // (every CTA has passed the pass before, in which it read the other bins)
+            hist[(pass + 1) & 1][tid] = 0;
+            // bins from the top: thread i looks at bin 255 - i of every CTA
+            int n = 0;
+            for (uint32_t c = 0; c < ctas; ++c)
+                n += (int)cluster_load(&bins[255 - tid], c);
             int before;
             block_scan(n, warp_sum, before);
-            if (threadIdx.x < 256 && before < want && before + n >= want) {
-                pick[0] = 255 - threadIdx.x;
+            if (before < want && before + n >= want) {
+                pick[0] = 255 - tid;
                 pick[1] = want - before;
             }
             __syncthreads();
             prefix |= pick[0] << shift;
             mask |= 255u << shift;
             want = (int)pick[1];
-            __syncthreads();
         }
         least = prefix;
         ties = want;
-    }
-
-    // ---- the chosen pages in ascending order ----
-    // (rest == middle: all of them; rest <= 0: none of the middle)
-    int out = 0, tied = 0;
-    for (int j0 = 0; j0 < pages; j0 += kSelThreads) {
-        const int j = j0 + threadIdx.x;
-        bool chosen = false, tie = false;
-        if (j < pages) {
-            if (j < sink || j >= tail)
-                chosen = true;
-            else if (rest >= middle)
-                chosen = true;
-            else if (rest > 0) {
-                chosen = keys[j - sink] > least;
-                tie = keys[j - sink] == least;
+        if (tid < 2)
+            taken[tid] = 0;
+        __syncthreads();
+        for (int j0 = 0; j0 < mine; j0 += kSelThreads) {
+            const int j = j0 + tid;
+            const uint32_t above = __ballot_sync(0xffffffffu, j < mine && keys[j] > least);
+            const uint32_t same = __ballot_sync(0xffffffffu, j < mine && keys[j] == least);
+            if ((tid & 31) == 0) {
+                atomicAdd(&taken[0], __popc(above));
+                atomicAdd(&taken[1], __popc(same));
             }
         }
-        int before;
-        const int n_tie = block_scan(tie, warp_sum, before);
-        if (tie && tied + before < ties)
-            chosen = true;
-        tied += n_tie;
-        const int n = block_scan(chosen, warp_sum, before);
-        if (chosen && out + before < a.n_select) {
-            const int64_t id = a.table[(int64_t)b * a.max_pages + j];
-            sel[out + before] = j;
-            // an id outside the pool stays outside the one-head pool
-            sub[out + before] = id < 0 || id >= a.n_pool ? -1 : (int32_t)(id * a.kv_heads + h);
+    } else {
+        __syncthreads();  // the ids
+    }
+
+    // ---- the chosen pages in ascending order: the runs before this one's go first ----
+    int out = sink, tied = 0;
+    if (choose) {
+        cluster_sync();
+        for (uint32_t c = 0; c < rank; ++c) {
+            const int above = (int)cluster_load(&taken[0], c), same = (int)cluster_load(&taken[1], c);
+            out += above + max(0, min(same, ties - tied));
+            tied += same;
         }
-        out += n;
+        // no CTA leaves while another may read its shared memory
+        cluster_sync();
+    } else if (rest > 0) {
+        out += first - sink;  // all of the middle
     }
-    for (int i = take + threadIdx.x; i < a.n_select; i += kSelThreads) {
-        sel[i] = -1;
-        sub[i] = -1;
+    if (rest > 0) {
+        for (int j0 = 0; j0 < mine; j0 += kSelThreads) {
+            const int j = j0 + tid;
+            bool chosen = j < mine;
+            if (choose) {
+                const bool tie = j < mine && keys[j] == least;
+                int before;
+                const int n_tie = block_scan(tie, warp_sum, before);
+                chosen = j < mine && (keys[j] > least || (tie && tied + before < ties));
+                tied += n_tie;
+            }
+            int before;
+            const int n = block_scan(chosen, warp_sum, before);
+            if (chosen) {
+                sel[out + before] = first + j;
+                sub[out + before] = sub_page(ids[j]);
+            }
+            out += n;
+        }
     }
-    if (threadIdx.x == 0) {
-        // the page of the newest token is the last one taken
-        const int rows = (take - 1) * a.page_size + total - (pages - 1) * a.page_size;
-        a.sub_len.past_abs[row] = total - 1;
-        a.sub_len.total_abs[row] = total;
-        a.sub_len.cache_past[row] = rows - 1;
-        a.sub_len.cache_total[row] = rows;
-        a.sub_len.evict[row] = 0;
+    if (rank == 0) {
+        for (int j = tid; j < sink; j += kSelThreads) {
+            sel[j] = j;
+            sub[j] = sub_page(__ldg(table + j));
+        }
+        for (int i = tid; i < a.n_select - (take - (pages - tail)); i += kSelThreads) {
+            const int at = take - (pages - tail) + i, j = tail + i;
+            sel[at] = j < pages ? j : -1;
+            sub[at] = j < pages ? sub_page(__ldg(table + j)) : -1;
+        }
+        if (tid == 0) {
+            // the page of the newest token is the last one taken
+            const int rows = (take - 1) * a.page_size + total - (pages - 1) * a.page_size;
+            a.sub_len.past_abs[row] = total - 1;
+            a.sub_len.total_abs[row] = total;
+            a.sub_len.cache_past[row] = rows - 1;
+            a.sub_len.cache_total[row] = rows;
+            a.sub_len.evict[row] = 0;
+        }
     }
 }
 
@@ -442,11 +525,27 @@ bool sizes_ok(int batch, int q_heads, int kv_heads, int page_size, int n_select,
 
 template <typename T, int D> kvc_status launch_select_dim(const SelectArgs &a, cudaStream_t stream)
 {
-    const int smem = a.max_pages * 4;
+    int ctas = 1;
+    while (ctas < kMaxCluster && ctas * kPagesPerCta < a.max_pages)
+        ctas *= 2;
+    const int run = (a.max_pages + ctas - 1) / ctas, smem = run * 8;
     if (smem > 32 * 1024 && cudaFuncSetAttribute(page_select_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  smem) != cudaSuccess)
         return KVC_ERR_CUDA;
-    page_select_kernel<T, D><<<dim3(a.kv_heads, a.batch), kSelThreads, smem, stream>>>(a);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(a.kv_heads * ctas, a.batch);
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = ctas;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, page_select_kernel<T, D>, a, run) != cudaSuccess)
+        return KVC_ERR_CUDA;
     return kvc_host::launch_status();
 }
 
