@@ -224,8 +224,7 @@ __device__ __forceinline__ int block_scan(int v, int *warp_sum, int &before)
     return total;
 }
 
-// thread-block clusters: rank, size, barrier, and a 32-bit load from the shared
-// memory of another CTA of the cluster
+// thread-block clusters: rank, size, barrier, and a 32-bit store
 __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
@@ -242,32 +241,48 @@ __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ uint32_t cluster_load(const uint32_t *p, uint32_t rank)
+// into the shared memory of another CTA of the cluster, at the place of p in this one's
+__device__ __forceinline__ void cluster_store(const uint32_t *p, uint32_t rank, uint32_t v)
 {
-    uint32_t at, v;
+    uint32_t at;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(kvc::smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-    return v;
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
 
+// A sum and what its roundings dropped (Knuth's exact two-term sum): 48 bits, on a
+// part whose 64-bit arithmetic takes a warp's addition in 16 clocks
+struct Sum2 {
+    float hi = 0.f, lo = 0.f;
+    __device__ __forceinline__ void add(float x)
+    {
+        const float s = __fadd_rn(hi, x), z = __fsub_rn(s, hi);
+        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, z)), __fsub_rn(x, z)));
+        hi = s;
+    }
+};
+
 // One cluster per (batch row, kv head), of one CTA for every kPagesPerCta pages that
-// the table holds, eight at most: each CTA scores a run of the pages and keeps the
-// scores in its shared memory.  The page ids are fetched first and kAhead pages'
-// bounds are under way at once (with one CTA a row and a page at a time, two loads
-// one after the other for each, 64 rows of 2048 pages took 71 us).  The rest-th
-// largest score is found 8 bits at a time from the histograms of all CTAs.
+// the table holds, eight at most: each CTA scores a run of the pages and sends the
+// scores to the first one, which chooses alone.  kAhead pages' bounds are under way
+// for each group of lanes, the first of them while the query's codes are made.
+// The choice is that of the rest-th largest key, found 8 bits at a time below the
+// highest bit in which the keys differ (keys are close together: on their leading
+// bits a histogram is one bin, and its atomics one queue).
+// 64 rows of up to 2048 pages took 71 us with one CTA a row and a page at a time,
+// 24 us with the histograms of eight CTAs joined at every step.
 template <typename T, int D>
 __global__ void __launch_bounds__(kSelThreads)
 page_select_kernel(const SelectArgs a, int run_max)
 {
-    extern __shared__ uint32_t keys[];            // the run's scores, as order_key, then its page ids
+    extern __shared__ uint32_t keys[];            // [max_pages] scores as order_key, then the run's page ids
     __shared__ float part[2][D];                  // sums of the positive and negative parts
     __shared__ __align__(16) int8_t code[2 * D];  // their codes
     __shared__ int warp_sum[kSelThreads / 32];
-    __shared__ uint32_t hist[2][256];
-    __shared__ uint32_t pick[2], taken[2];        // taken: pages above the last key, pages with it
+    __shared__ uint32_t hist[256];
+    __shared__ uint32_t pick[2];
     __shared__ float top_sh[kSelThreads / 32];
-    int32_t *ids = reinterpret_cast<int32_t *>(keys + run_max);
+    __shared__ uint32_t edge_sh[2][kSelThreads / 32];
+    int32_t *ids = reinterpret_cast<int32_t *>(keys + a.max_pages);
     const uint32_t rank = cluster_rank(), ctas = cluster_size();
     const int h = blockIdx.x / ctas, b = blockIdx.y, row = b * a.kv_heads + h;
     const int tid = threadIdx.x;
@@ -298,20 +313,40 @@ page_select_kernel(const SelectArgs a, int run_max)
     const int rest = take - sink - (pages - tail);  // to choose out of [sink, tail)
     const int middle = tail - sink;
     const bool choose = rest > 0 && rest < middle;
-    // this CTA's run of the middle pages
-    const int run = (middle + (int)ctas - 1) / (int)ctas;
-    const int first = sink + min(middle, (int)rank * run), mine = min(run, tail - first);
+    if (!choose && rank > 0)
+        return;
     const int32_t *table = a.table + (int64_t)b * a.max_pages;
-    auto sub_page = [&](int32_t id) {
-        // an id outside the pool stays outside the one-head pool
-        return id < 0 || id >= a.n_pool ? -1 : (int32_t)((int64_t)id * a.kv_heads + h);
-    };
-    for (int j = tid; j < mine; j += kSelThreads)
-        ids[j] = __ldg(table + first + j);
-
-    uint32_t least = 0;   // a page with a key above it is taken,
-    int ties = 0;         // and the first `ties` pages with that key
     if (choose) {
+        // (the first CTA has to run before another writes into it: the wait is below)
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+        // this CTA's run of the middle pages
+        const int run = (middle + (int)ctas - 1) / (int)ctas;
+        const int first = min(middle, (int)rank * run), mine = min(run, middle - first);
+        for (int j = tid; j < mine; j += kSelThreads)
+            ids[j] = __ldg(table + sink + first + j);
+        __syncthreads();
+
+        // ---- bounds: 16 codes a lane, D / 8 lanes a page ----
+        constexpr int LPP = D / 8, PPB = kSelThreads / LPP, kAhead = 8;
+        const int sub_lane = tid % LPP;
+        uint4 v[kAhead];
+        float s[kAhead];
+        uint32_t bad = 0;
+        auto fetch = [&](int j0) {
+            bad = 0;
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int32_t id = ids[min(j0 + u * PPB, mine - 1)];
+                const bool out = id < 0 || id >= a.n_pool;
+                bad |= (uint32_t)out << u;
+                const int64_t slice = (int64_t)(out ? 0 : id) * a.kv_heads + h;
+                v[u] = __ldg(reinterpret_cast<const uint4 *>(a.bounds + slice * 2 * D) + sub_lane);
+                s[u] = __ldg(a.scale + slice);
+            }
+        };
+        if (mine > 0)
+            fetch(tid / LPP);
+
         // ---- the group's query, in 8 bits ----
         if (tid < D / 2) {
             const int p = tid;
@@ -322,8 +357,8 @@ page_select_kernel(const SelectArgs a, int run_max)
                 cs = __ldg(a.cos_t + pos * (D / 2) + p);
                 sn = __ldg(a.sin_t + pos * (D / 2) + p);
             }
-            // in 64 bits, so that a sum does not hang on the order of the heads
-            double up[2] = {0., 0.}, down[2] = {0., 0.};
+            // in twice the digits, so that a sum does not hang on the order of the heads
+            Sum2 up[2], down[2];
 #pragma unroll 4
             for (int r = 0; r < a.group; ++r) {
                 float x[2] = {kvc::Elem<T>::to_f32(q[r * D + p]), kvc::Elem<T>::to_f32(q[r * D + D / 2 + p])};
@@ -331,14 +366,14 @@ page_select_kernel(const SelectArgs a, int run_max)
                     kvc::rope_pair(x[0], x[1], cs, sn);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    up[e] += x[e] > 0.f ? x[e] : 0.f;
-                    down[e] += x[e] < 0.f ? x[e] : 0.f;
+                    up[e].add(x[e] > 0.f ? x[e] : 0.f);
+                    down[e].add(x[e] < 0.f ? x[e] : 0.f);
                 }
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                part[0][p + e * (D / 2)] = (float)up[e];
-                part[1][p + e * (D / 2)] = (float)down[e];
+                part[0][p + e * (D / 2)] = __fadd_rn(up[e].hi, up[e].lo);
+                part[1][p + e * (D / 2)] = __fadd_rn(down[e].hi, down[e].lo);
             }
         }
         __syncthreads();
@@ -361,22 +396,10 @@ page_select_kernel(const SelectArgs a, int run_max)
         }
         __syncthreads();
 
-        // ---- scores: 16 codes a lane, D / 8 lanes a page ----
-        constexpr int LPP = D / 8, PPB = kSelThreads / LPP, kAhead = 4;
-        const int sub_lane = tid % LPP;
+        // ---- scores, to the first CTA ----
+        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
         const uint4 qc = reinterpret_cast<const uint4 *>(code)[sub_lane];
         for (int j0 = tid / LPP; j0 - tid / LPP < mine; j0 += kAhead * PPB) {
-            uint4 v[kAhead];
-            float s[kAhead];
-            bool bad[kAhead];
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int32_t id = ids[min(j0 + u * PPB, mine - 1)];
-                bad[u] = id < 0 || id >= a.n_pool;
-                const int64_t slice = (int64_t)(bad[u] ? 0 : id) * a.kv_heads + h;
-                v[u] = __ldg(reinterpret_cast<const uint4 *>(a.bounds + slice * 2 * D) + sub_lane);
-                s[u] = __ldg(a.scale + slice);
-            }
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 int sum = __dp4a((int)v[u].x, (int)qc.x, 0);
@@ -388,114 +411,118 @@ page_select_kernel(const SelectArgs a, int run_max)
                     sum += __shfl_xor_sync(0xffffffffu, sum, d);
                 const int j = j0 + u * PPB;
                 if (j < mine && sub_lane == 0) {
-                    if (bad[u])
+                    const bool out = bad >> u & 1u;
+                    if (out)
                         kvc::raise_status(a.status, KVC_DEV_INDEX_OOB);
                     // a page that does not exist orders first too: the attention reports it
-                    keys[j] = bad[u] || isinf(s[u]) ? 0xffffffffu : order_key(__fmul_rn(s[u], (float)sum));
+                    cluster_store(keys + first + j, 0,
+                                  out || isinf(s[u]) ? 0xffffffffu : order_key(__fmul_rn(s[u], (float)sum)));
                 }
             }
+            if (j0 - tid / LPP + kAhead * PPB < mine)
+                fetch(j0 + kAhead * PPB);
         }
+        cluster_sync();
+        if (rank > 0)
+            return;  // (nobody reads or writes this CTA's shared memory)
+    }
 
-        // ---- the rest-th largest key, 8 bits at a time ----
-        uint32_t prefix = 0, mask = 0;
+    // ---- the rest-th largest key ----
+    uint32_t least = 0;   // a page with a key above it is taken,
+    int ties = 0;         // and the first `ties` pages with that key
+    if (choose) {
+        uint32_t lo = 0xffffffffu, hi = 0;
+        for (int j = tid; j < middle; j += kSelThreads) {
+            lo = min(lo, keys[j]);
+            hi = max(hi, keys[j]);
+        }
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        if ((tid & 31) == 0) {
+            edge_sh[0][tid >> 5] = lo;
+            edge_sh[1][tid >> 5] = hi;
+        }
+        hist[tid] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kSelThreads / 32; ++w) {
+            lo = min(lo, edge_sh[0][w]);
+            hi = max(hi, edge_sh[1][w]);
+        }
+        int left = hi == lo ? 0 : 32 - __clz(hi - lo);  // bits of key - lo still to find
+        uint32_t prefix = 0;                            // the bits found, above them
         int want = rest;
-        hist[0][tid] = 0;
-        for (int pass = 0; pass < 4; ++pass) {
-            const int shift = 24 - 8 * pass;
-            uint32_t *bins = hist[pass & 1];
-            __syncthreads();  // the scores, and zeros in the bins
-            for (int j = tid; j < mine; j += kSelThreads)
-                if ((keys[j] & mask) == prefix)
-                    atomicAdd(&bins[keys[j] >> shift & 255u], 1u);
-            cluster_sync();
-            // (every CTA has passed the pass before, in which it read the other bins)
-            hist[(pass + 1) & 1][tid] = 0;
-            // bins from the top: thread i looks at bin 255 - i of every CTA
-            int n = 0;
-            for (uint32_t c = 0; c < ctas; ++c)
-                n += (int)cluster_load(&bins[255 - tid], c);
+        while (left > 0) {
+            const int shift = max(0, left - 8);
+            const uint32_t digit = (1u << (left - shift)) - 1;
+            for (int j = tid; j < middle; j += kSelThreads) {
+                const uint32_t x = keys[j] - lo;
+                if (left == 32 || x >> left == prefix)
+                    atomicAdd(&hist[x >> shift & digit], 1u);
+            }
+            __syncthreads();
+            // bins from the top: thread i looks at bin 255 - i
+            const int n = (int)hist[255 - tid];
             int before;
             block_scan(n, warp_sum, before);
+            hist[255 - tid] = 0;
             if (before < want && before + n >= want) {
                 pick[0] = 255 - tid;
                 pick[1] = want - before;
             }
             __syncthreads();
-            prefix |= pick[0] << shift;
-            mask |= 255u << shift;
+            prefix = prefix << (left - shift) | pick[0];
             want = (int)pick[1];
+            left = shift;
         }
-        least = prefix;
+        least = lo + prefix;
         ties = want;
-        if (tid < 2)
-            taken[tid] = 0;
-        __syncthreads();
-        for (int j0 = 0; j0 < mine; j0 += kSelThreads) {
-            const int j = j0 + tid;
-            const uint32_t above = __ballot_sync(0xffffffffu, j < mine && keys[j] > least);
-            const uint32_t same = __ballot_sync(0xffffffffu, j < mine && keys[j] == least);
-            if ((tid & 31) == 0) {
-                atomicAdd(&taken[0], __popc(above));
-                atomicAdd(&taken[1], __popc(same));
-            }
-        }
-    } else {
-        __syncthreads();  // the ids
     }
 
-    // ---- the chosen pages in ascending order: the runs before this one's go first ----
-    int out = sink, tied = 0;
-    if (choose) {
-        cluster_sync();
-        for (uint32_t c = 0; c < rank; ++c) {
-            const int above = (int)cluster_load(&taken[0], c), same = (int)cluster_load(&taken[1], c);
-            out += above + max(0, min(same, ties - tied));
-            tied += same;
+    // ---- the chosen pages in ascending order: a run of pages a thread ----
+    {
+        const int each = (pages + kSelThreads - 1) / kSelThreads;
+        const int j0 = min(pages, tid * each), j1 = min(pages, j0 + each);
+        auto rank_of = [&](int j) {  // 2: taken, 1: taken if among the first of its key, 0: not
+            if (j < sink || j >= tail)
+                return 2;
+            if (!choose)
+                return rest > 0 ? 2 : 0;
+            return keys[j - sink] > least ? 2 : keys[j - sink] == least ? 1 : 0;
+        };
+        int sure = 0, tied = 0;
+        for (int j = j0; j < j1; ++j) {
+            const int k = rank_of(j);
+            sure += k >> 1;
+            tied += k & 1;
         }
-        // no CTA leaves while another may read its shared memory
-        cluster_sync();
-    } else if (rest > 0) {
-        out += first - sink;  // all of the middle
-    }
-    if (rest > 0) {
-        for (int j0 = 0; j0 < mine; j0 += kSelThreads) {
-            const int j = j0 + tid;
-            bool chosen = j < mine;
-            if (choose) {
-                const bool tie = j < mine && keys[j] == least;
-                int before;
-                const int n_tie = block_scan(tie, warp_sum, before);
-                chosen = j < mine && (keys[j] > least || (tie && tied + before < ties));
-                tied += n_tie;
+        int tied_before = 0, before;
+        if (choose)
+            block_scan(tied, warp_sum, tied_before);
+        block_scan(sure + max(0, min(tied, ties - tied_before)), warp_sum, before);
+        for (int j = j0; j < j1; ++j) {
+            const int k = rank_of(j);
+            if (k == 2 || (k == 1 && tied_before++ < ties)) {
+                const int32_t id = __ldg(table + j);
+                sel[before] = j;
+                // an id outside the pool stays outside the one-head pool
+                sub[before] = id < 0 || id >= a.n_pool ? -1 : (int32_t)((int64_t)id * a.kv_heads + h);
+                ++before;
             }
-            int before;
-            const int n = block_scan(chosen, warp_sum, before);
-            if (chosen) {
-                sel[out + before] = first + j;
-                sub[out + before] = sub_page(ids[j]);
-            }
-            out += n;
         }
     }
-    if (rank == 0) {
-        for (int j = tid; j < sink; j += kSelThreads) {
-            sel[j] = j;
-            sub[j] = sub_page(__ldg(table + j));
-        }
-        for (int i = tid; i < a.n_select - (take - (pages - tail)); i += kSelThreads) {
-            const int at = take - (pages - tail) + i, j = tail + i;
-            sel[at] = j < pages ? j : -1;
-            sub[at] = j < pages ? sub_page(__ldg(table + j)) : -1;
-        }
-        if (tid == 0) {
-            // the page of the newest token is the last one taken
-            const int rows = (take - 1) * a.page_size + total - (pages - 1) * a.page_size;
-            a.sub_len.past_abs[row] = total - 1;
-            a.sub_len.total_abs[row] = total;
-            a.sub_len.cache_past[row] = rows - 1;
-            a.sub_len.cache_total[row] = rows;
-            a.sub_len.evict[row] = 0;
-        }
+    for (int i = take + tid; i < a.n_select; i += kSelThreads) {
+        sel[i] = -1;
+        sub[i] = -1;
+    }
+    if (tid == 0) {
+        // the page of the newest token is the last one taken
+        const int rows = (take - 1) * a.page_size + total - (pages - 1) * a.page_size;
+        a.sub_len.past_abs[row] = total - 1;
+        a.sub_len.total_abs[row] = total;
+        a.sub_len.cache_past[row] = rows - 1;
+        a.sub_len.cache_total[row] = rows;
+        a.sub_len.evict[row] = 0;
     }
 }
 
@@ -528,7 +555,7 @@ template <typename T, int D> kvc_status launch_select_dim(const SelectArgs &a, c
     int ctas = 1;
     while (ctas < kMaxCluster && ctas * kPagesPerCta < a.max_pages)
         ctas *= 2;
-    const int run = (a.max_pages + ctas - 1) / ctas, smem = run * 8;
+    const int run = (a.max_pages + ctas - 1) / ctas, smem = (a.max_pages + run) * 4;
     if (smem > 32 * 1024 && cudaFuncSetAttribute(page_select_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  smem) != cudaSuccess)
         return KVC_ERR_CUDA;
