@@ -318,8 +318,8 @@ dequant_rows_kernel(const DequantArgs a)
 // one-token attention over the codes
 // --------------------------------------------------------------------------
 
-constexpr int kUnit = 64;           // keys of one unit of work: 16 for each warp
 constexpr int kWarps = 4;
+constexpr int kRowCost = 2;         // units (kvc_flat.cuh) that a row costs beside its keys
 constexpr float kNone = -1e30f;     // a reference maximum before any score (finite: differences stay numbers)
 constexpr float kSlack = 8.f;       // log2 units a score may exceed its reference by
 
@@ -335,6 +335,7 @@ struct QuantDecodeArgs {
     float scale_log2;
     const float *cos_t, *sin_t;
     int64_t rope_max_pos;
+    int unit;                        // keys of a unit of work
     int grid;                        // CTAs of the attention launch
     float *ws_o, *ws_m, *ws_l;       // [2 * grid][group] (x D)
     int32_t *status;
@@ -359,6 +360,13 @@ __device__ __forceinline__ int visible(const QuantDecodeArgs &a, int b, int64_t 
     const int n = a.window > 0 ? min(L, a.window) : L;
     first = a.ring ? (int64_t)(T - n) % a.C : (int64_t)(L - n);
     return n;
+}
+
+// Units of a row on the line that the CTAs share: its keys', and kRowCost that hold
+// none but stand for what a CTA spends on a row beside its keys.
+__device__ __forceinline__ int row_units(int n, int unit)
+{
+    return n > 0 ? (n + unit - 1) / unit + kRowCost : 0;
 }
 
 __device__ __forceinline__ float fast_exp2(float x)
@@ -432,43 +440,75 @@ __device__ __forceinline__ void pairs_of(uint32_t x, uint32_t y, int e, uint32_t
     codes_to_halves<FMT, false>(__byte_perm(x, y, sel[e]), first, second);
 }
 
-__device__ __forceinline__ uint4 ldg_stream(const uint8_t *p)
+// asynchronous copies to shared memory: 16 bytes of codes past L1, 4 of a scale
+__device__ __forceinline__ void copy16(uint32_t to, const uint8_t *from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t to, const float *from)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ uint4 lds16(uint32_t p)
 {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-        : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-        : "l"(p));
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p) : "memory");
     return v;
 }
-__device__ __forceinline__ uint2 ldg_stream8(const uint8_t *p)
+__device__ __forceinline__ uint2 lds8(uint32_t p)
 {
     uint2 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p) : "memory");
     return v;
 }
-
+// Tiles of 16 keys that a warp takes in one step: two where registers and shared
+// memory allow, whose chains of products, exponentials and conversions fill each
+// other's waits.  A unit of work is a step of the four warps.
+__host__ __device__ constexpr int tiles_of(int D, int HB) { return D * HB <= 128 ? 2 : 1; }
+__host__ __device__ constexpr int unit_of(int D, int HB) { return 16 * tiles_of(D, HB) * kWarps; }
 // resident CTAs an SM, by the registers that O and the query fragments take
-__host__ __device__ constexpr int ctas_per_sm(int D, int HB)
-{
-    return D * HB <= 128 ? 4 : D * HB <= 256 ? 3 : 2;
-}
+__host__ __device__ constexpr int ctas_per_sm(int D, int HB) { return D * HB <= 256 ? 3 : 2; }
 
 template <int D, int HB> struct QuantSmem {
     static constexpr int HEADS = 8 * HB;
     static constexpr int Q_PITCH = D * 2 + 8;     // bytes: a fragment's 16 half-warp reads hit 16 distinct 8-byte banks
     static constexpr int Q_BYTES = HEADS * Q_PITCH;
-    static constexpr int O_PITCH = D + 4;         // floats
-    static constexpr int O_OFF = (Q_BYTES + 15) / 16 * 16;
-    static constexpr int O_WARP = HEADS * O_PITCH;  // floats of a warp's O
-    static constexpr int O_BYTES = kWarps * O_WARP * 4;
-    static constexpr int ML_OFF = O_OFF + O_BYTES;
+    // A stage of a warp's ring, a tile of 16 keys: K piece by piece, each lane's own 16 bytes; V row by
+    // row, its 16-byte chunks swizzled (v_chunk); a scale a lane
+    static constexpr int K_PIECES = 2 * (D / 64), V_OFF = K_PIECES * 512, S_OFF = V_OFF + 16 * D;
+    static constexpr int TILE = S_OFF + 128;                // and a scale
+    static constexpr int TILES = tiles_of(D, HB), STAGE = TILES * TILE;
+    static constexpr int RING_OFF = (Q_BYTES + 15) / 16 * 16;
     // each head's factor and bias, then m and l of each warp
-    static constexpr int TOTAL = ML_OFF + (2 + 2 * kWarps) * HEADS * 4;
+    static constexpr int ML_BYTES = (2 + 2 * kWarps) * HEADS * 4;
+    static constexpr int FIXED = RING_OFF + ML_BYTES;
+    static constexpr int FIT = ((228 * 1024 / ctas_per_sm(D, HB) - 1024) - FIXED) / (kWarps * STAGE);
+    static constexpr int STAGES = FIT < 4 ? FIT : 4;
+    static constexpr int WARP_RING = STAGES * STAGE;
+    static constexpr int ML_OFF = RING_OFF + kWarps * WARP_RING;
+    static constexpr int TOTAL = ML_OFF + ML_BYTES;
+    // at a segment's end a warp's O takes the place of its ring
+    static constexpr int O_PITCH = D + 4;                   // floats
+    static_assert(STAGES >= 2 && HEADS * O_PITCH * 4 <= WARP_RING, "two stages, and O in their place");
 };
 
+// byte offset of the 16-byte chunk c of row r of a tile of V: such that the eight
+// lanes of a phase, which read two neighbouring chunks (or, for D = 64, four
+// halves of two) of rows 2 t, hit distinct banks
+template <int D> __device__ __forceinline__ uint32_t v_chunk(int r, int c)
+{
+    if constexpr (D == 64)
+        return (r >> 1) * 128 + ((((r & 1) << 2) | c) ^ ((r >> 1 & 3) << 1)) * 16;
+    else
+        return r * D + (c ^ (r & 7)) * 16;
+}
+
 // Attention of one query over the codes of a flat share of the batch
-// (kvc_flat.cuh), a warp taking 16 keys at a time straight from global memory
-// into the operands of mma.sync m16n8k16:
+// (kvc_flat.cuh), a warp taking 16 keys at a time into the operands of mma.sync
+// m16n8k16:
 //   scores  S^T[key][head] = K[key][:] . Q[head][:]    A = K codes as halves
 //   output  O^T[d][head] += V^T[d][key] w[key][head]   A = V codes as halves
 // The sum over d does not care for the order of d, so lane (g, t) takes 16
@@ -476,7 +516,9 @@ template <int D, int HB> struct QuantSmem {
 // query's fragments are laid out to match: one 16-byte load feeds four MMAs.
 // Likewise the rows d of O^T are taken in the order in which lane (g, .) holds
 // the 16 (or 8) consecutive codes of its keys' V rows; the bytes of two keys
-// are interleaved with one permute for each two codes.
+// are interleaved with one permute for each two codes.  So a lane needs only
+// 16-byte pieces.  A warp copies them asynchronously into a ring of its own in
+// shared memory, a few tiles ahead, and reads them back without conflicts.
 // The keys' scales stay out of the products: s = (q . code) * ks in float32,
 // and a value's weight is 2^(s + log2(vs) - mo), with a reference maximum mo
 // of its own beside the m of the sum l = sum 2^(s - m).  So the weights are
@@ -492,9 +534,9 @@ quant_decode_kernel(const QuantDecodeArgs a)
     constexpr int HEADS = SM::HEADS;
     constexpr int KV4 = D / 64;               // 16-byte pieces of K a lane takes of one key
     constexpr int VW = D / 32;                // 32-bit words of V a lane takes of one key
-    constexpr bool QREG = D * HB <= 128;      // query fragments in registers
+    constexpr bool QREG = HB == 1;            // query fragments in registers
+    constexpr int TILES = SM::TILES, kUnit = unit_of(D, HB);
     extern __shared__ __align__(16) uint8_t smem[];
-    float *o_sh = reinterpret_cast<float *>(smem + SM::O_OFF);
     float *q_factor = reinterpret_cast<float *>(smem + SM::ML_OFF);
     float *q_bias = q_factor + HEADS;
     float *m_sh = q_bias + HEADS, *l_sh = m_sh + kWarps * HEADS;
@@ -509,7 +551,7 @@ quant_decode_kernel(const QuantDecodeArgs a)
         const int n = visible(a, b, first, bad);
         if (bad && c == 0 && warp == 0)
             kvc::raise_status(a.status, bad);
-        return (n + kUnit - 1) / kUnit;
+        return row_units(n, kUnit);
     };
     int b, base;
     const int U = kvc_flat::locate(a.batch, a.kv_heads, units, -1, b, base);
@@ -524,18 +566,18 @@ quant_decode_kernel(const QuantDecodeArgs a)
         int64_t first;
         uint32_t bad;
         const int n = visible(a, b, first, bad);
-        const int nu = (n + kUnit - 1) / kUnit;
-        const int h = (x - base) / nu;
-        const int u0 = (x - base) - h * nu;
-        const int u1 = min(nu, u0 + (x_end - x));
+        const int line = row_units(n, kUnit), nu = line - kRowCost;
+        const int h = (x - base) / line;
+        const int p0 = (x - base) - h * line, p1 = min(line, p0 + (x_end - x));
+        // the units that stand for the row's cost hold no keys
+        const int u0 = max(0, p0 - kRowCost), u1 = p1 - kRowCost;
+        if (u1 <= u0)
+            break;  // (the share ends in them)
         const int64_t slice = (int64_t)b * a.kv_heads + h;
 
-        const uint8_t *kb = a.kq + slice * a.C * D + 16 * t, *vb = a.vq + slice * a.C * D + (D == 64 ? 8 : 16) * g;
+        const uint8_t *kb = a.kq + slice * a.C * D + 16 * t, *vb = a.vq + slice * a.C * D + 16 * (lane % (D / 16));
         const float *ksb = a.ks + slice * a.C, *vsb = a.vs + slice * a.C;
         const uint32_t cap = (uint32_t)a.C, start = (uint32_t)first;
-        uint4 kr[2][KV4];
-        uint32_t vr[4][VW];
-        float ksr[2], vsr[2];
         // 16 keys whose rows follow one another: one address each for the keys, the values and the
         // scales, and constant steps.  Else (the last keys, or a ring's end among them) each row has its
         // own, a key past the last being the last again: its score is masked, and what is loaded is
@@ -548,69 +590,64 @@ quant_decode_kernel(const QuantDecodeArgs a)
             const uint32_t r = start + (uint32_t)min(j, n - 1);
             return min(r, r - cap);  // (r - cap is huge below cap)
         };
-        auto load_k = [&](int j0) {
+        const uint32_t ring = kvc::smem_u32(smem) + SM::RING_OFF + warp * SM::WARP_RING;
+        const uint32_t my16 = ring + lane * 16, my_s = ring + SM::S_OFF + lane * 4;
+        // V comes in whole rows, D / 16 lanes a row: with each lane fetching what it needs itself (32
+        // bytes of four rows for eight lanes) the memory system moved twice the bytes of V to the SM
+        constexpr int V_LANES = D / 16, V_ROWS = 32 / V_LANES;  // rows a load covers
+        const int v_row = lane / V_LANES, v_col = lane % V_LANES;
+        uint32_t v_to[16 / V_ROWS];
+#pragma unroll
+        for (int i = 0; i < 16 / V_ROWS; ++i)
+            v_to[i] = ring + SM::V_OFF + v_chunk<D>(i * V_ROWS + v_row, v_col);
+        // lane (g, t) fetches the scale of key g (t even) or g + 8, K's (t < 2) or V's: four side by side
+        const float *scales = t < 2 ? ksb : vsb;
+        auto fetch = [&](int j0, uint32_t at) {
             if (in_line(j0)) {
-                const uint32_t r = slot(j0 + g);
-                const uint8_t *p = kb + (uint64_t)r * D;
+                const uint32_t rk = slot(j0 + g);
+                const uint8_t *k = kb + (uint64_t)rk * D, *v = vb + (uint64_t)slot(j0 + v_row) * D;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
 #pragma unroll
                     for (int i = 0; i < KV4; ++i)
-                        kr[e][i] = ldg_stream(p + 8 * e * D + 64 * i);
-                    ksr[e] = __ldg(ksb + r + 8 * e);
-                    vsr[e] = __ldg(vsb + r + 8 * e);
+                        copy16(my16 + at + (e * KV4 + i) * 512, k + 8 * e * D + 64 * i);
                 }
-                return;
-            }
+                copy4(my_s + at, scales + rk + 8 * (t & 1));
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint32_t r = slot(j0 + g + 8 * e);
-                const uint8_t *p = kb + (uint64_t)r * D;
-#pragma unroll
-                for (int i = 0; i < KV4; ++i)
-                    kr[e][i] = ldg_stream(p + 64 * i);
-                ksr[e] = __ldg(ksb + r);
-                vsr[e] = __ldg(vsb + r);
-            }
-        };
-        auto take_v = [&](int e, const uint8_t *p) {
-            if constexpr (D == 64) {
-                const uint2 v = ldg_stream8(p);
-                vr[e][0] = v.x;
-                vr[e][1] = v.y;
+                for (int i = 0; i < 16 / V_ROWS; ++i)
+                    copy16(v_to[i] + at, v + i * V_ROWS * D);
             } else {
 #pragma unroll
-                for (int i = 0; i < D / 128; ++i) {
-                    const uint4 v = ldg_stream(p + 128 * i);
-                    vr[e][4 * i] = v.x;
-                    vr[e][4 * i + 1] = v.y;
-                    vr[e][4 * i + 2] = v.z;
-                    vr[e][4 * i + 3] = v.w;
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t r = slot(j0 + g + 8 * e);
+#pragma unroll
+                    for (int i = 0; i < KV4; ++i)
+                        copy16(my16 + at + (e * KV4 + i) * 512, kb + (uint64_t)r * D + 64 * i);
                 }
-            }
-        };
-        auto load_v = [&](int j0) {
-            if (in_line(j0)) {
-                const uint8_t *p = vb + (uint64_t)slot(j0 + 2 * t) * D;
+                copy4(my_s + at, scales + slot(j0 + g + 8 * (t & 1)));
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    take_v(e, p + ((e & 1) + 8 * (e >> 1)) * D);
-                return;
+                for (int i = 0; i < 16 / V_ROWS; ++i)
+                    copy16(v_to[i] + at, vb + (uint64_t)slot(j0 + i * V_ROWS + v_row) * D);
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                take_v(e, vb + (uint64_t)slot(j0 + 2 * t + (e & 1) + 8 * (e >> 1)) * D);
         };
         // the first keys are under way while the queries are made ready
         const int j_end = min(n, u1 * kUnit);
-        int j0 = u0 * kUnit + 16 * warp;
-        if (j0 < j_end) {
-            load_k(j0);
-            load_v(j0);
+        int j0 = u0 * kUnit + 16 * TILES * warp;
+        auto fetch_step = [&](int j0, uint32_t at) {
+#pragma unroll
+            for (int u = 0; u < TILES; ++u)
+                if (u == 0 || j0 + 16 * u < j_end)
+                    fetch(j0 + 16 * u, at + u * SM::TILE);
+        };
+        __syncthreads();  // the last segment's reads of shared memory are done
+#pragma unroll
+        for (int st = 0; st < SM::STAGES; ++st) {
+            if (j0 + st * kUnit < j_end)
+                fetch_step(j0 + st * kUnit, st * SM::STAGE);
+            copy_commit();
         }
 
         // ---- the group's queries: rotated, scaled by a power of two, halves ----
-        __syncthreads();  // the last segment's reads of shared memory are done
         {
             const int64_t pos = (int64_t)a.len.total_abs[b] - 1;
             const T *q = static_cast<const T *>(a.q) + slice * a.group * D;
@@ -695,65 +732,92 @@ quant_decode_kernel(const QuantDecodeArgs a)
             }
         }
 
+        uint32_t at = 0;  // the stage
         for (; j0 < j_end; j0 += kUnit) {
-            // ---- scores: two chains of products a head block ----
-            float s[HB][4], s2[HB][4];
+            copy_wait<SM::STAGES - 1>();
+            __syncwarp();  // the values and scales are fetched by all for all
+            // ---- scores: two chains of products a head block and tile ----
+            float s[TILES][HB][4], s2[TILES][HB][4];
 #pragma unroll
-            for (int hb = 0; hb < HB; ++hb)
+            for (int u = 0; u < TILES; ++u)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    s[hb][e] = s2[hb][e] = 0.f;
+                for (int hb = 0; hb < HB; ++hb)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        s[u][hb][e] = s2[u][hb][e] = 0.f;
 #pragma unroll
             for (int i = 0; i < KV4; ++i) {
-                const uint32_t wa[4] = {kr[0][i].x, kr[0][i].y, kr[0][i].z, kr[0][i].w};
-                const uint32_t wb[4] = {kr[1][i].x, kr[1][i].y, kr[1][i].z, kr[1][i].w};
+                uint32_t wa[TILES][4], wb[TILES][4];
+#pragma unroll
+                for (int u = 0; u < TILES; ++u) {
+                    const uint4 ka = lds16(my16 + at + u * SM::TILE + i * 512);
+                    const uint4 kc = lds16(my16 + at + u * SM::TILE + (KV4 + i) * 512);
+                    wa[u][0] = ka.x, wa[u][1] = ka.y, wa[u][2] = ka.z, wa[u][3] = ka.w;
+                    wb[u][0] = kc.x, wb[u][1] = kc.y, wb[u][2] = kc.z, wb[u][3] = kc.w;
+                }
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
-                    uint32_t a0, a1, a2, a3;
-                    codes_to_halves<FMT, true>(wa[w], a0, a2);
-                    codes_to_halves<FMT, true>(wb[w], a1, a3);
+                    uint2 f[HB];
 #pragma unroll
                     for (int hb = 0; hb < HB; ++hb) {
-                        uint2 f;
                         if constexpr (QREG)
-                            f = qf[hb][4 * i + w];
+                            f[hb] = qf[hb][4 * i + w];
                         else
-                            f = q_frag(hb, 4 * i + w);
-                        mma_f16(w & 1 ? s2[hb] : s[hb], a0, a1, a2, a3, f.x, f.y);
+                            f[hb] = q_frag(hb, 4 * i + w);
+                    }
+#pragma unroll
+                    for (int u = 0; u < TILES; ++u) {
+                        uint32_t a0, a1, a2, a3;
+                        codes_to_halves<FMT, true>(wa[u][w], a0, a2);
+                        codes_to_halves<FMT, true>(wb[u][w], a1, a3);
+#pragma unroll
+                        for (int hb = 0; hb < HB; ++hb)
+                            mma_f16(w & 1 ? s2[u][hb] : s[u][hb], a0, a1, a2, a3, f[hb].x, f[hb].y);
                     }
                 }
             }
-            const bool tail = j0 + 16 > n;
-            const bool in0 = j0 + g < n, in1 = j0 + g + 8 < n;
-            const float k0 = ksr[0], k1 = ksr[1];
-            const float lv0 = fast_log2(vsr[0]), lv1 = fast_log2(vsr[1]);
-            if (j0 + kUnit < j_end)
-                load_k(j0 + kUnit);
+            const bool tail = j0 + 16 * TILES > n;
+            float lv[TILES][2];
 
             // ---- softmax: x = s - m, y = s + log2(vs) - mo ----
-            float x[HB][4], y[HB][4], top = kNone;
+            float x[TILES][HB][4], y[TILES][HB][4], top = kNone;
 #pragma unroll
-            for (int hb = 0; hb < HB; ++hb) {
+            for (int u = 0; u < TILES; ++u) {
+                const uint4 sc = lds16(ring + SM::S_OFF + g * 16 + at + u * SM::TILE);
+                const float kk[2] = {__uint_as_float(sc.x), __uint_as_float(sc.y)};
+                lv[u][0] = fast_log2(__uint_as_float(sc.z));
+                lv[u][1] = fast_log2(__uint_as_float(sc.w));
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float sum = s[hb][e] + s2[hb][e];
-                    s[hb][e] = (FMT == KVC_INT8 ? fmaf(sum, qs[hb][e & 1], -qb[hb][e & 1]) : sum * qs[hb][e & 1]) *
-                               (e < 2 ? k0 : k1);
-                    if (tail)
-                        s[hb][e] = (e < 2 ? in0 : in1) ? s[hb][e] : -INFINITY;
-                    x[hb][e] = s[hb][e] - m[hb][e & 1];
-                    y[hb][e] = s[hb][e] + (e < 2 ? lv0 : lv1) - mo[hb][e & 1];
-                    top = fmaxf(top, fmaxf(x[hb][e], y[hb][e]));
+                for (int hb = 0; hb < HB; ++hb) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float sum = s[u][hb][e] + s2[u][hb][e];
+                        float z = (FMT == KVC_INT8 ? fmaf(sum, qs[hb][e & 1], -qb[hb][e & 1]) : sum * qs[hb][e & 1]) * kk[e >> 1];
+                        float lz = lv[u][e >> 1];
+                        if (tail && j0 + 16 * u + g + 8 * (e >> 1) >= n) {
+                            z = -INFINITY;
+                            lz = 0.f;  // (what a tile past the last holds is not looked at)
+                        }
+                        s[u][hb][e] = z;
+                        x[u][hb][e] = z - m[hb][e & 1];
+                        y[u][hb][e] = z + lz - mo[hb][e & 1];
+                        top = fmaxf(top, fmaxf(x[u][hb][e], y[u][hb][e]));
+                    }
                 }
             }
             if (__any_sync(0xffffffffu, top > kSlack)) {
-                // a reference is left behind: raise both to the tile's maxima
+                // a reference is left behind: raise both to the step's maxima
 #pragma unroll
                 for (int hb = 0; hb < HB; ++hb) {
                     float shrink[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float mx = fmaxf(s[hb][e], s[hb][2 + e]), my = fmaxf(s[hb][e] + lv0, s[hb][2 + e] + lv1);
+                        float mx = kNone, my = kNone;
+#pragma unroll
+                        for (int u = 0; u < TILES; ++u) {
+                            mx = fmaxf(mx, fmaxf(s[u][hb][e], s[u][hb][2 + e]));
+                            my = fmaxf(my, fmaxf(s[u][hb][e] + lv[u][0], s[u][hb][2 + e] + lv[u][1]));
+                        }
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) {
                             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
@@ -764,13 +828,20 @@ quant_decode_kernel(const QuantDecodeArgs a)
                         my = fmaxf(my, mo[hb][e]);
                         l[hb][e] *= fast_exp2(m[hb][e] - mx);
                         shrink[e] = fast_exp2(mo[hb][e] - my);
+#pragma unroll
+                        for (int u = 0; u < TILES; ++u)
+#pragma unroll
+                            for (int i = e; i < 4; i += 2) {
+                                // (a masked key stays at -infinity)
+                                x[u][hb][i] += m[hb][e] - mx;
+                                y[u][hb][i] += mo[hb][e] - my;
+                                if (m[hb][e] == kNone)
+                                    x[u][hb][i] = s[u][hb][i] - mx;
+                                if (mo[hb][e] == kNone)
+                                    y[u][hb][i] = s[u][hb][i] == -INFINITY ? -INFINITY : s[u][hb][i] + lv[u][i >> 1] - my;
+                            }
                         m[hb][e] = mx;
                         mo[hb][e] = my;
-#pragma unroll
-                        for (int u = 0; u < 4; u += 2) {
-                            x[hb][u + e] = s[hb][u + e] - m[hb][e];
-                            y[hb][u + e] = s[hb][u + e] + (u ? lv1 : lv0) - mo[hb][e];
-                        }
                     }
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {
@@ -781,35 +852,69 @@ quant_decode_kernel(const QuantDecodeArgs a)
                     }
                 }
             }
-            uint32_t b0[HB], b1[HB];
+            uint32_t b0[TILES][HB], b1[TILES][HB];
 #pragma unroll
-            for (int hb = 0; hb < HB; ++hb) {
+            for (int u = 0; u < TILES; ++u)
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    l[hb][e] += fast_exp2(x[hb][e]) + fast_exp2(x[hb][2 + e]);
-                const __half2 h0 = __floats2half2_rn(fast_exp2(y[hb][0]), fast_exp2(y[hb][1]));
-                const __half2 h1 = __floats2half2_rn(fast_exp2(y[hb][2]), fast_exp2(y[hb][3]));
-                b0[hb] = movm_trans(*reinterpret_cast<const uint32_t *>(&h0));
-                b1[hb] = movm_trans(*reinterpret_cast<const uint32_t *>(&h1));
-            }
+                for (int hb = 0; hb < HB; ++hb) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        l[hb][e] += fast_exp2(x[u][hb][e]) + fast_exp2(x[u][hb][2 + e]);
+                    const __half2 h0 = __floats2half2_rn(fast_exp2(y[u][hb][0]), fast_exp2(y[u][hb][1]));
+                    const __half2 h1 = __floats2half2_rn(fast_exp2(y[u][hb][2]), fast_exp2(y[u][hb][3]));
+                    b0[u][hb] = movm_trans(*reinterpret_cast<const uint32_t *>(&h0));
+                    b1[u][hb] = movm_trans(*reinterpret_cast<const uint32_t *>(&h1));
+                }
 
             // ---- output ----
+            constexpr int VP = D == 64 ? 2 : 4;  // words of a piece
 #pragma unroll
-            for (int w = 0; w < VW; ++w) {
+            for (int u = 0; u < TILES; ++u) {
+                // (a whole tile past the last: its values may be anything, and its weights are zeros)
+                if (u > 0 && j0 + 16 * u >= n)
+                    break;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    // columns 4 w + 2 e and + 1 of keys 2 t, 2 t + 1 and of 2 t + 8, 2 t + 9
-                    uint32_t a0, a1, a2, a3;
-                    pairs_of<FMT>(vr[0][w], vr[1][w], e, a0, a1);
-                    pairs_of<FMT>(vr[2][w], vr[3][w], e, a2, a3);
+                for (int p = 0; p < VW / VP; ++p) {
+                    uint32_t vr[4][VP];
 #pragma unroll
-                    for (int hb = 0; hb < HB; ++hb)
-                        mma_f16(o[hb][2 * w + e], a0, a1, a2, a3, b0[hb], b1[hb]);
+                    for (int e = 0; e < 4; ++e) {
+                        // columns of lane (g, .): the 16 (D = 64: 8) from 16 g (8 g) of each 128 on
+                        const int row = 2 * t + (e & 1) + 8 * (e >> 1);
+                        const uint32_t from = ring + SM::V_OFF + u * SM::TILE + at;
+                        if constexpr (D == 64) {
+                            const uint2 v = lds8(from + v_chunk<D>(row, g >> 1) + (g & 1) * 8);
+                            vr[e][0] = v.x;
+                            vr[e][1] = v.y;
+                        } else {
+                            const uint4 v = lds16(from + v_chunk<D>(row, 8 * p + g));
+                            vr[e][0] = v.x;
+                            vr[e][1] = v.y;
+                            vr[e][2] = v.z;
+                            vr[e][3] = v.w;
+                        }
+                    }
+#pragma unroll
+                    for (int w = 0; w < VP; ++w) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            // columns 4 w + 2 e and + 1 of keys 2 t, 2 t + 1 and of 2 t + 8, 2 t + 9
+                            uint32_t a0, a1, a2, a3;
+                            pairs_of<FMT>(vr[0][w], vr[1][w], e, a0, a1);
+                            pairs_of<FMT>(vr[2][w], vr[3][w], e, a2, a3);
+#pragma unroll
+                            for (int hb = 0; hb < HB; ++hb)
+                                mma_f16(o[hb][2 * (p * VP + w) + e], a0, a1, a2, a3, b0[u][hb], b1[u][hb]);
+                        }
+                    }
                 }
             }
-            if (j0 + kUnit < j_end)
-                load_v(j0 + kUnit);
+            __syncwarp();  // every byte of the stage has been read
+            if (j0 + SM::STAGES * kUnit < j_end)
+                fetch_step(j0 + SM::STAGES * kUnit, at);
+            copy_commit();
+            at = at + SM::STAGE == SM::WARP_RING ? 0 : at + SM::STAGE;
         }
+        copy_wait<0>();
 
         // ---- join the warps: m, l, then O relative to the common m ----
 #pragma unroll
@@ -837,6 +942,7 @@ quant_decode_kernel(const QuantDecodeArgs a)
                     top = fmaxf(top, m_sh[w * HEADS + hb * 8 + 2 * t + e]);
                 f[hb][e] = exp2f(mo[hb][e] - top);  // O is relative to mo
             }
+        auto o_of = [&](int w) { return reinterpret_cast<float *>(smem + SM::RING_OFF + w * SM::WARP_RING); };
         {
             // tile i holds columns 2 i and 2 i + 1 of the lane's run of consecutive columns
             constexpr int RUN = D == 64 ? 8 : 16;
@@ -848,7 +954,7 @@ quant_decode_kernel(const QuantDecodeArgs a)
                     for (int i = 0; i < D / 16; i += 2) {
                         const int col = (2 * i / RUN) * 128 + RUN * g + 2 * i % RUN;
                         const float x = f[hb][e];
-                        *reinterpret_cast<float4 *>(o_sh + warp * SM::O_WARP + (hb * 8 + 2 * t + e) * SM::O_PITCH + col) =
+                        *reinterpret_cast<float4 *>(o_of(warp) + (hb * 8 + 2 * t + e) * SM::O_PITCH + col) =
                             make_float4(o[hb][i][e] * x, o[hb][i][2 + e] * x, o[hb][i + 1][e] * x, o[hb][i + 1][2 + e] * x);
                     }
         }
@@ -868,7 +974,7 @@ quant_decode_kernel(const QuantDecodeArgs a)
             float v = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w)
-                v += o_sh[w * SM::O_WARP + r * SM::O_PITCH + d];
+                v += o_of(w)[r * SM::O_PITCH + d];
             if (whole) {
                 static_cast<T *>(a.out)[slice * a.group * D + idx] = kvc::Elem<T>::from_f32(v / sum);
             } else {
@@ -879,8 +985,8 @@ quant_decode_kernel(const QuantDecodeArgs a)
                 }
             }
         }
-        x += u1 - u0;
-        if (x == base + nu * a.kv_heads && x < x_end) {
+        x += p1 - p0;
+        if (x == base + line * a.kv_heads && x < x_end) {
             base = x;
             do {
                 ++b;
@@ -910,17 +1016,17 @@ quant_merge_kernel(const QuantDecodeArgs a)
     auto units = [&](int bb) {
         int64_t first;
         uint32_t bad;
-        return (visible(a, bb, first, bad) + kUnit - 1) / kUnit;
+        return row_units(visible(a, bb, first, bad), a.unit);
     };
     int b_out, base;
     const int U = kvc_flat::locate(a.batch, a.kv_heads, units, b, b_out, base);
-    const int nu = units(b);
+    const int line = units(b);
     const kvc_flat::Shares shares(U, a.grid);
-    const int x0 = base + h * nu;
+    const int x0 = base + h * line;
     kvc::grid_dep_wait();
-    if (nu == 0)
+    if (line == 0)
         return;
-    const int c0 = shares.of(x0), n = shares.of(x0 + nu - 1) - c0 + 1;
+    const int c0 = shares.of(x0 + kRowCost), n = shares.of(x0 + line - 1) - c0 + 1;
     if (n == 1)
         return;  // written by that CTA
     // the row's segment is the first of its CTA, but in CTA c0 if that began before the row
@@ -989,8 +1095,9 @@ quant_merge_kernel(const QuantDecodeArgs a)
 // one wave of resident CTAs, or one CTA a unit where the cache has fewer
 int decode_grid(int batch, int kv_heads, int group, int64_t C, int D)
 {
-    const int64_t most = (int64_t)batch * kv_heads * ((C + kUnit - 1) / kUnit);
-    const int64_t wave = (int64_t)kvc_host::sm_count() * ctas_per_sm(D, group > 8 ? 2 : 1);
+    const int hb = group > 8 ? 2 : 1, unit = unit_of(D, hb);
+    const int64_t most = (int64_t)batch * kv_heads * ((C + unit - 1) / unit + kRowCost);
+    const int64_t wave = (int64_t)kvc_host::sm_count() * ctas_per_sm(D, hb);
     return (int)std::max<int64_t>(1, std::min<int64_t>({most, wave, kMaxParts}));
 }
 
@@ -1003,7 +1110,7 @@ template <typename T, int FMT, int D, int HB> kvc_status launch_decode(const Qua
         return KVC_ERR_CUDA;
     kern<<<a.grid, 32 * kWarps, smem, stream>>>(a);
     // a row of one unit is never split
-    if (a.C > kUnit) {
+    if (a.C > a.unit) {
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(a.batch * a.kv_heads, a.group);
         cfg.blockDim = dim3(kMergeThreads);
@@ -1195,7 +1302,7 @@ KVC_API size_t kvc_gqa_decode_quant_workspace_size(int batch, int q_heads, int k
 {
     if (batch < 1 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || capacity < 1 || head_dim < 1)
         return 0;
-    if (capacity <= kUnit)
+    if (capacity <= unit_of(head_dim, q_heads / kv_heads > 8 ? 2 : 1))
         return 0;
     const size_t parts = 2 * (size_t)decode_grid(batch, kv_heads, q_heads / kv_heads, capacity, head_dim) * (q_heads / kv_heads);
     return parts * (head_dim + 2) * sizeof(float);
@@ -1220,7 +1327,7 @@ KVC_API kvc_status kvc_gqa_decode_quant(void *out, const void *q, const void *kq
         return KVC_ERR_UNSUPPORTED;
     if (capacity < 1 || capacity > (int64_t)INT32_MAX)
         return KVC_ERR_CAPACITY;
-    if ((int64_t)batch * kv_heads * ((capacity + kUnit - 1) / kUnit) > (int64_t)INT32_MAX)
+    if ((int64_t)batch * kv_heads * ((capacity + 63) / 64 + kRowCost) > (int64_t)INT32_MAX)
         return KVC_ERR_SHAPE;
     if ((rope_cos == nullptr) != (rope_sin == nullptr))
         return KVC_ERR_NULL;
@@ -1260,6 +1367,7 @@ KVC_API kvc_status kvc_gqa_decode_quant(void *out, const void *q, const void *kq
     a.cos_t = rope_cos;
     a.sin_t = rope_sin;
     a.rope_max_pos = rope_max_pos;
+    a.unit = unit_of(head_dim, a.group > 8 ? 2 : 1);
     a.grid = decode_grid(batch, kv_heads, a.group, capacity, head_dim);
     const int64_t parts = 2 * (int64_t)a.grid * a.group;
     a.ws_o = static_cast<float *>(workspace);

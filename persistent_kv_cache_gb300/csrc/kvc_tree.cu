@@ -339,6 +339,12 @@ __device__ __forceinline__ int tree_tiles(const TreeArgs &a, int b, int &P, int 
     return (int)((T - lo + kBN - 1) / kBN);
 }
 
+// Tiles of a row on the line that the CTAs share: those of its keys, and kRowCost
+// that hold none but stand for what a segment costs beside them (scores of the first
+// tile, output).
+constexpr int kRowCost = 4;
+__device__ __forceinline__ int line_tiles(int n) { return n > 0 ? n + kRowCost : 0; }
+
 // The segments of a CTA's share, one at a time: tiles [t0, t1) of the n tiles of
 // line row (b, head, row tile).
 struct Segment {
@@ -353,23 +359,28 @@ struct Walk {
     }
     __device__ __forceinline__ bool next(const TreeArgs &a, Segment &s)
     {
-        if (x >= x_end)
-            return false;
         const int rows = a.kv_heads * a.row_tiles;
-        while (x >= base + n * rows) {
-            base += n * rows;
-            ++b;
-            load(a);
+        while (x < x_end) {
+            while (x >= base + line_tiles(n) * rows) {
+                base += line_tiles(n) * rows;
+                ++b;
+                load(a);
+            }
+            const int line = line_tiles(n);
+            s.b = b;
+            s.P = P;
+            s.lo = lo;
+            s.n = n;
+            s.row = (x - base) / line;
+            const int p0 = (x - base) - s.row * line, p1 = min(line, p0 + (x_end - x));
+            x += p1 - p0;
+            // the tiles that stand for the row's cost hold no keys
+            s.t0 = max(0, p0 - kRowCost);
+            s.t1 = p1 - kRowCost;
+            if (s.t1 > s.t0)
+                return true;
         }
-        s.b = b;
-        s.P = P;
-        s.lo = lo;
-        s.n = n;
-        s.row = (x - base) / n;
-        s.t0 = (x - base) - s.row * n;
-        s.t1 = min(n, s.t0 + (x_end - x));
-        x += s.t1 - s.t0;
-        return true;
+        return false;
     }
 };
 
@@ -531,7 +542,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             const int n = tree_tiles(a, b, P, lo, bad);
             if (bad && blockIdx.x == 0 && warp == 0)
                 kvc::raise_status(a.status, bad);
-            return n;
+            return line_tiles(n);
         };
         const int U = kvc_flat::locate(a.batch, line_rows, count, -1, walk.b, walk.base);
         const kvc_flat::Shares shares(U, a.grid);
@@ -945,27 +956,29 @@ tree_merge_kernel(const TreeArgs a)
     auto count = [&](int b) {
         int P, lo;
         uint32_t bad;
-        return tree_tiles(a, b, P, lo, bad);
+        return line_tiles(tree_tiles(a, b, P, lo, bad));
     };
     int b, base;
     const int U = kvc_flat::locate(a.batch, line_rows, count, -1, b, base);
     const kvc_flat::Shares shares(U, a.grid);
     const int x0 = shares.begin(c0), x1 = shares.begin(c0 + 1);
-    int n = 0, row = 0, first = 0;
+    int n = 0, row = 0, first = 0, end = 0;  // of the row's keys on the line
     if (x0 < x1 && x1 < U) {
-        kvc_flat::row_of(a.batch, line_rows, count, x1, b, base);  // the row that the next CTA goes on with
+        kvc_flat::row_of(a.batch, line_rows, count, x1, b, base);  // the row that the next CTA begins in
         n = count(b);
         row = (x1 - base) / n;
-        first = base + row * n;
+        first = base + row * n + kRowCost;
+        end = base + row * n + n;
     }
     kvc::grid_dep_wait();
-    // (first == x1: it begins there; first < x0: it began before this CTA)
+    // (its keys begin in another CTA's share, or in the next one's)
     const int mt = row % a.row_tiles;
-    if (n == 0 || first == x1 || first < x0 || mt * kBM + m >= rows)
+    if (n == 0 || first < x0 || first >= x1 || mt * kBM + m >= rows)
         return;
-    const int parts = shares.of(first + n - 1) - c0 + 1;
+    const int parts = shares.of(end - 1) - c0 + 1;
     // the row's segment is the first of its CTA, but in CTA c0 if that began before the row
-    auto part = [&](int i) { return (2 * ((int64_t)c0 + i) + (i == 0 && x0 < first ? 1 : 0)) * kBM + m; };
+    const int slot0 = x0 < first - kRowCost ? 1 : 0;
+    auto part = [&](int i) { return (2 * ((int64_t)c0 + i) + (i == 0 ? slot0 : 0)) * kBM + m; };
     float top = -INFINITY;
     for (int i = lane; i < parts; i += 32)
         top = fmaxf(top, a.ws_l[part(i)] == 0.f ? -INFINITY : a.ws_m[part(i)]);
@@ -1248,7 +1261,7 @@ KVC_API kvc_status kvc_gqa_tree(void *out, const void *q, const void *k_cache, c
     a.rope_max_pos = rope_max_pos;
     a.status = dev_status;
     a.row_tiles = (a.group * nodes + kBM - 1) / kBM;
-    const int64_t units = (int64_t)batch * kv_heads * a.row_tiles * ((at.rows + kBN - 1) / kBN);
+    const int64_t units = (int64_t)batch * kv_heads * a.row_tiles * ((at.rows + kBN - 1) / kBN + kRowCost);
     if (units > (int64_t)INT32_MAX || (int64_t)batch * q_heads * nodes > (int64_t)INT32_MAX / 32)
         return KVC_ERR_SHAPE;
     a.grid = (int)std::min<int64_t>(units, kvc_host::sm_count());
