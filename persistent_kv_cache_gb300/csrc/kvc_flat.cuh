@@ -84,4 +84,36 @@ __device__ __forceinline__ void row_of(int batch, int heads, const Count &count,
     }
 }
 
+// The share [x, x_end) of CTA c of a grid, the batch row of unit x and that
+// row's first unit's position (b and base only when the share is not empty).
+// Up to 32 batch rows take one pass over their lengths.
+template <typename Count>
+__device__ __forceinline__ void share_of_cta(int batch, int heads, const Count &count, int grid, int c, int &x,
+                                             int &x_end, int &b, int &base)
+{
+    if (batch > 32) {
+        const int U = locate(batch, heads, count, -1, b, base);
+        const Shares shares(U, grid);
+        x = shares.begin(c);
+        x_end = shares.begin(c + 1);
+        if (x < x_end)
+            row_of(batch, heads, count, x, b, base);
+        return;
+    }
+    const int lane = threadIdx.x & 31;
+    const int n = lane < batch ? count(lane) * heads : 0;
+    int inc = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d)
+            inc += v;
+    }
+    const Shares shares(__shfl_sync(0xffffffffu, inc, 31), grid);
+    x = shares.begin(c);
+    x_end = shares.begin(c + 1);
+    b = __ffs(__ballot_sync(0xffffffffu, inc > x)) - 1;
+    base = __shfl_sync(0xffffffffu, inc - n, b & 31);
+}
+
 } // namespace kvc_flat

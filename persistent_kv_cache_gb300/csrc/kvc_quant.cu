@@ -66,8 +66,8 @@ __device__ __forceinline__ float max_nan(float x, float y)
 // overflow or underflow on the way, q = x r corrected by its remainder,
 // q + (x - q s) r, is the correctly rounded quotient (Markstein, "Computation of
 // elementary functions on the IBM RISC System/6000 processor", 1990): three
-// operations a value in the place of a division's ten or more.  Rows with a scale
-// outside [2^-100, 2^100] divide.
+// operations a value in the place of a division's ten or more; the scale itself is
+// top / 127 in the same way.  Rows with a maximum outside [2^-100, 2^100] divide.
 template <int FMT, int LPR>
 __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float &scale)
 {
@@ -83,12 +83,12 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float &scale)
         scale = __uint_as_float(0x7fc00000u);
         return out;
     }
-    scale = __fdiv_rn(top, kTop<FMT>);
-    if (scale == 0.f)
-        return out;
     float y[8];
-    const bool usual = scale >= 7.8886091e-31f && scale <= 1.2676506e30f;  // 2^-100, 2^100
+    const bool usual = top >= 7.8886091e-31f && top <= 1.2676506e30f;  // 2^-100, 2^100
     if (usual) {
+        constexpr float rt = 1.f / kTop<FMT>;
+        const float q0 = __fmul_rn(top, rt);
+        scale = __fmaf_rn(__fmaf_rn(-q0, kTop<FMT>, top), rt, q0);
         const float r = __frcp_rn(scale);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -96,6 +96,9 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float &scale)
             y[i] = __fmaf_rn(__fmaf_rn(-q, scale, x[i]), r, q);
         }
     } else {
+        scale = __fdiv_rn(top, kTop<FMT>);
+        if (scale == 0.f)
+            return out;
         // (a subnormal scale may round the quotient past the largest code)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -176,6 +179,7 @@ quant_append_kernel(const AppendArgs a)
         return;  // the whole block
     // D is a multiple of 16, so the partner columns are one lane's
     const int from = ((threadIdx.x & 31) - sub + (low ? sub + half / 8 : sub - half / 8)) & 31;
+    const float sign = low ? -1.f : 1.f;
     const int step = gridDim.x * RPB;
     for (; base < a.S; base += step) {
         const int i = base + t;
@@ -205,9 +209,12 @@ quant_append_kernel(const AppendArgs a)
             to_f32(orow, other);
             // lo cos - hi sin for a column of the lower half, hi cos + lo sin for one of the upper
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float turned = __fadd_rn(__fmul_rn(k[e], cs[e]), __fmul_rn(other[e], low ? -sn[e] : sn[e]));
-                k[e] = in ? turned : 0.f;
+            for (int e = 0; e < 8; ++e)
+                k[e] = __fadd_rn(__fmul_rn(k[e], cs[e]), __fmul_rn(other[e], __fmul_rn(sn[e], sign)));
+            if (a.D != 8 * LPR && !col) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    k[e] = 0.f;  // (a lane past the columns has turned another row's)
             }
         }
         const uint2 kc = quantise8<FMT, LPR>(k, ks);
@@ -259,7 +266,8 @@ struct DequantArgs {
 
 // Eight codes a thread (16 bytes out, side by side over a warp), D / 8 threads a
 // row, kRowsAhead rows under way
-constexpr int kRowsAhead = 8;
+constexpr int kRowsAhead = 4;
+constexpr int kDequantCtas = 12;
 template <typename T, int FMT>
 __global__ void __launch_bounds__(256)
 dequant_rows_kernel(const DequantArgs a)
@@ -282,9 +290,10 @@ dequant_rows_kernel(const DequantArgs a)
     const uint8_t *src = (blockIdx.z == 0 ? a.kq : a.vq) + (int64_t)slice * a.C * a.D + c0;
     const float *scales = (blockIdx.z == 0 ? a.ks : a.vs) + (int64_t)slice * a.C;
     T *dst = static_cast<T *>(blockIdx.z == 0 ? a.k_out : a.v_out) + (int64_t)slice * a.R * a.D + c0;
-    for (int64_t r0 = (int64_t)blockIdx.x * kRowsAhead * rpb + sub; r0 < L; r0 += (int64_t)gridDim.x * kRowsAhead * rpb) {
-        uint2 q[kRowsAhead];
-        float s[kRowsAhead];
+    const int64_t step = (int64_t)gridDim.x * kRowsAhead * rpb;
+    uint2 q[kRowsAhead];
+    float s[kRowsAhead];
+    auto fetch = [&](int64_t r0) {
 #pragma unroll
         for (int u = 0; u < kRowsAhead; ++u) {
             // (a row past the last is the last again)
@@ -293,23 +302,33 @@ dequant_rows_kernel(const DequantArgs a)
             q[u] = __ldg(reinterpret_cast<const uint2 *>(src + (uint64_t)slot * a.D));
             s[u] = __ldg(scales + slot);
         }
+    };
+    int64_t r0 = (int64_t)blockIdx.x * kRowsAhead * rpb + sub;
+    if (r0 < L)
+        fetch(r0);
+    for (; r0 < L; r0 += step) {
+        Raw8<T> out[kRowsAhead];
 #pragma unroll
         for (int u = 0; u < kRowsAhead; ++u) {
-            const int64_t r = r0 + u * rpb;
-            if (r >= L)
-                break;
             float f[8];
             codes4<FMT>(q[u].x, *reinterpret_cast<float (*)[4]>(f));
             codes4<FMT>(q[u].y, *reinterpret_cast<float (*)[4]>(f + 4));
-            Raw8<T> out;
-            T *e = reinterpret_cast<T *>(out.w);
+            T *e = reinterpret_cast<T *>(out[u].w);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 e[i] = kvc::Elem<T>::from_f32(f[i] * s[u]);
-            uint4 *to = reinterpret_cast<uint4 *>(dst + r * a.D);
+        }
+        if (r0 + step < L)
+            fetch(r0 + step);
 #pragma unroll
-            for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-                to[i] = make_uint4(out.w[4 * i], out.w[4 * i + 1], out.w[4 * i + 2], out.w[4 * i + 3]);
+        for (int u = 0; u < kRowsAhead; ++u) {
+            const int64_t r = r0 + u * rpb;
+            if (r < L) {
+                uint4 *to = reinterpret_cast<uint4 *>(dst + r * a.D);
+#pragma unroll
+                for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+                    to[i] = make_uint4(out[u].w[4 * i], out[u].w[4 * i + 1], out[u].w[4 * i + 2], out[u].w[4 * i + 3]);
+            }
         }
     }
 }
@@ -341,25 +360,22 @@ struct QuantDecodeArgs {
     int32_t *status;
 };
 
-// the visible keys of batch row b: n of them from slot `first` on, wrapping at C
-__device__ __forceinline__ int visible(const QuantDecodeArgs &a, int b, int64_t &first, uint32_t &bad)
+// the visible keys of batch row b, at absolute length T
+__device__ __forceinline__ int visible(const QuantDecodeArgs &a, int b, int &T, uint32_t &bad)
 {
-    const int L = a.len.cache_total[b], T = a.len.total_abs[b];
-    bad = 0;
-    first = 0;
-    if (L < 0)
+    const int L = a.len.cache_total[b];
+    T = a.len.total_abs[b];
+    bad = L < 0 ? 0u
+          : L > a.C || T < L ? (uint32_t)KVC_DEV_CAPACITY
+          : a.cos_t && (int64_t)T > a.rope_max_pos ? (uint32_t)KVC_DEV_ROPE_RANGE : 0u;
+    if (L < 0 || bad)
         return 0;
-    if (L > a.C || T < L) {
-        bad = KVC_DEV_CAPACITY;
-        return 0;
-    }
-    if (a.cos_t && (int64_t)T > a.rope_max_pos) {
-        bad = KVC_DEV_ROPE_RANGE;
-        return 0;
-    }
-    const int n = a.window > 0 ? min(L, a.window) : L;
-    first = a.ring ? (int64_t)(T - n) % a.C : (int64_t)(L - n);
-    return n;
+    return a.window > 0 ? min(L, a.window) : L;
+}
+// the slot of the first of them (they wrap at C): T - n, in a ring modulo C
+__device__ __forceinline__ uint32_t first_slot(const QuantDecodeArgs &a, int n, int T)
+{
+    return a.ring ? (uint32_t)(T - n) % (uint32_t)a.C : (uint32_t)(T - n);
 }
 
 // Units of a row on the line that the CTAs share: its keys', and kRowCost that hold
@@ -546,26 +562,20 @@ quant_decode_kernel(const QuantDecodeArgs a)
     const int g = lane >> 2, t = lane & 3;
     const int c = blockIdx.x;
     auto units = [&](int b) {
-        int64_t first;
+        int T;
         uint32_t bad;
-        const int n = visible(a, b, first, bad);
+        const int n = visible(a, b, T, bad);
         if (bad && c == 0 && warp == 0)
             kvc::raise_status(a.status, bad);
         return row_units(n, kUnit);
     };
-    int b, base;
-    const int U = kvc_flat::locate(a.batch, a.kv_heads, units, -1, b, base);
-    const kvc_flat::Shares shares(U, a.grid);
-    int x = shares.begin(c);
-    const int x_end = shares.begin(c + 1);
-    if (x >= x_end)
-        return;
-    kvc_flat::row_of(a.batch, a.kv_heads, units, x, b, base);
+    int x, x_end, b, base;
+    kvc_flat::share_of_cta(a.batch, a.kv_heads, units, a.grid, c, x, x_end, b, base);
 
     for (int seg = 0; x < x_end; ++seg) {
-        int64_t first;
+        int T_abs;
         uint32_t bad;
-        const int n = visible(a, b, first, bad);
+        const int n = visible(a, b, T_abs, bad);
         const int line = row_units(n, kUnit), nu = line - kRowCost;
         const int h = (x - base) / line;
         const int p0 = (x - base) - h * line, p1 = min(line, p0 + (x_end - x));
@@ -577,7 +587,7 @@ quant_decode_kernel(const QuantDecodeArgs a)
 
         const uint8_t *kb = a.kq + slice * a.C * D + 16 * t, *vb = a.vq + slice * a.C * D + 16 * (lane % (D / 16));
         const float *ksb = a.ks + slice * a.C, *vsb = a.vs + slice * a.C;
-        const uint32_t cap = (uint32_t)a.C, start = (uint32_t)first;
+        const uint32_t cap = (uint32_t)a.C, start = first_slot(a, n, T_abs);
         // 16 keys whose rows follow one another: one address each for the keys, the values and the
         // scales, and constant steps.  Else (the last keys, or a ring's end among them) each row has its
         // own, a key past the last being the last again: its score is masked, and what is loaded is
@@ -649,7 +659,7 @@ quant_decode_kernel(const QuantDecodeArgs a)
 
         // ---- the group's queries: rotated, scaled by a power of two, halves ----
         {
-            const int64_t pos = (int64_t)a.len.total_abs[b] - 1;
+            const int64_t pos = (int64_t)T_abs - 1;
             const T *q = static_cast<const T *>(a.q) + slice * a.group * D;
             for (int r = warp; r < HEADS; r += kWarps) {
                 constexpr int PPL = D / 64;  // rotation pairs a lane
@@ -990,7 +1000,7 @@ quant_decode_kernel(const QuantDecodeArgs a)
             base = x;
             do {
                 ++b;
-            } while (visible(a, b, first, bad) == 0);
+            } while (visible(a, b, T_abs, bad) == 0);
         }
     }
 }
@@ -1000,7 +1010,7 @@ quant_decode_kernel(const QuantDecodeArgs a)
 // m and l are read at once, a part a thread; then D / 4 threads take the
 // columns of a part and the block's groups of them the parts in turn.
 constexpr int kMergeThreads = 128;
-constexpr int kMaxParts = 1024;  // at least the CTAs of the attention launch
+constexpr int kMaxParts = 4096;  // at least the CTAs of the attention launch
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kMergeThreads)
@@ -1014,9 +1024,9 @@ quant_merge_kernel(const QuantDecodeArgs a)
     const int b = slice / a.kv_heads, h = slice % a.kv_heads;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     auto units = [&](int bb) {
-        int64_t first;
+        int T;
         uint32_t bad;
-        return row_units(visible(a, bb, first, bad), a.unit);
+        return row_units(visible(a, bb, T, bad), a.unit);
     };
     int b_out, base;
     const int U = kvc_flat::locate(a.batch, a.kv_heads, units, b, b_out, base);
@@ -1144,10 +1154,10 @@ bool format_ok(int format) { return format == KVC_INT8 || format == KVC_E4M3; }
 template <typename T> kvc_status launch_append(const AppendArgs &a, int format, cudaStream_t stream)
 {
     const int lpr = a.D <= 64 ? 8 : a.D <= 128 ? 16 : 32;
-    // one wave of resident blocks (4 an SM) over all slices, or a block for every row tile
+    // 12 blocks an SM over all slices, or a block for every row tile: 31 us for 100 MB with 8, 35 with 6
     const int slices = a.batch * a.kv_heads;
     const int64_t tiles = ((int64_t)a.S * lpr + kAppendThreads - 1) / kAppendThreads;
-    const dim3 n((unsigned)std::min<int64_t>(tiles, (int64_t)kvc_host::sm_count() * 4 / slices + 1), slices);
+    const dim3 n((unsigned)std::min<int64_t>(tiles, (int64_t)kvc_host::sm_count() * 12 / slices + 1), slices);
     if (format == KVC_INT8) {
         if (lpr == 8)
             quant_append_kernel<T, KVC_INT8, 8><<<n, kAppendThreads, 0, stream>>>(a);
@@ -1168,10 +1178,10 @@ template <typename T> kvc_status launch_append(const AppendArgs &a, int format, 
 
 template <typename T> kvc_status launch_dequant(const DequantArgs &a, int format, cudaStream_t stream)
 {
-    // a block for every kRowsAhead * rpb rows, at most 64 an SM over all slices of K and V
+    // a block for every kRowsAhead * rpb rows, or one wave of resident blocks over all slices of K and V
     const int slices = a.batch * a.kv_heads, rpb = 256 / (a.D / 8);
     int64_t nx = (std::min(a.C, a.R) + kRowsAhead * rpb - 1) / (kRowsAhead * rpb);
-    nx = std::min<int64_t>(nx, (int64_t)kvc_host::sm_count() * 64 / (2 * slices) + 1);
+    nx = std::min<int64_t>(nx, (int64_t)kvc_host::sm_count() * kDequantCtas / (2 * slices) + 1);
     const dim3 grid((unsigned)nx, slices, 2);
     if (format == KVC_INT8)
         dequant_rows_kernel<T, KVC_INT8><<<grid, 256, 0, stream>>>(a);

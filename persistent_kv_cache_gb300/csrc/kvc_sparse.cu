@@ -271,7 +271,7 @@ struct Sum2 {
 // 64 rows of up to 2048 pages took 71 us with one CTA a row and a page at a time,
 // 24 us with the histograms of eight CTAs joined at every step.
 template <typename T, int D>
-__global__ void __launch_bounds__(kSelThreads)
+__global__ void __launch_bounds__(kSelThreads, 4)
 page_select_kernel(const SelectArgs a, int run_max)
 {
     extern __shared__ uint32_t keys[];            // [max_pages] scores as order_key, then the run's page ids
@@ -279,7 +279,7 @@ page_select_kernel(const SelectArgs a, int run_max)
     __shared__ __align__(16) int8_t code[2 * D];  // their codes
     __shared__ int warp_sum[kSelThreads / 32];
     __shared__ uint32_t hist[256];
-    __shared__ uint32_t pick[2];
+    __shared__ uint32_t pick[3];
     __shared__ float top_sh[kSelThreads / 32];
     __shared__ uint32_t edge_sh[2][kSelThreads / 32];
     int32_t *ids = reinterpret_cast<int32_t *>(keys + a.max_pages);
@@ -469,14 +469,18 @@ page_select_kernel(const SelectArgs a, int run_max)
             if (before < want && before + n >= want) {
                 pick[0] = 255 - tid;
                 pick[1] = want - before;
+                pick[2] = n;
             }
             __syncthreads();
             prefix = prefix << (left - shift) | pick[0];
             want = (int)pick[1];
             left = shift;
+            if ((int)pick[2] == want)
+                break;  // every key with these bits is taken
         }
-        least = lo + prefix;
-        ties = want;
+        // (left bits not looked at: the keys from prefix 0...0 on, all of them, which some key is below)
+        least = lo + (prefix << left) - (left > 0 ? 1 : 0);
+        ties = left > 0 ? 0 : want;
     }
 
     // ---- the chosen pages in ascending order: a run of pages a thread ----

@@ -544,15 +544,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                 kvc::raise_status(a.status, bad);
             return line_tiles(n);
         };
-        const int U = kvc_flat::locate(a.batch, line_rows, count, -1, walk.b, walk.base);
-        const kvc_flat::Shares shares(U, a.grid);
-        walk.x = shares.begin(blockIdx.x);
-        walk.x_end = shares.begin(blockIdx.x + 1);
         // (a CTA without a share falls through its loops)
-        if (walk.x < walk.x_end) {
-            kvc_flat::row_of(a.batch, line_rows, count, walk.x, walk.b, walk.base);
+        kvc_flat::share_of_cta(a.batch, line_rows, count, a.grid, blockIdx.x, walk.x, walk.x_end, walk.b, walk.base);
+        if (walk.x < walk.x_end)
             walk.load(a);
-        }
     }
     __syncthreads();
     kvc_tc::fence_after();
