@@ -166,22 +166,39 @@ def _ptr(t):
     would be read in the wrong order, or past its storage)."""
     if t is None:
         return None
+    if t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"expected a CUDA tensor, got one on {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"expected a contiguous tensor, got shape {tuple(t.shape)} "
-                         f"with strides {t.stride()}")
-    return t.data_ptr()
+    raise ValueError(f"expected a contiguous tensor, got shape {tuple(t.shape)} "
+                     f"with strides {t.stride()}")
+
+
+# the current stream's handle without a Stream object around it (a twentieth of the time)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
+def _stream_for(stream, t):
+    """The stream of a call on t, which has to be on the current device."""
+    at = torch.cuda.current_device()
+    if t.get_device() != at:
+        raise ValueError(f"the tensors are on {t.device}, the current device is cuda:{at}")
+    return _stream(stream) if stream is not None or _raw_stream is None else _raw_stream(at)
+
+
+_DTYPE_CODES = {torch.float32: KVC_F32, torch.bfloat16: KVC_BF16, torch.float16: KVC_F16}
+
+
 def _dtype_code(t: torch.Tensor) -> int:
-    return {torch.float32: KVC_F32, torch.bfloat16: KVC_BF16, torch.float16: KVC_F16}[t.dtype]
+    return _DTYPE_CODES[t.dtype]
 
 
 def _check(fn: str, status: int):
@@ -472,25 +489,29 @@ def kvc_window_prefill_step(out, q, k_cache, v_cache, new_k, new_v, lengths, win
 def _same(name, t, shape, dtype=None):
     """t has the shape (and type) that the other arguments fix: the library
     gets sizes once, from one of them, and cannot see the others'."""
-    if tuple(t.shape) != tuple(shape) or (dtype is not None and t.dtype != dtype):
+    if t.shape != shape or (dtype is not None and t.dtype is not dtype):
         raise ValueError(f"{name}: expected {tuple(shape)}{'' if dtype is None else f' {dtype}'}, "
                          f"got {tuple(t.shape)} {t.dtype}")
 
 
+_CODE_FORMATS = {torch.int8: KVC_INT8, torch.float8_e4m3fn: KVC_E4M3}
+
+
 def _code_format(kq):
-    if kq.dtype not in (torch.int8, torch.float8_e4m3fn):
+    fmt = _CODE_FORMATS.get(kq.dtype)
+    if fmt is None:
         raise ValueError(f"a quantised cache is torch.int8 or torch.float8_e4m3fn, got {kq.dtype}")
-    return KVC_INT8 if kq.dtype == torch.int8 else KVC_E4M3
+    return fmt
 
 
 def _quant_cache(kq, vq, k_scale, v_scale):
     """The sizes and format of a quantised cache: kq, vq [B, Hkv, C, D] codes and k_scale,
     v_scale [B, Hkv, C] float32."""
-    fmt = _code_format(kq)
-    _same("vq", vq, kq.shape, kq.dtype)
-    _same("k_scale", k_scale, kq.shape[:3], torch.float32)
-    _same("v_scale", v_scale, kq.shape[:3], torch.float32)
-    return kq.shape, fmt
+    fmt, shape = _code_format(kq), kq.shape
+    _same("vq", vq, shape, kq.dtype)
+    _same("k_scale", k_scale, shape[:3], torch.float32)
+    _same("v_scale", v_scale, shape[:3], torch.float32)
+    return shape, fmt
 
 
 def kvc_quant_append(kq, vq, k_scale, v_scale, new_k, new_v, lengths, windowed, rope=None,
@@ -505,7 +526,7 @@ def kvc_quant_append(kq, vq, k_scale, v_scale, new_k, new_v, lengths, windowed, 
     _check("kvc_quant_append", library().kvc_quant_append(
         _ptr(kq), _ptr(vq), _ptr(k_scale), _ptr(v_scale), _ptr(new_k), _ptr(new_v), lengths.c(), B,
         Hkv, S, C, D, _dtype_code(new_k), fmt, int(windowed), cs, sn, rmax, _ptr(status),
-        _stream(stream)))
+        _stream_for(stream, kq)))
 
 
 def kvc_dequant_rows(k_out, v_out, kq, vq, k_scale, v_scale, lengths, windowed, status=None,
@@ -518,7 +539,8 @@ def kvc_dequant_rows(k_out, v_out, kq, vq, k_scale, v_scale, lengths, windowed, 
     _same("v_out", v_out, (B, Hkv, R, D), k_out.dtype)
     _check("kvc_dequant_rows", library().kvc_dequant_rows(
         _ptr(k_out), _ptr(v_out), _ptr(kq), _ptr(vq), _ptr(k_scale), _ptr(v_scale), lengths.c(), B,
-        Hkv, C, R, D, _dtype_code(k_out), fmt, int(windowed), _ptr(status), _stream(stream)))
+        Hkv, C, R, D, _dtype_code(k_out), fmt, int(windowed), _ptr(status),
+        _stream_for(stream, kq)))
 
 
 def quant_decode_workspace(q, kq):
@@ -543,7 +565,7 @@ def kvc_gqa_decode_quant(out, q, kq, vq, k_scale, v_scale, lengths, windowed, lo
         _ptr(out), _ptr(q), _ptr(kq), _ptr(vq), _ptr(k_scale), _ptr(v_scale), lengths.c(), B, Hq,
         Hkv, C, D, _dtype_code(q), fmt, int(windowed), local_window_size, scale, cs, sn, rmax,
         _ptr(workspace), 0 if workspace is None else workspace.numel(), _ptr(status),
-        _stream(stream)))
+        _stream_for(stream, kq)))
     return out
 
 
@@ -558,7 +580,8 @@ def kvc_page_bounds(bounds, bound_scale, k_pool, block_table, lengths, new_token
     _same("block_table", block_table, (B, max_pages), torch.int32)
     _check("kvc_page_bounds", library().kvc_page_bounds(
         _ptr(bounds), _ptr(bound_scale), _ptr(k_pool), _ptr(block_table), max_pages, n_pages, ps,
-        lengths.c(), B, Hkv, new_tokens, D, _dtype_code(k_pool), _ptr(status), _stream(stream)))
+        lengths.c(), B, Hkv, new_tokens, D, _dtype_code(k_pool), _ptr(status),
+        _stream_for(stream, k_pool)))
 
 
 def sparse_workspace(q, k_pool, selected):
@@ -591,7 +614,7 @@ def kvc_gqa_decode_sparse(out, q, k_pool, v_pool, bounds, bound_scale, block_tab
         _ptr(block_table), block_table.shape[1], n_pages, ps, lengths.c(), B, Hq, Hkv, D,
         _dtype_code(q), selected.shape[2], sink_pages, recent_pages, _ptr(selected), scale, cs, sn,
         rmax, _ptr(workspace), 0 if workspace is None else workspace.numel(), _ptr(status),
-        _stream(stream)))
+        _stream_for(stream, q)))
     return out
 
 
@@ -611,7 +634,7 @@ def kvc_tree_mask(parents, mask=None, depth=None, status=None, stream=None):
     _same("mask", mask, (B, N, (N + 31) // 32), torch.int32)
     _same("depth", depth, (B, N), torch.int32)
     _check("kvc_tree_mask", library().kvc_tree_mask(
-        _ptr(parents), B, N, _ptr(mask), _ptr(depth), _ptr(status), _stream(stream)))
+        _ptr(parents), B, N, _ptr(mask), _ptr(depth), _ptr(status), _stream_for(stream, parents)))
     return mask, depth
 
 
@@ -640,7 +663,7 @@ def kvc_tree_append(k_cache, v_cache, new_k, new_v, depth, lengths, block_table=
     _check("kvc_tree_append", library().kvc_tree_append(
         _ptr(k_cache), _ptr(v_cache), _ptr(new_k), _ptr(new_v), _ptr(depth), table, m, n, ps,
         lengths.c(), B, Hkv, N, C, D, _dtype_code(k_cache), cs, sn, rmax, _ptr(status),
-        _stream(stream)))
+        _stream_for(stream, k_cache)))
 
 
 def tree_workspace(q, k_cache):
@@ -667,7 +690,7 @@ def kvc_gqa_tree(out, q, k_cache, v_cache, mask, depth, lengths, block_table=Non
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(mask), _ptr(depth), table, m, n, ps,
         lengths.c(), B, Hq, Hkv, N, C, D, _dtype_code(q), local_window_size, scale, cs, sn, rmax,
         _ptr(workspace), 0 if workspace is None else workspace.numel(), _ptr(status),
-        _stream(stream)))
+        _stream_for(stream, q)))
     return out
 
 
@@ -683,4 +706,4 @@ def kvc_tree_commit(k_cache, v_cache, path, accepted, lengths, seqlens_k, nodes,
     _check("kvc_tree_commit", library().kvc_tree_commit(
         _ptr(k_cache), _ptr(v_cache), _ptr(path), _ptr(accepted), path_len, table, m, n, ps,
         lengths.c(), _ptr(seqlens_k), B, Hkv, nodes, C, D, _dtype_code(k_cache), _ptr(status),
-        _stream(stream)))
+        _stream_for(stream, k_cache)))
