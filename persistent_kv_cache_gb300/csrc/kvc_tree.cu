@@ -252,9 +252,10 @@ tree_commit_kernel(const CommitArgs a)
 //   warp 0        issues tcgen05.mma in the order S_0, S_1, PV_0, S_2, PV_1, ...
 //   warps 1-8     softmax and output: two threads a row (= TMEM lane), each half
 //                 of the columns
-//   warp 9        TMA producer of the ring in the order of use (K_0, K_1, V_0,
-//                 K_2, ...), through the next segment's tiles without a stop
-//   warp 10       TMA of the next segment's queries once this one's last scores
+//   warps 9, 10   TMA producers of K and of V into one ring in the order of use
+//                 (K_0, K_1, V_0, K_2, ...), through the next segment's tiles
+//                 without a stop
+//   warp 11       TMA of the next segment's queries once this one's last scores
 //                 have been issued and are done
 // so that from one segment to the next the stream of keys does not stop: while
 // the softmax warps write one segment's output, the next one's first scores are
@@ -264,7 +265,16 @@ tree_commit_kernel(const CommitArgs a)
 // A slab is one TMA box: KR = 128 rows (a whole tile of K or of V) where that is
 // 32 KB at most and, in a paged cache, pages are whole tiles; else 64 rows, so
 // that it lies inside a page.  (A box costs its issuing thread about 640 clocks
-// whatever its size: with 16 KB boxes that bound the kernel.)  Only key tiles
+// whatever its size: with 16 KB boxes from one thread that bound the kernel.)
+//
+// Three roundings to 16 bits meet in an output: of the rotated query, of the
+// weights and of the result, each about as large as the others.  One of the first
+// two is taken out with a second product, whose time the tensor cores have to
+// spare: with head_dim <= 128 the query is a sum of two 16-bit numbers (two query
+// tiles fit beside the ring), with 256 the weights are (their second halves fit
+// beside the first in the score columns).
+//
+// Only key tiles
 // that hold drafts, or that a window's edge may cut, are masked ("cut" tiles).  A
 // row of V that not every query row sees may hold anything: 0 x NaN would reach
 // the rows that do not see it.  So in the cut tiles the softmax warps look
@@ -273,7 +283,7 @@ tree_commit_kernel(const CommitArgs a)
 
 constexpr int kBM = 128, kBN = 128;
 constexpr int kSoftmaxWarps = 8;
-constexpr int kAttnThreads = 32 * (1 + kSoftmaxWarps + 2);
+constexpr int kAttnThreads = 32 * (1 + kSoftmaxWarps + 3);
 constexpr float kRescale = 8.f;  // log2 units by which a score may exceed the reference maximum
 
 struct TreeArgs {
@@ -292,13 +302,15 @@ struct TreeArgs {
     int64_t rope_max_pos;
     int grid;
     float *ws_o, *ws_m, *ws_l;  // [2 * grid][128] (x D)
-    void *ws_q;                 // rotated queries, as q
+    void *ws_q;                 // rotated queries, as q: rounded, then (q_split) what that left
+    int q_split;
     uint32_t *see;              // drafts that each node sees, as mask
     int32_t *status;
 };
 
 template <int D, int KR> struct TreeSmem {
-    static constexpr int Q_BYTES = kBM * D * 2;
+    static constexpr bool SPLIT_Q = D <= 128;  // two query tiles; else two parts of the weights
+    static constexpr int Q_TILE = kBM * D * 2, Q_BYTES = SPLIT_Q ? 2 * Q_TILE : Q_TILE;
     static constexpr int SLAB = KR * D * 2;
     static constexpr int SPT = kBN / KR;  // slabs of a tile of K (or V)
     static constexpr int BUDGET = 227 * 1024;
@@ -446,16 +458,25 @@ tree_prep_kernel(const TreeArgs a, int D, unsigned q_blocks)
             sn[4 * e] = y.x, sn[4 * e + 1] = y.y, sn[4 * e + 2] = y.z, sn[4 * e + 3] = y.w;
         }
         T *x = reinterpret_cast<T *>(&lo), *y = reinterpret_cast<T *>(&hi);
+        uint4 lo2, hi2;
+        T *x2 = reinterpret_cast<T *>(&lo2), *y2 = reinterpret_cast<T *>(&hi2);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             float u = kvc::Elem<T>::to_f32(x[e]), v = kvc::Elem<T>::to_f32(y[e]);
             kvc::rope_pair(u, v, cs[e], sn[e]);
             x[e] = kvc::Elem<T>::from_f32(u);
             y[e] = kvc::Elem<T>::from_f32(v);
+            x2[e] = kvc::Elem<T>::from_f32(u - kvc::Elem<T>::to_f32(x[e]));
+            y2[e] = kvc::Elem<T>::from_f32(v - kvc::Elem<T>::to_f32(y[e]));
         }
         T *to = static_cast<T *>(a.ws_q) + row * D + c0;
         *reinterpret_cast<uint4 *>(to) = lo;
         *reinterpret_cast<uint4 *>(to + D / 2) = hi;
+        if (a.q_split) {
+            to += (int64_t)a.batch * a.q_heads * N * D;
+            *reinterpret_cast<uint4 *>(to) = lo2;
+            *reinterpret_cast<uint4 *>(to + D / 2) = hi2;
+        }
         return;
     }
     const int words = (N + 31) / 32;
@@ -557,27 +578,33 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     Segment cur, nxt;
     bool more = walk.next(a, cur);
 
-    if (warp == 1 + kSoftmaxWarps) {
-        // ======================= TMA producer of K and V =======================
+    if (warp == 1 + kSoftmaxWarps || warp == 2 + kSoftmaxWarps) {
+        // ======================= TMA producers of K and of V =======================
         // (the cache's rows are those of the kernels before tree_prep_kernel: no wait for it)
         if (lane == 0) {
-            kvc::tma_prefetch_desc(&tmap_k);
-            kvc::tma_prefetch_desc(&tmap_v);
-            int q = 0;  // slabs put into the ring so far
+            const bool mine_v = warp == 2 + kSoftmaxWarps;
+            const CUtensorMap *tmap = mine_v ? &tmap_v : &tmap_k;
+            kvc::tma_prefetch_desc(tmap);
+            int q = 0;  // slabs put into the ring so far, by both
             bool ok = true;
+            uint32_t filled = 0, phase = 0;  // slots that this thread has filled, with the parity of the last time
             while (ok && more) {
                 const int h = cur.row / a.row_tiles, nt = cur.t1 - cur.t0;
                 const int64_t end = (int64_t)cur.P + N;
                 bool again = false;
                 for (int u = 0; u < 2 * SPT * nt; ++u, ++q) {
+                    if (u == 0)
+                        again = walk.next(a, nxt);
+                    bool is_v;
+                    int tile;
+                    ring_group(u / SPT, nt, is_v, tile);
+                    if (is_v != mine_v)
+                        continue;
                     const int slot = q % NSLAB;
                     if (q >= NSLAB && !wait_or_abort(&empty[slot], ((q / NSLAB) - 1) & 1, abort_flag, a.status)) {
                         ok = false;
                         break;
                     }
-                    bool is_v;
-                    int tile;
-                    ring_group(u / SPT, nt, is_v, tile);
                     const int64_t r = (int64_t)cur.lo + (cur.t0 + tile) * kBN + (u % SPT) * KR;
                     int64_t y = -1;
                     if (r < end) {
@@ -596,21 +623,21 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                         kvc::mbar_arrive(&full[slot]);
                     } else {
                         kvc::mbar_arrive_expect_tx(&full[slot], SM::SLAB);
-                        kvc::tma_load_3d(smem + SM::RING_OFF + slot * SM::SLAB, is_v ? &tmap_v : &tmap_k, 0, (int32_t)y,
-                                         0, &full[slot]);
+                        kvc::tma_load_3d(smem + SM::RING_OFF + slot * SM::SLAB, tmap, 0, (int32_t)y, 0, &full[slot]);
                     }
-                    if (u == 0)
-                        again = walk.next(a, nxt);
+                    filled |= 1u << slot;
+                    phase = (phase & ~(1u << slot)) | ((uint32_t)((q / NSLAB) & 1) << slot);
                 }
                 cur = nxt;
                 more = again;
             }
             if (*abort_flag)
                 // wind-down: let the loads in flight land before the CTA exits
-                for (int i = max(0, q - NSLAB); i < q; ++i)
-                    kvc::mbar_wait(&full[i % NSLAB], (i / NSLAB) & 1);
+                for (int i = 0; i < NSLAB; ++i)
+                    if (filled >> i & 1)
+                        kvc::mbar_wait(&full[i], phase >> i & 1);
         }
-    } else if (warp == 2 + kSoftmaxWarps) {
+    } else if (warp == 3 + kSoftmaxWarps) {
         // ======================= TMA of the queries =======================
         if (lane == 0) {
             kvc::tma_prefetch_desc(&tmap_q);
@@ -620,8 +647,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                 if (s_no > 0 && !wait_or_abort(q_empty, (s_no - 1) & 1, abort_flag, a.status))
                     break;
                 const int h = cur.row / a.row_tiles, mt = cur.row % a.row_tiles;
-                kvc::mbar_arrive_expect_tx(q_full, SM::Q_BYTES);
-                kvc::tma_load_3d(smem, &tmap_q, 0, (cur.b * a.kv_heads + h) * rows + mt * kBM, 0, q_full);
+                const int y = (cur.b * a.kv_heads + h) * rows + mt * kBM;
+                kvc::mbar_arrive_expect_tx(q_full, a.q_split ? 2 * SM::Q_TILE : SM::Q_TILE);
+                kvc::tma_load_3d(smem, &tmap_q, 0, y, 0, q_full);
+                if (SM::SPLIT_Q && a.q_split)
+                    kvc::tma_load_3d(smem + SM::Q_TILE, &tmap_q, 0, y + a.batch * a.q_heads * N, 0, q_full);
                 more = walk.next(a, cur);
             }
             if (*abort_flag && s_no > 0)
@@ -632,6 +662,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         if (lane == 0) {
             int q = 0, J = 0;  // slabs and tiles taken so far
             bool ok = true;
+            const int q_parts = SM::SPLIT_Q && a.q_split ? 2 : 1;
             const uint64_t q_desc = kvc_tc::sw128_desc(smem_base, 16);
             const uint64_t k_ring = kvc_tc::sw128_desc(smem_base + SM::RING_OFF, 16);
             const uint64_t v_ring = kvc_tc::sw128_desc(smem_base + SM::RING_OFF, KR * 128);
@@ -643,10 +674,17 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                     kvc_tc::fence_after();
                     const uint64_t kd = k_ring + (uint64_t)(slot * (SM::SLAB / 16));
                     const uint32_t d_s = tmem + SM::COL_S + buf * kBN + hf * KR;
+                    // (a loop over the parts, not unrolled: with the second part's products written out after
+                    // the first's, head_dim 64 came out wrong in every second tile)
+#pragma unroll 1
+                    for (int part = 0; part < q_parts; ++part) {
+                        const uint64_t qd = q_desc + (uint64_t)(part * (SM::Q_TILE / 16));
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)
-                        kvc_tc::mma_ss(d_s, q_desc + (uint64_t)(((ks >> 2) * (kBM * 128) + (ks & 3) * 32) / 16),
-                                       kd + (uint64_t)(((ks >> 2) * (KR * 128) + (ks & 3) * 32) / 16), IDESC_S, ks > 0);
+                        for (int ks = 0; ks < D / 16; ++ks)
+                            kvc_tc::mma_ss(d_s, qd + (uint64_t)(((ks >> 2) * (kBM * 128) + (ks & 3) * 32) / 16),
+                                           kd + (uint64_t)(((ks >> 2) * (KR * 128) + (ks & 3) * 32) / 16), IDESC_S,
+                                           part > 0 || ks > 0);
+                    }
                     kvc_tc::commit(&empty[slot]);
                 }
                 kvc_tc::commit(&s_full[buf]);
@@ -677,6 +715,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                         for (int k2 = 0; k2 < KR / 16; ++k2)
                             kvc_tc::mma_ts(tmem + SM::COL_O, pa + k2 * 8, vd + (uint64_t)(k2 * (2048 / 16)), IDESC_O,
                                            j > 0 || hf > 0 || k2 > 0);
+                        if constexpr (!SM::SPLIT_Q) {
+#pragma unroll
+                            for (int k2 = 0; k2 < KR / 16; ++k2)
+                                kvc_tc::mma_ts(tmem + SM::COL_O, pa + 64 + k2 * 8, vd + (uint64_t)(k2 * (2048 / 16)),
+                                               IDESC_O, 1);
+                        }
                         kvc_tc::commit(&empty[slot]);
                     }
                     if (!ok)
@@ -840,7 +884,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                     }
                     const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
                     float ps0 = 0.f, ps1 = 0.f;
-                    uint32_t pk[32];
+                    uint32_t pk[32], pk2[SM::SPLIT_Q ? 1 : 32];
 #pragma unroll
                     for (int c = 0; c < 64; c += 2) {
                         const float p0 = kvc_tc::fast_exp2(fmaf(v[c], c_log2, neg_m));
@@ -848,9 +892,16 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                         ps0 += p0;
                         ps1 += p1;
                         pk[c / 2] = kvc_tc::pack2<T>(p0, p1);
+                        if constexpr (!SM::SPLIT_Q) {
+                            const T *w = reinterpret_cast<const T *>(&pk[c / 2]);
+                            pk2[c / 2] =
+                                kvc_tc::pack2<T>(p0 - kvc::Elem<T>::to_f32(w[0]), p1 - kvc::Elem<T>::to_f32(w[1]));
+                        }
                     }
                     l_run = spoiled ? NAN : l_run * alpha + (ps0 + ps1);
                     kvc_tc::st32(lane_addr + SM::COL_S + s * kBN + 32 * half, pk);
+                    if constexpr (!SM::SPLIT_Q)
+                        kvc_tc::st32(lane_addr + SM::COL_S + s * kBN + 64 + 32 * half, pk2);
                     if (__any_sync(0xffffffffu, rescale)) {
                         // the reference moved: rescale this half of the O row (PV of the tile before is done;
                         // a wait that gives up is reported at the next barrier)
@@ -1032,7 +1083,7 @@ cudaError_t launch_after(void (*kern)(A...), dim3 grid, int threads, size_t smem
 }
 
 template <typename T, int D, int KR>
-kvc_status launch_attn_dim(const TreeArgs &a, const void *k, const void *v, cudaStream_t stream)
+kvc_status launch_attn_dim(TreeArgs &a, const void *k, const void *v, cudaStream_t stream)
 {
     using SM = TreeSmem<D, KR>;
     const CUtensorMapDataType tt = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
@@ -1040,8 +1091,10 @@ kvc_status launch_attn_dim(const TreeArgs &a, const void *k, const void *v, cuda
     const uint64_t rows = (a.at.table ? (uint64_t)a.at.n_pool * a.at.page_size : (uint64_t)a.batch * a.at.rows) *
                           a.kv_heads;
     const int64_t q_rows = (int64_t)a.batch * a.q_heads * a.nodes;
+    a.q_split = SM::SPLIT_Q && a.cos_t;  // (an unrotated query is 16-bit as it is)
     CUtensorMap tq, tk, tv;
-    if (!kvc_host::encode_3d_sw128(&tq, a.cos_t ? a.ws_q : a.q, (uint64_t)q_rows, D, kBM, D / 64, tt) ||
+    if (!kvc_host::encode_3d_sw128(&tq, a.cos_t ? a.ws_q : a.q, (uint64_t)q_rows * (a.q_split ? 2 : 1), D, kBM, D / 64,
+                                   tt) ||
         !kvc_host::encode_3d_sw128(&tk, k, rows, D, KR, D / 64, tt) ||
         !kvc_host::encode_3d_sw128(&tv, v, rows, D, KR, D / 64, tt))
         return KVC_ERR_CUDA;
@@ -1132,7 +1185,7 @@ TreeLayout tree_layout(int batch, int q_heads, int nodes, int D)
 {
     TreeLayout l;
     l.q = 2 * (size_t)kvc_host::sm_count() * kBM * (D + 2) * sizeof(float);
-    l.see = l.q + (size_t)batch * q_heads * nodes * D * 2;
+    l.see = l.q + (size_t)batch * q_heads * nodes * D * 2 * 2;
     l.total = l.see + (size_t)batch * nodes * ((nodes + 31) / 32) * 4;
     return l;
 }

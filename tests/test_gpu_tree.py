@@ -133,12 +133,14 @@ class Case:
             if window > 0:
                 see &= at[:, None] - torch.cat([torch.arange(P), at])[None] < window
             x, y = self.at(b, torch.arange(P + N))
+            # the query (head_dim <= 128) or the weights (256) are sums of two numbers of the type
             step = R.half_step(self.dtype)
+            q_step, w_step = (step ** 2, step) if self.D <= 128 else (step, step ** 2)
             for h in range(self.H) if rows is None else rows:
                 kk, vv = (c[x, h, y].double() for c in (self.k, self.v))
                 heads = slice(h * G, (h + 1) * G)
                 qq = R.rotate64(self.q[b, heads], at, self.rope).reshape(G * N, self.D)
-                want, bound = R.attention(qq, kk, vv, see.repeat(G, 1), scale or self.D ** -0.5, step if self.rope else 0.0, step,
+                want, bound = R.attention(qq, kk, vv, see.repeat(G, 1), scale or self.D ** -0.5, q_step if self.rope else 0.0, w_step,
                                           self.dtype, half_weights=torch.ones(P + N) if self.dtype == F16 else None)
                 R.assert_within(got[b, heads].reshape(G * N, self.D), want, bound, f"row {b} head {h}")
                 assert not got[b, heads][:, ~there].any()
