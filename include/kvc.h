@@ -784,7 +784,8 @@ kvc_status kvc_page_bounds(void *bounds, float *bound_scale, const void *k_pool,
  *              (that row's output is then undefined, as in kvc_gqa_decode_paged).
  * sink_pages >= 0, recent_pages >= 1, their sum at most n_select (KVC_ERR_SHAPE);
  * max_pages <= 49152 (KVC_ERR_CAPACITY); batch * kv_heads <= 65535.
- * Types and sizes as kvc_gqa_decode_paged; with n_select >= pages its results.
+ * Types and sizes as kvc_gqa_decode_paged; the rotated query and the weights
+ * enter with the digits of two 16-bit numbers, and only the result is rounded.
  * workspace    device, kvc_gqa_decode_sparse_workspace_size(...) bytes, 256-byte
  *              aligned.  Calls that may overlap on the GPU need their own.
  */

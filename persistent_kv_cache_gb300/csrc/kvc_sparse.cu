@@ -13,12 +13,14 @@
 // taken does not depend on the order of any sum.
 //
 //   page_bounds_kernel   the bounds of the pages that a step filled
-//   page_select_kernel   scores, the choice of n pages, and the page table and
-//                        lengths under which the paged decode reads them
+//   page_select_kernel   scores, and the choice of n pages for each row and kv head
+//   sparse_decode_kernel attention over them
 #include <algorithm>
 #include <type_traits>
 
 #include "kvc_common.cuh"
+#include "kvc_flat.cuh"
+#include "kvc_tc.cuh"
 
 namespace {
 
@@ -185,7 +187,7 @@ struct SelectArgs {
     int64_t rope_max_pos;
     int32_t *selected;     // [B, kv_heads, n_select] logical pages
     int32_t *sub_table;    // the same as pages of the pool seen one head at a time
-    kvc_lengths sub_len;   // lengths of the B * kv_heads one-head rows
+    int32_t *done;         // [B * kv_heads] units of work finished, for the attention
     int32_t *status;
 };
 
@@ -283,6 +285,7 @@ page_select_kernel(const SelectArgs a, int run_max)
     __shared__ float top_sh[kSelThreads / 32];
     __shared__ uint32_t edge_sh[2][kSelThreads / 32];
     int32_t *ids = reinterpret_cast<int32_t *>(keys + a.max_pages);
+    kvc::grid_dep_launch();
     const uint32_t rank = cluster_rank(), ctas = cluster_size();
     const int h = blockIdx.x / ctas, b = blockIdx.y, row = b * a.kv_heads + h;
     const int tid = threadIdx.x;
@@ -300,12 +303,10 @@ page_select_kernel(const SelectArgs a, int run_max)
         L = -1;
     }
     int32_t *sel = a.selected + (int64_t)row * a.n_select, *sub = a.sub_table + (int64_t)row * a.n_select;
-    if (L < 0) {  // (every CTA of the cluster)
-        if (lead)
-            a.sub_len.past_abs[row] = a.sub_len.total_abs[row] = a.sub_len.cache_past[row] =
-                a.sub_len.cache_total[row] = a.sub_len.evict[row] = -1;
+    if (L < 0)  // (every CTA of the cluster)
         return;
-    }
+    if (lead)
+        a.done[row] = 0;
     const int pages = (total + a.page_size - 1) / a.page_size;
     const int take = min(pages, a.n_select);
     // pages [0, sink) and [tail, pages) are always taken
@@ -322,32 +323,7 @@ page_select_kernel(const SelectArgs a, int run_max)
         // this CTA's run of the middle pages
         const int run = (middle + (int)ctas - 1) / (int)ctas;
         const int first = min(middle, (int)rank * run), mine = min(run, middle - first);
-        for (int j = tid; j < mine; j += kSelThreads)
-            ids[j] = __ldg(table + sink + first + j);
-        __syncthreads();
-
-        // ---- bounds: 16 codes a lane, D / 8 lanes a page ----
-        constexpr int LPP = D / 8, PPB = kSelThreads / LPP, kAhead = 8;
-        const int sub_lane = tid % LPP;
-        uint4 v[kAhead];
-        float s[kAhead];
-        uint32_t bad = 0;
-        auto fetch = [&](int j0) {
-            bad = 0;
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int32_t id = ids[min(j0 + u * PPB, mine - 1)];
-                const bool out = id < 0 || id >= a.n_pool;
-                bad |= (uint32_t)out << u;
-                const int64_t slice = (int64_t)(out ? 0 : id) * a.kv_heads + h;
-                v[u] = __ldg(reinterpret_cast<const uint4 *>(a.bounds + slice * 2 * D) + sub_lane);
-                s[u] = __ldg(a.scale + slice);
-            }
-        };
-        if (mine > 0)
-            fetch(tid / LPP);
-
-        // ---- the group's query, in 8 bits ----
+        // the group's query, and by the other half of the threads the ids of the run's pages
         if (tid < D / 2) {
             const int p = tid;
             const int64_t pos = (int64_t)total - 1;
@@ -375,8 +351,34 @@ page_select_kernel(const SelectArgs a, int run_max)
                 part[0][p + e * (D / 2)] = __fadd_rn(up[e].hi, up[e].lo);
                 part[1][p + e * (D / 2)] = __fadd_rn(down[e].hi, down[e].lo);
             }
+        } else if (tid >= kSelThreads / 2) {
+            for (int j = tid - kSelThreads / 2; j < mine; j += kSelThreads / 2)
+                ids[j] = __ldg(table + sink + first + j);
         }
         __syncthreads();
+
+        // ---- bounds: 16 codes a lane, D / 8 lanes a page ----
+        constexpr int LPP = D / 8, PPB = kSelThreads / LPP, kAhead = 8;
+        const int sub_lane = tid % LPP;
+        uint4 v[kAhead];
+        float s[kAhead];
+        uint32_t bad = 0;
+        auto fetch = [&](int j0) {
+            bad = 0;
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int32_t id = ids[min(j0 + u * PPB, mine - 1)];
+                const bool out = id < 0 || id >= a.n_pool;
+                bad |= (uint32_t)out << u;
+                const int64_t slice = (int64_t)(out ? 0 : id) * a.kv_heads + h;
+                v[u] = __ldg(reinterpret_cast<const uint4 *>(a.bounds + slice * 2 * D) + sub_lane);
+                s[u] = __ldg(a.scale + slice);
+            }
+        };
+        if (mine > 0)
+            fetch(tid / LPP);
+
+        // ---- the query's codes ----
         float top = 0.f;
         for (int i = tid; i < 2 * D; i += kSelThreads)
             top = fmaxf(top, fabsf(part[i / D][i % D]));
@@ -485,7 +487,7 @@ page_select_kernel(const SelectArgs a, int run_max)
 
     // ---- the chosen pages in ascending order: a run of pages a thread ----
     {
-        const int each = (pages + kSelThreads - 1) / kSelThreads;
+        const int each = ((pages + kSelThreads - 1) / kSelThreads) | 1;  // (odd: the runs start in different banks)
         const int j0 = min(pages, tid * each), j1 = min(pages, j0 + each);
         auto rank_of = [&](int j) {  // 2: taken, 1: taken if among the first of its key, 0: not
             if (j < sink || j >= tail)
@@ -519,33 +521,608 @@ page_select_kernel(const SelectArgs a, int run_max)
         sel[i] = -1;
         sub[i] = -1;
     }
-    if (tid == 0) {
-        // the page of the newest token is the last one taken
-        const int rows = (take - 1) * a.page_size + total - (pages - 1) * a.page_size;
-        a.sub_len.past_abs[row] = total - 1;
-        a.sub_len.total_abs[row] = total;
-        a.sub_len.cache_past[row] = rows - 1;
-        a.sub_len.cache_total[row] = rows;
-        a.sub_len.evict[row] = 0;
+}
+
+// --------------------------------------------------------------------------
+// attention over the chosen pages
+// --------------------------------------------------------------------------
+
+constexpr int kUnit = 64;           // keys of a unit of work: pages are whole units
+constexpr int kRowCost = 8;         // units (kvc_flat.cuh) that a row costs beside its keys: 53 us with 2, 49 with 6, 48 with 8
+constexpr int kWarps = 4;           // that compute, 16 keys of a unit each
+constexpr int kDecodeThreads = 32 * (kWarps + 2);
+constexpr float kNone = -1e30f;     // a reference maximum before any score (finite: differences stay numbers)
+constexpr float kSlack = 8.f;       // log2 units a score may exceed its reference by
+
+struct SparseArgs {
+    void *out;
+    const void *q;
+    const int32_t *sub_table;       // [B * kv_heads, n_select] pages of the pool seen one head at a time
+    int32_t *done;                  // [B * kv_heads]
+    kvc_lengths len;
+    int batch, kv_heads, group, n_select, max_pages, page_size;
+    float scale_log2;
+    const float *cos_t, *sin_t;
+    int64_t rope_max_pos;
+    int grid;
+    float *ws_o, *ws_m, *ws_l;      // [2 * grid][group] (x D)
+    int32_t *status;
+};
+
+// the keys of a row of batch row b, all of whose chosen pages but the last (that of
+// the newest token) are full; 0: the batch row is rejected
+__device__ __forceinline__ int chosen_rows(const SparseArgs &a, int b, int &total)
+{
+    total = a.len.total_abs[b];
+    if (a.len.cache_total[b] < 0 || total < 1 || total > (int64_t)a.max_pages * a.page_size ||
+        (a.cos_t && (int64_t)total > a.rope_max_pos))
+        return 0;
+    const int pages = (total - 1) / a.page_size + 1;
+    return (min(pages, a.n_select) - 1) * a.page_size + total - (pages - 1) * a.page_size;
+}
+
+__host__ __device__ constexpr int ctas_per_sm(int D) { return D == 64 ? 3 : D == 128 ? 2 : 1; }
+
+template <int D, int HB> struct SparseSmem {
+    static constexpr int SLAB = kUnit * D * 2;                 // a unit's K or V
+    // (deeper, the queues before the memory hold up the joins more than the keys: 51 us with 2, 53 with 3)
+    static constexpr int STAGES = D == 64 ? 4 : 2;
+    static constexpr int HEADS = 8 * HB;
+    static constexpr int V_OFF = STAGES * SLAB, Q_OFF = 2 * STAGES * SLAB;
+    static constexpr int Q_BYTES = D / 16 * HB * 32 * 16;      // a lane's fragments of a k-step: two parts of two words
+    static constexpr int O_PITCH = D + 4;                      // floats
+    static constexpr int O_BYTES = HEADS * O_PITCH * 4;        // at a segment's end, in the queries' place
+    static constexpr int ML_OFF = Q_OFF + (Q_BYTES > O_BYTES ? Q_BYTES : O_BYTES);  // m and l of each warp
+    static constexpr int BAR_OFF = ML_OFF + 2 * kWarps * HEADS * 4;
+    static constexpr int FLAG_OFF = BAR_OFF + 4 * STAGES * 8;  // the abort flag, and whether this CTA joins
+    static constexpr int TOTAL = FLAG_OFF + 16;
+    static_assert(ctas_per_sm(D) * (TOTAL + 1024 + 1024) <= 228 * 1024, "resident CTAs");
+};
+
+template <typename T>
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (std::is_same<T, __half>::value)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void load_tiles(uint32_t (&r)[4], uint32_t at)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ void load_tiles_trans(uint32_t (&r)[4], uint32_t at)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t x)
+{
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ void compute_bar() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
+// x as a 16-bit number, and what that left
+template <typename T> __device__ __forceinline__ void parts_of(float x, T &hi, T &lo)
+{
+    hi = kvc::Elem<T>::from_f32(x);
+    lo = kvc::Elem<T>::from_f32(x - kvc::Elem<T>::to_f32(hi));
+}
+
+// Attention of one query over the chosen pages of a flat share of the (batch row,
+// kv head) rows (kvc_flat.cuh).  Memory bounds it: two warps bring K and V, 64 rows
+// a TMA box (pages are multiples of 64 rows), through a ring that fills the SM's
+// shared memory, and four warps take 16 keys each into mma.sync m16n8k16,
+//   scores  S^T[key][head] = K[key][:] . Q[head][:]
+//   output  O^T[d][head] += V^T[d][key] w[key][head]
+// (a group has 16 heads at most: the tensor cores have nine tenths of their time to
+// spare).  So the query, rotated in float32, and the weights are sums of two 16-bit
+// numbers each, at the price of a second product: of the roundings to 16 bits only
+// the result's is left.  A row that several CTAs worked on is joined by the one of
+// them that finishes last, in the order of the shares whichever that is.
+template <typename T, int D, int HB>
+__global__ void __launch_bounds__(kDecodeThreads, ctas_per_sm(D))
+sparse_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                     const SparseArgs a)
+{
+    using SM = SparseSmem<D, HB>;
+    using kvc_tc::wait_or_abort;
+    constexpr int HEADS = SM::HEADS, STAGES = SM::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + SM::BAR_OFF), *empty = full + 2 * STAGES;  // K's, then V's
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + SM::FLAG_OFF);
+    int *joins = reinterpret_cast<int *>(smem + SM::FLAG_OFF + 4);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = blockIdx.x;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2 * STAGES; ++i) {
+            kvc::mbar_init(&full[i], 1);
+            kvc::mbar_init(&empty[i], kWarps);
+        }
+        *abort_flag = 0;
+        kvc::fence_mbar_init();
+    }
+    auto units_of = [&](int b) {
+        int total;
+        const int n = chosen_rows(a, b, total);
+        return n > 0 ? (n + kUnit - 1) / kUnit + kRowCost : 0;
+    };
+    int x, x_end, b, base;
+    kvc_flat::share_of_cta(a.batch, a.kv_heads, units_of, a.grid, c, x, x_end, b, base);
+    __syncthreads();
+
+    // the share's segments, one at a time: units [u0, u1) of row (b, h)
+    struct {
+        int n, total, line, h, u0, u1;
+    } sg;
+    auto segment = [&]() -> bool {
+        if (x >= x_end)
+            return false;
+        sg.n = chosen_rows(a, b, sg.total);
+        sg.line = (sg.n + kUnit - 1) / kUnit + kRowCost;
+        sg.h = (x - base) / sg.line;
+        const int p0 = (x - base) - sg.h * sg.line, p1 = min(sg.line, p0 + (x_end - x));
+        // (the units that stand for the row's cost hold no keys)
+        sg.u0 = max(0, p0 - kRowCost);
+        sg.u1 = p1 - kRowCost;
+        x += p1 - p0;
+        return sg.u1 > sg.u0;
+    };
+    auto next_row = [&]() {
+        if (x == base + sg.line * a.kv_heads && x < x_end) {
+            int total;
+            base = x;
+            do {
+                ++b;
+            } while (chosen_rows(a, b, total) == 0);
+        }
+    };
+
+    if (warp >= kWarps) {
+        // ======================= TMA producers of K and of V =======================
+        const bool is_v = warp == kWarps + 1;
+        const CUtensorMap *tmap = is_v ? &tmap_v : &tmap_k;
+        uint64_t *my_full = full + (is_v ? STAGES : 0), *my_empty = empty + (is_v ? STAGES : 0);
+        uint8_t *ring = smem + (is_v ? SM::V_OFF : 0);
+        if (lane == 0)
+            kvc::tma_prefetch_desc(tmap);
+        kvc::grid_dep_wait();
+        int i = 0;  // units so far
+        bool ok = true;
+        while (ok && segment()) {
+            const int32_t *table = a.sub_table + ((int64_t)b * a.kv_heads + sg.h) * a.n_select;
+            const int per_page = a.page_size / kUnit;
+            int32_t id = 0;
+            for (int u = sg.u0; u < sg.u1; ++u, ++i) {
+                if (((u - sg.u0) & 31) == 0)
+                    id = u + lane < sg.u1 ? __ldg(table + (u + lane) / per_page) : 0;
+                const int32_t page = __shfl_sync(0xffffffffu, id, (u - sg.u0) & 31);
+                const int slot = i % STAGES;
+                if (i >= STAGES)
+                    ok = wait_or_abort(&my_empty[slot], (i / STAGES - 1) & 1, abort_flag, a.status);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    break;
+                if (lane == 0) {
+                    // a page outside the pool: reported, and the pool's first in its place
+                    if (page < 0 && !is_v)
+                        kvc::raise_status(a.status, KVC_DEV_INDEX_OOB);
+                    const int32_t y = page < 0 ? 0 : page * a.page_size + u % per_page * kUnit;
+                    kvc::mbar_arrive_expect_tx(&my_full[slot], SM::SLAB);
+                    kvc::tma_load_3d(ring + slot * SM::SLAB, tmap, 0, y, 0, &my_full[slot]);
+                }
+                __syncwarp();
+            }
+            next_row();
+        }
+        if (*abort_flag && lane == 0)
+            // wind-down: let the loads in flight land before the CTA exits
+            for (int k = max(0, i - STAGES); k < i; ++k)
+                kvc::mbar_wait(&my_full[k % STAGES], (k / STAGES) & 1);
+        return;
+    }
+
+    // ======================= attention =======================
+    const int g = lane >> 2, t = lane & 3;
+    const uint32_t ring = kvc::smem_u32(smem);
+    uint4 *q_frag = reinterpret_cast<uint4 *>(smem + SM::Q_OFF);
+    float *o_sh = reinterpret_cast<float *>(smem + SM::Q_OFF);
+    float *m_sh = reinterpret_cast<float *>(smem + SM::ML_OFF), *l_sh = m_sh + kWarps * HEADS;
+    // this lane's row of the four 8 x 8 tiles of a fragment, in K (rows are keys) and in V (transposed)
+    const int k_row = 16 * warp + (lane & 15), v_row = 16 * warp + (lane & 7) + (lane >> 4) * 8;
+    const int k_col = lane >> 4, v_col = lane >> 3 & 1;
+    auto chunk = [](int row, int col) {  // of a slab: 16 bytes `col` of `row`, 128-byte swizzled
+        return (uint32_t)((col >> 3) * (kUnit * 128) + row * 128 + ((col & 7) ^ (row & 7)) * 16);
+    };
+    int b_none, base_none;
+    const kvc_flat::Shares shares(kvc_flat::locate(a.batch, a.kv_heads, units_of, -1, b_none, base_none), a.grid);
+    int i = 0;
+    bool ok = true, waited = false;
+    for (int seg = 0; segment(); ++seg) {
+        const int64_t slice = (int64_t)b * a.kv_heads + sg.h;
+        const int n = sg.n;
+        // ---- the group's queries: rotated, as two parts, in the order of the fragments ----
+        {
+            const int64_t pos = (int64_t)sg.total - 1;
+            const T *q = static_cast<const T *>(a.q) + slice * a.group * D;
+            T *to = reinterpret_cast<T *>(q_frag);
+            auto place = [&](int r, int d) {  // (in elements) of the upper part of head r's column d
+                return (((d >> 4) * HB + (r >> 3)) * 32 + (r & 7) * 4 + (d >> 1 & 3)) * 8 + (d >> 3 & 1) * 2 + (d & 1);
+            };
+            for (int idx = threadIdx.x; idx < HEADS * (D / 2); idx += 32 * kWarps) {
+                const int r = idx / (D / 2), p = idx % (D / 2);
+                float lo = 0.f, hi = 0.f;
+                if (r < a.group) {
+                    lo = kvc::Elem<T>::to_f32(q[r * D + p]);
+                    hi = kvc::Elem<T>::to_f32(q[r * D + D / 2 + p]);
+                    if (a.cos_t)
+                        kvc::rope_pair(lo, hi, __ldg(a.cos_t + pos * (D / 2) + p), __ldg(a.sin_t + pos * (D / 2) + p));
+                }
+                const int e = place(r, p), f = place(r, p + D / 2);
+                parts_of(lo, to[e], to[e + 4]);
+                parts_of(hi, to[f], to[f + 4]);
+            }
+        }
+        if (!waited) {
+            kvc::grid_dep_wait();
+            waited = true;
+        }
+        compute_bar();
+
+        float o[HB][D / 16][4], m[HB][2], l[HB][2];
+#pragma unroll
+        for (int hb = 0; hb < HB; ++hb) {
+#pragma unroll
+            for (int dt = 0; dt < D / 16; ++dt)
+                o[hb][dt][0] = o[hb][dt][1] = o[hb][dt][2] = o[hb][dt][3] = 0.f;
+            m[hb][0] = m[hb][1] = kNone;
+            l[hb][0] = l[hb][1] = 0.f;
+        }
+        for (int u = sg.u0; u < sg.u1; ++u, ++i) {
+            const int slot = i % STAGES, key = u * kUnit + 16 * warp;  // the warp's first
+            ok = ok && wait_or_abort(&full[slot], (i / STAGES) & 1, abort_flag, a.status);
+            ok = __all_sync(0xffffffffu, ok);
+            const bool any = ok && key < n;
+            // ---- scores: a chain of products for each part of the query ----
+            float s[HB][4], s2[HB][4];
+#pragma unroll
+            for (int hb = 0; hb < HB; ++hb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    s[hb][e] = s2[hb][e] = 0.f;
+            if (any) {
+                const uint32_t at = ring + slot * SM::SLAB;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    uint32_t f[4];
+                    load_tiles(f, at + chunk(k_row, 2 * ks + k_col));
+#pragma unroll
+                    for (int hb = 0; hb < HB; ++hb) {
+                        const uint4 qf = q_frag[(ks * HB + hb) * 32 + lane];
+                        mma16<T>(s[hb], f, qf.x, qf.y);
+                        mma16<T>(s2[hb], f, qf.z, qf.w);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0)
+                kvc::mbar_arrive(&empty[slot]);
+
+            uint32_t wt[HB][2][2];  // weights: part, keys from 0 or 8 on
+            if (any) {
+                // ---- softmax ----
+                const bool tail = key + 16 > n;
+                float z[HB][4], top = kNone;
+#pragma unroll
+                for (int hb = 0; hb < HB; ++hb)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float v = (s[hb][e] + s2[hb][e]) * a.scale_log2;
+                        if (tail && key + g + 8 * (e >> 1) >= n)
+                            v = -INFINITY;
+                        z[hb][e] = v;
+                        top = fmaxf(top, v - m[hb][e & 1]);
+                    }
+                if (__any_sync(0xffffffffu, top > kSlack)) {
+                    // a reference is left behind: raise it to the tile's maximum
+#pragma unroll
+                    for (int hb = 0; hb < HB; ++hb) {
+                        float shrink[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float mx = fmaxf(z[hb][e], z[hb][2 + e]);
+#pragma unroll
+                            for (int d = 4; d < 32; d <<= 1)
+                                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                            mx = fmaxf(mx, m[hb][e]);  // (fmaxf drops a NaN: the reference stays a number)
+                            shrink[e] = kvc_tc::fast_exp2(m[hb][e] - mx);
+                            l[hb][e] *= shrink[e];
+                            m[hb][e] = mx;
+                        }
+#pragma unroll
+                        for (int dt = 0; dt < D / 16; ++dt) {
+                            o[hb][dt][0] *= shrink[0];
+                            o[hb][dt][1] *= shrink[1];
+                            o[hb][dt][2] *= shrink[0];
+                            o[hb][dt][3] *= shrink[1];
+                        }
+                    }
+                }
+#pragma unroll
+                for (int hb = 0; hb < HB; ++hb)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float w0 = kvc_tc::fast_exp2(z[hb][2 * e] - m[hb][0]);
+                        const float w1 = kvc_tc::fast_exp2(z[hb][2 * e + 1] - m[hb][1]);
+                        l[hb][0] += w0;
+                        l[hb][1] += w1;
+                        const uint32_t hi = kvc_tc::pack2<T>(w0, w1);
+                        const T *back = reinterpret_cast<const T *>(&hi);
+                        wt[hb][0][e] = transposed(hi);
+                        wt[hb][1][e] = transposed(
+                            kvc_tc::pack2<T>(w0 - kvc::Elem<T>::to_f32(back[0]), w1 - kvc::Elem<T>::to_f32(back[1])));
+                    }
+            }
+
+            // ---- output ----
+            ok = ok && wait_or_abort(&full[STAGES + slot], (i / STAGES) & 1, abort_flag, a.status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (any && ok) {
+                const uint32_t at = ring + SM::V_OFF + slot * SM::SLAB;
+                // what a row past the last holds does not reach the sums
+                const bool tail = key + 16 > n;
+                const int k0 = key + 2 * t;
+                const uint32_t keep0 = (k0 < n ? 0xffffu : 0u) | (k0 + 1 < n ? 0xffff0000u : 0u);
+                const uint32_t keep1 = (k0 + 8 < n ? 0xffffu : 0u) | (k0 + 9 < n ? 0xffff0000u : 0u);
+#pragma unroll
+                for (int dt = 0; dt < D / 16; ++dt) {
+                    uint32_t f[4];
+                    load_tiles_trans(f, at + chunk(v_row, 2 * dt + v_col));
+                    if (tail) {
+                        f[0] &= keep0;
+                        f[1] &= keep0;
+                        f[2] &= keep1;
+                        f[3] &= keep1;
+                    }
+#pragma unroll
+                    for (int hb = 0; hb < HB; ++hb) {
+                        mma16<T>(o[hb][dt], f, wt[hb][0][0], wt[hb][0][1]);
+                        mma16<T>(o[hb][dt], f, wt[hb][1][0], wt[hb][1][1]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0)
+                kvc::mbar_arrive(&empty[STAGES + slot]);
+        }
+
+        // ---- join the warps: m, l, then O relative to the common m, one warp after another ----
+#pragma unroll
+        for (int hb = 0; hb < HB; ++hb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1)
+                    l[hb][e] += __shfl_xor_sync(0xffffffffu, l[hb][e], d);
+                if (g == 0) {
+                    m_sh[warp * HEADS + hb * 8 + 2 * t + e] = m[hb][e];
+                    l_sh[warp * HEADS + hb * 8 + 2 * t + e] = l[hb][e];
+                }
+            }
+        compute_bar();
+        float f[HB][2];
+#pragma unroll
+        for (int hb = 0; hb < HB; ++hb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w)
+                    top = fmaxf(top, m_sh[w * HEADS + hb * 8 + 2 * t + e]);
+                f[hb][e] = exp2f(m[hb][e] - top);
+            }
+        auto o_at = [&](int hb, int dt, int e) {
+            return (hb * 8 + 2 * t + (e & 1)) * SM::O_PITCH + dt * 16 + g + 8 * (e >> 1);
+        };
+        for (int w = 0; w < kWarps; ++w) {
+            if (warp == w) {
+#pragma unroll
+                for (int hb = 0; hb < HB; ++hb) {
+                    // (every load before the first store: they may not pass one another)
+                    if (w > 0) {
+#pragma unroll
+                        for (int dt = 0; dt < D / 16; ++dt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                o[hb][dt][e] = fmaf(o[hb][dt][e], f[hb][e & 1], o_sh[o_at(hb, dt, e)]);
+                    } else {
+#pragma unroll
+                        for (int dt = 0; dt < D / 16; ++dt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                o[hb][dt][e] *= f[hb][e & 1];
+                    }
+#pragma unroll
+                    for (int dt = 0; dt < D / 16; ++dt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o_sh[o_at(hb, dt, e)] = o[hb][dt][e];
+                }
+            }
+            compute_bar();
+        }
+        const bool whole = sg.u0 == 0 && sg.u1 == sg.line - kRowCost;
+        const int64_t part = 2 * (int64_t)c + (seg == 0 ? 0 : 1);
+        if (ok) {
+            for (int idx = threadIdx.x; idx < a.group * D; idx += 32 * kWarps) {
+                const int r = idx / D, d = idx % D;
+                float top = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w)
+                    top = fmaxf(top, m_sh[w * HEADS + r]);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w)
+                    sum += l_sh[w * HEADS + r] * exp2f(m_sh[w * HEADS + r] - top);
+                const float v = o_sh[r * SM::O_PITCH + d];
+                if (whole) {
+                    static_cast<T *>(a.out)[slice * a.group * D + idx] = kvc::Elem<T>::from_f32(v / sum);
+                } else {
+                    a.ws_o[(part * a.group + r) * D + d] = v;
+                    if (d == 0) {
+                        a.ws_m[part * a.group + r] = top;
+                        a.ws_l[part * a.group + r] = sum;
+                    }
+                }
+            }
+        }
+        if (!whole) {
+            // (after a wait that gave up the count stays short, and nobody joins)
+            __threadfence();
+            compute_bar();
+            if (threadIdx.x == 0) {
+                const int mine = ok ? sg.u1 - sg.u0 : 0;
+                *joins = ok && atomicAdd(a.done + slice, mine) + mine == sg.line - kRowCost;
+                __threadfence();
+            }
+            compute_bar();
+            if (*joins) {
+                const int x0 = base + sg.h * sg.line;
+                const int c0 = shares.of(x0 + kRowCost), parts = shares.of(x0 + sg.line - 1) - c0 + 1;
+                // the row's segment is the first of its CTA, but in CTA c0 if that began before the row
+                const int slot0 = shares.begin(c0) < x0 ? 1 : 0;
+                for (int r = warp; r < a.group; r += kWarps) {
+                    // eight parts under way at a time
+                    constexpr int AHEAD = 8;
+                    float top = -INFINITY, sum = 0.f, acc[D / 32];
+#pragma unroll
+                    for (int e = 0; e < D / 32; ++e)
+                        acc[e] = 0.f;
+                    for (int k0 = 0; k0 < parts; k0 += AHEAD) {
+                        float pm[AHEAD], pl[AHEAD], po[AHEAD][D / 32], was = top;
+#pragma unroll
+                        for (int k = 0; k < AHEAD; ++k) {
+                            const int kk = min(k0 + k, parts - 1);
+                            const int64_t at = (2 * (int64_t)(c0 + kk) + (kk == 0 ? slot0 : 0)) * a.group + r;
+                            pm[k] = k0 + k < parts ? __ldcg(a.ws_m + at) : -INFINITY;
+                            pl[k] = __ldcg(a.ws_l + at);
+#pragma unroll
+                            for (int e = 0; e < D / 32; ++e)
+                                po[k][e] = __ldcg(a.ws_o + at * D + lane + 32 * e);
+                        }
+#pragma unroll
+                        for (int k = 0; k < AHEAD; ++k)
+                            top = fmaxf(top, pm[k]);
+                        const float shrink = exp2f(was - top);
+                        sum *= shrink;
+#pragma unroll
+                        for (int e = 0; e < D / 32; ++e)
+                            acc[e] *= shrink;
+#pragma unroll
+                        for (int k = 0; k < AHEAD; ++k) {
+                            const float w = exp2f(pm[k] - top);
+                            // (a part that is not there has no weight, whatever was read in its place)
+                            if (k0 + k < parts) {
+                                sum = fmaf(w, pl[k], sum);
+#pragma unroll
+                                for (int e = 0; e < D / 32; ++e)
+                                    acc[e] = fmaf(w, po[k][e], acc[e]);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < D / 32; ++e)
+                        static_cast<T *>(a.out)[(slice * a.group + r) * D + lane + 32 * e] =
+                            kvc::Elem<T>::from_f32(acc[e] / sum);
+                }
+            }
+        }
+        compute_bar();  // shared memory may be written again
+        next_row();
     }
 }
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// the parts of the workspace: the sub-table, the sub-lengths, the decode's
-// own scratch
+// one wave of resident CTAs, or one CTA a unit where the rows have fewer
+int decode_grid(int batch, int kv_heads, int page_size, int n_select, int D)
+{
+    const int64_t most = (int64_t)batch * kv_heads * ((int64_t)n_select * page_size / kUnit + kRowCost);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(most, (int64_t)kvc_host::sm_count() * ctas_per_sm(D)));
+}
+
+// the parts of the workspace: the chosen pages, the counts, the partial results
 struct SparseLayout {
-    size_t lens, decode, total;
+    size_t done, o, m, l, total;
 };
-SparseLayout sparse_layout(int batch, int q_heads, int kv_heads, int page_size, int n_select, int D, int dtype)
+SparseLayout sparse_layout(int batch, int q_heads, int kv_heads, int page_size, int n_select, int D)
 {
     SparseLayout l;
     const size_t rows = (size_t)batch * kv_heads;
-    l.lens = align256(rows * n_select * 4);
-    l.decode = l.lens + align256(5 * rows * 4);
-    l.total = l.decode + kvc_gqa_decode_workspace_size((int)rows, q_heads / kv_heads, 1, (int64_t)n_select * page_size,
-                                                       D, dtype);
+    const size_t parts = 2 * (size_t)decode_grid(batch, kv_heads, page_size, n_select, D) * (q_heads / kv_heads);
+    l.done = align256(rows * n_select * 4);
+    l.o = l.done + align256(rows * 4);
+    l.m = l.o + parts * D * 4;
+    l.l = l.m + parts * 4;
+    l.total = l.l + parts * 4;
     return l;
+}
+
+template <typename T, int D, int HB>
+kvc_status launch_decode(const SparseArgs &a, const void *k_pool, const void *v_pool, int64_t n_pool,
+                         cudaStream_t stream)
+{
+    using SM = SparseSmem<D, HB>;
+    const CUtensorMapDataType type = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const uint64_t rows = (uint64_t)n_pool * a.kv_heads * a.page_size;
+    CUtensorMap tk, tv;
+    if (!kvc_host::encode_3d_sw128(&tk, k_pool, rows, D, kUnit, D / 64, type) ||
+        !kvc_host::encode_3d_sw128(&tv, v_pool, rows, D, kUnit, D / 64, type))
+        return KVC_ERR_CUDA;
+    auto kern = sparse_decode_kernel<T, D, HB>;
+    const int smem = SM::TOTAL + 1024;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return KVC_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(a.grid);
+    cfg.blockDim = dim3(kDecodeThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, tk, tv, a) != cudaSuccess)
+        return KVC_ERR_CUDA;
+    return kvc_host::launch_status();
+}
+
+template <typename T>
+kvc_status launch_decode_dim(const SparseArgs &a, const void *k, const void *v, int64_t n_pool, int D,
+                             cudaStream_t stream)
+{
+    const bool two = a.group > 8;
+    switch (D) {
+    case 64:
+        return two ? launch_decode<T, 64, 2>(a, k, v, n_pool, stream) : launch_decode<T, 64, 1>(a, k, v, n_pool, stream);
+    case 128:
+        return two ? launch_decode<T, 128, 2>(a, k, v, n_pool, stream) : launch_decode<T, 128, 1>(a, k, v, n_pool, stream);
+    default:
+        return two ? launch_decode<T, 256, 2>(a, k, v, n_pool, stream) : launch_decode<T, 256, 1>(a, k, v, n_pool, stream);
+    }
 }
 
 bool sizes_ok(int batch, int q_heads, int kv_heads, int page_size, int n_select, int D)
@@ -653,7 +1230,9 @@ KVC_API size_t kvc_gqa_decode_sparse_workspace_size(int batch, int q_heads, int 
     if (!sizes_ok(batch, q_heads, kv_heads, page_size, n_select, head_dim) || batch < 1 ||
         (int64_t)n_select * page_size > (int64_t)INT32_MAX || (int64_t)batch * kv_heads > 65535)
         return 0;
-    return sparse_layout(batch, q_heads, kv_heads, page_size, n_select, head_dim, dtype).total;
+    if (kvc_host::elem_bytes_of(dtype) == 0 || (head_dim != 64 && head_dim != 128 && head_dim != 256))
+        return 0;
+    return sparse_layout(batch, q_heads, kv_heads, page_size, n_select, head_dim).total;
 }
 
 KVC_API kvc_status kvc_gqa_decode_sparse(void *out, const void *q, const void *k_pool, const void *v_pool,
@@ -676,7 +1255,8 @@ KVC_API kvc_status kvc_gqa_decode_sparse(void *out, const void *q, const void *k
     if ((int64_t)batch * kv_heads > 65535)
         return KVC_ERR_SHAPE;
     if (max_pages > kMaxPages || (int64_t)max_pages * page_size > (int64_t)INT32_MAX || (int64_t)n_select * page_size > (int64_t)INT32_MAX ||
-        n_pool_pages * kv_heads * (int64_t)page_size > (int64_t)INT32_MAX)
+        n_pool_pages * kv_heads * (int64_t)page_size > (int64_t)INT32_MAX ||
+        (int64_t)batch * kv_heads * ((int64_t)n_select * page_size / kUnit + kRowCost) > (int64_t)INT32_MAX)
         return KVC_ERR_CAPACITY;
     if ((rope_cos == nullptr) != (rope_sin == nullptr))
         return KVC_ERR_NULL;
@@ -690,14 +1270,12 @@ KVC_API kvc_status kvc_gqa_decode_sparse(void *out, const void *q, const void *k
     for (const void *p : {(const void *)out, q, k_pool, v_pool, bounds, (const void *)bound_scale})
         if (!kvc_host::aligned16(p))
             return KVC_ERR_ALIGN;
-    const SparseLayout l = sparse_layout(batch, q_heads, kv_heads, page_size, n_select, head_dim, dtype);
+    const SparseLayout l = sparse_layout(batch, q_heads, kv_heads, page_size, n_select, head_dim);
     if (!workspace || workspace_bytes < l.total)
         return KVC_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u)
         return KVC_ERR_ALIGN;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const int rows = batch * kv_heads;
-    int32_t *lens = reinterpret_cast<int32_t *>(ws + l.lens);
     SelectArgs a{};
     a.q = q;
     a.bounds = static_cast<const int8_t *>(bounds);
@@ -718,17 +1296,34 @@ KVC_API kvc_status kvc_gqa_decode_sparse(void *out, const void *q, const void *k
     a.rope_max_pos = rope_max_pos;
     a.selected = selected;
     a.sub_table = reinterpret_cast<int32_t *>(ws);
-    a.sub_len = kvc_lengths{lens, lens + rows, lens + 2 * rows, lens + 3 * rows, lens + 4 * rows};
+    a.done = reinterpret_cast<int32_t *>(ws + l.done);
     a.status = dev_status;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     const kvc_status st =
         dtype == KVC_BF16 ? launch_select<__nv_bfloat16>(a, head_dim, stream) : launch_select<__half>(a, head_dim, stream);
     if (st != KVC_OK)
         return st;
-    // Page id of head h is page id * kv_heads + h of the same pool seen as
-    // one-head pages, and (b, h) a batch row of `group` query heads: the paged
-    // decode reads the chosen pages of every head as they lie.
-    return kvc_gqa_decode_paged(out, q, k_pool, v_pool, a.sub_table, n_select, n_pool_pages * kv_heads, page_size,
-                                a.sub_len, rows, a.group, 1, head_dim, dtype, 0, scale, rope_cos, rope_sin,
-                                rope_max_pos, ws + l.decode, workspace_bytes - l.decode, dev_status, stream_);
+    SparseArgs d{};
+    d.out = out;
+    d.q = q;
+    d.sub_table = a.sub_table;
+    d.done = a.done;
+    d.len = len;
+    d.batch = batch;
+    d.kv_heads = kv_heads;
+    d.group = a.group;
+    d.n_select = n_select;
+    d.max_pages = max_pages;
+    d.page_size = page_size;
+    d.scale_log2 = (scale == 0.f ? 1.f / sqrtf((float)head_dim) : scale) * 1.44269504088896340736f;
+    d.cos_t = rope_cos;
+    d.sin_t = rope_sin;
+    d.rope_max_pos = rope_max_pos;
+    d.grid = decode_grid(batch, kv_heads, page_size, n_select, head_dim);
+    d.ws_o = reinterpret_cast<float *>(ws + l.o);
+    d.ws_m = reinterpret_cast<float *>(ws + l.m);
+    d.ws_l = reinterpret_cast<float *>(ws + l.l);
+    d.status = dev_status;
+    return dtype == KVC_BF16 ? launch_decode_dim<__nv_bfloat16>(d, k_pool, v_pool, n_pool_pages, head_dim, stream)
+                             : launch_decode_dim<__half>(d, k_pool, v_pool, n_pool_pages, head_dim, stream);
 }

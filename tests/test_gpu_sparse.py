@@ -107,7 +107,7 @@ def run(K, dtype, B, H, G, D, page, m, n, sink, recent, totals, rope=True, seed=
     selected = torch.full((B, H, n), -7, dtype=torch.int32, device="cuda")
     d = [x.cuda() for x in (q, k, v, bounds, bscale, table)]
     K.kvc_gqa_decode_sparse(out, *d, L, selected, sink, recent, scale=scale, rope=tables and [x.cuda() for x in tables], status=st)
-    step = R.half_step(dtype)
+    step = R.half_step(dtype)  # (query and weights are sums of two numbers of the type)
     for b, T in enumerate(totals):
         if T < 1 or T > m * page:
             assert (out[b] == 7).all() and (selected[b] == -7).all()
@@ -123,7 +123,7 @@ def run(K, dtype, B, H, G, D, page, m, n, sink, recent, totals, rope=True, seed=
             rows = torch.cat([torch.arange(j * page, min(T, (j + 1) * page)) for j in mine])
             kk, vv = (x[table[b, rows // page].long(), h, rows % page].double() for x in (k, v))
             want, bound = R.attention(R.rotate64(q[b, heads], at, tables)[:, 0], kk, vv, torch.ones((G, len(rows)), dtype=torch.bool),
-                                      scale or D ** -0.5, step if rope else 0.0, step, dtype,
+                                      scale or D ** -0.5, step ** 2 if rope else 0.0, step ** 2, dtype,
                                       half_weights=torch.ones(len(rows)) if dtype == F16 else None)
             R.assert_within(out[b, heads, 0], want, bound, f"row {b} head {h}")
     return out, selected, st.item()
@@ -172,20 +172,30 @@ def test_a_page_that_is_not_finite_is_taken(K):
     assert torch.isnan(out[0, :2].float()).all()
 
 
-def test_every_page_is_the_paged_decode(K):
-    for dtype, D, G in ((BF16, 128, 4), (F16, 256, 16)):
-        B, H, m, page = 5, 2, 33, 64
-        g = gen(8)
-        table, k, v = make(g, B, H, D, page, m, dtype)
-        bounds, bscale = all_bounds(k)
-        q = torch.randn((B, H * G, 1, D), generator=g).to(dtype).cuda()
-        rope = [x.cuda() for x in R.rope_tables(m * page, D)]
-        L = lengths(K, [m * page, 1, 700, 64, 65], 1, m * page)
-        k, v, bounds, bscale, table = (x.cuda() for x in (k, v, bounds, bscale, table))
-        sel = torch.zeros((B, H, m), dtype=torch.int32, device="cuda")
-        a = K.kvc_gqa_decode_sparse(torch.zeros_like(q), q, k, v, bounds, bscale, table, L, sel, rope=rope)
-        b = K.kvc_gqa_decode_paged(torch.zeros_like(q), q, k, v, table, L, rope=rope)
-        assert torch.equal(a, b)
+def test_every_page_taken(K):
+    for dtype, D, G in ((BF16, 128, 4), (F16, 256, 16), (F16, 64, 12)):
+        _, sel, _ = run(K, dtype, 5, 2, G, D, 64, 33, 33, 0, 1, [33 * 64, 1, 700, 64, 65])
+        assert sel[2, 1].tolist() == list(range(11)) + [-1] * 22
+
+
+@pytest.mark.parametrize("B,H,D", [(1, 1, 128), (1, 3, 64), (40, 8, 64), (70, 2, 256), (3, 1, 128)])
+def test_shares_of_few_and_of_many_rows(K, B, H, D):
+    """rows that many CTAs join, and CTAs with many rows; again into the same workspace"""
+    g = gen(B)
+    m, n = 60 if B < 10 else 7, 50 if B < 10 else 4
+    totals = [int(torch.randint(0, m * 64 + 1, (), generator=g)) for _ in range(B)]
+    totals[0] = m * 64
+    a = run(K, F16, B, H, 3, D, 64, m, n, 1, 1, totals)
+    b = run(K, F16, B, H, 3, D, 64, m, n, 1, 1, totals)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_rows_past_the_newest_token_hold_anything(K):
+    def edit(q, k, v, table):
+        for x in (k, v):
+            x[table[0, 12], :, 10:] = math.nan
+            x[table[1, 3], :, 63] = math.inf
+    run(K, BF16, 2, 2, 4, 128, 64, 13, 4, 0, 1, [12 * 64 + 10, 4 * 64 - 1], edit=edit)
 
 
 def test_bad_pages(K):

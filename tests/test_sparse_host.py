@@ -33,8 +33,9 @@ def test_bounds(K):
 def test_decode(K):
     f, L, lib = "kvc_gqa_decode_sparse", K.KvcLengths(F, F, F, F, F), K.library()
     need = lib.kvc_gqa_decode_sparse_workspace_size(2, 8, 2, 64, 4, 64, 1)
-    # tables and lengths in 256-byte units, then the decode's own for four one-head rows
-    assert need == 256 + 256 + lib.kvc_gqa_decode_workspace_size(4, 4, 1, 256, 64, 1)
+    # page ids and counts in 256-byte units; four rows of 4 units and the 8 for a row, a CTA each, two slots each
+    assert need == 256 + 256 + 2 * 4 * (4 + 8) * 4 * (64 + 2) * 4
+    assert lib.kvc_gqa_decode_sparse_workspace_size(2, 8, 2, 64, 4, 96, 1) == 0
     assert lib.kvc_gqa_decode_sparse_workspace_size(2, 8, 3, 64, 4, 64, 1) == 0
     assert lib.kvc_gqa_decode_sparse_workspace_size(2, 8, 2, 63, 4, 64, 1) == 0
     a = dict(out=F, q=2 * F, k=3 * F, v=4 * F, bounds=5 * F, scale=6 * F, table=7 * F, m=8, n=32, page=64, len=L, B=2, Hq=8, H=2,
