@@ -488,18 +488,19 @@ __host__ __device__ constexpr int unit_of(int D, int HB) { return 16 * tiles_of(
 // resident CTAs an SM, by the registers that O and the query fragments take
 __host__ __device__ constexpr int ctas_per_sm(int D, int HB) { return D * HB <= 256 ? 3 : 2; }
 
-template <int D, int HB> struct QuantSmem {
+template <int D, int HB, bool F16> struct QuantSmem {
     static constexpr int HEADS = 8 * HB;
+    static constexpr int Q_ROWS = F16 ? 2 * HEADS : HEADS;  // fp16: what a row's rounding left, in a second one
     static constexpr int Q_PITCH = D * 2 + 8;     // bytes: a fragment's 16 half-warp reads hit 16 distinct 8-byte banks
-    static constexpr int Q_BYTES = HEADS * Q_PITCH;
+    static constexpr int Q_BYTES = Q_ROWS * Q_PITCH;
     // A stage of a warp's ring, a tile of 16 keys: K piece by piece, each lane's own 16 bytes; V row by
     // row, its 16-byte chunks swizzled (v_chunk); a scale a lane
     static constexpr int K_PIECES = 2 * (D / 64), V_OFF = K_PIECES * 512, S_OFF = V_OFF + 16 * D;
     static constexpr int TILE = S_OFF + 128;                // and a scale
     static constexpr int TILES = tiles_of(D, HB), STAGE = TILES * TILE;
     static constexpr int RING_OFF = (Q_BYTES + 15) / 16 * 16;
-    // each head's factor and bias, then m and l of each warp
-    static constexpr int ML_BYTES = (2 + 2 * kWarps) * HEADS * 4;
+    // each query row's factor and bias, then m and l of each warp
+    static constexpr int ML_BYTES = (2 * Q_ROWS + 2 * kWarps * HEADS) * 4;
     static constexpr int FIXED = RING_OFF + ML_BYTES;
     static constexpr int FIT = ((228 * 1024 / ctas_per_sm(D, HB) - 1024) - FIXED) / (kWarps * STAGE);
     static constexpr int STAGES = FIT < 4 ? FIT : 4;
@@ -542,26 +543,30 @@ template <int D> __device__ __forceinline__ uint32_t v_chunk(int r, int c)
 // tiny scale may carry all of the probability).
 // The query is scaled by a power of two to [2^14, 2^15) at its largest and
 // rounded to halves: 11 bits, three more than a bf16 query has, whose result's
-// own rounding hides it.  For fp16 and groups of four heads or fewer half of the
-// eight columns are free, and column r + 4 takes what the rounding of column r
-// left, of the query and of the weights: the two columns' scores are added before
-// the softmax and their outputs at the end, so that neither rounding is left (the
-// error falls from 5e-4 to the 2e-4 of the result's own rounding; 3 % of the time).
+// own rounding hides it.  For fp16 what the roundings of the query and of the
+// weights leave is taken along as halves too (the error falls from 5e-4 to the 2e-4
+// of the result's own rounding).  With groups of four heads or fewer half of the
+// eight columns are free, and column r + 4 takes what column r leaves: the two
+// columns' scores are added before the softmax and their outputs at the end, at the
+// price of four shuffles a tile (3 % of the time).  With more heads it is a second
+// product into the same sums.
 template <typename T, int FMT, int D, int HB>
 __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(D, HB))
 quant_decode_kernel(const QuantDecodeArgs a)
 {
-    using SM = QuantSmem<D, HB>;
+    constexpr bool F16 = std::is_same<T, __half>::value;
+    using SM = QuantSmem<D, HB, F16>;
     constexpr int HEADS = SM::HEADS;
     constexpr int KV4 = D / 64;               // 16-byte pieces of K a lane takes of one key
     constexpr int VW = D / 32;                // 32-bit words of V a lane takes of one key
     constexpr bool QREG = HB == 1;            // query fragments in registers
-    const bool split = std::is_same<T, __half>::value && HB == 1 && a.group <= 4;
+    const bool split = F16 && HB == 1 && a.group <= 4;  // columns r + 4
+    const bool twice = F16 && !split;                  // second products
     constexpr int TILES = SM::TILES, kUnit = unit_of(D, HB);
     extern __shared__ __align__(16) uint8_t smem[];
     float *q_factor = reinterpret_cast<float *>(smem + SM::ML_OFF);
-    float *q_bias = q_factor + HEADS;
-    float *m_sh = q_bias + HEADS, *l_sh = m_sh + kWarps * HEADS;
+    float *q_bias = q_factor + SM::Q_ROWS;
+    float *m_sh = q_bias + SM::Q_ROWS, *l_sh = m_sh + kWarps * HEADS;
 
     kvc::grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -667,10 +672,11 @@ quant_decode_kernel(const QuantDecodeArgs a)
         {
             const int64_t pos = (int64_t)T_abs - 1;
             const T *q = static_cast<const T *>(a.q) + slice * a.group * D;
-            for (int r = warp; r < HEADS; r += kWarps) {
+            for (int r = warp; r < (twice ? SM::Q_ROWS : HEADS); r += kWarps) {
                 constexpr int PPL = D / 64;  // rotation pairs a lane
-                const bool rest = split && r >= 4;
-                const int qr = rest ? r - 4 : r;
+                const int first_rest = split ? 4 : HEADS;
+                const bool rest = F16 && r >= first_rest;
+                const int qr = rest ? r - first_rest : r;
                 float lo[PPL], hi[PPL], top = 0.f;
 #pragma unroll
                 for (int e = 0; e < PPL; ++e) {
@@ -719,9 +725,9 @@ quant_decode_kernel(const QuantDecodeArgs a)
             }
         }
         __syncthreads();
-        auto q_frag = [&](int hb, int step) {
+        auto q_frag = [&](int hb, int step, int rest = 0) {
             // k-step `step` = (span of 64 columns, word of the 16-byte piece)
-            return *reinterpret_cast<const uint2 *>(smem + (hb * 8 + g) * SM::Q_PITCH +
+            return *reinterpret_cast<const uint2 *>(smem + (rest + hb * 8 + g) * SM::Q_PITCH +
                                                     2 * (64 * (step >> 2) + 16 * t + 4 * (step & 3)));
         };
         uint2 qf[QREG ? HB : 1][QREG ? D / 16 : 1];
@@ -738,7 +744,7 @@ quant_decode_kernel(const QuantDecodeArgs a)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 qs[hb][e] = q_factor[hb * 8 + 2 * t + e];
-                qb[hb][e] = q_bias[hb * 8 + 2 * t + e];
+                qb[hb][e] = q_bias[hb * 8 + 2 * t + e] + (twice ? q_bias[HEADS + hb * 8 + 2 * t + e] : 0.f);
             }
 
         float o[HB][D / 16][4], m[HB][2], mo[HB][2], l[HB][2];
@@ -795,6 +801,13 @@ quant_decode_kernel(const QuantDecodeArgs a)
 #pragma unroll
                         for (int hb = 0; hb < HB; ++hb)
                             mma_f16(w & 1 ? s2[u][hb] : s[u][hb], a0, a1, a2, a3, f[hb].x, f[hb].y);
+                        if (twice) {
+#pragma unroll
+                            for (int hb = 0; hb < HB; ++hb) {
+                                const uint2 r = q_frag(hb, 4 * i + w, HEADS);
+                                mma_f16(w & 1 ? s2[u][hb] : s[u][hb], a0, a1, a2, a3, r.x, r.y);
+                            }
+                        }
                     }
                 }
             }
@@ -878,6 +891,7 @@ quant_decode_kernel(const QuantDecodeArgs a)
                 }
             }
             uint32_t b0[TILES][HB], b1[TILES][HB];
+            uint32_t r0[F16 ? TILES : 1][F16 ? HB : 1], r1[F16 ? TILES : 1][F16 ? HB : 1];  // (twice) what b0, b1 leave
 #pragma unroll
             for (int u = 0; u < TILES; ++u)
 #pragma unroll
@@ -890,10 +904,17 @@ quant_decode_kernel(const QuantDecodeArgs a)
                     for (int e = 0; e < 4; ++e)
                         w[e] = fast_exp2(y[u][hb][e]);
                     __half2 h0 = __floats2half2_rn(w[0], w[1]), h1 = __floats2half2_rn(w[2], w[3]);
-                    if (split && t >= 2) {
-                        const float2 r0 = __half22float2(h0), r1 = __half22float2(h1);
-                        h0 = __floats2half2_rn(w[0] - r0.x, w[1] - r0.y);
-                        h1 = __floats2half2_rn(w[2] - r1.x, w[3] - r1.y);
+                    if constexpr (F16) {
+                        const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
+                        const __half2 g0 = __floats2half2_rn(w[0] - f0.x, w[1] - f0.y);
+                        const __half2 g1 = __floats2half2_rn(w[2] - f1.x, w[3] - f1.y);
+                        if (twice) {
+                            r0[u][hb] = movm_trans(*reinterpret_cast<const uint32_t *>(&g0));
+                            r1[u][hb] = movm_trans(*reinterpret_cast<const uint32_t *>(&g1));
+                        } else if (t >= 2) {
+                            h0 = g0;
+                            h1 = g1;
+                        }
                     }
                     b0[u][hb] = movm_trans(*reinterpret_cast<const uint32_t *>(&h0));
                     b1[u][hb] = movm_trans(*reinterpret_cast<const uint32_t *>(&h1));
@@ -937,6 +958,13 @@ quant_decode_kernel(const QuantDecodeArgs a)
 #pragma unroll
                             for (int hb = 0; hb < HB; ++hb)
                                 mma_f16(o[hb][2 * (p * VP + w) + e], a0, a1, a2, a3, b0[u][hb], b1[u][hb]);
+                            if constexpr (F16) {
+                                if (twice) {
+#pragma unroll
+                                    for (int hb = 0; hb < HB; ++hb)
+                                        mma_f16(o[hb][2 * (p * VP + w) + e], a0, a1, a2, a3, r0[u][hb], r1[u][hb]);
+                                }
+                            }
                         }
                     }
                 }
@@ -1136,7 +1164,7 @@ int decode_grid(int batch, int kv_heads, int group, int64_t C, int D)
 
 template <typename T, int FMT, int D, int HB> kvc_status launch_decode(const QuantDecodeArgs &a, cudaStream_t stream)
 {
-    constexpr int smem = QuantSmem<D, HB>::TOTAL;
+    constexpr int smem = QuantSmem<D, HB, std::is_same<T, __half>::value>::TOTAL;
     auto kern = quant_decode_kernel<T, FMT, D, HB>;
     if (smem > 32 * 1024 &&
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)

@@ -141,8 +141,8 @@ def decode_case(K, code_type, dtype, B, H, G, D, C, ring, window, totals, rope=T
             heads = slice(h * G, (h + 1) * G)
             qq = R.rotate64(q[b, heads], torch.tensor([T - 1]), rope)[:, 0]
             k, v = (R.values(x[b, h].view(torch.uint8)[at].view(code_type), s[b, h][at]) for x, s in ((kq, ks), (vq, vs)))
-            # fp16 and up to 4 heads: query and weights as sums of two halves, 22 bits; else one half
-            step = 2.0 ** -22 if G <= 4 and dtype == F16 else 2.0 ** -11
+            # query and weights as halves, and for fp16 as sums of two
+            step = 2.0 ** -22 if dtype == F16 else 2.0 ** -11
             want, bound = R.attention(qq, k, v, torch.ones((G, n), dtype=torch.bool), factor, step, step, dtype,
                                       half_weights=vs[b, h][at])
             R.assert_within(out[b, heads, 0], want, bound, f"row {b} head {h}")
