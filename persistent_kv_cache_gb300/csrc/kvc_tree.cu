@@ -271,8 +271,9 @@ tree_commit_kernel(const CommitArgs a)
 // weights and of the result, each about as large as the others.  One of the first
 // two is taken out with a second product, whose time the tensor cores have to
 // spare: with head_dim <= 128 the query is a sum of two 16-bit numbers (two query
-// tiles fit beside the ring), with 256 the weights are (their second halves fit
-// beside the first in the score columns).
+// tiles fit beside the ring), with 256 the weights are (their second parts fit
+// beside the first in the score columns; but they are work for the softmax warps:
+// 137 us instead of 123 with 128).
 //
 // Only key tiles
 // that hold drafts, or that a window's edge may cut, are masked ("cut" tiles).  A
@@ -397,21 +398,8 @@ struct Walk {
 };
 
 // The ring holds, for a segment of n tiles, K_0, K_1, then V_j and K_{j+2} while
-// there is one, then the last V's: group g of that order, and the place of V_j.
-__device__ __forceinline__ void ring_group(int g, int n, bool &is_v, int &tile)
-{
-    const int lead = n < 2 ? n : 2, paired = n - lead;
-    if (g < lead) {
-        is_v = false;
-        tile = g;
-    } else if (g - lead < 2 * paired) {
-        is_v = ((g - lead) & 1) == 0;
-        tile = (g - lead) / 2 + (is_v ? 0 : 2);
-    } else {
-        is_v = true;
-        tile = g - lead - paired;
-    }
-}
+// there is one, then the last V's: the places of K_j and of V_j in that order.
+__device__ __forceinline__ int k_group(int j, int) { return j < 2 ? j : 2 * j - 1; }
 __device__ __forceinline__ int v_group(int j, int n)
 {
     const int lead = n < 2 ? n : 2, paired = n - lead;
@@ -581,62 +569,67 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     if (warp == 1 + kSoftmaxWarps || warp == 2 + kSoftmaxWarps) {
         // ======================= TMA producers of K and of V =======================
         // (the cache's rows are those of the kernels before tree_prep_kernel: no wait for it)
-        if (lane == 0) {
-            const bool mine_v = warp == 2 + kSoftmaxWarps;
-            const CUtensorMap *tmap = mine_v ? &tmap_v : &tmap_k;
+        // Each lane finds the place of one of the next 32 slabs: one thread alone spent 1500 clocks a slab
+        // on a page's number, its division and the latency of the table.
+        const bool mine_v = warp == 2 + kSoftmaxWarps;
+        const CUtensorMap *tmap = mine_v ? &tmap_v : &tmap_k;
+        if (lane == 0)
             kvc::tma_prefetch_desc(tmap);
-            int q = 0;  // slabs put into the ring so far, by both
-            bool ok = true;
-            uint32_t filled = 0, phase = 0;  // slots that this thread has filled, with the parity of the last time
-            while (ok && more) {
-                const int h = cur.row / a.row_tiles, nt = cur.t1 - cur.t0;
-                const int64_t end = (int64_t)cur.P + N;
-                bool again = false;
-                for (int u = 0; u < 2 * SPT * nt; ++u, ++q) {
-                    if (u == 0)
-                        again = walk.next(a, nxt);
-                    bool is_v;
-                    int tile;
-                    ring_group(u / SPT, nt, is_v, tile);
-                    if (is_v != mine_v)
-                        continue;
-                    const int slot = q % NSLAB;
-                    if (q >= NSLAB && !wait_or_abort(&empty[slot], ((q / NSLAB) - 1) & 1, abort_flag, a.status)) {
-                        ok = false;
-                        break;
-                    }
-                    const int64_t r = (int64_t)cur.lo + (cur.t0 + tile) * kBN + (u % SPT) * KR;
-                    int64_t y = -1;
-                    if (r < end) {
+        int q0 = 0;  // slabs of the segments before
+        bool ok = true;
+        uint32_t filled = 0, phase = 0;  // slots that this warp has filled, with the parity of the last time
+        while (ok && more) {
+            const int h = cur.row / a.row_tiles, nt = cur.t1 - cur.t0;
+            const uint32_t end = (uint32_t)cur.P + N, first = (uint32_t)cur.lo + cur.t0 * kBN;
+            const bool again = walk.next(a, nxt);
+            int32_t place = -1;
+            for (int u = 0; u < SPT * nt; ++u) {
+                if ((u & 31) == 0) {
+                    const uint32_t r = first + (uint32_t)(u + lane) * KR;
+                    place = -1;
+                    if (u + lane < SPT * nt && r < end) {
                         if (a.at.table) {
-                            const int64_t id = __ldg(a.at.table + (int64_t)cur.b * a.at.max_pages + r / a.at.page_size);
+                            const uint32_t page = r / (uint32_t)a.at.page_size;
+                            const int32_t id = __ldg(a.at.table + (int64_t)cur.b * a.at.max_pages + page);
                             if (id >= 0 && id < a.at.n_pool)
-                                y = (id * a.kv_heads + h) * a.at.page_size + r % a.at.page_size;
+                                place = (id * a.kv_heads + h) * a.at.page_size + (int32_t)(r - page * a.at.page_size);
                             else
                                 kvc::raise_status(a.status, KVC_DEV_INDEX_OOB);
                         } else {
-                            y = ((int64_t)cur.b * a.kv_heads + h) * a.at.rows + r;
+                            place = (int32_t)(((int64_t)cur.b * a.kv_heads + h) * a.at.rows + r);
                         }
                     }
+                }
+                const int32_t y = __shfl_sync(0xffffffffu, place, u & 31);
+                const int q = q0 + SPT * (mine_v ? v_group(u / SPT, nt) : k_group(u / SPT, nt)) + u % SPT;
+                const int slot = q % NSLAB;
+                if (q >= NSLAB)
+                    ok = wait_or_abort(&empty[slot], ((q / NSLAB) - 1) & 1, abort_flag, a.status);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    break;
+                if (lane == 0) {
                     if (y < 0) {
                         // nothing to read: the slot keeps what it holds, and its columns are masked
                         kvc::mbar_arrive(&full[slot]);
                     } else {
                         kvc::mbar_arrive_expect_tx(&full[slot], SM::SLAB);
-                        kvc::tma_load_3d(smem + SM::RING_OFF + slot * SM::SLAB, tmap, 0, (int32_t)y, 0, &full[slot]);
+                        kvc::tma_load_3d(smem + SM::RING_OFF + slot * SM::SLAB, tmap, 0, y, 0, &full[slot]);
                     }
-                    filled |= 1u << slot;
-                    phase = (phase & ~(1u << slot)) | ((uint32_t)((q / NSLAB) & 1) << slot);
                 }
-                cur = nxt;
-                more = again;
+                __syncwarp();
+                filled |= 1u << slot;
+                phase = (phase & ~(1u << slot)) | ((uint32_t)((q / NSLAB) & 1) << slot);
             }
-            if (*abort_flag)
-                // wind-down: let the loads in flight land before the CTA exits
-                for (int i = 0; i < NSLAB; ++i)
-                    if (filled >> i & 1)
-                        kvc::mbar_wait(&full[i], phase >> i & 1);
+            q0 += 2 * SPT * nt;
+            cur = nxt;
+            more = again;
         }
+        if (*abort_flag && lane == 0)
+            // wind-down: let the loads in flight land before the CTA exits
+            for (int i = 0; i < NSLAB; ++i)
+                if (filled >> i & 1)
+                    kvc::mbar_wait(&full[i], phase >> i & 1);
     } else if (warp == 3 + kSoftmaxWarps) {
         // ======================= TMA of the queries =======================
         if (lane == 0) {
