@@ -249,14 +249,15 @@ tree_commit_kernel(const CommitArgs a)
 //                     the drafts that it sees (mask, window and absences in one)
 //   TMEM columns  O [0, D) fp32 | S / P double buffer [D, D + 256)
 //   shared        Q (128 x D, 128-byte swizzled) | ring of slabs of 64 or 128 rows
-//   warp 0        issues tcgen05.mma in the order S_0, S_1, PV_0, S_2, PV_1, ...
+//   warp 0        TMA of the queries and the score products S_0, S_1, ...: S_{j+2}
+//                 once PV_j has read the weights in its place
 //   warps 1-8     softmax and output: two threads a row (= TMEM lane), each half
 //                 of the columns
 //   warps 9, 10   TMA producers of K and of V into one ring in the order of use
 //                 (K_0, K_1, V_0, K_2, ...), through the next segment's tiles
 //                 without a stop
-//   warp 11       TMA of the next segment's queries once this one's last scores
-//                 have been issued and are done
+//   warp 11       the output products PV_0, PV_1, ... (one thread that issued all
+//                 products in turn was behind the softmax at every tile)
 // so that from one segment to the next the stream of keys does not stop: while
 // the softmax warps write one segment's output, the next one's first scores are
 // on their way.  (With the queries loaded and rotated by the softmax warps
@@ -315,13 +316,13 @@ template <int D, int KR> struct TreeSmem {
     static constexpr int SLAB = KR * D * 2;
     static constexpr int SPT = kBN / KR;  // slabs of a tile of K (or V)
     static constexpr int BUDGET = 227 * 1024;
-    static constexpr int NBAR = 9;        // beside the ring's
+    static constexpr int NBAR = 10;       // beside the ring's
     static constexpr int MISC = (2 * 12 + NBAR) * 8 + 16 + 4 * kBM * 4 + 16;
     static constexpr int FIT = (BUDGET - Q_BYTES - MISC) / SLAB;
     static constexpr int NSLAB = FIT < 12 ? FIT : 12;
     static constexpr int RING_OFF = Q_BYTES;
     static constexpr int BAR_OFF = RING_OFF + NSLAB * SLAB;
-    // full[NSLAB], empty[NSLAB], s_full[2], p_full[2], o_done[2], q_full, q_empty, drain
+    // full[NSLAB], empty[NSLAB], s_full[2], p_full[2], o_done[2], q_full, q_empty, drain[2]
     static constexpr int MISC_OFF = BAR_OFF + (2 * NSLAB + NBAR) * 8;
     static constexpr int RED_OFF = (MISC_OFF + 8 + 15) / 16 * 16;  // row maximum / sum exchange
     static constexpr int BAD_OFF = RED_OFF + 4 * kBM * 4;
@@ -534,7 +535,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         }
         kvc::mbar_init(q_full, 1);
         kvc::mbar_init(q_empty, 1);
-        kvc::mbar_init(drain, 1);
+        kvc::mbar_init(&drain[0], 1);
+        kvc::mbar_init(&drain[1], 1);
         *abort_flag = 0;
         kvc::fence_mbar_init();
     }
@@ -631,102 +633,113 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                 if (filled >> i & 1)
                     kvc::mbar_wait(&full[i], phase >> i & 1);
     } else if (warp == 3 + kSoftmaxWarps) {
-        // ======================= TMA of the queries =======================
+        // ======================= output products =======================
         if (lane == 0) {
-            kvc::tma_prefetch_desc(&tmap_q);
-            kvc::grid_dep_wait();  // tree_prep_kernel's
-            int s_no = 0;
-            for (; more; ++s_no) {
-                if (s_no > 0 && !wait_or_abort(q_empty, (s_no - 1) & 1, abort_flag, a.status))
-                    break;
-                const int h = cur.row / a.row_tiles, mt = cur.row % a.row_tiles;
-                const int y = (cur.b * a.kv_heads + h) * rows + mt * kBM;
-                kvc::mbar_arrive_expect_tx(q_full, a.q_split ? 2 * SM::Q_TILE : SM::Q_TILE);
-                kvc::tma_load_3d(smem, &tmap_q, 0, y, 0, q_full);
-                if (SM::SPLIT_Q && a.q_split)
-                    kvc::tma_load_3d(smem + SM::Q_TILE, &tmap_q, 0, y + a.batch * a.q_heads * N, 0, q_full);
-                more = walk.next(a, cur);
-            }
-            if (*abort_flag && s_no > 0)
-                kvc::mbar_wait(q_full, (s_no - 1) & 1);
-        }
-    } else if (warp == 0) {
-        // ======================= MMA issuer =======================
-        if (lane == 0) {
-            int q = 0, J = 0;  // slabs and tiles taken so far
-            bool ok = true;
-            const int q_parts = SM::SPLIT_Q && a.q_split ? 2 : 1;
-            const uint64_t q_desc = kvc_tc::sw128_desc(smem_base, 16);
-            const uint64_t k_ring = kvc_tc::sw128_desc(smem_base + SM::RING_OFF, 16);
             const uint64_t v_ring = kvc_tc::sw128_desc(smem_base + SM::RING_OFF, KR * 128);
-            auto issue_s = [&](int buf, bool last) -> bool {
-                for (int hf = 0; hf < SPT; ++hf, ++q) {
-                    const int slot = q % NSLAB;
-                    if (!wait_or_abort(&full[slot], (q / NSLAB) & 1, abort_flag, a.status))
-                        return false;
-                    kvc_tc::fence_after();
-                    const uint64_t kd = k_ring + (uint64_t)(slot * (SM::SLAB / 16));
-                    const uint32_t d_s = tmem + SM::COL_S + buf * kBN + hf * KR;
-                    // (a loop over the parts, not unrolled: with the second part's products written out after
-                    // the first's, head_dim 64 came out wrong in every second tile)
-#pragma unroll 1
-                    for (int part = 0; part < q_parts; ++part) {
-                        const uint64_t qd = q_desc + (uint64_t)(part * (SM::Q_TILE / 16));
-#pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks)
-                            kvc_tc::mma_ss(d_s, qd + (uint64_t)(((ks >> 2) * (kBM * 128) + (ks & 3) * 32) / 16),
-                                           kd + (uint64_t)(((ks >> 2) * (KR * 128) + (ks & 3) * 32) / 16), IDESC_S,
-                                           part > 0 || ks > 0);
-                    }
-                    kvc_tc::commit(&empty[slot]);
-                }
-                kvc_tc::commit(&s_full[buf]);
-                if (last)
-                    kvc_tc::commit(q_empty);  // the segment's last scores: its queries have been read
-                return true;
-            };
-            for (int s_no = 0; ok && more; ++s_no) {
+            int q0 = 0, J = 0;  // slabs of the segments before, tiles so far
+            bool ok = true;
+            while (ok && more) {
                 const int nt = cur.t1 - cur.t0;
-                ok = wait_or_abort(q_full, s_no & 1, abort_flag, a.status);
-                kvc_tc::fence_after();
-                for (int j = 0; ok && j < 2 && j < nt; ++j)
-                    ok = issue_s((J + j) & 1, j == nt - 1);
                 more = walk.next(a, nxt);
-                for (int j = 0; ok && j < nt; ++j, ++J) {
+                for (int j = 0; j < nt; ++j, ++J) {
                     const int s = J & 1;
                     if (!(ok = wait_or_abort(&p_full[s], (J >> 1) & 1, abort_flag, a.status)))
                         break;
                     kvc_tc::fence_after();
-                    for (int hf = 0; hf < SPT; ++hf, ++q) {
-                        const int slot = q % NSLAB;
+                    for (int hf = 0; hf < SPT; ++hf) {
+                        const int q = q0 + SPT * v_group(j, nt) + hf, slot = q % NSLAB;
                         if (!(ok = wait_or_abort(&full[slot], (q / NSLAB) & 1, abort_flag, a.status)))
                             break;
                         kvc_tc::fence_after();
                         const uint64_t vd = v_ring + (uint64_t)(slot * (SM::SLAB / 16));
                         const uint32_t pa = tmem + SM::COL_S + s * kBN + hf * (KR / 2);
-#pragma unroll
-                        for (int k2 = 0; k2 < KR / 16; ++k2)
-                            kvc_tc::mma_ts(tmem + SM::COL_O, pa + k2 * 8, vd + (uint64_t)(k2 * (2048 / 16)), IDESC_O,
-                                           j > 0 || hf > 0 || k2 > 0);
-                        if constexpr (!SM::SPLIT_Q) {
+#pragma unroll 1
+                        for (int part = 0; part < (SM::SPLIT_Q ? 1 : 2); ++part) {
 #pragma unroll
                             for (int k2 = 0; k2 < KR / 16; ++k2)
-                                kvc_tc::mma_ts(tmem + SM::COL_O, pa + 64 + k2 * 8, vd + (uint64_t)(k2 * (2048 / 16)),
-                                               IDESC_O, 1);
+                                kvc_tc::mma_ts(tmem + SM::COL_O, pa + part * 64 + k2 * 8,
+                                               vd + (uint64_t)(k2 * (2048 / 16)), IDESC_O,
+                                               j > 0 || hf > 0 || part > 0 || k2 > 0);
                         }
                         kvc_tc::commit(&empty[slot]);
                     }
                     if (!ok)
                         break;
                     kvc_tc::commit(&o_done[s]);
-                    if (j + 2 < nt)
-                        ok = issue_s(s, j + 2 == nt - 1);
                 }
+                q0 += 2 * SPT * nt;
                 cur = nxt;
             }
             // everything issued above has completed once this arrives
-            kvc_tc::commit(drain);
-            kvc::mbar_wait(drain, 0);
+            kvc_tc::commit(&drain[1]);
+            kvc::mbar_wait(&drain[1], 0);
+        }
+    } else if (warp == 0) {
+        // ======================= queries, score products =======================
+        if (lane == 0) {
+            kvc::tma_prefetch_desc(&tmap_q);
+            int q0 = 0, J = 0;  // slabs of the segments before, tiles so far
+            bool ok = true;
+            const int q_parts = SM::SPLIT_Q && a.q_split ? 2 : 1;
+            const uint64_t q_desc = kvc_tc::sw128_desc(smem_base, 16);
+            const uint64_t k_ring = kvc_tc::sw128_desc(smem_base + SM::RING_OFF, 16);
+            kvc::grid_dep_wait();  // tree_prep_kernel's
+            for (int s_no = 0; ok && more; ++s_no) {
+                // the last segment's scores are done: the queries' place is free
+                if (s_no > 0 && !wait_or_abort(q_empty, (s_no - 1) & 1, abort_flag, a.status))
+                    break;
+                const int nt = cur.t1 - cur.t0;
+                {
+                    const int h = cur.row / a.row_tiles, mt = cur.row % a.row_tiles;
+                    const int y = (cur.b * a.kv_heads + h) * rows + mt * kBM;
+                    kvc::mbar_arrive_expect_tx(q_full, q_parts * SM::Q_TILE);
+                    kvc::tma_load_3d(smem, &tmap_q, 0, y, 0, q_full);
+                    if (q_parts > 1)
+                        kvc::tma_load_3d(smem + SM::Q_TILE, &tmap_q, 0, y + a.batch * a.q_heads * N, 0, q_full);
+                }
+                more = walk.next(a, nxt);
+                if (!(ok = wait_or_abort(q_full, s_no & 1, abort_flag, a.status))) {
+                    kvc::mbar_wait(q_full, s_no & 1);  // (let the loads land before the CTA exits)
+                    break;
+                }
+                kvc_tc::fence_after();
+                for (int j = 0; ok && j < nt; ++j, ++J) {
+                    const int buf = J & 1;
+                    // PV of the tile before last has read the weights that lie here
+                    if (J >= 2 && !(ok = wait_or_abort(&o_done[buf], ((J >> 1) - 1) & 1, abort_flag, a.status)))
+                        break;
+                    for (int hf = 0; hf < SPT; ++hf) {
+                        const int q = q0 + SPT * k_group(j, nt) + hf, slot = q % NSLAB;
+                        if (!(ok = wait_or_abort(&full[slot], (q / NSLAB) & 1, abort_flag, a.status)))
+                            break;
+                        kvc_tc::fence_after();
+                        const uint64_t kd = k_ring + (uint64_t)(slot * (SM::SLAB / 16));
+                        const uint32_t d_s = tmem + SM::COL_S + buf * kBN + hf * KR;
+                        // (a loop over the parts, not unrolled: with the second part's products written out
+                        // after the first's, head_dim 64 came out wrong in every second tile)
+#pragma unroll 1
+                        for (int part = 0; part < q_parts; ++part) {
+                            const uint64_t qd = q_desc + (uint64_t)(part * (SM::Q_TILE / 16));
+#pragma unroll
+                            for (int ks = 0; ks < D / 16; ++ks)
+                                kvc_tc::mma_ss(d_s, qd + (uint64_t)(((ks >> 2) * (kBM * 128) + (ks & 3) * 32) / 16),
+                                               kd + (uint64_t)(((ks >> 2) * (KR * 128) + (ks & 3) * 32) / 16), IDESC_S,
+                                               part > 0 || ks > 0);
+                        }
+                        kvc_tc::commit(&empty[slot]);
+                    }
+                    if (!ok)
+                        break;
+                    kvc_tc::commit(&s_full[buf]);
+                    if (j == nt - 1)
+                        kvc_tc::commit(q_empty);
+                }
+                q0 += 2 * SPT * nt;
+                cur = nxt;
+            }
+            // everything issued above has completed once this arrives
+            kvc_tc::commit(&drain[0]);
+            kvc::mbar_wait(&drain[0], 0);
         }
     } else {
         // ======================= softmax =======================
