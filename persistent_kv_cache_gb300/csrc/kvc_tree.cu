@@ -263,10 +263,10 @@ tree_commit_kernel(const CommitArgs a)
 // on their way.  (With the queries loaded and rotated by the softmax warps
 // between segments, each segment cost 22,000 clocks, as much as ten tiles.)
 //
-// A slab is one TMA box: KR = 128 rows (a whole tile of K or of V) where that is
-// 32 KB at most and, in a paged cache, pages are whole tiles; else 64 rows, so
-// that it lies inside a page.  (A box costs its issuing thread about 640 clocks
-// whatever its size: with 16 KB boxes from one thread that bound the kernel.)
+// A slab is KR = 128 rows (a whole tile of K or of V) where that is 32 KB at most,
+// else 64.  It is one TMA box, or, where a page may end inside a tile, two rows of
+// boxes of 64 rows and 64 columns.  (Slabs of 64 rows there made each product one
+// of 64 keys, which takes the tensor cores as long as one of 128.)
 //
 // Three roundings to 16 bits meet in an output: of the rotated query, of the
 // weights and of the result, each about as large as the others.  One of the first
@@ -297,7 +297,7 @@ struct TreeArgs {
     kvc_lengths len;
     int batch, q_heads, kv_heads, group, nodes;
     int row_tiles;  // ceil(group * nodes / 128)
-    int slab_rows;  // KR
+    int box_rows;   // rows of a TMA box of K or V
     int window;
     float scale_log2;
     const float *cos_t, *sin_t;
@@ -349,7 +349,7 @@ __device__ __forceinline__ int tree_tiles(const TreeArgs &a, int b, int &P, int 
     if (bad)
         return 0;
     if (a.window > 0)
-        lo = max(0, P - a.window + 1) & ~(a.slab_rows - 1);  // what a node of depth 0 sees
+        lo = max(0, P - a.window + 1) & ~(a.box_rows - 1);  // what a node of depth 0 sees
     return (int)((T - lo + kBN - 1) / kBN);
 }
 
@@ -579,6 +579,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             kvc::tma_prefetch_desc(tmap);
         int q0 = 0;  // slabs of the segments before
         bool ok = true;
+        const int boxes = KR / a.box_rows;  // of a slab's rows: 1 or 2
         uint32_t filled = 0, phase = 0;  // slots that this warp has filled, with the parity of the last time
         while (ok && more) {
             const int h = cur.row / a.row_tiles, nt = cur.t1 - cur.t0;
@@ -586,10 +587,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             const bool again = walk.next(a, nxt);
             int32_t place = -1;
             for (int u = 0; u < SPT * nt; ++u) {
-                if ((u & 31) == 0) {
-                    const uint32_t r = first + (uint32_t)(u + lane) * KR;
+                if ((u * boxes & 31) == 0) {
+                    const int w = u * boxes + lane;
+                    const uint32_t r = first + (uint32_t)w * a.box_rows;
                     place = -1;
-                    if (u + lane < SPT * nt && r < end) {
+                    if (w < SPT * nt * boxes && r < end) {
                         if (a.at.table) {
                             const uint32_t page = r / (uint32_t)a.at.page_size;
                             const int32_t id = __ldg(a.at.table + (int64_t)cur.b * a.at.max_pages + page);
@@ -602,7 +604,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                         }
                     }
                 }
-                const int32_t y = __shfl_sync(0xffffffffu, place, u & 31);
+                const int32_t y0 = __shfl_sync(0xffffffffu, place, u * boxes & 31);
+                const int32_t y1 = __shfl_sync(0xffffffffu, place, (u * boxes + 1) & 31);
                 const int q = q0 + SPT * (mine_v ? v_group(u / SPT, nt) : k_group(u / SPT, nt)) + u % SPT;
                 const int slot = q % NSLAB;
                 if (q >= NSLAB)
@@ -611,12 +614,28 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                 if (!ok)
                     break;
                 if (lane == 0) {
-                    if (y < 0) {
-                        // nothing to read: the slot keeps what it holds, and its columns are masked
-                        kvc::mbar_arrive(&full[slot]);
+                    uint8_t *to = smem + SM::RING_OFF + slot * SM::SLAB;
+                    if (boxes == 1) {
+                        if (y0 < 0) {
+                            // nothing to read: the slot keeps what it holds, and its columns are masked
+                            kvc::mbar_arrive(&full[slot]);
+                        } else {
+                            kvc::mbar_arrive_expect_tx(&full[slot], SM::SLAB);
+                            kvc::tma_load_3d(to, tmap, 0, y0, 0, &full[slot]);
+                        }
                     } else {
-                        kvc::mbar_arrive_expect_tx(&full[slot], SM::SLAB);
-                        kvc::tma_load_3d(smem + SM::RING_OFF + slot * SM::SLAB, tmap, 0, y, 0, &full[slot]);
+                        // half a slab's rows a box, of 64 columns
+                        const int n = (y0 >= 0) + (y1 >= 0);
+                        if (n == 0)
+                            kvc::mbar_arrive(&full[slot]);
+                        else
+                            kvc::mbar_arrive_expect_tx(&full[slot], n * (SM::SLAB / 2));
+                        for (int c = 0; c < D / 64; ++c) {
+                            if (y0 >= 0)
+                                kvc::tma_load_3d(to + c * (KR * 128), tmap, 0, y0, c, &full[slot]);
+                            if (y1 >= 0)
+                                kvc::tma_load_3d(to + c * (KR * 128) + KR / 2 * 128, tmap, 0, y1, c, &full[slot]);
+                        }
                     }
                 }
                 __syncwarp();
@@ -1098,11 +1117,12 @@ kvc_status launch_attn_dim(TreeArgs &a, const void *k, const void *v, cudaStream
                           a.kv_heads;
     const int64_t q_rows = (int64_t)a.batch * a.q_heads * a.nodes;
     a.q_split = SM::SPLIT_Q && a.cos_t;  // (an unrotated query is 16-bit as it is)
+    const int blocks = a.box_rows == KR ? D / 64 : 1;  // column blocks of a box of K or V
     CUtensorMap tq, tk, tv;
     if (!kvc_host::encode_3d_sw128(&tq, a.cos_t ? a.ws_q : a.q, (uint64_t)q_rows * (a.q_split ? 2 : 1), D, kBM, D / 64,
                                    tt) ||
-        !kvc_host::encode_3d_sw128(&tk, k, rows, D, KR, D / 64, tt) ||
-        !kvc_host::encode_3d_sw128(&tv, v, rows, D, KR, D / 64, tt))
+        !kvc_host::encode_3d_sw128(&tk, k, rows, D, a.box_rows, blocks, tt) ||
+        !kvc_host::encode_3d_sw128(&tv, v, rows, D, a.box_rows, blocks, tt))
         return KVC_ERR_CUDA;
     int dev = 0, optin = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -1129,13 +1149,12 @@ kvc_status launch_attn_dim(TreeArgs &a, const void *k, const void *v, cudaStream
 template <typename T>
 kvc_status launch_attn(TreeArgs &a, const void *k, const void *v, int D, cudaStream_t stream)
 {
-    const bool whole = D <= 128 && (!a.at.table || a.at.page_size % kBN == 0);
-    a.slab_rows = whole ? kBN : 64;
+    a.box_rows = D <= 128 && (!a.at.table || a.at.page_size % kBN == 0) ? kBN : 64;
     switch (D) {
     case 64:
-        return whole ? launch_attn_dim<T, 64, 128>(a, k, v, stream) : launch_attn_dim<T, 64, 64>(a, k, v, stream);
+        return launch_attn_dim<T, 64, 128>(a, k, v, stream);
     case 128:
-        return whole ? launch_attn_dim<T, 128, 128>(a, k, v, stream) : launch_attn_dim<T, 128, 64>(a, k, v, stream);
+        return launch_attn_dim<T, 128, 128>(a, k, v, stream);
     default:
         return launch_attn_dim<T, 256, 64>(a, k, v, stream);
     }
