@@ -303,7 +303,7 @@ struct TreeArgs {
     const float *cos_t, *sin_t;
     int64_t rope_max_pos;
     int grid;
-    float *ws_o, *ws_m, *ws_l;  // [2 * grid][128] (x D)
+    float *ws_o, *ws_m, *ws_l;  // [2 * grid][D / 4][128][4], [2 * grid][128]
     void *ws_q;                 // rotated queries, as q: rounded, then (q_split) what that left
     int q_split;
     uint32_t *see;              // drafts that each node sees, as mask
@@ -965,7 +965,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             if (active) {
                 const float l = l_run + red[((J & 1) * 2 + (half ^ 1)) * kBM + m];
                 const bool whole = nt == cur.n;
-                const int64_t part = (2 * (int64_t)blockIdx.x + (s_no == 0 ? 0 : 1)) * kBM + m;
+                const int64_t part = 2 * (int64_t)blockIdx.x + (s_no == 0 ? 0 : 1);
                 // a row that saw nothing holds no sum: zeros, whatever O is
                 const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
@@ -991,15 +991,16 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                             *reinterpret_cast<uint4 *>(to + c) = x;
                         }
                     } else {
-                        uint4 *to = reinterpret_cast<uint4 *>(a.ws_o + part * D + cc);
+                        // four columns of all 128 rows side by side, so that a warp's store is one run
+                        uint4 *to = reinterpret_cast<uint4 *>(a.ws_o) + (part * (D / 4) + cc / 4) * kBM + m;
 #pragma unroll
                         for (int c = 0; c < 32; c += 4)
-                            to[c / 4] = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                            to[c / 4 * kBM] = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
                     }
                 }
                 if (!whole && half == 0 && r < rows) {
-                    a.ws_m[part] = m_run;
-                    a.ws_l[part] = l;
+                    a.ws_m[part * kBM + m] = m_run;
+                    a.ws_l[part * kBM + m] = l;
                 }
             }
             kvc_tc::fence_before();
@@ -1015,14 +1016,13 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     }
 }
 
-// Joins the partial results of a query row that several CTAs worked on, a warp
-// a row: out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.  A split row begins
+// Joins the partial results of eight query rows that several CTAs worked on: out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.  A split row begins
 // in the share of exactly one CTA, which the block takes its number from.
 template <typename T, int D>
 __global__ void __launch_bounds__(256)
 tree_merge_kernel(const TreeArgs a)
 {
-    const int c0 = blockIdx.x, lane = threadIdx.x & 31, m = blockIdx.y * 8 + (threadIdx.x >> 5);
+    const int c0 = blockIdx.x, lane = threadIdx.x & 31;
     const int rows = a.group * a.nodes, line_rows = a.kv_heads * a.row_tiles;
     auto count = [&](int b) {
         int P, lo;
@@ -1043,51 +1043,75 @@ tree_merge_kernel(const TreeArgs a)
     }
     kvc::grid_dep_wait();
     // (its keys begin in another CTA's share, or in the next one's)
-    const int mt = row % a.row_tiles;
-    if (n == 0 || first < x0 || first >= x1 || mt * kBM + m >= rows)
+    const int m0 = blockIdx.y * 8, r0 = row % a.row_tiles * kBM + m0;  // of the tile, of the head's rows
+    if (n == 0 || first < x0 || first >= x1 || r0 >= rows)
         return;
     const int parts = shares.of(end - 1) - c0 + 1;
     // the row's segment is the first of its CTA, but in CTA c0 if that began before the row
     const int slot0 = x0 < first - kRowCost ? 1 : 0;
-    auto part = [&](int i) { return (2 * ((int64_t)c0 + i) + (i == 0 ? slot0 : 0)) * kBM + m; };
-    float top = -INFINITY;
+    auto part = [&](int i) { return 2 * ((int64_t)c0 + i) + (i == 0 ? slot0 : 0); };
+    // weights: a warp a row.  Columns: a row a thread's low bits, so that eight threads read a run of 128 bytes
+    __shared__ float w_sh[8][33], sum_sh[8];
+    const int warp = threadIdx.x >> 5, mine = threadIdx.x & 7, c4 = threadIdx.x >> 3;
+    constexpr int COLS = D / 4, PER = (COLS + 31) / 32;  // float4 columns, of a thread
+    auto stat = [&](int i) { return part(i) * kBM + m0 + warp; };
+    float top = -INFINITY, sum = 0.f;
     for (int i = lane; i < parts; i += 32)
-        top = fmaxf(top, a.ws_l[part(i)] == 0.f ? -INFINITY : a.ws_m[part(i)]);
+        top = fmaxf(top, a.ws_l[stat(i)] == 0.f ? -INFINITY : a.ws_m[stat(i)]);
 #pragma unroll
     for (int x = 16; x; x >>= 1)
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    float acc[D / 32], sum = 0.f;
+    float4 acc[PER];
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e)
-        acc[e] = 0.f;
+    for (int e = 0; e < PER; ++e)
+        acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i0 = 0; i0 < parts; i0 += 32) {
         // a part's weight a lane; a part that saw nothing (no sum) has none, whatever its O holds
         float w = 0.f;
         if (i0 + lane < parts) {
-            const float l = a.ws_l[part(i0 + lane)], mc = a.ws_m[part(i0 + lane)];
+            const float l = a.ws_l[stat(i0 + lane)], mc = a.ws_m[stat(i0 + lane)];
             w = l == 0.f ? 0.f : mc == top || mc == -INFINITY ? 1.f : exp2f(mc - top);
             sum += l * w;
         }
+        __syncthreads();
+        w_sh[warp][lane] = w;
+        __syncthreads();
         const int here = min(32, parts - i0);
+        if (c4 < COLS) {
 #pragma unroll 4
-        for (int i = 0; i < here; ++i) {
-            const float wi = __shfl_sync(0xffffffffu, w, i);
-            const float *o = a.ws_o + part(i0 + i) * D;
+            for (int i = 0; i < here; ++i) {
+                const float wi = w_sh[mine][i];
+                const float4 *o = reinterpret_cast<const float4 *>(a.ws_o) + (part(i0 + i) * COLS + c4) * kBM + m0 + mine;
 #pragma unroll
-            for (int e = 0; e < D / 32; ++e) {
-                const float x = o[lane + 32 * e];
-                acc[e] += wi == 0.f ? 0.f : x * wi;
+                for (int e = 0; e < PER; ++e) {
+                    const float4 x = o[e * 32 * kBM];
+                    acc[e].x += wi == 0.f ? 0.f : x.x * wi;
+                    acc[e].y += wi == 0.f ? 0.f : x.y * wi;
+                    acc[e].z += wi == 0.f ? 0.f : x.z * wi;
+                    acc[e].w += wi == 0.f ? 0.f : x.w * wi;
+                }
             }
         }
     }
 #pragma unroll
     for (int x = 16; x; x >>= 1)
         sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    const int64_t out_row = ((int64_t)b * a.kv_heads + row / a.row_tiles) * rows + (int64_t)mt * kBM + m;
+    if (lane == 0)
+        sum_sh[warp] = sum;
+    __syncthreads();
+    if (c4 >= COLS || r0 + mine >= rows)
+        return;
+    sum = sum_sh[mine];
+    const int h = row / a.row_tiles;
+    T *to = static_cast<T *>(a.out) + (((int64_t)b * a.kv_heads + h) * rows + r0 + mine) * D;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e)
-        static_cast<T *>(a.out)[out_row * D + lane + 32 * e] =
-            kvc::Elem<T>::from_f32(sum == 0.f ? 0.f : acc[e] / sum);
+    for (int e = 0; e < PER; ++e) {
+        uint2 x;
+        x.x = sum == 0.f ? 0u : kvc_tc::pack2<T>(acc[e].x * inv, acc[e].y * inv);
+        x.y = sum == 0.f ? 0u : kvc_tc::pack2<T>(acc[e].z * inv, acc[e].w * inv);
+        *reinterpret_cast<uint2 *>(to + 4 * (c4 + 32 * e)) = x;
+    }
 }
 
 template <typename... A>
