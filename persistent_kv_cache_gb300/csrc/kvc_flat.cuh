@@ -88,8 +88,8 @@ __device__ __forceinline__ void row_of(int batch, int heads, const Count &count,
 // row's first unit's position (b and base only when the share is not empty).
 // Up to 32 batch rows take one pass over their lengths.
 template <typename Count>
-__device__ __forceinline__ void share_of_cta(int batch, int heads, const Count &count, int grid, int c, int &x,
-                                             int &x_end, int &b, int &base)
+__device__ __forceinline__ Shares share_of_cta(int batch, int heads, const Count &count, int grid, int c, int &x,
+                                               int &x_end, int &b, int &base)
 {
     if (batch > 32) {
         const int U = locate(batch, heads, count, -1, b, base);
@@ -98,7 +98,7 @@ __device__ __forceinline__ void share_of_cta(int batch, int heads, const Count &
         x_end = shares.begin(c + 1);
         if (x < x_end)
             row_of(batch, heads, count, x, b, base);
-        return;
+        return shares;
     }
     const int lane = threadIdx.x & 31;
     const int n = lane < batch ? count(lane) * heads : 0;
@@ -114,6 +114,7 @@ __device__ __forceinline__ void share_of_cta(int batch, int heads, const Count &
     x_end = shares.begin(c + 1);
     b = __ffs(__ballot_sync(0xffffffffu, inc > x)) - 1;
     base = __shfl_sync(0xffffffffu, inc - n, b & 31);
+    return shares;
 }
 
 } // namespace kvc_flat

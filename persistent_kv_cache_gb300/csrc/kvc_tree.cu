@@ -307,6 +307,8 @@ struct TreeArgs {
     void *ws_q;                 // rotated queries, as q: rounded, then (q_split) what that left
     int q_split;
     uint32_t *see;              // drafts that each node sees, as mask
+    int4 *split;                // [grid] the row of which a CTA has the first keys but not the last: batch row, row,
+                                // parts (0: there is none), slot of its own part
     int32_t *status;
 };
 
@@ -362,7 +364,7 @@ __device__ __forceinline__ int line_tiles(int n) { return n > 0 ? n + kRowCost :
 // The segments of a CTA's share, one at a time: tiles [t0, t1) of the n tiles of
 // line row (b, head, row tile).
 struct Segment {
-    int b, row, P, lo, n, t0, t1;
+    int b, row, P, lo, n, t0, t1, end;  // end: of the row on the line
 };
 struct Walk {
     int x, x_end, b, base, P, lo, n;
@@ -386,6 +388,7 @@ struct Walk {
             s.lo = lo;
             s.n = n;
             s.row = (x - base) / line;
+            s.end = base + (s.row + 1) * line;
             const int p0 = (x - base) - s.row * line, p1 = min(line, p0 + (x_end - x));
             x += p1 - p0;
             // the tiles that stand for the row's cost hold no keys
@@ -546,6 +549,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     }
     const int N = a.nodes, rows = a.group * N, line_rows = a.kv_heads * a.row_tiles;
     Walk walk;
+    kvc_flat::Shares shares(0, 1);
     {
         auto count = [&](int b) {
             int P, lo;
@@ -556,7 +560,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             return line_tiles(n);
         };
         // (a CTA without a share falls through its loops)
-        kvc_flat::share_of_cta(a.batch, line_rows, count, a.grid, blockIdx.x, walk.x, walk.x_end, walk.b, walk.base);
+        shares = kvc_flat::share_of_cta(a.batch, line_rows, count, a.grid, blockIdx.x, walk.x, walk.x_end, walk.b,
+                                        walk.base);
         if (walk.x < walk.x_end)
             walk.load(a);
     }
@@ -577,14 +582,20 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         const CUtensorMap *tmap = mine_v ? &tmap_v : &tmap_k;
         if (lane == 0)
             kvc::tma_prefetch_desc(tmap);
+        if (!mine_v && lane == 0)
+            a.split[blockIdx.x] = make_int4(0, 0, 0, 0);
         int q0 = 0;  // slabs of the segments before
-        bool ok = true;
+        bool ok = true, first_segment = true;
         const int boxes = KR / a.box_rows;  // of a slab's rows: 1 or 2
         uint32_t filled = 0, phase = 0;  // slots that this warp has filled, with the parity of the last time
         while (ok && more) {
             const int h = cur.row / a.row_tiles, nt = cur.t1 - cur.t0;
             const uint32_t end = (uint32_t)cur.P + N, first = (uint32_t)cur.lo + cur.t0 * kBN;
             const bool again = walk.next(a, nxt);
+            if (!mine_v && lane == 0 && cur.t0 == 0 && nt != cur.n)
+                a.split[blockIdx.x] =
+                    make_int4(cur.b, cur.row, shares.of(cur.end - 1) - (int)blockIdx.x + 1, first_segment ? 0 : 1);
+            first_segment = false;
             int32_t place = -1;
             for (int u = 0; u < SPT * nt; ++u) {
                 if ((u * boxes & 31) == 0) {
@@ -1016,39 +1027,24 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     }
 }
 
-// Joins the partial results of eight query rows that several CTAs worked on: out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.  A split row begins
-// in the share of exactly one CTA, which the block takes its number from.
+// Joins the partial results of eight query rows that several CTAs worked on:
+// out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.  A split row's first keys are in
+// the share of exactly one CTA, which the block takes its number from and which has
+// written down which row that is.  (With each of 2416 blocks finding that out from the
+// lengths, the join of 32 x 8 rows took 4 us longer.  A join by the CTA that ends last
+// cost the rows under way as much as the launch.)
 template <typename T, int D>
 __global__ void __launch_bounds__(256)
 tree_merge_kernel(const TreeArgs a)
 {
-    const int c0 = blockIdx.x, lane = threadIdx.x & 31;
-    const int rows = a.group * a.nodes, line_rows = a.kv_heads * a.row_tiles;
-    auto count = [&](int b) {
-        int P, lo;
-        uint32_t bad;
-        return line_tiles(tree_tiles(a, b, P, lo, bad));
-    };
-    int b, base;
-    const int U = kvc_flat::locate(a.batch, line_rows, count, -1, b, base);
-    const kvc_flat::Shares shares(U, a.grid);
-    const int x0 = shares.begin(c0), x1 = shares.begin(c0 + 1);
-    int n = 0, row = 0, first = 0, end = 0;  // of the row's keys on the line
-    if (x0 < x1 && x1 < U) {
-        kvc_flat::row_of(a.batch, line_rows, count, x1, b, base);  // the row that the next CTA begins in
-        n = count(b);
-        row = (x1 - base) / n;
-        first = base + row * n + kRowCost;
-        end = base + row * n + n;
-    }
     kvc::grid_dep_wait();
-    // (its keys begin in another CTA's share, or in the next one's)
+    const int c0 = blockIdx.x, lane = threadIdx.x & 31, rows = a.group * a.nodes;
+    const int4 split = a.split[c0];
+    const int b = split.x, row = split.y, parts = split.z, slot0 = split.w;
     const int m0 = blockIdx.y * 8, r0 = row % a.row_tiles * kBM + m0;  // of the tile, of the head's rows
-    if (n == 0 || first < x0 || first >= x1 || r0 >= rows)
+    if (parts == 0 || r0 >= rows)
         return;
-    const int parts = shares.of(end - 1) - c0 + 1;
-    // the row's segment is the first of its CTA, but in CTA c0 if that began before the row
-    const int slot0 = x0 < first - kRowCost ? 1 : 0;
+    // the row's segment is the first of its CTA, but in the first CTA if that began before the row
     auto part = [&](int i) { return 2 * ((int64_t)c0 + i) + (i == 0 ? slot0 : 0); };
     // weights: a warp a row.  Columns: a row a thread's low bits, so that eight threads read a run of 128 bytes
     __shared__ float w_sh[8][33], sum_sh[8];
@@ -1228,12 +1224,13 @@ kvc_status check_rope(const float *cos_t, const float *sin_t, int64_t max_pos)
 // the workspace: two partial results of a row tile for each CTA (one an SM), the
 // rotated queries, the drafts that each node sees
 struct TreeLayout {
-    size_t q, see, total;
+    size_t split, q, see, total;
 };
 TreeLayout tree_layout(int batch, int q_heads, int nodes, int D)
 {
     TreeLayout l;
-    l.q = 2 * (size_t)kvc_host::sm_count() * kBM * (D + 2) * sizeof(float);
+    l.split = 2 * (size_t)kvc_host::sm_count() * kBM * (D + 2) * sizeof(float);
+    l.q = l.split + (size_t)kvc_host::sm_count() * sizeof(int4);
     l.see = l.q + (size_t)batch * q_heads * nodes * D * 2 * 2;
     l.total = l.see + (size_t)batch * nodes * ((nodes + 31) / 32) * 4;
     return l;
@@ -1369,6 +1366,7 @@ KVC_API kvc_status kvc_gqa_tree(void *out, const void *q, const void *k_cache, c
     const TreeLayout layout = tree_layout(batch, q_heads, nodes, head_dim);
     a.ws_q = static_cast<uint8_t *>(workspace) + layout.q;
     a.see = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(workspace) + layout.see);
+    a.split = reinterpret_cast<int4 *>(static_cast<uint8_t *>(workspace) + layout.split);
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     return dtype == KVC_BF16 ? launch_attn<__nv_bfloat16>(a, k_cache, v_cache, head_dim, stream)
                              : launch_attn<__half>(a, k_cache, v_cache, head_dim, stream);
