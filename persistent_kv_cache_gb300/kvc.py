@@ -194,6 +194,17 @@ def _stream_for(stream, t):
     return _stream(stream) if stream is not None or _raw_stream is None else _raw_stream(at)
 
 
+def _held_by(stream, *buffers):
+    """Buffers that a call on `stream` allocated on the current stream: their memory goes to
+    nobody else before `stream` is past the call."""
+    if stream is None:
+        return
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
+    for t in buffers:
+        if t is not None:
+            t.record_stream(s)
+
+
 _DTYPE_CODES = {torch.float32: KVC_F32, torch.bfloat16: KVC_BF16, torch.float16: KVC_F16}
 
 
@@ -560,6 +571,7 @@ def kvc_gqa_decode_quant(out, q, kq, vq, k_scale, v_scale, lengths, windowed, lo
     _same("out", out, q.shape, q.dtype)
     if isinstance(workspace, str):
         workspace = quant_decode_workspace(q, kq)
+        _held_by(stream, workspace)
     cs, sn, rmax = _rope(rope)
     _check("kvc_gqa_decode_quant", library().kvc_gqa_decode_quant(
         _ptr(out), _ptr(q), _ptr(kq), _ptr(vq), _ptr(k_scale), _ptr(v_scale), lengths.c(), B, Hq,
@@ -608,6 +620,7 @@ def kvc_gqa_decode_sparse(out, q, k_pool, v_pool, bounds, bound_scale, block_tab
     _same("selected", selected, (B, Hkv, selected.shape[-1]), torch.int32)
     if isinstance(workspace, str):
         workspace = sparse_workspace(q, k_pool, selected)
+        _held_by(stream, workspace)
     cs, sn, rmax = _rope(rope)
     _check("kvc_gqa_decode_sparse", library().kvc_gqa_decode_sparse(
         _ptr(out), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(bounds), _ptr(bound_scale),
@@ -630,6 +643,7 @@ def kvc_tree_mask(parents, mask=None, depth=None, status=None, stream=None):
     B, N = parents.shape
     if mask is None:
         mask, depth = tree_buffers(parents)
+        _held_by(stream, mask, depth)
     _same("parents", parents, (B, N), torch.int32)
     _same("mask", mask, (B, N, (N + 31) // 32), torch.int32)
     _same("depth", depth, (B, N), torch.int32)
@@ -685,6 +699,7 @@ def kvc_gqa_tree(out, q, k_cache, v_cache, mask, depth, lengths, block_table=Non
     _same("depth", depth, (B, N), torch.int32)
     if isinstance(workspace, str):
         workspace = tree_workspace(q, k_cache)
+        _held_by(stream, workspace)
     cs, sn, rmax = _rope(rope)
     _check("kvc_gqa_tree", library().kvc_gqa_tree(
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(mask), _ptr(depth), table, m, n, ps,

@@ -304,3 +304,45 @@ def test_two_streams_with_their_own_workspaces(K):
             K.kvc_gqa_decode_quant(o, x, *d, L, K.KVC_CONTIGUOUS, workspace=w, stream=s)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def after_a_wait(K, call, spoil):
+    """call(stream) behind a wait on a stream of its own, and at once `spoil` bytes written on the current one"""
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    call(side)
+    junk = [torch.full((spoil // 4,), float("nan"), device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    del junk
+
+
+def test_a_workspace_made_for_another_stream_stays_its_own(K):
+    B, H, G, D, C = 2, 4, 4, 128, 3000
+    kq, ks = codes(gen(3), (B, H, C, D), INT8)
+    vq, vs = codes(gen(4), (B, H, C, D), INT8)
+    d = [x.cuda() for x in (kq, vq, ks, vs)]
+    q = torch.randn((B, H * G, 1, D), generator=gen(5)).to(BF16).cuda()
+    L = lengths(K, [C, 1234], 1, C, K.KVC_CONTIGUOUS)
+    want = K.kvc_gqa_decode_quant(torch.zeros_like(q), q, *d, L, K.KVC_CONTIGUOUS)
+    got = torch.zeros_like(q)
+    size = K.quant_decode_workspace(q, d[0]).numel()
+    torch.cuda.synchronize()
+    after_a_wait(K, lambda s: K.kvc_gqa_decode_quant(got, q, *d, L, K.KVC_CONTIGUOUS, stream=s), size)
+    assert torch.equal(want, got)
+    # a tree's masks and the attention's workspace
+    N = 9
+    parents = torch.tensor([[i // 2 - 1 if i else -1 for i in range(N)]] * B, dtype=torch.int32, device="cuda")
+    k, v = (torch.randn((B, H, C, D), generator=gen(6 + i)).to(BF16).cuda() for i in range(2))
+    x = torch.randn((B, H * G, N, D), generator=gen(8)).to(BF16).cuda()
+    L = lengths(K, [C, 1234], N, C, K.KVC_CONTIGUOUS)
+    mask, depth = K.kvc_tree_mask(parents)
+    want = K.kvc_gqa_tree(torch.zeros_like(x), x, k, v, mask, depth, L)
+    got = torch.zeros_like(x)
+    size = K.tree_workspace(x, k).numel()
+    torch.cuda.synchronize()
+    after_a_wait(K, lambda s: K.kvc_gqa_tree(got, x, k, v, mask, depth, L, stream=s), size)
+    assert torch.equal(want, got)
+    made = []
+    after_a_wait(K, lambda s: made.extend(K.kvc_tree_mask(parents, stream=s)), mask.numel() * 4)
+    assert torch.equal(made[0], mask) and torch.equal(made[1], depth)

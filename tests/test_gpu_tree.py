@@ -237,6 +237,36 @@ def test_what_no_node_sees_may_be_anything(K):
         assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("page,dtype,D", [(0, BF16, 128), (64, F16, 64), (64, BF16, 128), (192, BF16, 256)])
+def test_what_only_some_nodes_see(K, page, dtype, D):
+    """NaN and infinities in the K and V of drafts, and of cache rows that the window leaves to the first nodes only: NaN for the
+    nodes that see them, the others' results as they were."""
+    N = 20
+    trees = [[-1] + [i - 1 - (i % 3 == 0) for i in range(1, N)], [-1] * 5 + [0, 1, 2, 3, 4] * 3]
+    c = Case(K, gen(D), 2, 2, 5, D, 576, N, [250, 126], page, dtype, trees=trees)
+    c.append()
+    window = 40
+    want = c.attend(window).cpu()
+    for kind, draft, value in (("v", 4, float("inf")), ("k", 7, float("nan")), ("v", 11, float("nan")), ("v", None, float("nan"))):
+        kept = c.gpu[kind].clone()
+        for b, P in enumerate(c.past):
+            x, y = c.at(b, [P - window + 4 if draft is None else P + draft])
+            c.gpu[kind][x.cuda(), :, y.cuda()] = value
+        out = torch.full_like(c.gpu["q"], 7.0)
+        K.kvc_gqa_tree(out, c.gpu["q"], c.gpu["k"], c.gpu["v"], c.mask, c.depth, c.L, block_table=c.gpu_table,
+                       local_window_size=window, rope=c.gpu_rope)
+        out = out.cpu()
+        for b in range(2):
+            for i, line in enumerate(c.lines[b]):
+                # a row at distance W - 4 from P is seen up to depth 3
+                sees = len(line) - 1 <= 3 if draft is None else draft in line
+                if sees:
+                    assert torch.isnan(out[b, :, i]).all(), (kind, draft, b, i)
+                else:
+                    assert torch.equal(out[b, :, i], want[b, :, i]), (kind, draft, b, i)
+        c.gpu[kind].copy_(kept)
+
+
 @pytest.mark.parametrize("page,dtype,D", [(0, BF16, 128), (64, F16, 64), (192, BF16, 256)])
 def test_commit(K, page, dtype, D):
     N, C = 70, 576
