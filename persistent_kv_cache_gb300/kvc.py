@@ -72,6 +72,7 @@ class Lengths:
     FIELDS = ("past_abs", "total_abs", "cache_past", "cache_total", "evict")
 
     def __init__(self, batch: int, device):
+        self.batch = batch
         self.buf = torch.empty((5, batch), dtype=torch.int32, device=device)
         self._c = KvcLengths(*[self.buf[i].data_ptr() for i in range(5)])
 
@@ -176,22 +177,41 @@ def _ptr(t):
 
 # the current stream's handle without a Stream object around it (a twentieth of the time)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream(stream):
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_get_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
-def _stream_for(stream, t):
-    """The stream of a call on t, which has to be on the current device."""
-    at = torch.cuda.current_device()
-    if t.get_device() != at:
-        raise ValueError(f"the tensors are on {t.device}, the current device is cuda:{at}")
-    return _stream(stream) if stream is not None or _raw_stream is None else _raw_stream(at)
+def _addresses(*tensors):
+    """Device addresses (None for None) of tensors that the library reads or writes as dense
+    arrays on the current device; the first one is there."""
+    if not tensors[0].is_cuda:
+        raise ValueError(f"expected a CUDA tensor, got one on {tensors[0].device}")
+    at = _get_device()
+    found = []
+    for t in tensors:
+        if t is None:
+            found.append(None)
+        elif t.get_device() == at and t.is_contiguous():
+            found.append(t.data_ptr())
+        elif t.get_device() != at:
+            raise ValueError(f"expected a CUDA tensor on the current device, cuda:{at}, "
+                             f"got one on {t.device}")
+        else:
+            _ptr(t)  # (raises)
+    return found
+
+
+def _lengths_of(lengths, batch):
+    if lengths.batch != batch:
+        raise ValueError(f"lengths: made for {lengths.batch} batch rows, the tensors have {batch}")
+    return lengths.c()
 
 
 def _held_by(stream, *buffers):
@@ -224,6 +244,17 @@ def _rope(rope):
     if cos.dtype != torch.float32 or sin.dtype != torch.float32 or cos.shape != sin.shape:
         raise ValueError("rope: cos and sin are float32 tables of the same shape [max_pos, D/2]")
     return _ptr(cos), _ptr(sin), cos.shape[0]
+
+
+def _tables(rope):
+    """cos, sin and their length of a rope argument"""
+    if rope is None:
+        return None, None, 0
+    cos, sin = rope
+    shape = cos.shape
+    if sin.shape != shape or cos.dtype is not torch.float32 or sin.dtype is not torch.float32:
+        raise ValueError("rope: cos and sin are float32 tables of the same shape [max_pos, D/2]")
+    return cos, sin, shape[0]
 
 
 def kvc_tensor_scatter(present, past, update, write_indices=None, axis=-2, mode=KVC_LINEAR,
@@ -519,9 +550,10 @@ def _quant_cache(kq, vq, k_scale, v_scale):
     """The sizes and format of a quantised cache: kq, vq [B, Hkv, C, D] codes and k_scale,
     v_scale [B, Hkv, C] float32."""
     fmt, shape = _code_format(kq), kq.shape
+    B, Hkv, C, _ = shape
     _same("vq", vq, shape, kq.dtype)
-    _same("k_scale", k_scale, shape[:3], torch.float32)
-    _same("v_scale", v_scale, shape[:3], torch.float32)
+    _same("k_scale", k_scale, (B, Hkv, C), torch.float32)
+    _same("v_scale", v_scale, (B, Hkv, C), torch.float32)
     return shape, fmt
 
 
@@ -530,14 +562,17 @@ def kvc_quant_append(kq, vq, k_scale, v_scale, new_k, new_v, lengths, windowed, 
     """Write new rows [B, Hkv, S, D] into a quantised cache (include/kvc.h): kq, vq
     [B, Hkv, C, D] int8 or float8_e4m3fn, k_scale, v_scale [B, Hkv, C] float32."""
     (B, Hkv, C, D), fmt = _quant_cache(kq, vq, k_scale, v_scale)
-    S = new_k.shape[2]
-    _same("new_k", new_k, (B, Hkv, S, D))
-    _same("new_v", new_v, (B, Hkv, S, D), new_k.dtype)
-    cs, sn, rmax = _rope(rope)
+    shape = new_k.shape
+    S = shape[2]
+    _same("new_v", new_v, shape, new_k.dtype)
+    if shape != (B, Hkv, S, D):
+        _same("new_k", new_k, (B, Hkv, S, D))
+    cos, sin, rmax = _tables(rope)
+    a, b, c, d, e, f, cs, sn, st = _addresses(kq, vq, k_scale, v_scale, new_k, new_v, cos, sin,
+                                              status)
     _check("kvc_quant_append", library().kvc_quant_append(
-        _ptr(kq), _ptr(vq), _ptr(k_scale), _ptr(v_scale), _ptr(new_k), _ptr(new_v), lengths.c(), B,
-        Hkv, S, C, D, _dtype_code(new_k), fmt, int(windowed), cs, sn, rmax, _ptr(status),
-        _stream_for(stream, kq)))
+        a, b, c, d, e, f, _lengths_of(lengths, B), B, Hkv, S, C, D, _dtype_code(new_k), fmt,
+        int(windowed), cs, sn, rmax, st, _stream(stream)))
 
 
 def kvc_dequant_rows(k_out, v_out, kq, vq, k_scale, v_scale, lengths, windowed, status=None,
@@ -545,13 +580,15 @@ def kvc_dequant_rows(k_out, v_out, kq, vq, k_scale, v_scale, lengths, windowed, 
     """The resident rows of a quantised cache, oldest first, into k_out, v_out
     [B, Hkv, rows, D] (include/kvc.h)."""
     (B, Hkv, C, D), fmt = _quant_cache(kq, vq, k_scale, v_scale)
-    R = k_out.shape[2]
-    _same("k_out", k_out, (B, Hkv, R, D))
-    _same("v_out", v_out, (B, Hkv, R, D), k_out.dtype)
+    shape = k_out.shape
+    R = shape[2]
+    _same("v_out", v_out, shape, k_out.dtype)
+    if shape != (B, Hkv, R, D):
+        _same("k_out", k_out, (B, Hkv, R, D))
+    a, b, c, d, e, f, st = _addresses(k_out, v_out, kq, vq, k_scale, v_scale, status)
     _check("kvc_dequant_rows", library().kvc_dequant_rows(
-        _ptr(k_out), _ptr(v_out), _ptr(kq), _ptr(vq), _ptr(k_scale), _ptr(v_scale), lengths.c(), B,
-        Hkv, C, R, D, _dtype_code(k_out), fmt, int(windowed), _ptr(status),
-        _stream_for(stream, kq)))
+        a, b, c, d, e, f, _lengths_of(lengths, B), B, Hkv, C, R, D, _dtype_code(k_out), fmt,
+        int(windowed), st, _stream(stream)))
 
 
 def quant_decode_workspace(q, kq):
@@ -566,18 +603,21 @@ def kvc_gqa_decode_quant(out, q, kq, vq, k_scale, v_scale, lengths, windowed, lo
     """One-token attention over a quantised cache (include/kvc.h).  workspace: "auto" allocates
     what the call needs."""
     (B, Hkv, C, D), fmt = _quant_cache(kq, vq, k_scale, v_scale)
-    Hq = q.shape[1]
-    _same("q", q, (B, Hq, 1, D))
-    _same("out", out, q.shape, q.dtype)
+    shape = q.shape
+    Hq = shape[1]
+    if shape != (B, Hq, 1, D):
+        _same("q", q, (B, Hq, 1, D))
+    _same("out", out, shape, q.dtype)
     if isinstance(workspace, str):
         workspace = quant_decode_workspace(q, kq)
         _held_by(stream, workspace)
-    cs, sn, rmax = _rope(rope)
+    cos, sin, rmax = _tables(rope)
+    a, b, c, d, e, f, cs, sn, ws, st = _addresses(out, q, kq, vq, k_scale, v_scale, cos, sin,
+                                                  workspace, status)
     _check("kvc_gqa_decode_quant", library().kvc_gqa_decode_quant(
-        _ptr(out), _ptr(q), _ptr(kq), _ptr(vq), _ptr(k_scale), _ptr(v_scale), lengths.c(), B, Hq,
-        Hkv, C, D, _dtype_code(q), fmt, int(windowed), local_window_size, scale, cs, sn, rmax,
-        _ptr(workspace), 0 if workspace is None else workspace.numel(), _ptr(status),
-        _stream_for(stream, kq)))
+        a, b, c, d, e, f, _lengths_of(lengths, B), B, Hq, Hkv, C, D, _dtype_code(q), fmt,
+        int(windowed), local_window_size, scale, cs, sn, rmax, ws,
+        0 if workspace is None else workspace.nbytes, st, _stream(stream)))
     return out
 
 
@@ -589,11 +629,12 @@ def kvc_page_bounds(bounds, bound_scale, k_pool, block_table, lengths, new_token
     B, max_pages = block_table.shape
     _same("bounds", bounds, (n_pages, Hkv, 2, D), torch.int8)
     _same("bound_scale", bound_scale, (n_pages, Hkv), torch.float32)
-    _same("block_table", block_table, (B, max_pages), torch.int32)
+    if block_table.dtype is not torch.int32:
+        _same("block_table", block_table, (B, max_pages), torch.int32)
+    a, b, c, d, st = _addresses(bounds, bound_scale, k_pool, block_table, status)
     _check("kvc_page_bounds", library().kvc_page_bounds(
-        _ptr(bounds), _ptr(bound_scale), _ptr(k_pool), _ptr(block_table), max_pages, n_pages, ps,
-        lengths.c(), B, Hkv, new_tokens, D, _dtype_code(k_pool), _ptr(status),
-        _stream_for(stream, k_pool)))
+        a, b, c, d, max_pages, n_pages, ps, _lengths_of(lengths, B), B, Hkv, new_tokens, D,
+        _dtype_code(k_pool), st, _stream(stream)))
 
 
 def sparse_workspace(q, k_pool, selected):
@@ -609,25 +650,29 @@ def kvc_gqa_decode_sparse(out, q, k_pool, v_pool, bounds, bound_scale, block_tab
                           workspace="auto", status=None, stream=None):
     """One-token attention over the pages that their bounds select (include/kvc.h); the pages
     taken go to selected, int32 [B, Hkv, n]."""
-    n_pages, Hkv, ps, D = k_pool.shape
-    B, Hq = q.shape[:2]
-    _same("q", q, (B, Hq, 1, D), k_pool.dtype)
-    _same("out", out, q.shape, q.dtype)
-    _same("v_pool", v_pool, k_pool.shape, k_pool.dtype)
+    pool = k_pool.shape
+    n_pages, Hkv, ps, D = pool
+    B, Hq, one, _ = shape = q.shape
+    n, max_pages = selected.shape[-1], block_table.shape[-1]
+    if one != 1 or shape[3] != D or q.dtype is not k_pool.dtype:
+        _same("q", q, (B, Hq, 1, D), k_pool.dtype)
+    _same("out", out, shape, q.dtype)
+    _same("v_pool", v_pool, pool, q.dtype)
     _same("bounds", bounds, (n_pages, Hkv, 2, D), torch.int8)
     _same("bound_scale", bound_scale, (n_pages, Hkv), torch.float32)
-    _same("block_table", block_table, (B, block_table.shape[-1]), torch.int32)
-    _same("selected", selected, (B, Hkv, selected.shape[-1]), torch.int32)
+    _same("block_table", block_table, (B, max_pages), torch.int32)
+    _same("selected", selected, (B, Hkv, n), torch.int32)
     if isinstance(workspace, str):
         workspace = sparse_workspace(q, k_pool, selected)
         _held_by(stream, workspace)
-    cs, sn, rmax = _rope(rope)
+    cos, sin, rmax = _tables(rope)
+    a, b, c, d, e, f, g, h, cs, sn, ws, st = _addresses(
+        out, q, k_pool, v_pool, bounds, bound_scale, block_table, selected, cos, sin, workspace,
+        status)
     _check("kvc_gqa_decode_sparse", library().kvc_gqa_decode_sparse(
-        _ptr(out), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(bounds), _ptr(bound_scale),
-        _ptr(block_table), block_table.shape[1], n_pages, ps, lengths.c(), B, Hq, Hkv, D,
-        _dtype_code(q), selected.shape[2], sink_pages, recent_pages, _ptr(selected), scale, cs, sn,
-        rmax, _ptr(workspace), 0 if workspace is None else workspace.numel(), _ptr(status),
-        _stream_for(stream, q)))
+        a, b, c, d, e, f, g, max_pages, n_pages, ps, _lengths_of(lengths, B), B, Hq, Hkv, D,
+        _dtype_code(q), n, sink_pages, recent_pages, h, scale, cs, sn, rmax, ws,
+        0 if workspace is None else workspace.nbytes, st, _stream(stream)))
     return out
 
 
@@ -644,40 +689,44 @@ def kvc_tree_mask(parents, mask=None, depth=None, status=None, stream=None):
     if mask is None:
         mask, depth = tree_buffers(parents)
         _held_by(stream, mask, depth)
-    _same("parents", parents, (B, N), torch.int32)
+    if parents.dtype is not torch.int32:
+        _same("parents", parents, (B, N), torch.int32)
     _same("mask", mask, (B, N, (N + 31) // 32), torch.int32)
     _same("depth", depth, (B, N), torch.int32)
-    _check("kvc_tree_mask", library().kvc_tree_mask(
-        _ptr(parents), B, N, _ptr(mask), _ptr(depth), _ptr(status), _stream_for(stream, parents)))
+    a, b, c, st = _addresses(parents, mask, depth, status)
+    _check("kvc_tree_mask", library().kvc_tree_mask(a, B, N, b, c, st, _stream(stream)))
     return mask, depth
 
 
 def _cache_rows(k_cache, v_cache, block_table, B):
-    """(table pointer, max_pages, pool pages, page_size, kv heads, capacity, D) of a contiguous
-    cache [B, Hkv, C, D] (no block table) or of page pools [pages, Hkv, page_size, D]."""
-    _same("v_cache", v_cache, k_cache.shape, k_cache.dtype)
-    n, Hkv, rows, D = k_cache.shape
+    """(max_pages, pool pages, page_size, kv heads, capacity, D) of a contiguous cache
+    [B, Hkv, C, D] (no block table) or of page pools [pages, Hkv, page_size, D]."""
+    n, Hkv, rows, D = shape = k_cache.shape
+    _same("v_cache", v_cache, shape, k_cache.dtype)
     if block_table is None:
-        _same("k_cache", k_cache, (B, Hkv, rows, D))
-        return None, 0, 0, 0, Hkv, rows, D
-    _same("block_table", block_table, (B, block_table.shape[-1]), torch.int32)
-    return _ptr(block_table), block_table.shape[1], n, rows, Hkv, 0, D
+        if n != B:
+            _same("k_cache", k_cache, (B, Hkv, rows, D))
+        return 0, 0, 0, Hkv, rows, D
+    max_pages = block_table.shape[-1]
+    _same("block_table", block_table, (B, max_pages), torch.int32)
+    return max_pages, n, rows, Hkv, 0, D
 
 
 def kvc_tree_append(k_cache, v_cache, new_k, new_v, depth, lengths, block_table=None, rope=None,
                     status=None, stream=None):
     """The drafted nodes' rows [B, Hkv, N, D] behind the cache, K rotated at P + depth
     (include/kvc.h)."""
-    B, _, N, _ = new_k.shape
-    table, m, n, ps, Hkv, C, D = _cache_rows(k_cache, v_cache, block_table, B)
+    B, _, N, _ = shape = new_k.shape
+    m, n, ps, Hkv, C, D = _cache_rows(k_cache, v_cache, block_table, B)
     _same("new_k", new_k, (B, Hkv, N, D), k_cache.dtype)
-    _same("new_v", new_v, (B, Hkv, N, D), k_cache.dtype)
+    _same("new_v", new_v, shape, k_cache.dtype)
     _same("depth", depth, (B, N), torch.int32)
-    cs, sn, rmax = _rope(rope)
+    cos, sin, rmax = _tables(rope)
+    a, b, c, d, e, table, cs, sn, st = _addresses(k_cache, v_cache, new_k, new_v, depth,
+                                                  block_table, cos, sin, status)
     _check("kvc_tree_append", library().kvc_tree_append(
-        _ptr(k_cache), _ptr(v_cache), _ptr(new_k), _ptr(new_v), _ptr(depth), table, m, n, ps,
-        lengths.c(), B, Hkv, N, C, D, _dtype_code(k_cache), cs, sn, rmax, _ptr(status),
-        _stream_for(stream, k_cache)))
+        a, b, c, d, e, table, m, n, ps, _lengths_of(lengths, B), B, Hkv, N, C, D,
+        _dtype_code(k_cache), cs, sn, rmax, st, _stream(stream)))
 
 
 def tree_workspace(q, k_cache):
@@ -691,21 +740,23 @@ def kvc_gqa_tree(out, q, k_cache, v_cache, mask, depth, lengths, block_table=Non
                  local_window_size=0, scale=0.0, rope=None, workspace="auto", status=None,
                  stream=None):
     """Attention of the drafted nodes' queries [B, Hq, N, D] (include/kvc.h)."""
-    B, Hq, N, _ = q.shape
-    table, m, n, ps, Hkv, C, D = _cache_rows(k_cache, v_cache, block_table, B)
-    _same("q", q, (B, Hq, N, D), k_cache.dtype)
-    _same("out", out, q.shape, q.dtype)
+    B, Hq, N, _ = shape = q.shape
+    m, n, ps, Hkv, C, D = _cache_rows(k_cache, v_cache, block_table, B)
+    if shape[3] != D or q.dtype is not k_cache.dtype:
+        _same("q", q, (B, Hq, N, D), k_cache.dtype)
+    _same("out", out, shape, q.dtype)
     _same("mask", mask, (B, N, (N + 31) // 32), torch.int32)
     _same("depth", depth, (B, N), torch.int32)
     if isinstance(workspace, str):
         workspace = tree_workspace(q, k_cache)
         _held_by(stream, workspace)
-    cs, sn, rmax = _rope(rope)
+    cos, sin, rmax = _tables(rope)
+    a, b, c, d, e, f, table, cs, sn, ws, st = _addresses(
+        out, q, k_cache, v_cache, mask, depth, block_table, cos, sin, workspace, status)
     _check("kvc_gqa_tree", library().kvc_gqa_tree(
-        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(mask), _ptr(depth), table, m, n, ps,
-        lengths.c(), B, Hq, Hkv, N, C, D, _dtype_code(q), local_window_size, scale, cs, sn, rmax,
-        _ptr(workspace), 0 if workspace is None else workspace.numel(), _ptr(status),
-        _stream_for(stream, q)))
+        a, b, c, d, e, f, table, m, n, ps, _lengths_of(lengths, B), B, Hq, Hkv, N, C, D,
+        _dtype_code(q), local_window_size, scale, cs, sn, rmax, ws,
+        0 if workspace is None else workspace.nbytes, st, _stream(stream)))
     return out
 
 
@@ -714,11 +765,13 @@ def kvc_tree_commit(k_cache, v_cache, path, accepted, lengths, seqlens_k, nodes,
     """Keep the nodes path[b, :accepted[b]] of each tree (include/kvc.h): their rows follow the
     cache, seqlens_k holds the total so far minus one."""
     B, path_len = path.shape
-    table, m, n, ps, Hkv, C, D = _cache_rows(k_cache, v_cache, block_table, B)
-    _same("path", path, (B, path_len), torch.int32)
+    m, n, ps, Hkv, C, D = _cache_rows(k_cache, v_cache, block_table, B)
+    if path.dtype is not torch.int32:
+        _same("path", path, (B, path_len), torch.int32)
     _same("accepted", accepted, (B,), torch.int32)
     _same("seqlens_k", seqlens_k, (B,), torch.int32)
+    a, b, c, d, e, table, st = _addresses(k_cache, v_cache, path, accepted, seqlens_k, block_table,
+                                          status)
     _check("kvc_tree_commit", library().kvc_tree_commit(
-        _ptr(k_cache), _ptr(v_cache), _ptr(path), _ptr(accepted), path_len, table, m, n, ps,
-        lengths.c(), _ptr(seqlens_k), B, Hkv, nodes, C, D, _dtype_code(k_cache), _ptr(status),
-        _stream_for(stream, k_cache)))
+        a, b, c, d, path_len, table, m, n, ps, _lengths_of(lengths, B), e, B, Hkv, nodes, C, D,
+        _dtype_code(k_cache), st, _stream(stream)))
