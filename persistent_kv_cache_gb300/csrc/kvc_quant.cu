@@ -143,6 +143,9 @@ struct AppendArgs {
 // fetched from the lane that holds them.  A block walks the rows of one (batch
 // row, head) with the next rows under way while it works on these; the first
 // are asked for before the lengths say where they go.
+// 2 x 64 x 2048 rows of 128 (67 MB in, 34 out, bf16 to int8): 32 us, 3.1 TB/s.  The
+// instructions bound it (69 % of the issue slots: maximum, scale, exact quotients,
+// packing); with a row a block and nothing ahead it took 46 us.
 constexpr int kAppendThreads = 256;
 template <typename T, int FMT, int LPR>
 __global__ void __launch_bounds__(kAppendThreads)
@@ -265,7 +268,9 @@ struct DequantArgs {
 };
 
 // Eight codes a thread (16 bytes out, side by side over a warp), D / 8 threads a
-// row, kRowsAhead rows under way
+// row, kRowsAhead rows under way.
+// 2 x 64 x 4096 rows of 128 (69 MB in, 134 out): 25 us, part of the writes still in
+// L2 at the end; 31 us with 16 codes a thread.
 constexpr int kRowsAhead = 4;
 constexpr int kDequantCtas = 12;
 template <typename T, int FMT>
@@ -550,6 +555,10 @@ template <int D> __device__ __forceinline__ uint32_t v_chunk(int r, int c)
 // columns' scores are added before the softmax and their outputs at the end, at the
 // price of four shuffles a tile (3 % of the time).  With more heads it is a second
 // product into the same sums.
+// 32 x 8 rows of 512 to 8192 keys, head_dim 128, int8 (295 MB): 61 us, 4.8 TB/s; a
+// ring of 8 x 8 x 4096 keys of 256, e4m3: 29 us.  HBM bounds it while every CTA runs,
+// 5.2 TB/s, but the SMs do not get equal parts of it and the last ends 15 % late; the
+// logic pipe, which the codes' conversion takes, is half full.
 template <typename T, int FMT, int D, int HB>
 __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(D, HB))
 quant_decode_kernel(const QuantDecodeArgs a)

@@ -70,6 +70,8 @@ template <typename T> __device__ __forceinline__ uint32_t pair_min(uint32_t x, u
 // A warp takes the page of one head: D / 8 lanes a row, eight columns a lane,
 // maximum and minimum of two columns at once, kAhead loads of 16 bytes under way.
 // It reads 2 D bytes a row once and no block waits for another warp.
+// 64 x 256 pages of 64 rows of 128 (268 MB): 46 us, 6.0 TB/s of reads; 117 us with a
+// block a page.
 constexpr int kBoundWarps = 8;
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kBoundWarps)
@@ -270,8 +272,10 @@ struct Sum2 {
 // The choice is that of the rest-th largest key, found 8 bits at a time below the
 // highest bit in which the keys differ (keys are close together: on their leading
 // bits a histogram is one bin, and its atomics one queue).
-// 64 rows of up to 2048 pages took 71 us with one CTA a row and a page at a time,
-// 24 us with the histograms of eight CTAs joined at every step.
+// 64 rows of up to 2048 pages: 11 to 16 us, each step a chain of its own (ids 2, bounds
+// and query 2, scores 2 to 5, n-th largest 2, compaction 2 to 3).  They took 71 us with
+// one CTA a row and a page at a time, 24 us with the histograms of eight CTAs joined at
+// every step.
 template <typename T, int D>
 __global__ void __launch_bounds__(kSelThreads, 4)
 page_select_kernel(const SelectArgs a, int run_max)
@@ -528,7 +532,8 @@ page_select_kernel(const SelectArgs a, int run_max)
 // --------------------------------------------------------------------------
 
 constexpr int kUnit = 64;           // keys of a unit of work: pages are whole units
-constexpr int kRowCost = 8;         // units (kvc_flat.cuh) that a row costs beside its keys: 53 us with 2, 49 with 6, 48 with 8
+// units (kvc_flat.cuh) that a row costs beside its keys: 51 us with 2, 50 with 4, 49 with 6, 48 with 8
+constexpr int kRowCost = 8;
 constexpr int kWarps = 4;           // that compute, 16 keys of a unit each
 constexpr int kDecodeThreads = 32 * (kWarps + 2);
 constexpr float kNone = -1e30f;     // a reference maximum before any score (finite: differences stay numbers)
@@ -630,6 +635,9 @@ template <typename T> __device__ __forceinline__ void parts_of(float x, T &hi, T
 // numbers each, at the price of a second product: of the roundings to 16 bits only
 // the result's is left.  A row that several CTAs worked on is joined by the one of
 // them that finishes last, in the order of the shares whichever that is.
+// 64 rows of 64 pages of 64 keys of 128 (134 MB): 33 us alone, of which 20 are the
+// bytes; the first bytes come 3 us after the choice of pages is done, and the joins
+// take the rest.
 template <typename T, int D, int HB>
 __global__ void __launch_bounds__(kDecodeThreads, ctas_per_sm(D))
 sparse_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
@@ -1254,7 +1262,8 @@ KVC_API kvc_status kvc_gqa_decode_sparse(void *out, const void *q, const void *k
         return KVC_ERR_UNSUPPORTED;
     if ((int64_t)batch * kv_heads > 65535)
         return KVC_ERR_SHAPE;
-    if (max_pages > kMaxPages || (int64_t)max_pages * page_size > (int64_t)INT32_MAX || (int64_t)n_select * page_size > (int64_t)INT32_MAX ||
+    if (max_pages > kMaxPages || (int64_t)max_pages * page_size > (int64_t)INT32_MAX ||
+        (int64_t)n_select * page_size > (int64_t)INT32_MAX ||
         n_pool_pages * kv_heads * (int64_t)page_size > (int64_t)INT32_MAX ||
         (int64_t)batch * kv_heads * ((int64_t)n_select * page_size / kUnit + kRowCost) > (int64_t)INT32_MAX)
         return KVC_ERR_CAPACITY;
