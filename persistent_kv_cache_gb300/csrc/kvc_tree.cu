@@ -1034,12 +1034,13 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     }
 }
 
-// Joins the partial results of eight query rows that several CTAs worked on:
+// Joins the partial results of 16 query rows that several CTAs worked on:
 // out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.  A split row's first keys are in
 // the share of exactly one CTA, which the block takes its number from and which has
-// written down which row that is.  (With each of 2416 blocks finding that out from the
+// written down which row that is.  (With each of 2400 blocks finding that out from the
 // lengths, the join of 32 x 8 rows took 4 us longer.  A join by the CTA that ends last
 // cost the rows under way as much as the launch.)
+constexpr int kMergeRows = 16;
 template <typename T, int D>
 __global__ void __launch_bounds__(256)
 tree_merge_kernel(const TreeArgs a)
@@ -1048,72 +1049,101 @@ tree_merge_kernel(const TreeArgs a)
     const int c0 = blockIdx.x, lane = threadIdx.x & 31, rows = a.group * a.nodes;
     const int4 split = a.split[c0];
     const int b = split.x, row = split.y, parts = split.z, slot0 = split.w;
-    const int m0 = blockIdx.y * 8, r0 = row % a.row_tiles * kBM + m0;  // of the tile, of the head's rows
+    const int m0 = blockIdx.y * kMergeRows, r0 = row % a.row_tiles * kBM + m0;  // of the tile, of the head's rows
     if (parts == 0 || r0 >= rows)
         return;
     // the row's segment is the first of its CTA, but in the first CTA if that began before the row
     auto part = [&](int i) { return 2 * ((int64_t)c0 + i) + (i == 0 ? slot0 : 0); };
-    // weights: a warp a row.  Columns: a row a thread's low bits, so that eight threads read a run of 128 bytes
-    __shared__ float w_sh[8][33], sum_sh[8];
-    const int warp = threadIdx.x >> 5, mine = threadIdx.x & 7, c4 = threadIdx.x >> 3;
-    constexpr int COLS = D / 4, PER = (COLS + 31) / 32;  // float4 columns, of a thread
-    auto stat = [&](int i) { return part(i) * kBM + m0 + warp; };
-    float top = -INFINITY, sum = 0.f;
-    for (int i = lane; i < parts; i += 32)
-        top = fmaxf(top, a.ws_l[stat(i)] == 0.f ? -INFINITY : a.ws_m[stat(i)]);
+    // Weights: a warp two rows.  Columns: a row a thread's low bits, so that 16 threads read a run of
+    // 256 bytes; those of the first parts are under way while the weights are found.
+    constexpr int R = kMergeRows, W = R / 8;
+    constexpr int COLS = D / 4, LANES = 256 / R, PER = COLS / LANES;  // float4 columns, of a thread
+    __shared__ float w_sh[R][33], sum_sh[R];
+    const int warp = threadIdx.x >> 5, mine = threadIdx.x % R, c4 = threadIdx.x / R;
+    constexpr int AHEAD = PER <= 2 ? 4 : 2;  // parts under way
+    float4 acc[PER], x[AHEAD][PER];
+    auto load = [&](int i) {
 #pragma unroll
-    for (int x = 16; x; x >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    float4 acc[PER];
+        for (int k = 0; k < AHEAD; ++k) {
+            const float4 *o =
+                reinterpret_cast<const float4 *>(a.ws_o) + (part(min(i + k, parts - 1)) * COLS + c4) * kBM + m0 + mine;
+#pragma unroll
+            for (int e = 0; e < PER; ++e)
+                x[k][e] = o[e * LANES * kBM];
+        }
+    };
+    load(0);
 #pragma unroll
     for (int e = 0; e < PER; ++e)
         acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float top[W], sum[W];
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+        top[k] = -INFINITY;
+        sum[k] = 0.f;
+    }
+    auto stat = [&](int i, int k) { return part(i) * kBM + m0 + W * warp + k; };
+    for (int i = lane; i < parts; i += 32)
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+            top[k] = fmaxf(top[k], a.ws_l[stat(i, k)] == 0.f ? -INFINITY : a.ws_m[stat(i, k)]);
+#pragma unroll
+    for (int d = 16; d; d >>= 1)
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+            top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], d));
     for (int i0 = 0; i0 < parts; i0 += 32) {
-        // a part's weight a lane; a part that saw nothing (no sum) has none, whatever its O holds
-        float w = 0.f;
-        if (i0 + lane < parts) {
-            const float l = a.ws_l[stat(i0 + lane)], mc = a.ws_m[stat(i0 + lane)];
-            w = l == 0.f ? 0.f : mc == top || mc == -INFINITY ? 1.f : exp2f(mc - top);
-            sum += l * w;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            // a part's weight a lane; a part that saw nothing (no sum) has none, whatever its O holds
+            float w = 0.f;
+            if (i0 + lane < parts) {
+                const float l = a.ws_l[stat(i0 + lane, k)], mc = a.ws_m[stat(i0 + lane, k)];
+                w = l == 0.f ? 0.f : mc == top[k] || mc == -INFINITY ? 1.f : exp2f(mc - top[k]);
+                sum[k] += l * w;
+            }
+            w_sh[W * warp + k][lane] = w;
         }
         __syncthreads();
-        w_sh[warp][lane] = w;
-        __syncthreads();
         const int here = min(32, parts - i0);
-        if (c4 < COLS) {
-#pragma unroll 4
-            for (int i = 0; i < here; ++i) {
-                const float wi = w_sh[mine][i];
-                const float4 *o = reinterpret_cast<const float4 *>(a.ws_o) + (part(i0 + i) * COLS + c4) * kBM + m0 + mine;
+        for (int i = 0; i < here; i += AHEAD) {
 #pragma unroll
-                for (int e = 0; e < PER; ++e) {
-                    const float4 x = o[e * 32 * kBM];
-                    acc[e].x += wi == 0.f ? 0.f : x.x * wi;
-                    acc[e].y += wi == 0.f ? 0.f : x.y * wi;
-                    acc[e].z += wi == 0.f ? 0.f : x.z * wi;
-                    acc[e].w += wi == 0.f ? 0.f : x.w * wi;
+            for (int k = 0; k < AHEAD; ++k) {
+                const float w = w_sh[mine][i + k];  // (zero past the last part)
+                if (w != 0.f) {
+#pragma unroll
+                    for (int e = 0; e < PER; ++e) {
+                        acc[e].x += x[k][e].x * w;
+                        acc[e].y += x[k][e].y * w;
+                        acc[e].z += x[k][e].z * w;
+                        acc[e].w += x[k][e].w * w;
+                    }
                 }
             }
+            if (i0 + i + AHEAD < parts)
+                load(i0 + i + AHEAD);
         }
     }
 #pragma unroll
-    for (int x = 16; x; x >>= 1)
-        sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    if (lane == 0)
-        sum_sh[warp] = sum;
+    for (int k = 0; k < W; ++k) {
+#pragma unroll
+        for (int d = 16; d; d >>= 1)
+            sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], d);
+        if (lane == 0)
+            sum_sh[W * warp + k] = sum[k];
+    }
     __syncthreads();
-    if (c4 >= COLS || r0 + mine >= rows)
+    if (r0 + mine >= rows)
         return;
-    sum = sum_sh[mine];
-    const int h = row / a.row_tiles;
-    T *to = static_cast<T *>(a.out) + (((int64_t)b * a.kv_heads + h) * rows + r0 + mine) * D;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float total = sum_sh[mine], inv = total == 0.f ? 0.f : 1.f / total;
+    T *to = static_cast<T *>(a.out) + (((int64_t)b * a.kv_heads + row / a.row_tiles) * rows + r0 + mine) * D;
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
-        uint2 x;
-        x.x = sum == 0.f ? 0u : kvc_tc::pack2<T>(acc[e].x * inv, acc[e].y * inv);
-        x.y = sum == 0.f ? 0u : kvc_tc::pack2<T>(acc[e].z * inv, acc[e].w * inv);
-        *reinterpret_cast<uint2 *>(to + 4 * (c4 + 32 * e)) = x;
+        uint2 y;
+        y.x = total == 0.f ? 0u : kvc_tc::pack2<T>(acc[e].x * inv, acc[e].y * inv);
+        y.y = total == 0.f ? 0u : kvc_tc::pack2<T>(acc[e].z * inv, acc[e].w * inv);
+        *reinterpret_cast<uint2 *>(to + 4 * (c4 + LANES * e)) = y;
     }
 }
 
@@ -1167,7 +1197,8 @@ kvc_status launch_attn_dim(TreeArgs &a, const void *k, const void *v, cudaStream
     if (launch_after(kern, dim3(a.grid), kAttnThreads, smem, stream, tq, tk, tv, a) != cudaSuccess)
         return KVC_ERR_CUDA;
     if (a.grid > 1 && launch_after(tree_merge_kernel<T, D>,
-                                   dim3(a.grid - 1, (std::min(kBM, a.group * a.nodes) + 7) / 8), 256, 0, stream,
+                                   dim3(a.grid - 1, (std::min(kBM, a.group * a.nodes) + kMergeRows - 1) / kMergeRows), 256, 0,
+                                   stream,
                                    a) != cudaSuccess)
         return KVC_ERR_CUDA;
     return kvc_host::launch_status();

@@ -183,6 +183,15 @@ def test_shares(K, B, H, page):
     c.attend(rows=range(0, H, 2))
 
 
+@pytest.mark.parametrize("rope", [True, False])
+@pytest.mark.parametrize("D,dtype,page", [(64, F16, 0), (64, BF16, 64), (128, F16, 192), (128, BF16, 0), (256, F16, 64), (256, BF16, 0)])
+def test_many_tiles_of_a_row(K, D, dtype, page, rope):
+    """rows of a few to dozens of tiles, several of them to a CTA"""
+    c = Case(K, gen(D), 6, 8, 4, D, 3840, 40, [3800, 2011, 0, 1279, 600, 3583], page, dtype, rope=rope)
+    c.append()
+    c.attend(rows=[0, 3, 7])
+
+
 def test_without_rope_and_with_a_scale(K):
     for scale in (0.3, -0.05):
         c = Case(K, gen(3), 2, 2, 3, 64, 300, 20, [250, 31], dtype=F16, rope=False)
