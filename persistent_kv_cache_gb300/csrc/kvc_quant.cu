@@ -15,6 +15,7 @@
 //   quant_merge_kernel    joins the partial results of rows that several CTAs
 //                         worked on
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include <cuda_fp8.h>
@@ -360,7 +361,7 @@ struct QuantDecodeArgs {
     const float *cos_t, *sin_t;
     int64_t rope_max_pos;
     int unit;                        // keys of a unit of work
-    int grid;                        // CTAs of the attention launch
+    int grid, row_cost;              // CTAs of the attention launch, units that a row costs beside its keys
     float *ws_o, *ws_m, *ws_l;       // [2 * grid][group] (x D)
     int32_t *status;
 };
@@ -385,9 +386,9 @@ __device__ __forceinline__ uint32_t first_slot(const QuantDecodeArgs &a, int n, 
 
 // Units of a row on the line that the CTAs share: its keys', and kRowCost that hold
 // none but stand for what a CTA spends on a row beside its keys.
-__device__ __forceinline__ int row_units(int n, int unit)
+__device__ __forceinline__ int row_units(const QuantDecodeArgs &a, int n, int unit)
 {
-    return n > 0 ? (n + unit - 1) / unit + kRowCost : 0;
+    return n > 0 ? (n + unit - 1) / unit + a.row_cost : 0;
 }
 
 __device__ __forceinline__ float fast_exp2(float x)
@@ -587,7 +588,7 @@ quant_decode_kernel(const QuantDecodeArgs a)
         const int n = visible(a, b, T, bad);
         if (bad && c == 0 && warp == 0)
             kvc::raise_status(a.status, bad);
-        return row_units(n, kUnit);
+        return row_units(a, n, kUnit);
     };
     int x, x_end, b, base;
     kvc_flat::share_of_cta(a.batch, a.kv_heads, units, a.grid, c, x, x_end, b, base);
@@ -596,11 +597,11 @@ quant_decode_kernel(const QuantDecodeArgs a)
         int T_abs;
         uint32_t bad;
         const int n = visible(a, b, T_abs, bad);
-        const int line = row_units(n, kUnit), nu = line - kRowCost;
+        const int line = row_units(a, n, kUnit), nu = line - a.row_cost;
         const int h = (x - base) / line;
         const int p0 = (x - base) - h * line, p1 = min(line, p0 + (x_end - x));
         // the units that stand for the row's cost hold no keys
-        const int u0 = max(0, p0 - kRowCost), u1 = p1 - kRowCost;
+        const int u0 = max(0, p0 - a.row_cost), u1 = p1 - a.row_cost;
         if (u1 <= u0)
             break;  // (the share ends in them)
         const int64_t slice = (int64_t)b * a.kv_heads + h;
@@ -1086,7 +1087,7 @@ quant_merge_kernel(const QuantDecodeArgs a)
     auto units = [&](int bb) {
         int T;
         uint32_t bad;
-        return row_units(visible(a, bb, T, bad), a.unit);
+        return row_units(a, visible(a, bb, T, bad), a.unit);
     };
     int b_out, base;
     const int U = kvc_flat::locate(a.batch, a.kv_heads, units, b, b_out, base);
@@ -1096,7 +1097,7 @@ quant_merge_kernel(const QuantDecodeArgs a)
     kvc::grid_dep_wait();
     if (line == 0)
         return;
-    const int c0 = shares.of(x0 + kRowCost), n = shares.of(x0 + line - 1) - c0 + 1;
+    const int c0 = shares.of(x0 + a.row_cost), n = shares.of(x0 + line - 1) - c0 + 1;
     if (n == 1)
         return;  // written by that CTA
     // the row's segment is the first of its CTA, but in CTA c0 if that began before the row
@@ -1162,13 +1163,23 @@ quant_merge_kernel(const QuantDecodeArgs a)
     }
 }
 
-// one wave of resident CTAs, or one CTA a unit where the cache has fewer
-int decode_grid(int batch, int kv_heads, int group, int64_t C, int D)
+// One wave of resident CTAs over all rows, or, where the rows are so few that this
+// leaves each too many parts: a unit takes a CTA 0.5 us, and joining 16 parts 0.4 to
+// 0.8, so that a row of t units is done soonest by about sqrt(20 t) CTAs (one row of
+// 16000 keys of 256: 23 us with 250).  Rows then begin with a CTA each and cost
+// nothing beside their keys.
+struct Grid {
+    int ctas, row_cost;
+};
+Grid decode_grid(int batch, int kv_heads, int group, int64_t C, int D)
 {
     const int hb = group > 8 ? 2 : 1, unit = unit_of(D, hb);
-    const int64_t most = (int64_t)batch * kv_heads * ((C + unit - 1) / unit + kRowCost);
-    const int64_t wave = (int64_t)kvc_host::sm_count() * ctas_per_sm(D, hb);
-    return (int)std::max<int64_t>(1, std::min<int64_t>({most, wave, kMaxParts}));
+    const int64_t rows = (int64_t)batch * kv_heads, t = (C + unit - 1) / unit;
+    const int64_t wave = std::min((int64_t)kvc_host::sm_count() * ctas_per_sm(D, hb), (int64_t)kMaxParts);
+    const int64_t few = std::min(t, (int64_t)std::ceil(std::sqrt(20.0 * (double)t)));
+    if (rows * few <= wave)
+        return {(int)std::max<int64_t>(1, rows * few), 0};
+    return {(int)std::min(rows * (t + kRowCost), wave), kRowCost};
 }
 
 template <typename T, int FMT, int D, int HB> kvc_status launch_decode(const QuantDecodeArgs &a, cudaStream_t stream)
@@ -1374,7 +1385,8 @@ KVC_API size_t kvc_gqa_decode_quant_workspace_size(int batch, int q_heads, int k
         return 0;
     if (capacity <= unit_of(head_dim, q_heads / kv_heads > 8 ? 2 : 1))
         return 0;
-    const size_t parts = 2 * (size_t)decode_grid(batch, kv_heads, q_heads / kv_heads, capacity, head_dim) * (q_heads / kv_heads);
+    const size_t parts = 2 * (size_t)decode_grid(batch, kv_heads, q_heads / kv_heads, capacity, head_dim).ctas *
+                         (q_heads / kv_heads);
     return parts * (head_dim + 2) * sizeof(float);
 }
 
@@ -1438,7 +1450,9 @@ KVC_API kvc_status kvc_gqa_decode_quant(void *out, const void *q, const void *kq
     a.sin_t = rope_sin;
     a.rope_max_pos = rope_max_pos;
     a.unit = unit_of(head_dim, a.group > 8 ? 2 : 1);
-    a.grid = decode_grid(batch, kv_heads, a.group, capacity, head_dim);
+    const Grid grid = decode_grid(batch, kv_heads, a.group, capacity, head_dim);
+    a.grid = grid.ctas;
+    a.row_cost = grid.row_cost;
     const int64_t parts = 2 * (int64_t)a.grid * a.group;
     a.ws_o = static_cast<float *>(workspace);
     a.ws_m = a.ws_o ? a.ws_o + parts * head_dim : nullptr;

@@ -16,6 +16,7 @@
 //   page_select_kernel   scores, and the choice of n pages for each row and kv head
 //   sparse_decode_kernel attention over them
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "kvc_common.cuh"
@@ -549,7 +550,7 @@ struct SparseArgs {
     float scale_log2;
     const float *cos_t, *sin_t;
     int64_t rope_max_pos;
-    int grid;
+    int grid, row_cost;             // row_cost: units that a row costs beside its keys
     float *ws_o, *ws_m, *ws_l;      // [2 * grid][group] (x D)
     int32_t *status;
 };
@@ -665,7 +666,7 @@ sparse_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
     auto units_of = [&](int b) {
         int total;
         const int n = chosen_rows(a, b, total);
-        return n > 0 ? (n + kUnit - 1) / kUnit + kRowCost : 0;
+        return n > 0 ? (n + kUnit - 1) / kUnit + a.row_cost : 0;
     };
     int x, x_end, b, base;
     kvc_flat::share_of_cta(a.batch, a.kv_heads, units_of, a.grid, c, x, x_end, b, base);
@@ -679,12 +680,12 @@ sparse_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
         if (x >= x_end)
             return false;
         sg.n = chosen_rows(a, b, sg.total);
-        sg.line = (sg.n + kUnit - 1) / kUnit + kRowCost;
+        sg.line = (sg.n + kUnit - 1) / kUnit + a.row_cost;
         sg.h = (x - base) / sg.line;
         const int p0 = (x - base) - sg.h * sg.line, p1 = min(sg.line, p0 + (x_end - x));
         // (the units that stand for the row's cost hold no keys)
-        sg.u0 = max(0, p0 - kRowCost);
-        sg.u1 = p1 - kRowCost;
+        sg.u0 = max(0, p0 - a.row_cost);
+        sg.u1 = p1 - a.row_cost;
         x += p1 - p0;
         return sg.u1 > sg.u0;
     };
@@ -971,7 +972,7 @@ sparse_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
             }
             compute_bar();
         }
-        const bool whole = sg.u0 == 0 && sg.u1 == sg.line - kRowCost;
+        const bool whole = sg.u0 == 0 && sg.u1 == sg.line - a.row_cost;
         const int64_t part = 2 * (int64_t)c + (seg == 0 ? 0 : 1);
         if (ok) {
             for (int idx = threadIdx.x; idx < a.group * D; idx += 32 * kWarps) {
@@ -1001,13 +1002,13 @@ sparse_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
             compute_bar();
             if (threadIdx.x == 0) {
                 const int mine = ok ? sg.u1 - sg.u0 : 0;
-                *joins = ok && atomicAdd(a.done + slice, mine) + mine == sg.line - kRowCost;
+                *joins = ok && atomicAdd(a.done + slice, mine) + mine == sg.line - a.row_cost;
                 __threadfence();
             }
             compute_bar();
             if (*joins) {
                 const int x0 = base + sg.h * sg.line;
-                const int c0 = shares.of(x0 + kRowCost), parts = shares.of(x0 + sg.line - 1) - c0 + 1;
+                const int c0 = shares.of(x0 + a.row_cost), parts = shares.of(x0 + sg.line - 1) - c0 + 1;
                 // the row's segment is the first of its CTA, but in CTA c0 if that began before the row
                 const int slot0 = shares.begin(c0) < x0 ? 1 : 0;
                 for (int r = warp; r < a.group; r += kWarps) {
@@ -1063,11 +1064,22 @@ sparse_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// one wave of resident CTAs, or one CTA a unit where the rows have fewer
-int decode_grid(int batch, int kv_heads, int page_size, int n_select, int D)
+// One wave of resident CTAs over all rows, or, where the rows are so few that this
+// leaves each too many parts: a unit takes a CTA 0.4 us, and joining eight parts of
+// four heads 0.9, so that a row of t units is done soonest by about sqrt(3.6 t) CTAs
+// (one row of 500 units of 8 heads: 96 us with 304).  Rows then begin with a CTA each
+// and cost nothing beside their keys.
+struct Grid {
+    int ctas, row_cost;
+};
+Grid decode_grid(int batch, int kv_heads, int group, int page_size, int n_select, int D)
 {
-    const int64_t most = (int64_t)batch * kv_heads * ((int64_t)n_select * page_size / kUnit + kRowCost);
-    return (int)std::max<int64_t>(1, std::min<int64_t>(most, (int64_t)kvc_host::sm_count() * ctas_per_sm(D)));
+    const int64_t rows = (int64_t)batch * kv_heads, t = (int64_t)n_select * page_size / kUnit;
+    const int64_t wave = (int64_t)kvc_host::sm_count() * ctas_per_sm(D);
+    const int64_t few = std::min(t, (int64_t)std::ceil(std::sqrt(3.6 * (double)t / ((group + 3) / 4))));
+    if (rows * few <= wave)
+        return {(int)std::max<int64_t>(1, rows * few), 0};
+    return {(int)std::min(rows * (t + kRowCost), wave), kRowCost};
 }
 
 // the parts of the workspace: the chosen pages, the counts, the partial results
@@ -1078,7 +1090,8 @@ SparseLayout sparse_layout(int batch, int q_heads, int kv_heads, int page_size, 
 {
     SparseLayout l;
     const size_t rows = (size_t)batch * kv_heads;
-    const size_t parts = 2 * (size_t)decode_grid(batch, kv_heads, page_size, n_select, D) * (q_heads / kv_heads);
+    const size_t parts = 2 * (size_t)decode_grid(batch, kv_heads, q_heads / kv_heads, page_size, n_select, D).ctas *
+                         (q_heads / kv_heads);
     l.done = align256(rows * n_select * 4);
     l.o = l.done + align256(rows * 4);
     l.m = l.o + parts * D * 4;
@@ -1328,7 +1341,9 @@ KVC_API kvc_status kvc_gqa_decode_sparse(void *out, const void *q, const void *k
     d.cos_t = rope_cos;
     d.sin_t = rope_sin;
     d.rope_max_pos = rope_max_pos;
-    d.grid = decode_grid(batch, kv_heads, page_size, n_select, head_dim);
+    const Grid grid = decode_grid(batch, kv_heads, a.group, page_size, n_select, head_dim);
+    d.grid = grid.ctas;
+    d.row_cost = grid.row_cost;
     d.ws_o = reinterpret_cast<float *>(ws + l.o);
     d.ws_m = reinterpret_cast<float *>(ws + l.m);
     d.ws_l = reinterpret_cast<float *>(ws + l.l);

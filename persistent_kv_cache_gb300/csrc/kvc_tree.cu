@@ -13,6 +13,7 @@
 //   tree_attn_kernel     the attention of the N drafts
 //   tree_commit_kernel   the kept line's rows to [P, P + n), the next seqlens_k
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "kvc_common.cuh"
@@ -309,7 +310,7 @@ struct TreeArgs {
     float scale_log2;
     const float *cos_t, *sin_t;
     int64_t rope_max_pos;
-    int grid;
+    int grid, row_cost;
     float *ws_o, *ws_m, *ws_l;  // [2 * grid][D / 4][128][4], [2 * grid][128]
     void *ws_q;                 // rotated queries, as q: rounded, then (q_split) what that left
     int q_split;
@@ -366,7 +367,7 @@ __device__ __forceinline__ int tree_tiles(const TreeArgs &a, int b, int &P, int 
 // that hold none but stand for what a segment costs beside them (scores of the first
 // tile, output).
 constexpr int kRowCost = 4;
-__device__ __forceinline__ int line_tiles(int n) { return n > 0 ? n + kRowCost : 0; }
+__device__ __forceinline__ int line_tiles(const TreeArgs &a, int n) { return n > 0 ? n + a.row_cost : 0; }
 
 // The segments of a CTA's share, one at a time: tiles [t0, t1) of the n tiles of
 // line row (b, head, row tile).
@@ -384,12 +385,12 @@ struct Walk {
     {
         const int rows = a.kv_heads * a.row_tiles;
         while (x < x_end) {
-            while (x >= base + line_tiles(n) * rows) {
-                base += line_tiles(n) * rows;
+            while (x >= base + line_tiles(a, n) * rows) {
+                base += line_tiles(a, n) * rows;
                 ++b;
                 load(a);
             }
-            const int line = line_tiles(n);
+            const int line = line_tiles(a, n);
             s.b = b;
             s.P = P;
             s.lo = lo;
@@ -399,8 +400,8 @@ struct Walk {
             const int p0 = (x - base) - s.row * line, p1 = min(line, p0 + (x_end - x));
             x += p1 - p0;
             // the tiles that stand for the row's cost hold no keys
-            s.t0 = max(0, p0 - kRowCost);
-            s.t1 = p1 - kRowCost;
+            s.t0 = max(0, p0 - a.row_cost);
+            s.t1 = p1 - a.row_cost;
             if (s.t1 > s.t0)
                 return true;
         }
@@ -564,7 +565,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             const int n = tree_tiles(a, b, P, lo, bad);
             if (bad && blockIdx.x == 0 && warp == 0)
                 kvc::raise_status(a.status, bad);
-            return line_tiles(n);
+            return line_tiles(a, n);
         };
         // (a CTA without a share falls through its loops)
         shares = kvc_flat::share_of_cta(a.batch, line_rows, count, a.grid, blockIdx.x, walk.x, walk.x_end, walk.b,
@@ -1396,7 +1397,15 @@ KVC_API kvc_status kvc_gqa_tree(void *out, const void *q, const void *k_cache, c
     const int64_t units = (int64_t)batch * kv_heads * a.row_tiles * ((at.rows + kBN - 1) / kBN + kRowCost);
     if (units > (int64_t)INT32_MAX || (int64_t)batch * q_heads * nodes > (int64_t)INT32_MAX / 32)
         return KVC_ERR_SHAPE;
-    a.grid = (int)std::min<int64_t>(units, kvc_host::sm_count());
+    // One CTA an SM over all rows, or, where the rows are so few that this leaves each too many parts: a
+    // tile takes a CTA 1.4 us, and joining four parts 0.8, so that a row of t tiles is done soonest by about
+    // sqrt(7 t) CTAs (one row of 126 tiles: 32 us with 126).  Rows then begin with a CTA each and cost nothing
+    // beside their keys.
+    const int64_t line_rows = (int64_t)batch * kv_heads * a.row_tiles, t = (at.rows + kBN - 1) / kBN;
+    const int64_t few = std::min(t, (int64_t)std::ceil(std::sqrt(7.0 * (double)t)));
+    const bool alone = line_rows * few <= kvc_host::sm_count();
+    a.grid = (int)(alone ? line_rows * few : std::min<int64_t>(units, kvc_host::sm_count()));
+    a.row_cost = alone ? 0 : kRowCost;
     const int64_t parts = 2 * (int64_t)kvc_host::sm_count() * kBM;
     a.ws_o = static_cast<float *>(workspace);
     a.ws_m = a.ws_o + parts * head_dim;

@@ -55,7 +55,7 @@ def test_dequant(K, L):
 def test_decode(K, L):
     f = "kvc_gqa_decode_quant"
     need = K.library().kvc_gqa_decode_quant_workspace_size(2, 8, 2, 64 * 9, 64)
-    assert need == 2 * (2 * 2 * (5 + 2)) * 4 * 66 * 4  # a CTA for each of 20 units of 128 keys and 8 that stand for rows, two slots each
+    assert need == 2 * (2 * 2 * 5) * 4 * 66 * 4  # a CTA for each of 20 units of 128 keys, two slots each
     assert K.library().kvc_gqa_decode_quant_workspace_size(2, 8, 2, 64, 64) == 0
     assert K.library().kvc_gqa_decode_quant_workspace_size(2, 8, 3, 640, 64) == 0
     a = dict(out=5 * F, q=6 * F, kq=F, vq=2 * F, ks=3 * F, vs=4 * F, len=L, B=2, Hq=8, H=2, C=64 * 9, D=64, dtype=1, fmt=0,

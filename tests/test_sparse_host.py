@@ -33,8 +33,8 @@ def test_bounds(K):
 def test_decode(K):
     f, L, lib = "kvc_gqa_decode_sparse", K.KvcLengths(F, F, F, F, F), K.library()
     need = lib.kvc_gqa_decode_sparse_workspace_size(2, 8, 2, 64, 4, 64, 1)
-    # page ids and counts in 256-byte units; four rows of 4 units and the 8 for a row, a CTA each, two slots each
-    assert need == 256 + 256 + 2 * 4 * (4 + 8) * 4 * (64 + 2) * 4
+    # page ids and counts in 256-byte units; a CTA for each of four rows' four units, two slots each
+    assert need == 256 + 256 + 2 * (4 * 4) * 4 * (64 + 2) * 4
     assert lib.kvc_gqa_decode_sparse_workspace_size(2, 8, 2, 64, 4, 96, 1) == 0
     assert lib.kvc_gqa_decode_sparse_workspace_size(2, 8, 3, 64, 4, 64, 1) == 0
     assert lib.kvc_gqa_decode_sparse_workspace_size(2, 8, 2, 63, 4, 64, 1) == 0
