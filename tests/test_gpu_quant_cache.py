@@ -1,8 +1,8 @@
 """The quantised cache: rows quantised as they are written (kvc_quant_append), read back
 (kvc_dequant_rows) and attended over (kvc_gqa_decode_quant), against the float64 forms of
 _ops_reference.py.  Codes, scales and rows read back are equal bit for bit; the attention is
-within the bound that attention() derives: the query is rounded to halves (2^-11), so are the
-weights, the codes and scales are exact."""
+within the bound that attention() derives: query and weights are halves (2^-11), for fp16 sums of
+two, the codes and scales are exact."""
 import math
 
 import pytest

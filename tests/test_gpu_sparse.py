@@ -1,7 +1,7 @@
 """Attention over selected pages: the pages' bounds (kvc_page_bounds) and the pages taken
 (kvc_gqa_decode_sparse) equal bit for bit to the header's formulas, the attention over them within
-the bound that attention() of _ops_reference.py derives (query and weights rounded to the cache's
-type), and equal to kvc_gqa_decode_paged where every page is taken."""
+the bound that attention() of _ops_reference.py derives (query and weights with the digits of two
+numbers of the cache's type)."""
 import math
 
 import pytest
@@ -291,3 +291,10 @@ def test_prompt_then_steps(K):
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_the_smallest_cache(K, D):
+    _, sel, _ = run(K, F16, 1, 1, 1, D, 64, 1, 1, 0, 1, [1])
+    assert sel.tolist() == [[[0]]]
+    run(K, BF16, 2, 1, 2, D, 64, 1, 3, 1, 1, [64, 63])

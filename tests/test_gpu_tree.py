@@ -1,6 +1,7 @@
 """A tree of drafted tokens over a cache: masks, depths, appended and kept rows equal bit for bit to
 the header's statement, the attention (kvc_gqa_tree) within the bound that attention() of
-_ops_reference.py derives (query and weights rounded to the cache's type)."""
+_ops_reference.py derives (of query and weights one rounded to the cache's type, the other a sum of
+two numbers of it)."""
 import pytest
 import torch
 
@@ -190,6 +191,15 @@ def test_many_tiles_of_a_row(K, D, dtype, page, rope):
     c = Case(K, gen(D), 6, 8, 4, D, 3840, 40, [3800, 2011, 0, 1279, 600, 3583], page, dtype, rope=rope)
     c.append()
     c.attend(rows=[0, 3, 7])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("C,N,past", [(1, 1, [0, 1]), (3, 2, [1, 0]), (40, 7, [33, 5]), (129, 1, [128, 127])])
+def test_the_smallest_caches(K, D, C, N, past):
+    c = Case(K, gen(C), 2, 1, 2, D, C, N, past, 0, F16)
+    c.append()
+    c.attend()
+    c.attend(2)
 
 
 def test_without_rope_and_with_a_scale(K):
