@@ -287,6 +287,7 @@ page_select_kernel(const SelectArgs a, int run_max)
     __shared__ int warp_sum[kSelThreads / 32];
     __shared__ uint32_t hist[256];
     __shared__ uint32_t pick[3];
+    __shared__ int order[kSelThreads];
     __shared__ float top_sh[kSelThreads / 32];
     __shared__ uint32_t edge_sh[2][kSelThreads / 32];
     int32_t *ids = reinterpret_cast<int32_t *>(keys + a.max_pages);
@@ -511,16 +512,26 @@ page_select_kernel(const SelectArgs a, int run_max)
         if (choose)
             block_scan(tied, warp_sum, tied_before);
         block_scan(sure + max(0, min(tied, ties - tied_before)), warp_sum, before);
+        auto put = [&](int i, int j) {
+            const int32_t id = __ldg(table + j);
+            sel[i] = j;
+            // an id outside the pool stays outside the one-head pool
+            sub[i] = id < 0 || id >= a.n_pool ? -1 : (int32_t)((int64_t)id * a.kv_heads + h);
+        };
+        // (the first of them by a thread each: their ids come in at once)
         for (int j = j0; j < j1; ++j) {
             const int k = rank_of(j);
             if (k == 2 || (k == 1 && tied_before++ < ties)) {
-                const int32_t id = __ldg(table + j);
-                sel[before] = j;
-                // an id outside the pool stays outside the one-head pool
-                sub[before] = id < 0 || id >= a.n_pool ? -1 : (int32_t)((int64_t)id * a.kv_heads + h);
+                if (before < kSelThreads)
+                    order[before] = j;
+                else
+                    put(before, j);
                 ++before;
             }
         }
+        __syncthreads();
+        if (tid < take)
+            put(tid, order[tid]);
     }
     for (int i = take + tid; i < a.n_select; i += kSelThreads) {
         sel[i] = -1;
