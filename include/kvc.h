@@ -718,8 +718,9 @@ kvc_status kvc_dequant_rows(void *k_out, void *v_out, const void *kq_cache, cons
  * kvc_gqa_decode_quant -- kvc_gqa_decode (contiguous) or kvc_gqa_decode_ring
  * (ring) over a quantised cache, without a 16-bit copy of it: the codes go to
  * the tensor cores as halves (exactly) and the rows' scales enter in float32.
- * Masks, lengths, rope and errors as those calls; a NaN scale of a visible row
- * makes the output NaN.  Rejected batch rows keep their output.
+ * Masks, lengths, rope and errors as those calls: row r of the L rows of a
+ * contiguous cache is position T - L + r, for any T >= L (a windowed cache's
+ * lengths too).  A NaN scale of a visible row makes the output NaN.  Rejected batch rows keep their output.
  * out, q     device [batch, q_heads, 1, head_dim], KVC_BF16 or KVC_F16.
  * head_dim 64, 128 or 256, q_heads / kv_heads <= 16 (KVC_ERR_UNSUPPORTED).
  * workspace  device, kvc_gqa_decode_quant_workspace_size(...) bytes on the

@@ -366,10 +366,10 @@ struct QuantDecodeArgs {
     int32_t *status;
 };
 
-// the visible keys of batch row b, at absolute length T
-__device__ __forceinline__ int visible(const QuantDecodeArgs &a, int b, int &T, uint32_t &bad)
+// the visible keys of batch row b, at absolute length T with L rows resident
+__device__ __forceinline__ int visible(const QuantDecodeArgs &a, int b, int &T, int &L, uint32_t &bad)
 {
-    const int L = a.len.cache_total[b];
+    L = a.len.cache_total[b];
     T = a.len.total_abs[b];
     bad = L < 0 ? 0u
           : L > a.C || T < L ? (uint32_t)KVC_DEV_CAPACITY
@@ -378,10 +378,13 @@ __device__ __forceinline__ int visible(const QuantDecodeArgs &a, int b, int &T, 
         return 0;
     return a.window > 0 ? min(L, a.window) : L;
 }
-// the slot of the first of them (they wrap at C): T - n, in a ring modulo C
-__device__ __forceinline__ uint32_t first_slot(const QuantDecodeArgs &a, int n, int T)
+// The slot of the first of them (they wrap at C).  Position p of a ring lies in slot
+// p mod C; row r of a contiguous cache holds position T - L + r, and T may be more
+// than L, or than C (a window or a compaction has moved the rows down), so the last
+// n rows start at L - n, not at T - n.
+__device__ __forceinline__ uint32_t first_slot(const QuantDecodeArgs &a, int n, int T, int L)
 {
-    return a.ring ? (uint32_t)(T - n) % (uint32_t)a.C : (uint32_t)(T - n);
+    return a.ring ? (uint32_t)(T - n) % (uint32_t)a.C : (uint32_t)(L - n);
 }
 
 // Units of a row on the line that the CTAs share: its keys', and kRowCost that hold
@@ -583,9 +586,9 @@ quant_decode_kernel(const QuantDecodeArgs a)
     const int g = lane >> 2, t = lane & 3;
     const int c = blockIdx.x;
     auto units = [&](int b) {
-        int T;
+        int T, L;
         uint32_t bad;
-        const int n = visible(a, b, T, bad);
+        const int n = visible(a, b, T, L, bad);
         if (bad && c == 0 && warp == 0)
             kvc::raise_status(a.status, bad);
         return row_units(a, n, kUnit);
@@ -594,9 +597,9 @@ quant_decode_kernel(const QuantDecodeArgs a)
     kvc_flat::share_of_cta(a.batch, a.kv_heads, units, a.grid, c, x, x_end, b, base);
 
     for (int seg = 0; x < x_end; ++seg) {
-        int T_abs;
+        int T_abs, L;
         uint32_t bad;
-        const int n = visible(a, b, T_abs, bad);
+        const int n = visible(a, b, T_abs, L, bad);
         const int line = row_units(a, n, kUnit), nu = line - a.row_cost;
         const int h = (x - base) / line;
         const int p0 = (x - base) - h * line, p1 = min(line, p0 + (x_end - x));
@@ -608,7 +611,7 @@ quant_decode_kernel(const QuantDecodeArgs a)
 
         const uint8_t *kb = a.kq + slice * a.C * D + 16 * t, *vb = a.vq + slice * a.C * D + 16 * (lane % (D / 16));
         const float *ksb = a.ks + slice * a.C, *vsb = a.vs + slice * a.C;
-        const uint32_t cap = (uint32_t)a.C, start = first_slot(a, n, T_abs);
+        const uint32_t cap = (uint32_t)a.C, start = first_slot(a, n, T_abs, L);
         // 16 keys whose rows follow one another: one address each for the keys, the values and the
         // scales, and constant steps.  Else (the last keys, or a ring's end among them) each row has its
         // own, a key past the last being the last again: its score is masked, and what is loaded is
@@ -1061,7 +1064,7 @@ quant_decode_kernel(const QuantDecodeArgs a)
             base = x;
             do {
                 ++b;
-            } while (visible(a, b, T_abs, bad) == 0);
+            } while (visible(a, b, T_abs, L, bad) == 0);
         }
     }
 }
@@ -1085,9 +1088,9 @@ quant_merge_kernel(const QuantDecodeArgs a)
     const int b = slice / a.kv_heads, h = slice % a.kv_heads;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     auto units = [&](int bb) {
-        int T;
+        int T, L;
         uint32_t bad;
-        return row_units(a, visible(a, bb, T, bad), a.unit);
+        return row_units(a, visible(a, bb, T, L, bad), a.unit);
     };
     int b_out, base;
     const int U = kvc_flat::locate(a.batch, a.kv_heads, units, b, b_out, base);
