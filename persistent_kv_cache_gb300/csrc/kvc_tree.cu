@@ -975,14 +975,18 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
 
             // ---- output rows ----
             // (the next segment's first PV waits for its p_full, which every warp gives after this)
+            // The sums change hands where the last tile's maxima did: its PV is done, so every warp has read
+            // those.  The next segment's first tile writes the other pair, and its barrier lies between these
+            // reads and the next use of this one.
+            const int sums = ((J - 1) & 1) * 2;
             ok = ok && wait_or_abort(&o_done[(J - 1) & 1], ((J - 1) >> 1) & 1, abort_flag, a.status);
             kvc_tc::fence_after();
             if (active)
-                red[((J & 1) * 2 + half) * kBM + m] = l_run;
+                red[(sums + half) * kBM + m] = l_run;
             if (kvc_tc::named_bar_any(all_bar, 32 * kSoftmaxWarps, !ok))
                 break;
             if (active) {
-                const float l = l_run + red[((J & 1) * 2 + (half ^ 1)) * kBM + m];
+                const float l = l_run + red[(sums + (half ^ 1)) * kBM + m];
                 const bool whole = nt == cur.n;
                 const int64_t part = 2 * (int64_t)blockIdx.x + (s_no == 0 ? 0 : 1);
                 // a row that saw nothing holds no sum: zeros, whatever O is
