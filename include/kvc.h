@@ -851,6 +851,9 @@ kvc_status kvc_tree_append(void *k_cache, void *v_cache, const void *new_k, cons
 /*
  * kvc_gqa_tree -- the attention of the nodes after kvc_tree_append: queries
  * rotated at P + depth_i; an absent node, or one that sees nothing, gives zeros.
+ * A NaN or an infinity in a column of a V row that a node sees makes that column
+ * of its output NaN, whatever the row's weight; a NaN in a K row that it sees
+ * makes all of them NaN.  What it does not see may hold anything.
  * A batch row that kvc_seq_lengths rejected, or that kvc_tree_append would
  * refuse, keeps its output; a page id outside the pool among the rows read sets
  * KVC_DEV_INDEX_OOB (that row's output is then undefined).

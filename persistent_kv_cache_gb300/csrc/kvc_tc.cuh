@@ -128,6 +128,9 @@ __device__ __forceinline__ float fast_exp2(float x)
     return y;
 }
 
+// x, and NaN for an infinity
+__device__ __forceinline__ float finite_or_nan(float x) { return fmaf(x, 0.f, x); }
+
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");

@@ -280,10 +280,12 @@ tree_commit_kernel(const CommitArgs a)
 // made head_dim 128 slower that way: 137 us instead of 123).
 //
 // Only key tiles that hold drafts, or that a window's edge may cut, are masked
-// ("cut" tiles).  A row of V that not every query row sees may hold anything: 0 x NaN
-// would reach the rows that do not see it.  So in the cut tiles the softmax warps
-// look through V in shared memory, put zeros in the place of NaN and infinity, and
-// make the rows that do see such a value NaN.
+// ("cut" tiles).  A NaN or an infinity in a column of V makes that column of the output
+// NaN for the rows that see it, and for no other.  In the other tiles the products do
+// that by themselves (every row sees every key, and what comes out infinite is made
+// NaN).  In the cut tiles 0 x NaN would reach the rows that do not see it: there the
+// softmax warps look through V in shared memory, write down for each row the columns
+// of such values that it sees, and put zeros in their place.
 //
 // 32 nodes of 32 heads over 32 x 8 cache rows of up to 8160 keys (581 MB, bf16,
 // head_dim 128): 97 us for this kernel, 6.0 TB/s, 115 us for the call.  Memory bounds
@@ -549,6 +551,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         kvc::mbar_init(&drain[0], 1);
         kvc::mbar_init(&drain[1], 1);
         *abort_flag = 0;
+        for (int i = 0; i < 4; ++i)
+            reinterpret_cast<uint32_t *>(smem + SM::BAD_OFF)[i] = 0;
         kvc::fence_mbar_init();
     }
     if (warp == 0) {
@@ -824,6 +828,18 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             d_next = more ? row_depth(nxt) : -1;
             // cache rows from r_lo on are visible
             const int r_lo = a.window > 0 ? max(0, P + d - a.window + 1) : 0;
+            // those among the keys [k0, k0 + 32), a bit each
+            auto cache_keys = [&](int k0) {
+                uint32_t bits = 0;
+                if (d >= 0 && k0 < P && k0 + 32 > r_lo) {
+                    bits = k0 < r_lo ? ~0u << (r_lo - k0) : ~0u;
+                    if (k0 + 32 > P)
+                        bits &= ~0u >> (k0 + 32 - P);
+                }
+                return bits;
+            };
+            // this half's output columns in which the row has seen a NaN or an infinity, in the cut tiles
+            uint32_t nan_cols[D / 64] = {};
             float m_run = -INFINITY, l_run = 0.f;
             for (int j = 0; j < nt; ++j, ++J) {
                 const int s = J & 1;
@@ -835,42 +851,80 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                     const int sh = (c0 - P) & 31;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int k0 = c0 + 32 * e;  // key row of bit 0
-                        uint32_t bits = 0;
-                        if (d >= 0 && k0 < P && k0 + 32 > r_lo) {
-                            // cache rows [r_lo, P)
-                            bits = k0 < r_lo ? ~0u << (r_lo - k0) : ~0u;
-                            if (k0 + 32 > P)
-                                bits &= ~0u >> (k0 + 32 - P);
-                        }
-                        see[e] = bits | __funnelshift_r(w_next[e], w_next[e + 1], sh);
+                        see[e] = cache_keys(c0 + 32 * e) | __funnelshift_r(w_next[e], w_next[e + 1], sh);
                     }
                 }
                 load_words(j + 1);
                 ok = ok && wait_or_abort(&s_full[s], (J >> 1) & 1, abort_flag, a.status);
                 kvc_tc::fence_after();
-                uint64_t bad[2] = {0, 0};  // V rows of the tile in which this thread found one not finite
-                if (cut && ok) {
+                if (cut) {
+                    // V rows with a NaN or an infinity in them, a bit each in bad_sh (zero before)
+                    bool found = false;
 #pragma unroll
                     for (int hf = 0; hf < SPT; ++hf) {
                         const int qi = q0 + SPT * v_group(j, nt) + hf;
-                        if (!(ok = wait_or_abort(&full[qi % NSLAB], (qi / NSLAB) & 1, abort_flag, a.status)))
+                        ok = ok && wait_or_abort(&full[qi % NSLAB], (qi / NSLAB) & 1, abort_flag, a.status);
+                        if (!ok)
                             break;
-                        uint4 *v = reinterpret_cast<uint4 *>(smem + SM::RING_OFF + (qi % NSLAB) * SM::SLAB);
+                        const uint4 *v = reinterpret_cast<const uint4 *>(smem + SM::RING_OFF + (qi % NSLAB) * SM::SLAB);
 #pragma unroll
                         for (int e = 0; e < SM::SLAB / 16 / 256; ++e) {
-                            const int at = tid + 256 * e;
-                            const uint4 x = v[at];
-                            const uint4 nf = make_uint4(not_finite<T>(x.x), not_finite<T>(x.y), not_finite<T>(x.z),
-                                                        not_finite<T>(x.w));
-                            if (nf.x | nf.y | nf.z | nf.w) {
-                                v[at] = make_uint4(x.x & ~nf.x, x.y & ~nf.y, x.z & ~nf.z, x.w & ~nf.w);
-                                const int vr = hf * KR + ((at >> 3) & (KR - 1));
-                                bad[vr >> 6] |= 1ull << (vr & 63);
+                            const uint4 x = v[tid + 256 * e];
+                            if (not_finite<T>(x.x) | not_finite<T>(x.y) | not_finite<T>(x.z) | not_finite<T>(x.w)) {
+                                const int vr = hf * KR + (((tid + 256 * e) >> 3) & (KR - 1));
+                                atomicOr(&bad_sh[vr >> 5], 1u << (vr & 31));
+                                found = true;
                             }
                         }
                     }
-                    kvc::fence_proxy_async_smem();
+                    if (kvc_tc::named_bar_any(all_bar, 32 * kSoftmaxWarps, found)) {
+                        // what this row sees of them is written down by column, then they are zeros for all
+#pragma unroll 1
+                        for (int e = 0; e < 4 && d >= 0; ++e) {
+                            const int k0 = t_lo + 32 * e, w0 = (k0 - P) >> 5;
+                            auto word = [&](int w) { return w >= 0 && w < words ? __ldg(see_words + w) : 0u; };
+                            uint32_t left = bad_sh[e] & (cache_keys(k0) | __funnelshift_r(word(w0), word(w0 + 1), (k0 - P) & 31));
+                            while (left) {
+                                const int vr = 32 * e + __ffs(left) - 1, in = vr & (KR - 1);
+                                left &= left - 1;
+                                const uint8_t *slab =
+                                    smem + SM::RING_OFF + (q0 + SPT * v_group(j, nt) + vr / KR) % NSLAB * SM::SLAB;
+#pragma unroll 1
+                                for (int w = 0; w < D / 64; ++w) {
+                                    uint32_t cols = 0;
+#pragma unroll
+                                    for (int c = 0; c < 4; ++c) {
+                                        const int ch = half * (D / 16) + 4 * w + c;  // 16 bytes of the row
+                                        const uint4 x = *reinterpret_cast<const uint4 *>(
+                                            slab + (ch >> 3) * (KR * 128) + in * 128 + ((ch & 7) ^ (in & 7)) * 16);
+                                        const uint32_t nf[4] = {not_finite<T>(x.x), not_finite<T>(x.y), not_finite<T>(x.z),
+                                                                not_finite<T>(x.w)};
+#pragma unroll
+                                        for (int i = 0; i < 4; ++i)
+                                            cols |= ((nf[i] & 1u) | (nf[i] >> 30 & 2u)) << (8 * c + 2 * i);
+                                    }
+                                    nan_cols[w] |= cols;
+                                }
+                            }
+                        }
+                        kvc_tc::named_bar_sync(all_bar, 32 * kSoftmaxWarps);
+                        if (tid < 4)
+                            bad_sh[tid] = 0;
+#pragma unroll 1
+                        for (int hf = 0; hf < SPT && ok; ++hf) {
+                            uint4 *v = reinterpret_cast<uint4 *>(
+                                smem + SM::RING_OFF + (q0 + SPT * v_group(j, nt) + hf) % NSLAB * SM::SLAB);
+#pragma unroll 1
+                            for (int at = tid; at < SM::SLAB / 16; at += 256) {
+                                const uint4 x = v[at];
+                                const uint4 nf = make_uint4(not_finite<T>(x.x), not_finite<T>(x.y), not_finite<T>(x.z),
+                                                            not_finite<T>(x.w));
+                                if (nf.x | nf.y | nf.z | nf.w)
+                                    v[at] = make_uint4(x.x & ~nf.x, x.y & ~nf.y, x.z & ~nf.z, x.w & ~nf.w);
+                            }
+                        }
+                        kvc::fence_proxy_async_smem();
+                    }
                 }
                 float v[64];
                 if (active) {
@@ -898,22 +952,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                 }
                 // One barrier a tile of all softmax warps: the maxima are there, both halves' S has been
                 // read before either writes P, and a warp whose wait gave up takes the others with it.
-                bool spoiled = false;
-                if (kvc_tc::named_bar_any(all_bar, 32 * kSoftmaxWarps, !ok || (bad[0] | bad[1]))) {
-                    if (tid < 4)
-                        bad_sh[tid] = 0;
-                    if (kvc_tc::named_bar_any(all_bar, 32 * kSoftmaxWarps, !ok)) {
-                        stop = true;
-                        break;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (bad[e]) {
-                            atomicOr(&bad_sh[2 * e], (uint32_t)bad[e]);
-                            atomicOr(&bad_sh[2 * e + 1], (uint32_t)(bad[e] >> 32));
-                        }
-                    kvc_tc::named_bar_sync(all_bar, 32 * kSoftmaxWarps);
-                    spoiled = ((see[0] & bad_sh[2 * half]) | (see[1] & bad_sh[2 * half + 1])) != 0;
+                if (kvc_tc::named_bar_any(all_bar, 32 * kSoftmaxWarps, !ok)) {
+                    stop = true;
+                    break;
                 }
                 if (active) {
                     const float top = fmaxf(red[(s * 2 + half) * kBM + m], red[(s * 2 + (half ^ 1)) * kBM + m]) * c_log2;
@@ -942,7 +983,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                                 kvc_tc::pack2<T>(p0 - kvc::Elem<T>::to_f32(w[0]), p1 - kvc::Elem<T>::to_f32(w[1]));
                         }
                     }
-                    l_run = spoiled ? NAN : l_run * alpha + (ps0 + ps1);
+                    l_run = l_run * alpha + (ps0 + ps1);
                     kvc_tc::st32(lane_addr + SM::COL_S + s * kBN + 32 * half, pk);
                     if constexpr (!SM::SPLIT_Q)
                         kvc_tc::st32(lane_addr + SM::COL_S + s * kBN + 64 + 32 * half, pk2);
@@ -998,6 +1039,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                     kvc_tc::wait_ld();
                     if (r >= rows)
                         continue;
+                    if (const uint32_t bad = nan_cols[(cc - half * (D / 2)) / 32]) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            o[c] = bad >> c & 1u ? 0x7fc00000u : o[c];
+                    }
                     if (whole) {
                         const int64_t row0 = ((int64_t)cur.b * a.kv_heads + h) * rows + (int64_t)mt * kBM;
                         T *to = static_cast<T *>(a.out) + (row0 + m) * D + cc;
@@ -1009,7 +1055,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                             for (int e = 0; e < 4; ++e) {
                                 const float f0 = l == 0.f ? 0.f : __uint_as_float(o[c + 2 * e]) * inv;
                                 const float f1 = l == 0.f ? 0.f : __uint_as_float(o[c + 2 * e + 1]) * inv;
-                                w[e] = kvc_tc::pack2<T>(f0, f1);
+                                w[e] = kvc_tc::pack2<T>(kvc_tc::finite_or_nan(f0), kvc_tc::finite_or_nan(f1));
                             }
                             *reinterpret_cast<uint4 *>(to + c) = x;
                         }
@@ -1101,12 +1147,15 @@ tree_merge_kernel(const TreeArgs a)
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < W; ++k) {
-            // a part's weight a lane; a part that saw nothing (no sum) has none, whatever its O holds
-            float w = 0.f;
+            // a part's weight a lane; a part that saw nothing (no sum) has none (-1), whatever its O holds; one
+            // that is too small for a number still has its part's NaN
+            float w = -1.f;
             if (i0 + lane < parts) {
                 const float l = a.ws_l[stat(i0 + lane, k)], mc = a.ws_m[stat(i0 + lane, k)];
-                w = l == 0.f ? 0.f : mc == top[k] || mc == -INFINITY ? 1.f : exp2f(mc - top[k]);
-                sum[k] += l * w;
+                if (l != 0.f) {
+                    w = mc == top[k] || mc == -INFINITY ? 1.f : exp2f(mc - top[k]);
+                    sum[k] += l * w;
+                }
             }
             w_sh[W * warp + k][lane] = w;
         }
@@ -1115,8 +1164,8 @@ tree_merge_kernel(const TreeArgs a)
         for (int i = 0; i < here; i += AHEAD) {
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k) {
-                const float w = w_sh[mine][i + k];  // (zero past the last part)
-                if (w != 0.f) {
+                const float w = w_sh[mine][i + k];  // (-1 past the last part)
+                if (w >= 0.f) {
 #pragma unroll
                     for (int e = 0; e < PER; ++e) {
                         acc[e].x += x[k][e].x * w;
@@ -1146,8 +1195,8 @@ tree_merge_kernel(const TreeArgs a)
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
         uint2 y;
-        y.x = total == 0.f ? 0u : kvc_tc::pack2<T>(acc[e].x * inv, acc[e].y * inv);
-        y.y = total == 0.f ? 0u : kvc_tc::pack2<T>(acc[e].z * inv, acc[e].w * inv);
+        y.x = total == 0.f ? 0u : kvc_tc::pack2<T>(kvc_tc::finite_or_nan(acc[e].x * inv), kvc_tc::finite_or_nan(acc[e].y * inv));
+        y.y = total == 0.f ? 0u : kvc_tc::pack2<T>(kvc_tc::finite_or_nan(acc[e].z * inv), kvc_tc::finite_or_nan(acc[e].w * inv));
         *reinterpret_cast<uint2 *>(to + 4 * (c4 + LANES * e)) = y;
     }
 }
