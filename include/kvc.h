@@ -770,7 +770,8 @@ kvc_status kvc_page_bounds(void *bounds, float *bound_scale, const void *k_pool,
  * ceil(T / page_size) pages of each (batch row, kv head): the first sink_pages,
  * the last recent_pages (that of the newest token among them), and of the
  * others those with the largest scores, ties to the lower page.  With q the
- * rotated queries of the group (float32),
+ * rotated queries of the group (float32; -q when scale is negative, whose weights
+ * grow with -q . k),
  *     u_d = sum_h max(q_hd, 0), w_d = sum_h min(q_hd, 0), rounded to float32,
  *     sq = max(|u|, |w|) / 127, both rounded to codes rint(. / sq),
  *     score = s * float(sum_d code(u_d) hi_d + code(w_d) lo_d)

@@ -7,6 +7,7 @@
 // lo_d = floor(min_r k_rd / s).  For a query q no key of the page can exceed
 //     q . k <= s * sum_d max(q_d hi_d, q_d lo_d)
 //            = s * (sum_d max(q_d, 0) hi_d + sum_d min(q_d, 0) lo_d).
+// (With a negative `scale` the weights grow with -q . k: it is -q that is scored.)
 // Summed over the heads of a group this needs only the group's sums of the
 // positive and of the negative parts of the query, rounded to 8 bits: one
 // integer dot product of 2 D codes a page, exact, so that which pages are
@@ -186,6 +187,7 @@ struct SelectArgs {
     int64_t n_pool;
     kvc_lengths len;
     int batch, kv_heads, group, n_select, sink, recent;
+    int negate;            // score -q
     const float *cos_t, *sin_t;
     int64_t rope_max_pos;
     int32_t *selected;     // [B, kv_heads, n_select] logical pages
@@ -346,6 +348,10 @@ page_select_kernel(const SelectArgs a, int run_max)
                 float x[2] = {kvc::Elem<T>::to_f32(q[r * D + p]), kvc::Elem<T>::to_f32(q[r * D + D / 2 + p])};
                 if (a.cos_t)
                     kvc::rope_pair(x[0], x[1], cs, sn);
+                if (a.negate) {
+                    x[0] = -x[0];
+                    x[1] = -x[1];
+                }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     up[e].add(x[e] > 0.f ? x[e] : 0.f);
@@ -1324,6 +1330,7 @@ KVC_API kvc_status kvc_gqa_decode_sparse(void *out, const void *q, const void *k
     a.n_select = n_select;
     a.sink = sink_pages;
     a.recent = recent_pages;
+    a.negate = scale < 0.f;
     a.cos_t = rope_cos;
     a.sin_t = rope_sin;
     a.rope_max_pos = rope_max_pos;
