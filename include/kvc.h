@@ -788,6 +788,8 @@ kvc_status kvc_page_bounds(void *bounds, float *bound_scale, const void *k_pool,
  * max_pages <= 49152 (KVC_ERR_CAPACITY); batch * kv_heads <= 65535.
  * Types and sizes as kvc_gqa_decode_paged; the rotated query and the weights
  * enter with the digits of two 16-bit numbers, and only the result is rounded.
+ * A NaN or an infinity in a column of a V row that is read makes that column of
+ * the output NaN (rows behind the newest token may hold anything).
  * workspace    device, kvc_gqa_decode_sparse_workspace_size(...) bytes, 256-byte
  *              aligned.  Calls that may overlap on the GPU need their own.
  */

@@ -651,7 +651,9 @@ template <typename T> __device__ __forceinline__ void parts_of(float x, T &hi, T
 // (a group has 16 heads at most: the tensor cores have nine tenths of their time to
 // spare).  So the query, rotated in float32, and the weights are sums of two 16-bit
 // numbers each, at the price of a second product: of the roundings to 16 bits only
-// the result's is left.  A row that several CTAs worked on is joined by the one of
+// the result's is left.  (An infinity in V meets both parts of its weight, of which
+// the second may be zero or negative: what comes out is NaN or infinite as that falls,
+// and is made NaN.)  A row that several CTAs worked on is joined by the one of
 // them that finishes last, in the order of the shares whichever that is.
 // 64 rows of 64 pages of 64 keys of 128 (134 MB): 33 us alone, of which 20 are the
 // bytes; the first bytes come 3 us after the choice of pages is done, and the joins
@@ -1003,7 +1005,8 @@ sparse_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
                     sum += l_sh[w * HEADS + r] * exp2f(m_sh[w * HEADS + r] - top);
                 const float v = o_sh[r * SM::O_PITCH + d];
                 if (whole) {
-                    static_cast<T *>(a.out)[slice * a.group * D + idx] = kvc::Elem<T>::from_f32(v / sum);
+                    static_cast<T *>(a.out)[slice * a.group * D + idx] =
+                        kvc::Elem<T>::from_f32(kvc_tc::finite_or_nan(v / sum));
                 } else {
                     a.ws_o[(part * a.group + r) * D + d] = v;
                     if (d == 0) {
@@ -1070,7 +1073,7 @@ sparse_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
 #pragma unroll
                     for (int e = 0; e < D / 32; ++e)
                         static_cast<T *>(a.out)[(slice * a.group + r) * D + lane + 32 * e] =
-                            kvc::Elem<T>::from_f32(acc[e] / sum);
+                            kvc::Elem<T>::from_f32(kvc_tc::finite_or_nan(acc[e] / sum));
                 }
             }
         }
