@@ -214,15 +214,16 @@ def _lengths_of(lengths, batch):
     return lengths.c()
 
 
-def _held_by(stream, *buffers):
-    """Buffers that a call on `stream` allocated on the current stream: their memory goes to
-    nobody else before `stream` is past the call."""
+def _made_on(stream, make, *args):
+    """make(*args), its tensors from the memory of the stream that the call runs on.  Memory of the
+    current stream is not that stream's to write yet: a kernel queued on the current one may still
+    read what the block held before, and given back it would go to the current one's next kernel
+    while the call still runs."""
     if stream is None:
-        return
+        return make(*args)
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
-    for t in buffers:
-        if t is not None:
-            t.record_stream(s)
+    with torch.cuda.stream(s):
+        return make(*args)
 
 
 _DTYPE_CODES = {torch.float32: KVC_F32, torch.bfloat16: KVC_BF16, torch.float16: KVC_F16}
@@ -609,8 +610,7 @@ def kvc_gqa_decode_quant(out, q, kq, vq, k_scale, v_scale, lengths, windowed, lo
         _same("q", q, (B, Hq, 1, D))
     _same("out", out, shape, q.dtype)
     if isinstance(workspace, str):
-        workspace = quant_decode_workspace(q, kq)
-        _held_by(stream, workspace)
+        workspace = _made_on(stream, quant_decode_workspace, q, kq)
     cos, sin, rmax = _tables(rope)
     a, b, c, d, e, f, cs, sn, ws, st = _addresses(out, q, kq, vq, k_scale, v_scale, cos, sin,
                                                   workspace, status)
@@ -663,8 +663,7 @@ def kvc_gqa_decode_sparse(out, q, k_pool, v_pool, bounds, bound_scale, block_tab
     _same("block_table", block_table, (B, max_pages), torch.int32)
     _same("selected", selected, (B, Hkv, n), torch.int32)
     if isinstance(workspace, str):
-        workspace = sparse_workspace(q, k_pool, selected)
-        _held_by(stream, workspace)
+        workspace = _made_on(stream, sparse_workspace, q, k_pool, selected)
     cos, sin, rmax = _tables(rope)
     a, b, c, d, e, f, g, h, cs, sn, ws, st = _addresses(
         out, q, k_pool, v_pool, bounds, bound_scale, block_table, selected, cos, sin, workspace,
@@ -687,8 +686,10 @@ def kvc_tree_mask(parents, mask=None, depth=None, status=None, stream=None):
     """Ancestor bits and depths of the drafted trees parents, int32 [B, N] (include/kvc.h)."""
     B, N = parents.shape
     if mask is None:
-        mask, depth = tree_buffers(parents)
-        _held_by(stream, mask, depth)
+        mask, depth = _made_on(stream, tree_buffers, parents)
+        if stream is not None:  # (the caller reads them on the current stream too)
+            mask.record_stream(torch.cuda.current_stream())
+            depth.record_stream(torch.cuda.current_stream())
     if parents.dtype is not torch.int32:
         _same("parents", parents, (B, N), torch.int32)
     _same("mask", mask, (B, N, (N + 31) // 32), torch.int32)
@@ -748,8 +749,7 @@ def kvc_gqa_tree(out, q, k_cache, v_cache, mask, depth, lengths, block_table=Non
     _same("mask", mask, (B, N, (N + 31) // 32), torch.int32)
     _same("depth", depth, (B, N), torch.int32)
     if isinstance(workspace, str):
-        workspace = tree_workspace(q, k_cache)
-        _held_by(stream, workspace)
+        workspace = _made_on(stream, tree_workspace, q, k_cache)
     cos, sin, rmax = _tables(rope)
     a, b, c, d, e, f, table, cs, sn, ws, st = _addresses(
         out, q, k_cache, v_cache, mask, depth, block_table, cos, sin, workspace, status)
