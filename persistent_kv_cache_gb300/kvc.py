@@ -247,14 +247,17 @@ def _rope(rope):
     return _ptr(cos), _ptr(sin), cos.shape[0]
 
 
-def _tables(rope):
-    """cos, sin and their length of a rope argument"""
+def _tables(rope, D):
+    """cos, sin and their length of a rope argument for head_dim D (the library gets the length
+    alone, and would read tables of another width at the wrong places)"""
     if rope is None:
         return None, None, 0
     cos, sin = rope
     shape = cos.shape
-    if sin.shape != shape or cos.dtype is not torch.float32 or sin.dtype is not torch.float32:
-        raise ValueError("rope: cos and sin are float32 tables of the same shape [max_pos, D/2]")
+    if (sin.shape != shape or len(shape) != 2 or 2 * shape[1] != D or cos.dtype is not torch.float32
+            or sin.dtype is not torch.float32):
+        raise ValueError(f"rope: cos and sin are float32 tables of the same shape [max_pos, {D // 2}], got "
+                         f"{tuple(shape)} {cos.dtype} and {tuple(sin.shape)} {sin.dtype}")
     return cos, sin, shape[0]
 
 
@@ -568,7 +571,7 @@ def kvc_quant_append(kq, vq, k_scale, v_scale, new_k, new_v, lengths, windowed, 
     _same("new_v", new_v, shape, new_k.dtype)
     if shape != (B, Hkv, S, D):
         _same("new_k", new_k, (B, Hkv, S, D))
-    cos, sin, rmax = _tables(rope)
+    cos, sin, rmax = _tables(rope, D)
     a, b, c, d, e, f, cs, sn, st = _addresses(kq, vq, k_scale, v_scale, new_k, new_v, cos, sin,
                                               status)
     _check("kvc_quant_append", library().kvc_quant_append(
@@ -611,7 +614,7 @@ def kvc_gqa_decode_quant(out, q, kq, vq, k_scale, v_scale, lengths, windowed, lo
     _same("out", out, shape, q.dtype)
     if isinstance(workspace, str):
         workspace = _made_on(stream, quant_decode_workspace, q, kq)
-    cos, sin, rmax = _tables(rope)
+    cos, sin, rmax = _tables(rope, D)
     a, b, c, d, e, f, cs, sn, ws, st = _addresses(out, q, kq, vq, k_scale, v_scale, cos, sin,
                                                   workspace, status)
     _check("kvc_gqa_decode_quant", library().kvc_gqa_decode_quant(
@@ -664,7 +667,7 @@ def kvc_gqa_decode_sparse(out, q, k_pool, v_pool, bounds, bound_scale, block_tab
     _same("selected", selected, (B, Hkv, n), torch.int32)
     if isinstance(workspace, str):
         workspace = _made_on(stream, sparse_workspace, q, k_pool, selected)
-    cos, sin, rmax = _tables(rope)
+    cos, sin, rmax = _tables(rope, D)
     a, b, c, d, e, f, g, h, cs, sn, ws, st = _addresses(
         out, q, k_pool, v_pool, bounds, bound_scale, block_table, selected, cos, sin, workspace,
         status)
@@ -722,7 +725,7 @@ def kvc_tree_append(k_cache, v_cache, new_k, new_v, depth, lengths, block_table=
     _same("new_k", new_k, (B, Hkv, N, D), k_cache.dtype)
     _same("new_v", new_v, shape, k_cache.dtype)
     _same("depth", depth, (B, N), torch.int32)
-    cos, sin, rmax = _tables(rope)
+    cos, sin, rmax = _tables(rope, D)
     a, b, c, d, e, table, cs, sn, st = _addresses(k_cache, v_cache, new_k, new_v, depth,
                                                   block_table, cos, sin, status)
     _check("kvc_tree_append", library().kvc_tree_append(
@@ -750,7 +753,7 @@ def kvc_gqa_tree(out, q, k_cache, v_cache, mask, depth, lengths, block_table=Non
     _same("depth", depth, (B, N), torch.int32)
     if isinstance(workspace, str):
         workspace = _made_on(stream, tree_workspace, q, k_cache)
-    cos, sin, rmax = _tables(rope)
+    cos, sin, rmax = _tables(rope, D)
     a, b, c, d, e, f, table, cs, sn, ws, st = _addresses(
         out, q, k_cache, v_cache, mask, depth, block_table, cos, sin, workspace, status)
     _check("kvc_gqa_tree", library().kvc_gqa_tree(

@@ -1,0 +1,46 @@
+"""What the bindings of the quantised cache, the drafted trees and the selected pages refuse of the arguments whose
+shapes the library cannot see, and what they do with some that may be left out (no GPU needed)."""
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def K():
+    from persistent_kv_cache_gb300 import build
+    build.build()
+    from persistent_kv_cache_gb300 import kvc
+    return kvc
+
+
+def calls(K):
+    """each call that takes a rope argument, with everything else in order"""
+    B, H, C, D, N, page = 2, 2, 64, 64, 5, 64
+    z, bf, i32 = torch.zeros, torch.bfloat16, torch.int32
+    kq, s = z((B, H, C, D), dtype=torch.int8), z((B, H, C))
+    k, new = z((B, H, C, D), dtype=bf), z((B, H, N, D), dtype=bf)
+    q1, qn = z((B, 2 * H, 1, D), dtype=bf), z((B, 2 * H, N, D), dtype=bf)
+    depth, mask = z((B, N), dtype=i32), z((B, N, 1), dtype=i32)
+    table, sel = z((B, 1), dtype=i32), z((B, H, 2), dtype=i32)
+    bounds, bscale = z((B, H, 2, D), dtype=torch.int8), z((B, H))
+    return D, {
+        "kvc_quant_append": lambda rope: K.kvc_quant_append(kq, kq, s, s, new, new, None, 0, rope=rope),
+        "kvc_gqa_decode_quant": lambda rope: K.kvc_gqa_decode_quant(q1, q1, kq, kq, s, s, None, 0, rope=rope, workspace=None),
+        "kvc_gqa_decode_sparse": lambda rope: K.kvc_gqa_decode_sparse(q1, q1, k, k, bounds, bscale, table, None, sel, rope=rope,
+                                                                      workspace=None),
+        "kvc_tree_append": lambda rope: K.kvc_tree_append(k, k, new, new, depth, None, rope=rope),
+        "kvc_gqa_tree": lambda rope: K.kvc_gqa_tree(qn, qn, k, k, mask, depth, None, rope=rope, workspace=None),
+    }
+
+
+@pytest.mark.parametrize("name", ["kvc_quant_append", "kvc_gqa_decode_quant", "kvc_gqa_decode_sparse", "kvc_tree_append", "kvc_gqa_tree"])
+def test_rope_tables_of_another_shape(K, name):
+    D, made = calls(K)
+    call, z = made[name], torch.zeros
+    for cos, sin in ((z(9, D // 4), z(9, D // 4)), (z(9, D), z(9, D)), (z(9, D // 2 - 8), z(9, D // 2 - 8)), (z(9, D // 2), z(8, D // 2)),
+                     (z(9, 1, D // 2), z(9, 1, D // 2)), (z(9 * D // 2), z(9 * D // 2)), (z(9, D // 2).double(), z(9, D // 2).double()),
+                     (z(9, D // 2), z(9, D // 2).half())):
+        with pytest.raises(ValueError, match="rope"):
+            call((cos, sin))
+    # tables as they should be get as far as the check of the device
+    with pytest.raises(ValueError, match="CUDA"):
+        call((z(9, D // 2), z(9, D // 2)))
