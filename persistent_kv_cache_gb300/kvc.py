@@ -686,13 +686,15 @@ def tree_buffers(parents):
 
 
 def kvc_tree_mask(parents, mask=None, depth=None, status=None, stream=None):
-    """Ancestor bits and depths of the drafted trees parents, int32 [B, N] (include/kvc.h)."""
+    """Ancestor bits and depths of the drafted trees parents, int32 [B, N] (include/kvc.h), in mask
+    and depth where they are given."""
     B, N = parents.shape
-    if mask is None:
-        mask, depth = _made_on(stream, tree_buffers, parents)
+    if mask is None or depth is None:
+        made = _made_on(stream, tree_buffers, parents)
         if stream is not None:  # (the caller reads them on the current stream too)
-            mask.record_stream(torch.cuda.current_stream())
-            depth.record_stream(torch.cuda.current_stream())
+            for t in made:
+                t.record_stream(torch.cuda.current_stream())
+        mask, depth = made[0] if mask is None else mask, made[1] if depth is None else depth
     if parents.dtype is not torch.int32:
         _same("parents", parents, (B, N), torch.int32)
     _same("mask", mask, (B, N, (N + 31) // 32), torch.int32)

@@ -44,3 +44,29 @@ def test_rope_tables_of_another_shape(K, name):
     # tables as they should be get as far as the check of the device
     with pytest.raises(ValueError, match="CUDA"):
         call((z(9, D // 2), z(9, D // 2)))
+
+
+def test_tree_mask_fills_the_buffer_that_it_is_given(K, monkeypatch):
+    """mask without depth, depth without mask, both, neither: what is given is what is written and returned"""
+    parents = torch.full((3, 40), -1, dtype=torch.int32)
+    written = []
+
+    class Library:
+        def kvc_tree_mask(self, parents, batch, nodes, mask, depth, status, stream):
+            written.append((batch, nodes, mask, depth))
+            return 0
+
+    monkeypatch.setattr(K, "library", Library)
+    monkeypatch.setattr(K, "_addresses", lambda *tensors: [t if t is None else t.data_ptr() for t in tensors])
+    monkeypatch.setattr(K, "_stream", lambda stream: 0)
+    for has_mask in (False, True):
+        for has_depth in (False, True):
+            mask, depth = K.tree_buffers(parents)
+            got = K.kvc_tree_mask(parents, mask if has_mask else None, depth if has_depth else None)
+            assert got[0].shape == (3, 40, 2) and got[1].shape == (3, 40) and all(t.dtype == torch.int32 for t in got)
+            assert (got[0] is mask) == has_mask and (got[1] is depth) == has_depth
+            assert written.pop() == (3, 40, got[0].data_ptr(), got[1].data_ptr())
+    with pytest.raises(ValueError, match="depth"):
+        K.kvc_tree_mask(parents, mask, depth[:, :39])
+    with pytest.raises(ValueError, match="mask"):
+        K.kvc_tree_mask(parents, mask[..., :1], None)
