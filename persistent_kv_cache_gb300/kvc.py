@@ -211,6 +211,9 @@ def _addresses(*tensors):
 def _lengths_of(lengths, batch):
     if lengths.batch != batch:
         raise ValueError(f"lengths: made for {lengths.batch} batch rows, the tensors have {batch}")
+    at = _get_device()
+    if lengths.buf.get_device() != at:
+        raise ValueError(f"lengths: expected on the current device, cuda:{at}, got {lengths.buf.device}")
     return lengths.c()
 
 

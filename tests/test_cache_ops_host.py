@@ -70,3 +70,30 @@ def test_tree_mask_fills_the_buffer_that_it_is_given(K, monkeypatch):
         K.kvc_tree_mask(parents, mask, depth[:, :39])
     with pytest.raises(ValueError, match="mask"):
         K.kvc_tree_mask(parents, mask[..., :1], None)
+
+
+def test_lengths_of_another_device_or_batch(K, monkeypatch):
+    """every call that reads lengths refuses those that are not on the current device, before anything is launched"""
+    B, H, C, D, N = 2, 2, 64, 64, 5
+    z, bf, i32 = torch.zeros, torch.bfloat16, torch.int32
+    kq, s, k, new = z((B, H, C, D), dtype=torch.int8), z((B, H, C)), z((B, H, C, D), dtype=bf), z((B, H, N, D), dtype=bf)
+    q1, qn = z((B, 2 * H, 1, D), dtype=bf), z((B, 2 * H, N, D), dtype=bf)
+    depth, mask, count = z((B, N), dtype=i32), z((B, N, 1), dtype=i32), z(B, dtype=i32)
+    table, sel, bounds, bscale = z((B, 1), dtype=i32), z((B, H, 2), dtype=i32), z((B, H, 2, D), dtype=torch.int8), z((B, H))
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: pytest.fail(f"{name} was called")
+
+    monkeypatch.setattr(K, "library", Library)
+    monkeypatch.setattr(K, "_addresses", lambda *tensors: [0] * len(tensors))
+    monkeypatch.setattr(K, "_get_device", lambda: 0)
+    for L, what in ((K.Lengths(B, "cpu"), "current device, cuda:0, got cpu"), (K.Lengths(B + 1, "cpu"), "made for 3 batch rows")):
+        for call in (lambda: K.kvc_quant_append(kq, kq, s, s, new, new, L, 0), lambda: K.kvc_dequant_rows(k, k, kq, kq, s, s, L, 0),
+                     lambda: K.kvc_gqa_decode_quant(q1, q1, kq, kq, s, s, L, 0, workspace=None),
+                     lambda: K.kvc_page_bounds(bounds, bscale, k, table, L, 1),
+                     lambda: K.kvc_gqa_decode_sparse(q1, q1, k, k, bounds, bscale, table, L, sel, workspace=None),
+                     lambda: K.kvc_tree_append(k, k, new, new, depth, L), lambda: K.kvc_gqa_tree(qn, qn, k, k, mask, depth, L, workspace=None),
+                     lambda: K.kvc_tree_commit(k, k, depth, count, L, count, N)):
+            with pytest.raises(ValueError, match=what):
+                call()
