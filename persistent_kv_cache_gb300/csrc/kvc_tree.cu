@@ -695,7 +695,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                         kvc_tc::fence_after();
                         const uint64_t vd = v_ring + (uint64_t)(slot * (SM::SLAB / 16));
                         const uint32_t pa = tmem + SM::COL_S + s * kBN + hf * (KR / 2);
-#pragma unroll 1
+#pragma unroll
                         for (int part = 0; part < (SM::SPLIT_Q ? 1 : 2); ++part) {
 #pragma unroll
                             for (int k2 = 0; k2 < KR / 16; ++k2)
@@ -747,7 +747,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                 kvc_tc::fence_after();
                 for (int j = 0; ok && j < nt; ++j, ++J) {
                     const int buf = J & 1;
-                    // PV of the tile before last has read the weights that lie here
+                    // S_J is written where PV_{J-2} reads its weights.  Products follow one another in the order
+                    // of their issue only when they share accumulator and shape, which these two do not: the
+                    // wait for PV_{J-2} is what keeps its weights.  (With S_J issued right behind PV_{J-2} and no
+                    // wait, head_dim 64 came out wrong in every second tile when the products of S were written
+                    // out and so followed closely; with the wait both forms are right.)
                     if (J >= 2 && !(ok = wait_or_abort(&o_done[buf], ((J >> 1) - 1) & 1, abort_flag, a.status)))
                         break;
                     for (int hf = 0; hf < SPT; ++hf) {
@@ -757,10 +761,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                         kvc_tc::fence_after();
                         const uint64_t kd = k_ring + (uint64_t)(slot * (SM::SLAB / 16));
                         const uint32_t d_s = tmem + SM::COL_S + buf * kBN + hf * KR;
-                        // (a loop over the parts, not unrolled: with the second part's products written out
-                        // after the first's, head_dim 64 came out wrong in every second tile)
-#pragma unroll 1
-                        for (int part = 0; part < q_parts; ++part) {
+#pragma unroll
+                        for (int part = 0; part < (SM::SPLIT_Q ? 2 : 1); ++part) {
+                            if (part == q_parts)
+                                break;
                             const uint64_t qd = q_desc + (uint64_t)(part * (SM::Q_TILE / 16));
 #pragma unroll
                             for (int ks = 0; ks < D / 16; ++ks)
