@@ -348,10 +348,6 @@ page_select_kernel(const SelectArgs a, int run_max)
                 float x[2] = {kvc::Elem<T>::to_f32(q[r * D + p]), kvc::Elem<T>::to_f32(q[r * D + D / 2 + p])};
                 if (a.cos_t)
                     kvc::rope_pair(x[0], x[1], cs, sn);
-                if (a.negate) {
-                    x[0] = -x[0];
-                    x[1] = -x[1];
-                }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     up[e].add(x[e] > 0.f ? x[e] : 0.f);
@@ -360,8 +356,10 @@ page_select_kernel(const SelectArgs a, int run_max)
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                part[0][p + e * (D / 2)] = __fadd_rn(up[e].hi, up[e].lo);
-                part[1][p + e * (D / 2)] = __fadd_rn(down[e].hi, down[e].lo);
+                // (the positive parts of -q are the negative ones of q, with the other sign)
+                const float u = __fadd_rn(up[e].hi, up[e].lo), w = __fadd_rn(down[e].hi, down[e].lo);
+                part[0][p + e * (D / 2)] = a.negate ? -w : u;
+                part[1][p + e * (D / 2)] = a.negate ? -u : w;
             }
         } else if (tid >= kSelThreads / 2) {
             for (int j = tid - kSelThreads / 2; j < mine; j += kSelThreads / 2)
@@ -550,7 +548,8 @@ page_select_kernel(const SelectArgs a, int run_max)
 // --------------------------------------------------------------------------
 
 constexpr int kUnit = 64;           // keys of a unit of work: pages are whole units
-// units (kvc_flat.cuh) that a row costs beside its keys: 51 us with 2, 50 with 4, 49 with 6, 48 with 8
+// units (kvc_flat.cuh) that a row costs beside its keys: sparse-long of perf/operators.py takes
+// 48.3 us with 2, 47.5 with 4, 46.5 with 6, 45.7 with 8
 constexpr int kRowCost = 8;
 constexpr int kWarps = 4;           // that compute, 16 keys of a unit each
 constexpr int kDecodeThreads = 32 * (kWarps + 2);
@@ -588,7 +587,7 @@ __host__ __device__ constexpr int ctas_per_sm(int D) { return D == 64 ? 3 : D ==
 
 template <int D, int HB> struct SparseSmem {
     static constexpr int SLAB = kUnit * D * 2;                 // a unit's K or V
-    // (deeper, the queues before the memory hold up the joins more than the keys: 51 us with 2, 53 with 3)
+    // (deeper, the queues before the memory hold up the joins more than the keys: 45.7 us with 2, 47.6 with 3)
     static constexpr int STAGES = D == 64 ? 4 : 2;
     static constexpr int HEADS = 8 * HB;
     static constexpr int V_OFF = STAGES * SLAB, Q_OFF = 2 * STAGES * SLAB;
