@@ -74,6 +74,7 @@ class Lengths:
     def __init__(self, batch: int, device):
         self.batch = batch
         self.buf = torch.empty((5, batch), dtype=torch.int32, device=device)
+        self.at = self.buf.get_device()
         self._c = KvcLengths(*[self.buf[i].data_ptr() for i in range(5)])
 
     def __getattr__(self, name):
@@ -211,9 +212,8 @@ def _addresses(*tensors):
 def _lengths_of(lengths, batch):
     if lengths.batch != batch:
         raise ValueError(f"lengths: made for {lengths.batch} batch rows, the tensors have {batch}")
-    at = _get_device()
-    if lengths.buf.get_device() != at:
-        raise ValueError(f"lengths: expected on the current device, cuda:{at}, got {lengths.buf.device}")
+    if lengths.at != _get_device():
+        raise ValueError(f"lengths: expected on the current device, cuda:{_get_device()}, got {lengths.buf.device}")
     return lengths.c()
 
 
