@@ -729,6 +729,10 @@ kvc_status kvc_dequant_rows(void *k_out, void *v_out, const void *kq_cache, cons
  * Every CTA takes the same share of the batch's visible rows, whatever the
  * lengths; rows that several CTAs worked on are joined by a second launch, in
  * a fixed order.
+ * Beside the result, the rotated query (over a power of two) and the weights are
+ * rounded to halves for KVC_BF16; for KVC_F16 they enter with the digits of two.
+ * Query values up to 2^120 and scores (q . k times scale) up to 1e30 in magnitude;
+ * beyond, the output may be NaN.
  */
 kvc_status kvc_gqa_decode_quant(void *out, const void *q, const void *kq_cache,
                                 const void *vq_cache, const float *k_scale, const float *v_scale,
@@ -790,6 +794,7 @@ kvc_status kvc_page_bounds(void *bounds, float *bound_scale, const void *k_pool,
  * enter with the digits of two 16-bit numbers, and only the result is rounded.
  * A NaN or an infinity in a column of a V row that is read makes that column of
  * the output NaN (rows behind the newest token may hold anything).
+ * Scores (q . k times scale) up to 1e30 in magnitude; beyond, it may be NaN.
  * workspace    device, kvc_gqa_decode_sparse_workspace_size(...) bytes, 256-byte
  *              aligned.  Calls that may overlap on the GPU need their own.
  */
@@ -857,9 +862,13 @@ kvc_status kvc_tree_append(void *k_cache, void *v_cache, const void *new_k, cons
  * A NaN or an infinity in a column of a V row that a node sees makes that column
  * of its output NaN, whatever the row's weight; a NaN in a K row that it sees
  * makes all of them NaN.  What it does not see may hold anything.
- * A batch row that kvc_seq_lengths rejected, or that kvc_tree_append would
- * refuse, keeps its output; a page id outside the pool among the rows read sets
+ * A batch row that kvc_seq_lengths rejected, or with P + nodes past the capacity
+ * (KVC_DEV_CAPACITY) or rope_max_pos (KVC_DEV_ROPE_RANGE), keeps its output; a page
+ * id outside the pool among the rows read, the nodes' own among them, sets
  * KVC_DEV_INDEX_OOB (that row's output is then undefined).
+ * Beside the result, one of two numbers is rounded to the cache's type: the
+ * weights (head_dim 64 and 128) or the rotated query (256); the other enters with
+ * the digits of two 16-bit numbers.
  * out, q     device [batch, q_heads, nodes, head_dim]; q_heads / kv_heads <= 16,
  *            any whole number.
  * workspace  device, kvc_gqa_tree_workspace_size(...) bytes on the current device,
