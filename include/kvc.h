@@ -28,6 +28,9 @@
  *                          drafted tokens verified over the cache
  *     kvc_page_bounds, kvc_gqa_decode_sparse  one-token attention over the
  *                          pages that a cheap score selects
+ *     kvc_page_release, kvc_ragged_plan, kvc_rope_tables, kvc_ragged_append,
+ *     kvc_gqa_ragged       a step whose requests bring different numbers of new
+ *                          tokens: pages and places, tables, append, attention
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -97,6 +100,13 @@ typedef enum {
 typedef enum { KVC_F32 = 0, KVC_BF16 = 1, KVC_F16 = 2 } kvc_dtype;
 /* 8-bit codes of a quantised row (code * scale is the value) */
 typedef enum { KVC_INT8 = 0, KVC_E4M3 = 1 } kvc_quant_format;
+/* how rotation frequencies are stretched for contexts longer than those trained on */
+typedef enum {
+    KVC_ROPE_PLAIN = 0,  /* as trained                                           */
+    KVC_ROPE_LINEAR = 1, /* positions divided by a factor                        */
+    KVC_ROPE_BASE = 2,   /* a larger base: the slowest pair is slowed by it      */
+    KVC_ROPE_PARTS = 3   /* slow pairs slowed, fast ones kept, a ramp between    */
+} kvc_rope_scaling;
 typedef enum { KVC_LINEAR = 0, KVC_CIRCULAR = 1 } kvc_mode;
 typedef enum { KVC_APPEND = 0, KVC_COPY_BACK = 1 } kvc_phase;
 /* How the resident rows of a cache follow the absolute length T (the
@@ -903,6 +913,122 @@ kvc_status kvc_tree_commit(void *k_cache, void *v_cache, const int32_t *path,
                            int max_pages, int64_t n_pool_pages, int page_size, kvc_lengths len,
                            int32_t *seqlens_k, int batch, int kv_heads, int nodes, int64_t capacity,
                            int head_dim, int dtype, int32_t *dev_status, void *stream);
+
+/*
+ * A ragged step over a paged cache ("Persistent KV Cache and Decode Performance
+ * Roadmap", "Phase 2").  The calls above take the same number of new tokens for
+ * every batch row; here request b (a row of the block table) brings n_b >= 0 of
+ * its own -- one while it decodes, many while its prompt is read, none while it
+ * waits -- and the new tokens lie packed, request behind request, in buffers of
+ * `tokens` rows of which the last ones may be unused:
+ *     offsets    device int32 [batch + 1]: request b's tokens are rows
+ *                [offsets[b], offsets[b + 1])
+ *     positions  device int32 [tokens]: a token's position in its request
+ *     slots      device int32 [tokens]: page * page_size + row of the pool, where
+ *                its K and V go
+ * (positions and slots -1 for a row that is unused or whose request was rejected).
+ * Pools, tables and pages are those of kvc_paged_append; page_size >= 1, at most
+ * 16384 requests (KVC_ERR_UNSUPPORTED), max_pages * page_size and n_pool_pages *
+ * page_size below 2^31 (KVC_ERR_CAPACITY).
+ *
+ * Free pages are a stack: free_pages device int32 [n_pool_pages], its first
+ * *free_count entries (device int32) the ids of the free pages.  Both calls read
+ * *free_count and write *free_left, which must be another word: a loop that uses
+ * both calls passes (a, b) to one and (b, a) to the other.  A count outside
+ * [0, n_pool_pages] sets KVC_DEV_INDEX_OOB and counts as 0.
+ *
+ * kvc_page_release -- the pages of the first released[b] tokens of each row
+ * (device int32 [batch], 0: keeps all) are pushed, row by row, lower pages first.
+ * The table's entries stay as they are.  A negative count or one past the table
+ * sets KVC_DEV_SEQLEN_RANGE and releases nothing of that row; rows that the stack
+ * has no room for release nothing (KVC_DEV_CAPACITY); an id outside the pool is
+ * pushed as it is and sets KVC_DEV_INDEX_OOB.
+ */
+kvc_status kvc_page_release(const int32_t *released, const int32_t *block_table, int max_pages,
+                            int page_size, int32_t *free_pages, int64_t n_pool_pages,
+                            const int32_t *free_count, int32_t *free_left, int batch,
+                            int32_t *dev_status, void *stream);
+
+/*
+ * kvc_ragged_plan -- a step's places.  Request b holds cached[b] tokens in the
+ * ceil(cached[b] / page_size) first pages of its table row and brings
+ * new_tokens[b]; the pages that it lacks are popped off the stack, request by
+ * request, lower pages first, and written into the table.  offsets, positions and
+ * slots as above; len as kvc_seq_lengths(KVC_CONTIGUOUS) would: past_abs =
+ * cache_past = cached, total_abs = cache_total = cached + new_tokens, evict = 0,
+ * for use with the other calls of a paged cache.
+ * A rejected request has lengths -1, takes no page, and its rows of positions and
+ * slots are -1 (they keep their place in the buffer):
+ *   cached or new_tokens negative, or their sum past 2^31 - 1: KVC_DEV_SEQLEN_RANGE
+ *   (it takes no place); tokens past the table's row, past `tokens` rows, or pages
+ *   that the stack has not left (a request that wants pages after it is then
+ *   rejected too): KVC_DEV_CAPACITY; new tokens that would go on in a page whose id
+ *   is outside the pool: KVC_DEV_INDEX_OOB.
+ * A popped id outside the pool sets KVC_DEV_INDEX_OOB; its entry and slots are -1.
+ * offsets never exceed `tokens`.  positions, slots 16-byte aligned.
+ */
+kvc_status kvc_ragged_plan(const int32_t *cached, const int32_t *new_tokens, int32_t *block_table,
+                           int max_pages, int page_size, const int32_t *free_pages,
+                           int64_t n_pool_pages, const int32_t *free_count, int32_t *free_left,
+                           int batch, int tokens, int32_t *offsets, kvc_lengths len,
+                           int32_t *positions, int32_t *slots, int32_t *dev_status, void *stream);
+
+/*
+ * kvc_rope_tables -- the cos and sin tables that the calls here take, for
+ * positions first, first + 1, ...: cos_table[p][i] = magnitude * cos((first + p) *
+ * speed_i), sin likewise, i < rotary_dim / 2.  With speed = base^(-2 i / rotary_dim)
+ *   KVC_ROPE_PLAIN   speed_i = speed
+ *   KVC_ROPE_LINEAR  speed_i = speed / factor
+ *   KVC_ROPE_BASE    speed_i = speed with base * factor^(rotary_dim / (rotary_dim - 2))
+ *   KVC_ROPE_PARTS   a pair that goes round `high` times or more within `trained`
+ *                    positions keeps its speed, one that goes round `low` times or
+ *                    less has speed / factor, and between them g = (trained * speed /
+ *                    2 pi - low) / (high - low): g * speed + (1 - g) * speed / factor
+ * Speeds are float64, angles are reduced in whole numbers, so that far positions
+ * are as exact as near ones: off by a float32 rounding or two at any position.
+ * cos_table, sin_table  device float32 [positions, rotary_dim / 2] (4-byte aligned; the
+ *             calls that read them want 16).
+ * rotary_dim  even, 2..256 (KVC_ERR_UNSUPPORTED above).  base > 0; factor > 0
+ *             (ignored by KVC_ROPE_PLAIN); KVC_ROPE_PARTS: trained >= 1, low < high;
+ *             all finite (KVC_ERR_SHAPE).
+ */
+kvc_status kvc_rope_tables(float *cos_table, float *sin_table, int64_t first, int64_t positions,
+                           int rotary_dim, double base, int scaling, double factor,
+                           int64_t trained, double low, double high, double magnitude,
+                           void *stream);
+
+/*
+ * kvc_ragged_append -- from the projections of a packed batch to attention: each
+ * head's query and key is normed (x / sqrt(mean x^2 + eps) * weight, over the
+ * head's head_dim values; not where the weight is NULL) and its first rotary_dim
+ * columns rotated at the token's position, in float32 with one rounding at the
+ * end; queries go to q_out, K and V rows (V as given) to the token's slot.
+ * Pairs are (i, i + rotary_dim / 2), or with interleaved != 0 (2 i, 2 i + 1), with
+ * entry i of the tables; the other columns stay.  Products and sums of the rotation
+ * are rounded separately, so that without a norm and with rotary_dim = head_dim a
+ * row is bit for bit that of kvc_paged_append.
+ * q, k, v    device [tokens, heads, head_dim], the heads of a token dense, tokens
+ *            q_stride, k_stride, v_stride elements apart (slices of one projection's
+ *            output): multiples of 8, 16-byte aligned.
+ * q_out      device [tokens, q_heads, head_dim]; may be q where that is dense.
+ * q_weight, k_weight  device [head_dim] of `dtype`, or NULL.
+ * rope_cos, rope_sin  device float32 [rope_max_pos, rotary_dim / 2], or NULL (no
+ *            rotation; rotary_dim is then ignored).
+ * A token with slot < 0 is skipped: its row of q_out stays as it was.  So is one
+ * with a slot outside the pool (KVC_DEV_INDEX_OOB) or a position outside the tables
+ * (KVC_DEV_ROPE_RANGE).  Of two tokens with one slot either may end up there.
+ * KVC_BF16/KVC_F16; head_dim a multiple of 16 up to 256, rotary_dim a multiple of 16
+ * up to head_dim (KVC_ERR_UNSUPPORTED).  q_out and the pools may not overlap what is
+ * read (KVC_ERR_SHAPE).
+ */
+kvc_status kvc_ragged_append(void *q_out, void *k_pool, void *v_pool, const void *q, const void *k,
+                             const void *v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                             const void *q_weight, const void *k_weight, float eps,
+                             const int32_t *positions, const int32_t *slots, int tokens,
+                             int q_heads, int kv_heads, int64_t n_pool_pages, int page_size,
+                             int head_dim, int dtype, int rotary_dim, int interleaved,
+                             const float *rope_cos, const float *rope_sin, int64_t rope_max_pos,
+                             int32_t *dev_status, void *stream);
 
 /* Human-readable name of a status code (static storage). */
 const char *kvc_status_string(kvc_status status);

@@ -1,0 +1,696 @@
+// kvc_ragged.cu -- a serving step whose requests bring different numbers of
+// new tokens, packed one behind the other ("Persistent KV Cache and Decode
+// Performance Roadmap", "Phase 2": fixed-size pages read through a page table).
+//
+//   page_release_kernel  pages of ended requests go back onto the free stack
+//   ragged_plan_kernel   lengths -> pages taken, offsets, positions, slots
+//   rope_tables_kernel   cos and sin of every position, stretched for long contexts
+//   ragged_append_kernel norm of each head's query and key, their rotation, K and
+//                        V rows to their slots, in one pass
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <type_traits>
+
+#include "kvc_common.cuh"
+
+namespace {
+
+constexpr int kPlanThreads = 256;
+constexpr int kPlanTokens = 4 * kPlanThreads;  // tokens of a block
+constexpr int kMaxRequests = 16384;            // two words of shared memory each
+
+// Inclusive prefix sum over the block's threads; `sums` holds a word a warp.
+__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t *sums, int64_t &total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d)
+            x += y;
+    }
+    if (lane == 31)
+        sums[warp] = x;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        if (w == warp)
+            x += total;
+        total += sums[w];
+    }
+    __syncthreads();
+    return x;
+}
+
+__device__ __forceinline__ int64_t pages_of(int64_t tokens, int page_size)
+{
+    return (tokens + page_size - 1) / page_size;
+}
+
+struct Stack {
+    const int32_t *count;  // free pages before the call
+    int64_t n_pool;
+    // 0 for a count that no stack of the pool has
+    __device__ __forceinline__ int64_t depth(int32_t *status) const
+    {
+        const int64_t n = *count;
+        if (n >= 0 && n <= n_pool)
+            return n;
+        if (threadIdx.x == 0)
+            kvc::raise_status(status, KVC_DEV_INDEX_OOB);
+        return 0;
+    }
+};
+
+struct ReleaseArgs {
+    const int32_t *released, *table;
+    int max_pages, page_size;
+    int32_t *free_pages;
+    Stack stack;
+    int32_t *left;
+    int batch;
+    int32_t *status;
+};
+
+// Every block finds the place of every row's first page on the stack (a prefix
+// sum over the rows) and copies the pages of its own rows, a warp a row.
+__global__ void __launch_bounds__(kPlanThreads)
+page_release_kernel(const ReleaseArgs a)
+{
+    extern __shared__ int32_t place[];  // [batch], -1: nothing goes back
+    __shared__ int64_t sums[kPlanThreads / 32];
+    const int64_t depth = a.stack.depth(a.status);
+    int64_t before = 0;
+    int given = 0;  // pages that rows of this thread give back, for the number left
+    for (int b0 = 0; b0 < a.batch; b0 += kPlanThreads) {
+        const int b = b0 + threadIdx.x;
+        int64_t n = 0;
+        if (b < a.batch) {
+            const int t = a.released[b];
+            n = t > 0 ? pages_of(t, a.page_size) : 0;
+            if (t < 0 || n > a.max_pages) {
+                if (blockIdx.x == 0)
+                    kvc::raise_status(a.status, KVC_DEV_SEQLEN_RANGE);
+                n = 0;
+            }
+        }
+        int64_t total;
+        const int64_t end = before + block_scan(n, sums, total);
+        if (b < a.batch) {
+            const bool fits = depth + end <= a.stack.n_pool;
+            if (n > 0 && !fits && blockIdx.x == 0)
+                kvc::raise_status(a.status, KVC_DEV_CAPACITY);
+            place[b] = n > 0 && fits ? (int32_t)(depth + end - n) : -1;
+            given += n > 0 && fits ? (int)n : 0;
+        }
+        before += total;
+    }
+    int64_t total;
+    block_scan(given, sums, total);
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        *a.left = (int32_t)(depth + total);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int b = blockIdx.x * (kPlanThreads / 32) + warp; b < a.batch; b += gridDim.x * (kPlanThreads / 32)) {
+        const int at = place[b];
+        if (at < 0)
+            continue;
+        const int n = (int)pages_of(a.released[b], a.page_size);
+        for (int j = lane; j < n; j += 32) {
+            const int32_t id = a.table[(int64_t)b * a.max_pages + j];
+            if (id < 0 || id >= a.stack.n_pool)
+                kvc::raise_status(a.status, KVC_DEV_INDEX_OOB);
+            a.free_pages[at + j] = id;
+        }
+    }
+}
+
+struct PlanArgs {
+    const int32_t *cached, *fresh;
+    int32_t *table;
+    int max_pages, page_size;
+    const int32_t *free_pages;
+    Stack stack;
+    int32_t *left;
+    int batch, tokens;
+    int32_t *offsets;
+    kvc_lengths len;
+    int32_t *positions, *slots;
+    int32_t *status;
+};
+
+// Every block finds where every request's tokens begin and which pages it
+// takes (two prefix sums over the requests, in shared memory), block 0 writes
+// that down, and each block fills in the places of its 1024 tokens: a token
+// that begins a page that its request did not hold writes the page's id into the table.
+// (One launch: a second one for the tokens would cost as much as the sums.)
+__global__ void __launch_bounds__(kPlanThreads)
+ragged_plan_kernel(const PlanArgs a)
+{
+    extern __shared__ int32_t plan[];
+    __shared__ int64_t sums[kPlanThreads / 32];
+    int32_t *begin = plan;                // [batch + 1] first token
+    int32_t *taken = plan + a.batch + 1;  // [batch] pages that requests before it take, -1: rejected
+    const int64_t depth = a.stack.depth(a.status), capacity = (int64_t)a.max_pages * a.page_size;
+    const bool writer = blockIdx.x == 0;
+    int64_t tokens_before = 0, pages_before = 0, left = depth;
+    if (threadIdx.x == 0)
+        begin[0] = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += kPlanThreads) {
+        const int b = b0 + threadIdx.x;
+        int64_t P = 0, n = 0;
+        uint32_t bad = 0;
+        if (b < a.batch) {
+            P = a.cached[b];
+            n = a.fresh[b];
+            if (P < 0 || n < 0 || P + n > INT32_MAX) {
+                bad = KVC_DEV_SEQLEN_RANGE;
+                P = n = 0;
+            }
+        }
+        int64_t total;
+        const int64_t end = tokens_before + block_scan(n, sums, total);
+        tokens_before += total;
+        int64_t want = 0;
+        if (b < a.batch && !bad) {
+            if (P + n > capacity || (n > 0 && end > a.tokens)) {
+                bad = KVC_DEV_CAPACITY;
+            } else if (n > 0 && P % a.page_size) {
+                // new tokens go on in a page that the request holds
+                const int32_t id = a.table[(int64_t)b * a.max_pages + P / a.page_size];
+                if (id < 0 || id >= a.stack.n_pool)
+                    bad = KVC_DEV_INDEX_OOB;
+            }
+            if (!bad)
+                want = pages_of(P + n, a.page_size) - pages_of(P, a.page_size);
+        }
+        const int64_t upto = pages_before + block_scan(want, sums, total);
+        pages_before += total;
+        if (want > 0 && upto > depth)
+            bad = KVC_DEV_CAPACITY;
+        else if (want > 0)
+            left = depth - upto;
+        if (b < a.batch) {
+            begin[b + 1] = (int32_t)(end < a.tokens ? end : a.tokens);
+            taken[b] = bad ? -1 : (int32_t)(upto - want);
+            if (writer) {
+                if (bad)
+                    kvc::raise_status(a.status, bad);
+                a.offsets[b + 1] = begin[b + 1];
+                a.len.past_abs[b] = a.len.cache_past[b] = bad ? -1 : (int32_t)P;
+                a.len.total_abs[b] = a.len.cache_total[b] = bad ? -1 : (int32_t)(P + n);
+                a.len.evict[b] = bad ? -1 : 0;
+            }
+        }
+    }
+    if (writer) {
+        if (threadIdx.x == 0)
+            a.offsets[0] = 0;
+        // the least that any thread's requests leave (those that take pages are the first of those that want some)
+        __shared__ int least;
+        if (threadIdx.x == 0)
+            least = (int)depth;
+        __syncthreads();
+        atomicMin(&least, (int)left);
+        __syncthreads();
+        if (threadIdx.x == 0)
+            *a.left = least;
+    }
+    __syncthreads();
+
+    const int t0 = blockIdx.x * kPlanTokens + threadIdx.x * 4;
+    if (t0 >= a.tokens)
+        return;
+    // the last request that begins at t0 or before (empty ones begin where the next does)
+    int lo = 0, hi = a.batch;
+    while (hi - lo > 0) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (begin[mid] <= t0)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    int b = lo, P = 0;
+    if (b < a.batch)
+        P = a.cached[b];
+    int32_t pos[4], slot[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int t = t0 + e;
+        pos[e] = slot[e] = -1;
+        if (b < a.batch && t >= begin[b + 1]) {
+            do
+                ++b;
+            while (b < a.batch && t >= begin[b + 1]);
+            if (b < a.batch)
+                P = a.cached[b];
+        }
+        if (b >= a.batch || t >= a.tokens || taken[b] < 0)
+            continue;
+        const int p = P + (t - begin[b]);
+        const int j = p / a.page_size, at = p - j * a.page_size;
+        const int held = (int)pages_of(P, a.page_size);
+        int32_t *entry = a.table + (int64_t)b * a.max_pages + j;
+        const int32_t id = j < held ? *entry : a.free_pages[depth - 1 - (taken[b] + (j - held))];
+        const bool there = id >= 0 && id < a.stack.n_pool;
+        if (!there)
+            kvc::raise_status(a.status, KVC_DEV_INDEX_OOB);
+        if (j >= held && at == 0)
+            *entry = there ? id : -1;
+        pos[e] = p;
+        slot[e] = there ? id * a.page_size + at : -1;
+    }
+    if (t0 + 4 <= a.tokens) {
+        *reinterpret_cast<int4 *>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        *reinterpret_cast<int4 *>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+    } else {
+        for (int e = 0; t0 + e < a.tokens; ++e) {
+            a.positions[t0 + e] = pos[e];
+            a.slots[t0 + e] = slot[e];
+        }
+    }
+}
+
+kvc_status check_pages(int batch, int max_pages, int page_size, int64_t n_pool_pages)
+{
+    if (batch < 0 || max_pages < 1 || page_size < 1 || n_pool_pages < 1)
+        return KVC_ERR_SHAPE;
+    if (batch > kMaxRequests)
+        return KVC_ERR_UNSUPPORTED;
+    // slots and lengths are 32-bit
+    if ((int64_t)max_pages * page_size > INT32_MAX || n_pool_pages > INT32_MAX || n_pool_pages * page_size > INT32_MAX)
+        return KVC_ERR_CAPACITY;
+    return KVC_OK;
+}
+
+template <typename Kernel> bool allow_smem(Kernel kern, size_t bytes)
+{
+    return bytes <= 48 * 1024 ||
+           cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+}
+
+// --------------------------------------------------------------------------
+// rotation tables
+// --------------------------------------------------------------------------
+
+constexpr int kMaxPairs = 128;
+
+// What a position adds to each pair's angle, in units of 2^-64 of a turn: the
+// angle of position p is p times that modulo 2^64, exact for any p, so that far
+// positions lose nothing (in float32 an angle of 10^5 is known to 2^-7 only,
+// and float64 arithmetic is slow on this machine).
+struct TurnRates {
+    uint64_t per[kMaxPairs];
+};
+
+// cos and sin of x / 2^64 turns: the nearest quarter turn in whole numbers, the
+// rest, at most an eighth, in float32
+__device__ __forceinline__ void turn(uint64_t x, float &c, float &s)
+{
+    const uint32_t q = (uint32_t)((x + (1ull << 61)) >> 62);
+    const int64_t rest = (int64_t)(x - ((uint64_t)q << 62));
+    float sn, cs;
+    sincospif((float)rest * 0x1p-63f, &sn, &cs);
+    c = q & 1u ? sn : cs;
+    s = q & 1u ? cs : sn;
+    // quarter turns 1 and 2 have a negative cosine, 2 and 3 a negative sine
+    c = (q + 1u) & 2u ? -c : c;
+    s = q & 2u ? -s : s;
+}
+
+template <int VEC>
+__global__ void __launch_bounds__(256)
+rope_tables_kernel(float *__restrict__ cos_t, float *__restrict__ sin_t, int64_t first, int64_t positions, int half,
+                   const __grid_constant__ TurnRates rates, float magnitude)
+{
+    const int pieces = half / VEC;
+    const int64_t w = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    const int64_t p = w / pieces;
+    if (p >= positions)
+        return;
+    const int i0 = (int)(w - p * pieces) * VEC;
+    float c[VEC], s[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        turn((uint64_t)(first + p) * rates.per[i0 + e], c[e], s[e]);
+        c[e] *= magnitude;
+        s[e] *= magnitude;
+    }
+    const int64_t at = p * half + i0;
+    if constexpr (VEC == 4) {
+        *reinterpret_cast<float4 *>(cos_t + at) = make_float4(c[0], c[1], c[2], c[3]);
+        *reinterpret_cast<float4 *>(sin_t + at) = make_float4(s[0], s[1], s[2], s[3]);
+    } else {
+        cos_t[at] = c[0];
+        sin_t[at] = s[0];
+    }
+}
+
+// --------------------------------------------------------------------------
+// norm, rotation and append
+// --------------------------------------------------------------------------
+
+struct AppendArgs {
+    void *q_out, *k_pool, *v_pool;
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;  // elements from token to token
+    const void *q_weight, *k_weight;       // NULL: no norm
+    float eps;
+    const int32_t *positions, *slots;
+    int tokens, q_heads, kv_heads, D, page_size;
+    int64_t rows;  // of the pool: pages * page_size
+    int turned;    // columns rotated
+    int interleaved;
+    const float *cos_t, *sin_t;
+    int64_t rope_max_pos;
+    int split;     // parts of a token's rows (gridDim.y)
+    int32_t *status;
+};
+
+// A row (one head of one token) is LPR lanes of eight columns each.  GPT groups
+// of LPR lanes share a token's rows, so that a lane's cos, sin and weights stay
+// in registers from row to row; a block holds 256 / LPR / GPT tokens.
+template <typename T, int LPR>
+__global__ void __launch_bounds__(256)
+ragged_append_kernel(const AppendArgs a, int gpt)
+{
+    const int group = threadIdx.x / LPR, lane = threadIdx.x % LPR;
+    const int t = blockIdx.x * (256 / LPR / gpt) + group / gpt;
+    const int c0 = lane * 8;
+    const bool mine = c0 < a.D;
+    // (a warp's groups may be at rows of different kinds)
+    const uint32_t peers = LPR == 32 ? 0xffffffffu : ((1u << (LPR & 31)) - 1u) << (threadIdx.x & 31 & ~(LPR - 1));
+    const int slot = t < a.tokens ? a.slots[t] : -1;
+    const int pos = t < a.tokens ? a.positions[t] : -1;
+    bool there = slot >= 0;
+    if (there) {
+        const uint32_t bad = (slot >= a.rows ? KVC_DEV_INDEX_OOB : 0u) |
+                             (a.cos_t && (pos < 0 || pos >= a.rope_max_pos) ? KVC_DEV_ROPE_RANGE : 0u);
+        if (bad) {
+            if (lane == 0)
+                kvc::raise_status(a.status, bad);
+            there = false;
+        }
+    }
+    const int half = a.turned / 2;
+    const bool turns = a.cos_t && c0 < a.turned;  // (a multiple of 16: whole lanes turn or stay)
+    const bool low = c0 < half;
+    float cs[8], sn[8];
+    if (there && turns) {
+        if (a.interleaved) {
+            const float *c = a.cos_t + (int64_t)pos * half + c0 / 2, *s = a.sin_t + (int64_t)pos * half + c0 / 2;
+            const float4 x = *reinterpret_cast<const float4 *>(c), y = *reinterpret_cast<const float4 *>(s);
+            cs[0] = x.x, cs[1] = x.y, cs[2] = x.z, cs[3] = x.w;
+            sn[0] = y.x, sn[1] = y.y, sn[2] = y.z, sn[3] = y.w;
+        } else {
+            const int64_t at = (int64_t)pos * half + (low ? c0 : c0 - half);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float4 x = *reinterpret_cast<const float4 *>(a.cos_t + at + 4 * e);
+                const float4 y = *reinterpret_cast<const float4 *>(a.sin_t + at + 4 * e);
+                cs[4 * e] = x.x, cs[4 * e + 1] = x.y, cs[4 * e + 2] = x.z, cs[4 * e + 3] = x.w;
+                sn[4 * e] = y.x, sn[4 * e + 1] = y.y, sn[4 * e + 2] = y.z, sn[4 * e + 3] = y.w;
+            }
+        }
+    }
+    // the lane that holds the other half of this one's pairs
+    const int other = a.interleaved || !turns ? lane : low ? lane + half / 8 : lane - half / 8;
+    const int rows = a.q_heads + 2 * a.kv_heads;
+    const int64_t page = there ? slot / a.page_size : 0, in_page = there ? slot % a.page_size : 0;
+    for (int r = group % gpt + blockIdx.y * gpt; r < rows; r += gpt * a.split) {
+        const bool is_q = r < a.q_heads, is_v = r >= a.q_heads + a.kv_heads;
+        const int h = is_q ? r : is_v ? r - a.q_heads - a.kv_heads : r - a.q_heads;
+        const T *from = static_cast<const T *>(is_q ? a.q : is_v ? a.v : a.k) +
+                        t * (is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride) + (int64_t)h * a.D + c0;
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if (there && mine)
+            raw = *reinterpret_cast<const uint4 *>(from);
+        const void *weight = is_q ? a.q_weight : is_v ? nullptr : a.k_weight;
+        if (!is_v && (weight || a.cos_t)) {
+            T *x = reinterpret_cast<T *>(&raw);
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                f[e] = kvc::Elem<T>::to_f32(x[e]);
+            if (weight) {
+                float sum = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    sum = fmaf(f[e], f[e], sum);
+#pragma unroll
+                for (int d = LPR / 2; d; d >>= 1)
+                    sum += __shfl_xor_sync(peers, sum, d, LPR);
+                const float by = rsqrtf(sum / (float)a.D + a.eps);
+                uint4 w4 = make_uint4(0, 0, 0, 0);
+                if (mine)
+                    w4 = *reinterpret_cast<const uint4 *>(static_cast<const T *>(weight) + c0);
+                const T *w = reinterpret_cast<const T *>(&w4);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    f[e] = f[e] * by * kvc::Elem<T>::to_f32(w[e]);
+            }
+            if (a.cos_t) {
+                if (a.interleaved) {
+                    if (turns) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            kvc::rope_pair(f[2 * e], f[2 * e + 1], cs[e], sn[e]);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float o = __shfl_sync(peers, f[e], other, LPR);
+                        float lo = low ? f[e] : o, hi = low ? o : f[e];
+                        kvc::rope_pair(lo, hi, cs[e], sn[e]);
+                        f[e] = !turns ? f[e] : low ? lo : hi;
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                x[e] = kvc::Elem<T>::from_f32(f[e]);
+        }
+        if (there && mine) {
+            T *to = is_q ? static_cast<T *>(a.q_out) + ((int64_t)t * a.q_heads + h) * a.D
+                         : static_cast<T *>(is_v ? a.v_pool : a.k_pool) +
+                               ((page * a.kv_heads + h) * a.page_size + in_page) * a.D;
+            *reinterpret_cast<uint4 *>(to + c0) = raw;
+        }
+    }
+}
+
+template <typename T> void launch_append(const AppendArgs &a, cudaStream_t stream)
+{
+    const int rows = a.q_heads + 2 * a.kv_heads;
+    int lpr = 2;
+    while (lpr * 8 < a.D)
+        lpr *= 2;
+    const int groups = 256 / lpr;
+    int gpt = 1;
+    while (gpt < groups && gpt < rows)
+        gpt *= 2;
+    const int per_block = groups / gpt;
+    AppendArgs b = a;
+    const int blocks = (a.tokens + per_block - 1) / per_block;
+    // few tokens: a token's rows go to several blocks
+    b.split = std::max(1, std::min((rows + gpt - 1) / gpt, 4 * kvc_host::sm_count() / std::max(1, blocks)));
+    const dim3 grid(blocks, b.split);
+    switch (lpr) {
+    case 2:
+        ragged_append_kernel<T, 2><<<grid, 256, 0, stream>>>(b, gpt);
+        break;
+    case 4:
+        ragged_append_kernel<T, 4><<<grid, 256, 0, stream>>>(b, gpt);
+        break;
+    case 8:
+        ragged_append_kernel<T, 8><<<grid, 256, 0, stream>>>(b, gpt);
+        break;
+    case 16:
+        ragged_append_kernel<T, 16><<<grid, 256, 0, stream>>>(b, gpt);
+        break;
+    default:
+        ragged_append_kernel<T, 32><<<grid, 256, 0, stream>>>(b, gpt);
+        break;
+    }
+}
+
+} // namespace
+
+KVC_API kvc_status kvc_page_release(const int32_t *released, const int32_t *block_table, int max_pages, int page_size,
+                                    int32_t *free_pages, int64_t n_pool_pages, const int32_t *free_count,
+                                    int32_t *free_left, int batch, int32_t *dev_status, void *stream_)
+{
+    const kvc_status st = check_pages(batch, max_pages, page_size, n_pool_pages);
+    if (st != KVC_OK)
+        return st;
+    if (!free_pages || !free_count || !free_left || (batch > 0 && (!released || !block_table)))
+        return KVC_ERR_NULL;
+    if (free_left == free_count)
+        return KVC_ERR_SHAPE;
+    const ReleaseArgs a{released, block_table, max_pages, page_size, free_pages, {free_count, n_pool_pages}, free_left,
+                        batch, dev_status};
+    const size_t smem = (size_t)batch * sizeof(int32_t);
+    if (!allow_smem(page_release_kernel, smem))
+        return KVC_ERR_CUDA;
+    const int rows = kPlanThreads / 32;
+    const int grid = std::max(1, std::min((batch + rows - 1) / rows, kvc_host::sm_count()));
+    page_release_kernel<<<grid, kPlanThreads, smem, static_cast<cudaStream_t>(stream_)>>>(a);
+    return kvc_host::launch_status();
+}
+
+KVC_API kvc_status kvc_ragged_plan(const int32_t *cached, const int32_t *new_tokens, int32_t *block_table,
+                                   int max_pages, int page_size, const int32_t *free_pages, int64_t n_pool_pages,
+                                   const int32_t *free_count, int32_t *free_left, int batch, int tokens,
+                                   int32_t *offsets, kvc_lengths len, int32_t *positions, int32_t *slots,
+                                   int32_t *dev_status, void *stream_)
+{
+    const kvc_status st = check_pages(batch, max_pages, page_size, n_pool_pages);
+    if (st != KVC_OK)
+        return st;
+    if (tokens < 0)
+        return KVC_ERR_SHAPE;
+    if (!free_pages || !free_count || !free_left || !offsets || (tokens > 0 && (!positions || !slots)) ||
+        (batch > 0 && (!cached || !new_tokens || !block_table || !kvc_host::lengths_ok(len))))
+        return KVC_ERR_NULL;
+    if (!kvc_host::aligned16(positions) || !kvc_host::aligned16(slots))
+        return KVC_ERR_ALIGN;
+    if (free_left == free_count)
+        return KVC_ERR_SHAPE;
+    const PlanArgs a{cached, new_tokens, block_table, max_pages, page_size, free_pages, {free_count, n_pool_pages},
+                     free_left, batch, tokens, offsets, len, positions, slots, dev_status};
+    const size_t smem = (2 * (size_t)batch + 1) * sizeof(int32_t);
+    if (!allow_smem(ragged_plan_kernel, smem))
+        return KVC_ERR_CUDA;
+    const int grid = std::max(1, (int)(((int64_t)tokens + kPlanTokens - 1) / kPlanTokens));
+    ragged_plan_kernel<<<grid, kPlanThreads, smem, static_cast<cudaStream_t>(stream_)>>>(a);
+    return kvc_host::launch_status();
+}
+
+KVC_API kvc_status kvc_rope_tables(float *cos_table, float *sin_table, int64_t first, int64_t positions,
+                                   int rotary_dim, double base, int scaling, double factor, int64_t trained, double low,
+                                   double high, double magnitude, void *stream_)
+{
+    if (positions < 0 || first < 0 || first > INT64_MAX - positions || rotary_dim < 2 || rotary_dim % 2)
+        return KVC_ERR_SHAPE;
+    if (rotary_dim > 2 * kMaxPairs || scaling < KVC_ROPE_PLAIN || scaling > KVC_ROPE_PARTS)
+        return KVC_ERR_UNSUPPORTED;
+    if (!(base > 0.0) || !std::isfinite(base) || !std::isfinite(magnitude))
+        return KVC_ERR_SHAPE;
+    if (scaling != KVC_ROPE_PLAIN && (!(factor > 0.0) || !std::isfinite(factor)))
+        return KVC_ERR_SHAPE;
+    if (scaling == KVC_ROPE_BASE && rotary_dim == 2)
+        return KVC_ERR_SHAPE;
+    if (scaling == KVC_ROPE_PARTS && (trained < 1 || !(low < high) || !std::isfinite(low) || !std::isfinite(high)))
+        return KVC_ERR_SHAPE;
+    if (positions == 0)
+        return KVC_OK;
+    if (!cos_table || !sin_table)
+        return KVC_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(cos_table) | reinterpret_cast<uintptr_t>(sin_table)) & 3u)
+        return KVC_ERR_ALIGN;
+    const int half = rotary_dim / 2;
+    const size_t bytes = (size_t)positions * half * sizeof(float);
+    if (kvc_host::overlaps(cos_table, bytes, sin_table, bytes))
+        return KVC_ERR_SHAPE;
+    constexpr double kTurn = 6.283185307179586476925286766559;
+    if (scaling == KVC_ROPE_BASE)
+        base *= std::pow(factor, (double)rotary_dim / (rotary_dim - 2));
+    TurnRates rates{};
+    for (int i = 0; i < half; ++i) {
+        double speed = std::pow(base, -2.0 * i / rotary_dim);
+        if (scaling == KVC_ROPE_LINEAR) {
+            speed /= factor;
+        } else if (scaling == KVC_ROPE_PARTS) {
+            const double keep = std::min(1.0, std::max(0.0, (trained * (speed / kTurn) - low) / (high - low)));
+            speed = speed * keep + speed / factor * (1.0 - keep);
+        }
+        if (!std::isfinite(speed))
+            return KVC_ERR_SHAPE;
+        // whole turns a position change nothing
+        const double turns = speed / kTurn, rest = turns - std::floor(turns);
+        rates.per[i] = (uint64_t)std::ldexp(rest, 63) * 2;
+    }
+    const int vec = half % 4 == 0 && kvc_host::aligned16(cos_table) && kvc_host::aligned16(sin_table) ? 4 : 1;
+    const int64_t blocks = (positions * (half / vec) + 255) / 256;
+    if (blocks > INT32_MAX)
+        return KVC_ERR_SHAPE;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    if (vec == 4)
+        rope_tables_kernel<4><<<(unsigned)blocks, 256, 0, stream>>>(cos_table, sin_table, first, positions, half, rates,
+                                                                    (float)magnitude);
+    else
+        rope_tables_kernel<1><<<(unsigned)blocks, 256, 0, stream>>>(cos_table, sin_table, first, positions, half, rates,
+                                                                    (float)magnitude);
+    return kvc_host::launch_status();
+}
+
+KVC_API kvc_status kvc_ragged_append(void *q_out, void *k_pool, void *v_pool, const void *q, const void *k,
+                                     const void *v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                     const void *q_weight, const void *k_weight, float eps, const int32_t *positions,
+                                     const int32_t *slots, int tokens, int q_heads, int kv_heads, int64_t n_pool_pages,
+                                     int page_size, int head_dim, int dtype, int rotary_dim, int interleaved,
+                                     const float *rope_cos, const float *rope_sin, int64_t rope_max_pos,
+                                     int32_t *dev_status, void *stream_)
+{
+    if (kvc_host::elem_bytes_of(dtype) == 0)
+        return KVC_ERR_DTYPE;
+    if (dtype == KVC_F32)
+        return KVC_ERR_UNSUPPORTED;
+    if (tokens < 0 || q_heads < 1 || kv_heads < 1 || n_pool_pages < 1 || page_size < 1 || head_dim < 1)
+        return KVC_ERR_SHAPE;
+    if (head_dim % 16 || head_dim > 256 || q_heads > 32767 || kv_heads > 32767)
+        return KVC_ERR_UNSUPPORTED;
+    if (n_pool_pages > INT32_MAX || n_pool_pages * page_size > INT32_MAX)
+        return KVC_ERR_CAPACITY;
+    if ((rope_cos == nullptr) != (rope_sin == nullptr))
+        return KVC_ERR_NULL;
+    if (rope_cos) {
+        if (rope_max_pos < 1 || rotary_dim < 2 || rotary_dim > head_dim)
+            return KVC_ERR_SHAPE;
+        if (rotary_dim % 16)
+            return KVC_ERR_UNSUPPORTED;
+    }
+    if ((q_weight || k_weight) && !(eps >= 0.f && std::isfinite(eps)))
+        return KVC_ERR_SHAPE;
+    const int64_t q_row = (int64_t)q_heads * head_dim, kv_row = (int64_t)kv_heads * head_dim;
+    if (tokens > 1 && (q_stride < q_row || k_stride < kv_row || v_stride < kv_row))
+        return KVC_ERR_SHAPE;
+    if (tokens == 0)
+        return KVC_OK;
+    if (!q_out || !k_pool || !v_pool || !q || !k || !v || !positions || !slots)
+        return KVC_ERR_NULL;
+    for (const void *p : {(const void *)q_out, (const void *)k_pool, (const void *)v_pool, q, k, v, q_weight, k_weight,
+                          (const void *)rope_cos, (const void *)rope_sin})
+        if (p && !kvc_host::aligned16(p))
+            return KVC_ERR_ALIGN;
+    if (tokens > 1 && (q_stride % 8 || k_stride % 8 || v_stride % 8))
+        return KVC_ERR_ALIGN;
+    if (tokens == 1)
+        q_stride = q_row, k_stride = v_stride = kv_row;
+    if (q_stride > INT64_MAX / 4 / tokens || k_stride > INT64_MAX / 4 / tokens || v_stride > INT64_MAX / 4 / tokens)
+        return KVC_ERR_SHAPE;
+    // what is written shares no bytes with what is read (q_out == q, packed alike, is the one way in place)
+    const size_t pool = (size_t)n_pool_pages * page_size * kv_row * 2, out = (size_t)tokens * q_row * 2;
+    const size_t q_bytes = ((size_t)(tokens - 1) * q_stride + q_row) * 2,
+                 k_bytes = ((size_t)(tokens - 1) * k_stride + kv_row) * 2,
+                 v_bytes = ((size_t)(tokens - 1) * v_stride + kv_row) * 2;
+    const bool in_place = q_out == q && q_stride == q_row;
+    if (kvc_host::overlaps(k_pool, pool, v_pool, pool) || kvc_host::overlaps(q_out, out, k_pool, pool) ||
+        kvc_host::overlaps(q_out, out, v_pool, pool) || (!in_place && kvc_host::overlaps(q_out, out, q, q_bytes)) ||
+        kvc_host::overlaps(q_out, out, k, k_bytes) || kvc_host::overlaps(q_out, out, v, v_bytes))
+        return KVC_ERR_SHAPE;
+    for (const void *p : {(const void *)k_pool, (const void *)v_pool})
+        if (kvc_host::overlaps(p, pool, q, q_bytes) || kvc_host::overlaps(p, pool, k, k_bytes) ||
+            kvc_host::overlaps(p, pool, v, v_bytes))
+            return KVC_ERR_SHAPE;
+    const AppendArgs a{q_out, k_pool, v_pool, q, k, v, q_stride, k_stride, v_stride, q_weight, k_weight, eps, positions,
+                       slots, tokens, q_heads, kv_heads, head_dim, page_size, n_pool_pages * page_size,
+                       rope_cos ? rotary_dim : 0, interleaved, rope_cos, rope_sin, rope_max_pos, 1, dev_status};
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    if (dtype == KVC_BF16)
+        launch_append<__nv_bfloat16>(a, stream);
+    else
+        launch_append<__half>(a, stream);
+    return kvc_host::launch_status();
+}

@@ -18,6 +18,8 @@ KVC_F32, KVC_BF16, KVC_F16 = 0, 1, 2
 KVC_LINEAR, KVC_CIRCULAR = 0, 1
 KVC_APPEND, KVC_COPY_BACK = 0, 1
 KVC_INT8, KVC_E4M3 = 0, 1
+# stretching of rotation frequencies (kvc_rope_tables)
+KVC_ROPE_PLAIN, KVC_ROPE_LINEAR, KVC_ROPE_BASE, KVC_ROPE_PARTS = 0, 1, 2, 3
 
 KVC_OK = 0
 STATUS_NAMES = {
@@ -44,6 +46,7 @@ EXPORTS = ("kvc_tensor_scatter", "kvc_seq_lengths", "kvc_window_append", "kvc_gq
            "kvc_gqa_decode_quant_workspace_size", "kvc_page_bounds", "kvc_gqa_decode_sparse",
            "kvc_gqa_decode_sparse_workspace_size", "kvc_tree_mask", "kvc_tree_append",
            "kvc_gqa_tree", "kvc_gqa_tree_workspace_size", "kvc_tree_commit",
+           "kvc_page_release", "kvc_ragged_plan", "kvc_rope_tables", "kvc_ragged_append",
            "kvc_status_string", "kvc_abi_version")
 KVC_DECODE_STATIC_SCRATCH_BYTES = 16 << 20
 KVC_PAGE_QUANT = 0x40000000  # block-table flag: the entry names an int8 page
@@ -98,6 +101,7 @@ def library() -> ctypes.CDLL:
         lib = ctypes.CDLL(LIB_PATH)
         P, I, I64, F, SZ = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float,
                             ctypes.c_size_t)
+        DBL = ctypes.c_double
         L = KvcLengths
         sig = {
             "kvc_tensor_scatter": [P, P, P, P, I, P, I64, I, I, I, P, P],
@@ -143,6 +147,11 @@ def library() -> ctypes.CDLL:
                              P, SZ, P, P],
             "kvc_gqa_tree_workspace_size": [I, I, I, I, I],
             "kvc_tree_commit": [P, P, P, P, I, P, I, I64, I, L, P, I, I, I, I64, I, I, P, P],
+            "kvc_page_release": [P, P, I, I, P, I64, P, P, I, P, P],
+            "kvc_ragged_plan": [P, P, P, I, I, P, I64, P, P, I, I, P, L, P, P, P, P],
+            "kvc_rope_tables": [P, P, I64, I64, I, DBL, I, DBL, I64, DBL, DBL, DBL, P],
+            "kvc_ragged_append": [P, P, P, P, P, P, I64, I64, I64, P, P, F, P, P, I, I, I, I64, I, I, I, I,
+                                  I, P, P, I64, P, P],
             "kvc_status_string": [I],
             "kvc_abi_version": [],
         }
@@ -783,3 +792,116 @@ def kvc_tree_commit(k_cache, v_cache, path, accepted, lengths, seqlens_k, nodes,
     _check("kvc_tree_commit", library().kvc_tree_commit(
         a, b, c, d, path_len, table, m, n, ps, _lengths_of(lengths, B), e, B, Hkv, nodes, C, D,
         _dtype_code(k_cache), st, _stream(stream)))
+
+
+class RaggedPlan:
+    """A ragged step's places, written by kvc_ragged_plan (include/kvc.h): offsets int32
+    [batch + 1], positions and slots int32 [tokens], and lengths (Lengths)."""
+
+    def __init__(self, batch: int, tokens: int, device):
+        self.batch, self.tokens = batch, tokens
+        self.offsets = torch.empty(batch + 1, dtype=torch.int32, device=device)
+        self.positions = torch.empty(tokens, dtype=torch.int32, device=device)
+        self.slots = torch.empty(tokens, dtype=torch.int32, device=device)
+        self.lengths = Lengths(batch, device)
+
+
+def _free_stack(free_pages, free_count, free_left):
+    shape = free_pages.shape
+    if len(shape) != 1 or free_pages.dtype is not torch.int32:
+        _same("free_pages", free_pages, (free_pages.numel(),), torch.int32)
+    if free_count.numel() != 1 or free_count.dtype is not torch.int32:
+        _same("free_count", free_count, (1,), torch.int32)
+    if free_left.numel() != 1 or free_left.dtype is not torch.int32:
+        _same("free_left", free_left, (1,), torch.int32)
+    return shape[0]
+
+
+def kvc_page_release(released, block_table, page_size, free_pages, free_count, free_left,
+                     status=None, stream=None):
+    """The pages of the first released[b] tokens of each request go back onto the stack
+    free_pages int32 [pool pages] (include/kvc.h)."""
+    B, max_pages = block_table.shape
+    n = _free_stack(free_pages, free_count, free_left)
+    _same("block_table", block_table, (B, max_pages), torch.int32)
+    _same("released", released, (B,), torch.int32)
+    a, b, c, d, e, st = _addresses(released, block_table, free_pages, free_count, free_left, status)
+    _check("kvc_page_release", library().kvc_page_release(
+        a, b, max_pages, page_size, c, n, d, e, B, st, _stream(stream)))
+
+
+def kvc_ragged_plan(cached, new_tokens, block_table, page_size, free_pages, free_count, free_left,
+                    plan, status=None, stream=None):
+    """The pages, offsets, positions, slots and lengths of a step in which request b brings
+    new_tokens[b] to the cached[b] it holds (include/kvc.h), in plan (RaggedPlan)."""
+    B, max_pages = block_table.shape
+    n = _free_stack(free_pages, free_count, free_left)
+    _same("block_table", block_table, (B, max_pages), torch.int32)
+    _same("cached", cached, (B,), torch.int32)
+    _same("new_tokens", new_tokens, (B,), torch.int32)
+    _same("plan.offsets", plan.offsets, (B + 1,), torch.int32)
+    _same("plan.positions", plan.positions, (plan.tokens,), torch.int32)
+    _same("plan.slots", plan.slots, (plan.tokens,), torch.int32)
+    a, b, c, d, e, f, g, h, i, st = _addresses(cached, new_tokens, block_table, free_pages, free_count,
+                                               free_left, plan.offsets, plan.positions, plan.slots,
+                                               status)
+    _check("kvc_ragged_plan", library().kvc_ragged_plan(
+        a, b, c, max_pages, page_size, d, n, e, f, B, plan.tokens, g, _lengths_of(plan.lengths, B), h, i,
+        st, _stream(stream)))
+    return plan
+
+
+def kvc_rope_tables(cos, sin, first=0, base=10000.0, scaling=KVC_ROPE_PLAIN, factor=1.0, trained=1,
+                    low=1.0, high=32.0, magnitude=1.0, stream=None):
+    """cos and sin, float32 [positions, rotary_dim / 2], of the positions from first on
+    (include/kvc.h); the pair that the rope arguments here take."""
+    n, half = cos.shape
+    _same("cos", cos, (n, half), torch.float32)
+    _same("sin", sin, (n, half), torch.float32)
+    a, b = _addresses(cos, sin)
+    _check("kvc_rope_tables", library().kvc_rope_tables(
+        a, b, first, n, 2 * half, base, scaling, factor, trained, low, high, magnitude,
+        _stream(stream)))
+    return cos, sin
+
+
+def _token_rows(name, t, tokens, heads, D, dtype):
+    """Address and token stride of t [tokens, heads, D], whose heads are dense (a slice of a
+    projection's output)."""
+    if t.shape != (tokens, heads, D) or t.dtype is not dtype:
+        _same(name, t, (tokens, heads, D), dtype)
+    step, row, one = t.stride()
+    if (one != 1 and D > 1) or (row != D and heads > 1) or t.get_device() != _get_device():
+        _addresses(t)  # (raises, but for a dense tensor)
+    return t.data_ptr(), step
+
+
+def kvc_ragged_append(q_out, k_pool, v_pool, q, k, v, positions, slots, rope=None,
+                      interleaved=False, q_weight=None, k_weight=None, eps=1e-6, status=None,
+                      stream=None):
+    """Norm (with weights [D]) and rotation of the packed queries and keys, queries to q_out
+    [tokens, Hq, D], K and V to their slots (include/kvc.h).  q, k, v [tokens, heads, D] may be
+    slices of one tensor along their second dimension; rotary_dim is twice the tables' width."""
+    n_pages, H, ps, D = pool = k_pool.shape
+    T, Hq, _ = shape = q.shape
+    dtype = q.dtype
+    if not q.is_cuda:
+        raise ValueError(f"expected a CUDA tensor, got one on {q.device}")
+    _same("k_pool", k_pool, pool, dtype)
+    _same("v_pool", v_pool, pool, dtype)
+    _same("q_out", q_out, shape, dtype)
+    _same("positions", positions, (T,), torch.int32)
+    _same("slots", slots, (T,), torch.int32)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _same(name, w, (D,), dtype)
+    (qa, qs), (ka, ks), (va, vs) = (_token_rows("q", q, T, Hq, D, dtype), _token_rows("k", k, T, H, D, dtype),
+                                    _token_rows("v", v, T, H, D, dtype))
+    cos, sin, rmax = _tables(rope, D if rope is None else 2 * rope[0].shape[-1])
+    turned = 0 if cos is None else 2 * cos.shape[1]
+    a, b, c, d, e, wq, wk, cs, sn, st = _addresses(q_out, k_pool, v_pool, positions, slots, q_weight,
+                                                   k_weight, cos, sin, status)
+    _check("kvc_ragged_append", library().kvc_ragged_append(
+        a, b, c, qa, ka, va, qs, ks, vs, wq, wk, eps, d, e, T, Hq, H, n_pages, ps, D,
+        _dtype_code(q), turned, int(bool(interleaved)), cs, sn, rmax, st, _stream(stream)))
+    return q_out

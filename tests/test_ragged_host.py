@@ -1,0 +1,139 @@
+"""The calls of a ragged step without a GPU: arguments that the library and its binding refuse before
+anything is enqueued (fake addresses are never touched)."""
+import ctypes
+import inspect
+
+import pytest
+import torch
+
+FAKE = 0x100000
+
+
+@pytest.fixture(scope="module")
+def K():
+    from persistent_kv_cache_gb300 import build
+    build.build()
+    from persistent_kv_cache_gb300 import kvc
+    return kvc
+
+
+def lengths(K, at=FAKE):
+    return K.KvcLengths(at, at, at, at, at)
+
+
+def caller(fn, **base):
+    """fn(**changes) with named arguments in the order of `base`"""
+    def call(**kw):
+        assert set(kw) <= set(base), set(kw) - set(base)
+        return fn(*{**base, **kw}.values())
+    return call
+
+
+def test_page_release(K):
+    f = caller(K.library().kvc_page_release, released=FAKE, table=FAKE, max_pages=4, page=16, free=FAKE, pool=64, count=FAKE,
+               left=FAKE + 64, batch=0, status=None, stream=None)
+    assert f(max_pages=0) == 2 and f(page=0) == 2 and f(pool=0) == 2 and f(batch=-1) == 2
+    assert f(batch=16385) == 5
+    assert f(max_pages=1 << 20, page=2048) == 6 and f(pool=1 << 27) == 6 and f(pool=1 << 40) == 6
+    assert f(free=None) == 1 and f(count=None) == 1 and f(left=None) == 1
+    assert f(batch=1, released=None) == 1 and f(batch=1, table=None) == 1
+    assert f(left=FAKE) == 2  # the same word as the count
+
+
+def test_ragged_plan(K):
+    f = caller(K.library().kvc_ragged_plan, cached=FAKE, new=FAKE, table=FAKE, max_pages=4, page=16, free=FAKE, pool=64, count=FAKE,
+               left=FAKE + 64, batch=1, tokens=8, offsets=FAKE, len=lengths(K), positions=FAKE, slots=FAKE, status=None, stream=None)
+    assert f(max_pages=0) == 2 and f(page=0) == 2 and f(pool=0) == 2 and f(batch=-1) == 2 and f(tokens=-1) == 2
+    assert f(batch=16385) == 5
+    assert f(max_pages=1 << 20, page=2048) == 6 and f(pool=1 << 27) == 6
+    for name in ("cached", "new", "table", "free", "count", "left", "offsets", "positions", "slots"):
+        assert f(**{name: None}) == 1, name
+    assert f(len=lengths(K, None)) == 1
+    assert f(positions=FAKE + 4) == 4 and f(slots=FAKE + 8) == 4
+    assert f(left=FAKE) == 2
+
+
+def test_rope_tables(K):
+    f = caller(K.library().kvc_rope_tables, cos=FAKE, sin=FAKE * 8, first=0, positions=8, dim=64, base=1e4, scaling=0, factor=0.0,
+               trained=0, low=0.0, high=0.0, magnitude=1.0, stream=None)
+    inf, nan = float("inf"), float("nan")
+    assert f(positions=-1) == 2 and f(first=-1) == 2 and f(first=(1 << 63) - 4) == 2 and f(dim=0) == 2 and f(dim=7) == 2
+    assert f(dim=258) == 5 and f(scaling=-1) == 5 and f(scaling=4) == 5
+    assert f(base=0.0) == 2 and f(base=-1.0) == 2 and f(base=nan) == 2 and f(base=inf) == 2 and f(magnitude=nan) == 2
+    assert f(scaling=1) == 2 and f(scaling=1, factor=-2.0) == 2 and f(scaling=2, factor=inf) == 2 and f(scaling=2, factor=2.0, dim=2) == 2
+    parts = dict(scaling=3, factor=4.0, trained=64, low=1.0, high=4.0)
+    assert f(**{**parts, "trained": 0}) == 2 and f(**{**parts, "high": 1.0}) == 2 and f(**{**parts, "low": nan}) == 2
+    assert f(cos=None) == 1 and f(sin=None) == 1 and f(cos=FAKE + 2) == 4 and f(sin=FAKE * 8 + 1) == 4
+    assert f(sin=FAKE + 512) == 2  # overlapping tables
+    assert f(positions=0, cos=None, sin=None) == 0
+    assert f(base=1e-300, dim=256, scaling=1, factor=1e-300) == 2  # a speed that is no number
+
+
+def test_ragged_append(K):
+    f = caller(K.library().kvc_ragged_append, q_out=FAKE, k_pool=1 << 30, v_pool=1 << 31, q=1 << 32, k=(1 << 32) + 1024,
+               v=(1 << 32) + 1536, qs=1024, ks=1024, vs=1024, qw=None, kw=None, eps=1e-6, positions=FAKE, slots=FAKE, tokens=4,
+               q_heads=4, kv_heads=2, pool=8, page=16, dim=128, dtype=1, turned=128, inter=0, cos=FAKE, sin=FAKE, rmax=64,
+               status=None, stream=None)
+    assert f(dtype=7) == 3 and f(dtype=0) == 5
+    assert f(tokens=-1) == 2 and f(q_heads=0) == 2 and f(kv_heads=0) == 2 and f(pool=0) == 2 and f(page=0) == 2 and f(dim=0) == 2
+    assert f(dim=72) == 5 and f(dim=272) == 5 and f(q_heads=40000) == 5
+    assert f(pool=1 << 28) == 6
+    assert f(sin=None) == 1 and f(cos=None) == 1
+    assert f(rmax=0) == 2 and f(turned=0) == 2 and f(turned=144) == 2 and f(turned=24) == 5
+    assert f(qw=FAKE, eps=-1.0) == 2 and f(kw=FAKE, eps=float("nan")) == 2
+    assert f(qs=256) == 2 and f(ks=128) == 2 and f(vs=128) == 2
+    for name in ("q_out", "k_pool", "v_pool", "q", "k", "v", "positions", "slots"):
+        assert f(**{name: None}) == 1, name
+    for name in ("q_out", "k_pool", "v_pool", "q", "k", "v"):
+        assert f(**{name: (1 << 33) + 8}) == 4, name
+    for name in ("qw", "kw", "cos", "sin"):
+        assert f(**{name: FAKE + 4}) == 4, name
+    assert f(qs=1028) == 4 and f(ks=1026) == 4 and f(vs=1025) == 4
+    # what is written over what is read or written
+    assert f(v_pool=(1 << 30) + 64) == 2 and f(q_out=1 << 30) == 2 and f(q_out=1 << 32) == 2 and f(k_pool=1 << 32) == 2
+    assert f(v_pool=(1 << 32) - 16) == 2 and f(q_out=(1 << 32) + 2048) == 2
+    assert f(tokens=0, q_out=None) == 0
+
+
+def test_binding_refuses_other_shapes(K, monkeypatch):
+    """The library gets sizes from one tensor of each kind: the binding compares the others.  (Tensors of
+    the meta device stand in for the GPU's.)"""
+    monkeypatch.setattr(K, "_get_device", lambda: -1)
+    monkeypatch.setattr(K, "_addresses", lambda *a: (_ for _ in ()).throw(AssertionError("got as far as the addresses")))
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    f32 = lambda *s: torch.zeros(s)  # noqa: E731
+    table, free, one = i32(3, 4), i32(64), i32(1)
+    for kw in (dict(released=i32(2)), dict(released=i32(3).long()), dict(block_table=i32(3, 4).long()), dict(free_count=i32(2)),
+               dict(free_left=one.long()), dict(free_pages=free.long())):
+        args = {**dict(released=i32(3), block_table=table, page_size=16, free_pages=free, free_count=one, free_left=i32(1)), **kw}
+        with pytest.raises(ValueError, match="expected"):
+            K.kvc_page_release(**args)
+    plan = K.RaggedPlan(3, 8, "cpu")
+    for kw in (dict(cached=i32(2)), dict(new_tokens=i32(4)), dict(new_tokens=i32(3).long()), dict(block_table=i32(3, 4).short()),
+               dict(plan=K.RaggedPlan(2, 8, "cpu"))):
+        args = {**dict(cached=i32(3), new_tokens=i32(3), block_table=table, page_size=16, free_pages=free, free_count=one,
+                       free_left=i32(1), plan=plan), **kw}
+        with pytest.raises(ValueError, match="expected"):
+            K.kvc_ragged_plan(**args)
+    for a, b in ((f32(4, 8), f32(5, 8)), (f32(4, 8).double(), f32(4, 8)), (f32(4, 8), f32(4, 8).half())):
+        with pytest.raises(ValueError, match="expected"):
+            K.kvc_rope_tables(a, b)
+
+
+def test_append_binding_refuses(K):
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    with pytest.raises(ValueError, match="CUDA"):
+        K.kvc_ragged_append(bf(4, 4, 64), bf(8, 2, 16, 64), bf(8, 2, 16, 64), bf(4, 4, 64), bf(4, 2, 64), bf(4, 2, 64),
+                            torch.zeros(4, dtype=torch.int32), torch.zeros(4, dtype=torch.int32))
+    x = bf(4, 8, 64)
+    assert "stride" in inspect.getsource(K._token_rows)
+    with pytest.raises(ValueError):
+        K._token_rows("q", x[:, ::2], 4, 4, 64, torch.bfloat16)   # heads that are not dense
+    with pytest.raises(ValueError):
+        K._token_rows("q", x, 4, 4, 64, torch.bfloat16)           # another number of heads
+    with pytest.raises(ValueError):
+        K._token_rows("q", x, 4, 8, 64, torch.float16)
+
+
+def test_struct_of_lengths_is_five_addresses(K):
+    assert ctypes.sizeof(K.KvcLengths) == 5 * ctypes.sizeof(ctypes.c_void_p)
