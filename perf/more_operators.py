@@ -224,10 +224,11 @@ def _kept(s, make):
 
 def _own_plan(s):
     c = s["case"]
-    K, plan = _kept(s, lambda K: [K.RaggedPlan(c["batch"], c["tokens"], DEV)])
+    # room for the longest prompts: a request whose tokens find no row is rejected
+    K, plan = _kept(s, lambda K: [K.RaggedPlan(c["batch"], max(c["tokens"], c["batch"] + c["prompts"] * c["longest"]), DEV)])
     K.kvc_page_release(s["released"], s["table"], c["page"], s["free"], s["count"], s["between"])
     K.kvc_ragged_plan(s["cached"], s["new"], s["table"], c["page"], s["free"], s["between"], s["left"], plan)
-    return [plan.offsets, plan.positions, plan.slots, plan.lengths.buf, s["table"], s["free"], s["left"]]
+    return [plan.offsets, plan.positions[:c["tokens"]], plan.slots[:c["tokens"]], plan.lengths.buf, s["table"], s["free"], s["left"]]
 
 
 def _own_tables(s):
