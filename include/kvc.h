@@ -1030,6 +1030,42 @@ kvc_status kvc_ragged_append(void *q_out, void *k_pool, void *v_pool, const void
                              const float *rope_cos, const float *rope_sin, int64_t rope_max_pos,
                              int32_t *dev_status, void *stream);
 
+/*
+ * kvc_gqa_ragged -- the attention of the new tokens of a packed batch after their
+ * K and V are in the cache (kvc_ragged_append): the token at position p of request
+ * b sees the rows of that request's positions 0..p, with a local window W > 0 those
+ * less than W positions back.  Prompts, chunks of prompts over what is cached and
+ * single tokens go together in one call.
+ * out, q     device [tokens, q_heads, head_dim], q rotated; out may not overlap
+ *            what is read (KVC_ERR_SHAPE).
+ * offsets, len  as kvc_ragged_plan wrote them.  A request with lengths -1 keeps its
+ *            rows of `out`, as do rows behind the last request's.  So does one whose
+ *            offsets are outside [0, tokens] or not total_abs - past_abs apart
+ *            (KVC_DEV_SEQLEN_RANGE), or with more tokens than its row of the table
+ *            has room for (KVC_DEV_CAPACITY).  A page id outside the pool among the
+ *            rows that are read sets KVC_DEV_INDEX_OOB (that request's output is then
+ *            undefined).
+ * page_size  a multiple of 16 (KVC_ERR_SHAPE).
+ * KVC_BF16/KVC_F16, head_dim 64, 128 or 256, q_heads / kv_heads any whole number up
+ * to 16, batch <= 65535 (KVC_ERR_UNSUPPORTED); scale 0 -> 1 / sqrt(head_dim).
+ * Beside the result, the softmax weights are rounded to the cache's type.
+ * A NaN or an infinity in a column of a V row that a token sees makes that column of
+ * its output NaN, whatever the row's weight; a NaN in a K row that it sees makes all
+ * of them NaN.  What it does not see may hold anything.
+ * workspace  device, kvc_gqa_ragged_workspace_size(...) bytes on the current device,
+ *            256-byte aligned.  Calls that may overlap on the GPU need their own.
+ */
+kvc_status kvc_gqa_ragged(void *out, const void *q, const void *k_pool, const void *v_pool,
+                          const int32_t *offsets, const int32_t *block_table, int max_pages,
+                          int64_t n_pool_pages, int page_size, kvc_lengths len, int batch,
+                          int tokens, int q_heads, int kv_heads, int head_dim, int dtype,
+                          int local_window_size, float scale, void *workspace,
+                          size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* Bytes of workspace kvc_gqa_ragged needs for these sizes (0 on bad sizes). */
+size_t kvc_gqa_ragged_workspace_size(int batch, int tokens, int q_heads, int kv_heads,
+                                     int head_dim);
+
 /* Human-readable name of a status code (static storage). */
 const char *kvc_status_string(kvc_status status);
 

@@ -17,7 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libkvc.so")
 SOURCES = ["kvc_scatter.cu", "kvc_cache.cu", "kvc_decode.cu", "kvc_prefill.cu", "kvc_quant.cu",
-           "kvc_sparse.cu", "kvc_tree.cu", "kvc_ragged.cu"]
+           "kvc_sparse.cu", "kvc_tree.cu", "kvc_ragged.cu",
+           "kvc_ragged_attn.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("kvc_common.cuh", "kvc_flat.cuh", "kvc_tc.cuh")] + [
            os.path.join(ROOT, "include", "kvc.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -47,6 +47,7 @@ EXPORTS = ("kvc_tensor_scatter", "kvc_seq_lengths", "kvc_window_append", "kvc_gq
            "kvc_gqa_decode_sparse_workspace_size", "kvc_tree_mask", "kvc_tree_append",
            "kvc_gqa_tree", "kvc_gqa_tree_workspace_size", "kvc_tree_commit",
            "kvc_page_release", "kvc_ragged_plan", "kvc_rope_tables", "kvc_ragged_append",
+           "kvc_gqa_ragged", "kvc_gqa_ragged_workspace_size",
            "kvc_status_string", "kvc_abi_version")
 KVC_DECODE_STATIC_SCRATCH_BYTES = 16 << 20
 KVC_PAGE_QUANT = 0x40000000  # block-table flag: the entry names an int8 page
@@ -152,6 +153,8 @@ def library() -> ctypes.CDLL:
             "kvc_rope_tables": [P, P, I64, I64, I, DBL, I, DBL, I64, DBL, DBL, DBL, P],
             "kvc_ragged_append": [P, P, P, P, P, P, I64, I64, I64, P, P, F, P, P, I, I, I, I64, I, I, I, I,
                                   I, P, P, I64, P, P],
+            "kvc_gqa_ragged": [P, P, P, P, P, P, I, I64, I, L, I, I, I, I, I, I, I, F, P, SZ, P, P],
+            "kvc_gqa_ragged_workspace_size": [I, I, I, I, I],
             "kvc_status_string": [I],
             "kvc_abi_version": [],
         }
@@ -166,6 +169,7 @@ def library() -> ctypes.CDLL:
         lib.kvc_gqa_decode_quant_workspace_size.restype = SZ
         lib.kvc_gqa_decode_sparse_workspace_size.restype = SZ
         lib.kvc_gqa_tree_workspace_size.restype = SZ
+        lib.kvc_gqa_ragged_workspace_size.restype = SZ
         lib.kvc_status_string.restype = ctypes.c_char_p
         _lib = lib
     return _lib
@@ -905,3 +909,34 @@ def kvc_ragged_append(q_out, k_pool, v_pool, q, k, v, positions, slots, rope=Non
         a, b, c, qa, ka, va, qs, ks, vs, wq, wk, eps, d, e, T, Hq, H, n_pages, ps, D,
         _dtype_code(q), turned, int(bool(interleaved)), cs, sn, rmax, st, _stream(stream)))
     return q_out
+
+
+def ragged_workspace(q, k_pool, batch):
+    """Workspace for kvc_gqa_ragged."""
+    T, Hq, D = q.shape
+    n = library().kvc_gqa_ragged_workspace_size(batch, T, Hq, k_pool.shape[1], D)
+    return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
+def kvc_gqa_ragged(out, q, k_pool, v_pool, block_table, offsets, lengths, local_window_size=0,
+                   scale=0.0, workspace="auto", status=None, stream=None):
+    """Attention of the packed new tokens' rotated queries [tokens, Hq, D] over the pages of
+    their requests (include/kvc.h); offsets and lengths as a RaggedPlan holds them."""
+    n_pages, H, ps, D = pool = k_pool.shape
+    T, Hq, _ = shape = q.shape
+    B, max_pages = block_table.shape
+    if shape[2] != D or q.dtype is not k_pool.dtype:
+        _same("q", q, (T, Hq, D), k_pool.dtype)
+    _same("out", out, shape, q.dtype)
+    _same("v_pool", v_pool, pool, q.dtype)
+    _same("block_table", block_table, (B, max_pages), torch.int32)
+    _same("offsets", offsets, (B + 1,), torch.int32)
+    if isinstance(workspace, str):
+        workspace = _made_on(stream, ragged_workspace, q, k_pool, B)
+    a, b, c, d, e, f, ws, st = _addresses(out, q, k_pool, v_pool, offsets, block_table, workspace,
+                                          status)
+    _check("kvc_gqa_ragged", library().kvc_gqa_ragged(
+        a, b, c, d, e, f, max_pages, n_pages, ps, _lengths_of(lengths, B), B, T, Hq, H, D,
+        _dtype_code(q), local_window_size, scale, ws, 0 if workspace is None else workspace.nbytes,
+        st, _stream(stream)))
+    return out

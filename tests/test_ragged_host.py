@@ -95,6 +95,29 @@ def test_ragged_append(K):
     assert f(tokens=0, q_out=None) == 0
 
 
+def test_gqa_ragged(K):
+    lib = K.library()
+    f = caller(lib.kvc_gqa_ragged, out=FAKE, q=1 << 24, k=1 << 30, v=1 << 31, offsets=FAKE, table=FAKE, max_pages=4, pool=8, page=16,
+               len=lengths(K), batch=2, tokens=4, q_heads=4, kv_heads=2, dim=128, dtype=1, window=0, scale=0.0, ws=FAKE, bytes=1 << 40,
+               status=None, stream=None)
+    assert f(dtype=9) == 3 and f(dtype=0) == 5
+    assert f(batch=-1) == 2 and f(tokens=-1) == 2 and f(q_heads=0) == 2 and f(kv_heads=0) == 2 and f(q_heads=5) == 2
+    assert f(max_pages=0) == 2 and f(pool=0) == 2 and f(page=0) == 2 and f(page=24) == 2 and f(page=8) == 2
+    assert f(dim=96) == 5 and f(q_heads=34) == 5 and f(batch=65536) == 5
+    assert f(max_pages=1 << 28) == 6 and f(pool=1 << 27) == 6 and f(pool=1 << 26, kv_heads=4) == 6 and f(tokens=1 << 30) == 6
+    for name in ("out", "q", "k", "v", "offsets", "table"):
+        assert f(**{name: None}) == 1, name
+    assert f(len=lengths(K, None)) == 1
+    for name in ("out", "q", "k", "v"):
+        assert f(**{name: (1 << 33) + 8}) == 4, name
+    assert f(out=1 << 24) == 2 and f(out=(1 << 24) + 64) == 2 and f(out=1 << 30) == 2 and f(out=1 << 31) == 2
+    assert f(ws=None) == 8 and f(bytes=0) == 8 and f(ws=FAKE + 16) == 4
+    assert f(batch=0, out=None) == 0 and f(tokens=0, out=None) == 0
+    size = lib.kvc_gqa_ragged_workspace_size
+    assert size(0, 1, 4, 2, 64) == 0 and size(1, 0, 4, 2, 64) == 0 and size(1, 1, 5, 2, 64) == 0 and size(1, 1, 4, 2, 0) == 0
+    assert size(1, 1, 4, 2, 64) > 0
+
+
 def test_binding_refuses_other_shapes(K, monkeypatch):
     """The library gets sizes from one tensor of each kind: the binding compares the others.  (Tensors of
     the meta device stand in for the GPU's.)"""
@@ -115,6 +138,13 @@ def test_binding_refuses_other_shapes(K, monkeypatch):
                        free_left=i32(1), plan=plan), **kw}
         with pytest.raises(ValueError, match="expected"):
             K.kvc_ragged_plan(**args)
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    good = dict(out=bf(5, 4, 64), q=bf(5, 4, 64), k_pool=bf(8, 2, 16, 64), v_pool=bf(8, 2, 16, 64), block_table=table,
+                offsets=i32(4), lengths=K.Lengths(3, "cpu"), workspace=i32(64))
+    for kw in (dict(out=bf(4, 4, 64)), dict(q=bf(5, 4, 64).half()), dict(q=bf(5, 4, 32)), dict(v_pool=bf(8, 2, 32, 64)),
+               dict(offsets=i32(3)), dict(offsets=i32(4).long()), dict(block_table=table.long()), dict(out=bf(5, 4, 64).float())):
+        with pytest.raises(ValueError, match="expected"):
+            K.kvc_gqa_ragged(**{**good, **kw})
     for a, b in ((f32(4, 8), f32(5, 8)), (f32(4, 8).double(), f32(4, 8)), (f32(4, 8), f32(4, 8).half())):
         with pytest.raises(ValueError, match="expected"):
             K.kvc_rope_tables(a, b)
