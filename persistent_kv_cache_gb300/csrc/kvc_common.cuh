@@ -397,9 +397,10 @@ bool encode_4d_heads_sw128(CUtensorMap *map, const void *base, uint64_t heads, u
 // the same tensor as (span, rows, heads, column blocks): a box of (span,
 // box_rows, box_heads, every block) lands as [blocks][box_heads][box_rows]
 // [128 B], i.e. column block by column block, the heads' rows stacked
+// (box_blocks: that many blocks a box instead of every one)
 bool encode_4d_blocks_sw128(CUtensorMap *map, const void *base, uint64_t heads, uint64_t rows,
                             uint64_t cols, uint32_t elem_bytes, uint32_t box_rows,
-                            uint32_t box_heads, CUtensorMapDataType type);
+                            uint32_t box_heads, CUtensorMapDataType type, uint32_t box_blocks = 0);
 
 } // namespace kvc_host
 

@@ -1,113 +1,1201 @@
 // kvc_ragged_attn.cu -- attention of a packed batch's new tokens over a paged
 // cache ("Persistent KV Cache and Decode Performance Roadmap", "Phase 1" and
-// "Phase 2": streaming online softmax, pages read through a page table).
+// "Phase 2": streaming online softmax, a KV block read once per query-head
+// group, pages read through a page table).
+//
+// The queries of one kv head's G heads at `toks` = 128 / G consecutive tokens
+// are the 128 rows of a query tile (row m: token m / G, head m % G, as they lie in
+// memory).  An item is one or, with head_dim <= 128, two such tiles of one
+// (request, kv head), and streams the keys that its last token sees past the
+// tensor cores in tiles of 128.
+//
+//   ragged_attn_kernel   the attention; every CTA (one an SM) takes the same share
+//                        of the keys of all items, in segments of one item each
+//   ragged_merge_kernel  joins the items that several CTAs worked on
 #include <algorithm>
+#include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "kvc_common.cuh"
+#include "kvc_tc.cuh"
 
 namespace {
 
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kBM = 128, kBN = 128;
+constexpr int kThreads = 32 * 12;
+constexpr int kSoftmax = 256;    // threads of the softmax warps
+constexpr float kRescale = 8.f;  // log2 units by which a score may exceed the reference maximum
+constexpr int kItemCost = 512;   // keys that stand for what an item costs beside its keys
+constexpr int kMaxRequests = 65535;
+
 struct RaggedArgs {
     void *out;
-    const void *q, *k, *v;
     const int32_t *offsets, *table;
     int max_pages, page_size;
     int64_t n_pool;
     kvc_lengths len;
     int batch, tokens, q_heads, kv_heads, group;
+    int toks, item;  // tokens of a query tile, of an item
+    int box_rows;    // rows of a TMA box of K or V
     int window;
-    float scale;
+    float scale_log2;
+    float *ws_o, *ws_m, *ws_l;  // partial results: [2 * grid * tiles][D / 4][128][4], [..][128]
+    int4 *split;  // [grid] the item of which a CTA has the first keys but not the last: request, kv head, item,
+                  // 2 * parts + slot of its own part (parts 0: there is none)
     int32_t *status;
 };
 
-// The new tokens of request b: how many, the first one's row and position.  0 for
-// a request that was rejected; one whose lengths and offsets do not go together
-// is too.
-__device__ __forceinline__ int request(const RaggedArgs &a, int b, int &row0, int &P, uint32_t &bad)
+// --------------------------------------------------------------------------
+// the items and their shares
+// --------------------------------------------------------------------------
+
+// The new tokens of request b.  n = 0 for a request that was rejected; one whose
+// lengths and offsets do not go together is too.
+struct Request {
+    int row0, P, n, items;
+};
+__device__ __forceinline__ Request request(const RaggedArgs &a, int b, uint32_t &bad)
 {
-    const int o0 = a.offsets[b], o1 = a.offsets[b + 1], T = a.len.total_abs[b];
-    row0 = o0;
-    P = a.len.past_abs[b];
+    const int o0 = a.offsets[b], o1 = a.offsets[b + 1], T = a.len.total_abs[b], L = a.len.cache_total[b];
+    Request r;
+    r.row0 = o0;
+    r.P = a.len.past_abs[b];
+    r.n = 0;
     bad = 0;
-    if (a.len.cache_total[b] < 0 || P < 0)
-        return 0;
-    if (T < P || o0 < 0 || o1 < o0 || o1 > a.tokens || T - P != o1 - o0)
-        bad = KVC_DEV_SEQLEN_RANGE;
-    else if (T > (int64_t)a.max_pages * a.page_size)
-        bad = KVC_DEV_CAPACITY;
-    return bad ? 0 : o1 - o0;
+    if (L >= 0 && r.P >= 0) {
+        if (T < r.P || o0 < 0 || o1 < o0 || o1 > a.tokens || T - r.P != o1 - o0)
+            bad = KVC_DEV_SEQLEN_RANGE;
+        else if (T > (int64_t)a.max_pages * a.page_size)
+            bad = KVC_DEV_CAPACITY;
+        else
+            r.n = o1 - o0;
+    }
+    r.items = (r.n + a.item - 1) / a.item;
+    return r;
 }
 
-// A block a token and kv head, a warp a query head, the keys one by one.
-template <typename T, int D>
-__global__ void __launch_bounds__(512)
-ragged_attn_kernel(const RaggedArgs a)
+// first key row that item i's tokens see, and one past the last
+__device__ __forceinline__ void key_range(const RaggedArgs &a, const Request &r, int i, int &lo, int &hi)
 {
-    constexpr int PER = D / 32;
-    const int t = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, head = h * a.group + (threadIdx.x >> 5);
-    int b = 0, n = 0, row0 = 0, P = 0;
-    if (t == 0 && h == 0)
-        for (int i = threadIdx.x; i < a.batch; i += blockDim.x) {
+    lo = a.window > 0 ? max(0, r.P + i * a.item - a.window + 1) : 0;
+    hi = r.P + min(r.n, (i + 1) * a.item);
+}
+
+// keys of the items before j: the sum over i < j of hi - lo, in closed form
+__device__ __forceinline__ int64_t keys_before(const RaggedArgs &a, const Request &r, int j)
+{
+    const int64_t K = a.item, full = min(j, r.n / a.item);
+    int64_t sum = (int64_t)j * r.P + K * full * (full + 1) / 2 + (j - full) * (int64_t)r.n;
+    if (a.window > 0) {
+        const int64_t i0 = r.P >= a.window ? 0 : ((int64_t)a.window - r.P + K - 1) / K;  // first with lo > 0
+        if (j > i0) {
+            const int64_t count = j - i0;
+            sum -= count * ((int64_t)r.P - a.window + 1) + K * (i0 + j - 1) * count / 2;
+        }
+    }
+    return sum;
+}
+
+// All items laid end to end (request, then kv head, then item; each as long as its
+// keys and `cost`) are one line, cut into equal shares: every CTA gets the
+// same work whatever the lengths, and the split is the same on every run.
+struct Line {
+    int grid, cost;
+    int64_t each, longer;  // shares [0, longer) are one longer than `each`
+    __device__ __forceinline__ int64_t begin(int64_t c) const { return c * each + min(c, longer); }
+    __device__ __forceinline__ int of(int64_t x) const
+    {
+        const int64_t head = longer * (each + 1);
+        return (int)(x < head ? x / (each + 1) : longer + (x - head) / each);
+    }
+};
+
+// A row of t key tiles is done soonest by about sqrt(7 t) CTAs, since joining costs
+// each part about half a tile's time: with so few rows that this leaves CTAs
+// over, rows begin with a CTA each and cost nothing beside their keys.
+__device__ __forceinline__ Line make_line(int64_t keys, int64_t rows, int grid)
+{
+    Line l;
+    l.cost = kItemCost;
+    const float t = fmaxf(1.f, (float)keys / (128.f * (float)max(rows, (int64_t)1)));
+    const int64_t few = rows * (int64_t)ceilf(sqrtf(7.f * t));
+    l.grid = grid;
+    if (few <= grid) {
+        l.grid = (int)max(few, (int64_t)1);
+        l.cost = 0;
+    }
+    int64_t total = keys + rows * l.cost;
+    // no share shorter than a tile: no segment of a row between two others is empty
+    l.grid = (int)max((int64_t)1, min((int64_t)l.grid, total / kBN));
+    l.each = total / l.grid;
+    l.longer = total % l.grid;
+    return l;
+}
+
+struct Segment {
+    int b, h, i;
+    int row0, P, n;    // of the request
+    int lo, t0, t1, tiles;  // key tiles [t0, t1) of `tiles` from key row lo on
+    int64_t end;            // of the item on the line
+};
+
+// The segments of a CTA's share, one at a time.
+struct Walk {
+    int64_t x, x_end, base;  // base: of the item at (b, h, i)
+    int b, h, i;
+    Request r;
+    __device__ __forceinline__ bool next(const RaggedArgs &a, int cost, Segment &s)
+    {
+        while (x < x_end) {
+            while (i >= r.items) {
+                i = 0;
+                if (r.items == 0 || ++h == a.kv_heads) {
+                    h = 0;
+                    ++b;
+                    uint32_t bad;
+                    r = request(a, b, bad);
+                }
+            }
+            int lo, hi;
+            key_range(a, r, i, lo, hi);
+            const int64_t keys = hi - lo, end = base + keys + cost;
+            s.b = b;
+            s.h = h;
+            s.i = i;
+            s.row0 = r.row0;
+            s.P = r.P;
+            s.n = r.n;
+            s.lo = lo & ~(a.box_rows - 1);
+            s.tiles = (hi - s.lo + kBN - 1) / kBN;
+            s.end = end;
+            // the keys that stand for the item's cost hold none
+            const int64_t p0 = x - base - cost, p1 = x_end - base - cost;
+            s.t0 = p0 <= 0 ? 0 : (int)(p0 / kBN);
+            s.t1 = x_end >= end ? s.tiles : p1 <= 0 ? 0 : (int)(p1 / kBN);
+            if (x_end >= end) {
+                x = base = end;
+                ++i;
+            } else {
+                x = x_end;
+            }
+            if (s.t1 > s.t0)
+                return true;
+        }
+        return false;
+    }
+};
+
+// The CTA's share: the requests' keys and items summed by groups of 32 (a warp a
+// group), the sums in shared memory, then the group, the request and the item of the
+// share's first unit.  `scratch` holds 12 bytes a group.
+__device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch, int grid, Walk &w)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, groups = (a.batch + 31) / 32;
+    int64_t *keys = reinterpret_cast<int64_t *>(scratch);
+    int *rows = reinterpret_cast<int *>(scratch + 8 * (size_t)groups);
+    for (int g = warp; g < groups; g += kThreads / 32) {
+        const int b = 32 * g + lane;
+        int64_t k = 0;
+        int n = 0;
+        if (b < a.batch) {
             uint32_t bad;
-            request(a, i, row0, P, bad);
-            if (bad)
+            const Request r = request(a, b, bad);
+            if (bad && blockIdx.x == 0)
                 kvc::raise_status(a.status, bad);
+            k = keys_before(a, r, r.items);
+            n = r.items;
         }
-    for (; b < a.batch; ++b) {
-        uint32_t bad;
-        n = request(a, b, row0, P, bad);
-        if (n && t >= row0 && t < row0 + n)
-            break;
-    }
-    if (b == a.batch)
-        return;
-    const int pos = P + t - row0, first = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-    float q[PER], o[PER], m = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int e = 0; e < PER; ++e) {
-        q[e] = kvc::Elem<T>::to_f32(static_cast<const T *>(a.q)[((int64_t)t * a.q_heads + head) * D + lane + 32 * e]);
-        o[e] = 0.f;
-    }
-    for (int r = first; r <= pos; ++r) {
-        const int64_t id = a.table[(int64_t)b * a.max_pages + r / a.page_size];
-        if (id < 0 || id >= a.n_pool) {
-            if (lane == 0)
-                kvc::raise_status(a.status, KVC_DEV_INDEX_OOB);
-            continue;
+        for (int d = 16; d; d >>= 1) {
+            k += __shfl_xor_sync(0xffffffffu, k, d);
+            n += __shfl_xor_sync(0xffffffffu, n, d);
         }
-        const int64_t at = ((id * a.kv_heads + h) * a.page_size + r % a.page_size) * D + lane;
-        float s = 0.f;
+        if (lane == 0) {
+            keys[g] = k;
+            rows[g] = n;
+        }
+    }
+    __syncthreads();
+    int64_t k = 0, n = 0;
+    for (int g = lane; g < groups; g += 32) {
+        k += keys[g];
+        n += rows[g];
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        k += __shfl_xor_sync(0xffffffffu, k, d);
+        n += __shfl_xor_sync(0xffffffffu, n, d);
+    }
+    const Line line = make_line(k * a.kv_heads, n * a.kv_heads, grid);
+    w.x = w.x_end = 0;
+    if (n > 0 && blockIdx.x < line.grid) {
+        w.x = line.begin(blockIdx.x);
+        w.x_end = line.begin(blockIdx.x + 1);
+    }
+    if (w.x < w.x_end) {
+        // the group
+        int64_t before = 0;
+        int at = 0;
+        for (int g0 = 0; g0 < groups; g0 += 32) {
+            const int g = g0 + lane;
+            const int64_t len = g < groups ? (keys[g] + (int64_t)rows[g] * line.cost) * a.kv_heads : 0;
+            int64_t inc = len;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, inc, d);
+                if (lane >= d)
+                    inc += y;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, before + inc > w.x);
+            if (past) {
+                const int first = __ffs(past) - 1;
+                at = g0 + first;
+                before += __shfl_sync(0xffffffffu, inc - len, first);
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        // the request
+        {
+            const int b = 32 * at + lane;
+            uint32_t bad;
+            Request r{0, 0, 0, 0};
+            if (b < a.batch)
+                r = request(a, b, bad);
+            const int64_t len = (keys_before(a, r, r.items) + (int64_t)r.items * line.cost) * a.kv_heads;
+            int64_t inc = len;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, inc, d);
+                if (lane >= d)
+                    inc += y;
+            }
+            const int first = __ffs(__ballot_sync(0xffffffffu, before + inc > w.x)) - 1;
+            w.b = 32 * at + first;
+            before += __shfl_sync(0xffffffffu, inc - len, first);
+            w.r.row0 = __shfl_sync(0xffffffffu, r.row0, first);
+            w.r.P = __shfl_sync(0xffffffffu, r.P, first);
+            w.r.n = __shfl_sync(0xffffffffu, r.n, first);
+            w.r.items = __shfl_sync(0xffffffffu, r.items, first);
+        }
+        // the kv head and the item: the last that begins at x or before it
+        const int64_t head = keys_before(a, w.r, w.r.items) + (int64_t)w.r.items * line.cost;
+        w.h = (int)((w.x - before) / head);
+        before += w.h * head;
+        int low = 0, count = w.r.items;  // among [low, low + count)
+        while (count > 1) {
+            const int step = (count + 31) / 32, j = low + lane * step;
+            const bool begun = lane * step < count && before + keys_before(a, w.r, j) + (int64_t)j * line.cost <= w.x;
+            const int last = 31 - __clz(__ballot_sync(0xffffffffu, begun));
+            low += last * step;
+            count = min(step, count - last * step);
+        }
+        w.i = low;
+        w.base = before + keys_before(a, w.r, low) + (int64_t)low * line.cost;
+    }
+    __syncthreads();
+    return line;
+}
+
+// --------------------------------------------------------------------------
+// the attention
+// --------------------------------------------------------------------------
+//
+//   TMEM columns  an output O of D columns and a buffer S of 128 for each of two
+//                 streams (head_dim 256: one O, two buffers S)
+//   shared        queries (two tiles; 256: one) | ring of slabs of K and V
+//   warp 0        TMA of the queries, the score products
+//   warps 1, 2    TMA of K and of V into one ring in the order of use
+//   warp 3        the output products
+//   warps 4-11    softmax and output, a warp a quarter of the 128 TMEM lanes
+//
+// head_dim <= 128: the warps 4-7 and 8-11 are two streams, each with a score buffer
+// and an output of its own, so that one's softmax runs while the other's products
+// do.  An item of two query tiles gives each stream one of them, over the same keys
+// (read once for both); an item of one tile (a decoding request, the end of a prompt)
+// gives each stream every second key tile, and the two results are joined
+// in tensor memory at the end.  A thread has a row, and writes the weights as 16-bit
+// pairs over the scores that it has read.
+// head_dim 256: no room for two outputs; two threads a row (each half of the
+// columns), the two score buffers used in turn.
+//
+// Only key tiles that hold the last tokens' own rows, or that a window's edge cuts,
+// are masked ("cut" tiles).  A NaN or an infinity in a column of V makes that column of
+// the output NaN for the rows that see it, and for no other.  In whole tiles the
+// products do that by themselves.  In cut tiles 0 x NaN would reach the rows that
+// do not see it, and a page's rows behind the request's last may hold anything:
+// there the softmax warps look through V in shared memory, write down for each row
+// the columns of such values that it sees, and put zeros in their place.
+
+template <int D> struct Smem {
+    static constexpr int TILES = D <= 128 ? 2 : 1;  // query tiles, streams
+    static constexpr int HALVES = 3 - TILES;        // threads of a row
+    static constexpr int KR = D <= 128 ? 128 : 64;  // rows of a slab
+    static constexpr int SPT = kBN / KR;            // slabs of a tile of K (or V)
+    static constexpr int Q_TILE = kBM * D * 2, Q_BYTES = TILES * Q_TILE;
+    static constexpr int SLAB = KR * D * 2;
+    static constexpr int BUDGET = 227 * 1024;
+    static constexpr int NBAR = 10;  // beside the ring's
+    static constexpr int MISC = (2 * 12 + NBAR) * 8 + 16 + 4 * kBM * 4 + 16;
+    static constexpr int FIT = (BUDGET - Q_BYTES - MISC) / SLAB;
+    static constexpr int NSLAB = FIT < 12 ? FIT : 12;
+    static constexpr int RING_OFF = Q_BYTES;
+    static constexpr int BAR_OFF = RING_OFF + NSLAB * SLAB;
+    // full[NSLAB], empty[NSLAB], s_full[2], p_full[2], o_done[2], q_full, q_empty, drain[2]
+    static constexpr int MISC_OFF = BAR_OFF + (2 * NSLAB + NBAR) * 8;
+    static constexpr int RED_OFF = (MISC_OFF + 8 + 15) / 16 * 16;  // 4 x 128 floats: maxima and sums that change hands
+    static constexpr int BAD_OFF = RED_OFF + 4 * kBM * 4;
+    static constexpr int TOTAL = BAD_OFF + 16;
+    static_assert(TOTAL <= BUDGET && NSLAB >= 2 * SPT + 1, "a tile of K, one of V and the next slab must fit");
+    static_assert(NSLAB * SLAB >= 12 * ((kMaxRequests + 31) / 32), "the groups' sums lie where the ring will");
+    static constexpr uint32_t COL_S = TILES * D, TMEM_COLS = 512;
+    static_assert(COL_S + 2 * kBN <= TMEM_COLS, "tensor memory");
+};
+
+// Registers: 384 threads are launched with 168 each; the four warps that move data
+// and issue products keep 88, the softmax warps, whose scores stay in registers
+// from the maximum to the exponential, take 208 (4 x 32 x 88 + 8 x 32 x 208 = 384 x 168).
+constexpr int kLaunchRegs = 168, kFewRegs = 88, kManyRegs = 208;
+static_assert(128 * kFewRegs + 256 * kManyRegs <= kThreads * kLaunchRegs, "a block has no more registers than at launch");
+
+// The ring holds, for a segment of n tiles, K_0, K_1, then V_j and K_{j+2} while
+// there is one, then the last V's: the places of K_j and of V_j in that order.
+__device__ __forceinline__ int k_group(int j) { return j < 2 ? j : 2 * j - 1; }
+__device__ __forceinline__ int v_group(int j, int n)
+{
+    const int lead = n < 2 ? n : 2, paired = n - lead;
+    return j < paired ? lead + 2 * j : lead + paired + j;
+}
+
+// the 16-bit halves of w that are NaN or infinite, as 0xffff each
+template <typename T> __device__ __forceinline__ uint32_t not_finite(uint32_t w)
+{
+    constexpr uint32_t ex = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
+    return __vcmpeq2(w & ex, ex);
+}
+
+// What the streams do in a segment: `two` query tiles over the same keys, the first
+// of which needs the first n0 of the tiles only; or one, whose tiles alternate.
+struct Streams {
+    bool two;
+    int n, n0;
+    template <int TILES>
+    static __device__ __forceinline__ Streams of(const RaggedArgs &a, const Segment &s)
+    {
+        Streams r;
+        const int first = s.i * a.item;  // token
+        r.n = s.t1 - s.t0;
+        r.two = TILES == 2 && s.n - first > a.toks;
+        // the last token of the first tile sees the rows up to its own
+        r.n0 = r.two ? max(0, min(r.n, (s.P + first + a.toks - s.lo + kBN - 1) / kBN - s.t0)) : r.n;
+        return r;
+    }
+    // does stream k work on tile j, and is it the tile's last one
+    __device__ __forceinline__ bool has(int k, int j) const { return two ? k == 1 || j < n0 : (j & 1) == k; }
+    __device__ __forceinline__ int tiles(int k) const { return two ? (k ? n : n0) : (n + 1 - k) >> 1; }
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                   const __grid_constant__ CUtensorMap tmap_v, const RaggedArgs a)
+{
+    using SM = Smem<D>;
+    using kvc_tc::wait_or_abort;
+    constexpr int NSLAB = SM::NSLAB, SPT = SM::SPT, KR = SM::KR, TILES = SM::TILES, HALVES = SM::HALVES;
+    constexpr uint32_t AB = std::is_same<T, __half>::value ? 0u : 1u;
+    constexpr uint32_t IDESC_S = kvc_tc::f16_idesc(AB, 0, kBM, KR);
+    constexpr uint32_t IDESC_O = kvc_tc::f16_idesc(AB, 1, kBM, D);
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    {
+        // the swizzled tiles need a 1024-byte aligned base
+        uint32_t dyn;
+        asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(dyn));
+        if ((uint32_t)(smem - smem_raw) + SM::TOTAL > dyn) {
+            if (threadIdx.x == 0) {
+                kvc::raise_status(a.status, KVC_DEV_CAPACITY);
+                a.split[blockIdx.x] = make_int4(0, 0, 0, 0);
+            }
+            return;
+        }
+    }
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + SM::BAR_OFF), *empty = full + NSLAB,
+             *s_full = full + 2 * NSLAB, *p_full = s_full + 2, *o_done = s_full + 4, *q_full = s_full + 6,
+             *q_empty = s_full + 7, *drain = s_full + 8;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + SM::MISC_OFF);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + SM::MISC_OFF + 4);
+
+    kvc::grid_dep_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NSLAB; ++i) {
+            kvc::mbar_init(&full[i], 1);
+            kvc::mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            kvc::mbar_init(&s_full[i], 1);
+            kvc::mbar_init(&p_full[i], TILES == 2 ? 4 : 8);
+            kvc::mbar_init(&o_done[i], 1);
+        }
+        kvc::mbar_init(q_full, 1);
+        kvc::mbar_init(q_empty, 1);
+        kvc::mbar_init(&drain[0], 1);
+        kvc::mbar_init(&drain[1], 1);
+        *abort_flag = 0;
+        for (int i = 0; i < 4; ++i)
+            reinterpret_cast<uint32_t *>(smem + SM::BAD_OFF)[i] = 0;
+        kvc::fence_mbar_init();
+    }
+    if (warp == 0) {
+        kvc_tc::tmem_alloc(tmem_slot, SM::TMEM_COLS);
+        kvc_tc::fence_before();
+    }
+    Walk walk;
+    const Line line = find_share(a, smem + SM::RING_OFF, gridDim.x, walk);
+    // (the sums were read from where the ring's first slabs will be written)
+    kvc::fence_proxy_async_smem();
+    __syncthreads();
+    kvc_tc::fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t smem_base = kvc::smem_u32(smem);
+    // each role looks one segment ahead, so that the lengths are there when it gets to it
+    Segment cur, nxt;
+    bool more = walk.next(a, line.cost, cur);
+
+    if (warp < 4) {
+        kvc_tc::regs_down<kFewRegs>();
+        if (warp == 1 || warp == 2) {
+            // ======================= TMA producers of K and of V =======================
+            // Each lane finds the place of one of the next 32 boxes' rows, and issues one of the slab's boxes.
+            const bool mine_v = warp == 2;
+            const CUtensorMap *tmap = mine_v ? &tmap_v : &tmap_k;
+            if (lane == 0)
+                kvc::tma_prefetch_desc(tmap);
+            if (!mine_v && lane == 0)
+                a.split[blockIdx.x] = make_int4(0, 0, 0, 0);
+            int q0 = 0;  // slabs of the segments before
+            bool ok = true, first_segment = true;
+            const int pieces = KR / a.box_rows;  // of a slab's rows: a power of two up to 8
+            uint32_t filled = 0, phase = 0;  // slots that this warp has filled, with the parity of the last time
+            while (ok && more) {
+                const int nt = cur.t1 - cur.t0;
+                const uint32_t end = (uint32_t)cur.P + min(cur.n, (cur.i + 1) * a.item), first = (uint32_t)cur.lo + cur.t0 * kBN;
+                const bool again = walk.next(a, line.cost, nxt);
+                if (!mine_v && lane == 0 && cur.t0 == 0 && nt != cur.tiles)
+                    a.split[blockIdx.x] = make_int4(cur.b, cur.h, cur.i,
+                                                    2 * (line.of(cur.end - 1) - (int)blockIdx.x + 1) + (first_segment ? 0 : 1));
+                first_segment = false;
+                int32_t place = -1;
+                for (int u = 0; u < SPT * nt; ++u) {
+                    if ((u * pieces & 31) == 0) {
+                        const int w = u * pieces + lane;
+                        const uint32_t r = first + (uint32_t)w * a.box_rows;
+                        place = -1;
+                        if (w < SPT * nt * pieces && r < end) {
+                            const uint32_t page = r / (uint32_t)a.page_size;
+                            const int32_t id = __ldg(a.table + (int64_t)cur.b * a.max_pages + page);
+                            if (id >= 0 && id < a.n_pool)
+                                place = (id * a.kv_heads + cur.h) * a.page_size + (int32_t)(r - page * a.page_size);
+                            else
+                                kvc::raise_status(a.status, KVC_DEV_INDEX_OOB);
+                        }
+                    }
+                    const int q = q0 + SPT * (mine_v ? v_group(u / SPT, nt) : k_group(u / SPT)) + u % SPT;
+                    const int slot = q % NSLAB;
+                    if (q >= NSLAB)
+                        ok = wait_or_abort(&empty[slot], ((q / NSLAB) - 1) & 1, abort_flag, a.status);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok)
+                        break;
+                    uint8_t *to = smem + SM::RING_OFF + slot * SM::SLAB;
+                    if (pieces == 1) {
+                        const int32_t y = __shfl_sync(0xffffffffu, place, u & 31);
+                        if (lane == 0) {
+                            if (y < 0) {
+                                // nothing to read: the slot keeps what it holds, and its columns are masked
+                                kvc::mbar_arrive(&full[slot]);
+                            } else {
+                                kvc::mbar_arrive_expect_tx(&full[slot], SM::SLAB);
+                                kvc::tma_load_3d(to, tmap, 0, y, 0, &full[slot]);
+                            }
+                        }
+                    } else {
+                        // boxes of 64 columns, piece by piece
+                        const int piece = lane / (D / 64), c = lane % (D / 64);
+                        const int32_t y = __shfl_sync(0xffffffffu, place, (u * pieces + piece) & 31);
+                        const bool load = piece < pieces && y >= 0;
+                        const int n = __popc(__ballot_sync(0xffffffffu, load));
+                        if (lane == 0) {
+                            if (n == 0)
+                                kvc::mbar_arrive(&full[slot]);
+                            else
+                                kvc::mbar_arrive_expect_tx(&full[slot], n * a.box_rows * 128);
+                        }
+                        __syncwarp();
+                        if (load)
+                            kvc::tma_load_3d(to + c * (KR * 128) + piece * a.box_rows * 128, tmap, 0, y, c, &full[slot]);
+                    }
+                    __syncwarp();
+                    filled |= 1u << slot;
+                    phase = (phase & ~(1u << slot)) | ((uint32_t)((q / NSLAB) & 1) << slot);
+                }
+                q0 += 2 * SPT * nt;
+                cur = nxt;
+                more = again;
+            }
+            if (*abort_flag && lane == 0)
+                // wind-down: let the loads in flight land before the CTA exits
+                for (int i = 0; i < NSLAB; ++i)
+                    if (filled >> i & 1)
+                        kvc::mbar_wait(&full[i], phase >> i & 1);
+        } else if (warp == 3) {
+            // ======================= output products =======================
+            if (lane == 0) {
+                const uint64_t v_ring = kvc_tc::sw128_desc(smem_base + SM::RING_OFF, KR * 128);
+                int q0 = 0;              // slabs of the segments before
+                uint32_t used[2] = {0, 0};  // tiles that went through each score buffer
+                bool ok = true;
+                while (ok && more) {
+                    const Streams st = Streams::of<TILES>(a, cur);
+                    more = walk.next(a, line.cost, nxt);
+                    for (int j = 0; ok && j < st.n; ++j) {
+#pragma unroll
+                        for (int k = 0; k < TILES; ++k) {
+                            if (TILES == 2 && !st.has(k, j))
+                                continue;
+                            const int s = TILES == 2 ? k : (int)(used[0] & 1);
+                            uint32_t &u = used[TILES == 2 ? k : 0];
+                            const uint32_t parity = TILES == 2 ? u & 1 : (u >> 1) & 1;
+                            if (!(ok = wait_or_abort(&p_full[s], parity, abort_flag, a.status)))
+                                break;
+                            kvc_tc::fence_after();
+                            const bool fresh = TILES == 2 && !st.two ? j < 2 : j == 0;  // first of the stream
+                            const bool last = TILES == 1 || !st.two || k == 1;          // of the tile
+                            for (int hf = 0; hf < SPT; ++hf) {
+                                const int q = q0 + SPT * v_group(j, st.n) + hf, slot = q % NSLAB;
+                                if (!(ok = wait_or_abort(&full[slot], (q / NSLAB) & 1, abort_flag, a.status)))
+                                    break;
+                                kvc_tc::fence_after();
+                                const uint64_t vd = v_ring + (uint64_t)(slot * (SM::SLAB / 16));
+                                const uint32_t pa = tmem + SM::COL_S + s * kBN + hf * (KR / 2);
+#pragma unroll
+                                for (int k2 = 0; k2 < KR / 16; ++k2)
+                                    kvc_tc::mma_ts(tmem + (TILES == 2 ? k * D : 0), pa + k2 * 8,
+                                                   vd + (uint64_t)(k2 * (2048 / 16)), IDESC_O,
+                                                   !fresh || hf > 0 || k2 > 0);
+                                if (last)
+                                    kvc_tc::commit(&empty[slot]);
+                            }
+                            if (!ok)
+                                break;
+                            kvc_tc::commit(&o_done[s]);
+                            ++u;
+                        }
+                    }
+                    q0 += 2 * SPT * st.n;
+                    cur = nxt;
+                }
+                // everything issued above has completed once this arrives
+                kvc_tc::commit(&drain[1]);
+                kvc::mbar_wait(&drain[1], 0);
+            }
+        } else {
+            // ======================= queries, score products =======================
+            if (lane == 0) {
+                kvc::tma_prefetch_desc(&tmap_q);
+                int q0 = 0;
+                uint32_t used[2] = {0, 0};
+                bool ok = true;
+                const uint64_t q_desc = kvc_tc::sw128_desc(smem_base, 16);
+                const uint64_t k_ring = kvc_tc::sw128_desc(smem_base + SM::RING_OFF, 16);
+                const uint32_t q_box = (uint32_t)a.toks * a.group * 128;
+                for (int s_no = 0; ok && more; ++s_no) {
+                    // the last segment's scores are done: the queries' place is free
+                    if (s_no > 0 && !wait_or_abort(q_empty, (s_no - 1) & 1, abort_flag, a.status))
+                        break;
+                    const Streams st = Streams::of<TILES>(a, cur);
+                    const int tiles = st.two ? 2 : 1;
+                    kvc::mbar_arrive_expect_tx(q_full, tiles * (D / 64) * q_box);
+                    for (int k = 0; k < tiles; ++k)
+                        for (int c = 0; c < D / 64; ++c)
+                            kvc::tma_load_4d(smem + k * SM::Q_TILE + c * (kBM * 128), &tmap_q, 0, cur.h * a.group,
+                                             cur.row0 + cur.i * a.item + k * a.toks, c, q_full);
+                    more = walk.next(a, line.cost, nxt);
+                    if (!(ok = wait_or_abort(q_full, s_no & 1, abort_flag, a.status))) {
+                        kvc::mbar_wait(q_full, s_no & 1);  // (let the loads land before the CTA exits)
+                        break;
+                    }
+                    kvc_tc::fence_after();
+                    for (int j = 0; ok && j < st.n; ++j) {
+#pragma unroll
+                        for (int k = 0; k < TILES; ++k) {
+                            if (TILES == 2 && !st.has(k, j))
+                                continue;
+                            const int s = TILES == 2 ? k : (int)(used[0] & 1);
+                            uint32_t &u = used[TILES == 2 ? k : 0];
+                            // Scores are written where the output products of the tile before (256: before last) read
+                            // their weights.  Products of another accumulator or shape are not ordered by their
+                            // issue: the wait for those is what keeps the weights.
+                            const uint32_t before = TILES == 2 ? u : u >> 1;
+                            if (before > 0 && !(ok = wait_or_abort(&o_done[s], (before - 1) & 1, abort_flag, a.status)))
+                                break;
+                            kvc_tc::fence_after();
+                            const bool last = TILES == 1 || !st.two || k == 1;
+                            for (int hf = 0; hf < SPT; ++hf) {
+                                const int q = q0 + SPT * k_group(j) + hf, slot = q % NSLAB;
+                                if (!(ok = wait_or_abort(&full[slot], (q / NSLAB) & 1, abort_flag, a.status)))
+                                    break;
+                                kvc_tc::fence_after();
+                                const uint64_t qd = q_desc + (uint64_t)((st.two ? k : 0) * (SM::Q_TILE / 16));
+                                const uint64_t kd = k_ring + (uint64_t)(slot * (SM::SLAB / 16));
+                                const uint32_t d_s = tmem + SM::COL_S + s * kBN + hf * KR;
+#pragma unroll
+                                for (int ks = 0; ks < D / 16; ++ks)
+                                    kvc_tc::mma_ss(d_s, qd + (uint64_t)(((ks >> 2) * (kBM * 128) + (ks & 3) * 32) / 16),
+                                                   kd + (uint64_t)(((ks >> 2) * (KR * 128) + (ks & 3) * 32) / 16), IDESC_S,
+                                                   ks > 0);
+                                if (last)
+                                    kvc_tc::commit(&empty[slot]);
+                            }
+                            if (!ok)
+                                break;
+                            kvc_tc::commit(&s_full[s]);
+                            ++u;
+                        }
+                        if (ok && j == st.n - 1)
+                            kvc_tc::commit(q_empty);
+                    }
+                    q0 += 2 * SPT * st.n;
+                    cur = nxt;
+                }
+                // everything issued above has completed once this arrives
+                kvc_tc::commit(&drain[0]);
+                kvc::mbar_wait(&drain[0], 0);
+            }
+        }
+        __syncwarp();
+    } else {
+        kvc_tc::regs_up<kManyRegs>();
+        // ======================= softmax =======================
+        // A warp whose wait gave up goes on through the tiles without work or waits: the barriers
+        // below have no limit, and every warp comes to each of them.
+        constexpr int CT = kBN / HALVES;  // columns of a thread
+        const int tid = threadIdx.x - 128, quad = warp & 3, side = (warp - 4) >> 2;
+        const int stream = TILES == 2 ? side : 0, half = TILES == 2 ? 0 : side;
+        const int m = quad * 32 + lane;  // row of the tile
+        const int tok = m / a.group, head = m - tok * a.group;
+        const bool in_tile = tok < a.toks;
+        const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
+        float *red = reinterpret_cast<float *>(smem + SM::RED_OFF);
+        uint32_t *bad_sh = reinterpret_cast<uint32_t *>(smem + SM::BAD_OFF);
+        constexpr uint32_t all_bar = 1;
+        const uint32_t pair_bar = 2 + quad;
+        const float c_log2 = fabsf(a.scale_log2);
+        int q0 = 0;         // slabs before the segment
+        uint32_t used = 0;  // tiles that this stream has had
+        bool ok = true;
+        for (int s_no = 0; more; ++s_no) {
+            const Streams st = Streams::of<TILES>(a, cur);
+            const int first = cur.i * a.item + (st.two ? stream * a.toks : 0);  // the tile's first token
+            const int pos = cur.P + first + tok;                               // of this row
+            const bool there = in_tile && first + tok < cur.n;
+            const bool active = first + quad * 32 / a.group < cur.n;  // the warp has rows at all
+            // this row sees the key rows [r_lo, r_hi]
+            const int r_hi = there ? pos : -1, r_lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+            const int64_t out_row = (int64_t)(cur.row0 + first + tok) * a.q_heads + cur.h * a.group + head;
+            // what every row of the item sees: up to its first token, from the last one's window on
+            const int whole_hi = cur.P + cur.i * a.item;
+            const int whole_lo = a.window > 0 ? cur.P + min(cur.n, (cur.i + 1) * a.item) - a.window : 0;
+            const int lo0 = cur.lo + cur.t0 * kBN;
+            const bool whole = st.n == cur.tiles;
+            more = walk.next(a, line.cost, nxt);
+            // output columns in which the row has seen a NaN or an infinity, in cut tiles
+            uint32_t nan_cols[D / 32 / HALVES] = {};
+            float m_run = -INFINITY, l_run = 0.f;
+            for (int j = 0; j < st.n; ++j) {
+                const int t_lo = lo0 + j * kBN;
+                if (t_lo + kBN - 1 > whole_hi || t_lo < whole_lo) {
+                    // V rows with a NaN or an infinity in them, a bit each in bad_sh (zero before)
+                    bool found = false;
+#pragma unroll
+                    for (int hf = 0; hf < SPT; ++hf) {
+                        const int qi = q0 + SPT * v_group(j, st.n) + hf;
+                        ok = ok && wait_or_abort(&full[qi % NSLAB], (qi / NSLAB) & 1, abort_flag, a.status);
+                        if (!ok)
+                            break;
+                        const uint4 *v = reinterpret_cast<const uint4 *>(smem + SM::RING_OFF + (qi % NSLAB) * SM::SLAB);
+#pragma unroll
+                        for (int e = 0; e < SM::SLAB / 16 / kSoftmax; ++e) {
+                            const uint4 x = v[tid + kSoftmax * e];
+                            if (not_finite<T>(x.x) | not_finite<T>(x.y) | not_finite<T>(x.z) | not_finite<T>(x.w)) {
+                                const int vr = hf * KR + (((tid + kSoftmax * e) >> 3) & (KR - 1));
+                                atomicOr(&bad_sh[vr >> 5], 1u << (vr & 31));
+                                found = true;
+                            }
+                        }
+                    }
+                    if (kvc_tc::named_bar_any(all_bar, kSoftmax, found)) {
+                        // what this row sees of them is written down by column, then they are zeros for all
+#pragma unroll 1
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t left = ok && r_hi >= 0 ? bad_sh[e] : 0u;
+                            while (left) {
+                                const int vr = 32 * e + __ffs(left) - 1, in = vr & (KR - 1);
+                                left &= left - 1;
+                                if (t_lo + vr < r_lo || t_lo + vr > r_hi)
+                                    continue;
+                                const uint8_t *slab =
+                                    smem + SM::RING_OFF + (q0 + SPT * v_group(j, st.n) + vr / KR) % NSLAB * SM::SLAB;
+#pragma unroll
+                                for (int w = 0; w < D / 32 / HALVES; ++w) {
+                                    uint32_t cols = 0;
+#pragma unroll 1
+                                    for (int c = 0; c < 4; ++c) {
+                                        const int ch = half * (D / 16) + 4 * w + c;  // 16 bytes of the row
+                                        const uint4 x = *reinterpret_cast<const uint4 *>(
+                                            slab + (ch >> 3) * (KR * 128) + in * 128 + ((ch & 7) ^ (in & 7)) * 16);
+                                        const uint32_t nf[4] = {not_finite<T>(x.x), not_finite<T>(x.y), not_finite<T>(x.z),
+                                                                not_finite<T>(x.w)};
+#pragma unroll
+                                        for (int i = 0; i < 4; ++i)
+                                            cols |= ((nf[i] & 1u) | (nf[i] >> 30 & 2u)) << (8 * c + 2 * i);
+                                    }
+                                    nan_cols[w] |= cols;
+                                }
+                            }
+                        }
+                        kvc_tc::named_bar_sync(all_bar, kSoftmax);
+                        if (tid < 4)
+                            bad_sh[tid] = 0;
+#pragma unroll 1
+                        for (int hf = 0; hf < SPT && ok; ++hf) {
+                            uint4 *v = reinterpret_cast<uint4 *>(
+                                smem + SM::RING_OFF + (q0 + SPT * v_group(j, st.n) + hf) % NSLAB * SM::SLAB);
+#pragma unroll 1
+                            for (int at = tid; at < SM::SLAB / 16; at += kSoftmax) {
+                                const uint4 x = v[at];
+                                const uint4 nf = make_uint4(not_finite<T>(x.x), not_finite<T>(x.y), not_finite<T>(x.z),
+                                                            not_finite<T>(x.w));
+                                if (nf.x | nf.y | nf.z | nf.w)
+                                    v[at] = make_uint4(x.x & ~nf.x, x.y & ~nf.y, x.z & ~nf.z, x.w & ~nf.w);
+                            }
+                        }
+                        kvc::fence_proxy_async_smem();
+                        // (either stream's products may come first)
+                        kvc_tc::named_bar_sync(all_bar, kSoftmax);
+                    }
+                }
+                if (TILES == 2 && !st.has(stream, j))
+                    continue;
+                const int s = TILES == 2 ? stream : (int)(used & 1);
+                const uint32_t parity = TILES == 2 ? used & 1 : (used >> 1) & 1;
+                const uint32_t s_col = lane_addr + SM::COL_S + s * kBN;
+                ok = ok && wait_or_abort(&s_full[s], parity, abort_flag, a.status);
+                ++used;
+                kvc_tc::fence_after();
+                const int c0 = t_lo + CT * half;  // key row of this thread's first column
+                float v[CT], top = -INFINITY;
+                if (active && ok) {
+                    uint32_t *raw = reinterpret_cast<uint32_t *>(v);
+#pragma unroll
+                    for (int c = 0; c < CT; c += 32)
+                        kvc_tc::ld32(s_col + CT * half + c, raw + c);
+                    kvc_tc::wait_ld();
+                    if (a.scale_log2 < 0.f) {
+#pragma unroll
+                        for (int c = 0; c < CT; ++c)
+                            v[c] = -v[c];
+                    }
+                    if (c0 < r_lo || c0 + CT - 1 > r_hi) {
+                        const int z0 = r_lo - c0, z1 = r_hi - c0;
+#pragma unroll
+                        for (int c = 0; c < CT; ++c)
+                            v[c] = c >= z0 && c <= z1 ? v[c] : -INFINITY;
+                    }
+                    float mx[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+                    for (int c = 4; c < CT; c += 4)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            mx[e] = fmaxf(mx[e], v[c + e]);
+                    top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                }
+                if constexpr (HALVES == 2) {
+                    // the barrier also orders both halves' reads of S before either writes weights there
+                    red[(s * 2 + half) * kBM + m] = top;
+                    kvc_tc::named_bar_sync(pair_bar, 64);
+                    top = fmaxf(top, red[(s * 2 + (half ^ 1)) * kBM + m]);
+                }
+                if (active && ok) {
+                    top *= c_log2;
+                    float alpha = 1.f;
+                    bool rescale = false;
+                    if (top > m_run + kRescale || (m_run == -INFINITY && top > -INFINITY)) {
+                        if (m_run > -INFINITY) {
+                            alpha = kvc_tc::fast_exp2(m_run - top);
+                            rescale = true;
+                        }
+                        m_run = top;
+                    }
+                    const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+                    float ps0 = 0.f, ps1 = 0.f;
+#pragma unroll
+                    for (int c = 0; c < CT; c += 32) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const float p0 = kvc_tc::fast_exp2(fmaf(v[c + e], c_log2, neg_m));
+                            const float p1 = kvc_tc::fast_exp2(fmaf(v[c + e + 1], c_log2, neg_m));
+                            ps0 += p0;
+                            ps1 += p1;
+                            pk[e / 2] = kvc_tc::pack2<T>(p0, p1);
+                        }
+                        kvc_tc::st16(s_col + (CT * half + c) / 2, pk);
+                    }
+                    l_run = l_run * alpha + (ps0 + ps1);
+                    if (__any_sync(0xffffffffu, rescale)) {
+                        // the reference moved: rescale this thread's part of the O row
+                        // (the products of the tile before; with two streams they were done before S was written)
+                        ok = TILES == 2 ? wait_or_abort(&o_done[s], (used - 2) & 1, abort_flag, a.status)
+                                        : wait_or_abort(&o_done[s ^ 1], ((used - 2) >> 1) & 1, abort_flag, a.status);
+                        kvc_tc::fence_after();
+#pragma unroll 1
+                        for (int cc = half * (D / HALVES); cc < (half + 1) * (D / HALVES); cc += 32) {
+                            uint32_t o[32];
+                            kvc_tc::ld32(lane_addr + stream * D + cc, o);
+                            kvc_tc::wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                            kvc_tc::st32(lane_addr + stream * D + cc, o);
+                        }
+                    }
+                    kvc_tc::wait_st();
+                }
+                kvc_tc::fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    kvc::mbar_arrive(&p_full[s]);
+            }
+            q0 += 2 * SPT * st.n;
+
+            // ---- output rows ----
+            // (the next segment's first output products wait for its p_full, which every warp gives after this)
+            if (st.tiles(stream) > 0) {
+                const uint32_t last = used - 1;
+                ok = ok && (TILES == 2 ? wait_or_abort(&o_done[stream], last & 1, abort_flag, a.status)
+                                       : wait_or_abort(&o_done[last & 1], (last >> 1) & 1, abort_flag, a.status));
+            }
+            kvc_tc::fence_after();
+            const int64_t part = (2 * (int64_t)blockIdx.x + (s_no == 0 ? 0 : 1)) * TILES + (st.two ? stream : 0);
+            float l = l_run, ref = m_run;
+            float w0 = 1.f, w1 = 0.f;  // what the two streams' outputs of a row count
+            int col0 = 0, col1 = D;    // output columns of this thread
+            bool share = false;        // two threads have this row
+            if (HALVES == 2) {
+                // the sums change hands where the last tile's maxima did not
+                const uint32_t at = ((used - 1) & 1) ^ 1;
+                red[(at * 2 + half) * kBM + m] = l_run;
+                kvc_tc::named_bar_sync(pair_bar, 64);
+                l += red[(at * 2 + (half ^ 1)) * kBM + m];
+                col0 = half * (D / 2);
+                col1 = col0 + D / 2;
+            } else if (!st.two) {
+                // one query tile, two streams of keys: each thread joins half of the columns
+                red[(2 * side) * kBM + m] = m_run;
+                red[(2 * side + 1) * kBM + m] = l_run;
+                kvc_tc::fence_before();
+                kvc_tc::named_bar_sync(all_bar, kSoftmax);
+                kvc_tc::fence_after();
+                const float m0 = red[m], l0 = red[kBM + m], m1 = red[2 * kBM + m], l1 = red[3 * kBM + m];
+                // (a stream without a visible key has no sum, and its output may hold anything)
+                ref = fmaxf(l0 == 0.f ? -INFINITY : m0, l1 == 0.f ? -INFINITY : m1);
+                w0 = l0 == 0.f ? -1.f : m0 == ref || ref == -INFINITY ? 1.f : kvc_tc::fast_exp2(m0 - ref);
+                w1 = l1 == 0.f ? -1.f : m1 == ref || ref == -INFINITY ? 1.f : kvc_tc::fast_exp2(m1 - ref);
+                l = (l0 == 0.f ? 0.f : l0 * w0) + (l1 == 0.f ? 0.f : l1 * w1);
+                col0 = side * (D / 2);
+                col1 = col0 + D / 2;
+                share = true;
+            }
+            if (active && ok) {
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+                for (int cc = col0; cc < col1; cc += 32) {
+                    uint32_t o[32];
+                    if (!share) {
+                        kvc_tc::ld32(lane_addr + stream * D + cc, o);
+                        kvc_tc::wait_ld();
+                    } else {
+                        uint32_t o1[32];
+                        kvc_tc::ld32(lane_addr + cc, o);
+                        kvc_tc::ld32(lane_addr + D + cc, o1);
+                        kvc_tc::wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            const float x = w0 >= 0.f ? __uint_as_float(o[c]) * w0 : 0.f;
+                            o[c] = __float_as_uint(w1 >= 0.f ? fmaf(__uint_as_float(o1[c]), w1, x) : x);
+                        }
+                    }
+                    if (!there)
+                        continue;
+                    uint32_t bad = 0;
+#pragma unroll
+                    for (int w = 0; w < D / 32 / HALVES; ++w)
+                        bad = w == (cc - (HALVES == 2 ? col0 : 0)) / 32 ? nan_cols[w] : bad;
+                    if (bad) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            o[c] = bad >> c & 1u ? 0x7fc00000u : o[c];
+                    }
+                    if (whole) {
+                        T *to = static_cast<T *>(a.out) + out_row * D + cc;
+#pragma unroll
+                        for (int c = 0; c < 32; c += 8) {
+                            uint4 x;
+                            uint32_t *w = reinterpret_cast<uint32_t *>(&x);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                w[e] = kvc_tc::pack2<T>(kvc_tc::finite_or_nan(__uint_as_float(o[c + 2 * e]) * inv),
+                                                        kvc_tc::finite_or_nan(__uint_as_float(o[c + 2 * e + 1]) * inv));
+                            *reinterpret_cast<uint4 *>(to + c) = x;
+                        }
+                    } else {
+                        // four columns of all 128 rows side by side, so that a warp's store is one run
+                        uint4 *to = reinterpret_cast<uint4 *>(a.ws_o) + (part * (D / 4) + cc / 4) * kBM + m;
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4)
+                            to[c / 4 * kBM] = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                    }
+                }
+                if (!whole && there && col0 == 0) {
+                    a.ws_m[part * kBM + m] = ref;
+                    a.ws_l[part * kBM + m] = l;
+                }
+            }
+            kvc_tc::fence_before();
+            if (TILES == 2 && !st.two)
+                // both streams' outputs have been read, and the sums: the next segment may write them
+                kvc_tc::named_bar_sync(all_bar, kSoftmax);
+            cur = nxt;
+        }
+    }
+
+    __syncthreads();
+    if (warp == 0) {
+        kvc_tc::fence_after();
+        kvc_tc::tmem_dealloc(tmem, SM::TMEM_COLS);
+    }
+}
+
+// Joins the partial results of an item's rows that several CTAs worked on:
+// out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.  The item's first keys are in the
+// share of exactly one CTA, which the block takes its number from and which has
+// written down which item that is.  A block takes 16 rows at a time: a row a
+// thread's low bits, so that 16 threads read a run of 256 bytes.
+constexpr int kMergeRows = 16, kMergeBlocks = 4;
+template <typename T, int D>
+__global__ void __launch_bounds__(256)
+ragged_merge_kernel(const RaggedArgs a)
+{
+    constexpr int TILES = Smem<D>::TILES;
+    kvc::grid_dep_wait();
+    const int c0 = blockIdx.x, lane = threadIdx.x & 31;
+    const int4 split = a.split[c0];
+    const int parts = split.w >> 1, slot0 = split.w & 1;
+    if (parts == 0)
+        return;
+    const int h = split.y, i = split.z;
+    uint32_t wrong;
+    const Request req = request(a, split.x, wrong);
+    const int left = min(req.n - i * a.item, a.item);  // tokens of the item
+    // the item's segment is the first of its CTA, but in the first CTA if that began before it
+    auto part = [&](int p, int tile) { return (2 * ((int64_t)c0 + p) + (p == 0 ? slot0 : 0)) * TILES + tile; };
+    constexpr int R = kMergeRows, W = R / 8;
+    constexpr int COLS = D / 4, LANES = 256 / R, PER = COLS / LANES;  // float4 columns, of a thread
+    __shared__ float w_sh[R][33], sum_sh[R];
+    const int warp = threadIdx.x >> 5, mine = threadIdx.x % R, c4 = threadIdx.x / R;
+    constexpr int AHEAD = PER <= 2 ? 4 : 2;  // parts under way
+    for (int g = blockIdx.y; g < TILES * kBM / R; g += gridDim.y) {
+        const int tile = g / (kBM / R), m0 = g % (kBM / R) * R;
+        // rows of the tile that hold queries
+        const int rows = min(left - tile * a.toks, a.toks) * a.group;
+        if (m0 >= rows)
+            continue;
+        float4 acc[PER], x[AHEAD][PER];
+        auto load = [&](int p) {
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                const float4 *o = reinterpret_cast<const float4 *>(a.ws_o) +
+                                  (part(min(p + k, parts - 1), tile) * COLS + c4) * kBM + m0 + mine;
+#pragma unroll
+                for (int e = 0; e < PER; ++e)
+                    x[k][e] = o[e * LANES * kBM];
+            }
+        };
+        load(0);
 #pragma unroll
         for (int e = 0; e < PER; ++e)
-            s = fmaf(q[e], kvc::Elem<T>::to_f32(static_cast<const T *>(a.k)[at + 32 * e]), s);
+            acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        float top[W], sum[W];
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            top[k] = -INFINITY;
+            sum[k] = 0.f;
+        }
+        auto stat = [&](int p, int k) { return part(p, tile) * kBM + m0 + W * warp + k; };
+        auto row_there = [&](int k) { return m0 + W * warp + k < rows; };
+        for (int p = lane; p < parts; p += 32)
+#pragma unroll
+            for (int k = 0; k < W; ++k)
+                if (row_there(k))
+                    top[k] = fmaxf(top[k], a.ws_l[stat(p, k)] == 0.f ? -INFINITY : a.ws_m[stat(p, k)]);
 #pragma unroll
         for (int d = 16; d; d >>= 1)
-            s += __shfl_xor_sync(0xffffffffu, s, d);
-        s *= a.scale;
-        const float top = fmaxf(m, s), old = m == -INFINITY ? 0.f : expf(m - top), p = expf(s - top);
-        l = l * old + p;
-        m = top;
 #pragma unroll
-        for (int e = 0; e < PER; ++e) {
-            const float v = kvc::Elem<T>::to_f32(static_cast<const T *>(a.v)[at + 32 * e]);
-            o[e] = o[e] * old + p * fmaf(v, 0.f, v);  // (an infinity counts as NaN)
+            for (int k = 0; k < W; ++k)
+                top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], d));
+        for (int p0 = 0; p0 < parts; p0 += 32) {
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+                // a part's weight a lane; a part that saw nothing (no sum) has none (-1), whatever its O holds; one
+                // that is too small for a number still has its part's NaN
+                float w = -1.f;
+                if (p0 + lane < parts && row_there(k)) {
+                    const float l = a.ws_l[stat(p0 + lane, k)], mc = a.ws_m[stat(p0 + lane, k)];
+                    if (l != 0.f) {
+                        w = mc == top[k] || mc == -INFINITY ? 1.f : exp2f(mc - top[k]);
+                        sum[k] += l * w;
+                    }
+                }
+                w_sh[W * warp + k][lane] = w;
+            }
+            __syncthreads();
+            const int here = min(32, parts - p0);
+            for (int p = 0; p < here; p += AHEAD) {
+#pragma unroll
+                for (int k = 0; k < AHEAD; ++k) {
+                    const float w = w_sh[mine][p + k];  // (-1 past the last part)
+                    if (w >= 0.f) {
+#pragma unroll
+                        for (int e = 0; e < PER; ++e) {
+                            acc[e].x += x[k][e].x * w;
+                            acc[e].y += x[k][e].y * w;
+                            acc[e].z += x[k][e].z * w;
+                            acc[e].w += x[k][e].w * w;
+                        }
+                    }
+                }
+                if (p0 + p + AHEAD < parts)
+                    load(p0 + p + AHEAD);
+            }
         }
-    }
 #pragma unroll
-    for (int e = 0; e < PER; ++e)
-        static_cast<T *>(a.out)[((int64_t)t * a.q_heads + head) * D + lane + 32 * e] = kvc::Elem<T>::from_f32(o[e] / l);
+        for (int k = 0; k < W; ++k) {
+#pragma unroll
+            for (int d = 16; d; d >>= 1)
+                sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], d);
+            if (lane == 0)
+                sum_sh[W * warp + k] = sum[k];
+        }
+        __syncthreads();
+        const int m = m0 + mine;
+        if (m < rows) {
+            const float total = sum_sh[mine], inv = total == 0.f ? 0.f : 1.f / total;
+            const int tok = m / a.group;
+            const int64_t row = (int64_t)(req.row0 + i * a.item + tile * a.toks + tok) * a.q_heads + h * a.group +
+                                (m - tok * a.group);
+            T *to = static_cast<T *>(a.out) + row * D;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+                uint2 y;
+                y.x = kvc_tc::pack2<T>(kvc_tc::finite_or_nan(acc[e].x * inv), kvc_tc::finite_or_nan(acc[e].y * inv));
+                y.y = kvc_tc::pack2<T>(kvc_tc::finite_or_nan(acc[e].z * inv), kvc_tc::finite_or_nan(acc[e].w * inv));
+                *reinterpret_cast<uint2 *>(to + 4 * (c4 + LANES * e)) = y;
+            }
+        }
+        __syncthreads();
+    }
 }
 
-template <typename T> void launch_attn(const RaggedArgs &a, int D, cudaStream_t stream)
+template <typename T, int D>
+kvc_status launch_attn(RaggedArgs &a, const void *q, const void *k, const void *v, int grid, cudaStream_t stream)
 {
-    const dim3 grid(a.tokens, a.kv_heads);
-    if (D == 64)
-        ragged_attn_kernel<T, 64><<<grid, 32 * a.group, 0, stream>>>(a);
-    else if (D == 128)
-        ragged_attn_kernel<T, 128><<<grid, 32 * a.group, 0, stream>>>(a);
-    else
-        ragged_attn_kernel<T, 256><<<grid, 32 * a.group, 0, stream>>>(a);
+    using SM = Smem<D>;
+    const CUtensorMapDataType tt = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                  : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const uint64_t rows = (uint64_t)a.n_pool * a.page_size * a.kv_heads;
+    const int blocks = a.box_rows == SM::KR ? D / 64 : 1;  // column blocks of a box of K or V
+    CUtensorMap tq, tk, tv;
+    if (!kvc_host::encode_4d_blocks_sw128(&tq, q, (uint64_t)a.tokens, (uint64_t)a.q_heads, D, 2, (uint32_t)a.group,
+                                          (uint32_t)a.toks, tt, 1) ||
+        !kvc_host::encode_3d_sw128(&tk, k, rows, D, a.box_rows, blocks, tt) ||
+        !kvc_host::encode_3d_sw128(&tv, v, rows, D, a.box_rows, blocks, tt))
+        return KVC_ERR_CUDA;
+    auto kern = ragged_attn_kernel<T, D>;
+    int dev = 0, optin = 0;
+    cudaFuncAttributes attr;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
+        cudaFuncGetAttributes(&attr, kern) != cudaSuccess)
+        return KVC_ERR_CUDA;
+    const size_t smem = std::min<size_t>((size_t)SM::TOTAL + 1024, (size_t)optin);
+    // (the softmax warps would wait for registers that the block does not have)
+    if (smem < (size_t)SM::TOTAL || attr.numRegs != kLaunchRegs)
+        return KVC_ERR_UNSUPPORTED;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return KVC_ERR_CUDA;
+    kern<<<grid, kThreads, smem, stream>>>(tq, tk, tv, a);
+    if (grid > 1) {
+        // may start while the attention runs, and waits for it
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(grid - 1, kMergeBlocks);
+        cfg.blockDim = dim3(256);
+        cfg.stream = stream;
+        cudaLaunchAttribute la[1];
+        la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        la[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = la;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, ragged_merge_kernel<T, D>, a) != cudaSuccess)
+            return KVC_ERR_CUDA;
+    }
+    return kvc_host::launch_status();
+}
+
+template <typename T>
+kvc_status dispatch(RaggedArgs &a, const void *q, const void *k, const void *v, int D, int grid, cudaStream_t stream)
+{
+    switch (D) {
+    case 64:
+        return launch_attn<T, 64>(a, q, k, v, grid, stream);
+    case 128:
+        return launch_attn<T, 128>(a, q, k, v, grid, stream);
+    default:
+        return launch_attn<T, 256>(a, q, k, v, grid, stream);
+    }
+}
+
+// the workspace: two partial results of an item for each CTA (one an SM)
+struct Layout {
+    int grid;
+    int64_t parts;  // of a query tile
+    size_t m, l, split, total;
+};
+Layout layout_of(int head_dim)
+{
+    Layout w;
+    w.grid = kvc_host::sm_count();
+    w.parts = 2 * (int64_t)w.grid * (head_dim <= 128 ? 2 : 1);
+    w.m = (size_t)w.parts * kBM * head_dim * sizeof(float);
+    w.l = w.m + (size_t)w.parts * kBM * sizeof(float);
+    w.split = w.l + (size_t)w.parts * kBM * sizeof(float);
+    w.total = w.split + (size_t)w.grid * sizeof(int4);
+    return w;
 }
 
 } // namespace
@@ -116,7 +1204,7 @@ KVC_API size_t kvc_gqa_ragged_workspace_size(int batch, int tokens, int q_heads,
 {
     if (batch < 1 || tokens < 1 || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads != 0 || head_dim < 1)
         return 0;
-    return 256;
+    return layout_of(head_dim).total;
 }
 
 KVC_API kvc_status kvc_gqa_ragged(void *out, const void *q, const void *k_pool, const void *v_pool,
@@ -155,12 +1243,35 @@ KVC_API kvc_status kvc_gqa_ragged(void *out, const void *q, const void *k_pool, 
         return KVC_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u)
         return KVC_ERR_ALIGN;
-    const RaggedArgs a{out, q, k_pool, v_pool, offsets, block_table, max_pages, page_size, n_pool_pages, len, batch,
-                       tokens, q_heads, kv_heads, q_heads / kv_heads, local_window_size,
-                       scale == 0.f ? 1.0f / sqrtf((float)head_dim) : scale, dev_status};
-    if (dtype == KVC_BF16)
-        launch_attn<__nv_bfloat16>(a, head_dim, static_cast<cudaStream_t>(stream_));
-    else
-        launch_attn<__half>(a, head_dim, static_cast<cudaStream_t>(stream_));
-    return kvc_host::launch_status();
+    RaggedArgs a{};
+    a.out = out;
+    a.offsets = offsets;
+    a.table = block_table;
+    a.max_pages = max_pages;
+    a.page_size = page_size;
+    a.n_pool = n_pool_pages;
+    a.len = len;
+    a.batch = batch;
+    a.tokens = tokens;
+    a.q_heads = q_heads;
+    a.kv_heads = kv_heads;
+    a.group = q_heads / kv_heads;
+    a.toks = kBM / a.group;
+    a.item = a.toks * (head_dim <= 128 ? 2 : 1);
+    // rows of a box: as many as a slab holds that no page's end cuts
+    a.box_rows = head_dim <= 128 ? 128 : 64;
+    while (page_size % a.box_rows)
+        a.box_rows /= 2;
+    a.window = local_window_size;
+    a.scale_log2 = (scale == 0.f ? 1.0f / sqrtf((float)head_dim) : scale) * kLog2e;
+    a.status = dev_status;
+    const Layout w = layout_of(head_dim);
+    uint8_t *base = static_cast<uint8_t *>(workspace);
+    a.ws_o = reinterpret_cast<float *>(base);
+    a.ws_m = reinterpret_cast<float *>(base + w.m);
+    a.ws_l = reinterpret_cast<float *>(base + w.l);
+    a.split = reinterpret_cast<int4 *>(base + w.split);
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    return dtype == KVC_BF16 ? dispatch<__nv_bfloat16>(a, q, k_pool, v_pool, head_dim, w.grid, stream)
+                             : dispatch<__half>(a, q, k_pool, v_pool, head_dim, w.grid, stream);
 }

@@ -88,6 +88,28 @@ __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t *r)
                  : "memory");
 }
 
+// the same, 16 columns
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+                 "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+                 "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+                 "r"(r[15])
+                 : "memory");
+}
+
+// A warpgroup gives registers up (to N a thread) or takes some (waiting until they are free):
+// what a block's warpgroups hold together may not exceed what it was launched with.
+template <int N> __device__ __forceinline__ void regs_down()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void regs_up()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Shared-memory matrix descriptor of a 128-byte-swizzled operand: rows of 128
 // bytes, 8-row groups 1024 bytes apart, `lbo` bytes between 64-element column
 // blocks where the other dimension is the contiguous one.
