@@ -24,8 +24,6 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kBM = 128, kBN = 128;
-constexpr int kThreads = 32 * 12;
-constexpr int kSoftmax = 256;    // threads of the softmax warps
 constexpr float kRescale = 8.f;  // log2 units by which a score may exceed the reference maximum
 constexpr int kItemCost = 512;   // keys that stand for what an item costs beside its keys
 constexpr int kMaxRequests = 65535;
@@ -190,12 +188,13 @@ struct Walk {
 // The CTA's share: the requests' keys and items summed by groups of 32 (a warp a
 // group), the sums in shared memory, then the group, the request and the item of the
 // share's first unit.  `scratch` holds 12 bytes a group.
+template <int THREADS>
 __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch, int grid, Walk &w)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, groups = (a.batch + 31) / 32;
     int64_t *keys = reinterpret_cast<int64_t *>(scratch);
     int *rows = reinterpret_cast<int *>(scratch + 8 * (size_t)groups);
-    for (int g = warp; g < groups; g += kThreads / 32) {
+    for (int g = warp; g < groups; g += THREADS / 32) {
         const int b = 32 * g + lane;
         int64_t k = 0;
         int n = 0;
@@ -309,7 +308,8 @@ __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch
 //   warp 0        TMA of the queries, the score products
 //   warps 1, 2    TMA of K and of V into one ring in the order of use
 //   warp 3        the output products
-//   warps 4-11    softmax and output, a warp a quarter of the 128 TMEM lanes
+//   other warps   softmax and output: eight a stream, two threads a row (= TMEM
+//                 lane), each half of the columns
 //
 // head_dim <= 128: the warps 4-7 and 8-11 are two streams, each with a score buffer
 // and an output of its own, so that one's softmax runs while the other's products
@@ -329,36 +329,46 @@ __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch
 // there the softmax warps look through V in shared memory, write down for each row
 // the columns of such values that it sees, and put zeros in their place.
 
+// The segments of a stream's softmax warps: one warp looks one ahead for all.
+struct Kept {
+    Walk walk;
+    Segment seg[2];
+    int more[2];
+};
+
 template <int D> struct Smem {
     static constexpr int TILES = D <= 128 ? 2 : 1;  // query tiles, streams
-    static constexpr int HALVES = 3 - TILES;        // threads of a row
+    static constexpr int SOFTMAX = TILES * 256;     // threads of the softmax warps: two a row
+    static constexpr int THREADS = 128 + SOFTMAX;
     static constexpr int KR = D <= 128 ? 128 : 64;  // rows of a slab
     static constexpr int SPT = kBN / KR;            // slabs of a tile of K (or V)
     static constexpr int Q_TILE = kBM * D * 2, Q_BYTES = TILES * Q_TILE;
     static constexpr int SLAB = KR * D * 2;
     static constexpr int BUDGET = 227 * 1024;
     static constexpr int NBAR = 10;  // beside the ring's
-    static constexpr int MISC = (2 * 12 + NBAR) * 8 + 16 + 4 * kBM * 4 + 16;
-    static constexpr int FIT = (BUDGET - Q_BYTES - MISC) / SLAB;
-    static constexpr int NSLAB = FIT < 12 ? FIT : 12;
+    // beside the queries and n slabs: barriers, tensor memory's address and a flag, maxima and sums, rows, `Kept`
+    static constexpr int misc(int n) { return (2 * n + NBAR) * 8 + 16 + 4 * kBM * 4 + 16 + 2 * (int)sizeof(Kept); }
+    static constexpr int fit()
+    {
+        int n = 12;
+        while (Q_BYTES + n * SLAB + misc(n) > BUDGET)
+            --n;
+        return n;
+    }
+    static constexpr int NSLAB = fit();
     static constexpr int RING_OFF = Q_BYTES;
     static constexpr int BAR_OFF = RING_OFF + NSLAB * SLAB;
     // full[NSLAB], empty[NSLAB], s_full[2], p_full[2], o_done[2], q_full, q_empty, drain[2]
     static constexpr int MISC_OFF = BAR_OFF + (2 * NSLAB + NBAR) * 8;
     static constexpr int RED_OFF = (MISC_OFF + 8 + 15) / 16 * 16;  // 4 x 128 floats: maxima and sums that change hands
     static constexpr int BAD_OFF = RED_OFF + 4 * kBM * 4;
-    static constexpr int TOTAL = BAD_OFF + 16;
+    static constexpr int WALK_OFF = BAD_OFF + 16;  // of each stream
+    static constexpr int TOTAL = WALK_OFF + 2 * (int)sizeof(Kept);
     static_assert(TOTAL <= BUDGET && NSLAB >= 2 * SPT + 1, "a tile of K, one of V and the next slab must fit");
     static_assert(NSLAB * SLAB >= 12 * ((kMaxRequests + 31) / 32), "the groups' sums lie where the ring will");
     static constexpr uint32_t COL_S = TILES * D, TMEM_COLS = 512;
     static_assert(COL_S + 2 * kBN <= TMEM_COLS, "tensor memory");
 };
-
-// Registers: 384 threads are launched with 168 each; the four warps that move data
-// and issue products keep 88, the softmax warps, whose scores stay in registers
-// from the maximum to the exponential, take 208 (4 x 32 x 88 + 8 x 32 x 208 = 384 x 168).
-constexpr int kLaunchRegs = 168, kFewRegs = 88, kManyRegs = 208;
-static_assert(128 * kFewRegs + 256 * kManyRegs <= kThreads * kLaunchRegs, "a block has no more registers than at launch");
 
 // The ring holds, for a segment of n tiles, K_0, K_1, then V_j and K_{j+2} while
 // there is one, then the last V's: the places of K_j and of V_j in that order.
@@ -374,6 +384,85 @@ template <typename T> __device__ __forceinline__ uint32_t not_finite(uint32_t w)
 {
     constexpr uint32_t ex = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
     return __vcmpeq2(w & ex, ex);
+}
+
+// Scores of the key rows from k0 on: those outside [r_lo, r_hi] become -infinity, and
+// a negative scale turns the others' sign (the maximum is of scale * score / |scale|).
+__device__ __forceinline__ void seen_only(uint32_t (&x)[32], int k0, int r_lo, int r_hi, uint32_t flip)
+{
+    const int lo = r_lo - k0, hi = r_hi - k0;
+    uint32_t bits = lo > 0 ? lo < 32 ? ~0u << lo : 0u : ~0u;
+    bits &= hi < 0 ? 0u : hi < 31 ? (2u << hi) - 1u : ~0u;
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+        x[c] = bits >> c & 1u ? x[c] ^ flip : 0xff800000u;
+}
+
+__device__ __forceinline__ float top_of(const uint32_t (&x)[32])
+{
+    float m[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        m[e] = fmaxf(__uint_as_float(x[e]), __uint_as_float(x[4 + e]));
+#pragma unroll
+    for (int c = 8; c < 32; c += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            m[e] = fmaxf(fmaxf(m[e], __uint_as_float(x[c + e])), __uint_as_float(x[c + 4 + e]));
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// scores -> weights 2^(x c - m), summed in float32 and packed to 16-bit pairs in x[0..15]
+template <typename T>
+__device__ __forceinline__ void weights(uint32_t (&x)[32], float c_log2, float neg_m, float2 (&sum)[2])
+{
+    const float2 c2 = make_float2(c_log2, c_log2), m2 = make_float2(neg_m, neg_m);
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+        const float2 z = kvc_tc::fma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2, m2);
+        const float2 p = make_float2(kvc_tc::fast_exp2(z.x), kvc_tc::fast_exp2(z.y));
+        sum[e / 2 % 2] = kvc_tc::add2(sum[e / 2 % 2], p);
+        x[e / 2] = kvc_tc::pack2<T>(p.x, p.y);
+    }
+}
+
+// The maximum and the weights of a row's CT scores in tensor memory (columns from key
+// row c0 on).  MASK: those of the key rows [r_lo, r_hi] count.  Both read the scores, 32
+// at a time in a rolled loop: unrolled, with the scores in registers from the maximum
+// to the exponential, a tile was longer than the instruction cache next to the tensor
+// cores' issue loops and took twice the time.
+template <int CT, bool MASK>
+__device__ __forceinline__ float row_top(uint32_t from, int c0, int r_lo, int r_hi, uint32_t flip)
+{
+    uint32_t x[32];
+    float mx = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < CT; c += 32) {
+        kvc_tc::ld32(from + c, x);
+        kvc_tc::wait_ld32(x);
+        if (MASK)
+            seen_only(x, c0 + c, r_lo, r_hi, flip);
+        mx = fmaxf(mx, top_of(x));
+    }
+    return mx;
+}
+
+template <typename T, int CT, bool MASK>
+__device__ __forceinline__ float row_weights(uint32_t from, uint32_t to, int c0, int r_lo, int r_hi, uint32_t flip,
+                                             float c_log2, float neg_m)
+{
+    uint32_t x[32];
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+    for (int c = 0; c < CT; c += 32) {
+        kvc_tc::ld32(from + c, x);
+        kvc_tc::wait_ld32(x);
+        if (MASK)
+            seen_only(x, c0 + c, r_lo, r_hi, flip);
+        weights<T>(x, c_log2, neg_m, sum);
+        kvc_tc::st16(to + c / 2, x);
+    }
+    return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
 // What the streams do in a segment: `two` query tiles over the same keys, the first
@@ -398,13 +487,13 @@ struct Streams {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Smem<D>::THREADS, 1)
 ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                    const __grid_constant__ CUtensorMap tmap_v, const RaggedArgs a)
 {
     using SM = Smem<D>;
     using kvc_tc::wait_or_abort;
-    constexpr int NSLAB = SM::NSLAB, SPT = SM::SPT, KR = SM::KR, TILES = SM::TILES, HALVES = SM::HALVES;
+    constexpr int NSLAB = SM::NSLAB, SPT = SM::SPT, KR = SM::KR, TILES = SM::TILES, kSoftmax = SM::SOFTMAX, THREADS = SM::THREADS;
     constexpr uint32_t AB = std::is_same<T, __half>::value ? 0u : 1u;
     constexpr uint32_t IDESC_S = kvc_tc::f16_idesc(AB, 0, kBM, KR);
     constexpr uint32_t IDESC_O = kvc_tc::f16_idesc(AB, 1, kBM, D);
@@ -438,7 +527,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         }
         for (int i = 0; i < 2; ++i) {
             kvc::mbar_init(&s_full[i], 1);
-            kvc::mbar_init(&p_full[i], TILES == 2 ? 4 : 8);
+            kvc::mbar_init(&p_full[i], 8);
             kvc::mbar_init(&o_done[i], 1);
         }
         kvc::mbar_init(q_full, 1);
@@ -455,7 +544,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         kvc_tc::fence_before();
     }
     Walk walk;
-    const Line line = find_share(a, smem + SM::RING_OFF, gridDim.x, walk);
+    const Line line = find_share<THREADS>(a, smem + SM::RING_OFF, gridDim.x, walk);
     // (the sums were read from where the ring's first slabs will be written)
     kvc::fence_proxy_async_smem();
     __syncthreads();
@@ -467,7 +556,6 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     bool more = walk.next(a, line.cost, cur);
 
     if (warp < 4) {
-        kvc_tc::regs_down<kFewRegs>();
         if (warp == 1 || warp == 2) {
             // ======================= TMA producers of K and of V =======================
             // Each lane finds the place of one of the next 32 boxes' rows, and issues one of the slab's boxes.
@@ -581,10 +669,11 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                                     break;
                                 kvc_tc::fence_after();
                                 const uint64_t vd = v_ring + (uint64_t)(slot * (SM::SLAB / 16));
-                                const uint32_t pa = tmem + SM::COL_S + s * kBN + hf * (KR / 2);
+                                // (the weights of 64 keys are 32 columns, the next ones' begin 64 further on)
+                                const uint32_t pa = tmem + SM::COL_S + s * kBN + hf * 64;
 #pragma unroll
                                 for (int k2 = 0; k2 < KR / 16; ++k2)
-                                    kvc_tc::mma_ts(tmem + (TILES == 2 ? k * D : 0), pa + k2 * 8,
+                                    kvc_tc::mma_ts(tmem + (TILES == 2 ? k * D : 0), pa + k2 / 4 * 64 + k2 % 4 * 8,
                                                    vd + (uint64_t)(k2 * (2048 / 16)), IDESC_O,
                                                    !fresh || hf > 0 || k2 > 0);
                                 if (last)
@@ -679,42 +768,60 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         }
         __syncwarp();
     } else {
-        kvc_tc::regs_up<kManyRegs>();
         // ======================= softmax =======================
         // A warp whose wait gave up goes on through the tiles without work or waits: the barriers
         // below have no limit, and every warp comes to each of them.
-        constexpr int CT = kBN / HALVES;  // columns of a thread
-        const int tid = threadIdx.x - 128, quad = warp & 3, side = (warp - 4) >> 2;
-        const int stream = TILES == 2 ? side : 0, half = TILES == 2 ? 0 : side;
+        constexpr int CT = kBN / 2;  // columns of a thread
+        const int tid = threadIdx.x - 128, quad = warp & 3, half = (warp >> 2) & 1 ^ 1, stream = (warp - 4) >> 3;
         const int m = quad * 32 + lane;  // row of the tile
-        const int tok = m / a.group, head = m - tok * a.group;
-        const bool in_tile = tok < a.toks;
         const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
         float *red = reinterpret_cast<float *>(smem + SM::RED_OFF);
         uint32_t *bad_sh = reinterpret_cast<uint32_t *>(smem + SM::BAD_OFF);
         constexpr uint32_t all_bar = 1;
-        const uint32_t pair_bar = 2 + quad;
+        const uint32_t pair_bar = 2 + 4 * stream + quad;  // of the row's two threads
         const float c_log2 = fabsf(a.scale_log2);
+        const uint32_t flip = a.scale_log2 < 0.f ? 0x80000000u : 0u;
+        const uint32_t stream_bar = 10 + stream;
+        // what a tile does not need, kept apart from the registers that its scores take
+        Kept *kept = reinterpret_cast<Kept *>(smem + SM::WALK_OFF) + stream;
+        const bool scout = (warp & 7) == 4;  // of a stream's warps, the one that looks ahead
+        if (scout && lane == 0) {
+            kept->walk = walk;
+            kept->seg[0] = cur;
+            kept->more[0] = more;
+        }
+        kvc_tc::named_bar_sync(stream_bar, 256);
         int q0 = 0;         // slabs before the segment
         uint32_t used = 0;  // tiles that this stream has had
         bool ok = true;
-        for (int s_no = 0; more; ++s_no) {
-            const Streams st = Streams::of<TILES>(a, cur);
-            const int first = cur.i * a.item + (st.two ? stream * a.toks : 0);  // the tile's first token
-            const int pos = cur.P + first + tok;                               // of this row
-            const bool there = in_tile && first + tok < cur.n;
-            const bool active = first + quad * 32 / a.group < cur.n;  // the warp has rows at all
-            // this row sees the key rows [r_lo, r_hi]
-            const int r_hi = there ? pos : -1, r_lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-            const int64_t out_row = (int64_t)(cur.row0 + first + tok) * a.q_heads + cur.h * a.group + head;
-            // what every row of the item sees: up to its first token, from the last one's window on
-            const int whole_hi = cur.P + cur.i * a.item;
-            const int whole_lo = a.window > 0 ? cur.P + min(cur.n, (cur.i + 1) * a.item) - a.window : 0;
-            const int lo0 = cur.lo + cur.t0 * kBN;
-            const bool whole = st.n == cur.tiles;
-            more = walk.next(a, line.cost, nxt);
-            // output columns in which the row has seen a NaN or an infinity, in cut tiles
-            uint32_t nan_cols[D / 32 / HALVES] = {};
+        for (int s_no = 0; *(volatile int *)&kept->more[s_no & 1]; ++s_no) {
+            Streams st;
+            bool active;          // the warp has rows at all
+            int r_lo, r_hi;       // this row sees the key rows [r_lo, r_hi]; one without a query nothing in particular
+            int whole_lo, whole_hi;  // what every row of the item sees: up to its first token, from the last one's window on
+            int lo0;
+            {
+                const Segment seg = kept->seg[s_no & 1];
+                st = Streams::of<TILES>(a, seg);
+                const int first = seg.i * a.item + (st.two ? stream * a.toks : 0);  // the tile's first token
+                const int tok = m / a.group, pos = seg.P + first + tok;
+                const bool there = tok < a.toks && first + tok < seg.n;
+                active = first + quad * 32 / a.group < seg.n;
+                r_hi = there ? pos : INT_MAX;
+                r_lo = there && a.window > 0 ? max(0, pos - a.window + 1) : 0;
+                whole_hi = seg.P + seg.i * a.item;
+                whole_lo = a.window > 0 ? seg.P + min(seg.n, (seg.i + 1) * a.item) - a.window : 0;
+                lo0 = seg.lo + seg.t0 * kBN;
+            }
+            if (scout && lane == 0) {
+                Walk next = kept->walk;
+                kept->more[(s_no + 1) & 1] = next.next(a, line.cost, kept->seg[(s_no + 1) & 1]);
+                kept->walk = next;
+            }
+            __syncwarp();
+            // output columns in which the row has seen a NaN or an infinity, in cut tiles (written once there is one)
+            volatile uint32_t nan_cols[D / 64];
+            bool nans = false;
             float m_run = -INFINITY, l_run = 0.f;
             for (int j = 0; j < st.n; ++j) {
                 const int t_lo = lo0 + j * kBN;
@@ -742,16 +849,20 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                         // what this row sees of them is written down by column, then they are zeros for all
 #pragma unroll 1
                         for (int e = 0; e < 4; ++e) {
-                            uint32_t left = ok && r_hi >= 0 ? bad_sh[e] : 0u;
+                            uint32_t left = ok && r_hi != INT_MAX ? bad_sh[e] : 0u;
                             while (left) {
                                 const int vr = 32 * e + __ffs(left) - 1, in = vr & (KR - 1);
                                 left &= left - 1;
                                 if (t_lo + vr < r_lo || t_lo + vr > r_hi)
                                     continue;
+                                if (!nans)
+                                    for (int w = 0; w < D / 64; ++w)
+                                        nan_cols[w] = 0;
+                                nans = true;
                                 const uint8_t *slab =
                                     smem + SM::RING_OFF + (q0 + SPT * v_group(j, st.n) + vr / KR) % NSLAB * SM::SLAB;
-#pragma unroll
-                                for (int w = 0; w < D / 32 / HALVES; ++w) {
+#pragma unroll 1
+                                for (int w = 0; w < D / 64; ++w) {
                                     uint32_t cols = 0;
 #pragma unroll 1
                                     for (int c = 0; c < 4; ++c) {
@@ -764,7 +875,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                                         for (int i = 0; i < 4; ++i)
                                             cols |= ((nf[i] & 1u) | (nf[i] >> 30 & 2u)) << (8 * c + 2 * i);
                                     }
-                                    nan_cols[w] |= cols;
+                                    nan_cols[w] = nan_cols[w] | cols;
                                 }
                             }
                         }
@@ -798,34 +909,15 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 ++used;
                 kvc_tc::fence_after();
                 const int c0 = t_lo + CT * half;  // key row of this thread's first column
-                float v[CT], top = -INFINITY;
-                if (active && ok) {
-                    uint32_t *raw = reinterpret_cast<uint32_t *>(v);
-#pragma unroll
-                    for (int c = 0; c < CT; c += 32)
-                        kvc_tc::ld32(s_col + CT * half + c, raw + c);
-                    kvc_tc::wait_ld();
-                    if (a.scale_log2 < 0.f) {
-#pragma unroll
-                        for (int c = 0; c < CT; ++c)
-                            v[c] = -v[c];
-                    }
-                    if (c0 < r_lo || c0 + CT - 1 > r_hi) {
-                        const int z0 = r_lo - c0, z1 = r_hi - c0;
-#pragma unroll
-                        for (int c = 0; c < CT; ++c)
-                            v[c] = c >= z0 && c <= z1 ? v[c] : -INFINITY;
-                    }
-                    float mx[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-                    for (int c = 4; c < CT; c += 4)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            mx[e] = fmaxf(mx[e], v[c + e]);
-                    top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                }
-                if constexpr (HALVES == 2) {
-                    // the barrier also orders both halves' reads of S before either writes weights there
+                // the weights of either half go where its own scores were, so that neither waits for the other
+                const uint32_t from = s_col + CT * half, to = s_col + CT * half;
+                // tiles whose scores are taken as they are (all of the warp's rows see all of its columns) apart
+                // from those that are looked at one by one
+                const bool plain = __all_sync(0xffffffffu, c0 >= r_lo && c0 + CT - 1 <= r_hi) && !flip;
+                float top = -INFINITY;
+                if (active && ok)
+                    top = plain ? row_top<CT, false>(from, c0, r_lo, r_hi, flip) : row_top<CT, true>(from, c0, r_lo, r_hi, flip);
+                {
                     red[(s * 2 + half) * kBM + m] = top;
                     kvc_tc::named_bar_sync(pair_bar, 64);
                     top = fmaxf(top, red[(s * 2 + (half ^ 1)) * kBM + m]);
@@ -842,21 +934,9 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                         m_run = top;
                     }
                     const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
-                    float ps0 = 0.f, ps1 = 0.f;
-#pragma unroll
-                    for (int c = 0; c < CT; c += 32) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const float p0 = kvc_tc::fast_exp2(fmaf(v[c + e], c_log2, neg_m));
-                            const float p1 = kvc_tc::fast_exp2(fmaf(v[c + e + 1], c_log2, neg_m));
-                            ps0 += p0;
-                            ps1 += p1;
-                            pk[e / 2] = kvc_tc::pack2<T>(p0, p1);
-                        }
-                        kvc_tc::st16(s_col + (CT * half + c) / 2, pk);
-                    }
-                    l_run = l_run * alpha + (ps0 + ps1);
+                    const float sum = plain ? row_weights<T, CT, false>(from, to, c0, r_lo, r_hi, flip, c_log2, neg_m)
+                                            : row_weights<T, CT, true>(from, to, c0, r_lo, r_hi, flip, c_log2, neg_m);
+                    l_run = l_run * alpha + sum;
                     if (__any_sync(0xffffffffu, rescale)) {
                         // the reference moved: rescale this thread's part of the O row
                         // (the products of the tile before; with two streams they were done before S was written)
@@ -864,7 +944,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                                         : wait_or_abort(&o_done[s ^ 1], ((used - 2) >> 1) & 1, abort_flag, a.status);
                         kvc_tc::fence_after();
 #pragma unroll 1
-                        for (int cc = half * (D / HALVES); cc < (half + 1) * (D / HALVES); cc += 32) {
+                        for (int cc = half * (D / 2); cc < (half + 1) * (D / 2); cc += 32) {
                             uint32_t o[32];
                             kvc_tc::ld32(lane_addr + stream * D + cc, o);
                             kvc_tc::wait_ld();
@@ -891,70 +971,68 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                                        : wait_or_abort(&o_done[last & 1], (last >> 1) & 1, abort_flag, a.status));
             }
             kvc_tc::fence_after();
+            const Segment seg = kept->seg[s_no & 1];
+            const int first = seg.i * a.item + (st.two ? stream * a.toks : 0), tok = m / a.group;
+            const bool there = tok < a.toks && first + tok < seg.n, whole = seg.t1 - seg.t0 == seg.tiles;
+            const int64_t out_row = (int64_t)(seg.row0 + first + tok) * a.q_heads + seg.h * a.group + (m - tok * a.group);
             const int64_t part = (2 * (int64_t)blockIdx.x + (s_no == 0 ? 0 : 1)) * TILES + (st.two ? stream : 0);
             float l = l_run, ref = m_run;
             float w0 = 1.f, w1 = 0.f;  // what the two streams' outputs of a row count
-            int col0 = 0, col1 = D;    // output columns of this thread
-            bool share = false;        // two threads have this row
-            if (HALVES == 2) {
-                // the sums change hands where the last tile's maxima did not
-                const uint32_t at = ((used - 1) & 1) ^ 1;
-                red[(at * 2 + half) * kBM + m] = l_run;
-                kvc_tc::named_bar_sync(pair_bar, 64);
-                l += red[(at * 2 + (half ^ 1)) * kBM + m];
-                col0 = half * (D / 2);
-                col1 = col0 + D / 2;
-            } else if (!st.two) {
-                // one query tile, two streams of keys: each thread joins half of the columns
-                red[(2 * side) * kBM + m] = m_run;
-                red[(2 * side + 1) * kBM + m] = l_run;
+            int col0 = half * (D / 2), cols = D / 2;  // output columns of this thread
+            // The halves' sums change hands where the maxima did (of the last tile: read, or its products would
+            // not be done; two buffers in turn: in the other one).
+            const uint32_t at = TILES == 2 ? stream : (used & 1);
+            red[(at * 2 + half) * kBM + m] = l_run;
+            kvc_tc::named_bar_sync(pair_bar, 64);
+            l += red[(at * 2 + (half ^ 1)) * kBM + m];
+            const bool share = TILES == 2 && !st.two;
+            if (share) {
+                // one query tile, two streams of keys: four threads have the row, each joins a quarter of the columns
                 kvc_tc::fence_before();
                 kvc_tc::named_bar_sync(all_bar, kSoftmax);
                 kvc_tc::fence_after();
+                red[(stream * 2 + half) * kBM + m] = half ? l : m_run;
+                kvc_tc::named_bar_sync(all_bar, kSoftmax);
                 const float m0 = red[m], l0 = red[kBM + m], m1 = red[2 * kBM + m], l1 = red[3 * kBM + m];
                 // (a stream without a visible key has no sum, and its output may hold anything)
                 ref = fmaxf(l0 == 0.f ? -INFINITY : m0, l1 == 0.f ? -INFINITY : m1);
                 w0 = l0 == 0.f ? -1.f : m0 == ref || ref == -INFINITY ? 1.f : kvc_tc::fast_exp2(m0 - ref);
                 w1 = l1 == 0.f ? -1.f : m1 == ref || ref == -INFINITY ? 1.f : kvc_tc::fast_exp2(m1 - ref);
                 l = (l0 == 0.f ? 0.f : l0 * w0) + (l1 == 0.f ? 0.f : l1 * w1);
-                col0 = side * (D / 2);
-                col1 = col0 + D / 2;
-                share = true;
+                cols = D / 4;
+                col0 += stream * cols;
             }
             if (active && ok) {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
-                for (int cc = col0; cc < col1; cc += 32) {
-                    uint32_t o[32];
+                for (int cc = col0; cc < col0 + cols; cc += 16) {
+                    uint32_t o[16];
                     if (!share) {
-                        kvc_tc::ld32(lane_addr + stream * D + cc, o);
+                        kvc_tc::ld16(lane_addr + stream * D + cc, o);
                         kvc_tc::wait_ld();
                     } else {
-                        uint32_t o1[32];
-                        kvc_tc::ld32(lane_addr + cc, o);
-                        kvc_tc::ld32(lane_addr + D + cc, o1);
+                        uint32_t o1[16];
+                        kvc_tc::ld16(lane_addr + cc, o);
+                        kvc_tc::ld16(lane_addr + D + cc, o1);
                         kvc_tc::wait_ld();
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) {
+                        for (int c = 0; c < 16; ++c) {
                             const float x = w0 >= 0.f ? __uint_as_float(o[c]) * w0 : 0.f;
                             o[c] = __float_as_uint(w1 >= 0.f ? fmaf(__uint_as_float(o1[c]), w1, x) : x);
                         }
                     }
                     if (!there)
                         continue;
-                    uint32_t bad = 0;
-#pragma unroll
-                    for (int w = 0; w < D / 32 / HALVES; ++w)
-                        bad = w == (cc - (HALVES == 2 ? col0 : 0)) / 32 ? nan_cols[w] : bad;
+                    const uint32_t bad = nans ? nan_cols[(cc - half * (D / 2)) / 32] >> (cc & 16) : 0u;
                     if (bad) {
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
+                        for (int c = 0; c < 16; ++c)
                             o[c] = bad >> c & 1u ? 0x7fc00000u : o[c];
                     }
                     if (whole) {
                         T *to = static_cast<T *>(a.out) + out_row * D + cc;
 #pragma unroll
-                        for (int c = 0; c < 32; c += 8) {
+                        for (int c = 0; c < 16; c += 8) {
                             uint4 x;
                             uint32_t *w = reinterpret_cast<uint32_t *>(&x);
 #pragma unroll
@@ -967,7 +1045,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                         // four columns of all 128 rows side by side, so that a warp's store is one run
                         uint4 *to = reinterpret_cast<uint4 *>(a.ws_o) + (part * (D / 4) + cc / 4) * kBM + m;
 #pragma unroll
-                        for (int c = 0; c < 32; c += 4)
+                        for (int c = 0; c < 16; c += 4)
                             to[c / 4 * kBM] = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
                     }
                 }
@@ -977,10 +1055,11 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 }
             }
             kvc_tc::fence_before();
-            if (TILES == 2 && !st.two)
+            if (share)
                 // both streams' outputs have been read, and the sums: the next segment may write them
                 kvc_tc::named_bar_sync(all_bar, kSoftmax);
-            cur = nxt;
+            // the next segment is there, and this one's rows and sums have been read
+            kvc_tc::named_bar_sync(stream_bar, 256);
         }
     }
 
@@ -1138,18 +1217,15 @@ kvc_status launch_attn(RaggedArgs &a, const void *q, const void *k, const void *
         return KVC_ERR_CUDA;
     auto kern = ragged_attn_kernel<T, D>;
     int dev = 0, optin = 0;
-    cudaFuncAttributes attr;
     if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
-        cudaFuncGetAttributes(&attr, kern) != cudaSuccess)
+        cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess)
         return KVC_ERR_CUDA;
     const size_t smem = std::min<size_t>((size_t)SM::TOTAL + 1024, (size_t)optin);
-    // (the softmax warps would wait for registers that the block does not have)
-    if (smem < (size_t)SM::TOTAL || attr.numRegs != kLaunchRegs)
+    if (smem < (size_t)SM::TOTAL)
         return KVC_ERR_UNSUPPORTED;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return KVC_ERR_CUDA;
-    kern<<<grid, kThreads, smem, stream>>>(tq, tk, tv, a);
+    kern<<<grid, SM::THREADS, smem, stream>>>(tq, tk, tv, a);
     if (grid > 1) {
         // may start while the attention runs, and waits for it
         cudaLaunchConfig_t cfg{};

@@ -75,6 +75,17 @@ __device__ __forceinline__ void ld32(uint32_t taddr, uint32_t *r)
                  : "r"(taddr));
 }
 
+// the same, 16 columns
+__device__ __forceinline__ void ld16(uint32_t taddr, uint32_t *r)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+                   "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+}
+
 __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t *r)
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -99,15 +110,32 @@ __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t *r)
                  : "memory");
 }
 
-// A warpgroup gives registers up (to N a thread) or takes some (waiting until they are free):
-// what a block's warpgroups hold together may not exceed what it was launched with.
-template <int N> __device__ __forceinline__ void regs_down()
+// wait_ld for values that a load was given: they are read behind it
+__device__ __forceinline__ void wait_ld32(uint32_t *r)
 {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27])
+                 :
+                 : "memory");
+    asm volatile("" : "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
 }
-template <int N> __device__ __forceinline__ void regs_up()
+
+// two float32 products and sums, or sums, in one instruction
+__device__ __forceinline__ uint64_t bits2(float2 x) { return *reinterpret_cast<const uint64_t *>(&x); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return *reinterpret_cast<const float2 *>(&d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
+    return *reinterpret_cast<const float2 *>(&d);
 }
 
 // Shared-memory matrix descriptor of a 128-byte-swizzled operand: rows of 128
