@@ -36,7 +36,7 @@ struct RaggedArgs {
     kvc_lengths len;
     int batch, tokens, q_heads, kv_heads, group;
     int toks, item;  // tokens of a query tile, of an item
-    int box_rows;    // rows of a TMA box of K or V
+    int box_rows;    // rows of a TMA box of K (of V: up to a slab's)
     int window;
     float scale_log2;
     float *ws_o, *ws_m, *ws_l;  // partial results: [2 * grid * tiles][D / 4][128][4], [..][128]
@@ -340,7 +340,7 @@ template <int D> struct Smem {
     static constexpr int TILES = D <= 128 ? 2 : 1;  // query tiles, streams
     static constexpr int SOFTMAX = TILES * 256;     // threads of the softmax warps: two a row
     static constexpr int THREADS = 128 + SOFTMAX;
-    static constexpr int KR = D <= 128 ? 128 : 64;  // rows of a slab
+    static constexpr int KR = D <= 128 ? 128 : 64;  // rows of a slab of V
     static constexpr int SPT = kBN / KR;            // slabs of a tile of K (or V)
     static constexpr int Q_TILE = kBM * D * 2, Q_BYTES = TILES * Q_TILE;
     static constexpr int SLAB = KR * D * 2;
@@ -386,39 +386,38 @@ template <typename T> __device__ __forceinline__ uint32_t not_finite(uint32_t w)
     return __vcmpeq2(w & ex, ex);
 }
 
-// Scores of the key rows from k0 on: those outside [r_lo, r_hi] become -infinity, and
-// a negative scale turns the others' sign (the maximum is of scale * score / |scale|).
-__device__ __forceinline__ void seen_only(uint32_t (&x)[32], int k0, int r_lo, int r_hi, uint32_t flip)
+// Scores of up to 32 columns: those outside [lo, hi] become -infinity, and a negative
+// scale turns the others' sign (the maximum is of scale * score / |scale|).
+template <int N> __device__ __forceinline__ void seen_only(uint32_t (&x)[N], int lo, int hi, uint32_t flip)
 {
-    const int lo = r_lo - k0, hi = r_hi - k0;
     uint32_t bits = lo > 0 ? lo < 32 ? ~0u << lo : 0u : ~0u;
     bits &= hi < 0 ? 0u : hi < 31 ? (2u << hi) - 1u : ~0u;
 #pragma unroll
-    for (int c = 0; c < 32; ++c)
+    for (int c = 0; c < N; ++c)
         x[c] = bits >> c & 1u ? x[c] ^ flip : 0xff800000u;
 }
 
-__device__ __forceinline__ float top_of(const uint32_t (&x)[32])
+template <int N> __device__ __forceinline__ float top_of(const uint32_t (&x)[N])
 {
     float m[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
         m[e] = fmaxf(__uint_as_float(x[e]), __uint_as_float(x[4 + e]));
 #pragma unroll
-    for (int c = 8; c < 32; c += 8)
+    for (int c = 8; c < N; c += 8)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             m[e] = fmaxf(fmaxf(m[e], __uint_as_float(x[c + e])), __uint_as_float(x[c + 4 + e]));
     return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
-// scores -> weights 2^(x c - m), summed in float32 and packed to 16-bit pairs in x[0..15]
-template <typename T>
-__device__ __forceinline__ void weights(uint32_t (&x)[32], float c_log2, float neg_m, float2 (&sum)[2])
+// scores -> weights 2^(x c - m), summed in float32 and packed to 16-bit pairs in the first half of x
+template <typename T, int N>
+__device__ __forceinline__ void weights(uint32_t (&x)[N], float c_log2, float neg_m, float2 (&sum)[2])
 {
     const float2 c2 = make_float2(c_log2, c_log2), m2 = make_float2(neg_m, neg_m);
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) {
+    for (int e = 0; e < N; e += 2) {
         const float2 z = kvc_tc::fma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2, m2);
         const float2 p = make_float2(kvc_tc::fast_exp2(z.x), kvc_tc::fast_exp2(z.y));
         sum[e / 2 % 2] = kvc_tc::add2(sum[e / 2 % 2], p);
@@ -426,13 +425,21 @@ __device__ __forceinline__ void weights(uint32_t (&x)[32], float c_log2, float n
     }
 }
 
-// The maximum and the weights of a row's CT scores in tensor memory (columns from key
-// row c0 on).  MASK: those of the key rows [r_lo, r_hi] count.  Both read the scores, 32
-// at a time in a rolled loop: unrolled, with the scores in registers from the maximum
-// to the exponential, a tile was longer than the instruction cache next to the tensor
-// cores' issue loops and took twice the time.
-template <int CT, bool MASK>
-__device__ __forceinline__ float row_top(uint32_t from, int c0, int r_lo, int r_hi, uint32_t flip)
+// The maximum of a row's CT scores in tensor memory, found as they are loaded; then of
+// those of the columns [lo, hi].
+template <int CT> __device__ __forceinline__ float row_top(uint32_t from)
+{
+    uint32_t x[32];
+    float mx = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < CT; c += 32) {
+        float top = kvc_tc::ld32_max(from + c, x);
+        kvc_tc::wait_ld_max(top);
+        mx = fmaxf(mx, top);
+    }
+    return mx;
+}
+template <int CT> __device__ __forceinline__ float row_top(uint32_t from, int lo, int hi, uint32_t flip)
 {
     uint32_t x[32];
     float mx = -INFINITY;
@@ -440,16 +447,19 @@ __device__ __forceinline__ float row_top(uint32_t from, int c0, int r_lo, int r_
     for (int c = 0; c < CT; c += 32) {
         kvc_tc::ld32(from + c, x);
         kvc_tc::wait_ld32(x);
-        if (MASK)
-            seen_only(x, c0 + c, r_lo, r_hi, flip);
+        seen_only(x, lo - c, hi - c, flip);
         mx = fmaxf(mx, top_of(x));
     }
     return mx;
 }
 
+// Scores -> weights in tensor memory, and their sum.  MASK: the scores of the columns
+// [lo, hi] count.  Read 32 at a time in a rolled loop: with a row's scores in registers
+// from the maximum to the exponential, and the code unrolled over them, a tile was
+// longer than the instruction cache next to the tensor cores' issue loops.
 template <typename T, int CT, bool MASK>
-__device__ __forceinline__ float row_weights(uint32_t from, uint32_t to, int c0, int r_lo, int r_hi, uint32_t flip,
-                                             float c_log2, float neg_m)
+__device__ __forceinline__ float row_weights(uint32_t from, uint32_t to, int lo, int hi, uint32_t flip, float c_log2,
+                                             float neg_m)
 {
     uint32_t x[32];
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -458,7 +468,7 @@ __device__ __forceinline__ float row_weights(uint32_t from, uint32_t to, int c0,
         kvc_tc::ld32(from + c, x);
         kvc_tc::wait_ld32(x);
         if (MASK)
-            seen_only(x, c0 + c, r_lo, r_hi, flip);
+            seen_only(x, lo - c, hi - c, flip);
         weights<T>(x, c_log2, neg_m, sum);
         kvc_tc::st16(to + c / 2, x);
     }
@@ -495,7 +505,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     using kvc_tc::wait_or_abort;
     constexpr int NSLAB = SM::NSLAB, SPT = SM::SPT, KR = SM::KR, TILES = SM::TILES, kSoftmax = SM::SOFTMAX, THREADS = SM::THREADS;
     constexpr uint32_t AB = std::is_same<T, __half>::value ? 0u : 1u;
-    constexpr uint32_t IDESC_S = kvc_tc::f16_idesc(AB, 0, kBM, KR);
+    constexpr uint32_t IDESC_S = kvc_tc::f16_idesc(AB, 0, kBM, kBN);
     constexpr uint32_t IDESC_O = kvc_tc::f16_idesc(AB, 1, kBM, D);
 
     extern __shared__ uint8_t smem_raw[];
@@ -551,14 +561,16 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     kvc_tc::fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t smem_base = kvc::smem_u32(smem);
-    // each role looks one segment ahead, so that the lengths are there when it gets to it
+    // (products and softmax look one segment ahead, so that the lengths are there when they get to it)
     Segment cur, nxt;
     bool more = walk.next(a, line.cost, cur);
 
     if (warp < 4) {
         if (warp == 1 || warp == 2) {
             // ======================= TMA producers of K and of V =======================
-            // Each lane finds the place of one of the next 32 boxes' rows, and issues one of the slab's boxes.
+            // A slab of K is all 128 rows and D / SPT columns of a tile, one of V KR rows and all columns (so that every
+            // product has 128 keys or D columns to its name).  Each lane finds the place of one of the next 32
+            // boxes' rows, and issues one of a slab's boxes.
             const bool mine_v = warp == 2;
             const CUtensorMap *tmap = mine_v ? &tmap_v : &tmap_k;
             if (lane == 0)
@@ -567,23 +579,25 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 a.split[blockIdx.x] = make_int4(0, 0, 0, 0);
             int q0 = 0;  // slabs of the segments before
             bool ok = true, first_segment = true;
-            const int pieces = KR / a.box_rows;  // of a slab's rows: a power of two up to 8
+            const int box = mine_v ? min(a.box_rows, KR) : a.box_rows, slab_rows = mine_v ? KR : kBN;
+            const int per_tile = kBN / box, pieces = slab_rows / box;  // boxes of a tile's, of a slab's rows: powers of two up to 8
+            const int blocks = mine_v ? D / 64 : D / 64 / SPT;         // column blocks of a slab
+            const int piece = lane / blocks, block = lane % blocks;
             uint32_t filled = 0, phase = 0;  // slots that this warp has filled, with the parity of the last time
             while (ok && more) {
                 const int nt = cur.t1 - cur.t0;
                 const uint32_t end = (uint32_t)cur.P + min(cur.n, (cur.i + 1) * a.item), first = (uint32_t)cur.lo + cur.t0 * kBN;
-                const bool again = walk.next(a, line.cost, nxt);
                 if (!mine_v && lane == 0 && cur.t0 == 0 && nt != cur.tiles)
                     a.split[blockIdx.x] = make_int4(cur.b, cur.h, cur.i,
                                                     2 * (line.of(cur.end - 1) - (int)blockIdx.x + 1) + (first_segment ? 0 : 1));
                 first_segment = false;
                 int32_t place = -1;
-                for (int u = 0; u < SPT * nt; ++u) {
-                    if ((u * pieces & 31) == 0) {
-                        const int w = u * pieces + lane;
-                        const uint32_t r = first + (uint32_t)w * a.box_rows;
+                for (int j = 0; ok && j < nt; ++j) {
+                    if ((j * per_tile & 31) == 0) {
+                        const int w = j * per_tile + lane;
+                        const uint32_t r = first + (uint32_t)w * box;
                         place = -1;
-                        if (w < SPT * nt * pieces && r < end) {
+                        if (w < nt * per_tile && r < end) {
                             const uint32_t page = r / (uint32_t)a.page_size;
                             const int32_t id = __ldg(a.table + (int64_t)cur.b * a.max_pages + page);
                             if (id >= 0 && id < a.n_pool)
@@ -592,48 +606,48 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                                 kvc::raise_status(a.status, KVC_DEV_INDEX_OOB);
                         }
                     }
-                    const int q = q0 + SPT * (mine_v ? v_group(u / SPT, nt) : k_group(u / SPT)) + u % SPT;
-                    const int slot = q % NSLAB;
-                    if (q >= NSLAB)
-                        ok = wait_or_abort(&empty[slot], ((q / NSLAB) - 1) & 1, abort_flag, a.status);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok)
-                        break;
-                    uint8_t *to = smem + SM::RING_OFF + slot * SM::SLAB;
-                    if (pieces == 1) {
-                        const int32_t y = __shfl_sync(0xffffffffu, place, u & 31);
-                        if (lane == 0) {
-                            if (y < 0) {
-                                // nothing to read: the slot keeps what it holds, and its columns are masked
-                                kvc::mbar_arrive(&full[slot]);
-                            } else {
-                                kvc::mbar_arrive_expect_tx(&full[slot], SM::SLAB);
-                                kvc::tma_load_3d(to, tmap, 0, y, 0, &full[slot]);
+                    for (int u = 0; u < SPT; ++u) {
+                        const int q = q0 + SPT * (mine_v ? v_group(j, nt) : k_group(j)) + u, slot = q % NSLAB;
+                        if (q >= NSLAB)
+                            ok = wait_or_abort(&empty[slot], ((q / NSLAB) - 1) & 1, abort_flag, a.status);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok)
+                            break;
+                        uint8_t *to = smem + SM::RING_OFF + slot * SM::SLAB;
+                        const int at = j * per_tile + (mine_v ? u * pieces : 0), block0 = mine_v ? 0 : u * blocks;
+                        const int32_t y = __shfl_sync(0xffffffffu, place, (at + (pieces == 1 ? 0 : piece)) & 31);
+                        if (pieces == 1) {
+                            if (lane == 0) {
+                                if (y < 0) {
+                                    // nothing to read: the slot keeps what it holds, and its columns are masked
+                                    kvc::mbar_arrive(&full[slot]);
+                                } else {
+                                    kvc::mbar_arrive_expect_tx(&full[slot], SM::SLAB);
+                                    kvc::tma_load_3d(to, tmap, 0, y, block0, &full[slot]);
+                                }
                             }
-                        }
-                    } else {
-                        // boxes of 64 columns, piece by piece
-                        const int piece = lane / (D / 64), c = lane % (D / 64);
-                        const int32_t y = __shfl_sync(0xffffffffu, place, (u * pieces + piece) & 31);
-                        const bool load = piece < pieces && y >= 0;
-                        const int n = __popc(__ballot_sync(0xffffffffu, load));
-                        if (lane == 0) {
-                            if (n == 0)
-                                kvc::mbar_arrive(&full[slot]);
-                            else
-                                kvc::mbar_arrive_expect_tx(&full[slot], n * a.box_rows * 128);
+                        } else {
+                            // boxes of 64 columns, piece by piece
+                            const bool load = piece < pieces && y >= 0;
+                            const int n = __popc(__ballot_sync(0xffffffffu, load));
+                            if (lane == 0) {
+                                if (n == 0)
+                                    kvc::mbar_arrive(&full[slot]);
+                                else
+                                    kvc::mbar_arrive_expect_tx(&full[slot], n * box * 128);
+                            }
+                            __syncwarp();
+                            if (load)
+                                kvc::tma_load_3d(to + block * (slab_rows * 128) + piece * box * 128, tmap, 0, y,
+                                                 block0 + block, &full[slot]);
                         }
                         __syncwarp();
-                        if (load)
-                            kvc::tma_load_3d(to + c * (KR * 128) + piece * a.box_rows * 128, tmap, 0, y, c, &full[slot]);
+                        filled |= 1u << slot;
+                        phase = (phase & ~(1u << slot)) | ((uint32_t)((q / NSLAB) & 1) << slot);
                     }
-                    __syncwarp();
-                    filled |= 1u << slot;
-                    phase = (phase & ~(1u << slot)) | ((uint32_t)((q / NSLAB) & 1) << slot);
                 }
                 q0 += 2 * SPT * nt;
-                cur = nxt;
-                more = again;
+                more = walk.next(a, line.cost, cur);
             }
             if (*abort_flag && lane == 0)
                 // wind-down: let the loads in flight land before the CTA exits
@@ -739,14 +753,14 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                                 if (!(ok = wait_or_abort(&full[slot], (q / NSLAB) & 1, abort_flag, a.status)))
                                     break;
                                 kvc_tc::fence_after();
-                                const uint64_t qd = q_desc + (uint64_t)((st.two ? k : 0) * (SM::Q_TILE / 16));
+                                const uint64_t qd = q_desc + (uint64_t)(((st.two ? k : 0) * SM::Q_TILE + hf * (D / 64 / SPT) * (kBM * 128)) / 16);
                                 const uint64_t kd = k_ring + (uint64_t)(slot * (SM::SLAB / 16));
-                                const uint32_t d_s = tmem + SM::COL_S + s * kBN + hf * KR;
+                                const uint32_t d_s = tmem + SM::COL_S + s * kBN;
 #pragma unroll
-                                for (int ks = 0; ks < D / 16; ++ks)
+                                for (int ks = 0; ks < D / 16 / SPT; ++ks)
                                     kvc_tc::mma_ss(d_s, qd + (uint64_t)(((ks >> 2) * (kBM * 128) + (ks & 3) * 32) / 16),
-                                                   kd + (uint64_t)(((ks >> 2) * (KR * 128) + (ks & 3) * 32) / 16), IDESC_S,
-                                                   ks > 0);
+                                                   kd + (uint64_t)(((ks >> 2) * (kBN * 128) + (ks & 3) * 32) / 16), IDESC_S,
+                                                   hf > 0 || ks > 0);
                                 if (last)
                                     kvc_tc::commit(&empty[slot]);
                             }
@@ -771,20 +785,20 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         // ======================= softmax =======================
         // A warp whose wait gave up goes on through the tiles without work or waits: the barriers
         // below have no limit, and every warp comes to each of them.
-        constexpr int CT = kBN / 2;  // columns of a thread
-        const int tid = threadIdx.x - 128, quad = warp & 3, half = (warp >> 2) & 1 ^ 1, stream = (warp - 4) >> 3;
+        constexpr int CT = kBN / 2, OT = D / 2;  // columns of S and of O of a thread
+        const int tid = threadIdx.x - 128, quad = warp & 3, half = ((warp - 4) >> 2) & 1, stream = (warp - 4) >> 3;
         const int m = quad * 32 + lane;  // row of the tile
         const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
         float *red = reinterpret_cast<float *>(smem + SM::RED_OFF);
         uint32_t *bad_sh = reinterpret_cast<uint32_t *>(smem + SM::BAD_OFF);
         constexpr uint32_t all_bar = 1;
-        const uint32_t pair_bar = 2 + 4 * stream + quad;  // of the row's two threads
+        const uint32_t pair_bar = 2 + 4 * stream + quad;  // of a row's two threads
         const float c_log2 = fabsf(a.scale_log2);
         const uint32_t flip = a.scale_log2 < 0.f ? 0x80000000u : 0u;
         const uint32_t stream_bar = 10 + stream;
         // what a tile does not need, kept apart from the registers that its scores take
         Kept *kept = reinterpret_cast<Kept *>(smem + SM::WALK_OFF) + stream;
-        const bool scout = (warp & 7) == 4;  // of a stream's warps, the one that looks ahead
+        const bool scout = quad == 0 && half == 0;  // of a stream's warps, the one that looks ahead
         if (scout && lane == 0) {
             kept->walk = walk;
             kept->seg[0] = cur;
@@ -796,23 +810,28 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         bool ok = true;
         for (int s_no = 0; *(volatile int *)&kept->more[s_no & 1]; ++s_no) {
             Streams st;
-            bool active;          // the warp has rows at all
-            int r_lo, r_hi;       // this row sees the key rows [r_lo, r_hi]; one without a query nothing in particular
-            int whole_lo, whole_hi;  // what every row of the item sees: up to its first token, from the last one's window on
-            int lo0;
+            bool active;           // the warp has rows at all
+            int head_cut, tail_cut;  // tiles [0, head_cut) and from tail_cut on are cut
             {
                 const Segment seg = kept->seg[s_no & 1];
                 st = Streams::of<TILES>(a, seg);
-                const int first = seg.i * a.item + (st.two ? stream * a.toks : 0);  // the tile's first token
-                const int tok = m / a.group, pos = seg.P + first + tok;
-                const bool there = tok < a.toks && first + tok < seg.n;
-                active = first + quad * 32 / a.group < seg.n;
-                r_hi = there ? pos : INT_MAX;
-                r_lo = there && a.window > 0 ? max(0, pos - a.window + 1) : 0;
-                whole_hi = seg.P + seg.i * a.item;
-                whole_lo = a.window > 0 ? seg.P + min(seg.n, (seg.i + 1) * a.item) - a.window : 0;
-                lo0 = seg.lo + seg.t0 * kBN;
+                active = seg.i * a.item + (st.two ? stream * a.toks : 0) + quad * 32 / a.group < seg.n;
+                // what every row of the item sees: up to its first token, from the last one's window on
+                const int lo0 = seg.lo + seg.t0 * kBN, hi = seg.P + seg.i * a.item;
+                const int lo = a.window > 0 ? seg.P + min(seg.n, (seg.i + 1) * a.item) - a.window : 0;
+                head_cut = lo > lo0 ? (lo - lo0 + kBN - 1) / kBN : 0;
+                tail_cut = hi + 1 > lo0 ? (hi + 1 - lo0) / kBN : 0;
             }
+            // This row sees the key rows [r_lo, r_hi], counted from tile j's first one; a row without a query
+            // nothing in particular.  (Made again for each cut tile: kept, they cost registers in all others.)
+            auto rows_seen = [&](int j, int &r_lo, int &r_hi) {
+                const Segment &seg = kept->seg[s_no & 1];
+                const int tok = m / a.group, i = seg.i * a.item + (st.two ? stream * a.toks : 0) + tok;
+                const int pos = seg.P + i - (seg.lo + (seg.t0 + j) * kBN);
+                const bool there = tok < a.toks && i < seg.n;
+                r_hi = there ? pos : INT_MAX / 2;
+                r_lo = there && a.window > 0 ? pos - a.window + 1 : INT_MIN / 2;
+            };
             if (scout && lane == 0) {
                 Walk next = kept->walk;
                 kept->more[(s_no + 1) & 1] = next.next(a, line.cost, kept->seg[(s_no + 1) & 1]);
@@ -820,12 +839,12 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             }
             __syncwarp();
             // output columns in which the row has seen a NaN or an infinity, in cut tiles (written once there is one)
-            volatile uint32_t nan_cols[D / 64];
+            volatile uint32_t nan_cols[OT / 32];
             bool nans = false;
             float m_run = -INFINITY, l_run = 0.f;
             for (int j = 0; j < st.n; ++j) {
-                const int t_lo = lo0 + j * kBN;
-                if (t_lo + kBN - 1 > whole_hi || t_lo < whole_lo) {
+                const bool cut = j < head_cut || j >= tail_cut;
+                if (cut) {
                     // V rows with a NaN or an infinity in them, a bit each in bad_sh (zero before)
                     bool found = false;
 #pragma unroll
@@ -847,26 +866,28 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     }
                     if (kvc_tc::named_bar_any(all_bar, kSoftmax, found)) {
                         // what this row sees of them is written down by column, then they are zeros for all
+                        int r_lo, r_hi;
+                        rows_seen(j, r_lo, r_hi);
 #pragma unroll 1
                         for (int e = 0; e < 4; ++e) {
-                            uint32_t left = ok && r_hi != INT_MAX ? bad_sh[e] : 0u;
+                            uint32_t left = ok && r_hi < INT_MAX / 2 ? bad_sh[e] : 0u;
                             while (left) {
                                 const int vr = 32 * e + __ffs(left) - 1, in = vr & (KR - 1);
                                 left &= left - 1;
-                                if (t_lo + vr < r_lo || t_lo + vr > r_hi)
+                                if (vr < r_lo || vr > r_hi)
                                     continue;
                                 if (!nans)
-                                    for (int w = 0; w < D / 64; ++w)
+                                    for (int w = 0; w < OT / 32; ++w)
                                         nan_cols[w] = 0;
                                 nans = true;
                                 const uint8_t *slab =
                                     smem + SM::RING_OFF + (q0 + SPT * v_group(j, st.n) + vr / KR) % NSLAB * SM::SLAB;
 #pragma unroll 1
-                                for (int w = 0; w < D / 64; ++w) {
+                                for (int w = 0; w < OT / 32; ++w) {
                                     uint32_t cols = 0;
 #pragma unroll 1
                                     for (int c = 0; c < 4; ++c) {
-                                        const int ch = half * (D / 16) + 4 * w + c;  // 16 bytes of the row
+                                        const int ch = half * (OT / 8) + 4 * w + c;  // 16 bytes of the row
                                         const uint4 x = *reinterpret_cast<const uint4 *>(
                                             slab + (ch >> 3) * (KR * 128) + in * 128 + ((ch & 7) ^ (in & 7)) * 16);
                                         const uint32_t nf[4] = {not_finite<T>(x.x), not_finite<T>(x.y), not_finite<T>(x.z),
@@ -908,22 +929,23 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 ok = ok && wait_or_abort(&s_full[s], parity, abort_flag, a.status);
                 ++used;
                 kvc_tc::fence_after();
-                const int c0 = t_lo + CT * half;  // key row of this thread's first column
                 // the weights of either half go where its own scores were, so that neither waits for the other
                 const uint32_t from = s_col + CT * half, to = s_col + CT * half;
-                // tiles whose scores are taken as they are (all of the warp's rows see all of its columns) apart
-                // from those that are looked at one by one
-                const bool plain = __all_sync(0xffffffffu, c0 >= r_lo && c0 + CT - 1 <= r_hi) && !flip;
                 float top = -INFINITY;
-                if (active && ok)
-                    top = plain ? row_top<CT, false>(from, c0, r_lo, r_hi, flip) : row_top<CT, true>(from, c0, r_lo, r_hi, flip);
-                {
-                    red[(s * 2 + half) * kBM + m] = top;
-                    kvc_tc::named_bar_sync(pair_bar, 64);
-                    top = fmaxf(top, red[(s * 2 + (half ^ 1)) * kBM + m]);
+                // (every row sees all of a whole tile)
+                const bool plain = !cut && !flip;
+                int lo = 0, hi = 0;
+                if (!plain) {
+                    rows_seen(j, lo, hi);
+                    lo -= CT * half;
+                    hi -= CT * half;
                 }
+                if (active && ok)
+                    top = plain ? row_top<CT>(from) : row_top<CT>(from, lo, hi, flip);
+                red[(s * 2 + half) * kBM + m] = top;
+                kvc_tc::named_bar_sync(pair_bar, 64);
                 if (active && ok) {
-                    top *= c_log2;
+                    top = fmaxf(top, red[(s * 2 + (half ^ 1)) * kBM + m]) * c_log2;
                     float alpha = 1.f;
                     bool rescale = false;
                     if (top > m_run + kRescale || (m_run == -INFINITY && top > -INFINITY)) {
@@ -934,8 +956,8 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                         m_run = top;
                     }
                     const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
-                    const float sum = plain ? row_weights<T, CT, false>(from, to, c0, r_lo, r_hi, flip, c_log2, neg_m)
-                                            : row_weights<T, CT, true>(from, to, c0, r_lo, r_hi, flip, c_log2, neg_m);
+                    const float sum = plain ? row_weights<T, CT, false>(from, to, lo, hi, flip, c_log2, neg_m)
+                                            : row_weights<T, CT, true>(from, to, lo, hi, flip, c_log2, neg_m);
                     l_run = l_run * alpha + sum;
                     if (__any_sync(0xffffffffu, rescale)) {
                         // the reference moved: rescale this thread's part of the O row
@@ -944,7 +966,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                                         : wait_or_abort(&o_done[s ^ 1], ((used - 2) >> 1) & 1, abort_flag, a.status);
                         kvc_tc::fence_after();
 #pragma unroll 1
-                        for (int cc = half * (D / 2); cc < (half + 1) * (D / 2); cc += 32) {
+                        for (int cc = half * OT; cc < (half + 1) * OT; cc += 32) {
                             uint32_t o[32];
                             kvc_tc::ld32(lane_addr + stream * D + cc, o);
                             kvc_tc::wait_ld();
@@ -978,7 +1000,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             const int64_t part = (2 * (int64_t)blockIdx.x + (s_no == 0 ? 0 : 1)) * TILES + (st.two ? stream : 0);
             float l = l_run, ref = m_run;
             float w0 = 1.f, w1 = 0.f;  // what the two streams' outputs of a row count
-            int col0 = half * (D / 2), cols = D / 2;  // output columns of this thread
+            int col0 = half * OT, cols = OT;  // output columns of this thread
             // The halves' sums change hands where the maxima did (of the last tile: read, or its products would
             // not be done; two buffers in turn: in the other one).
             const uint32_t at = TILES == 2 ? stream : (used & 1);
@@ -999,7 +1021,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 w0 = l0 == 0.f ? -1.f : m0 == ref || ref == -INFINITY ? 1.f : kvc_tc::fast_exp2(m0 - ref);
                 w1 = l1 == 0.f ? -1.f : m1 == ref || ref == -INFINITY ? 1.f : kvc_tc::fast_exp2(m1 - ref);
                 l = (l0 == 0.f ? 0.f : l0 * w0) + (l1 == 0.f ? 0.f : l1 * w1);
-                cols = D / 4;
+                cols = OT / 2;
                 col0 += stream * cols;
             }
             if (active && ok) {
@@ -1023,7 +1045,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     }
                     if (!there)
                         continue;
-                    const uint32_t bad = nans ? nan_cols[(cc - half * (D / 2)) / 32] >> (cc & 16) : 0u;
+                    const uint32_t bad = nans ? nan_cols[(cc - half * OT) / 32] >> (cc & 16) : 0u;
                     if (bad) {
 #pragma unroll
                         for (int c = 0; c < 16; ++c)
@@ -1208,12 +1230,14 @@ kvc_status launch_attn(RaggedArgs &a, const void *q, const void *k, const void *
     const CUtensorMapDataType tt = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                                   : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const uint64_t rows = (uint64_t)a.n_pool * a.page_size * a.kv_heads;
-    const int blocks = a.box_rows == SM::KR ? D / 64 : 1;  // column blocks of a box of K or V
+    // column blocks of a box: a slab's, where the box has all its rows
+    const int k_blocks = a.box_rows == kBN ? D / 64 / SM::SPT : 1, v_rows = std::min(a.box_rows, SM::KR),
+              v_blocks = v_rows == SM::KR ? D / 64 : 1;
     CUtensorMap tq, tk, tv;
     if (!kvc_host::encode_4d_blocks_sw128(&tq, q, (uint64_t)a.tokens, (uint64_t)a.q_heads, D, 2, (uint32_t)a.group,
                                           (uint32_t)a.toks, tt, 1) ||
-        !kvc_host::encode_3d_sw128(&tk, k, rows, D, a.box_rows, blocks, tt) ||
-        !kvc_host::encode_3d_sw128(&tv, v, rows, D, a.box_rows, blocks, tt))
+        !kvc_host::encode_3d_sw128(&tk, k, rows, D, a.box_rows, k_blocks, tt) ||
+        !kvc_host::encode_3d_sw128(&tv, v, rows, D, v_rows, v_blocks, tt))
         return KVC_ERR_CUDA;
     auto kern = ragged_attn_kernel<T, D>;
     int dev = 0, optin = 0;
@@ -1334,8 +1358,8 @@ KVC_API kvc_status kvc_gqa_ragged(void *out, const void *q, const void *k_pool, 
     a.group = q_heads / kv_heads;
     a.toks = kBM / a.group;
     a.item = a.toks * (head_dim <= 128 ? 2 : 1);
-    // rows of a box: as many as a slab holds that no page's end cuts
-    a.box_rows = head_dim <= 128 ? 128 : 64;
+    // rows of a box: as many of a tile's that no page's end cuts
+    a.box_rows = kBN;
     while (page_size % a.box_rows)
         a.box_rows /= 2;
     a.window = local_window_size;

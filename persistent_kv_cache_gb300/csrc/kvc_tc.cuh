@@ -123,6 +123,28 @@ __device__ __forceinline__ void wait_ld32(uint32_t *r)
     asm volatile("" : "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
 }
 
+// ld32, and the largest of the 32 (a NaN counts for nothing) with it
+__device__ __forceinline__ float ld32_max(uint32_t taddr, uint32_t *r)
+{
+    float m;
+    asm volatile("tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+                   "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+                   "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+                   "=r"(r[30]), "=r"(r[31]), "=f"(m)
+                 : "r"(taddr));
+    return m;
+}
+// wait_ld for the maximum of such a load
+__device__ __forceinline__ void wait_ld_max(float &a)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(a) : : "memory");
+}
+
 // two float32 products and sums, or sums, in one instruction
 __device__ __forceinline__ uint64_t bits2(float2 x) { return *reinterpret_cast<const uint64_t *>(&x); }
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
