@@ -13,6 +13,7 @@
 #include <type_traits>
 
 #include "kvc_common.cuh"
+#include "kvc_tc.cuh"
 
 namespace {
 
@@ -304,46 +305,65 @@ struct TurnRates {
     uint64_t per[kMaxPairs];
 };
 
-// cos and sin of x / 2^64 turns: the nearest quarter turn in whole numbers, the
-// rest, at most an eighth, in float32
-__device__ __forceinline__ void turn(uint64_t x, float &c, float &s)
+// cos and sin of x / 2^32 turns: the nearest quarter turn in whole numbers, the rest u,
+// at most an eighth of a turn, by the Taylor series of sin and cos of 2 pi u (terms
+// (2 pi)^k / k!; the first left out are below 2^-29).  With sincospif, which reduces
+// its argument again, the 131072 x 64 table took 34 us.
+__device__ __forceinline__ void turn(uint32_t x, float magnitude, float &c, float &s)
 {
-    const uint32_t q = (uint32_t)((x + (1ull << 61)) >> 62);
-    const int64_t rest = (int64_t)(x - ((uint64_t)q << 62));
-    float sn, cs;
-    sincospif((float)rest * 0x1p-63f, &sn, &cs);
-    c = q & 1u ? sn : cs;
-    s = q & 1u ? cs : sn;
-    // quarter turns 1 and 2 have a negative cosine, 2 and 3 a negative sine
-    c = (q + 1u) & 2u ? -c : c;
-    s = q & 2u ? -s : s;
+    const uint32_t q = (x + (1u << 29)) >> 30;
+    const float u = (float)(int32_t)(x - (q << 30)) * 0x1p-32f, z = u * u;
+    float sn = 42.0586939f, cs = -26.4262568f;
+    sn = fmaf(sn, z, -76.7058598f);
+    sn = fmaf(sn, z, 81.6052493f);
+    sn = fmaf(sn, z, -41.3417022f);
+    sn = fmaf(sn, z, 6.28318531f) * u;
+    cs = fmaf(cs, z, 60.2446414f);
+    cs = fmaf(cs, z, -85.4568172f);
+    cs = fmaf(cs, z, 64.939394f);
+    cs = fmaf(cs, z, -19.7392088f);
+    cs = fmaf(cs, z, 1.f);
+    // an odd number of quarter turns exchanges the two; one or two of them make the cosine negative, two or
+    // three the sine
+    const uint32_t flip_c = (q + 1u) << 30 & 0x80000000u, flip_s = q << 30 & 0x80000000u;
+    c = __uint_as_float(__float_as_uint(q & 1u ? sn : cs) ^ flip_c) * magnitude;
+    s = __uint_as_float(__float_as_uint(q & 1u ? cs : sn) ^ flip_s) * magnitude;
 }
 
+// VEC columns of kPositions positions a thread
+constexpr int kPositions = 4;
 template <int VEC>
 __global__ void __launch_bounds__(256)
 rope_tables_kernel(float *__restrict__ cos_t, float *__restrict__ sin_t, int64_t first, int64_t positions, int half,
                    const __grid_constant__ TurnRates rates, float magnitude)
 {
     const int pieces = half / VEC;
-    const int64_t w = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    const int64_t p = w / pieces;
-    if (p >= positions)
+    const int64_t w = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, step = (positions + kPositions - 1) / kPositions;
+    const int64_t p0 = w / pieces;
+    const int i0 = (int)(w - p0 * pieces) * VEC;
+    if (p0 >= step)
         return;
-    const int i0 = (int)(w - p * pieces) * VEC;
-    float c[VEC], s[VEC];
+    uint64_t rate[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        turn((uint64_t)(first + p) * rates.per[i0 + e], c[e], s[e]);
-        c[e] *= magnitude;
-        s[e] *= magnitude;
-    }
-    const int64_t at = p * half + i0;
-    if constexpr (VEC == 4) {
-        *reinterpret_cast<float4 *>(cos_t + at) = make_float4(c[0], c[1], c[2], c[3]);
-        *reinterpret_cast<float4 *>(sin_t + at) = make_float4(s[0], s[1], s[2], s[3]);
-    } else {
-        cos_t[at] = c[0];
-        sin_t[at] = s[0];
+    for (int e = 0; e < VEC; ++e)
+        rate[e] = rates.per[i0 + e];
+#pragma unroll
+    for (int k = 0; k < kPositions; ++k) {
+        const int64_t p = p0 + k * step;
+        if (p >= positions)
+            return;
+        float c[VEC], s[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            turn((uint32_t)(((uint64_t)(first + p) * rate[e] + 0x80000000u) >> 32), magnitude, c[e], s[e]);
+        const int64_t at = p * half + i0;
+        if constexpr (VEC == 4) {
+            *reinterpret_cast<float4 *>(cos_t + at) = make_float4(c[0], c[1], c[2], c[3]);
+            *reinterpret_cast<float4 *>(sin_t + at) = make_float4(s[0], s[1], s[2], s[3]);
+        } else {
+            cos_t[at] = c[0];
+            sin_t[at] = s[0];
+        }
     }
 }
 
@@ -364,119 +384,200 @@ struct AppendArgs {
     int interleaved;
     const float *cos_t, *sin_t;
     int64_t rope_max_pos;
-    int split;     // parts of a token's rows (gridDim.y)
+    int part;      // of a token's rows, that a block has (gridDim.y parts)
     int32_t *status;
 };
 
-// A row (one head of one token) is LPR lanes of eight columns each.  GPT groups
-// of LPR lanes share a token's rows, so that a lane's cos, sin and weights stay
-// in registers from row to row; a block holds 256 / LPR / GPT tokens.
-template <typename T, int LPR>
-__global__ void __launch_bounds__(256)
-ragged_append_kernel(const AppendArgs a, int gpt)
+// two 16-bit values -> float32, and back
+template <typename T> __device__ __forceinline__ float2 unpack2(uint32_t w)
 {
-    const int group = threadIdx.x / LPR, lane = threadIdx.x % LPR;
-    const int t = blockIdx.x * (256 / LPR / gpt) + group / gpt;
-    const int c0 = lane * 8;
-    const bool mine = c0 < a.D;
-    // (a warp's groups may be at rows of different kinds)
-    const uint32_t peers = LPR == 32 ? 0xffffffffu : ((1u << (LPR & 31)) - 1u) << (threadIdx.x & 31 & ~(LPR - 1));
-    const int slot = t < a.tokens ? a.slots[t] : -1;
-    const int pos = t < a.tokens ? a.positions[t] : -1;
-    bool there = slot >= 0;
-    if (there) {
-        const uint32_t bad = (slot >= a.rows ? KVC_DEV_INDEX_OOB : 0u) |
-                             (a.cos_t && (pos < 0 || pos >= a.rope_max_pos) ? KVC_DEV_ROPE_RANGE : 0u);
-        if (bad) {
-            if (lane == 0)
-                kvc::raise_status(a.status, bad);
-            there = false;
+    if constexpr (std::is_same<T, __half>::value)
+        return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    else
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// A row (one head of one token) is LPR lanes of eight columns each.  A block holds
+// 256 / LPR / share tokens and the same part of each one's rows (its queries, keys and
+// values one behind the other), which `share` groups of LPR lanes have between them.  A
+// column of a query or key becomes
+//     (x cos w + x' sin w') / rms
+// with its partner x' (of the lane that holds the pair's other half, or the same
+// word), the sine negative for a pair's first; cos w and sin w' are made once for the
+// token's rows that a group has (a dozen where there are tokens enough: with three rows
+// a group, making them took more instructions than the rows).  Products and the sum are rounded separately: without a norm w and 1 / rms
+// are 1 and the bits those of the other calls' rotation.  A lane asks for kAhead rows
+// before it works on the first (one at a time held the pass to 2.6 TB/s).
+constexpr int kAhead = 4;
+enum Turn { kNoTurn, kHalves, kNeighbours };
+
+template <typename T, int LPR, bool NORM, int TURN>
+__device__ __forceinline__ void append_rows(const AppendArgs &a, int first, int end, int step, bool mine, uint32_t peers,
+                                            const T *from, T *to, int64_t to_step, bool turns, int other,
+                                            const float2 (&cs)[4], const float2 (&sn)[4])
+{
+    using kvc_tc::add2;
+    using kvc_tc::mul2;
+    const float by_d = 1.f / (float)a.D;
+    const int64_t from_step = (int64_t)a.D * step;
+    from += first * (int64_t)a.D;
+    to += first * to_step;
+    to_step *= step;
+    for (int r0 = first; r0 < end; r0 += kAhead * step) {
+        uint4 raw[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            raw[u] = make_uint4(0, 0, 0, 0);
+            if (mine && r0 + u * step < end)
+                raw[u] = *reinterpret_cast<const uint4 *>(from);
+            from += from_step;
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u, to += to_step) {
+            if (r0 + u * step >= end)
+                break;
+            if constexpr (NORM || TURN != kNoTurn) {
+                uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+                float2 x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[e] = unpack2<T>(w[e]);
+                float by = 1.f;
+                if constexpr (NORM) {
+                    float2 s2 = mul2(x[0], x[0]);
+#pragma unroll
+                    for (int e = 1; e < 4; ++e)
+                        s2 = kvc_tc::fma2(x[e], x[e], s2);
+                    float sum = s2.x + s2.y;
+#pragma unroll
+                    for (int d = LPR / 2; d; d >>= 1)
+                        sum += __shfl_xor_sync(peers, sum, d, LPR);
+                    by = rsqrtf(fmaf(sum, by_d, a.eps));
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float2 z = mul2(x[e], cs[e]);
+                    if constexpr (TURN != kNoTurn) {
+                        const uint32_t o = TURN == kHalves ? __shfl_sync(peers, w[e], other, LPR) : __byte_perm(w[e], 0, 0x1032);
+                        // (a column that is not turned has no partner)
+                        z = add2(z, mul2(unpack2<T>(turns ? o : 0u), sn[e]));
+                    }
+                    if constexpr (NORM)
+                        z = mul2(z, make_float2(by, by));
+                    const uint32_t y = kvc_tc::pack2<T>(z.x, z.y);
+                    w[e] = NORM || turns ? y : w[e];
+                }
+                raw[u] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            if (mine)
+                *reinterpret_cast<uint4 *>(to) = raw[u];
         }
     }
+}
+
+template <typename T, int LPR>
+__global__ void __launch_bounds__(256, 4)
+ragged_append_kernel(const AppendArgs a, int share)
+{
+    const int group = threadIdx.x / LPR, lane = threadIdx.x % LPR;
+    const int t = blockIdx.x * (256 / LPR / share) + group / share;
+    const int c0 = lane * 8;
+    // (a warp's groups may be at different tokens)
+    const uint32_t peers = LPR == 32 ? 0xffffffffu : ((1u << (LPR & 31)) - 1u) << (threadIdx.x & 31 & ~(LPR - 1));
+    const int r0 = blockIdx.y * a.part, r1 = min(r0 + a.part, a.q_heads + 2 * a.kv_heads);  // of the token's rows
+    const int lead = group % share;
+    const int slot = t < a.tokens ? a.slots[t] : -1;
+    const int pos = t < a.tokens ? a.positions[t] : -1;
+    if (slot < 0)
+        return;
+    const uint32_t bad = (slot >= a.rows ? KVC_DEV_INDEX_OOB : 0u) |
+                         (a.cos_t && (pos < 0 || pos >= a.rope_max_pos) ? KVC_DEV_ROPE_RANGE : 0u);
+    if (bad) {
+        if (lane == 0)
+            kvc::raise_status(a.status, bad);
+        return;
+    }
+    const bool mine = c0 < a.D;
     const int half = a.turned / 2;
     const bool turns = a.cos_t && c0 < a.turned;  // (a multiple of 16: whole lanes turn or stay)
     const bool low = c0 < half;
-    float cs[8], sn[8];
-    if (there && turns) {
-        if (a.interleaved) {
-            const float *c = a.cos_t + (int64_t)pos * half + c0 / 2, *s = a.sin_t + (int64_t)pos * half + c0 / 2;
-            const float4 x = *reinterpret_cast<const float4 *>(c), y = *reinterpret_cast<const float4 *>(s);
-            cs[0] = x.x, cs[1] = x.y, cs[2] = x.z, cs[3] = x.w;
-            sn[0] = y.x, sn[1] = y.y, sn[2] = y.z, sn[3] = y.w;
-        } else {
+    // the lane that holds the other half of this one's pairs
+    const int other = a.interleaved || !turns ? lane : low ? lane + half / 8 : lane - half / 8;
+    auto factors = [&](const void *weight, float2 (&cs)[4], float2 (&sn)[4]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            cs[e] = make_float2(1.f, 1.f);
+            sn[e] = make_float2(0.f, 0.f);
+        }
+        if (turns && a.interleaved) {
+            const int64_t at = (int64_t)pos * half + c0 / 2;
+            const float4 x = *reinterpret_cast<const float4 *>(a.cos_t + at);
+            const float4 y = *reinterpret_cast<const float4 *>(a.sin_t + at);
+            cs[0] = make_float2(x.x, x.x), cs[1] = make_float2(x.y, x.y), cs[2] = make_float2(x.z, x.z), cs[3] = make_float2(x.w, x.w);
+            sn[0] = make_float2(-y.x, y.x), sn[1] = make_float2(-y.y, y.y), sn[2] = make_float2(-y.z, y.z), sn[3] = make_float2(-y.w, y.w);
+        } else if (turns) {
             const int64_t at = (int64_t)pos * half + (low ? c0 : c0 - half);
+            const float sign = low ? -1.f : 1.f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float4 x = *reinterpret_cast<const float4 *>(a.cos_t + at + 4 * e);
                 const float4 y = *reinterpret_cast<const float4 *>(a.sin_t + at + 4 * e);
-                cs[4 * e] = x.x, cs[4 * e + 1] = x.y, cs[4 * e + 2] = x.z, cs[4 * e + 3] = x.w;
-                sn[4 * e] = y.x, sn[4 * e + 1] = y.y, sn[4 * e + 2] = y.z, sn[4 * e + 3] = y.w;
+                cs[2 * e] = make_float2(x.x, x.y), cs[2 * e + 1] = make_float2(x.z, x.w);
+                sn[2 * e] = make_float2(sign * y.x, sign * y.y), sn[2 * e + 1] = make_float2(sign * y.z, sign * y.w);
             }
         }
-    }
-    // the lane that holds the other half of this one's pairs
-    const int other = a.interleaved || !turns ? lane : low ? lane + half / 8 : lane - half / 8;
-    const int rows = a.q_heads + 2 * a.kv_heads;
-    const int64_t page = there ? slot / a.page_size : 0, in_page = there ? slot % a.page_size : 0;
-    for (int r = group % gpt + blockIdx.y * gpt; r < rows; r += gpt * a.split) {
-        const bool is_q = r < a.q_heads, is_v = r >= a.q_heads + a.kv_heads;
-        const int h = is_q ? r : is_v ? r - a.q_heads - a.kv_heads : r - a.q_heads;
-        const T *from = static_cast<const T *>(is_q ? a.q : is_v ? a.v : a.k) +
-                        t * (is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride) + (int64_t)h * a.D + c0;
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (there && mine)
-            raw = *reinterpret_cast<const uint4 *>(from);
-        const void *weight = is_q ? a.q_weight : is_v ? nullptr : a.k_weight;
-        if (!is_v && (weight || a.cos_t)) {
-            T *x = reinterpret_cast<T *>(&raw);
-            float f[8];
+        if (weight) {
+            uint4 w4 = make_uint4(0, 0, 0, 0);
+            if (mine)
+                w4 = *reinterpret_cast<const uint4 *>(static_cast<const T *>(weight) + c0);
+            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                f[e] = kvc::Elem<T>::to_f32(x[e]);
-            if (weight) {
-                float sum = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    sum = fmaf(f[e], f[e], sum);
-#pragma unroll
-                for (int d = LPR / 2; d; d >>= 1)
-                    sum += __shfl_xor_sync(peers, sum, d, LPR);
-                const float by = rsqrtf(sum / (float)a.D + a.eps);
-                uint4 w4 = make_uint4(0, 0, 0, 0);
-                if (mine)
-                    w4 = *reinterpret_cast<const uint4 *>(static_cast<const T *>(weight) + c0);
-                const T *w = reinterpret_cast<const T *>(&w4);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    f[e] = f[e] * by * kvc::Elem<T>::to_f32(w[e]);
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t o = a.interleaved ? __byte_perm(w[e], 0, 0x1032) : __shfl_sync(peers, w[e], other, LPR);
+                cs[e] = kvc_tc::mul2(cs[e], unpack2<T>(w[e]));
+                sn[e] = kvc_tc::mul2(sn[e], unpack2<T>(o));
             }
-            if (a.cos_t) {
-                if (a.interleaved) {
-                    if (turns) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            kvc::rope_pair(f[2 * e], f[2 * e + 1], cs[e], sn[e]);
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float o = __shfl_sync(peers, f[e], other, LPR);
-                        float lo = low ? f[e] : o, hi = low ? o : f[e];
-                        kvc::rope_pair(lo, hi, cs[e], sn[e]);
-                        f[e] = !turns ? f[e] : low ? lo : hi;
-                    }
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                x[e] = kvc::Elem<T>::from_f32(f[e]);
         }
-        if (there && mine) {
-            T *to = is_q ? static_cast<T *>(a.q_out) + ((int64_t)t * a.q_heads + h) * a.D
-                         : static_cast<T *>(is_v ? a.v_pool : a.k_pool) +
-                               ((page * a.kv_heads + h) * a.page_size + in_page) * a.D;
-            *reinterpret_cast<uint4 *>(to + c0) = raw;
+    };
+    const int page = slot / a.page_size, in_page = slot - page * a.page_size;
+    const int64_t kv_to = ((int64_t)page * a.kv_heads * a.page_size + in_page) * a.D + c0, kv_step = (int64_t)a.page_size * a.D;
+    const int k0 = a.q_heads, v0 = k0 + a.kv_heads;
+#pragma unroll 1
+    for (int kind = 0; kind < 3; ++kind) {
+        // the block's rows of the token's queries, keys or values
+        const int from = kind == 0 ? 0 : kind == 1 ? k0 : v0, to = kind == 0 ? k0 : kind == 1 ? v0 : v0 + a.kv_heads;
+        const int begin = max(r0, from) - from + lead, end = min(r1, to) - from;
+        if (r0 >= to || r1 <= from)
+            continue;
+        const T *src = kind == 0   ? static_cast<const T *>(a.q) + t * a.q_stride
+                       : kind == 1 ? static_cast<const T *>(a.k) + t * a.k_stride
+                                   : static_cast<const T *>(a.v) + t * a.v_stride;
+        T *dst = kind == 0   ? static_cast<T *>(a.q_out) + (int64_t)t * a.q_heads * a.D + c0
+                 : kind == 1 ? static_cast<T *>(a.k_pool) + kv_to
+                             : static_cast<T *>(a.v_pool) + kv_to;
+        const int64_t dst_step = kind == 0 ? a.D : kv_step;
+        const void *weight = kind == 0 ? a.q_weight : kind == 1 ? a.k_weight : nullptr;
+        float2 cs[4], sn[4];
+        auto run = [&](auto norm, auto turn) {
+            append_rows<T, LPR, decltype(norm)::value, decltype(turn)::value>(a, begin, end, share, mine, peers, src + c0, dst,
+                                                                              dst_step, turns, other, cs, sn);
+        };
+        using std::integral_constant;
+        if (kind == 2 || (!weight && !a.cos_t)) {
+            run(std::false_type{}, integral_constant<int, kNoTurn>{});
+            continue;
         }
+        factors(weight, cs, sn);
+        if (!a.cos_t)
+            run(std::true_type{}, integral_constant<int, kNoTurn>{});
+        else if (a.interleaved && weight)
+            run(std::true_type{}, integral_constant<int, kNeighbours>{});
+        else if (a.interleaved)
+            run(std::false_type{}, integral_constant<int, kNeighbours>{});
+        else if (weight)
+            run(std::true_type{}, integral_constant<int, kHalves>{});
+        else
+            run(std::false_type{}, integral_constant<int, kHalves>{});
     }
 }
 
@@ -486,31 +587,33 @@ template <typename T> void launch_append(const AppendArgs &a, cudaStream_t strea
     int lpr = 2;
     while (lpr * 8 < a.D)
         lpr *= 2;
-    const int groups = 256 / lpr;
-    int gpt = 1;
-    while (gpt < groups && gpt < rows)
-        gpt *= 2;
-    const int per_block = groups / gpt;
+    const int groups = 256 / lpr, sms = kvc_host::sm_count();
+    // Rows of a group: a dozen, or as few as make four blocks an SM; the groups of a token in parts of its rows,
+    // at least three where there are that many groups, so that most have to do with one kind alone.
+    const int each = (int)std::max<int64_t>(1, std::min<int64_t>(12, (int64_t)a.tokens * rows / ((int64_t)groups * 4 * sms)));
+    int share = 1;
+    while (share < groups && 2 * share * 3 * each <= rows)
+        share *= 2;
+    const int per_block = groups / share;
     AppendArgs b = a;
-    const int blocks = (a.tokens + per_block - 1) / per_block;
-    // few tokens: a token's rows go to several blocks
-    b.split = std::max(1, std::min((rows + gpt - 1) / gpt, 4 * kvc_host::sm_count() / std::max(1, blocks)));
-    const dim3 grid(blocks, b.split);
+    const int parts = (rows + share * each - 1) / (share * each);
+    b.part = (rows + parts - 1) / parts;
+    const dim3 grid((a.tokens + per_block - 1) / per_block, (rows + b.part - 1) / b.part);
     switch (lpr) {
     case 2:
-        ragged_append_kernel<T, 2><<<grid, 256, 0, stream>>>(b, gpt);
+        ragged_append_kernel<T, 2><<<grid, 256, 0, stream>>>(b, share);
         break;
     case 4:
-        ragged_append_kernel<T, 4><<<grid, 256, 0, stream>>>(b, gpt);
+        ragged_append_kernel<T, 4><<<grid, 256, 0, stream>>>(b, share);
         break;
     case 8:
-        ragged_append_kernel<T, 8><<<grid, 256, 0, stream>>>(b, gpt);
+        ragged_append_kernel<T, 8><<<grid, 256, 0, stream>>>(b, share);
         break;
     case 16:
-        ragged_append_kernel<T, 16><<<grid, 256, 0, stream>>>(b, gpt);
+        ragged_append_kernel<T, 16><<<grid, 256, 0, stream>>>(b, share);
         break;
     default:
-        ragged_append_kernel<T, 32><<<grid, 256, 0, stream>>>(b, gpt);
+        ragged_append_kernel<T, 32><<<grid, 256, 0, stream>>>(b, share);
         break;
     }
 }
@@ -612,7 +715,7 @@ KVC_API kvc_status kvc_rope_tables(float *cos_table, float *sin_table, int64_t f
         rates.per[i] = (uint64_t)std::ldexp(rest, 63) * 2;
     }
     const int vec = half % 4 == 0 && kvc_host::aligned16(cos_table) && kvc_host::aligned16(sin_table) ? 4 : 1;
-    const int64_t blocks = (positions * (half / vec) + 255) / 256;
+    const int64_t blocks = ((positions + kPositions - 1) / kPositions * (half / vec) + 255) / 256;
     if (blocks > INT32_MAX)
         return KVC_ERR_SHAPE;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);

@@ -145,12 +145,18 @@ __device__ __forceinline__ void wait_ld_max(float &a)
     asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(a) : : "memory");
 }
 
-// two float32 products and sums, or sums, in one instruction
+// two float32 products and sums, sums, or products in one instruction
 __device__ __forceinline__ uint64_t bits2(float2 x) { return *reinterpret_cast<const uint64_t *>(&x); }
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {
     uint64_t d;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return *reinterpret_cast<const float2 *>(&d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
     return *reinterpret_cast<const float2 *>(&d);
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b)
