@@ -36,6 +36,7 @@ struct RaggedArgs {
     kvc_lengths len;
     int batch, tokens, q_heads, kv_heads, group;
     int toks, item;  // tokens of a query tile, of an item
+    int one, two;    // what a key of an item of one, of two query tiles counts
     int box_rows;    // rows of a TMA box of K (of V: up to a slab's)
     int window;
     float scale_log2;
@@ -96,8 +97,27 @@ __device__ __forceinline__ int64_t keys_before(const RaggedArgs &a, const Reques
     return sum;
 }
 
+// what a key of item i counts
+__device__ __forceinline__ int weight_of(const RaggedArgs &a, const Request &r, int i)
+{
+    return r.n - i * a.item <= a.toks ? a.one : a.two;
+}
+
+// the same of the items before j, with what each key counts (all items but the last
+// have two query tiles) and with every item's cost
+__device__ __forceinline__ int64_t units_before(const RaggedArgs &a, const Request &r, int j, int cost)
+{
+    int64_t sum = keys_before(a, r, j) * a.two + (int64_t)j * cost;
+    if (j > 0 && j == r.items) {
+        int lo, hi;
+        key_range(a, r, j - 1, lo, hi);
+        sum -= (int64_t)(hi - lo) * (a.two - weight_of(a, r, j - 1));
+    }
+    return sum;
+}
+
 // All items laid end to end (request, then kv head, then item; each as long as its
-// keys and `cost`) are one line, cut into equal shares: every CTA gets the
+// keys count and `cost`) are one line, cut into equal shares: every CTA gets the
 // same work whatever the lengths, and the split is the same on every run.
 struct Line {
     int grid, cost;
@@ -113,20 +133,20 @@ struct Line {
 // A row of t key tiles is done soonest by about sqrt(7 t) CTAs, since joining costs
 // each part about half a tile's time: with so few rows that this leaves CTAs
 // over, rows begin with a CTA each and cost nothing beside their keys.
-__device__ __forceinline__ Line make_line(int64_t keys, int64_t rows, int grid)
+__device__ __forceinline__ Line make_line(const RaggedArgs &a, int64_t units, int64_t rows, int grid)
 {
     Line l;
-    l.cost = kItemCost;
-    const float t = fmaxf(1.f, (float)keys / (128.f * (float)max(rows, (int64_t)1)));
+    l.cost = kItemCost * a.one;
+    const float t = fmaxf(1.f, (float)units / (128.f * a.one * (float)max(rows, (int64_t)1)));
     const int64_t few = rows * (int64_t)ceilf(sqrtf(7.f * t));
     l.grid = grid;
     if (few <= grid) {
         l.grid = (int)max(few, (int64_t)1);
         l.cost = 0;
     }
-    int64_t total = keys + rows * l.cost;
+    int64_t total = units + rows * l.cost;
     // no share shorter than a tile: no segment of a row between two others is empty
-    l.grid = (int)max((int64_t)1, min((int64_t)l.grid, total / kBN));
+    l.grid = (int)max((int64_t)1, min((int64_t)l.grid, total / (kBN * a.two)));
     l.each = total / l.grid;
     l.longer = total % l.grid;
     return l;
@@ -158,7 +178,8 @@ struct Walk {
             }
             int lo, hi;
             key_range(a, r, i, lo, hi);
-            const int64_t keys = hi - lo, end = base + keys + cost;
+            const int weight = weight_of(a, r, i);
+            const int64_t end = base + (int64_t)(hi - lo) * weight + cost;
             s.b = b;
             s.h = h;
             s.i = i;
@@ -168,10 +189,10 @@ struct Walk {
             s.lo = lo & ~(a.box_rows - 1);
             s.tiles = (hi - s.lo + kBN - 1) / kBN;
             s.end = end;
-            // the keys that stand for the item's cost hold none
+            // (what stands for the item's cost comes first and holds no keys; positions over 128 fit 32 bits)
             const int64_t p0 = x - base - cost, p1 = x_end - base - cost;
-            s.t0 = p0 <= 0 ? 0 : (int)(p0 / kBN);
-            s.t1 = x_end >= end ? s.tiles : p1 <= 0 ? 0 : (int)(p1 / kBN);
+            s.t0 = p0 <= 0 ? 0 : (int)((uint32_t)(p0 / kBN) / (uint32_t)weight);
+            s.t1 = x_end >= end ? s.tiles : p1 <= 0 ? 0 : (int)((uint32_t)(p1 / kBN) / (uint32_t)weight);
             if (x_end >= end) {
                 x = base = end;
                 ++i;
@@ -185,14 +206,14 @@ struct Walk {
     }
 };
 
-// The CTA's share: the requests' keys and items summed by groups of 32 (a warp a
+// The CTA's share: the requests' units and items summed by groups of 32 (a warp a
 // group), the sums in shared memory, then the group, the request and the item of the
 // share's first unit.  `scratch` holds 12 bytes a group.
 template <int THREADS>
 __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch, int grid, Walk &w)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, groups = (a.batch + 31) / 32;
-    int64_t *keys = reinterpret_cast<int64_t *>(scratch);
+    int64_t *units = reinterpret_cast<int64_t *>(scratch);
     int *rows = reinterpret_cast<int *>(scratch + 8 * (size_t)groups);
     for (int g = warp; g < groups; g += THREADS / 32) {
         const int b = 32 * g + lane;
@@ -203,7 +224,7 @@ __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch
             const Request r = request(a, b, bad);
             if (bad && blockIdx.x == 0)
                 kvc::raise_status(a.status, bad);
-            k = keys_before(a, r, r.items);
+            k = units_before(a, r, r.items, 0);
             n = r.items;
         }
 #pragma unroll
@@ -212,14 +233,14 @@ __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch
             n += __shfl_xor_sync(0xffffffffu, n, d);
         }
         if (lane == 0) {
-            keys[g] = k;
+            units[g] = k;
             rows[g] = n;
         }
     }
     __syncthreads();
     int64_t k = 0, n = 0;
     for (int g = lane; g < groups; g += 32) {
-        k += keys[g];
+        k += units[g];
         n += rows[g];
     }
 #pragma unroll
@@ -227,7 +248,7 @@ __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch
         k += __shfl_xor_sync(0xffffffffu, k, d);
         n += __shfl_xor_sync(0xffffffffu, n, d);
     }
-    const Line line = make_line(k * a.kv_heads, n * a.kv_heads, grid);
+    const Line line = make_line(a, k * a.kv_heads, n * a.kv_heads, grid);
     w.x = w.x_end = 0;
     if (n > 0 && blockIdx.x < line.grid) {
         w.x = line.begin(blockIdx.x);
@@ -239,7 +260,7 @@ __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch
         int at = 0;
         for (int g0 = 0; g0 < groups; g0 += 32) {
             const int g = g0 + lane;
-            const int64_t len = g < groups ? (keys[g] + (int64_t)rows[g] * line.cost) * a.kv_heads : 0;
+            const int64_t len = g < groups ? (units[g] + (int64_t)rows[g] * line.cost) * a.kv_heads : 0;
             int64_t inc = len;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -263,7 +284,7 @@ __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch
             Request r{0, 0, 0, 0};
             if (b < a.batch)
                 r = request(a, b, bad);
-            const int64_t len = (keys_before(a, r, r.items) + (int64_t)r.items * line.cost) * a.kv_heads;
+            const int64_t len = units_before(a, r, r.items, line.cost) * a.kv_heads;
             int64_t inc = len;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -280,19 +301,19 @@ __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch
             w.r.items = __shfl_sync(0xffffffffu, r.items, first);
         }
         // the kv head and the item: the last that begins at x or before it
-        const int64_t head = keys_before(a, w.r, w.r.items) + (int64_t)w.r.items * line.cost;
+        const int64_t head = units_before(a, w.r, w.r.items, line.cost);
         w.h = (int)((w.x - before) / head);
         before += w.h * head;
         int low = 0, count = w.r.items;  // among [low, low + count)
         while (count > 1) {
             const int step = (count + 31) / 32, j = low + lane * step;
-            const bool begun = lane * step < count && before + keys_before(a, w.r, j) + (int64_t)j * line.cost <= w.x;
+            const bool begun = lane * step < count && before + units_before(a, w.r, j, line.cost) <= w.x;
             const int last = 31 - __clz(__ballot_sync(0xffffffffu, begun));
             low += last * step;
             count = min(step, count - last * step);
         }
         w.i = low;
-        w.base = before + keys_before(a, w.r, low) + (int64_t)low * line.cost;
+        w.base = before + units_before(a, w.r, low, line.cost);
     }
     __syncthreads();
     return line;
@@ -325,9 +346,12 @@ __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch
 // are masked ("cut" tiles).  A NaN or an infinity in a column of V makes that column of
 // the output NaN for the rows that see it, and for no other.  In whole tiles the
 // products do that by themselves.  In cut tiles 0 x NaN would reach the rows that
-// do not see it, and a page's rows behind the request's last may hold anything:
-// there the softmax warps look through V in shared memory, write down for each row
-// the columns of such values that it sees, and put zeros in their place.
+// do not see it, and rows that no token of the item sees (behind the last one, before a
+// window) may hold anything: there the softmax warps look through V in shared memory,
+// write down for each row the columns of such values that it sees, and put zeros in
+// their place.  (Zeros for the rows that none sees, without looking, took longer: by the
+// warp of the output products, or by the stream's warps before they give the weights,
+// 672 and 665 us for 645 in chunks of 8 prompts.)
 
 // The segments of a stream's softmax warps: one warp looks one ahead for all.
 struct Kept {
@@ -366,8 +390,10 @@ template <int D> struct Smem {
     static constexpr int TOTAL = WALK_OFF + 2 * (int)sizeof(Kept);
     static_assert(TOTAL <= BUDGET && NSLAB >= 2 * SPT + 1, "a tile of K, one of V and the next slab must fit");
     static_assert(NSLAB * SLAB >= 12 * ((kMaxRequests + 31) / 32), "the groups' sums lie where the ring will");
-    static constexpr uint32_t COL_S = TILES * D, TMEM_COLS = 512;
-    static_assert(COL_S + 2 * kBN <= TMEM_COLS, "tensor memory");
+    // the weights have columns of their own where there are some left: the next scores need not wait for them to be read
+    static constexpr bool OWN_P = D == 64;
+    static constexpr uint32_t COL_S = TILES * D, COL_P = OWN_P ? COL_S + 2 * kBN : COL_S, TMEM_COLS = 512;
+    static_assert(COL_S + 2 * kBN + (OWN_P ? 2 * 64 : 0) <= TMEM_COLS, "tensor memory");
 };
 
 // The ring holds, for a segment of n tiles, K_0, K_1, then V_j and K_{j+2} while
@@ -658,7 +684,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             // ======================= output products =======================
             if (lane == 0) {
                 const uint64_t v_ring = kvc_tc::sw128_desc(smem_base + SM::RING_OFF, KR * 128);
-                int q0 = 0;              // slabs of the segments before
+                int q0 = 0;                 // slabs of the segments before
                 uint32_t used[2] = {0, 0};  // tiles that went through each score buffer
                 bool ok = true;
                 while (ok && more) {
@@ -683,11 +709,11 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                                     break;
                                 kvc_tc::fence_after();
                                 const uint64_t vd = v_ring + (uint64_t)(slot * (SM::SLAB / 16));
-                                // (the weights of 64 keys are 32 columns, the next ones' begin 64 further on)
-                                const uint32_t pa = tmem + SM::COL_S + s * kBN + hf * 64;
+                                // (the weights of 64 keys are 32 columns; over the scores, the next ones' begin 64 further on)
+                                const uint32_t pa = tmem + SM::COL_P + s * (SM::OWN_P ? 64 : kBN) + hf * 64;
 #pragma unroll
                                 for (int k2 = 0; k2 < KR / 16; ++k2)
-                                    kvc_tc::mma_ts(tmem + (TILES == 2 ? k * D : 0), pa + k2 / 4 * 64 + k2 % 4 * 8,
+                                    kvc_tc::mma_ts(tmem + (TILES == 2 ? k * D : 0), pa + k2 / 4 * (SM::OWN_P ? 32 : 64) + k2 % 4 * 8,
                                                    vd + (uint64_t)(k2 * (2048 / 16)), IDESC_O,
                                                    !fresh || hf > 0 || k2 > 0);
                                 if (last)
@@ -742,9 +768,11 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                             uint32_t &u = used[TILES == 2 ? k : 0];
                             // Scores are written where the output products of the tile before (256: before last) read
                             // their weights.  Products of another accumulator or shape are not ordered by their
-                            // issue: the wait for those is what keeps the weights.
+                            // issue: the wait for those is what keeps the weights.  (Weights in columns of their own:
+                            // where the softmax warps read the scores before, until they gave the weights.)
                             const uint32_t before = TILES == 2 ? u : u >> 1;
-                            if (before > 0 && !(ok = wait_or_abort(&o_done[s], (before - 1) & 1, abort_flag, a.status)))
+                            if (before > 0 && !(ok = wait_or_abort(SM::OWN_P ? &p_full[s] : &o_done[s], (before - 1) & 1,
+                                                                   abort_flag, a.status)))
                                 break;
                             kvc_tc::fence_after();
                             const bool last = TILES == 1 || !st.two || k == 1;
@@ -930,7 +958,8 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 ++used;
                 kvc_tc::fence_after();
                 // the weights of either half go where its own scores were, so that neither waits for the other
-                const uint32_t from = s_col + CT * half, to = s_col + CT * half;
+                const uint32_t from = s_col + CT * half;
+                const uint32_t to = SM::OWN_P ? lane_addr + SM::COL_P + s * 64 + 32 * half : from;
                 float top = -INFINITY;
                 // (every row sees all of a whole tile)
                 const bool plain = !cut && !flip;
@@ -956,6 +985,11 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                         m_run = top;
                     }
                     const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+                    if (SM::OWN_P && used > 1) {
+                        // the products of the tile before have read its weights
+                        ok = wait_or_abort(&o_done[s], (used - 2) & 1, abort_flag, a.status);
+                        kvc_tc::fence_after();
+                    }
                     const float sum = plain ? row_weights<T, CT, false>(from, to, lo, hi, flip, c_log2, neg_m)
                                             : row_weights<T, CT, true>(from, to, lo, hi, flip, c_log2, neg_m);
                     l_run = l_run * alpha + sum;
@@ -1097,7 +1131,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 // share of exactly one CTA, which the block takes its number from and which has
 // written down which item that is.  A block takes 16 rows at a time: a row a
 // thread's low bits, so that 16 threads read a run of 256 bytes.
-constexpr int kMergeRows = 16, kMergeBlocks = 4;
+constexpr int kMergeRows = 16;
 template <typename T, int D>
 __global__ void __launch_bounds__(256)
 ragged_merge_kernel(const RaggedArgs a)
@@ -1253,7 +1287,10 @@ kvc_status launch_attn(RaggedArgs &a, const void *q, const void *k, const void *
     if (grid > 1) {
         // may start while the attention runs, and waits for it
         cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(grid - 1, kMergeBlocks);
+        // blocks for the rows that an item has if requests are alike (they go round for more)
+        const int64_t rows_each = (int64_t)((a.tokens + a.batch - 1) / a.batch) * a.group;
+        cfg.gridDim = dim3(grid - 1, (unsigned)std::min<int64_t>((rows_each + kMergeRows - 1) / kMergeRows,
+                                                                 SM::TILES * kBM / kMergeRows));
         cfg.blockDim = dim3(256);
         cfg.stream = stream;
         cudaLaunchAttribute la[1];
@@ -1358,6 +1395,10 @@ KVC_API kvc_status kvc_gqa_ragged(void *out, const void *q, const void *k_pool, 
     a.group = q_heads / kv_heads;
     a.toks = kBM / a.group;
     a.item = a.toks * (head_dim <= 128 ? 2 : 1);
+    // (an item of one query tile has both streams for its keys: half the time for each, but with head_dim 128 its
+    // bytes take more than that)
+    a.one = head_dim == 128 ? 2 : 1;
+    a.two = head_dim == 128 ? 3 : head_dim == 64 ? 2 : 1;
     // rows of a box: as many of a tile's that no page's end cuts
     a.box_rows = kBN;
     while (page_size % a.box_rows)
