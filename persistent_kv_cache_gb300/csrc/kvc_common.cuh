@@ -353,6 +353,25 @@ inline kvc_status launch_status()
     return cudaGetLastError() == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }
 
+// A launch that may start while the kernel before it in the stream ends (or, once all
+// of that one's blocks have said so, runs): the kernel has grid_dep_wait() before the
+// first thing that it reads or writes.
+template <typename... A, typename... B>
+cudaError_t launch_chained(void (*kern)(A...), dim3 grid, int threads, size_t smem, cudaStream_t stream, const B &...args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, A(args)...);
+}
+
 inline bool lengths_ok(const kvc_lengths &l)
 {
     return l.past_abs && l.total_abs && l.cache_past && l.cache_total && l.evict;

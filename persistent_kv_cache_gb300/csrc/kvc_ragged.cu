@@ -82,6 +82,7 @@ page_release_kernel(const ReleaseArgs a)
 {
     extern __shared__ int32_t place[];  // [batch], -1: nothing goes back
     __shared__ int64_t sums[kPlanThreads / 32];
+    kvc::grid_dep_wait();
     const int64_t depth = a.stack.depth(a.status);
     int64_t before = 0;
     int given = 0;  // pages that rows of this thread give back, for the number left
@@ -153,6 +154,7 @@ ragged_plan_kernel(const PlanArgs a)
     __shared__ int64_t sums[kPlanThreads / 32];
     int32_t *begin = plan;                // [batch + 1] first token
     int32_t *taken = plan + a.batch + 1;  // [batch] pages that requests before it take, -1: rejected
+    kvc::grid_dep_wait();
     const int64_t depth = a.stack.depth(a.status), capacity = (int64_t)a.max_pages * a.page_size;
     const bool writer = blockIdx.x == 0;
     int64_t tokens_before = 0, pages_before = 0, left = depth;
@@ -486,6 +488,7 @@ ragged_append_kernel(const AppendArgs a, int share)
     const uint32_t peers = LPR == 32 ? 0xffffffffu : ((1u << (LPR & 31)) - 1u) << (threadIdx.x & 31 & ~(LPR - 1));
     const int r0 = blockIdx.y * a.part, r1 = min(r0 + a.part, a.q_heads + 2 * a.kv_heads);  // of the token's rows
     const int lead = group % share;
+    kvc::grid_dep_wait();
     const int slot = t < a.tokens ? a.slots[t] : -1;
     const int pos = t < a.tokens ? a.positions[t] : -1;
     if (slot < 0)
@@ -581,7 +584,7 @@ ragged_append_kernel(const AppendArgs a, int share)
     }
 }
 
-template <typename T> void launch_append(const AppendArgs &a, cudaStream_t stream)
+template <typename T> cudaError_t launch_append(const AppendArgs &a, cudaStream_t stream)
 {
     const int rows = a.q_heads + 2 * a.kv_heads;
     int lpr = 2;
@@ -601,20 +604,15 @@ template <typename T> void launch_append(const AppendArgs &a, cudaStream_t strea
     const dim3 grid((a.tokens + per_block - 1) / per_block, (rows + b.part - 1) / b.part);
     switch (lpr) {
     case 2:
-        ragged_append_kernel<T, 2><<<grid, 256, 0, stream>>>(b, share);
-        break;
+        return kvc_host::launch_chained(ragged_append_kernel<T, 2>, grid, 256, 0, stream, b, share);
     case 4:
-        ragged_append_kernel<T, 4><<<grid, 256, 0, stream>>>(b, share);
-        break;
+        return kvc_host::launch_chained(ragged_append_kernel<T, 4>, grid, 256, 0, stream, b, share);
     case 8:
-        ragged_append_kernel<T, 8><<<grid, 256, 0, stream>>>(b, share);
-        break;
+        return kvc_host::launch_chained(ragged_append_kernel<T, 8>, grid, 256, 0, stream, b, share);
     case 16:
-        ragged_append_kernel<T, 16><<<grid, 256, 0, stream>>>(b, share);
-        break;
+        return kvc_host::launch_chained(ragged_append_kernel<T, 16>, grid, 256, 0, stream, b, share);
     default:
-        ragged_append_kernel<T, 32><<<grid, 256, 0, stream>>>(b, share);
-        break;
+        return kvc_host::launch_chained(ragged_append_kernel<T, 32>, grid, 256, 0, stream, b, share);
     }
 }
 
@@ -638,7 +636,9 @@ KVC_API kvc_status kvc_page_release(const int32_t *released, const int32_t *bloc
         return KVC_ERR_CUDA;
     const int rows = kPlanThreads / 32;
     const int grid = std::max(1, std::min((batch + rows - 1) / rows, kvc_host::sm_count()));
-    page_release_kernel<<<grid, kPlanThreads, smem, static_cast<cudaStream_t>(stream_)>>>(a);
+    if (kvc_host::launch_chained(page_release_kernel, dim3(grid), kPlanThreads, smem, static_cast<cudaStream_t>(stream_), a) !=
+        cudaSuccess)
+        return KVC_ERR_CUDA;
     return kvc_host::launch_status();
 }
 
@@ -666,7 +666,9 @@ KVC_API kvc_status kvc_ragged_plan(const int32_t *cached, const int32_t *new_tok
     if (!allow_smem(ragged_plan_kernel, smem))
         return KVC_ERR_CUDA;
     const int grid = std::max(1, (int)(((int64_t)tokens + kPlanTokens - 1) / kPlanTokens));
-    ragged_plan_kernel<<<grid, kPlanThreads, smem, static_cast<cudaStream_t>(stream_)>>>(a);
+    if (kvc_host::launch_chained(ragged_plan_kernel, dim3(grid), kPlanThreads, smem, static_cast<cudaStream_t>(stream_), a) !=
+        cudaSuccess)
+        return KVC_ERR_CUDA;
     return kvc_host::launch_status();
 }
 
@@ -791,9 +793,7 @@ KVC_API kvc_status kvc_ragged_append(void *q_out, void *k_pool, void *v_pool, co
                        slots, tokens, q_heads, kv_heads, head_dim, page_size, n_pool_pages * page_size,
                        rope_cos ? rotary_dim : 0, interleaved, rope_cos, rope_sin, rope_max_pos, 1, dev_status};
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-    if (dtype == KVC_BF16)
-        launch_append<__nv_bfloat16>(a, stream);
-    else
-        launch_append<__half>(a, stream);
+    if ((dtype == KVC_BF16 ? launch_append<__nv_bfloat16>(a, stream) : launch_append<__half>(a, stream)) != cudaSuccess)
+        return KVC_ERR_CUDA;
     return kvc_host::launch_status();
 }

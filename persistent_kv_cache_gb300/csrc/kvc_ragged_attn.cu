@@ -37,12 +37,13 @@ struct RaggedArgs {
     int batch, tokens, q_heads, kv_heads, group;
     int toks, item;  // tokens of a query tile, of an item
     int one, two;    // what a key of an item of one, of two query tiles counts
+    int streams;     // of softmax and products in a CTA
     int box_rows;    // rows of a TMA box of K (of V: up to a slab's)
     int window;
     float scale_log2;
     float *ws_o, *ws_m, *ws_l;  // partial results: [2 * grid * tiles][D / 4][128][4], [..][128]
-    int4 *split;  // [grid] the item of which a CTA has the first keys but not the last: request, kv head, item,
-                  // 2 * parts + slot of its own part (parts 0: there is none)
+    int4 *split;  // [grid] the item of which a CTA has the first keys but not the last: its first row, its tokens, kv
+                  // head, 2 * parts + slot of its own part (parts 0: there is none)
     int32_t *status;
 };
 
@@ -130,14 +131,14 @@ struct Line {
     }
 };
 
-// A row of t key tiles is done soonest by about sqrt(7 t) CTAs, since joining costs
-// each part about half a tile's time: with so few rows that this leaves CTAs
-// over, rows begin with a CTA each and cost nothing beside their keys.
+// What `streams` key tiles of a row take a CTA, the join of two parts takes for each: a
+// row of t such is done soonest by about sqrt(7 t) CTAs.  With so few rows that this
+// leaves CTAs over, rows begin with a CTA each and cost nothing beside their keys.
 __device__ __forceinline__ Line make_line(const RaggedArgs &a, int64_t units, int64_t rows, int grid)
 {
     Line l;
     l.cost = kItemCost * a.one;
-    const float t = fmaxf(1.f, (float)units / (128.f * a.one * (float)max(rows, (int64_t)1)));
+    const float t = fmaxf(1.f, (float)units / (128.f * a.one * a.streams * (float)max(rows, (int64_t)1)));
     const int64_t few = rows * (int64_t)ceilf(sqrtf(7.f * t));
     l.grid = grid;
     if (few <= grid) {
@@ -145,8 +146,8 @@ __device__ __forceinline__ Line make_line(const RaggedArgs &a, int64_t units, in
         l.cost = 0;
     }
     int64_t total = units + rows * l.cost;
-    // no share shorter than a tile: no segment of a row between two others is empty
-    l.grid = (int)max((int64_t)1, min((int64_t)l.grid, total / (kBN * a.two)));
+    // no share shorter than a tile (no segment of a row between two others is empty), nor than one for each stream
+    l.grid = (int)max((int64_t)1, min((int64_t)l.grid, total / (kBN * max(a.two, a.streams * a.one))));
     l.each = total / l.grid;
     l.longer = total % l.grid;
     return l;
@@ -215,7 +216,18 @@ __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, groups = (a.batch + 31) / 32;
     int64_t *units = reinterpret_cast<int64_t *>(scratch);
     int *rows = reinterpret_cast<int *>(scratch + 8 * (size_t)groups);
-    for (int g = warp; g < groups; g += THREADS / 32) {
+    // (a single group: every warp has it in registers)
+    Request mine{0, 0, 0, 0};
+    int64_t k = 0, n = 0;
+    if (groups == 1 && lane < a.batch) {
+        uint32_t bad;
+        mine = request(a, lane, bad);
+        if (bad && blockIdx.x == 0)
+            kvc::raise_status(a.status, bad);
+        k = units_before(a, mine, mine.items, 0);
+        n = mine.items;
+    }
+    for (int g = groups == 1 ? groups : warp; g < groups; g += THREADS / 32) {
         const int b = 32 * g + lane;
         int64_t k = 0;
         int n = 0;
@@ -237,11 +249,12 @@ __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch
             rows[g] = n;
         }
     }
-    __syncthreads();
-    int64_t k = 0, n = 0;
-    for (int g = lane; g < groups; g += 32) {
-        k += units[g];
-        n += rows[g];
+    if (groups > 1) {
+        __syncthreads();
+        for (int g = lane; g < groups; g += 32) {
+            k += units[g];
+            n += rows[g];
+        }
     }
 #pragma unroll
     for (int d = 16; d; d >>= 1) {
@@ -258,7 +271,7 @@ __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch
         // the group
         int64_t before = 0;
         int at = 0;
-        for (int g0 = 0; g0 < groups; g0 += 32) {
+        for (int g0 = 0; groups > 1 && g0 < groups; g0 += 32) {
             const int g = g0 + lane;
             const int64_t len = g < groups ? (units[g] + (int64_t)rows[g] * line.cost) * a.kv_heads : 0;
             int64_t inc = len;
@@ -281,8 +294,8 @@ __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch
         {
             const int b = 32 * at + lane;
             uint32_t bad;
-            Request r{0, 0, 0, 0};
-            if (b < a.batch)
+            Request r = mine;
+            if (groups > 1 && b < a.batch)
                 r = request(a, b, bad);
             const int64_t len = units_before(a, r, r.items, line.cost) * a.kv_heads;
             int64_t inc = len;
@@ -579,6 +592,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         kvc_tc::tmem_alloc(tmem_slot, SM::TMEM_COLS);
         kvc_tc::fence_before();
     }
+    kvc::grid_dep_wait();  // the kernels before: lengths, queries, cache, this workspace's last use
     Walk walk;
     const Line line = find_share<THREADS>(a, smem + SM::RING_OFF, gridDim.x, walk);
     // (the sums were read from where the ring's first slabs will be written)
@@ -614,7 +628,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 const int nt = cur.t1 - cur.t0;
                 const uint32_t end = (uint32_t)cur.P + min(cur.n, (cur.i + 1) * a.item), first = (uint32_t)cur.lo + cur.t0 * kBN;
                 if (!mine_v && lane == 0 && cur.t0 == 0 && nt != cur.tiles)
-                    a.split[blockIdx.x] = make_int4(cur.b, cur.h, cur.i,
+                    a.split[blockIdx.x] = make_int4(cur.row0 + cur.i * a.item, min(cur.n - cur.i * a.item, a.item), cur.h,
                                                     2 * (line.of(cur.end - 1) - (int)blockIdx.x + 1) + (first_segment ? 0 : 1));
                 first_segment = false;
                 int32_t place = -1;
@@ -1143,10 +1157,7 @@ ragged_merge_kernel(const RaggedArgs a)
     const int parts = split.w >> 1, slot0 = split.w & 1;
     if (parts == 0)
         return;
-    const int h = split.y, i = split.z;
-    uint32_t wrong;
-    const Request req = request(a, split.x, wrong);
-    const int left = min(req.n - i * a.item, a.item);  // tokens of the item
+    const int row0 = split.x, left = split.y, h = split.z;
     // the item's segment is the first of its CTA, but in the first CTA if that began before it
     auto part = [&](int p, int tile) { return (2 * ((int64_t)c0 + p) + (p == 0 ? slot0 : 0)) * TILES + tile; };
     constexpr int R = kMergeRows, W = R / 8;
@@ -1242,7 +1253,7 @@ ragged_merge_kernel(const RaggedArgs a)
         if (m < rows) {
             const float total = sum_sh[mine], inv = total == 0.f ? 0.f : 1.f / total;
             const int tok = m / a.group;
-            const int64_t row = (int64_t)(req.row0 + i * a.item + tile * a.toks + tok) * a.q_heads + h * a.group +
+            const int64_t row = (int64_t)(row0 + tile * a.toks + tok) * a.q_heads + h * a.group +
                                 (m - tok * a.group);
             T *to = static_cast<T *>(a.out) + row * D;
 #pragma unroll
@@ -1283,22 +1294,13 @@ kvc_status launch_attn(RaggedArgs &a, const void *q, const void *k, const void *
         return KVC_ERR_UNSUPPORTED;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return KVC_ERR_CUDA;
-    kern<<<grid, SM::THREADS, smem, stream>>>(tq, tk, tv, a);
+    if (kvc_host::launch_chained(kern, dim3(grid), SM::THREADS, smem, stream, tq, tk, tv, a) != cudaSuccess)
+        return KVC_ERR_CUDA;
     if (grid > 1) {
-        // may start while the attention runs, and waits for it
-        cudaLaunchConfig_t cfg{};
         // blocks for the rows that an item has if requests are alike (they go round for more)
         const int64_t rows_each = (int64_t)((a.tokens + a.batch - 1) / a.batch) * a.group;
-        cfg.gridDim = dim3(grid - 1, (unsigned)std::min<int64_t>((rows_each + kMergeRows - 1) / kMergeRows,
-                                                                 SM::TILES * kBM / kMergeRows));
-        cfg.blockDim = dim3(256);
-        cfg.stream = stream;
-        cudaLaunchAttribute la[1];
-        la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        la[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = la;
-        cfg.numAttrs = 1;
-        if (cudaLaunchKernelEx(&cfg, ragged_merge_kernel<T, D>, a) != cudaSuccess)
+        const int64_t blocks = std::min<int64_t>((rows_each + kMergeRows - 1) / kMergeRows, SM::TILES * kBM / kMergeRows);
+        if (kvc_host::launch_chained(ragged_merge_kernel<T, D>, dim3(grid - 1, (unsigned)blocks), 256, 0, stream, a) != cudaSuccess)
             return KVC_ERR_CUDA;
     }
     return kvc_host::launch_status();
@@ -1399,6 +1401,7 @@ KVC_API kvc_status kvc_gqa_ragged(void *out, const void *q, const void *k_pool, 
     // bytes take more than that)
     a.one = head_dim == 128 ? 2 : 1;
     a.two = head_dim == 128 ? 3 : head_dim == 64 ? 2 : 1;
+    a.streams = head_dim <= 128 ? 2 : 1;
     // rows of a box: as many of a tile's that no page's end cuts
     a.box_rows = kBN;
     while (page_size % a.box_rows)

@@ -804,31 +804,41 @@ class RaggedPlan:
 
     def __init__(self, batch: int, tokens: int, device):
         self.batch, self.tokens = batch, tokens
-        self.offsets = torch.empty(batch + 1, dtype=torch.int32, device=device)
-        self.positions = torch.empty(tokens, dtype=torch.int32, device=device)
-        self.slots = torch.empty(tokens, dtype=torch.int32, device=device)
+        # one tensor, its parts from 16-byte boundaries on
+        at = (batch + 1 + 3) // 4 * 4
+        step = (tokens + 3) // 4 * 4
+        self.buf = torch.empty(at + 2 * step, dtype=torch.int32, device=device)
+        self.at = self.buf.get_device()
+        self.offsets = self.buf[:batch + 1]
+        self.positions = self.buf[at:at + tokens]
+        self.slots = self.buf[at + step:at + step + tokens]
         self.lengths = Lengths(batch, device)
+        base = self.buf.data_ptr()
+        self._c = base, base + 4 * at, base + 4 * (at + step)
+
+
+def _i32(name, t, shape):
+    if t.dtype is not torch.int32 or t.shape != shape:
+        _same(name, t, shape, torch.int32)
 
 
 def _free_stack(free_pages, free_count, free_left):
-    shape = free_pages.shape
-    if len(shape) != 1 or free_pages.dtype is not torch.int32:
-        _same("free_pages", free_pages, (free_pages.numel(),), torch.int32)
-    if free_count.numel() != 1 or free_count.dtype is not torch.int32:
-        _same("free_count", free_count, (1,), torch.int32)
-    if free_left.numel() != 1 or free_left.dtype is not torch.int32:
-        _same("free_left", free_left, (1,), torch.int32)
-    return shape[0]
+    n = free_pages.numel()
+    _i32("free_pages", free_pages, (n,))
+    for name, t in (("free_count", free_count), ("free_left", free_left)):
+        if t.numel() != 1 or t.dtype is not torch.int32:
+            _same(name, t, (1,), torch.int32)
+    return n
 
 
 def kvc_page_release(released, block_table, page_size, free_pages, free_count, free_left,
                      status=None, stream=None):
     """The pages of the first released[b] tokens of each request go back onto the stack
     free_pages int32 [pool pages] (include/kvc.h)."""
-    B, max_pages = block_table.shape
+    B, max_pages = shape = block_table.shape
     n = _free_stack(free_pages, free_count, free_left)
-    _same("block_table", block_table, (B, max_pages), torch.int32)
-    _same("released", released, (B,), torch.int32)
+    _i32("block_table", block_table, shape)
+    _i32("released", released, (B,))
     a, b, c, d, e, st = _addresses(released, block_table, free_pages, free_count, free_left, status)
     _check("kvc_page_release", library().kvc_page_release(
         a, b, max_pages, page_size, c, n, d, e, B, st, _stream(stream)))
@@ -838,19 +848,20 @@ def kvc_ragged_plan(cached, new_tokens, block_table, page_size, free_pages, free
                     plan, status=None, stream=None):
     """The pages, offsets, positions, slots and lengths of a step in which request b brings
     new_tokens[b] to the cached[b] it holds (include/kvc.h), in plan (RaggedPlan)."""
-    B, max_pages = block_table.shape
+    B, max_pages = shape = block_table.shape
     n = _free_stack(free_pages, free_count, free_left)
-    _same("block_table", block_table, (B, max_pages), torch.int32)
-    _same("cached", cached, (B,), torch.int32)
-    _same("new_tokens", new_tokens, (B,), torch.int32)
-    _same("plan.offsets", plan.offsets, (B + 1,), torch.int32)
-    _same("plan.positions", plan.positions, (plan.tokens,), torch.int32)
-    _same("plan.slots", plan.slots, (plan.tokens,), torch.int32)
-    a, b, c, d, e, f, g, h, i, st = _addresses(cached, new_tokens, block_table, free_pages, free_count,
-                                               free_left, plan.offsets, plan.positions, plan.slots,
-                                               status)
+    _i32("block_table", block_table, shape)
+    _i32("cached", cached, (B,))
+    _i32("new_tokens", new_tokens, (B,))
+    if plan.batch != B or plan.at != plan.lengths.at:
+        raise ValueError(f"plan: expected one made for {B} requests on the current device, got one for "
+                         f"{plan.batch} on {plan.buf.device}")
+    lengths = _lengths_of(plan.lengths, B)
+    a, b, c, d, e, f, st = _addresses(cached, new_tokens, block_table, free_pages, free_count,
+                                      free_left, status)
+    offsets, positions, slots = plan._c
     _check("kvc_ragged_plan", library().kvc_ragged_plan(
-        a, b, c, max_pages, page_size, d, n, e, f, B, plan.tokens, g, _lengths_of(plan.lengths, B), h, i,
+        a, b, c, max_pages, page_size, d, n, e, f, B, plan.tokens, offsets, lengths, positions, slots,
         st, _stream(stream)))
     return plan
 
@@ -869,14 +880,18 @@ def kvc_rope_tables(cos, sin, first=0, base=10000.0, scaling=KVC_ROPE_PLAIN, fac
     return cos, sin
 
 
-def _token_rows(name, t, tokens, heads, D, dtype):
+def _token_rows(name, t, shape, dtype):
     """Address and token stride of t [tokens, heads, D], whose heads are dense (a slice of a
     projection's output)."""
-    if t.shape != (tokens, heads, D) or t.dtype is not dtype:
-        _same(name, t, (tokens, heads, D), dtype)
+    if t.shape != shape or t.dtype is not dtype:
+        _same(name, t, shape, dtype)
     step, row, one = t.stride()
-    if (one != 1 and D > 1) or (row != D and heads > 1) or t.get_device() != _get_device():
-        _addresses(t)  # (raises, but for a dense tensor)
+    D = shape[2]
+    if (one != 1 and D > 1) or (row != D and shape[1] > 1):
+        raise ValueError(f"{name}: expected dense heads, got strides {t.stride()}")
+    if t.get_device() != _get_device():
+        raise ValueError(f"expected a CUDA tensor on the current device, cuda:{_get_device()}, "
+                         f"got one on {t.device}")
     return t.data_ptr(), step
 
 
@@ -889,22 +904,28 @@ def kvc_ragged_append(q_out, k_pool, v_pool, q, k, v, positions, slots, rope=Non
     n_pages, H, ps, D = pool = k_pool.shape
     T, Hq, _ = shape = q.shape
     dtype = q.dtype
-    if not q.is_cuda:
-        raise ValueError(f"expected a CUDA tensor, got one on {q.device}")
-    _same("k_pool", k_pool, pool, dtype)
-    _same("v_pool", v_pool, pool, dtype)
-    _same("q_out", q_out, shape, dtype)
-    _same("positions", positions, (T,), torch.int32)
-    _same("slots", slots, (T,), torch.int32)
+    # (q_out's device is the current one, and the others are compared with that)
+    a, b, c, d, e, wq, wk, st = _addresses(q_out, k_pool, v_pool, positions, slots, q_weight, k_weight,
+                                           status)
+    if q_out.shape != shape or q_out.dtype is not dtype:
+        _same("q_out", q_out, shape, dtype)
+    if k_pool.dtype is not dtype or v_pool.dtype is not dtype or v_pool.shape != pool:
+        _same("k_pool", k_pool, pool, dtype)
+        _same("v_pool", v_pool, pool, dtype)
+    _i32("positions", positions, (T,))
+    _i32("slots", slots, (T,))
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None:
             _same(name, w, (D,), dtype)
-    (qa, qs), (ka, ks), (va, vs) = (_token_rows("q", q, T, Hq, D, dtype), _token_rows("k", k, T, H, D, dtype),
-                                    _token_rows("v", v, T, H, D, dtype))
-    cos, sin, rmax = _tables(rope, D if rope is None else 2 * rope[0].shape[-1])
-    turned = 0 if cos is None else 2 * cos.shape[1]
-    a, b, c, d, e, wq, wk, cs, sn, st = _addresses(q_out, k_pool, v_pool, positions, slots, q_weight,
-                                                   k_weight, cos, sin, status)
+    qa, qs = _token_rows("q", q, (T, Hq, D), dtype)
+    ka, ks = _token_rows("k", k, (T, H, D), dtype)
+    va, vs = _token_rows("v", v, (T, H, D), dtype)
+    cs = sn = None
+    rmax = turned = 0
+    if rope is not None:
+        turned = 2 * rope[0].shape[-1]
+        cos, sin, rmax = _tables(rope, turned)
+        cs, sn = _addresses(cos, sin)
     _check("kvc_ragged_append", library().kvc_ragged_append(
         a, b, c, qa, ka, va, qs, ks, vs, wq, wk, eps, d, e, T, Hq, H, n_pages, ps, D,
         _dtype_code(q), turned, int(bool(interleaved)), cs, sn, rmax, st, _stream(stream)))

@@ -158,11 +158,11 @@ def test_append_binding_refuses(K):
     x = bf(4, 8, 64)
     assert "stride" in inspect.getsource(K._token_rows)
     with pytest.raises(ValueError):
-        K._token_rows("q", x[:, ::2], 4, 4, 64, torch.bfloat16)   # heads that are not dense
+        K._token_rows("q", x[:, ::2], (4, 4, 64), torch.bfloat16)   # heads that are not dense
     with pytest.raises(ValueError):
-        K._token_rows("q", x, 4, 4, 64, torch.bfloat16)           # another number of heads
+        K._token_rows("q", x, (4, 4, 64), torch.bfloat16)           # another number of heads
     with pytest.raises(ValueError):
-        K._token_rows("q", x, 4, 8, 64, torch.float16)
+        K._token_rows("q", x, (4, 8, 64), torch.float16)
 
 
 def test_struct_of_lengths_is_five_addresses(K):
