@@ -988,6 +988,7 @@ kvc_status kvc_ragged_plan(const int32_t *cached, const int32_t *new_tokens, int
  * are as exact as near ones: off by a float32 rounding or two at any position.
  * cos_table, sin_table  device float32 [positions, rotary_dim / 2] (4-byte aligned; the
  *             calls that read them want 16).
+ * positions   up to 2^31 - 1; first >= 0 (KVC_ERR_SHAPE).
  * rotary_dim  even, 2..256 (KVC_ERR_UNSUPPORTED above).  base > 0; factor > 0
  *             (ignored by KVC_ROPE_PLAIN); KVC_ROPE_PARTS: trained >= 1, low < high;
  *             all finite (KVC_ERR_SHAPE).
@@ -1048,7 +1049,8 @@ kvc_status kvc_ragged_append(void *q_out, void *k_pool, void *v_pool, const void
  * page_size  a multiple of 16 (KVC_ERR_SHAPE).
  * KVC_BF16/KVC_F16, head_dim 64, 128 or 256, q_heads / kv_heads any whole number up
  * to 16, batch <= 65535 (KVC_ERR_UNSUPPORTED); scale 0 -> 1 / sqrt(head_dim).
- * Beside the result, the softmax weights are rounded to the cache's type.
+ * Beside the result, the softmax weights are rounded to the cache's type.  Scores
+ * (q . k times scale) up to 1e30 in magnitude; beyond, the output may be NaN.
  * A NaN or an infinity in a column of a V row that a token sees makes that column of
  * its output NaN, whatever the row's weight; a NaN in a K row that it sees makes all
  * of them NaN.  What it does not see may hold anything.

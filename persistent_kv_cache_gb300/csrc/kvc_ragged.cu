@@ -676,7 +676,7 @@ KVC_API kvc_status kvc_rope_tables(float *cos_table, float *sin_table, int64_t f
                                    int rotary_dim, double base, int scaling, double factor, int64_t trained, double low,
                                    double high, double magnitude, void *stream_)
 {
-    if (positions < 0 || first < 0 || first > INT64_MAX - positions || rotary_dim < 2 || rotary_dim % 2)
+    if (positions < 0 || positions > INT32_MAX || first < 0 || first > INT64_MAX - positions || rotary_dim < 2 || rotary_dim % 2)
         return KVC_ERR_SHAPE;
     if (rotary_dim > 2 * kMaxPairs || scaling < KVC_ROPE_PLAIN || scaling > KVC_ROPE_PARTS)
         return KVC_ERR_UNSUPPORTED;
@@ -718,8 +718,6 @@ KVC_API kvc_status kvc_rope_tables(float *cos_table, float *sin_table, int64_t f
     }
     const int vec = half % 4 == 0 && kvc_host::aligned16(cos_table) && kvc_host::aligned16(sin_table) ? 4 : 1;
     const int64_t blocks = ((positions + kPositions - 1) / kPositions * (half / vec) + 255) / 256;
-    if (blocks > INT32_MAX)
-        return KVC_ERR_SHAPE;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     if (vec == 4)
         rope_tables_kernel<4><<<(unsigned)blocks, 256, 0, stream>>>(cos_table, sin_table, first, positions, half, rates,

@@ -72,7 +72,7 @@ __device__ __forceinline__ Request request(const RaggedArgs &a, int b, uint32_t 
         else
             r.n = o1 - o0;
     }
-    r.items = (r.n + a.item - 1) / a.item;
+    r.items = (int)((uint32_t)(r.n + a.item - 1) / (uint32_t)a.item);
     return r;
 }
 
@@ -86,13 +86,14 @@ __device__ __forceinline__ void key_range(const RaggedArgs &a, const Request &r,
 // keys of the items before j: the sum over i < j of hi - lo, in closed form
 __device__ __forceinline__ int64_t keys_before(const RaggedArgs &a, const Request &r, int j)
 {
-    const int64_t K = a.item, full = min(j, r.n / a.item);
-    int64_t sum = (int64_t)j * r.P + K * full * (full + 1) / 2 + (j - full) * (int64_t)r.n;
+    // items of item tokens among them (all but perhaps the last)
+    const int K = a.item, full = j == r.items && j * K != r.n ? j - 1 : j;
+    int64_t sum = (int64_t)j * r.P + (int64_t)K * ((int64_t)full * (full + 1) / 2) + (j > full ? r.n : 0);
     if (a.window > 0) {
-        const int64_t i0 = r.P >= a.window ? 0 : ((int64_t)a.window - r.P + K - 1) / K;  // first with lo > 0
+        const int i0 = r.P >= a.window ? 0 : (int)(((uint32_t)(a.window - r.P) + (uint32_t)(K - 1)) / (uint32_t)K);  // first with lo > 0
         if (j > i0) {
             const int64_t count = j - i0;
-            sum -= count * ((int64_t)r.P - a.window + 1) + K * (i0 + j - 1) * count / 2;
+            sum -= count * ((int64_t)r.P - a.window + 1) + K * ((i0 + (int64_t)j - 1) * count / 2);
         }
     }
     return sum;
@@ -117,6 +118,14 @@ __device__ __forceinline__ int64_t units_before(const RaggedArgs &a, const Reque
     return sum;
 }
 
+// x / y for x >= 0, y > 0 (in 32 bits where they fit: the other takes a thousand clocks of a CTA's start)
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y)
+{
+    if (((x | y) >> 32) == 0)
+        return (uint32_t)x / (uint32_t)y;
+    return x / y;
+}
+
 // All items laid end to end (request, then kv head, then item; each as long as its
 // keys count and `cost`) are one line, cut into equal shares: every CTA gets the
 // same work whatever the lengths, and the split is the same on every run.
@@ -127,7 +136,7 @@ struct Line {
     __device__ __forceinline__ int of(int64_t x) const
     {
         const int64_t head = longer * (each + 1);
-        return (int)(x < head ? x / (each + 1) : longer + (x - head) / each);
+        return (int)(x < head ? quotient(x, each + 1) : longer + quotient(x - head, each));
     }
 };
 
@@ -147,9 +156,9 @@ __device__ __forceinline__ Line make_line(const RaggedArgs &a, int64_t units, in
     }
     int64_t total = units + rows * l.cost;
     // no share shorter than a tile (no segment of a row between two others is empty), nor than one for each stream
-    l.grid = (int)max((int64_t)1, min((int64_t)l.grid, total / (kBN * max(a.two, a.streams * a.one))));
-    l.each = total / l.grid;
-    l.longer = total % l.grid;
+    l.grid = (int)max((int64_t)1, min((int64_t)l.grid, quotient(total, kBN * max(a.two, a.streams * a.one))));
+    l.each = quotient(total, l.grid);
+    l.longer = total - l.each * l.grid;
     return l;
 }
 
@@ -159,6 +168,12 @@ struct Segment {
     int lo, t0, t1, tiles;  // key tiles [t0, t1) of `tiles` from key row lo on
     int64_t end;            // of the item on the line
 };
+
+// x / weight, for the weights that there are: 1, 2, 3
+__device__ __forceinline__ int over_weight(uint32_t x, int weight)
+{
+    return (int)(weight == 3 ? x / 3u : x >> (weight - 1));
+}
 
 // The segments of a CTA's share, one at a time.
 struct Walk {
@@ -192,8 +207,8 @@ struct Walk {
             s.end = end;
             // (what stands for the item's cost comes first and holds no keys; positions over 128 fit 32 bits)
             const int64_t p0 = x - base - cost, p1 = x_end - base - cost;
-            s.t0 = p0 <= 0 ? 0 : (int)((uint32_t)(p0 / kBN) / (uint32_t)weight);
-            s.t1 = x_end >= end ? s.tiles : p1 <= 0 ? 0 : (int)((uint32_t)(p1 / kBN) / (uint32_t)weight);
+            s.t0 = p0 <= 0 ? 0 : over_weight((uint32_t)(p0 / kBN), weight);
+            s.t1 = x_end >= end ? s.tiles : p1 <= 0 ? 0 : over_weight((uint32_t)(p1 / kBN), weight);
             if (x_end >= end) {
                 x = base = end;
                 ++i;
@@ -206,6 +221,24 @@ struct Walk {
         return false;
     }
 };
+
+// sum over a warp of x (0 <= x < 2^54, which no tokens and keys that fit a GPU's memory reach)
+__device__ __forceinline__ int64_t warp_sum(int64_t x)
+{
+    const uint32_t low = __reduce_add_sync(0xffffffffu, (uint32_t)x & 0x7ffffffu);
+    return (int64_t)low + ((int64_t)__reduce_add_sync(0xffffffffu, (uint32_t)(x >> 27)) << 27);
+}
+
+// inclusive prefix sum over a warp
+template <typename U> __device__ __forceinline__ U warp_scan(U x)
+{
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const U y = __shfl_up_sync(0xffffffffu, x, d);
+        x += (int)(threadIdx.x & 31) >= d ? y : 0;
+    }
+    return x;
+}
 
 // The CTA's share: the requests' units and items summed by groups of 32 (a warp a
 // group), the sums in shared memory, then the group, the request and the item of the
@@ -239,11 +272,8 @@ __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch
             k = units_before(a, r, r.items, 0);
             n = r.items;
         }
-#pragma unroll
-        for (int d = 16; d; d >>= 1) {
-            k += __shfl_xor_sync(0xffffffffu, k, d);
-            n += __shfl_xor_sync(0xffffffffu, n, d);
-        }
+        k = warp_sum(k);
+        n = __reduce_add_sync(0xffffffffu, n);
         if (lane == 0) {
             units[g] = k;
             rows[g] = n;
@@ -256,11 +286,8 @@ __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch
             n += rows[g];
         }
     }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) {
-        k += __shfl_xor_sync(0xffffffffu, k, d);
-        n += __shfl_xor_sync(0xffffffffu, n, d);
-    }
+    k = warp_sum(k);
+    n = warp_sum(n);
     const Line line = make_line(a, k * a.kv_heads, n * a.kv_heads, grid);
     w.x = w.x_end = 0;
     if (n > 0 && blockIdx.x < line.grid) {
@@ -274,13 +301,7 @@ __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch
         for (int g0 = 0; groups > 1 && g0 < groups; g0 += 32) {
             const int g = g0 + lane;
             const int64_t len = g < groups ? (units[g] + (int64_t)rows[g] * line.cost) * a.kv_heads : 0;
-            int64_t inc = len;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, inc, d);
-                if (lane >= d)
-                    inc += y;
-            }
+            const int64_t inc = warp_scan(len);
             const uint32_t past = __ballot_sync(0xffffffffu, before + inc > w.x);
             if (past) {
                 const int first = __ffs(past) - 1;
@@ -298,13 +319,9 @@ __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch
             if (groups > 1 && b < a.batch)
                 r = request(a, b, bad);
             const int64_t len = units_before(a, r, r.items, line.cost) * a.kv_heads;
-            int64_t inc = len;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, inc, d);
-                if (lane >= d)
-                    inc += y;
-            }
+            // (the group's units, in 32 bits where they fit)
+            const int64_t group = warp_sum(len);
+            const int64_t inc = group >> 31 ? warp_scan(len) : (int64_t)warp_scan((int)len);
             const int first = __ffs(__ballot_sync(0xffffffffu, before + inc > w.x)) - 1;
             w.b = 32 * at + first;
             before += __shfl_sync(0xffffffffu, inc - len, first);
@@ -315,7 +332,7 @@ __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch
         }
         // the kv head and the item: the last that begins at x or before it
         const int64_t head = units_before(a, w.r, w.r.items, line.cost);
-        w.h = (int)((w.x - before) / head);
+        w.h = (int)quotient(w.x - before, head);
         before += w.h * head;
         int low = 0, count = w.r.items;  // among [low, low + count)
         while (count > 1) {

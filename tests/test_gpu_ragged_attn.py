@@ -136,6 +136,51 @@ def test_lengths_around_tiles(K, n, D):
     c.check(out)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("page", [16, 80, 112, 160, 256, 320])
+def test_page_sizes(K, page, D):
+    past, new = ragged(page + D, 6, 600, 200, 0)
+    c = Case(K, page, past, new, 2, 4, D, page)
+    for window in (0, 333):
+        out, st = c.run(local_window_size=window)
+        assert st == 0
+        c.check(out, window)
+
+
+def test_extreme_windows(K):
+    """No window, the widest and the narrowest."""
+    past, new = ragged(77, 5, 400, 150, 0)
+    c = Case(K, 77, past, new, 2, 4, 128, 64)
+    want, _ = c.run()
+    for window in (-1, -2 ** 31, 2 ** 31 - 1, 100000):
+        out, st = c.run(local_window_size=window)
+        assert st == 0 and (out.float() - want.float()).abs().max() <= 2.0 ** -6  # (other shares of the keys, at most)
+        c.check(out)
+    out, _ = c.run(local_window_size=1)  # each token itself
+    for b in range(5):
+        o, n = int(c.offsets[b]), new[b]
+        v = c.rows[b][1][:, past[b]:past[b] + n].transpose(0, 1).repeat_interleave(4, 1)
+        assert torch.equal(out[o:o + n], v)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_beside_the_paged_decode(K, D):
+    """One token a request: what kvc_gqa_decode_paged gives for the same cache, within both calls' roundings (either is
+    within the bound of the definition)."""
+    past = [0, 63, 64, 500, 1000, 127]
+    c = Case(K, 90 + D, past, [1] * 6, 2, 4, D, 64, pad=0)
+    c.k, c.v = torch.nan_to_num(c.k), torch.nan_to_num(c.v)
+    out, st = c.run()
+    _, q, k, v, table, offsets = c.gpu()
+    other = torch.empty((6, 8, 1, D), dtype=BF16, device="cuda")
+    K.kvc_gqa_decode_paged(other, q.reshape(6, 8, 1, D), k, v, table, c.L)
+    other = other.cpu().reshape(6, 8, D)
+    for b in range(6):
+        want, bound = c.want(b)
+        R.assert_within(out[b:b + 1], want, bound, f"ragged {b}")
+        assert ((other[b:b + 1].double() - want).abs() <= 2 * bound + 2.0 ** -7).all()
+
+
 @pytest.mark.parametrize("D,G", [(64, 8), (128, 4), (128, 7), (256, 2)])
 def test_long_rows(K, D, G):
     """Rows whose keys go to many blocks, beside short ones."""
