@@ -37,12 +37,14 @@ struct RaggedArgs {
     int batch, tokens, q_heads, kv_heads, group;
     int toks, item;  // tokens of a query tile, of an item
     int one, two;    // what a key of an item of one, of two query tiles counts
+    int rounds;      // at most so many
+    int key_bytes;   // of a key and its value, all kv heads
     int streams;     // of softmax and products in a CTA
     int box_rows;    // rows of a TMA box of K (of V: up to a slab's)
     int window;
     float scale_log2;
-    float *ws_o, *ws_m, *ws_l;  // partial results: [2 * grid * tiles][D / 4][128][4], [..][128]
-    int4 *split;  // [grid] the item of which a CTA has the first keys but not the last: its first row, its tokens, kv
+    float *ws_o, *ws_m, *ws_l;  // partial results: [2 * pieces * tiles][D / 4][128][4], [..][128]
+    int4 *split;  // [pieces] the item of which a piece has the first keys but not the last: its first row, its tokens, kv
                   // head, 2 * parts + slot of its own part (parts 0: there is none)
     int32_t *status;
 };
@@ -129,8 +131,15 @@ __device__ __forceinline__ int64_t quotient(int64_t x, int64_t y)
 // All items laid end to end (request, then kv head, then item; each as long as its
 // keys count and `cost`) are one line, cut into equal shares: every CTA gets the
 // same work whatever the lengths, and the split is the same on every run.
+// A CTA's share is in one piece, or in up to `rounds` of them, a grid's pieces apart:
+// then the CTAs are at work in a part of the line at a time, whose keys and values L2
+// can hold.  (head_dim 256, where a key tile is read for 128 query rows only: windowed
+// chunks of 8 prompts read each key from memory seven times.  A round costs each CTA two
+// partial results, and its pieces are long enough for that to be little.)
+constexpr int kRounds = 4;
+constexpr int64_t kRoundBytes = 64 << 20, kRoundUnits = 64 * kBN;
 struct Line {
-    int grid, cost;
+    int grid, cost, rounds;  // grid: pieces of the line
     int64_t each, longer;  // shares [0, longer) are one longer than `each`
     __device__ __forceinline__ int64_t begin(int64_t c) const { return c * each + min(c, longer); }
     __device__ __forceinline__ int of(int64_t x) const
@@ -143,9 +152,10 @@ struct Line {
 // What `streams` key tiles of a row take a CTA, the join of two parts takes for each: a
 // row of t such is done soonest by about sqrt(7 t) CTAs.  With so few rows that this
 // leaves CTAs over, rows begin with a CTA each and cost nothing beside their keys.
-__device__ __forceinline__ Line make_line(const RaggedArgs &a, int64_t units, int64_t rows, int grid)
+__device__ __forceinline__ Line make_line(const RaggedArgs &a, int64_t units, int64_t rows, int64_t keys, int grid)
 {
     Line l;
+    l.rounds = 1;
     l.cost = kItemCost * a.one;
     const float t = fmaxf(1.f, (float)units / (128.f * a.one * a.streams * (float)max(rows, (int64_t)1)));
     const int64_t few = rows * (int64_t)ceilf(sqrtf(7.f * t));
@@ -157,6 +167,11 @@ __device__ __forceinline__ Line make_line(const RaggedArgs &a, int64_t units, in
     int64_t total = units + rows * l.cost;
     // no share shorter than a tile (no segment of a row between two others is empty), nor than one for each stream
     l.grid = (int)max((int64_t)1, min((int64_t)l.grid, quotient(total, kBN * max(a.two, a.streams * a.one))));
+    if (a.rounds > 1 && l.grid == grid) {
+        const int64_t fit = quotient(keys * a.key_bytes + kRoundBytes - 1, kRoundBytes), longest = quotient(total, grid * kRoundUnits);
+        l.rounds = (int)max((int64_t)1, min((int64_t)a.rounds, min(fit, longest)));
+        l.grid *= l.rounds;
+    }
     l.each = quotient(total, l.grid);
     l.longer = total - l.each * l.grid;
     return l;
@@ -166,6 +181,7 @@ struct Segment {
     int b, h, i;
     int row0, P, n;    // of the request
     int lo, t0, t1, tiles;  // key tiles [t0, t1) of `tiles` from key row lo on
+    int slot;               // of its partial result: two a piece of the line, the first for the piece's first segment
     int64_t end;            // of the item on the line
 };
 
@@ -179,10 +195,18 @@ __device__ __forceinline__ int over_weight(uint32_t x, int weight)
 struct Walk {
     int64_t x, x_end, base;  // base: of the item at (b, h, i)
     int b, h, i;
+    int round, slot;         // which of the CTA's pieces; of the piece's next segment
     Request r;
-    __device__ __forceinline__ bool next(const RaggedArgs &a, int cost, Segment &s)
+    // `pieces`: the CTA's later ones, as they begin
+    __device__ __forceinline__ bool next(const RaggedArgs &a, int cost, int rounds, const Walk *pieces, Segment &s)
     {
-        while (x < x_end) {
+        for (;;) {
+            if (x >= x_end) {
+                if (round + 1 >= rounds)
+                    return false;
+                *this = pieces[round];
+                continue;
+            }
             while (i >= r.items) {
                 i = 0;
                 if (r.items == 0 || ++h == a.kv_heads) {
@@ -215,10 +239,12 @@ struct Walk {
             } else {
                 x = x_end;
             }
-            if (s.t1 > s.t0)
+            if (s.t1 > s.t0) {
+                s.slot = 2 * (int)(blockIdx.x + round * gridDim.x) + slot;
+                slot = 1;
                 return true;
+            }
         }
-        return false;
     }
 };
 
@@ -240,110 +266,128 @@ template <typename U> __device__ __forceinline__ U warp_scan(U x)
     return x;
 }
 
-// The CTA's share: the requests' units and items summed by groups of 32 (a warp a
-// group), the sums in shared memory, then the group, the request and the item of the
-// share's first unit.  `scratch` holds 12 bytes a group.
+// Where unit x of the line is: the group of 32 requests (whose sums are in units and
+// rows), the request, the kv head and the item.  `mine`: of a single group, this lane's
+// request.
+__device__ __forceinline__ void locate(const RaggedArgs &a, const int64_t *units, const int *rows, int groups, int cost,
+                                       const Request &mine, Walk &w)
+{
+    const int lane = threadIdx.x & 31;
+    int64_t before = 0;
+    int at = 0;
+    for (int g0 = 0; groups > 1 && g0 < groups; g0 += 32) {
+        const int g = g0 + lane;
+        const int64_t len = g < groups ? (units[g] + (int64_t)rows[g] * cost) * a.kv_heads : 0;
+        const int64_t inc = warp_scan(len);
+        const uint32_t past = __ballot_sync(0xffffffffu, before + inc > w.x);
+        if (past) {
+            const int first = __ffs(past) - 1;
+            at = g0 + first;
+            before += __shfl_sync(0xffffffffu, inc - len, first);
+            break;
+        }
+        before += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    {
+        const int b = 32 * at + lane;
+        uint32_t bad;
+        Request r = mine;
+        if (groups > 1 && b < a.batch)
+            r = request(a, b, bad);
+        const int64_t len = units_before(a, r, r.items, cost) * a.kv_heads;
+        // (the group's units, in 32 bits where they fit)
+        const int64_t group = warp_sum(len);
+        const int64_t inc = group >> 31 ? warp_scan(len) : (int64_t)warp_scan((int)len);
+        const int first = __ffs(__ballot_sync(0xffffffffu, before + inc > w.x)) - 1;
+        w.b = 32 * at + first;
+        before += __shfl_sync(0xffffffffu, inc - len, first);
+        w.r.row0 = __shfl_sync(0xffffffffu, r.row0, first);
+        w.r.P = __shfl_sync(0xffffffffu, r.P, first);
+        w.r.n = __shfl_sync(0xffffffffu, r.n, first);
+        w.r.items = __shfl_sync(0xffffffffu, r.items, first);
+    }
+    const int64_t head = units_before(a, w.r, w.r.items, cost);
+    w.h = (int)quotient(w.x - before, head);
+    before += w.h * head;
+    int low = 0, count = w.r.items;  // the last item that begins at x or before it, among [low, low + count)
+    while (count > 1) {
+        const int step = (count + 31) / 32, j = low + lane * step;
+        const bool begun = lane * step < count && before + units_before(a, w.r, j, cost) <= w.x;
+        const int last = 31 - __clz(__ballot_sync(0xffffffffu, begun));
+        low += last * step;
+        count = min(step, count - last * step);
+    }
+    w.i = low;
+    w.base = before + units_before(a, w.r, low, cost);
+}
+
+// The CTA's share: the requests' units, items and keys summed by groups of 32 (a warp a
+// group), the sums in shared memory, and where the share's pieces begin.  `scratch` holds
+// 20 bytes a group.
 template <int THREADS>
-__device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch, int grid, Walk &w)
+__device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch, Walk &w, Walk *pieces)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, groups = (a.batch + 31) / 32;
-    int64_t *units = reinterpret_cast<int64_t *>(scratch);
-    int *rows = reinterpret_cast<int *>(scratch + 8 * (size_t)groups);
+    int64_t *units = reinterpret_cast<int64_t *>(scratch), *seen = units + groups;
+    int *rows = reinterpret_cast<int *>(seen + groups);
     // (a single group: every warp has it in registers)
     Request mine{0, 0, 0, 0};
-    int64_t k = 0, n = 0;
-    if (groups == 1 && lane < a.batch) {
+    int64_t k = 0, n = 0, keys = 0;
+    auto count = [&](int b, Request &r, int64_t &k, int64_t &keys) {
         uint32_t bad;
-        mine = request(a, lane, bad);
+        r = request(a, b, bad);
         if (bad && blockIdx.x == 0)
             kvc::raise_status(a.status, bad);
-        k = units_before(a, mine, mine.items, 0);
+        k = units_before(a, r, r.items, 0);
+        keys = r.n == 0 ? 0 : a.window > 0 ? r.n + min(r.P, a.window - 1) : r.n + r.P;
+    };
+    if (groups == 1 && lane < a.batch) {
+        count(lane, mine, k, keys);
         n = mine.items;
     }
     for (int g = groups == 1 ? groups : warp; g < groups; g += THREADS / 32) {
         const int b = 32 * g + lane;
-        int64_t k = 0;
-        int n = 0;
-        if (b < a.batch) {
-            uint32_t bad;
-            const Request r = request(a, b, bad);
-            if (bad && blockIdx.x == 0)
-                kvc::raise_status(a.status, bad);
-            k = units_before(a, r, r.items, 0);
-            n = r.items;
-        }
-        k = warp_sum(k);
-        n = __reduce_add_sync(0xffffffffu, n);
+        Request r{0, 0, 0, 0};
+        int64_t mine_k = 0, mine_keys = 0;
+        if (b < a.batch)
+            count(b, r, mine_k, mine_keys);
+        mine_k = warp_sum(mine_k);
+        mine_keys = warp_sum(mine_keys);
+        const int items = __reduce_add_sync(0xffffffffu, r.items);
         if (lane == 0) {
-            units[g] = k;
-            rows[g] = n;
+            units[g] = mine_k;
+            seen[g] = mine_keys;
+            rows[g] = items;
         }
     }
     if (groups > 1) {
         __syncthreads();
         for (int g = lane; g < groups; g += 32) {
             k += units[g];
+            keys += seen[g];
             n += rows[g];
         }
     }
     k = warp_sum(k);
     n = warp_sum(n);
-    const Line line = make_line(a, k * a.kv_heads, n * a.kv_heads, grid);
+    if (a.rounds > 1)
+        keys = warp_sum(keys);
+    const Line line = make_line(a, k * a.kv_heads, n * a.kv_heads, keys, gridDim.x);
     w.x = w.x_end = 0;
-    if (n > 0 && blockIdx.x < line.grid) {
-        w.x = line.begin(blockIdx.x);
-        w.x_end = line.begin(blockIdx.x + 1);
-    }
-    if (w.x < w.x_end) {
-        // the group
-        int64_t before = 0;
-        int at = 0;
-        for (int g0 = 0; groups > 1 && g0 < groups; g0 += 32) {
-            const int g = g0 + lane;
-            const int64_t len = g < groups ? (units[g] + (int64_t)rows[g] * line.cost) * a.kv_heads : 0;
-            const int64_t inc = warp_scan(len);
-            const uint32_t past = __ballot_sync(0xffffffffu, before + inc > w.x);
-            if (past) {
-                const int first = __ffs(past) - 1;
-                at = g0 + first;
-                before += __shfl_sync(0xffffffffu, inc - len, first);
+    w.round = w.slot = 0;
+    if (n > 0) {
+#pragma unroll 1
+        for (int round = line.rounds - 1; round >= 0; --round) {
+            const int piece = blockIdx.x + round * gridDim.x;
+            if (piece >= line.grid)
                 break;
-            }
-            before += __shfl_sync(0xffffffffu, inc, 31);
+            w.round = round;
+            w.x = line.begin(piece);
+            w.x_end = line.begin(piece + 1);
+            locate(a, units, rows, groups, line.cost, mine, w);
+            if (round > 0 && threadIdx.x == 0)
+                pieces[round - 1] = w;
         }
-        // the request
-        {
-            const int b = 32 * at + lane;
-            uint32_t bad;
-            Request r = mine;
-            if (groups > 1 && b < a.batch)
-                r = request(a, b, bad);
-            const int64_t len = units_before(a, r, r.items, line.cost) * a.kv_heads;
-            // (the group's units, in 32 bits where they fit)
-            const int64_t group = warp_sum(len);
-            const int64_t inc = group >> 31 ? warp_scan(len) : (int64_t)warp_scan((int)len);
-            const int first = __ffs(__ballot_sync(0xffffffffu, before + inc > w.x)) - 1;
-            w.b = 32 * at + first;
-            before += __shfl_sync(0xffffffffu, inc - len, first);
-            w.r.row0 = __shfl_sync(0xffffffffu, r.row0, first);
-            w.r.P = __shfl_sync(0xffffffffu, r.P, first);
-            w.r.n = __shfl_sync(0xffffffffu, r.n, first);
-            w.r.items = __shfl_sync(0xffffffffu, r.items, first);
-        }
-        // the kv head and the item: the last that begins at x or before it
-        const int64_t head = units_before(a, w.r, w.r.items, line.cost);
-        w.h = (int)quotient(w.x - before, head);
-        before += w.h * head;
-        int low = 0, count = w.r.items;  // among [low, low + count)
-        while (count > 1) {
-            const int step = (count + 31) / 32, j = low + lane * step;
-            const bool begun = lane * step < count && before + units_before(a, w.r, j, line.cost) <= w.x;
-            const int last = 31 - __clz(__ballot_sync(0xffffffffu, begun));
-            low += last * step;
-            count = min(step, count - last * step);
-        }
-        w.i = low;
-        w.base = before + units_before(a, w.r, low, line.cost);
     }
     __syncthreads();
     return line;
@@ -399,9 +443,12 @@ template <int D> struct Smem {
     static constexpr int Q_TILE = kBM * D * 2, Q_BYTES = TILES * Q_TILE;
     static constexpr int SLAB = KR * D * 2;
     static constexpr int BUDGET = 227 * 1024;
-    static constexpr int NBAR = 10;  // beside the ring's
-    // beside the queries and n slabs: barriers, tensor memory's address and a flag, maxima and sums, rows, `Kept`
-    static constexpr int misc(int n) { return (2 * n + NBAR) * 8 + 16 + 4 * kBM * 4 + 16 + 2 * (int)sizeof(Kept); }
+    static constexpr int NBAR = 12;  // beside the ring's
+    // beside the queries and n slabs: barriers, tensor memory's address and a flag, maxima and sums, rows, `Kept`, pieces
+    static constexpr int misc(int n)
+    {
+        return (2 * n + NBAR) * 8 + 16 + 4 * kBM * 4 + 16 + 2 * (int)sizeof(Kept) + (kRounds - 1) * (int)sizeof(Walk);
+    }
     static constexpr int fit()
     {
         int n = 12;
@@ -412,16 +459,21 @@ template <int D> struct Smem {
     static constexpr int NSLAB = fit();
     static constexpr int RING_OFF = Q_BYTES;
     static constexpr int BAR_OFF = RING_OFF + NSLAB * SLAB;
-    // full[NSLAB], empty[NSLAB], s_full[2], p_full[2], o_done[2], q_full, q_empty, drain[2]
+    // full[NSLAB], empty[NSLAB], s_full[2], p_full[2], o_done[2], q_full, q_empty, drain[2], h_full[2]
+    static constexpr int HALF_OFF = BAR_OFF + (2 * NSLAB + 10) * 8;  // h_full
     static constexpr int MISC_OFF = BAR_OFF + (2 * NSLAB + NBAR) * 8;
     static constexpr int RED_OFF = (MISC_OFF + 8 + 15) / 16 * 16;  // 4 x 128 floats: maxima and sums that change hands
     static constexpr int BAD_OFF = RED_OFF + 4 * kBM * 4;
     static constexpr int WALK_OFF = BAD_OFF + 16;  // of each stream
-    static constexpr int TOTAL = WALK_OFF + 2 * (int)sizeof(Kept);
+    static constexpr int PIECES_OFF = WALK_OFF + 2 * (int)sizeof(Kept);
+    static constexpr int TOTAL = PIECES_OFF + (kRounds - 1) * (int)sizeof(Walk);
     static_assert(TOTAL <= BUDGET && NSLAB >= 2 * SPT + 1, "a tile of K, one of V and the next slab must fit");
-    static_assert(NSLAB * SLAB >= 12 * ((kMaxRequests + 31) / 32), "the groups' sums lie where the ring will");
+    static_assert(NSLAB * SLAB >= 20 * ((kMaxRequests + 31) / 32), "the groups' sums lie where the ring will");
     // the weights have columns of their own where there are some left: the next scores need not wait for them to be read
     static constexpr bool OWN_P = D == 64;
+    // head_dim 128: the output products of half of a tile's keys start while the other half's weights are made (632 ->
+    // 614 us, chunks of 8 prompts; at 64, whose products are short, 106 -> 113, decoding and prompts in one call)
+    static constexpr bool EARLY = D == 128;
     static constexpr uint32_t COL_S = TILES * D, COL_P = OWN_P ? COL_S + 2 * kBN : COL_S, TMEM_COLS = 512;
     static_assert(COL_S + 2 * kBN + (OWN_P ? 2 * 64 : 0) <= TMEM_COLS, "tensor memory");
 };
@@ -515,7 +567,7 @@ template <int CT> __device__ __forceinline__ float row_top(uint32_t from, int lo
 // longer than the instruction cache next to the tensor cores' issue loops.
 template <typename T, int CT, bool MASK>
 __device__ __forceinline__ float row_weights(uint32_t from, uint32_t to, int lo, int hi, uint32_t flip, float c_log2,
-                                             float neg_m)
+                                             float neg_m, uint32_t half_there)
 {
     uint32_t x[32];
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -527,6 +579,13 @@ __device__ __forceinline__ float row_weights(uint32_t from, uint32_t to, int lo,
             seen_only(x, lo - c, hi - c, flip);
         weights<T>(x, c_log2, neg_m, sum);
         kvc_tc::st16(to + c / 2, x);
+        kvc_tc::wait_st();
+        if (c == 0 && half_there) {
+            kvc_tc::fence_before();
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0)
+                kvc_tc::arrive_at(half_there);
+        }
     }
     return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
@@ -573,14 +632,15 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         if ((uint32_t)(smem - smem_raw) + SM::TOTAL > dyn) {
             if (threadIdx.x == 0) {
                 kvc::raise_status(a.status, KVC_DEV_CAPACITY);
-                a.split[blockIdx.x] = make_int4(0, 0, 0, 0);
+                for (int p = 0; p < a.rounds; ++p)
+                    a.split[blockIdx.x + p * gridDim.x] = make_int4(0, 0, 0, 0);
             }
             return;
         }
     }
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + SM::BAR_OFF), *empty = full + NSLAB,
              *s_full = full + 2 * NSLAB, *p_full = s_full + 2, *o_done = s_full + 4, *q_full = s_full + 6,
-             *q_empty = s_full + 7, *drain = s_full + 8;
+             *q_empty = s_full + 7, *drain = s_full + 8, *h_full = s_full + 10;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + SM::MISC_OFF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + SM::MISC_OFF + 4);
 
@@ -595,6 +655,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             kvc::mbar_init(&s_full[i], 1);
             kvc::mbar_init(&p_full[i], 8);
             kvc::mbar_init(&o_done[i], 1);
+            kvc::mbar_init(&h_full[i], 8);
         }
         kvc::mbar_init(q_full, 1);
         kvc::mbar_init(q_empty, 1);
@@ -611,7 +672,11 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     }
     kvc::grid_dep_wait();  // the kernels before: lengths, queries, cache, this workspace's last use
     Walk walk;
-    const Line line = find_share<THREADS>(a, smem + SM::RING_OFF, gridDim.x, walk);
+    Walk *later = reinterpret_cast<Walk *>(smem + SM::PIECES_OFF);
+    const Line line = find_share<THREADS>(a, smem + SM::RING_OFF, walk, later);
+    const int rounds = TILES == 1 ? line.rounds : 1;
+    if (TILES == 2)
+        walk.round = 0;  // (known to the compiler)
     // (the sums were read from where the ring's first slabs will be written)
     kvc::fence_proxy_async_smem();
     __syncthreads();
@@ -620,7 +685,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     const uint32_t smem_base = kvc::smem_u32(smem);
     // (products and softmax look one segment ahead, so that the lengths are there when they get to it)
     Segment cur, nxt;
-    bool more = walk.next(a, line.cost, cur);
+    bool more = walk.next(a, line.cost, rounds, later, cur);
 
     if (warp < 4) {
         if (warp == 1 || warp == 2) {
@@ -633,9 +698,10 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             if (lane == 0)
                 kvc::tma_prefetch_desc(tmap);
             if (!mine_v && lane == 0)
-                a.split[blockIdx.x] = make_int4(0, 0, 0, 0);
+                for (int p = 0; p < a.rounds; ++p)
+                    a.split[blockIdx.x + p * gridDim.x] = make_int4(0, 0, 0, 0);
             int q0 = 0;  // slabs of the segments before
-            bool ok = true, first_segment = true;
+            bool ok = true;
             const int box = mine_v ? min(a.box_rows, KR) : a.box_rows, slab_rows = mine_v ? KR : kBN;
             const int per_tile = kBN / box, pieces = slab_rows / box;  // boxes of a tile's, of a slab's rows: powers of two up to 8
             const int blocks = mine_v ? D / 64 : D / 64 / SPT;         // column blocks of a slab
@@ -645,9 +711,8 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 const int nt = cur.t1 - cur.t0;
                 const uint32_t end = (uint32_t)cur.P + min(cur.n, (cur.i + 1) * a.item), first = (uint32_t)cur.lo + cur.t0 * kBN;
                 if (!mine_v && lane == 0 && cur.t0 == 0 && nt != cur.tiles)
-                    a.split[blockIdx.x] = make_int4(cur.row0 + cur.i * a.item, min(cur.n - cur.i * a.item, a.item), cur.h,
-                                                    2 * (line.of(cur.end - 1) - (int)blockIdx.x + 1) + (first_segment ? 0 : 1));
-                first_segment = false;
+                    a.split[cur.slot >> 1] = make_int4(cur.row0 + cur.i * a.item, min(cur.n - cur.i * a.item, a.item), cur.h,
+                                                       2 * (line.of(cur.end - 1) - (cur.slot >> 1) + 1) + (cur.slot & 1));
                 int32_t place = -1;
                 for (int j = 0; ok && j < nt; ++j) {
                     if ((j * per_tile & 31) == 0) {
@@ -704,7 +769,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     }
                 }
                 q0 += 2 * SPT * nt;
-                more = walk.next(a, line.cost, cur);
+                more = walk.next(a, line.cost, rounds, later, cur);
             }
             if (*abort_flag && lane == 0)
                 // wind-down: let the loads in flight land before the CTA exits
@@ -720,7 +785,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 bool ok = true;
                 while (ok && more) {
                     const Streams st = Streams::of<TILES>(a, cur);
-                    more = walk.next(a, line.cost, nxt);
+                    more = walk.next(a, line.cost, rounds, later, nxt);
                     for (int j = 0; ok && j < st.n; ++j) {
 #pragma unroll
                         for (int k = 0; k < TILES; ++k) {
@@ -729,26 +794,35 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                             const int s = TILES == 2 ? k : (int)(used[0] & 1);
                             uint32_t &u = used[TILES == 2 ? k : 0];
                             const uint32_t parity = TILES == 2 ? u & 1 : (u >> 1) & 1;
-                            if (!(ok = wait_or_abort(&p_full[s], parity, abort_flag, a.status)))
-                                break;
-                            kvc_tc::fence_after();
                             const bool fresh = TILES == 2 && !st.two ? j < 2 : j == 0;  // first of the stream
                             const bool last = TILES == 1 || !st.two || k == 1;          // of the tile
-                            for (int hf = 0; hf < SPT; ++hf) {
-                                const int q = q0 + SPT * v_group(j, st.n) + hf, slot = q % NSLAB;
-                                if (!(ok = wait_or_abort(&full[slot], (q / NSLAB) & 1, abort_flag, a.status)))
+                            // (EARLY: the products with each thread's first 32 weights, then the others)
+                            constexpr int PARTS = SM::EARLY ? 2 : 1;
+#pragma unroll
+                            for (int part = 0; ok && part < PARTS; ++part) {
+                                if (!(ok = wait_or_abort(SM::EARLY && part == 0 ? &h_full[s] : &p_full[s], parity, abort_flag, a.status)))
                                     break;
                                 kvc_tc::fence_after();
-                                const uint64_t vd = v_ring + (uint64_t)(slot * (SM::SLAB / 16));
-                                // (the weights of 64 keys are 32 columns; over the scores, the next ones' begin 64 further on)
-                                const uint32_t pa = tmem + SM::COL_P + s * (SM::OWN_P ? 64 : kBN) + hf * 64;
+                                for (int hf = 0; hf < SPT; ++hf) {
+                                    const int q = q0 + SPT * v_group(j, st.n) + hf, slot = q % NSLAB;
+                                    if (part == 0 && !(ok = wait_or_abort(&full[slot], (q / NSLAB) & 1, abort_flag, a.status)))
+                                        break;
+                                    kvc_tc::fence_after();
+                                    const uint64_t vd = v_ring + (uint64_t)(slot * (SM::SLAB / 16));
+                                    // (the weights of 64 keys are 32 columns; over the scores, the next ones' begin 64 further on)
+                                    const uint32_t pa = tmem + SM::COL_P + s * (SM::OWN_P ? 64 : kBN) + hf * 64;
 #pragma unroll
-                                for (int k2 = 0; k2 < KR / 16; ++k2)
-                                    kvc_tc::mma_ts(tmem + (TILES == 2 ? k * D : 0), pa + k2 / 4 * (SM::OWN_P ? 32 : 64) + k2 % 4 * 8,
-                                                   vd + (uint64_t)(k2 * (2048 / 16)), IDESC_O,
-                                                   !fresh || hf > 0 || k2 > 0);
-                                if (last)
-                                    kvc_tc::commit(&empty[slot]);
+                                    for (int k2 = 0; k2 < KR / 16; ++k2) {
+                                        if (SM::EARLY && (k2 >> 1 & 1) != part)
+                                            continue;
+                                        kvc_tc::mma_ts(tmem + (TILES == 2 ? k * D : 0),
+                                                       pa + k2 / 4 * (SM::OWN_P ? 32 : 64) + k2 % 4 * 8,
+                                                       vd + (uint64_t)(k2 * (2048 / 16)), IDESC_O,
+                                                       !fresh || hf > 0 || k2 > 0);
+                                    }
+                                    if (last && part == PARTS - 1)
+                                        kvc_tc::commit(&empty[slot]);
+                                }
                             }
                             if (!ok)
                                 break;
@@ -784,7 +858,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                         for (int c = 0; c < D / 64; ++c)
                             kvc::tma_load_4d(smem + k * SM::Q_TILE + c * (kBM * 128), &tmap_q, 0, cur.h * a.group,
                                              cur.row0 + cur.i * a.item + k * a.toks, c, q_full);
-                    more = walk.next(a, line.cost, nxt);
+                    more = walk.next(a, line.cost, rounds, later, nxt);
                     if (!(ok = wait_or_abort(q_full, s_no & 1, abort_flag, a.status))) {
                         kvc::mbar_wait(q_full, s_no & 1);  // (let the loads land before the CTA exits)
                         break;
@@ -893,7 +967,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             };
             if (scout && lane == 0) {
                 Walk next = kept->walk;
-                kept->more[(s_no + 1) & 1] = next.next(a, line.cost, kept->seg[(s_no + 1) & 1]);
+                kept->more[(s_no + 1) & 1] = next.next(a, line.cost, rounds, later, kept->seg[(s_no + 1) & 1]);
                 kept->walk = next;
             }
             __syncwarp();
@@ -992,6 +1066,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 const uint32_t from = s_col + CT * half;
                 const uint32_t to = SM::OWN_P ? lane_addr + SM::COL_P + s * 64 + 32 * half : from;
                 float top = -INFINITY;
+                const uint32_t half_there = SM::EARLY ? smem_base + (uint32_t)SM::HALF_OFF + 8u * stream : 0u;
                 // (every row sees all of a whole tile)
                 const bool plain = !cut && !flip;
                 int lo = 0, hi = 0;
@@ -1015,15 +1090,6 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                         }
                         m_run = top;
                     }
-                    const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
-                    if (SM::OWN_P && used > 1) {
-                        // the products of the tile before have read its weights
-                        ok = wait_or_abort(&o_done[s], (used - 2) & 1, abort_flag, a.status);
-                        kvc_tc::fence_after();
-                    }
-                    const float sum = plain ? row_weights<T, CT, false>(from, to, lo, hi, flip, c_log2, neg_m)
-                                            : row_weights<T, CT, true>(from, to, lo, hi, flip, c_log2, neg_m);
-                    l_run = l_run * alpha + sum;
                     if (__any_sync(0xffffffffu, rescale)) {
                         // the reference moved: rescale this thread's part of the O row
                         // (the products of the tile before; with two streams they were done before S was written)
@@ -1040,8 +1106,22 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                                 o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
                             kvc_tc::st32(lane_addr + stream * D + cc, o);
                         }
+                        kvc_tc::wait_st();
                     }
-                    kvc_tc::wait_st();
+                    const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+                    if (SM::OWN_P && used > 1) {
+                        // the products of the tile before have read its weights
+                        ok = wait_or_abort(&o_done[s], (used - 2) & 1, abort_flag, a.status);
+                        kvc_tc::fence_after();
+                    }
+                    const float sum = plain ? row_weights<T, CT, false>(from, to, lo, hi, flip, c_log2, neg_m, half_there)
+                                            : row_weights<T, CT, true>(from, to, lo, hi, flip, c_log2, neg_m, half_there);
+                    l_run = l_run * alpha + sum;
+                } else if (half_there) {
+                    kvc_tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        kvc_tc::arrive_at(half_there);
                 }
                 kvc_tc::fence_before();
                 __syncwarp();
@@ -1062,7 +1142,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             const int first = seg.i * a.item + (st.two ? stream * a.toks : 0), tok = m / a.group;
             const bool there = tok < a.toks && first + tok < seg.n, whole = seg.t1 - seg.t0 == seg.tiles;
             const int64_t out_row = (int64_t)(seg.row0 + first + tok) * a.q_heads + seg.h * a.group + (m - tok * a.group);
-            const int64_t part = (2 * (int64_t)blockIdx.x + (s_no == 0 ? 0 : 1)) * TILES + (st.two ? stream : 0);
+            const int64_t part = (int64_t)seg.slot * TILES + (st.two ? stream : 0);
             float l = l_run, ref = m_run;
             float w0 = 1.f, w1 = 0.f;  // what the two streams' outputs of a row count
             int col0 = half * OT, cols = OT;  // output columns of this thread
@@ -1159,7 +1239,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 
 // Joins the partial results of an item's rows that several CTAs worked on:
 // out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.  The item's first keys are in the
-// share of exactly one CTA, which the block takes its number from and which has
+// piece of exactly one CTA, which the block takes its number from and which has
 // written down which item that is.  A block takes 16 rows at a time: a row a
 // thread's low bits, so that 16 threads read a run of 256 bytes.
 constexpr int kMergeRows = 16;
@@ -1313,11 +1393,11 @@ kvc_status launch_attn(RaggedArgs &a, const void *q, const void *k, const void *
         return KVC_ERR_CUDA;
     if (kvc_host::launch_chained(kern, dim3(grid), SM::THREADS, smem, stream, tq, tk, tv, a) != cudaSuccess)
         return KVC_ERR_CUDA;
-    if (grid > 1) {
+    if (grid * a.rounds > 1) {
         // blocks for the rows that an item has if requests are alike (they go round for more)
         const int64_t rows_each = (int64_t)((a.tokens + a.batch - 1) / a.batch) * a.group;
         const int64_t blocks = std::min<int64_t>((rows_each + kMergeRows - 1) / kMergeRows, SM::TILES * kBM / kMergeRows);
-        if (kvc_host::launch_chained(ragged_merge_kernel<T, D>, dim3(grid - 1, (unsigned)blocks), 256, 0, stream, a) != cudaSuccess)
+        if (kvc_host::launch_chained(ragged_merge_kernel<T, D>, dim3(grid * a.rounds - 1, (unsigned)blocks), 256, 0, stream, a) != cudaSuccess)
             return KVC_ERR_CUDA;
     }
     return kvc_host::launch_status();
@@ -1336,9 +1416,9 @@ kvc_status dispatch(RaggedArgs &a, const void *q, const void *k, const void *v, 
     }
 }
 
-// the workspace: two partial results of an item for each CTA (one an SM)
+// the workspace: two partial results of an item for each piece of each CTA (one an SM)
 struct Layout {
-    int grid;
+    int grid, rounds;
     int64_t parts;  // of a query tile
     size_t m, l, split, total;
 };
@@ -1346,11 +1426,12 @@ Layout layout_of(int head_dim)
 {
     Layout w;
     w.grid = kvc_host::sm_count();
-    w.parts = 2 * (int64_t)w.grid * (head_dim <= 128 ? 2 : 1);
+    w.rounds = head_dim <= 128 ? 1 : kRounds;
+    w.parts = 2 * (int64_t)w.grid * w.rounds * (head_dim <= 128 ? 2 : 1);
     w.m = (size_t)w.parts * kBM * head_dim * sizeof(float);
     w.l = w.m + (size_t)w.parts * kBM * sizeof(float);
     w.split = w.l + (size_t)w.parts * kBM * sizeof(float);
-    w.total = w.split + (size_t)w.grid * sizeof(int4);
+    w.total = w.split + (size_t)w.grid * w.rounds * sizeof(int4);
     return w;
 }
 
@@ -1427,6 +1508,8 @@ KVC_API kvc_status kvc_gqa_ragged(void *out, const void *q, const void *k_pool, 
     a.scale_log2 = (scale == 0.f ? 1.0f / sqrtf((float)head_dim) : scale) * kLog2e;
     a.status = dev_status;
     const Layout w = layout_of(head_dim);
+    a.rounds = w.rounds;
+    a.key_bytes = kv_heads * head_dim * 4;
     uint8_t *base = static_cast<uint8_t *>(workspace);
     a.ws_o = reinterpret_cast<float *>(base);
     a.ws_m = reinterpret_cast<float *>(base + w.m);

@@ -228,6 +228,12 @@ __device__ __forceinline__ bool named_bar_any(uint32_t id, uint32_t nthreads, bo
     return r != 0;
 }
 
+// arrival on a barrier at a shared-memory address
+__device__ __forceinline__ void arrive_at(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // A bounded wait: false once `abort_flag` is set, or after about a second
 // (which sets it and KVC_DEV_TIMEOUT).
 __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
