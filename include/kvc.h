@@ -929,7 +929,9 @@ kvc_status kvc_tree_commit(void *k_cache, void *v_cache, const int32_t *path,
  * (positions and slots -1 for a row that is unused or whose request was rejected).
  * Pools, tables and pages are those of kvc_paged_append; page_size >= 1, at most
  * 16384 requests (KVC_ERR_UNSUPPORTED), max_pages * page_size and n_pool_pages *
- * page_size below 2^31 (KVC_ERR_CAPACITY).
+ * page_size below 2^31, `tokens` up to 2^31 - 1024 (KVC_ERR_CAPACITY).  What a call
+ * writes may not overlap what it reads (KVC_ERR_SHAPE); in particular a step's
+ * `cached` is not an array of the `len` that it writes: copy it.
  *
  * Free pages are a stack: free_pages device int32 [n_pool_pages], its first
  * *free_count entries (device int32) the ids of the free pages.  Both calls read
@@ -991,7 +993,7 @@ kvc_status kvc_ragged_plan(const int32_t *cached, const int32_t *new_tokens, int
  * positions   up to 2^31 - 1; first >= 0 (KVC_ERR_SHAPE).
  * rotary_dim  even, 2..256 (KVC_ERR_UNSUPPORTED above).  base > 0; factor > 0
  *             (ignored by KVC_ROPE_PLAIN); KVC_ROPE_PARTS: trained >= 1, low < high;
- *             all finite (KVC_ERR_SHAPE).
+ *             all finite, magnitude also as a float32 (KVC_ERR_SHAPE).
  */
 kvc_status kvc_rope_tables(float *cos_table, float *sin_table, int64_t first, int64_t positions,
                            int rotary_dim, double base, int scaling, double factor,
@@ -1017,7 +1019,7 @@ kvc_status kvc_rope_tables(float *cos_table, float *sin_table, int64_t first, in
  *            rotation; rotary_dim is then ignored).
  * A token with slot < 0 is skipped: its row of q_out stays as it was.  So is one
  * with a slot outside the pool (KVC_DEV_INDEX_OOB) or a position outside the tables
- * (KVC_DEV_ROPE_RANGE).  Of two tokens with one slot either may end up there.
+ * (KVC_DEV_ROPE_RANGE).  Two tokens with one slot leave parts of either there.
  * KVC_BF16/KVC_F16; head_dim a multiple of 16 up to 256, rotary_dim a multiple of 16
  * up to head_dim (KVC_ERR_UNSUPPORTED).  q_out and the pools may not overlap what is
  * read (KVC_ERR_SHAPE).
@@ -1043,7 +1045,7 @@ kvc_status kvc_ragged_append(void *q_out, void *k_pool, void *v_pool, const void
  *            rows of `out`, as do rows behind the last request's.  So does one whose
  *            offsets are outside [0, tokens] or not total_abs - past_abs apart
  *            (KVC_DEV_SEQLEN_RANGE), or with more tokens than its row of the table
- *            has room for (KVC_DEV_CAPACITY).  A page id outside the pool among the
+ *            has room for, or than 2^31 - 512 (KVC_DEV_CAPACITY).  A page id outside the pool among the
  *            rows that are read sets KVC_DEV_INDEX_OOB (that request's output is then
  *            undefined).
  * page_size  a multiple of 16 (KVC_ERR_SHAPE).
@@ -1055,7 +1057,8 @@ kvc_status kvc_ragged_append(void *q_out, void *k_pool, void *v_pool, const void
  * its output NaN, whatever the row's weight; a NaN in a K row that it sees makes all
  * of them NaN.  What it does not see may hold anything.
  * workspace  device, kvc_gqa_ragged_workspace_size(...) bytes on the current device,
- *            256-byte aligned.  Calls that may overlap on the GPU need their own.
+ *            256-byte aligned, apart from every other argument (KVC_ERR_SHAPE).
+ *            Calls that may overlap on the GPU need their own.
  */
 kvc_status kvc_gqa_ragged(void *out, const void *q, const void *k_pool, const void *v_pool,
                           const int32_t *offsets, const int32_t *block_table, int max_pages,

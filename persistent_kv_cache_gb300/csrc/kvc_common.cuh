@@ -1,6 +1,7 @@
 // kvc_common.cuh -- shared device/host helpers of the GB300 KV-cache library.
 #pragma once
 
+#include <initializer_list>
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -343,6 +344,26 @@ inline bool overlaps(const void *a, size_t na, const void *b, size_t nb)
     return x < y + nb && y < x + na;
 }
 
+// Bytes that a call reads or writes; does anything written share some with what is read, or
+// with something else written?
+struct Span {
+    const void *at;
+    size_t bytes;
+};
+inline bool collide(std::initializer_list<Span> written, std::initializer_list<Span> read)
+{
+    auto hit = [](const Span &x, const Span &y) { return x.bytes && y.bytes && overlaps(x.at, x.bytes, y.at, y.bytes); };
+    for (const Span *w = written.begin(); w != written.end(); ++w) {
+        for (const Span *o = w + 1; o != written.end(); ++o)
+            if (hit(*w, *o))
+                return true;
+        for (const Span &r : read)
+            if (hit(*w, r))
+                return true;
+    }
+    return false;
+}
+
 inline int elem_bytes_of(int dtype)
 {
     return dtype == KVC_F32 ? 4 : (dtype == KVC_BF16 || dtype == KVC_F16) ? 2 : 0;
@@ -416,10 +437,9 @@ bool encode_4d_heads_sw128(CUtensorMap *map, const void *base, uint64_t heads, u
 // the same tensor as (span, rows, heads, column blocks): a box of (span,
 // box_rows, box_heads, every block) lands as [blocks][box_heads][box_rows]
 // [128 B], i.e. column block by column block, the heads' rows stacked
-// (box_blocks: that many blocks a box instead of every one)
 bool encode_4d_blocks_sw128(CUtensorMap *map, const void *base, uint64_t heads, uint64_t rows,
                             uint64_t cols, uint32_t elem_bytes, uint32_t box_rows,
-                            uint32_t box_heads, CUtensorMapDataType type, uint32_t box_blocks = 0);
+                            uint32_t box_heads, CUtensorMapDataType type);
 
 } // namespace kvc_host
 

@@ -20,6 +20,7 @@ namespace {
 constexpr int kPlanThreads = 256;
 constexpr int kPlanTokens = 4 * kPlanThreads;  // tokens of a block
 constexpr int kMaxRequests = 16384;            // two words of shared memory each
+constexpr int kMaxTokens = INT_MAX - 1023;     // (a last block's tokens are numbered past the end)
 
 // Inclusive prefix sum over the block's threads; `sums` holds a word a warp.
 __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t *sums, int64_t &total)
@@ -627,15 +628,17 @@ KVC_API kvc_status kvc_page_release(const int32_t *released, const int32_t *bloc
         return st;
     if (!free_pages || !free_count || !free_left || (batch > 0 && (!released || !block_table)))
         return KVC_ERR_NULL;
-    if (free_left == free_count)
+    const size_t rows = (size_t)batch * sizeof(int32_t), one = sizeof(int32_t);
+    if (kvc_host::collide({{free_pages, n_pool_pages * one}, {free_left, one}},
+                          {{released, rows}, {block_table, rows * max_pages}, {free_count, one}}))
         return KVC_ERR_SHAPE;
     const ReleaseArgs a{released, block_table, max_pages, page_size, free_pages, {free_count, n_pool_pages}, free_left,
                         batch, dev_status};
-    const size_t smem = (size_t)batch * sizeof(int32_t);
+    const size_t smem = rows;
     if (!allow_smem(page_release_kernel, smem))
         return KVC_ERR_CUDA;
-    const int rows = kPlanThreads / 32;
-    const int grid = std::max(1, std::min((batch + rows - 1) / rows, kvc_host::sm_count()));
+    const int warps = kPlanThreads / 32;
+    const int grid = std::max(1, std::min((batch + warps - 1) / warps, kvc_host::sm_count()));
     if (kvc_host::launch_chained(page_release_kernel, dim3(grid), kPlanThreads, smem, static_cast<cudaStream_t>(stream_), a) !=
         cudaSuccess)
         return KVC_ERR_CUDA;
@@ -653,13 +656,26 @@ KVC_API kvc_status kvc_ragged_plan(const int32_t *cached, const int32_t *new_tok
         return st;
     if (tokens < 0)
         return KVC_ERR_SHAPE;
+    if (tokens > kMaxTokens)
+        return KVC_ERR_CAPACITY;
     if (!free_pages || !free_count || !free_left || !offsets || (tokens > 0 && (!positions || !slots)) ||
         (batch > 0 && (!cached || !new_tokens || !block_table || !kvc_host::lengths_ok(len))))
         return KVC_ERR_NULL;
     if (!kvc_host::aligned16(positions) || !kvc_host::aligned16(slots))
         return KVC_ERR_ALIGN;
-    if (free_left == free_count)
+    // (every block reads what the requests hold and bring, block 0 writes: a step's `cached` may not be the lengths
+    // that the step before wrote into the same plan)
+    const size_t rows = (size_t)batch * sizeof(int32_t), one = sizeof(int32_t), places = tokens * one;
+    const std::initializer_list<kvc_host::Span> read = {
+        {cached, rows}, {new_tokens, rows}, {free_pages, n_pool_pages * one}, {free_count, one}};
+    if (kvc_host::collide({{block_table, rows * max_pages}, {offsets, rows + one}, {positions, places}, {slots, places},
+                           {free_left, one}}, read))
         return KVC_ERR_SHAPE;
+    for (const void *p : {len.past_abs, len.cache_past, len.total_abs, len.cache_total, len.evict})
+        if (kvc_host::collide({{p, rows}}, read) ||
+            kvc_host::collide({{p, rows}}, {{block_table, rows * max_pages}, {offsets, rows + one}, {positions, places},
+                                            {slots, places}, {free_left, one}}))
+            return KVC_ERR_SHAPE;
     const PlanArgs a{cached, new_tokens, block_table, max_pages, page_size, free_pages, {free_count, n_pool_pages},
                      free_left, batch, tokens, offsets, len, positions, slots, dev_status};
     const size_t smem = (2 * (size_t)batch + 1) * sizeof(int32_t);
@@ -680,7 +696,7 @@ KVC_API kvc_status kvc_rope_tables(float *cos_table, float *sin_table, int64_t f
         return KVC_ERR_SHAPE;
     if (rotary_dim > 2 * kMaxPairs || scaling < KVC_ROPE_PLAIN || scaling > KVC_ROPE_PARTS)
         return KVC_ERR_UNSUPPORTED;
-    if (!(base > 0.0) || !std::isfinite(base) || !std::isfinite(magnitude))
+    if (!(base > 0.0) || !std::isfinite(base) || !std::isfinite((float)magnitude))
         return KVC_ERR_SHAPE;
     if (scaling != KVC_ROPE_PLAIN && (!(factor > 0.0) || !std::isfinite(factor)))
         return KVC_ERR_SHAPE;
@@ -744,7 +760,7 @@ KVC_API kvc_status kvc_ragged_append(void *q_out, void *k_pool, void *v_pool, co
         return KVC_ERR_SHAPE;
     if (head_dim % 16 || head_dim > 256 || q_heads > 32767 || kv_heads > 32767)
         return KVC_ERR_UNSUPPORTED;
-    if (n_pool_pages > INT32_MAX || n_pool_pages * page_size > INT32_MAX)
+    if (n_pool_pages > INT32_MAX || n_pool_pages * page_size > INT32_MAX || tokens > kMaxTokens)
         return KVC_ERR_CAPACITY;
     if ((rope_cos == nullptr) != (rope_sin == nullptr))
         return KVC_ERR_NULL;
@@ -786,6 +802,13 @@ KVC_API kvc_status kvc_ragged_append(void *q_out, void *k_pool, void *v_pool, co
     for (const void *p : {(const void *)k_pool, (const void *)v_pool})
         if (kvc_host::overlaps(p, pool, q, q_bytes) || kvc_host::overlaps(p, pool, k, k_bytes) ||
             kvc_host::overlaps(p, pool, v, v_bytes))
+            return KVC_ERR_SHAPE;
+    // (positions are 32-bit: no row of the tables past 2^31 is read)
+    const size_t list = tokens * sizeof(int32_t), weight = head_dim * 2,
+                 table = rope_cos ? (size_t)std::min<int64_t>(rope_max_pos, (int64_t)1 << 31) * (rotary_dim / 2) * 4 : 0;
+    for (const kvc_host::Span &w : {kvc_host::Span{q_out, out}, kvc_host::Span{k_pool, pool}, kvc_host::Span{v_pool, pool}})
+        if (kvc_host::collide({w}, {{positions, list}, {slots, list}, {rope_cos, table}, {rope_sin, table},
+                                    {q_weight, q_weight ? weight : 0}, {k_weight, k_weight ? weight : 0}}))
             return KVC_ERR_SHAPE;
     const AppendArgs a{q_out, k_pool, v_pool, q, k, v, q_stride, k_stride, v_stride, q_weight, k_weight, eps, positions,
                        slots, tokens, q_heads, kv_heads, head_dim, page_size, n_pool_pages * page_size,

@@ -17,6 +17,8 @@
 #include <cmath>
 #include <type_traits>
 
+#include <cudaTypedefs.h>
+
 #include "kvc_common.cuh"
 #include "kvc_tc.cuh"
 
@@ -27,6 +29,7 @@ constexpr int kBM = 128, kBN = 128;
 constexpr float kRescale = 8.f;  // log2 units by which a score may exceed the reference maximum
 constexpr int kItemCost = 512;   // keys that stand for what an item costs beside its keys
 constexpr int kMaxRequests = 65535;
+constexpr int kMaxKeys = INT_MAX - 511;  // of a request: rows are rounded up to tiles and items in 32 bits
 
 struct RaggedArgs {
     void *out;
@@ -69,7 +72,7 @@ __device__ __forceinline__ Request request(const RaggedArgs &a, int b, uint32_t 
     if (L >= 0 && r.P >= 0) {
         if (T < r.P || o0 < 0 || o1 < o0 || o1 > a.tokens || T - r.P != o1 - o0)
             bad = KVC_DEV_SEQLEN_RANGE;
-        else if (T > (int64_t)a.max_pages * a.page_size)
+        else if (T > min((int64_t)a.max_pages * a.page_size, (int64_t)kMaxKeys))
             bad = KVC_DEV_CAPACITY;
         else
             r.n = o1 - o0;
@@ -397,8 +400,9 @@ __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch
 // the attention
 // --------------------------------------------------------------------------
 //
-//   TMEM columns  an output O of D columns and a buffer S of 128 for each of two
-//                 streams (head_dim 256: one O, two buffers S)
+//   TMEM columns  an output O of D columns and a score buffer S of 128 for each of two
+//                 streams, the weights over the scores (64: in 64 columns of their
+//                 own; 256: one O, two buffers S)
 //   shared        queries (two tiles; 256: one) | ring of slabs of K and V
 //   warp 0        TMA of the queries, the score products
 //   warps 1, 2    TMA of K and of V into one ring in the order of use
@@ -406,15 +410,30 @@ __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch
 //   other warps   softmax and output: eight a stream, two threads a row (= TMEM
 //                 lane), each half of the columns
 //
-// head_dim <= 128: the warps 4-7 and 8-11 are two streams, each with a score buffer
+// head_dim <= 128: the warps 4-11 and 12-19 are two streams, each with a score buffer
 // and an output of its own, so that one's softmax runs while the other's products
 // do.  An item of two query tiles gives each stream one of them, over the same keys
 // (read once for both); an item of one tile (a decoding request, the end of a prompt)
 // gives each stream every second key tile, and the two results are joined
-// in tensor memory at the end.  A thread has a row, and writes the weights as 16-bit
-// pairs over the scores that it has read.
-// head_dim 256: no room for two outputs; two threads a row (each half of the
-// columns), the two score buffers used in turn.
+// from tensor memory at the end.
+// head_dim 256: no room for two outputs; one stream, the two score buffers in turn.
+//
+// What bounds it (one GB300, bf16; times of the whole call, with the join):
+//   chunks of 8 prompts, head_dim 128, group 4, 770 GFLOP: 616 us, 66 % of the measured
+//   bf16 peak.  A pair of tiles takes 3900 clocks where its products need 2048: a
+//   stream's chain (scores 512, their maximum 370, weights 1150, output products 512, the
+//   barriers between them) is longer than two streams hide.  Three streams, or scores a
+//   tile ahead, want more than the 512 columns of tensor memory.  Steps on the way: one
+//   thread a row, unrolled, with its scores in registers 869 us (the code missed the
+//   instruction cache; a spilled register in the loop costs the release of every
+//   arrival behind it hundreds of clocks); two threads a row and rolled loops 650.
+//   windowed chunks, head_dim 256, 825 GFLOP: 618 us, 70 %.  128 KB of K and V a tile for
+//   16.8 MFLOP: L2 delivers about 10 TB/s.
+//   decoding batch, 571 MB: 99 to 101 us, 84 % of the measured copy rate.
+//   decoding and prompts, head_dim 64, window 1000, pages of 16 (127 MB): 107 us; nine
+//   tiles an item, three of them cut, and the exponentials of 128 rows for a decoding
+//   request's eight.
+//   17 tokens of one user over 700: 18.5 us, a chain of loads (lengths, table, rows, join).
 //
 // Only key tiles that hold the last tokens' own rows, or that a window's edge cuts,
 // are masked ("cut" tiles).  A NaN or an infinity in a column of V makes that column of
@@ -1365,6 +1384,28 @@ ragged_merge_kernel(const RaggedArgs a)
     }
 }
 
+// The packed queries [tokens, q_heads, D] as (64 columns, heads, tokens, D / 64 column
+// blocks): a box of (64, group, toks, 1) is a column block of a query tile.
+bool encode_queries(CUtensorMap *map, const void *q, const RaggedArgs &a, int D, CUtensorMapDataType type)
+{
+    static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    if (!encode)
+        return false;
+    const cuuint64_t dims[4] = {64, (cuuint64_t)a.q_heads, (cuuint64_t)a.tokens, (cuuint64_t)D / 64};
+    const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)a.q_heads * D * 2, 128};
+    const cuuint32_t box[4] = {64, (cuuint32_t)a.group, (cuuint32_t)a.toks, 1}, step[4] = {1, 1, 1, 1};
+    return encode(map, type, 4, const_cast<void *>(q), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
 template <typename T, int D>
 kvc_status launch_attn(RaggedArgs &a, const void *q, const void *k, const void *v, int grid, cudaStream_t stream)
 {
@@ -1376,8 +1417,7 @@ kvc_status launch_attn(RaggedArgs &a, const void *q, const void *k, const void *
     const int k_blocks = a.box_rows == kBN ? D / 64 / SM::SPT : 1, v_rows = std::min(a.box_rows, SM::KR),
               v_blocks = v_rows == SM::KR ? D / 64 : 1;
     CUtensorMap tq, tk, tv;
-    if (!kvc_host::encode_4d_blocks_sw128(&tq, q, (uint64_t)a.tokens, (uint64_t)a.q_heads, D, 2, (uint32_t)a.group,
-                                          (uint32_t)a.toks, tt, 1) ||
+    if (!encode_queries(&tq, q, a, D, tt) ||
         !kvc_host::encode_3d_sw128(&tk, k, rows, D, a.box_rows, k_blocks, tt) ||
         !kvc_host::encode_3d_sw128(&tv, v, rows, D, v_rows, v_blocks, tt))
         return KVC_ERR_CUDA;
@@ -1480,6 +1520,13 @@ KVC_API kvc_status kvc_gqa_ragged(void *out, const void *q, const void *k_pool, 
         return KVC_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u)
         return KVC_ERR_ALIGN;
+    const size_t each = (size_t)batch * sizeof(int32_t);
+    const kvc_host::Span offs{offsets, each + sizeof(int32_t)}, table{block_table, each * max_pages}, past{len.past_abs, each},
+        total{len.total_abs, each}, resident{len.cache_total, each};
+    if (kvc_host::collide({{out, rows}}, {offs, table, past, total, resident}) ||
+        kvc_host::collide({{workspace, workspace_bytes}}, {{out, rows}, {q, rows}, {k_pool, pool}, {v_pool, pool}, offs, table, past,
+                                                           total, resident}))
+        return KVC_ERR_SHAPE;
     RaggedArgs a{};
     a.out = out;
     a.offsets = offsets;

@@ -265,7 +265,7 @@ bool encode_4d_heads_sw128(CUtensorMap *map, const void *base, uint64_t heads, u
 
 bool encode_4d_blocks_sw128(CUtensorMap *map, const void *base, uint64_t heads, uint64_t rows,
                             uint64_t cols, uint32_t elem_bytes, uint32_t box_rows,
-                            uint32_t box_heads, CUtensorMapDataType type, uint32_t box_blocks)
+                            uint32_t box_heads, CUtensorMapDataType type)
 {
     PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
     if (!fn || elem_bytes == 0 || 128 % elem_bytes != 0)
@@ -275,7 +275,7 @@ bool encode_4d_blocks_sw128(CUtensorMap *map, const void *base, uint64_t heads, 
         return false;
     cuuint64_t dims[4] = {span, rows, heads, cols / span};
     cuuint64_t strides[3] = {cols * elem_bytes, rows * cols * elem_bytes, 128};
-    cuuint32_t box[4] = {(cuuint32_t)span, box_rows, box_heads, box_blocks ? box_blocks : (cuuint32_t)(cols / span)};
+    cuuint32_t box[4] = {(cuuint32_t)span, box_rows, box_heads, (cuuint32_t)(cols / span)};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     CUresult r = fn(map, type, 4, const_cast<void *>(base), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,

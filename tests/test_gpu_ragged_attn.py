@@ -203,6 +203,20 @@ def test_long_chunk(K, D):
     c.check(out, 400, some=some)
 
 
+def test_shares_in_pieces(K):
+    """head_dim 256 and more keys than L2 holds: the CTAs' shares are in two or three pieces (2.6 million units of the line,
+    167 MB of keys and values), with and without a window."""
+    c = Case(K, 60, [4096, 3900, 4200, 4096], [1024, 1000, 1100, 1], 8, 4, 256, 64)
+    some = [0, 1, 31, 32, 63, 64, 500, 767, 999]
+    out, st = c.run()
+    assert st == 0
+    c.check(out, some=some)
+    again, _ = c.run()
+    assert torch.equal(out, again)
+    out, st = c.run(local_window_size=4000)
+    c.check(out, 4000, some=some)
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("scale", [1.0, 0.01, -0.3])
 def test_scales(K, scale, D):
@@ -454,3 +468,48 @@ def test_a_whole_step(K):
                 R.assert_within(out[o:o + z, h * G:(h + 1) * G].reshape(-1, D), want, bound, f"step {step} request {b}")
             cached[b], o = total, o + z
         assert torch.equal(out[o:], torch.zeros_like(out[o:]))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_requests_that_share_pages(K, D):
+    """A prefix whose pages are in three rows of the table, and a page twice in one of them."""
+    page, H = 32, 2
+    c = Case(K, 50, [200, 220, 192, 64], [20, 1, 150, 1], H, 4, D, page)
+    for b in (1, 2):
+        c.table[b, :6] = c.table[0, :6]
+        for x, y in zip(c.rows[b], c.rows[0]):
+            x[:, :192] = y[:, :192]
+    c.table[3, 1] = c.table[3, 0]
+    for x in c.rows[3]:
+        x[:, 32:64] = x[:, :32]
+    out, st = c.run()
+    assert st == 0
+    c.check(out)
+
+
+@pytest.mark.parametrize("D", [64, 256])
+def test_positions_up_to_the_last(K, D):
+    """Positions up to 2^31 - 512 in a window, the table's entries all one page; a request past that is rejected."""
+    page, H, G, W, n = 112, 2, 4, 300, 5
+    most, last = ((1 << 31) - 1) // page, (1 << 31) - 512
+    c = Case(K, 51, [0], [page], H, G, D, page)
+    c.new, c.past = [n, 1], [last - n, last]
+    c.T = n + 1
+    table = torch.full((2, most), int(c.table[0, 0]), dtype=torch.int32, device="cuda")
+    c.offsets = torch.tensor([0, n, n + 1], dtype=torch.int32)
+    t = lambda x: torch.tensor(x, dtype=torch.int32)  # noqa: E731
+    total = [last, last + 1]
+    c.lens = torch.stack([t(c.past), t(total), t(c.past), t(total), t([0, 0])])
+    out, q, k, v, _, offsets = c.gpu()
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    K.kvc_gqa_ragged(out, q, k, v, table, offsets, c.L, local_window_size=W, status=st)
+    assert st.item() == K.KVC_DEV_CAPACITY
+    # the same window over the rows that the positions fall on
+    first = last - n - W
+    at = (torch.arange(first, last) % page)
+    c.rows[0] = tuple(x[:, at] for x in c.rows[0])
+    c.past[0] -= first
+    got = out.cpu()
+    want, bound = c.want(0, W)
+    R.assert_within(got[:n], want, bound, "last positions")
+    assert torch.equal(got[n:], c.out[n:])

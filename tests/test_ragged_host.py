@@ -167,3 +167,62 @@ def test_append_binding_refuses(K):
 
 def test_struct_of_lengths_is_five_addresses(K):
     assert ctypes.sizeof(K.KvcLengths) == 5 * ctypes.sizeof(ctypes.c_void_p)
+
+
+def test_release_and_plan_write_apart_from_what_they_read(K):
+    A = [i << 20 for i in range(1, 20)]
+    f = caller(K.library().kvc_page_release, released=A[0], table=A[1], max_pages=4, page=16, free=A[2], pool=64, count=A[3],
+               left=A[4], batch=8, status=None, stream=None)
+    for kw in (dict(released=A[2] + 252), dict(table=A[2] - 124), dict(count=A[2]), dict(left=A[2] + 128), dict(left=A[0] + 28),
+               dict(left=A[1])):
+        assert f(**kw) == 2, kw
+    L = lambda at: K.KvcLengths(*at)  # noqa: E731
+    lens = A[10:15]
+    f = caller(K.library().kvc_ragged_plan, cached=A[0], new=A[1], table=A[2], max_pages=4, page=16, free=A[3], pool=64, count=A[4],
+               left=A[5], batch=8, tokens=100, offsets=A[6], len=L(lens), positions=A[7], slots=A[8], status=None, stream=None)
+    for i, at in enumerate(lens):
+        # the lengths of the step before as what is cached now
+        assert f(cached=at) == 2 and f(new=at + 28) == 2, i
+        for over in (A[2] + 124, A[3] + 252, A[4], A[5], A[6] + 32, A[7] + 384, A[8]):
+            assert f(len=L(lens[:i] + [over] + lens[i + 1:])) == 2, (i, over)
+    for kw in (dict(cached=A[6]), dict(new=A[7]), dict(cached=A[8] + 396), dict(table=A[3]), dict(table=A[0] - 124), dict(offsets=A[7]),
+               dict(left=A[0]), dict(left=A[6] + 32), dict(slots=A[7] + 384), dict(free=A[2])):
+        assert f(**kw) == 2, kw
+    assert f(tokens=(1 << 31) - 1023) == 6
+
+
+def test_append_writes_apart_from_lists_tables_and_weights(K):
+    G = 1 << 30
+    f = caller(K.library().kvc_ragged_append, q_out=G, k_pool=2 * G, v_pool=3 * G, q=4 * G, k=5 * G, v=6 * G, qs=512, ks=256, vs=256,
+               qw=7 * G, kw=7 * G + 256, eps=1e-6, positions=8 * G, slots=8 * G + 16, tokens=4, q_heads=4, kv_heads=2, pool=8, page=16,
+               dim=128, dtype=1, turned=64, inter=0, cos=9 * G, sin=10 * G, rmax=64, status=None, stream=None)
+    for at, size in ((G, 4 * 4 * 128 * 2), (2 * G, 8 * 16 * 2 * 128 * 2), (3 * G, 8 * 16 * 2 * 128 * 2)):
+        for name, own in (("qw", 256), ("kw", 256), ("positions", 16), ("slots", 16), ("cos", 64 * 32 * 4), ("sin", 64 * 32 * 4)):
+            assert f(**{name: at + size - 16}) == 2 and f(**{name: at - own + 16}) == 2, (name, at)
+    assert f(cos=1 << 40, rmax=1 << 62, sin=G // 2) == 2  # (tables past 2^31 positions)
+    assert f(tokens=(1 << 31) - 1023) == 6
+
+
+def test_attention_writes_apart_from_what_it_reads(K):
+    G = 1 << 30
+    size = K.library().kvc_gqa_ragged_workspace_size(2, 4, 4, 2, 128)
+    assert size < G
+    f = caller(K.library().kvc_gqa_ragged, out=G, q=2 * G, k=3 * G, v=4 * G, offsets=5 * G, table=6 * G, max_pages=4, pool=8, page=16,
+               len=K.KvcLengths(7 * G, 8 * G, 9 * G, 10 * G, 11 * G), batch=2, tokens=4, q_heads=4, kv_heads=2, dim=128, dtype=1,
+               window=0, scale=0.0, ws=12 * G, bytes=size, status=None, stream=None)
+    for at, span in ((G, 4 * 4 * 128 * 2), (12 * G, size)):
+        last = at + span - 4
+        assert f(offsets=last) == 2 and f(offsets=at - 8) == 2 and f(table=last) == 2 and f(table=at - 28) == 2
+        for i in (0, 1, 3):  # those that are read
+            lens = [7 * G, 8 * G, 9 * G, 10 * G, 11 * G]
+            lens[i] = last
+            assert f(len=K.KvcLengths(*lens)) == 2, i
+    for name in ("out", "q", "k", "v"):
+        assert f(**{name: 12 * G}) == 2, name
+    assert f(out=12 * G + (size - 16) // 16 * 16) == 2
+
+
+def test_magnitude_beyond_float32(K):
+    f = caller(K.library().kvc_rope_tables, cos=FAKE, sin=FAKE * 8, first=0, positions=8, dim=64, base=1e4, scaling=0, factor=0.0,
+               trained=0, low=0.0, high=0.0, magnitude=1e39, stream=None)
+    assert f() == 2
