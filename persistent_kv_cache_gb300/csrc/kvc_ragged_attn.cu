@@ -419,7 +419,7 @@ __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch
 // head_dim 256: no room for two outputs; one stream, the two score buffers in turn.
 //
 // What bounds it (one GB300, bf16; times of the whole call, with the join):
-//   chunks of 8 prompts, head_dim 128, group 4, 770 GFLOP: 616 us, 66 % of the measured
+//   chunks of 8 prompts, head_dim 128, group 4, 770 GFLOP: 608 us, 67 % of the measured
 //   bf16 peak.  A pair of tiles takes 3900 clocks where its products need 2048: a
 //   stream's chain (scores 512, their maximum 370, weights 1150, output products 512, the
 //   barriers between them) is longer than two streams hide.  Three streams, or scores a
@@ -427,10 +427,10 @@ __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch
 //   thread a row, unrolled, with its scores in registers 869 us (the code missed the
 //   instruction cache; a spilled register in the loop costs the release of every
 //   arrival behind it hundreds of clocks); two threads a row and rolled loops 650.
-//   windowed chunks, head_dim 256, 825 GFLOP: 618 us, 70 %.  128 KB of K and V a tile for
+//   windowed chunks, head_dim 256, 825 GFLOP: 587 us, 74 %.  128 KB of K and V a tile for
 //   16.8 MFLOP: L2 delivers about 10 TB/s.
 //   decoding batch, 571 MB: 99 to 101 us, 84 % of the measured copy rate.
-//   decoding and prompts, head_dim 64, window 1000, pages of 16 (127 MB): 107 us; nine
+//   decoding and prompts, head_dim 64, window 1000, pages of 16 (127 MB): 106 us; nine
 //   tiles an item, three of them cut, and the exponentials of 128 rows for a decoding
 //   request's eight.
 //   17 tokens of one user over 700: 18.5 us, a chain of loads (lengths, table, rows, join).
@@ -506,11 +506,17 @@ __device__ __forceinline__ int v_group(int j, int n)
     return j < paired ? lead + 2 * j : lead + paired + j;
 }
 
-// the 16-bit halves of w that are NaN or infinite, as 0xffff each
+// The 16-bit halves of w that are NaN or infinite: bit 15 of each (the other bits are
+// anything), which an exponent of ones carries into; then 0xffff for each.  (Comparing
+// halves took several instructions more a word: chunks 617 -> 608, windowed 620 -> 604 us.)
+template <typename T> __device__ __forceinline__ uint32_t odd_bits(uint32_t w)
+{
+    constexpr bool H = std::is_same<T, __half>::value;
+    return (w & (H ? 0x7c007c00u : 0x7f807f80u)) + (H ? 0x04000400u : 0x00800080u);
+}
 template <typename T> __device__ __forceinline__ uint32_t not_finite(uint32_t w)
 {
-    constexpr uint32_t ex = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
-    return __vcmpeq2(w & ex, ex);
+    return (odd_bits<T>(w) >> 15 & 0x10001u) * 0xffffu;
 }
 
 // Scores of up to 32 columns: those outside [lo, hi] become -infinity, and a negative
@@ -950,7 +956,8 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         const uint32_t stream_bar = 10 + stream;
         // what a tile does not need, kept apart from the registers that its scores take
         Kept *kept = reinterpret_cast<Kept *>(smem + SM::WALK_OFF) + stream;
-        const bool scout = quad == 0 && half == 0;  // of a stream's warps, the one that looks ahead
+        // of a stream's warps, the one that looks ahead: one that a decoding request's few rows leave idle
+        const bool scout = quad == 3 && half == 1;
         if (scout && lane == 0) {
             kept->walk = walk;
             kept->seg[0] = cur;
@@ -996,8 +1003,22 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             float m_run = -INFINITY, l_run = 0.f;
             for (int j = 0; j < st.n; ++j) {
                 const bool cut = j < head_cut || j >= tail_cut;
-                if (cut) {
-                    // V rows with a NaN or an infinity in them, a bit each in bad_sh (zero before)
+                // Before the scores are waited for with two streams, so that both come to it at once and before the
+                // first output products of EARLY; with one stream after the weights, by when V is there (608 -> 604 us).
+                auto scan = [&]() {
+                    // V rows with a NaN or an infinity in them, a bit each in bad_sh (zero before).
+                    // Rows that all of the item's tokens see need none of that: looked at are groups of kRows rows with
+                    // another among them (604 -> 589 us, windowed chunks at 256; at 64, whose groups are one load of a
+                    // thread, finding out took longer: 107.7 -> 109.2, decoding and prompts).
+                    constexpr int kRows = kSoftmax / 8, kGroups = KR / kRows;
+                    int all_lo = 0, all_hi = -1;
+                    if (D > 64) {
+                        const Segment &seg = kept->seg[s_no & 1];
+                        const int base = seg.lo + (seg.t0 + j) * kBN;
+                        all_hi = seg.P + seg.i * a.item - base;
+                        all_lo = a.window > 0 ? seg.P + min(seg.n, (seg.i + 1) * a.item) - a.window - base : INT_MIN / 2;
+                    }
+                    auto looked_at = [&](int row) { return row < all_lo || row + kRows - 1 > all_hi; };
                     bool found = false;
 #pragma unroll
                     for (int hf = 0; hf < SPT; ++hf) {
@@ -1007,10 +1028,17 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                             break;
                         const uint4 *v = reinterpret_cast<const uint4 *>(smem + SM::RING_OFF + (qi % NSLAB) * SM::SLAB);
 #pragma unroll
-                        for (int e = 0; e < SM::SLAB / 16 / kSoftmax; ++e) {
-                            const uint4 x = v[tid + kSoftmax * e];
-                            if (not_finite<T>(x.x) | not_finite<T>(x.y) | not_finite<T>(x.z) | not_finite<T>(x.w)) {
-                                const int vr = hf * KR + (((tid + kSoftmax * e) >> 3) & (KR - 1));
+                        for (int g = 0; g < kGroups; ++g) {
+                            if (!looked_at(hf * KR + g * kRows))
+                                continue;
+                            uint32_t odd = 0;
+#pragma unroll
+                            for (int c = 0; c < D / 64; ++c) {
+                                const uint4 x = v[tid + kSoftmax * (g + c * kGroups)];
+                                odd |= odd_bits<T>(x.x) | odd_bits<T>(x.y) | odd_bits<T>(x.z) | odd_bits<T>(x.w);
+                            }
+                            if (odd & 0x80008000u) {
+                                const int vr = hf * KR + g * kRows + (tid >> 3);
                                 atomicOr(&bad_sh[vr >> 5], 1u << (vr & 31));
                                 found = true;
                             }
@@ -1060,7 +1088,10 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                             uint4 *v = reinterpret_cast<uint4 *>(
                                 smem + SM::RING_OFF + (q0 + SPT * v_group(j, st.n) + hf) % NSLAB * SM::SLAB);
 #pragma unroll 1
-                            for (int at = tid; at < SM::SLAB / 16; at += kSoftmax) {
+                            for (int e = 0; e < SM::SLAB / 16 / kSoftmax; ++e) {
+                                if (!looked_at(hf * KR + e % kGroups * kRows))
+                                    continue;
+                                const int at = tid + kSoftmax * e;
                                 const uint4 x = v[at];
                                 const uint4 nf = make_uint4(not_finite<T>(x.x), not_finite<T>(x.y), not_finite<T>(x.z),
                                                             not_finite<T>(x.w));
@@ -1072,7 +1103,9 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                         // (either stream's products may come first)
                         kvc_tc::named_bar_sync(all_bar, kSoftmax);
                     }
-                }
+                };
+                if (TILES == 2 && cut)
+                    scan();
                 if (TILES == 2 && !st.has(stream, j))
                     continue;
                 const int s = TILES == 2 ? stream : (int)(used & 1);
@@ -1142,6 +1175,8 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     if (lane == 0)
                         kvc_tc::arrive_at(half_there);
                 }
+                if (TILES == 1 && cut)
+                    scan();
                 kvc_tc::fence_before();
                 __syncwarp();
                 if (lane == 0)

@@ -513,3 +513,25 @@ def test_positions_up_to_the_last(K, D):
     want, bound = c.want(0, W)
     R.assert_within(got[:n], want, bound, "last positions")
     assert torch.equal(got[n:], c.out[n:])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("W", [0, 150])
+def test_a_value_row_that_is_not_finite_anywhere(K, D, W):
+    """One value that is no number in a V row, the row in each place of tiles that are cut, and of those beside them:
+    its column is NaN for the tokens that see the row, and for no other."""
+    places = [0, 31, 32, 62, 63, 64, 95, 96, 127, 128, 129, 159, 160, 161, 191, 192, 199, 200, 201, 220, 223, 224, 239]
+    c = Case(K, D + W, [200] * len(places), [40] * len(places), 1, 4, D, 16)
+    for b, r in enumerate(places):
+        bad = c.rows[b][1][:, r].clone()
+        bad[:, b % D] = (math.nan, math.inf, -math.inf)[b % 3]
+        c.set_row(b, r, v=bad)
+    out, st = c.run(local_window_size=W)
+    assert st == 0
+    for b, r in enumerate(places):
+        got, pos = out[40 * b:40 * b + 40], 200 + torch.arange(40)
+        nan = torch.zeros(got.shape, dtype=torch.bool)
+        nan[(pos >= r) & (pos - r < (W or 1 << 30)), :, b % D] = True
+        assert torch.equal(torch.isnan(got), nan), f"row {r}"
+        want, bound = _clean(c, b, W)
+        assert ((got.double() - want).abs() <= bound)[~nan].all(), f"row {r}"
