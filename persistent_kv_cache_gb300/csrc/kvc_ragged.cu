@@ -148,6 +148,8 @@ struct PlanArgs {
 // that down, and each block fills in the places of its 1024 tokens: a token
 // that begins a page that its request did not hold writes the page's id into the table.
 // (One launch: a second one for the tokens would cost as much as the sums.)
+// A chain of loads and barriers bounds both kernels: 6.3 us the two for 32 requests, 10.2
+// for 256 with 16 prompts (17000 tokens).
 __global__ void __launch_bounds__(kPlanThreads)
 ragged_plan_kernel(const PlanArgs a)
 {
@@ -311,7 +313,8 @@ struct TurnRates {
 // cos and sin of x / 2^32 turns: the nearest quarter turn in whole numbers, the rest u,
 // at most an eighth of a turn, by the Taylor series of sin and cos of 2 pi u (terms
 // (2 pi)^k / k!; the first left out are below 2^-29).  With sincospif, which reduces
-// its argument again, the 131072 x 64 table took 34 us.
+// its argument again, the 131072 x 64 table took 34 us, now 14.7: 67 % of the copy rate,
+// with two thirds of the issue slots taken.
 __device__ __forceinline__ void turn(uint32_t x, float magnitude, float &c, float &s)
 {
     const uint32_t q = (x + (1u << 29)) >> 30;
@@ -407,10 +410,12 @@ template <typename T> __device__ __forceinline__ float2 unpack2(uint32_t w)
 //     (x cos w + x' sin w') / rms
 // with its partner x' (of the lane that holds the pair's other half, or the same
 // word), the sine negative for a pair's first; cos w and sin w' are made once for the
-// token's rows that a group has (a dozen where there are tokens enough: with three rows
-// a group, making them took more instructions than the rows).  Products and the sum are rounded separately: without a norm w and 1 / rms
+// token's rows that a group has (with three rows a group, making them took more
+// instructions than the rows).  Products and the sum are rounded separately: without a norm w and 1 / rms
 // are 1 and the bits those of the other calls' rotation.  A lane asks for kAhead rows
 // before it works on the first (one at a time held the pass to 2.6 TB/s).
+// 16384 tokens of 48 rows of 128, normed and rotated: 79 us, 5.2 TB/s or 76 % of the copy
+// rate, with 55 % of the issue slots taken; 1543 of 80 rows of 64: 9.4 us; 32 tokens: 3.7.
 constexpr int kAhead = 4;
 enum Turn { kNoTurn, kHalves, kNeighbours };
 
@@ -592,9 +597,16 @@ template <typename T> cudaError_t launch_append(const AppendArgs &a, cudaStream_
     while (lpr * 8 < a.D)
         lpr *= 2;
     const int groups = 256 / lpr, sms = kvc_host::sm_count();
-    // Rows of a group: a dozen, or as few as make four blocks an SM; the groups of a token in parts of its rows,
-    // at least three where there are that many groups, so that most have to do with one kind alone.
-    const int each = (int)std::max<int64_t>(1, std::min<int64_t>(12, (int64_t)a.tokens * rows / ((int64_t)groups * 4 * sms)));
+    // Rows of a group: as few as make three blocks an SM, or all of a token's (rows are taken four at a time, and a
+    // group makes cos, sin and weights once; a dozen at most and four blocks, rounded down, took 83 for 79 us with 16384
+    // tokens of 48 rows, 13.2 for 9.3 with 1543 of 80, 7.9 for 5.7 with 512 of 48, 3.7 with 32 either way).  Where
+    // blocks of whole tokens leave the last wave of four an SM mostly empty, 24 at most (12000 tokens of 48: 67 -> 60 us).
+    // The groups of a token in parts of its rows, at least three where there are that many groups, so that most
+    // have to do with one kind alone.
+    const int64_t wanted = (int64_t)groups * 3 * sms, blocks = (a.tokens + (int64_t)groups - 1) / groups, wave = 4 * sms;
+    const bool uneven = blocks > wave && 10 * blocks < 7 * ((blocks + wave - 1) / wave * wave);
+    const int most = uneven ? std::min(rows, 24) : rows;
+    const int each = (int)std::max<int64_t>(1, std::min<int64_t>(most, ((int64_t)a.tokens * rows + wanted - 1) / wanted));
     int share = 1;
     while (share < groups && 2 * share * 3 * each <= rows)
         share *= 2;
