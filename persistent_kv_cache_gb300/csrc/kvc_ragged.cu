@@ -310,58 +310,79 @@ struct TurnRates {
     uint64_t per[kMaxPairs];
 };
 
-// cos and sin of x / 2^32 turns: the nearest quarter turn in whole numbers, the rest u,
-// at most an eighth of a turn, by the Taylor series of sin and cos of 2 pi u (terms
-// (2 pi)^k / k!; the first left out are below 2^-29).  With sincospif, which reduces
-// its argument again, the 131072 x 64 table took 34 us, now 14.7: 67 % of the copy rate,
-// with two thirds of the issue slots taken.
-__device__ __forceinline__ void turn(uint32_t x, float magnitude, float &c, float &s)
+// cos and sin of x / 2^32 turns, times `magnitude`, two at a time: the nearest quarter
+// turn in whole numbers, the rest u, at most an eighth of a turn, by the Taylor series of sin
+// and cos of 2 pi u (terms (2 pi)^k / k!; the first left out are below 2^-29).  With
+// sincospif, which reduces its argument again, the 131072 x 64 table took 34 us; one at a
+// time, each position's angle a product, in three waves of blocks 14.7; now 11.5, 87 % of
+// the copy rate.
+__device__ __forceinline__ void turns2(const uint32_t (&x)[2], float magnitude, float *c, float *s)
 {
-    const uint32_t q = (x + (1u << 29)) >> 30;
-    const float u = (float)(int32_t)(x - (q << 30)) * 0x1p-32f, z = u * u;
-    float sn = 42.0586939f, cs = -26.4262568f;
-    sn = fmaf(sn, z, -76.7058598f);
-    sn = fmaf(sn, z, 81.6052493f);
-    sn = fmaf(sn, z, -41.3417022f);
-    sn = fmaf(sn, z, 6.28318531f) * u;
-    cs = fmaf(cs, z, 60.2446414f);
-    cs = fmaf(cs, z, -85.4568172f);
-    cs = fmaf(cs, z, 64.939394f);
-    cs = fmaf(cs, z, -19.7392088f);
-    cs = fmaf(cs, z, 1.f);
-    // an odd number of quarter turns exchanges the two; one or two of them make the cosine negative, two or
-    // three the sine
-    const uint32_t flip_c = (q + 1u) << 30 & 0x80000000u, flip_s = q << 30 & 0x80000000u;
-    c = __uint_as_float(__float_as_uint(q & 1u ? sn : cs) ^ flip_c) * magnitude;
-    s = __uint_as_float(__float_as_uint(q & 1u ? cs : sn) ^ flip_s) * magnitude;
+    using kvc_tc::fma2;
+    using kvc_tc::mul2;
+    uint32_t q[2];
+    float v[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        q[e] = (x[e] + (1u << 29)) >> 30;
+        v[e] = (float)(int32_t)(x[e] - (q[e] << 30));
+    }
+    auto both = [](float k) { return make_float2(k, k); };
+    const float2 u = mul2(make_float2(v[0], v[1]), both(0x1p-32f)), z = mul2(u, u);
+    float2 sn = both(42.0586939f), cs = both(-26.4262568f);
+    sn = fma2(sn, z, both(-76.7058598f));
+    sn = fma2(sn, z, both(81.6052493f));
+    sn = fma2(sn, z, both(-41.3417022f));
+    sn = mul2(fma2(sn, z, both(6.28318531f)), u);
+    cs = fma2(cs, z, both(60.2446414f));
+    cs = fma2(cs, z, both(-85.4568172f));
+    cs = fma2(cs, z, both(64.939394f));
+    cs = fma2(cs, z, both(-19.7392088f));
+    cs = fma2(cs, z, both(1.f));
+    sn = mul2(sn, both(magnitude));
+    cs = mul2(cs, both(magnitude));
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        // an odd number of quarter turns exchanges the two; one or two of them make the cosine negative, two or
+        // three the sine
+        const float a = e ? sn.y : sn.x, b = e ? cs.y : cs.x;
+        const uint32_t flip_c = (q[e] + 1u) << 30 & 0x80000000u, flip_s = q[e] << 30 & 0x80000000u;
+        c[e] = __uint_as_float(__float_as_uint(q[e] & 1u ? a : b) ^ flip_c);
+        s[e] = __uint_as_float(__float_as_uint(q[e] & 1u ? b : a) ^ flip_s);
+    }
 }
 
-// VEC columns of kPositions positions a thread
-constexpr int kPositions = 4;
+// VEC columns a thread, of every `step`-th position: its angles go on by the same steps,
+// exactly.
+constexpr int kTableBlock = 4 * 256;  // pieces of a block, at least
 template <int VEC>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 6)
 rope_tables_kernel(float *__restrict__ cos_t, float *__restrict__ sin_t, int64_t first, int64_t positions, int half,
                    const __grid_constant__ TurnRates rates, float magnitude)
 {
-    const int pieces = half / VEC;
-    const int64_t w = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, step = (positions + kPositions - 1) / kPositions;
-    const int64_t p0 = w / pieces;
+    const uint32_t pieces = half / VEC, w = blockIdx.x * blockDim.x + threadIdx.x;
+    const uint32_t step = gridDim.x * blockDim.x / pieces, p0 = w / pieces;
     const int i0 = (int)(w - p0 * pieces) * VEC;
     if (p0 >= step)
         return;
-    uint64_t rate[VEC];
+    constexpr int N = VEC == 1 ? 2 : VEC;  // (a single column is computed twice)
+    uint64_t angle[N], by[N];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e)
-        rate[e] = rates.per[i0 + e];
+    for (int e = 0; e < N; ++e) {
+        const uint64_t rate = rates.per[i0 + (VEC == 1 ? 0 : e)];
+        angle[e] = (uint64_t)(first + p0) * rate + 0x80000000u;  // (rounded to 2^-32 of a turn)
+        by[e] = step * rate;
+    }
+#pragma unroll 1
+    for (int64_t p = p0; p < positions; p += step) {
+        float c[N], s[N];
 #pragma unroll
-    for (int k = 0; k < kPositions; ++k) {
-        const int64_t p = p0 + k * step;
-        if (p >= positions)
-            return;
-        float c[VEC], s[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-            turn((uint32_t)(((uint64_t)(first + p) * rate[e] + 0x80000000u) >> 32), magnitude, c[e], s[e]);
+        for (int e = 0; e < N; e += 2) {
+            const uint32_t x[2] = {(uint32_t)(angle[e] >> 32), (uint32_t)(angle[e + 1] >> 32)};
+            turns2(x, magnitude, c + e, s + e);
+            angle[e] += by[e];
+            angle[e + 1] += by[e + 1];
+        }
         const int64_t at = p * half + i0;
         if constexpr (VEC == 4) {
             *reinterpret_cast<float4 *>(cos_t + at) = make_float4(c[0], c[1], c[2], c[3]);
@@ -745,7 +766,9 @@ KVC_API kvc_status kvc_rope_tables(float *cos_table, float *sin_table, int64_t f
         rates.per[i] = (uint64_t)std::ldexp(rest, 63) * 2;
     }
     const int vec = half % 4 == 0 && kvc_host::aligned16(cos_table) && kvc_host::aligned16(sin_table) ? 4 : 1;
-    const int64_t blocks = ((positions + kPositions - 1) / kPositions * (half / vec) + 255) / 256;
+    // as many blocks as run at once, and four positions a thread before that (8192 x 64: one 4.0, two 3.1, four 3.0,
+    // eight 3.8 us; a thread's rates are as much work as a position)
+    const int64_t blocks = std::min<int64_t>((positions * (half / vec) + kTableBlock - 1) / kTableBlock, 6 * kvc_host::sm_count());
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     if (vec == 4)
         rope_tables_kernel<4><<<(unsigned)blocks, 256, 0, stream>>>(cos_table, sin_table, first, positions, half, rates,
