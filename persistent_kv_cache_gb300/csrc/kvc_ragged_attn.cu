@@ -418,22 +418,24 @@ __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch
 // from tensor memory at the end.
 // head_dim 256: no room for two outputs; one stream, the two score buffers in turn.
 //
-// What bounds it (one GB300, bf16; times of the whole call, with the join):
-//   chunks of 8 prompts, head_dim 128, group 4, 770 GFLOP: 608 us, 67 % of the measured
-//   bf16 peak.  A pair of tiles takes 3900 clocks where its products need 2048: a
+// What bounds it (one GB300, bf16; times of the whole call, with the join; means of 16
+// drawn batches and the products of the pairs that are seen; times of steps, here and below,
+// are of three such batches):
+//   chunks of 8 prompts, head_dim 128, group 4, 737 GFLOP: 675 us, 57 % of the measured
+//   bf16 peak (55 to 61).  A pair of tiles takes 3900 clocks where its products need 2048: a
 //   stream's chain (scores 512, their maximum 370, weights 1150, output products 512, the
 //   barriers between them) is longer than two streams hide.  Three streams, or scores a
 //   tile ahead, want more than the 512 columns of tensor memory.  Steps on the way: one
 //   thread a row, unrolled, with its scores in registers 869 us (the code missed the
 //   instruction cache; a spilled register in the loop costs the release of every
 //   arrival behind it hundreds of clocks); two threads a row and rolled loops 650.
-//   windowed chunks, head_dim 256, 825 GFLOP: 587 us, 74 %.  128 KB of K and V a tile for
+//   windowed chunks, head_dim 256, 718 GFLOP: 606 us, 62 %.  128 KB of K and V a tile for
 //   16.8 MFLOP: L2 delivers about 10 TB/s.
-//   decoding batch, 571 MB: 99 to 101 us, 84 % of the measured copy rate.
-//   decoding and prompts, head_dim 64, window 1000, pages of 16 (127 MB): 106 us; nine
+//   decoding batch, 544 MB: 97 us, 82 % of the measured copy rate.
+//   decoding and prompts, head_dim 64, window 1000, pages of 16 (116 MB): 104 us; nine
 //   tiles an item, three of them cut, and the exponentials of 128 rows for a decoding
 //   request's eight.
-//   17 tokens of one user over 700: 18.5 us, a chain of loads (lengths, table, rows, join).
+//   17 tokens of one user over 700: 18.5 us (20 with a cold L2), a chain of loads (lengths, table, rows, join).
 //
 // Only key tiles that hold the last tokens' own rows, or that a window's edge cuts,
 // are masked ("cut" tiles).  A NaN or an infinity in a column of V makes that column of
