@@ -27,7 +27,9 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kBM = 128, kBN = 128;
 constexpr float kRescale = 8.f;  // log2 units by which a score may exceed the reference maximum
-constexpr int kItemCost = 512;   // keys that stand for what an item costs beside its keys
+// Keys that stand for what an item costs beside its keys (256, 512, 768, 1024, 1536: chunks of 8 prompts 718, 673, 656,
+// 659, 676 us, windowed 614, 602, 601, 601, 609, decoding and prompts 111, 105, 105, 106, 106).
+constexpr int kItemCost = 768;
 constexpr int kMaxRequests = 65535;
 constexpr int kMaxKeys = INT_MAX - 511;  // of a request: rows are rounded up to tiles and items in 32 bits
 
@@ -421,18 +423,18 @@ __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch
 // What bounds it (one GB300, bf16; times of the whole call, with the join; means of 16
 // drawn batches and the products of the pairs that are seen; times of steps, here and below,
 // are of three such batches):
-//   chunks of 8 prompts, head_dim 128, group 4, 737 GFLOP: 675 us, 57 % of the measured
-//   bf16 peak (55 to 61).  A pair of tiles takes 3900 clocks where its products need 2048: a
+//   chunks of 8 prompts, head_dim 128, group 4, 737 GFLOP: 656 us, 59 % of the measured
+//   bf16 peak (57 to 61).  A pair of tiles takes 3900 clocks where its products need 2048: a
 //   stream's chain (scores 512, their maximum 370, weights 1150, output products 512, the
 //   barriers between them) is longer than two streams hide.  Three streams, or scores a
 //   tile ahead, want more than the 512 columns of tensor memory.  Steps on the way: one
 //   thread a row, unrolled, with its scores in registers 869 us (the code missed the
 //   instruction cache; a spilled register in the loop costs the release of every
 //   arrival behind it hundreds of clocks); two threads a row and rolled loops 650.
-//   windowed chunks, head_dim 256, 718 GFLOP: 606 us, 62 %.  128 KB of K and V a tile for
+//   windowed chunks, head_dim 256, 718 GFLOP: 601 us, 63 %.  128 KB of K and V a tile for
 //   16.8 MFLOP: L2 delivers about 10 TB/s.
-//   decoding batch, 544 MB: 97 us, 82 % of the measured copy rate.
-//   decoding and prompts, head_dim 64, window 1000, pages of 16 (116 MB): 104 us; nine
+//   decoding batch, 544 MB: 98 us, 82 % of the measured copy rate.
+//   decoding and prompts, head_dim 64, window 1000, pages of 16 (116 MB): 105 us; nine
 //   tiles an item, three of them cut, and the exponentials of 128 rows for a decoding
 //   request's eight.
 //   17 tokens of one user over 700: 18.5 us (20 with a cold L2), a chain of loads (lengths, table, rows, join).
