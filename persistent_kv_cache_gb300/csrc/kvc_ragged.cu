@@ -290,10 +290,10 @@ kvc_status check_pages(int batch, int max_pages, int page_size, int64_t n_pool_p
     return KVC_OK;
 }
 
+// (asked for at any size: a kernel has 48 KB without, what it holds beside the dynamic part included)
 template <typename Kernel> bool allow_smem(Kernel kern, size_t bytes)
 {
-    return bytes <= 48 * 1024 ||
-           cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
 }
 
 // --------------------------------------------------------------------------
