@@ -290,11 +290,14 @@ kvc_status check_pages(int batch, int max_pages, int page_size, int64_t n_pool_p
     return KVC_OK;
 }
 
-// (asked for at any size: a kernel has 48 KB without, what it holds beside the dynamic part included)
-template <typename Kernel> bool allow_smem(Kernel kern, size_t bytes)
+// Asked for at any size: a kernel has 48 KB without, what it holds beside the dynamic part included.  And what the
+// most requests take, whatever the call's: another thread's smaller call must not lower it before this one's launch.
+template <int BYTES, typename Kernel> bool allow_smem(Kernel kern)
 {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES) == cudaSuccess;
 }
+constexpr int words_of_release(int batch) { return batch; }
+constexpr int words_of_plan(int batch) { return 2 * batch + 1; }
 
 // --------------------------------------------------------------------------
 // rotation tables
@@ -667,8 +670,8 @@ KVC_API kvc_status kvc_page_release(const int32_t *released, const int32_t *bloc
         return KVC_ERR_SHAPE;
     const ReleaseArgs a{released, block_table, max_pages, page_size, free_pages, {free_count, n_pool_pages}, free_left,
                         batch, dev_status};
-    const size_t smem = rows;
-    if (!allow_smem(page_release_kernel, smem))
+    const size_t smem = words_of_release(batch) * sizeof(int32_t);
+    if (!allow_smem<words_of_release(kMaxRequests) * (int)sizeof(int32_t)>(page_release_kernel))
         return KVC_ERR_CUDA;
     const int warps = kPlanThreads / 32;
     const int grid = std::max(1, std::min((batch + warps - 1) / warps, kvc_host::sm_count()));
@@ -711,8 +714,8 @@ KVC_API kvc_status kvc_ragged_plan(const int32_t *cached, const int32_t *new_tok
             return KVC_ERR_SHAPE;
     const PlanArgs a{cached, new_tokens, block_table, max_pages, page_size, free_pages, {free_count, n_pool_pages},
                      free_left, batch, tokens, offsets, len, positions, slots, dev_status};
-    const size_t smem = (2 * (size_t)batch + 1) * sizeof(int32_t);
-    if (!allow_smem(ragged_plan_kernel, smem))
+    const size_t smem = words_of_plan(batch) * sizeof(int32_t);
+    if (!allow_smem<words_of_plan(kMaxRequests) * (int)sizeof(int32_t)>(ragged_plan_kernel))
         return KVC_ERR_CUDA;
     const int grid = std::max(1, (int)(((int64_t)tokens + kPlanTokens - 1) / kPlanTokens));
     if (kvc_host::launch_chained(ragged_plan_kernel, dim3(grid), kPlanThreads, smem, static_cast<cudaStream_t>(stream_), a) !=

@@ -53,3 +53,23 @@ def test_plan(batches):
 @pytest.mark.parametrize("batches", [(12272, 12273, 12288, 12289), (12288,)])
 def test_release(batches):
     run(RELEASE + f"\nfor B in {batches}: call(B)")
+
+
+@pytest.mark.parametrize("code", [PLAN, RELEASE], ids=["plan", "release"])
+def test_two_threads(code):
+    """Calls of the most requests beside smaller ones of another thread, each on a stream of its own."""
+    run(code + """
+import threading
+failed = []
+def calls(B, n):
+    try:
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(n):
+                call(B)
+    except Exception as e:
+        failed.append((B, e))
+threads = [threading.Thread(target=calls, args=a) for a in ((16384, 100), (13000, 300), (50, 300))]
+for t in threads: t.start()
+for t in threads: t.join()
+assert not failed, failed
+""")
