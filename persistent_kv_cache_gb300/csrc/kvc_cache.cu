@@ -729,7 +729,7 @@ kvc_status append_typed(void *k_cache, void *v_cache, const void *new_k, const v
             auto kern = compact_cluster_kernel<T>;
             if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      kCompactSmem) != cudaSuccess)
-                return KVC_ERR_CUDA;
+                return kvc_host::cuda_failed();
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(cl, slices, 2);
             cfg.blockDim = dim3(32);
@@ -744,7 +744,7 @@ kvc_status append_typed(void *k_cache, void *v_cache, const void *new_k, const v
             cfg.numAttrs = 1;
             if (cudaLaunchKernelEx(&cfg, kern, kc, vc, nk, nv, len, kv_heads, D, C, cos_t, sin_t,
                                    rope_max_pos, status) != cudaSuccess)
-                return KVC_ERR_CUDA;
+                return kvc_host::cuda_failed();
         }
     } else if (hazard_w > 0 && phase == KVC_APPEND) {
         // kvc_window_prefill_step: staged rows seed the stage; the others
@@ -755,7 +755,7 @@ kvc_status append_typed(void *k_cache, void *v_cache, const void *new_k, const v
                     C, 0, kvc::kStageSeedRows, hazard_w);
         if (cudaFuncSetAttribute(shift_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kShiftSmem) != cudaSuccess)
-            return KVC_ERR_CUDA;
+            return kvc_host::cuda_failed();
         shift_rows_kernel<<<dim3(slices, 2), 32, kShiftSmem, stream>>>(
             reinterpret_cast<char *>(kc), reinterpret_cast<char *>(vc), len, kv_heads,
             (int64_t)D * sizeof(T), C, S, cos_t ? rope_max_pos : -1, status, hazard_w, 0);
@@ -766,7 +766,7 @@ kvc_status append_typed(void *k_cache, void *v_cache, const void *new_k, const v
         // move down in the cache, then their new rows follow from the stage
         if (cudaFuncSetAttribute(shift_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kShiftSmem) != cudaSuccess)
-            return KVC_ERR_CUDA;
+            return kvc_host::cuda_failed();
         shift_rows_kernel<<<dim3(slices, 2), 32, kShiftSmem, stream>>>(
             reinterpret_cast<char *>(kc), reinterpret_cast<char *>(vc), len, kv_heads,
             (int64_t)D * sizeof(T), C, S, cos_t ? rope_max_pos : -1, status, hazard_w, 1);
@@ -968,7 +968,7 @@ KVC_API kvc_status kvc_window_append_inplace(void *k_rows, void *v_rows, const v
     }
     if (cudaFuncSetAttribute(shift_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kShiftSmem) != cudaSuccess)
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     shift_rows_kernel<<<dim3(slices, 2), 32, kShiftSmem, stream>>>(
         static_cast<char *>(k_rows), static_cast<char *>(v_rows), len, kv_heads,
         (int64_t)head_dim * eb, rows_per_head, new_tokens, rope_cos ? rope_max_pos : -1,

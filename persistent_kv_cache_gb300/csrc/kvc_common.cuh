@@ -373,6 +373,13 @@ inline kvc_status launch_status()
 {
     return cudaGetLastError() == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }
+// What a call returns when CUDA refuses something to it.  The runtime keeps such an error until it is read: left
+// there, the next call's launch_status() would find it behind a launch that succeeded.
+inline kvc_status cuda_failed()
+{
+    (void)cudaGetLastError();
+    return KVC_ERR_CUDA;
+}
 
 // A launch that may start while the kernel before it in the stream ends (or, once all
 // of that one's blocks have said so, runs): the kernel has grid_dep_wait() before the

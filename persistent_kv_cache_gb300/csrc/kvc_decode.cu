@@ -1890,7 +1890,7 @@ kvc_status launch_decode16(void *out, const void *q, const void *k_cache, const 
         return KVC_ERR_SHAPE;
     if (!kvc_host::encode_2d_bf16_sw128(&tk, k_cache, rows, D, kTile, tt) ||
         !kvc_host::encode_2d_bf16_sw128(&tv, v_cache, rows, D, kTile, tt))
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     DecodeArgs a{};
     a.out = out;
     a.q = q;
@@ -1951,7 +1951,7 @@ kvc_status launch_decode16(void *out, const void *q, const void *k_cache, const 
                             : decode_split_kernel<T, D, kPlain, 1>);
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
         cudaSuccess)
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     const dim3 grid(a.max_splits, kv_heads, batch);
     kern<<<grid, threads, smem, stream>>>(tk, tv, a);
     if (a.max_splits > 1) {
@@ -2334,11 +2334,11 @@ kvc_status launch_window_step(const WindowStepArgs &a, int batch, cudaStream_t s
     CUtensorMap tk, tv;
     if (!kvc_host::encode_2d_bf16_sw128(&tk, a.k_cache, rows, D, kTile, tt) ||
         !kvc_host::encode_2d_bf16_sw128(&tv, a.v_cache, rows, D, kTile, tt))
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     auto kern = a.group > 8 ? window_step_kernel<T, D, 2> : window_step_kernel<T, D, 1>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
         cudaSuccess)
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(batch * a.kv_heads));
     cfg.blockDim = dim3(128);
@@ -2350,7 +2350,7 @@ kvc_status launch_window_step(const WindowStepArgs &a, int batch, cudaStream_t s
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kern, tk, tv, a) != cudaSuccess)
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     return kvc_host::launch_status();
 }
 
@@ -2504,12 +2504,12 @@ kvc_status scratch_address(void **addr)
 {
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 256)
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     std::lock_guard<std::mutex> lock(g_scratch_mutex);
     if (g_scratch_addr[dev] == nullptr) {
         void *p = nullptr;
         if (cudaGetSymbolAddress(&p, g_decode_scratch) != cudaSuccess || p == nullptr)
-            return KVC_ERR_CUDA;
+            return kvc_host::cuda_failed();
         g_scratch_addr[dev] = p;
     }
     *addr = g_scratch_addr[dev];

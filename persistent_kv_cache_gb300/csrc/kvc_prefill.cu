@@ -1021,7 +1021,7 @@ kvc_status launch_prefill_tc(void *out, const void *q, const void *k_rows, const
         !kvc_host::encode_4d_blocks_sw128(&tq, q, (uint64_t)batch * q_heads, (uint64_t)S, D,
                                           sizeof(T), (uint32_t)(kBM / (q_heads / kv_heads)),
                                           (uint32_t)(q_heads / kv_heads), tt))
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     PrefillArgs a;
     a.out = out;
     a.q = q;
@@ -1061,7 +1061,7 @@ kvc_status launch_prefill_tc(void *out, const void *q, const void *k_rows, const
     auto kern = prefill_tc_kernel<T, D>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
         cudaSuccess)
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     // the output tile store: [batch * q_heads, S, D] 16-bit, or the fp32
     // partials [nsplit * batch * q_heads, S, D]; a box is one query block of
     // every head of a group
@@ -1071,7 +1071,7 @@ kvc_status launch_prefill_tc(void *out, const void *q, const void *k_rows, const
             (uint64_t)(part ? a.nsplit : 1) * batch * q_heads, (uint64_t)S, D, part ? 4 : 2,
             (uint32_t)a.qb_rows, (uint32_t)a.group,
             part ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : tt))
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     const int qblocks = (S + a.qb_rows - 1) / a.qb_rows;
     dim3 grid(qblocks * a.nsplit, kv_heads, batch);
     kern<<<grid, kThreads, smem, stream>>>(tq, tk, tv, tk2, tv2, to, a);

@@ -1191,7 +1191,7 @@ template <typename T, int FMT, int D, int HB> kvc_status launch_decode(const Qua
     auto kern = quant_decode_kernel<T, FMT, D, HB>;
     if (smem > 32 * 1024 &&
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     kern<<<a.grid, 32 * kWarps, smem, stream>>>(a);
     // a row of one unit is never split
     if (a.C > a.unit) {
@@ -1205,7 +1205,7 @@ template <typename T, int FMT, int D, int HB> kvc_status launch_decode(const Qua
         cfg.attrs = at;
         cfg.numAttrs = 1;
         if (cudaLaunchKernelEx(&cfg, quant_merge_kernel<T, D>, a) != cudaSuccess)
-            return KVC_ERR_CUDA;
+            return kvc_host::cuda_failed();
     }
     return kvc_host::launch_status();
 }

@@ -672,12 +672,12 @@ KVC_API kvc_status kvc_page_release(const int32_t *released, const int32_t *bloc
                         batch, dev_status};
     const size_t smem = words_of_release(batch) * sizeof(int32_t);
     if (!allow_smem<words_of_release(kMaxRequests) * (int)sizeof(int32_t)>(page_release_kernel))
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     const int warps = kPlanThreads / 32;
     const int grid = std::max(1, std::min((batch + warps - 1) / warps, kvc_host::sm_count()));
     if (kvc_host::launch_chained(page_release_kernel, dim3(grid), kPlanThreads, smem, static_cast<cudaStream_t>(stream_), a) !=
         cudaSuccess)
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     return kvc_host::launch_status();
 }
 
@@ -716,11 +716,11 @@ KVC_API kvc_status kvc_ragged_plan(const int32_t *cached, const int32_t *new_tok
                      free_left, batch, tokens, offsets, len, positions, slots, dev_status};
     const size_t smem = words_of_plan(batch) * sizeof(int32_t);
     if (!allow_smem<words_of_plan(kMaxRequests) * (int)sizeof(int32_t)>(ragged_plan_kernel))
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     const int grid = std::max(1, (int)(((int64_t)tokens + kPlanTokens - 1) / kPlanTokens));
     if (kvc_host::launch_chained(ragged_plan_kernel, dim3(grid), kPlanThreads, smem, static_cast<cudaStream_t>(stream_), a) !=
         cudaSuccess)
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     return kvc_host::launch_status();
 }
 
@@ -853,6 +853,6 @@ KVC_API kvc_status kvc_ragged_append(void *q_out, void *k_pool, void *v_pool, co
                        rope_cos ? rotary_dim : 0, interleaved, rope_cos, rope_sin, rope_max_pos, 1, dev_status};
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     if ((dtype == KVC_BF16 ? launch_append<__nv_bfloat16>(a, stream) : launch_append<__half>(a, stream)) != cudaSuccess)
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     return kvc_host::launch_status();
 }

@@ -1459,25 +1459,25 @@ kvc_status launch_attn(RaggedArgs &a, const void *q, const void *k, const void *
     if (!encode_queries(&tq, q, a, D, tt) ||
         !kvc_host::encode_3d_sw128(&tk, k, rows, D, a.box_rows, k_blocks, tt) ||
         !kvc_host::encode_3d_sw128(&tv, v, rows, D, v_rows, v_blocks, tt))
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     auto kern = ragged_attn_kernel<T, D>;
     int dev = 0, optin = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess)
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     const size_t smem = std::min<size_t>((size_t)SM::TOTAL + 1024, (size_t)optin);
     if (smem < (size_t)SM::TOTAL)
         return KVC_ERR_UNSUPPORTED;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     if (kvc_host::launch_chained(kern, dim3(grid), SM::THREADS, smem, stream, tq, tk, tv, a) != cudaSuccess)
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     if (grid * a.rounds > 1) {
         // blocks for the rows that an item has if requests are alike (they go round for more)
         const int64_t rows_each = (int64_t)((a.tokens + a.batch - 1) / a.batch) * a.group;
         const int64_t blocks = std::min<int64_t>((rows_each + kMergeRows - 1) / kMergeRows, SM::TILES * kBM / kMergeRows);
         if (kvc_host::launch_chained(ragged_merge_kernel<T, D>, dim3(grid * a.rounds - 1, (unsigned)blocks), 256, 0, stream, a) != cudaSuccess)
-            return KVC_ERR_CUDA;
+            return kvc_host::cuda_failed();
     }
     return kvc_host::launch_status();
 }

@@ -1130,11 +1130,11 @@ kvc_status launch_decode(const SparseArgs &a, const void *k_pool, const void *v_
     CUtensorMap tk, tv;
     if (!kvc_host::encode_3d_sw128(&tk, k_pool, rows, D, kUnit, D / 64, type) ||
         !kvc_host::encode_3d_sw128(&tv, v_pool, rows, D, kUnit, D / 64, type))
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     auto kern = sparse_decode_kernel<T, D, HB>;
     const int smem = SM::TOTAL + 1024;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(a.grid);
     cfg.blockDim = dim3(kDecodeThreads);
@@ -1146,7 +1146,7 @@ kvc_status launch_decode(const SparseArgs &a, const void *k_pool, const void *v_
     cfg.attrs = at;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kern, tk, tv, a) != cudaSuccess)
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     return kvc_host::launch_status();
 }
 
@@ -1179,7 +1179,7 @@ template <typename T, int D> kvc_status launch_select_dim(const SelectArgs &a, c
     const int run = (a.max_pages + ctas - 1) / ctas, smem = (a.max_pages + run) * 4;
     if (smem > 32 * 1024 && cudaFuncSetAttribute(page_select_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  smem) != cudaSuccess)
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(a.kv_heads * ctas, a.batch);
     cfg.blockDim = dim3(kSelThreads);
@@ -1193,7 +1193,7 @@ template <typename T, int D> kvc_status launch_select_dim(const SelectArgs &a, c
     cfg.attrs = at;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, page_select_kernel<T, D>, a, run) != cudaSuccess)
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     return kvc_host::launch_status();
 }
 

@@ -1238,27 +1238,27 @@ kvc_status launch_attn_dim(TreeArgs &a, const void *k, const void *v, cudaStream
                                    tt) ||
         !kvc_host::encode_3d_sw128(&tk, k, rows, D, a.box_rows, blocks, tt) ||
         !kvc_host::encode_3d_sw128(&tv, v, rows, D, a.box_rows, blocks, tt))
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     int dev = 0, optin = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess)
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     const size_t smem = std::min<size_t>((size_t)SM::TOTAL + 1024, (size_t)optin);
     if (smem < (size_t)SM::TOTAL)
         return KVC_ERR_UNSUPPORTED;
     auto kern = tree_attn_kernel<T, D, KR>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     const unsigned q_blocks = a.cos_t ? (unsigned)((q_rows * (D / 16) + 255) / 256) : 0u;
     const int64_t words = (int64_t)a.batch * a.nodes * ((a.nodes + 31) / 32);
     tree_prep_kernel<T><<<q_blocks + (unsigned)((words + 255) / 256), 256, 0, stream>>>(a, D, q_blocks);
     if (launch_after(kern, dim3(a.grid), kAttnThreads, smem, stream, tq, tk, tv, a) != cudaSuccess)
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     if (a.grid > 1 && launch_after(tree_merge_kernel<T, D>,
                                    dim3(a.grid - 1, (std::min(kBM, a.group * a.nodes) + kMergeRows - 1) / kMergeRows), 256, 0,
                                    stream,
                                    a) != cudaSuccess)
-        return KVC_ERR_CUDA;
+        return kvc_host::cuda_failed();
     return kvc_host::launch_status();
 }
 

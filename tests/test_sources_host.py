@@ -1,0 +1,25 @@
+"""What the library's sources keep to, where no call can show it: failures that cannot be made to order."""
+import glob
+import os
+import re
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def sources():
+    out = {}
+    for path in sorted(glob.glob(os.path.join(ROOT, "persistent_kv_cache_gb300", "csrc", "*.cu*"))):
+        with open(path) as f:
+            out[os.path.basename(path)] = re.sub(r"//[^\n]*", "", f.read())
+    assert len(out) >= 12
+    return out
+
+
+def test_errors_of_cuda_are_read_where_they_are_returned():
+    """A call that fails leaves no error behind for the next one to find."""
+    for name, text in sources().items():
+        if name == "kvc_common.cuh":
+            # launch_status and cuda_failed read it
+            assert len(re.findall(r"KVC_ERR_CUDA", text)) == text.count("cudaGetLastError()") == 2
+        else:
+            assert not re.findall(r"return\s+KVC_ERR_CUDA", text) and not re.findall(r"[?:]\s*KVC_ERR_CUDA\b\s*[;)]", text), name
