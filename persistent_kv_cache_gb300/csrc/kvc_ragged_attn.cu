@@ -750,7 +750,8 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                         place = -1;
                         if (w < nt * per_tile && r < end) {
                             const uint32_t page = r / (uint32_t)a.page_size;
-                            const int32_t id = __ldg(a.table + (int64_t)cur.b * a.max_pages + page);
+                            // (an ordinary load: this kernel's life may begin while a plan still writes the table)
+                            const int32_t id = a.table[(int64_t)cur.b * a.max_pages + page];
                             if (id >= 0 && id < a.n_pool)
                                 place = (id * a.kv_heads + cur.h) * a.page_size + (int32_t)(r - page * a.page_size);
                             else

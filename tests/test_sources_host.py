@@ -23,3 +23,12 @@ def test_errors_of_cuda_are_read_where_they_are_returned():
             assert len(re.findall(r"KVC_ERR_CUDA", text)) == text.count("cudaGetLastError()") == 2
         else:
             assert not re.findall(r"return\s+KVC_ERR_CUDA", text) and not re.findall(r"[?:]\s*KVC_ERR_CUDA\b\s*[;)]", text), name
+
+
+def test_ragged_kernels_load_by_ordinary_loads():
+    """The kernels of a ragged step may start before the kernel in front of them has ended: what that one may write (a
+    plan the table, an append the queries) was not read-only for their whole life, as the non-coherent path wants it."""
+    text = sources()
+    for name in ("kvc_ragged.cu", "kvc_ragged_attn.cu"):
+        assert "launch_chained" in text[name]
+        assert not re.findall(r"__ldg|__ldnc|ld\.global(\.\w+)*\.nc|__restrict__ (?!cos_t|sin_t)", text[name]), name
