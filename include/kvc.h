@@ -986,11 +986,13 @@ kvc_status kvc_ragged_plan(const int32_t *cached, const int32_t *new_tokens, int
  *                    positions keeps its speed, one that goes round `low` times or
  *                    less has speed / factor, and between them g = (trained * speed /
  *                    2 pi - low) / (high - low): g * speed + (1 - g) * speed / factor
- * Speeds are float64, angles are reduced in whole numbers, so that far positions
- * are as exact as near ones: off by a float32 rounding or two at any position.
+ * Speeds are float64; the angle that a speed has at a position is reduced in whole
+ * numbers, to 2^-32 of a turn at any position, so that far positions are as exact as
+ * near ones: off by a float32 rounding or two, beside the few 2^-53 of itself that the
+ * speed, and with it the angle, is off (up to positions of 2^27 that is less).
  * cos_table, sin_table  device float32 [positions, rotary_dim / 2] (4-byte aligned; the
  *             calls that read them want 16).
- * positions   up to 2^31 - 1; first >= 0 (KVC_ERR_SHAPE).
+ * positions   up to 2^31 - 1; first >= 0, first + positions up to 2^31 (KVC_ERR_SHAPE).
  * rotary_dim  even, 2..256 (KVC_ERR_UNSUPPORTED above).  base > 0; factor > 0
  *             (ignored by KVC_ROPE_PLAIN); KVC_ROPE_PARTS: trained >= 1, low < high;
  *             all finite, magnitude also as a float32 (KVC_ERR_SHAPE).

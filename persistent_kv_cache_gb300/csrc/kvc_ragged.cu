@@ -306,12 +306,32 @@ constexpr int words_of_plan(int batch) { return 2 * batch + 1; }
 constexpr int kMaxPairs = 128;
 
 // What a position adds to each pair's angle, in units of 2^-64 of a turn: the
-// angle of position p is p times that modulo 2^64, exact for any p, so that far
-// positions lose nothing (in float32 an angle of 10^5 is known to 2^-7 only,
-// and float64 arithmetic is slow on this machine).
+// angle of position p is p times that modulo 2^64.  The rate is within one unit of
+// the speed's, so that the last position, 2^31, is off by 2^-33 of a turn (in
+// float32 an angle of 10^5 is known to 2^-7 only, and float64 arithmetic is slow on
+// this machine).
 struct TurnRates {
     uint64_t per[kMaxPairs];
 };
+constexpr int64_t kMaxPositions = (int64_t)1 << 31;
+
+// x in [0, 1] in units of 2^-64, modulo 2^64
+uint64_t units_of(double x)
+{
+    const double high = std::ldexp(x, 32), whole = std::floor(high);
+    return ((uint64_t)whole << 32) + (uint64_t)std::nearbyint(std::ldexp(high - whole, 32));
+}
+
+// Turns a position of `speed` radians a position, the whole ones left out.  1 / 2 pi and
+// the product are sums of two float64: with one, an error of 2^-53 of the turns would
+// grow with the position (a speed of 8: 17 * 2^-24 radians at 2^31).
+uint64_t turns_of(double speed)
+{
+    constexpr double kInverse = 0x1.45f306dc9c883p-3, kRest = -0x1.6b01ec5417056p-57;  // of 1 / 2 pi
+    const double turns = speed * kInverse, error = std::fma(speed, kInverse, -turns) + speed * kRest;
+    const uint64_t more = units_of(std::fabs(error) - std::floor(std::fabs(error)));
+    return units_of(turns - std::floor(turns)) + (error < 0.0 ? 0 - more : more);
+}
 
 // cos and sin of x / 2^32 turns, times `magnitude`, two at a time: the nearest quarter
 // turn in whole numbers, the rest u, at most an eighth of a turn, by the Taylor series of sin
@@ -728,7 +748,7 @@ KVC_API kvc_status kvc_rope_tables(float *cos_table, float *sin_table, int64_t f
                                    int rotary_dim, double base, int scaling, double factor, int64_t trained, double low,
                                    double high, double magnitude, void *stream_)
 {
-    if (positions < 0 || positions > INT32_MAX || first < 0 || first > INT64_MAX - positions || rotary_dim < 2 || rotary_dim % 2)
+    if (positions < 0 || positions > INT32_MAX || first < 0 || first > kMaxPositions - positions || rotary_dim < 2 || rotary_dim % 2)
         return KVC_ERR_SHAPE;
     if (rotary_dim > 2 * kMaxPairs || scaling < KVC_ROPE_PLAIN || scaling > KVC_ROPE_PARTS)
         return KVC_ERR_UNSUPPORTED;
@@ -764,9 +784,7 @@ KVC_API kvc_status kvc_rope_tables(float *cos_table, float *sin_table, int64_t f
         }
         if (!std::isfinite(speed))
             return KVC_ERR_SHAPE;
-        // whole turns a position change nothing
-        const double turns = speed / kTurn, rest = turns - std::floor(turns);
-        rates.per[i] = (uint64_t)std::ldexp(rest, 63) * 2;
+        rates.per[i] = turns_of(speed);
     }
     const int vec = half % 4 == 0 && kvc_host::aligned16(cos_table) && kvc_host::aligned16(sin_table) ? 4 : 1;
     // as many blocks as run at once, and four positions a thread before that (8192 x 64: one 4.0, two 3.1, four 3.0,
