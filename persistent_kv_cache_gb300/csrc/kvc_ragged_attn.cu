@@ -647,6 +647,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 {
     using SM = Smem<D>;
     using kvc_tc::wait_or_abort;
+    using kvc_tc::warp_wait_or_abort;
     constexpr int NSLAB = SM::NSLAB, SPT = SM::SPT, KR = SM::KR, TILES = SM::TILES, kSoftmax = SM::SOFTMAX, THREADS = SM::THREADS;
     constexpr uint32_t AB = std::is_same<T, __half>::value ? 0u : 1u;
     constexpr uint32_t IDESC_S = kvc_tc::f16_idesc(AB, 0, kBM, kBN);
@@ -761,8 +762,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     for (int u = 0; u < SPT; ++u) {
                         const int q = q0 + SPT * (mine_v ? v_group(j, nt) : k_group(j)) + u, slot = q % NSLAB;
                         if (q >= NSLAB)
-                            ok = wait_or_abort(&empty[slot], ((q / NSLAB) - 1) & 1, abort_flag, a.status);
-                        ok = __all_sync(0xffffffffu, ok);
+                            ok = warp_wait_or_abort(true, &empty[slot], ((q / NSLAB) - 1) & 1, abort_flag, a.status);
                         if (!ok)
                             break;
                         uint8_t *to = smem + SM::RING_OFF + slot * SM::SLAB;
@@ -947,7 +947,9 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     } else {
         // ======================= softmax =======================
         // A warp whose wait gave up goes on through the tiles without work or waits: the barriers
-        // below have no limit, and every warp comes to each of them.
+        // below have no limit, and every warp comes to each of them.  Tensor memory is loaded and stored by
+        // whole warps: `ok` is a lane's between its waits, but one for the warp wherever it is asked whether there
+        // is work.  (A vote a tile and one for the output: nothing to 1.8 % of the call's time.)
         constexpr int CT = kBN / 2, OT = D / 2;  // columns of S and of O of a thread
         const int tid = threadIdx.x - 128, quad = warp & 3, half = ((warp - 4) >> 2) & 1, stream = (warp - 4) >> 3;
         const int m = quad * 32 + lane;  // row of the tile
@@ -1116,7 +1118,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 const int s = TILES == 2 ? stream : (int)(used & 1);
                 const uint32_t parity = TILES == 2 ? used & 1 : (used >> 1) & 1;
                 const uint32_t s_col = lane_addr + SM::COL_S + s * kBN;
-                ok = ok && wait_or_abort(&s_full[s], parity, abort_flag, a.status);
+                ok = warp_wait_or_abort(ok, &s_full[s], parity, abort_flag, a.status);
                 ++used;
                 kvc_tc::fence_after();
                 // the weights of either half go where its own scores were, so that neither waits for the other
@@ -1168,7 +1170,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
                     if (SM::OWN_P && used > 1) {
                         // the products of the tile before have read its weights
-                        ok = wait_or_abort(&o_done[s], (used - 2) & 1, abort_flag, a.status);
+                        ok = ok && wait_or_abort(&o_done[s], (used - 2) & 1, abort_flag, a.status);
                         kvc_tc::fence_after();
                     }
                     const float sum = plain ? row_weights<T, CT, false>(from, to, lo, hi, flip, c_log2, neg_m, half_there)
@@ -1196,6 +1198,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 ok = ok && (TILES == 2 ? wait_or_abort(&o_done[stream], last & 1, abort_flag, a.status)
                                        : wait_or_abort(&o_done[last & 1], (last >> 1) & 1, abort_flag, a.status));
             }
+            ok = __all_sync(0xffffffffu, ok);
             kvc_tc::fence_after();
             const Segment seg = kept->seg[s_no & 1];
             const int first = seg.i * a.item + (st.two ? stream * a.toks : 0), tok = m / a.group;

@@ -257,4 +257,12 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, vo
     }
 }
 
+// The same for a warp: one answer for all lanes, that all of them were `ok` before and none gave up.  (Lanes
+// look at the flag and the time one by one; what needs the whole warp after a wait must not find part of it.)
+__device__ __forceinline__ bool warp_wait_or_abort(bool ok, uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                                   int32_t *status)
+{
+    return __all_sync(0xffffffffu, ok && wait_or_abort(bar, parity, abort_flag, status));
+}
+
 } // namespace kvc_tc

@@ -32,3 +32,18 @@ def test_ragged_kernels_load_by_ordinary_loads():
     for name in ("kvc_ragged.cu", "kvc_ragged_attn.cu"):
         assert "launch_chained" in text[name]
         assert not re.findall(r"__ldg|__ldnc|ld\.global(\.\w+)*\.nc|__restrict__ (?!cos_t|sin_t)", text[name]), name
+
+
+def test_waits_of_whole_warps_have_one_answer():
+    """A warp that loads and stores tensor memory, votes and shuffles as a whole decides as a whole whether it does: in
+    the softmax warps of the ragged attention a vote comes between the last wait and every such question."""
+    text = sources()["kvc_ragged_attn.cu"]
+    kernel = text[text.index("ragged_attn_kernel(const"):text.index("ragged_merge_kernel(const")]
+    softmax = kernel[kernel.index("quad = warp & 3"):]
+    assert "tcgen05" not in softmax and "mbar_wait" not in softmax
+    asked = [m.start() for m in re.finditer(r"\bactive && ok\b", softmax)]
+    assert len(asked) == 3 and not re.findall(r"\bok && active\b|if \(ok\)", softmax)
+    given = [(m.start(), m.group(1)) for m in re.finditer(r"\bok = ([^;]*);", softmax)]
+    for at in asked:
+        last = [what for begin, what in given if begin < at][-1]
+        assert "warp_wait_or_abort(ok, " in last or "__all_sync(0xffffffffu, ok)" in last, last
