@@ -660,6 +660,8 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         uint32_t dyn;
         asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(dyn));
         if ((uint32_t)(smem - smem_raw) + SM::TOTAL > dyn) {
+            // (the call before may still join by what is written here, and what comes after counts on its end)
+            kvc::grid_dep_wait();
             if (threadIdx.x == 0) {
                 kvc::raise_status(a.status, KVC_DEV_CAPACITY);
                 for (int p = 0; p < a.rounds; ++p)

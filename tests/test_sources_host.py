@@ -47,3 +47,16 @@ def test_waits_of_whole_warps_have_one_answer():
     for at in asked:
         last = [what for begin, what in given if begin < at][-1]
         assert "warp_wait_or_abort(ok, " in last or "__all_sync(0xffffffffu, ok)" in last, last
+
+
+def test_chained_kernels_wait_before_they_write_or_end():
+    """A kernel that may start before the one in front has ended waits for that in every block, also in one that has
+    nothing to do: the kernel behind counts on all before it having ended too."""
+    text = sources()
+    kernels = {"kvc_ragged.cu": ("page_release_kernel", "ragged_plan_kernel", "ragged_append_kernel"),
+               "kvc_ragged_attn.cu": ("ragged_attn_kernel", "ragged_merge_kernel")}
+    for name, ones in kernels.items():
+        for kernel in ones:
+            body = re.search(kernel + r"\(const .*?\n\}\n", text[name], re.S).group(0)
+            before = body[:body.index("grid_dep_wait()")]
+            assert "return" not in before and "raise_status" not in before and not re.findall(r"\ba\.\w+\[[^\]]*\] = ", before), kernel
