@@ -588,7 +588,9 @@ ragged_append_kernel(const AppendArgs a, int share)
             for (int e = 0; e < 4; ++e) {
                 const uint32_t o = a.interleaved ? __byte_perm(w[e], 0, 0x1032) : __shfl_sync(peers, w[e], other, LPR);
                 cs[e] = kvc_tc::mul2(cs[e], unpack2<T>(w[e]));
-                sn[e] = kvc_tc::mul2(sn[e], unpack2<T>(o));
+                // (a column that is not turned keeps its zero: that times an infinite weight is none)
+                if (turns)
+                    sn[e] = kvc_tc::mul2(sn[e], unpack2<T>(o));
             }
         }
     };
