@@ -3,6 +3,7 @@
 
 #include <initializer_list>
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -422,8 +423,12 @@ kvc_status hazard_rows(void *k_cache, void *v_cache, const void *new_k, const vo
                        const float *cos_t, const float *sin_t, int64_t rope_max_pos,
                        int32_t *status, cudaStream_t stream);
 
-// cuTensorMapEncodeTiled through the runtime's driver entry point
-// (no link-time dependency on libcuda)
+// cuTensorMapEncodeTiled through the runtime's driver entry point (no link-time
+// dependency on libcuda), for a thread that has a context from then on; null where
+// there is none to be had
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
+// a [rows, cols] 16-bit matrix in boxes of (64 columns, box_rows)
 bool encode_2d_bf16_sw128(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,
                           uint32_t box_rows, CUtensorMapDataType type);
 

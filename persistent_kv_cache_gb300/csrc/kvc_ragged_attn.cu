@@ -17,8 +17,6 @@
 #include <cmath>
 #include <type_traits>
 
-#include <cudaTypedefs.h>
-
 #include "kvc_common.cuh"
 #include "kvc_tc.cuh"
 
@@ -1433,14 +1431,7 @@ ragged_merge_kernel(const RaggedArgs a)
 // blocks): a box of (64, group, toks, 1) is a column block of a query tile.
 bool encode_queries(CUtensorMap *map, const void *q, const RaggedArgs &a, int D, CUtensorMapDataType type)
 {
-    static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-            found != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }();
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = kvc_host::tensor_map_encoder();
     if (!encode)
         return false;
     const cuuint64_t dims[4] = {64, (cuuint64_t)a.q_heads, (cuuint64_t)a.tokens, (cuuint64_t)D / 64};

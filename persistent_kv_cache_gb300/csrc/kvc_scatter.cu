@@ -8,7 +8,6 @@
 // that the two latencies overlap.  The functional form writes every vector of
 // present once in a single bandwidth-bound pass, each from the update or from
 // past; with no update rows it is a plain vector copy.
-#include <cudaTypedefs.h>
 
 #include <atomic>
 #include <mutex>
@@ -196,25 +195,40 @@ int sm_count()
     return n;
 }
 
-static PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
+// The driver's entry points through the runtime, and a context for the calling thread: a
+// thread has none before its first runtime call that needs the device, and
+// the driver encodes nothing without (cudaSetDevice makes the device's own current; a
+// context that is there stays).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
 {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    static PFN_cuCtxGetCurrent_v4000 current = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                             cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+        auto entry = [](const char *name, unsigned version) -> void * {
+            void *p = nullptr;
+            cudaDriverEntryPointQueryResult q;
+            return cudaGetDriverEntryPointByVersion(name, &p, version, cudaEnableDefault, &q) == cudaSuccess &&
+                           q == cudaDriverEntryPointSuccess
+                       ? p
+                       : nullptr;
+        };
+        current = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(entry("cuCtxGetCurrent", 4000));
+        encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(entry("cuTensorMapEncodeTiled", 12000));
     });
-    return fn;
+    CUcontext context = nullptr;
+    if (!current || !encode || current(&context) != CUDA_SUCCESS)
+        return nullptr;
+    int dev = 0;
+    if (!context && (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess))
+        return nullptr;
+    return encode;
 }
 
 bool encode_3d_sw128(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,
                      uint32_t box_rows, uint32_t box_blocks, CUtensorMapDataType type)
 {
-    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
     if (!fn || cols % 64 != 0)
         return false;
     cuuint64_t dims[3] = {64, rows, cols / 64};
@@ -230,7 +244,7 @@ bool encode_3d_sw128(CUtensorMap *map, const void *base, uint64_t rows, uint64_t
 bool encode_2d_bf16_sw128(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,
                           uint32_t box_rows, CUtensorMapDataType type)
 {
-    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
     if (!fn)
         return false;
     cuuint64_t dims[2] = {cols, rows};
@@ -247,7 +261,7 @@ bool encode_4d_heads_sw128(CUtensorMap *map, const void *base, uint64_t heads, u
                            uint64_t cols, uint32_t elem_bytes, uint32_t box_rows,
                            uint32_t box_heads, CUtensorMapDataType type)
 {
-    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
     if (!fn || elem_bytes == 0 || 128 % elem_bytes != 0)
         return false;
     const uint64_t span = 128 / elem_bytes;
@@ -267,7 +281,7 @@ bool encode_4d_blocks_sw128(CUtensorMap *map, const void *base, uint64_t heads, 
                             uint64_t cols, uint32_t elem_bytes, uint32_t box_rows,
                             uint32_t box_heads, CUtensorMapDataType type)
 {
-    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
     if (!fn || elem_bytes == 0 || 128 % elem_bytes != 0)
         return false;
     const uint64_t span = 128 / elem_bytes;
