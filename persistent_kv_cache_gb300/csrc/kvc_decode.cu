@@ -2336,7 +2336,12 @@ kvc_status launch_window_step(const WindowStepArgs &a, int batch, cudaStream_t s
         !kvc_host::encode_2d_bf16_sw128(&tv, a.v_cache, rows, D, kTile, tt))
         return kvc_host::cuda_failed();
     auto kern = a.group > 8 ? window_step_kernel<T, D, 2> : window_step_kernel<T, D, 1>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+    // (what the largest window takes, whatever the call's: another thread's call with a
+    // smaller one must not lower it before this one's launch)
+    constexpr int most = 1024 + (int)kWindowStepMaxElems * 4 + 16 * (D + 8) * 2 +
+                         8 * (int)(kWindowStepMaxElems / D / kTile);
+    static_assert(kWindowStepMaxElems % (D * kTile) == 0, "the largest window is whole tiles");
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most) !=
         cudaSuccess)
         return kvc_host::cuda_failed();
     cudaLaunchConfig_t cfg = {};

@@ -1177,8 +1177,10 @@ template <typename T, int D> kvc_status launch_select_dim(const SelectArgs &a, c
     while (ctas < kMaxCluster && ctas * kPagesPerCta < a.max_pages)
         ctas *= 2;
     const int run = (a.max_pages + ctas - 1) / ctas, smem = (a.max_pages + run) * 4;
+    // (what the most pages take, whatever the call's: another thread's smaller call must not lower it)
+    constexpr int most = (kMaxPages + kMaxPages / kMaxCluster) * 4;
     if (smem > 32 * 1024 && cudaFuncSetAttribute(page_select_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 smem) != cudaSuccess)
+                                                 most) != cudaSuccess)
         return kvc_host::cuda_failed();
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(a.kv_heads * ctas, a.batch);
