@@ -762,7 +762,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     for (int u = 0; u < SPT; ++u) {
                         const int q = q0 + SPT * (mine_v ? v_group(j, nt) : k_group(j)) + u, slot = q % NSLAB;
                         if (q >= NSLAB)
-                            ok = warp_wait_or_abort(true, &empty[slot], ((q / NSLAB) - 1) & 1, abort_flag, a.status);
+                            ok = warp_wait_or_abort(&empty[slot], ((q / NSLAB) - 1) & 1, abort_flag, a.status);
                         if (!ok)
                             break;
                         uint8_t *to = smem + SM::RING_OFF + slot * SM::SLAB;
@@ -946,10 +946,11 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         __syncwarp();
     } else {
         // ======================= softmax =======================
-        // A warp whose wait gave up goes on through the tiles without work or waits: the barriers
-        // below have no limit, and every warp comes to each of them.  Tensor memory is loaded and stored by
-        // whole warps: `ok` is a lane's between its waits, but one for the warp wherever it is asked whether there
-        // is work.  (A vote a tile and one for the output: nothing to 1.8 % of the call's time.)
+        // A wait that gives up has set the flag that ends all others, and the warps go on through the
+        // tiles, whatever they find there, up to the stores, which ask for the flag: lanes give up one
+        // by one, and the barriers below, which have no limit, want every warp and tensor memory whole
+        // ones, so that nothing on the way may hang on a wait's answer.  (With a vote a tile, or each
+        // lane's answer carried along, calls took 1 to 3 % longer.)
         constexpr int CT = kBN / 2, OT = D / 2;  // columns of S and of O of a thread
         const int tid = threadIdx.x - 128, quad = warp & 3, half = ((warp - 4) >> 2) & 1, stream = (warp - 4) >> 3;
         const int m = quad * 32 + lane;  // row of the tile
@@ -973,7 +974,6 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         kvc_tc::named_bar_sync(stream_bar, 256);
         int q0 = 0;         // slabs before the segment
         uint32_t used = 0;  // tiles that this stream has had
-        bool ok = true;
         for (int s_no = 0; *(volatile int *)&kept->more[s_no & 1]; ++s_no) {
             Streams st;
             bool active;           // the warp has rows at all
@@ -1030,9 +1030,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 #pragma unroll
                     for (int hf = 0; hf < SPT; ++hf) {
                         const int qi = q0 + SPT * v_group(j, st.n) + hf;
-                        ok = ok && wait_or_abort(&full[qi % NSLAB], (qi / NSLAB) & 1, abort_flag, a.status);
-                        if (!ok)
-                            break;
+                        wait_or_abort(&full[qi % NSLAB], (qi / NSLAB) & 1, abort_flag, a.status);
                         const uint4 *v = reinterpret_cast<const uint4 *>(smem + SM::RING_OFF + (qi % NSLAB) * SM::SLAB);
 #pragma unroll
                         for (int g = 0; g < kGroups; ++g) {
@@ -1057,7 +1055,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                         rows_seen(j, r_lo, r_hi);
 #pragma unroll 1
                         for (int e = 0; e < 4; ++e) {
-                            uint32_t left = ok && r_hi < INT_MAX / 2 ? bad_sh[e] : 0u;
+                            uint32_t left = r_hi < INT_MAX / 2 ? bad_sh[e] : 0u;
                             while (left) {
                                 const int vr = 32 * e + __ffs(left) - 1, in = vr & (KR - 1);
                                 left &= left - 1;
@@ -1091,7 +1089,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                         if (tid < 4)
                             bad_sh[tid] = 0;
 #pragma unroll 1
-                        for (int hf = 0; hf < SPT && ok; ++hf) {
+                        for (int hf = 0; hf < SPT; ++hf) {
                             uint4 *v = reinterpret_cast<uint4 *>(
                                 smem + SM::RING_OFF + (q0 + SPT * v_group(j, st.n) + hf) % NSLAB * SM::SLAB);
 #pragma unroll 1
@@ -1118,7 +1116,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 const int s = TILES == 2 ? stream : (int)(used & 1);
                 const uint32_t parity = TILES == 2 ? used & 1 : (used >> 1) & 1;
                 const uint32_t s_col = lane_addr + SM::COL_S + s * kBN;
-                ok = warp_wait_or_abort(ok, &s_full[s], parity, abort_flag, a.status);
+                wait_or_abort(&s_full[s], parity, abort_flag, a.status);
                 ++used;
                 kvc_tc::fence_after();
                 // the weights of either half go where its own scores were, so that neither waits for the other
@@ -1134,11 +1132,11 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     lo -= CT * half;
                     hi -= CT * half;
                 }
-                if (active && ok)
+                if (active)
                     top = plain ? row_top<CT>(from) : row_top<CT>(from, lo, hi, flip);
                 red[(s * 2 + half) * kBM + m] = top;
                 kvc_tc::named_bar_sync(pair_bar, 64);
-                if (active && ok) {
+                if (active) {
                     top = fmaxf(top, red[(s * 2 + (half ^ 1)) * kBM + m]) * c_log2;
                     float alpha = 1.f;
                     bool rescale = false;
@@ -1152,8 +1150,10 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     if (__any_sync(0xffffffffu, rescale)) {
                         // the reference moved: rescale this thread's part of the O row
                         // (the products of the tile before; with two streams they were done before S was written)
-                        ok = TILES == 2 ? wait_or_abort(&o_done[s], (used - 2) & 1, abort_flag, a.status)
-                                        : wait_or_abort(&o_done[s ^ 1], ((used - 2) >> 1) & 1, abort_flag, a.status);
+                        if (TILES == 2)
+                            wait_or_abort(&o_done[s], (used - 2) & 1, abort_flag, a.status);
+                        else
+                            wait_or_abort(&o_done[s ^ 1], ((used - 2) >> 1) & 1, abort_flag, a.status);
                         kvc_tc::fence_after();
 #pragma unroll 1
                         for (int cc = half * OT; cc < (half + 1) * OT; cc += 32) {
@@ -1170,7 +1170,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
                     if (SM::OWN_P && used > 1) {
                         // the products of the tile before have read its weights
-                        ok = ok && wait_or_abort(&o_done[s], (used - 2) & 1, abort_flag, a.status);
+                        wait_or_abort(&o_done[s], (used - 2) & 1, abort_flag, a.status);
                         kvc_tc::fence_after();
                     }
                     const float sum = plain ? row_weights<T, CT, false>(from, to, lo, hi, flip, c_log2, neg_m, half_there)
@@ -1195,14 +1195,15 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             // (the next segment's first output products wait for its p_full, which every warp gives after this)
             if (st.tiles(stream) > 0) {
                 const uint32_t last = used - 1;
-                ok = ok && (TILES == 2 ? wait_or_abort(&o_done[stream], last & 1, abort_flag, a.status)
-                                       : wait_or_abort(&o_done[last & 1], (last >> 1) & 1, abort_flag, a.status));
+                if (TILES == 2)
+                    wait_or_abort(&o_done[stream], last & 1, abort_flag, a.status);
+                else
+                    wait_or_abort(&o_done[last & 1], (last >> 1) & 1, abort_flag, a.status);
             }
-            ok = __all_sync(0xffffffffu, ok);
             kvc_tc::fence_after();
             const Segment seg = kept->seg[s_no & 1];
             const int first = seg.i * a.item + (st.two ? stream * a.toks : 0), tok = m / a.group;
-            const bool there = tok < a.toks && first + tok < seg.n, whole = seg.t1 - seg.t0 == seg.tiles;
+            const bool there = tok < a.toks && first + tok < seg.n && !*abort_flag, whole = seg.t1 - seg.t0 == seg.tiles;
             const int64_t out_row = (int64_t)(seg.row0 + first + tok) * a.q_heads + seg.h * a.group + (m - tok * a.group);
             const int64_t part = (int64_t)seg.slot * TILES + (st.two ? stream : 0);
             float l = l_run, ref = m_run;
@@ -1231,7 +1232,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 cols = OT / 2;
                 col0 += stream * cols;
             }
-            if (active && ok) {
+            if (active) {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
                 for (int cc = col0; cc < col0 + cols; cc += 16) {

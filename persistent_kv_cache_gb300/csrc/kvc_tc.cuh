@@ -245,24 +245,22 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, vo
     for (uint32_t i = 0;; ++i) {
         if (kvc::mbar_try_wait_sleep(bar, parity, 20000))
             return true;
-        if ((i & 7u) == 7u) {
-            if (*abort_flag)
-                return false;
-            if (kvc::global_ns() - t0 > kvc::kWaitLimitNs) {
-                kvc::raise_status(status, KVC_DEV_TIMEOUT);
-                *abort_flag = 1;
-                return false;
-            }
+        if (*abort_flag)
+            return false;
+        if ((i & 7u) == 7u && kvc::global_ns() - t0 > kvc::kWaitLimitNs) {
+            kvc::raise_status(status, KVC_DEV_TIMEOUT);
+            *abort_flag = 1;
+            return false;
         }
     }
 }
 
-// The same for a warp: one answer for all lanes, that all of them were `ok` before and none gave up.  (Lanes
-// look at the flag and the time one by one; what needs the whole warp after a wait must not find part of it.)
-__device__ __forceinline__ bool warp_wait_or_abort(bool ok, uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+// The same for a warp: one answer for all lanes, that none gave up.  (Lanes look at the flag and the time
+// one by one; a warp that decides by the answer whether to load or to shuffle must not come apart.)
+__device__ __forceinline__ bool warp_wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
                                                    int32_t *status)
 {
-    return __all_sync(0xffffffffu, ok && wait_or_abort(bar, parity, abort_flag, status));
+    return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag, status));
 }
 
 } // namespace kvc_tc

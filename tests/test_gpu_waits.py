@@ -17,8 +17,7 @@ CODE = r"""
 #include "kvc_common.cuh"
 #include "kvc_tc.cuh"
 
-// out[0 .. 31] the lanes' answers alone, [32 .. 63] the warp's, [64 .. 95] the warp's where all are complete,
-// [96 .. 127] where a lane had given up before
+// out[0 .. 31] the lanes' answers alone, [32 .. 63] the warp's, [64 .. 95] the warp's where all are complete
 __global__ void waits(int *out, int32_t *status)
 {
     __shared__ uint64_t bar[32], done;
@@ -38,9 +37,8 @@ __global__ void waits(int *out, int32_t *status)
     __syncwarp();
     out[lane] = kvc_tc::wait_or_abort(&bar[lane], 0, &flag, status);
     __syncwarp();
-    out[32 + lane] = kvc_tc::warp_wait_or_abort(true, &bar[lane], 0, &flag, status);
-    out[64 + lane] = kvc_tc::warp_wait_or_abort(true, &done, 0, &flag, status);
-    out[96 + lane] = kvc_tc::warp_wait_or_abort(lane != 5, &done, 0, &flag, status);
+    out[32 + lane] = kvc_tc::warp_wait_or_abort(&bar[lane], 0, &flag, status);
+    out[64 + lane] = kvc_tc::warp_wait_or_abort(&done, 0, &flag, status);
 }
 
 extern "C" __attribute__((visibility("default"))) int run(int *out, int32_t *status)
@@ -57,9 +55,9 @@ def test_lanes_with_different_answers(tmp_path):
     src.write_text(CODE)
     subprocess.run([B._nvcc(), *B.ARCH, "-O3", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC", "-shared", "-cudart", "static",
                     "-I", B.CSRC, "-I", os.path.join(ROOT, "include"), "-o", str(lib), str(src)], check=True, capture_output=True, text=True)
-    out, st = torch.full((128,), -1, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, st = torch.full((96,), -1, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
     torch.cuda.synchronize()
     assert ctypes.CDLL(str(lib)).run(ctypes.c_void_p(out.data_ptr()), ctypes.c_void_p(st.data_ptr())) == 0
-    alone, warp, complete, before = out.cpu().reshape(4, 32).tolist()
-    assert alone == [1, 0] * 16 and warp == [0] * 32 and complete == [1] * 32 and before == [0] * 32
+    alone, warp, complete = out.cpu().reshape(3, 32).tolist()
+    assert alone == [1, 0] * 16 and warp == [0] * 32 and complete == [1] * 32
     assert st.item() == 0  # (the flag ended the waits, not their limit)

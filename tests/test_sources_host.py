@@ -34,19 +34,21 @@ def test_ragged_kernels_load_by_ordinary_loads():
         assert not re.findall(r"__ldg|__ldnc|ld\.global(\.\w+)*\.nc|__restrict__ (?!cos_t|sin_t)", text[name]), name
 
 
-def test_waits_of_whole_warps_have_one_answer():
-    """A warp that loads and stores tensor memory, votes and shuffles as a whole decides as a whole whether it does: in
-    the softmax warps of the ragged attention a vote comes between the last wait and every such question."""
-    text = sources()["kvc_ragged_attn.cu"]
-    kernel = text[text.index("ragged_attn_kernel(const"):text.index("ragged_merge_kernel(const")]
-    softmax = kernel[kernel.index("quad = warp & 3"):]
-    assert "tcgen05" not in softmax and "mbar_wait" not in softmax
-    asked = [m.start() for m in re.finditer(r"\bactive && ok\b", softmax)]
-    assert len(asked) == 3 and not re.findall(r"\bok && active\b|if \(ok\)", softmax)
-    given = [(m.start(), m.group(1)) for m in re.finditer(r"\bok = ([^;]*);", softmax)]
-    for at in asked:
-        last = [what for begin, what in given if begin < at][-1]
-        assert "warp_wait_or_abort(ok, " in last or "__all_sync(0xffffffffu, ok)" in last, last
+def test_nothing_hangs_on_what_a_wait_of_softmax_warps_answers():
+    """Lanes whose bounded wait runs out do so one by one, and what follows wants whole warps (tensor memory) and every
+    warp (barriers without a limit): the answer, which is the flag that the lane has set or found, is asked for at the
+    stores alone."""
+    text = sources()
+    kernel = text["kvc_ragged_attn.cu"]
+    softmax = kernel[kernel.index("quad = warp & 3"):kernel.index("ragged_merge_kernel(const")]
+    for section, waits in ((softmax, 7),):
+        assert "tcgen05" not in section
+        # (each a statement of its own)
+        assert len(re.findall(r"wait_or_abort\(", section)) == len(re.findall(r"(?<=[;{})])\s*(else\s+)?wait_or_abort\([^;]*\);", section)) == waits
+    # the flag: a store's condition, where no load or barrier follows that not all come to
+    assert re.findall(r".*\*abort_flag", softmax) == ["            const bool there = tok < a.toks && first + tok < seg.n && !*abort_flag"]
+    stores = softmax[softmax.index("if (!there)"):softmax.index("if (!whole && there && col0 == 0)")]
+    assert "kvc_tc::ld" not in stores and "sync(" not in stores and softmax.count("!there") == 1
 
 
 def test_chained_kernels_wait_before_they_write_or_end():
