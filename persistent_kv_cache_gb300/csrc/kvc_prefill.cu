@@ -341,14 +341,12 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, vo
     for (uint32_t i = 0;; ++i) {
         if (kvc::mbar_try_wait_sleep(bar, parity, 20000))
             return true;
-        if ((i & 7u) == 7u) {
-            if (*abort_flag)
-                return false;
-            if (kvc::global_ns() - t0 > kvc::kWaitLimitNs) {
-                kvc::raise_status(status, KVC_DEV_TIMEOUT);
-                *abort_flag = 1;
-                return false;
-            }
+        if (*abort_flag)
+            return false;
+        if ((i & 7u) == 7u && kvc::global_ns() - t0 > kvc::kWaitLimitNs) {
+            kvc::raise_status(status, KVC_DEV_TIMEOUT);
+            *abort_flag = 1;
+            return false;
         }
     }
 }
@@ -715,15 +713,15 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         const int r_lo = a.window > 0 ? max(0, r_hi - a.window + 1) : 0;
         const float c_log2 = a.scale_log2;
         float m_run = -INFINITY, l_run = 0.f;
-        bool ok = true;
+        // A wait that gives up has set the flag that ends all others, and the warps go on through the
+        // tiles, whatever they find there, up to the output, which asks for the flag: lanes give up one
+        // by one, and the barriers below, which have no limit, want every warp and tensor memory whole
+        // ones, so that nothing on the way may hang on a wait's answer.
         for (int j = 0; j < ntiles; ++j) {
             const int s = j & 1;
             const int t_lo = lo + j * kBN;
             const int c0 = t_lo + 64 * half;  // key row of my first column
-            if (!wait_or_abort(&s_full[s], (j >> 1) & 1, abort_flag, a.status)) {
-                ok = false;
-                break;
-            }
+            wait_or_abort(&s_full[s], (j >> 1) & 1, abort_flag, a.status);
             tc_fence_after();
             float v[64];
             tmem_ld64(lane_addr + COL_S + s * kBN + 64 * half, v);
@@ -783,10 +781,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 const int q_first = (2 * ntiles - 1) * NST;  // V_{n-1} is the last group
                 for (int sl = first_bad / KPS; sl < NST; ++sl) {
                     const int q = q_first + sl;
-                    if (!wait_or_abort(&full[q % NSLAB], (q / NSLAB) & 1, abort_flag, a.status)) {
-                        ok = false;
-                        break;
-                    }
+                    wait_or_abort(&full[q % NSLAB], (q / NSLAB) & 1, abort_flag, a.status);
                     uint8_t *vt = smem + SM::RING_OFF + (q % NSLAB) * SM::SLAB;
                     const int r0 = max(0, first_bad - sl * KPS);  // first bad row in this slab
                     const int nbad = KPS - r0;
@@ -797,18 +792,12 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                             make_uint4(0, 0, 0, 0);
                     }
                 }
-                if (!ok)
-                    break;
                 kvc::fence_proxy_async_smem();
             }
 
             // the running max moved: rescale my half of this O row (PV_{j-1} done)
             if (__any_sync(0xffffffffu, rescale)) {
-                if (!wait_or_abort(&o_done[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag,
-                                   a.status)) {
-                    ok = false;
-                    break;
-                }
+                wait_or_abort(&o_done[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, a.status);
                 tc_fence_after();
 #pragma unroll 1
                 for (int cc = half * (D / 2); cc < (half + 1) * (D / 2); cc += 32) {
@@ -837,8 +826,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         red[((ntiles & 1) * 2 + half) * kBM + m] = l_run;
         named_bar_sync(pair_bar, 64);
         const float l_tot = l_run + red[((ntiles & 1) * 2 + (half ^ 1)) * kBM + m];
-        const bool have_o = ok && wait_or_abort(&o_done[(ntiles - 1) & 1],
-                                                ((ntiles - 1) >> 1) & 1, abort_flag, a.status);
+        wait_or_abort(&o_done[(ntiles - 1) & 1], ((ntiles - 1) >> 1) & 1, abort_flag, a.status);
+        const bool have_o = __all_sync(0xffffffffu, !*abort_flag);
         const int r_in = m - hh * QB;  // query of this row within the block
         if (have_o) {
             tc_fence_after();

@@ -41,14 +41,18 @@ def test_nothing_hangs_on_what_a_wait_of_softmax_warps_answers():
     text = sources()
     kernel = text["kvc_ragged_attn.cu"]
     softmax = kernel[kernel.index("quad = warp & 3"):kernel.index("ragged_merge_kernel(const")]
-    for section, waits in ((softmax, 7),):
+    prefill = text["kvc_prefill.cu"]
+    tiles = prefill[prefill.index("float m_run", prefill.index("pair_bar = 1 + quad")):prefill.index("prefill_combine_kernel(")]
+    for section, waits in ((softmax, 7), (tiles, 4)):
         assert "tcgen05" not in section
         # (each a statement of its own)
         assert len(re.findall(r"wait_or_abort\(", section)) == len(re.findall(r"(?<=[;{})])\s*(else\s+)?wait_or_abort\([^;]*\);", section)) == waits
-    # the flag: a store's condition, where no load or barrier follows that not all come to
+    # the flag: a store's condition, where no load or barrier follows that not all come to; a vote
     assert re.findall(r".*\*abort_flag", softmax) == ["            const bool there = tok < a.toks && first + tok < seg.n && !*abort_flag"]
     stores = softmax[softmax.index("if (!there)"):softmax.index("if (!whole && there && col0 == 0)")]
     assert "kvc_tc::ld" not in stores and "sync(" not in stores and softmax.count("!there") == 1
+    assert "const bool have_o = __all_sync(0xffffffffu, !*abort_flag);" in tiles
+    assert re.search(r"if \(sw == 0 && lane == 0 && !\*abort_flag\)", tiles)
 
 
 def test_chained_kernels_wait_before_they_write_or_end():
