@@ -1120,24 +1120,19 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
         // the tile's K and V (16-bit), or its int8 K and V payloads (kgen)
         uint8_t *kgen, *vgen;
         int s0, s1;
+        bool there;
         if constexpr (SLOTS) {
             s0 = pos % NBAR;
             s1 = (pos + 1) % NBAR;
             kgen = stages + s0 * SLOT_BYTES;
             vgen = stages + s1 * SLOT_BYTES;
-            if (!kvc::mbar_wait(&full[s0], (uint32_t)(pos / NBAR) & 1u) ||
-                (!q8 && !kvc::mbar_wait(&full[s1], (uint32_t)((pos + 1) / NBAR) & 1u))) {
-                timed_out = true;
-                break;
-            }
+            there = kvc::mbar_wait(&full[s0], (uint32_t)(pos / NBAR) & 1u) &&
+                    (q8 || kvc::mbar_wait(&full[s1], (uint32_t)((pos + 1) / NBAR) & 1u));
         } else {
             s0 = s1 = t % NBAR;
             kgen = stages + s0 * SLOT_BYTES;
             vgen = kgen + KT_BYTES;
-            if (!kvc::mbar_wait(&full[s0], (uint32_t)(t / NBAR) & 1u)) {
-                timed_out = true;
-                break;
-            }
+            there = kvc::mbar_wait(&full[s0], (uint32_t)(t / NBAR) & 1u);
         }
         const int rows_t = tile_rows(t);
         const int my_valid = min(16, max(0, rows_t - 16 * warp));
@@ -1202,6 +1197,12 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
         if (wrote)
             kvc::fence_proxy_async_smem();
         __syncwarp();
+        // A wait that ran out did so for a lane at a time, and the tile's work wants whole warps: they
+        // all do it, on whatever the slots hold, and leave together before the slots are given back.
+        if (!__all_sync(0xffffffffu, there)) {
+            timed_out = true;
+            break;
+        }
         if constexpr (NOPROD) {
             release_slot(pos);
             release_slot(pos + 1);
@@ -1638,12 +1639,13 @@ window_step_kernel(const __grid_constant__ CUtensorMap tmap_k,
     GroupAttn<T, D, HB, decode_q_in_registers<D, HB>()> ga;
     ga.init();
     ga.load_q(qs, QS, lane);
-    // (a wait that runs out marks this thread; the loop goes on, skipping
-    // the work, so that every thread meets the same barriers)
+    // (a wait that runs out marks this warp, whose lanes give up one by one;
+    // the loop goes on, skipping the work, so that every thread meets the
+    // same barriers)
     bool ok = true;
     for (int t = 0; t < ntiles; ++t) {
-        if (t >= t_lo && t < t_hi && !kvc::mbar_wait(&bar[t], 0))
-            ok = false;
+        if (t >= t_lo && t < t_hi)
+            ok = __all_sync(0xffffffffu, kvc::mbar_wait(&bar[t], 0)) && ok;
         const int r_lo = t * kTile, r_hi = r_lo + kTile;
         const bool has_new = new_r >= r_lo && new_r < r_hi;
         const int zl = max(z0, r_lo), zh = min(z1, r_hi);

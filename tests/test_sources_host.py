@@ -55,6 +55,18 @@ def test_nothing_hangs_on_what_a_wait_of_softmax_warps_answers():
     assert re.search(r"if \(sw == 0 && lane == 0 && !\*abort_flag\)", tiles)
 
 
+def test_decode_warps_leave_their_tiles_whole():
+    """The decodes' tiles are the work of whole warps (shuffles, products): a lane's answer to a wait goes through a vote
+    before a branch hangs on it."""
+    text = sources()["kvc_decode.cu"]
+    tiles = text[text.index("bool timed_out = false;"):text.index("if (timed_out) {")]
+    assert len(re.findall(r"\bthere = kvc::mbar_wait\(", tiles)) == 2 and tiles.count("mbar_wait(") == 3
+    assert len(re.findall(r"\bthere\b", tiles)) == 4 and len(re.findall(r"if \(!__all_sync\(0xffffffffu, there\)\) \{\s*timed_out = true;\s*break;", tiles)) == 1
+    step = text[text.index("window_step_kernel("):]
+    step = step[:step.index("__syncthreads_and(ok)")]
+    assert re.findall(r"(?<!_)\bok = [^;]*;", step) == ["ok = true;", "ok = __all_sync(0xffffffffu, kvc::mbar_wait(&bar[t], 0)) && ok;"]
+
+
 def test_chained_kernels_wait_before_they_write_or_end():
     """A kernel that may start before the one in front has ended waits for that in every block, also in one that has
     nothing to do: the kernel behind counts on all before it having ended too."""
