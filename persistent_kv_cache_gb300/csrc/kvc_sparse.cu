@@ -733,8 +733,9 @@ sparse_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
             const int per_page = a.page_size / kUnit;
             int32_t id = 0;
             for (int u = sg.u0; u < sg.u1; ++u, ++i) {
+                // (an ordinary load: page_select_kernel still writes the table when this kernel's life begins)
                 if (((u - sg.u0) & 31) == 0)
-                    id = u + lane < sg.u1 ? __ldg(table + (u + lane) / per_page) : 0;
+                    id = u + lane < sg.u1 ? table[(u + lane) / per_page] : 0;
                 const int32_t page = __shfl_sync(0xffffffffu, id, (u - sg.u0) & 31);
                 const int slot = i % STAGES;
                 if (i >= STAGES)

@@ -814,6 +814,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             const int r = mt * kBM + m;
             const bool active = mt * kBM + quad * 32 < rows;  // of the warp: it has rows at all
             const int d = d_next >= 0 && d_next < N ? d_next : -1;
+            // (ordinary loads: tree_prep_kernel still writes them when this kernel's life begins)
             const uint32_t *see_words = a.see + ((int64_t)cur.b * N + r % N) * words;
             // the words that hold the drafts of this thread's columns of tile j
             uint32_t w_next[3];
@@ -824,7 +825,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                     const int w0 = j0 >> 5;
 #pragma unroll
                     for (int e = 0; e < 3; ++e)
-                        w_next[e] = w0 + e >= 0 && w0 + e < words ? __ldg(see_words + w0 + e) : 0u;
+                        w_next[e] = w0 + e >= 0 && w0 + e < words ? see_words[w0 + e] : 0u;
                 }
             };
             load_words(0);
@@ -886,7 +887,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
 #pragma unroll 1
                         for (int e = 0; e < 4 && d >= 0; ++e) {
                             const int k0 = t_lo + 32 * e, w0 = (k0 - P) >> 5;
-                            auto word = [&](int w) { return w >= 0 && w < words ? __ldg(see_words + w) : 0u; };
+                            auto word = [&](int w) { return w >= 0 && w < words ? see_words[w] : 0u; };
                             uint32_t left = bad_sh[e] & (cache_keys(k0) | __funnelshift_r(word(w0), word(w0 + 1), (k0 - P) & 31));
                             while (left) {
                                 const int vr = 32 * e + __ffs(left) - 1, in = vr & (KR - 1);

@@ -34,6 +34,14 @@ def test_ragged_kernels_load_by_ordinary_loads():
         assert not re.findall(r"__ldg|__ldnc|ld\.global(\.\w+)*\.nc|__restrict__ (?!cos_t|sin_t)", text[name]), name
 
 
+def test_what_the_first_kernel_of_a_call_writes_is_loaded_by_ordinary_loads():
+    """The same where a call's second kernel begins while its first one runs."""
+    text = sources()
+    assert not re.findall(r"__ldg\(see_words", text["kvc_tree.cu"]) and text["kvc_tree.cu"].count("see_words[") == 2
+    decode = text["kvc_sparse.cu"][text["kvc_sparse.cu"].index("sparse_decode_kernel(const"):]
+    assert "a.sub_table" in decode and not re.findall(r"__ldg\((?!a\.(cos|sin)_t)", decode)
+
+
 def test_nothing_hangs_on_what_a_wait_of_softmax_warps_answers():
     """Lanes whose bounded wait runs out do so one by one, and what follows wants whole warps (tensor memory) and every
     warp (barriers without a limit): the answer, which is the flag that the lane has set or found, is asked for at the
