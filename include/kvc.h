@@ -43,6 +43,8 @@
  *    the call only.
  *  * Streams: `stream` is a cudaStream_t (NULL = legacy default stream).  Work
  *    is enqueued, never waited for.
+ *  * Threads: calls may come from several host threads at once, a new thread's
+ *    first CUDA call among them; what they write is theirs to keep apart.
  *  * Layout: caches and staging buffers are BNSH: [batch, kv_heads, rows, D],
  *    row-major, rows of D contiguous elements.  Queries and outputs are
  *    [batch, q_heads, new_tokens, D].  Query head h reads KV head
@@ -986,6 +988,9 @@ kvc_status kvc_ragged_plan(const int32_t *cached, const int32_t *new_tokens, int
  *                    positions keeps its speed, one that goes round `low` times or
  *                    less has speed / factor, and between them g = (trained * speed /
  *                    2 pi - low) / (high - low): g * speed + (1 - g) * speed / factor
+ *                    (a ramp over the rounds, not over a pair's index between two
+ *                    indices rounded to whole numbers: a model that was extended by
+ *                    the latter wants tables of its own)
  * Speeds are float64; the angle that a speed has at a position is reduced in whole
  * numbers, to 2^-32 of a turn at any position, so that far positions are as exact as
  * near ones: off by a float32 rounding or two, beside the few 2^-53 of itself that the
@@ -1023,7 +1028,7 @@ kvc_status kvc_rope_tables(float *cos_table, float *sin_table, int64_t first, in
  * with a slot outside the pool (KVC_DEV_INDEX_OOB) or a position outside the tables
  * (KVC_DEV_ROPE_RANGE).  Two tokens with one slot leave parts of either there.
  * KVC_BF16/KVC_F16; head_dim a multiple of 16 up to 256, rotary_dim a multiple of 16
- * up to head_dim (KVC_ERR_UNSUPPORTED).  q_out and the pools may not overlap what is
+ * up to head_dim, q_heads and kv_heads up to 32767 (KVC_ERR_UNSUPPORTED).  q_out and the pools may not overlap what is
  * read (KVC_ERR_SHAPE).
  */
 kvc_status kvc_ragged_append(void *q_out, void *k_pool, void *v_pool, const void *q, const void *k,
@@ -1052,7 +1057,9 @@ kvc_status kvc_ragged_append(void *q_out, void *k_pool, void *v_pool, const void
  *            undefined).
  * page_size  a multiple of 16 (KVC_ERR_SHAPE).
  * KVC_BF16/KVC_F16, head_dim 64, 128 or 256, q_heads / kv_heads any whole number up
- * to 16, batch <= 65535 (KVC_ERR_UNSUPPORTED); scale 0 -> 1 / sqrt(head_dim).
+ * to 16, kv_heads <= 32767, batch <= 65535 (KVC_ERR_UNSUPPORTED); n_pool_pages *
+ * page_size * kv_heads and tokens * q_heads below 2^31 (KVC_ERR_CAPACITY); scale 0 ->
+ * 1 / sqrt(head_dim).
  * Beside the result, the softmax weights are rounded to the cache's type.  Scores
  * (q . k times scale) up to 1e30 in magnitude; beyond, the output may be NaN.
  * A NaN or an infinity in a column of a V row that a token sees makes that column of

@@ -337,8 +337,8 @@ uint64_t turns_of(double speed)
 // turn in whole numbers, the rest u, at most an eighth of a turn, by the Taylor series of sin
 // and cos of 2 pi u (terms (2 pi)^k / k!; the first left out are below 2^-29).  With
 // sincospif, which reduces its argument again, the 131072 x 64 table took 34 us; one at a
-// time, each position's angle a product, in three waves of blocks 14.7; now 11.5, 87 % of
-// the copy rate.
+// time, each position's angle a product, in three waves of blocks 14.7; now 11.1 to 12.2, 81
+// to 89 % of the copy rate.
 __device__ __forceinline__ void turns2(const uint32_t (&x)[2], float magnitude, float *c, float *s)
 {
     using kvc_tc::fma2;

@@ -154,7 +154,10 @@ struct Line {
 
 // What `streams` key tiles of a row take a CTA, the join of two parts takes for each: a
 // row of t such is done soonest by about sqrt(7 t) CTAs.  With so few rows that this
-// leaves CTAs over, rows begin with a CTA each and cost nothing beside their keys.
+// leaves CTAs over, an item costs nothing beside its keys, and a row of a few tiles has its
+// CTAs to itself.  Rows of less than a share's least (a tile's keys, two with two streams) then
+// stand behind one another in a CTA, each with its start and end: 6 requests of 8 kv heads with
+// 17 keys have 3 CTAs and take 75 us, where 7, whose items' cost counts, take 12.
 __device__ __forceinline__ Line make_line(const RaggedArgs &a, int64_t units, int64_t rows, int64_t keys, int grid)
 {
     Line l;
@@ -421,21 +424,24 @@ __device__ __forceinline__ Line find_share(const RaggedArgs &a, uint8_t *scratch
 // What bounds it (one GB300, bf16; times of the whole call, with the join; means of 16
 // drawn batches and the products of the pairs that are seen; times of steps, here and below,
 // are of three such batches):
-//   chunks of 8 prompts, head_dim 128, group 4, 737 GFLOP: 656 us, 59 % of the measured
-//   bf16 peak (57 to 61).  A pair of tiles takes 3900 clocks where its products need 2048: a
+//   chunks of 8 prompts, head_dim 128, group 4, 737 GFLOP: 643 us, 60 % of the measured
+//   bf16 peak (58 to 63).  A pair of tiles takes 3800 clocks where its products need 2048: a
 //   stream's chain (scores 512, their maximum 370, weights 1150, output products 512, the
 //   barriers between them) is longer than two streams hide.  Three streams, or scores a
-//   tile ahead, want more than the 512 columns of tensor memory.  Steps on the way: one
+//   tile ahead, want more than the 512 columns of tensor memory; the maximum and the weights
+//   each read the scores, of which a thread's 64 do not fit the 96 registers that all
+//   threads are compiled for (another split of the registers between the warps has not been
+//   tried in this form).  Steps on the way: one
 //   thread a row, unrolled, with its scores in registers 869 us (the code missed the
 //   instruction cache; a spilled register in the loop costs the release of every
 //   arrival behind it hundreds of clocks); two threads a row and rolled loops 650.
-//   windowed chunks, head_dim 256, 718 GFLOP: 601 us, 63 %.  128 KB of K and V a tile for
-//   16.8 MFLOP: L2 delivers about 10 TB/s.
-//   decoding batch, 544 MB: 98 us, 82 % of the measured copy rate.
-//   decoding and prompts, head_dim 64, window 1000, pages of 16 (116 MB): 105 us; nine
+//   windowed chunks, head_dim 256, 718 GFLOP: 597 us, 63 %.  128 KB of K and V a tile for
+//   16.8 MFLOP: L2 delivers about 11 TB/s.
+//   decoding batch, 544 MB: 97 us, 83 % of the measured copy rate.
+//   decoding and prompts, head_dim 64, window 1000, pages of 16 (116 MB): 102 us; nine
 //   tiles an item, three of them cut, and the exponentials of 128 rows for a decoding
 //   request's eight.
-//   17 tokens of one user over 700: 18.5 us (20 with a cold L2), a chain of loads (lengths, table, rows, join).
+//   17 tokens of one user over 700: 18.4 us (20 with a cold L2), a chain of loads (lengths, table, rows, join).
 //
 // Only key tiles that hold the last tokens' own rows, or that a window's edge cuts,
 // are masked ("cut" tiles).  A NaN or an infinity in a column of V makes that column of
@@ -546,7 +552,11 @@ template <int N> __device__ __forceinline__ float top_of(const uint32_t (&x)[N])
     return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
-// scores -> weights 2^(x c - m), summed in float32 and packed to 16-bit pairs in the first half of x
+// scores -> weights 2^(x c - m), summed in float32 and packed to 16-bit pairs in the first half of x.
+// (The output products take both operands in one 16-bit type, V's.  A weight is rounded once, by at most half a
+// step of itself, which a result's own rounding exceeds a little: the relative error against 64 bits goes from 1.7e-3,
+// a result that is only rounded, to 2.3e-3 with bf16, from 2.1e-4 to 2.9e-4 with fp16.  A second product with what
+// the rounding left over would make the output products, half of all, twice as long.)
 template <typename T, int N>
 __device__ __forceinline__ void weights(uint32_t (&x)[N], float c_log2, float neg_m, float2 (&sum)[2])
 {
