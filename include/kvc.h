@@ -1064,7 +1064,9 @@ kvc_status kvc_ragged_append(void *q_out, void *k_pool, void *v_pool, const void
  * (q . k times scale) up to 1e30 in magnitude; beyond, the output may be NaN.
  * A NaN or an infinity in a column of a V row that a token sees makes that column of
  * its output NaN, whatever the row's weight; a NaN in a K row that it sees makes all
- * of them NaN.  What it does not see may hold anything.
+ * of them NaN.  What it does not see may hold anything; table entries before the page of
+ * the first row that a request's first token sees are not read (pages that a window has
+ * left behind may be given back).
  * workspace  device, kvc_gqa_ragged_workspace_size(...) bytes on the current device,
  *            256-byte aligned, apart from every other argument (KVC_ERR_SHAPE).
  *            Calls that may overlap on the GPU need their own.
