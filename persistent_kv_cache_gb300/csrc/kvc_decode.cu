@@ -1221,6 +1221,11 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
         if (lane == 0) {
             kvc::raise_status(a.status, KVC_DEV_TIMEOUT);
             atomicExch(abort_flag, 1);
+            // The loads that may be in flight yet, one a slot from this warp's place on, land before
+            // the CTA merges and ends (each wait bounded: one for a load that was never issued runs out).
+            const int at = SLOTS ? pos : pos / 2;
+            for (int k = 0; k < NBAR; ++k)
+                kvc::mbar_wait(&full[(at + k) % NBAR], (uint32_t)((at + k) / NBAR) & 1u);
         }
     }
     // ---- merge the four warps' (m, l, o) through shared memory ----

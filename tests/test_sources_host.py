@@ -70,6 +70,10 @@ def test_decode_warps_leave_their_tiles_whole():
     tiles = text[text.index("bool timed_out = false;"):text.index("if (timed_out) {")]
     assert len(re.findall(r"\bthere = kvc::mbar_wait\(", tiles)) == 2 and tiles.count("mbar_wait(") == 3
     assert len(re.findall(r"\bthere\b", tiles)) == 4 and len(re.findall(r"if \(!__all_sync\(0xffffffffu, there\)\) \{\s*timed_out = true;\s*break;", tiles)) == 1
+    # (and the loads in flight land before the warps meet)
+    left = text[text.index("if (timed_out) {"):]
+    left = left[:left.index("consumer_sync();")]
+    assert left.index("atomicExch(abort_flag, 1);") < left.index("kvc::mbar_wait(&full[(at + k) % NBAR], (uint32_t)((at + k) / NBAR) & 1u);")
     step = text[text.index("window_step_kernel("):]
     step = step[:step.index("__syncthreads_and(ok)")]
     assert re.findall(r"(?<!_)\bok = [^;]*;", step) == ["ok = true;", "ok = __all_sync(0xffffffffu, kvc::mbar_wait(&bar[t], 0)) && ok;"]
